@@ -6,6 +6,7 @@ library has not been built, or its kernels cannot run on this device, the
 calls raise; there is no other implementation to fall back to.
 """
 import ctypes
+import functools
 import os
 
 import torch
@@ -75,6 +76,19 @@ def lib():
         L.ne_attn_qkv_workspace_size.restype = sz
         L.ne_attn_qkv_rmsnorm.argtypes = [vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, f, f, i, vp, sz, vp]
         L.ne_attn_qkv_rmsnorm.restype = i
+        ll = ctypes.c_longlong
+        L.ne_attn_qk_norm.argtypes = [vp, vp, vp, vp, i, i, i, i, i, ll, ll, f, f, i, vp, sz, vp]
+        L.ne_attn_qk_norm.restype = i
+        L.ne_attn_qk_norm_bwd_workspace_size.argtypes = [i, i, i, i, i]
+        L.ne_attn_qk_norm_bwd_workspace_size.restype = sz
+        L.ne_attn_qk_norm_bwd.argtypes = [vp] * 10 + [i] * 5 + [ll] * 4 + [f, i, vp, sz, vp]
+        L.ne_attn_qk_norm_bwd.restype = i
+        L.ne_attn_kv_append_paged.argtypes = [vp] * 8 + [i] * 7 + [ll] * 3 + [f, f, i, vp]
+        L.ne_attn_kv_append_paged.restype = i
+        L.ne_attn_decode_paged_workspace_size.argtypes = [i, i, i, i, i, i]
+        L.ne_attn_decode_paged_workspace_size.restype = sz
+        L.ne_attn_decode_paged.argtypes = [vp] * 9 + [i] * 8 + [ll, ll, i, f, f, i, vp, sz, vp]
+        L.ne_attn_decode_paged.restype = i
         _lib = L
     return _lib
 
@@ -207,7 +221,7 @@ def status_of_last_kernels(stream=None):
 
 
 KERNEL_KINDS = ("fwd", "bwd_prep", "bwd_dkdv", "bwd_dq", "fwd_rope", "kv_append", "decode", "decode_aux",
-                "qkv_prep", "qkv")
+                "qkv_prep", "qkv", "qk_norm", "qk_norm_bwd", "qk_norm_dw", "kv_append_paged", "decode_paged")
 
 
 def profile_start(capacity):
@@ -363,6 +377,225 @@ def rotated_qk(workspace, B, T, Hq, Hkv, D):
     qr = workspace[:nq].view(torch.float16).view(B, T, Hq, D)
     kr = workspace[up(nq):up(nq) + nk].view(torch.float16).view(B, T, Hkv, D)
     return qr, kr
+
+
+# ------------------------------------------------------------------ query/key norms, paged cache
+def _need(ok, what):
+    if not ok:
+        raise ValueError(what)
+
+
+def _run(name, device, stream, temps, *args):
+    """Calls library function `name` with the launch stream as its last argument,
+    on `device` (the current one or not).  `temps`, tensors the call allocated on
+    the current stream, are kept from reuse until the work on another stream is done."""
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return _run(name, device, stream, temps, *args)
+    s = torch.cuda.current_stream() if stream is None else stream
+    _check(name, getattr(lib(), name)(*args, s.cuda_stream))
+    if stream is not None:
+        for t in temps:
+            t.record_stream(stream)
+
+
+def _optr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _head_rows(t, name, dtype=torch.bfloat16, device=None):
+    """Row stride (values between positions) of t [B, T, H, D] or [N, H, D]: heads
+    contiguous, positions evenly spaced."""
+    s, n = t.stride(), t.shape
+    _need(t.dtype == dtype and t.is_cuda and (device is None or t.device == device),
+          "%s must be %s on the call's CUDA device" % (name, dtype))
+    H, D = n[-2], n[-1]
+    ok = s[-1] == 1 and (H == 1 or s[-2] == D)
+    if len(n) == 3:
+        row = s[0] if n[0] > 1 else H * D
+    else:
+        row = s[1] if n[1] > 1 else (s[0] if n[0] > 1 else H * D)
+        ok = ok and (n[0] == 1 or n[1] == 1 or s[0] == n[1] * s[1])
+    _need(ok, "%s: the heads of a position must be contiguous and the positions evenly spaced" % name)
+    return row
+
+
+def _vector(t, D, name, device):
+    _need(t.dtype == torch.bfloat16 and t.device == device and t.shape == (D,) and t.is_contiguous(),
+          "%s must be a contiguous bfloat16 [%d] on the call's device" % (name, D))
+
+
+def _int32(t, name, device, shape):
+    _need(t.dtype == torch.int32 and t.device == device and t.is_contiguous() and tuple(t.shape) == shape,
+          "%s must be a contiguous int32 %s on the call's device" % (name, list(shape)))
+
+
+def qk_norm(q, k, q_weight, k_weight, eps=1e-6, rope_base=10000.0, rope_half=False, workspace=None, stream=None):
+    """RMS norm of every head of q [B,T,Hq,D] and k [B,T,Hkv,D] (bf16) with weights
+    [D], then the rotary embedding, in one pass (ne_attn_qk_norm).
+
+    q and k may be slices of a fused projection's rows.  The rotated fp16 q and k
+    land at the start of `workspace` (a uint8 CUDA tensor of at least
+    fwd_workspace_size bytes; allocated if None), which is returned: attn_fwd and
+    attn_bwd take it with qk_rotated=True (q and k then None), rotated_qk views it.
+    """
+    B, T, Hq, D = q.shape
+    Hkv, dev = k.shape[2], q.device
+    _need(k.shape == (B, T, Hkv, D), "k must be [B, T, Hkv, D] like q")
+    qs, ks = _head_rows(q, "q"), _head_rows(k, "k", device=dev)
+    _vector(q_weight, D, "q_weight", dev)
+    _vector(k_weight, D, "k_weight", dev)
+    temps = ()
+    if workspace is None:
+        n = fwd_workspace_size(B, T, Hq, Hkv, D)
+        _need(n > 0, "unsupported shape")
+        workspace = torch.empty(n, dtype=torch.uint8, device=dev)
+        temps = (workspace,)
+    _need(workspace.dtype == torch.uint8 and workspace.device == dev, "workspace must be uint8 on the call's device")
+    _run("ne_attn_qk_norm", dev, stream, temps, q.data_ptr(), k.data_ptr(), q_weight.data_ptr(), k_weight.data_ptr(),
+         B, T, Hq, Hkv, D, qs, ks, eps, rope_base, ROPE_HALF if rope_half else 0, workspace.data_ptr(),
+         workspace.numel())
+    return workspace
+
+
+def qk_norm_bwd(q, k, q_weight, k_weight, dqn, dkn, eps=1e-6, dq=None, dk=None, workspace=None, stream=None):
+    """Backward of qk_norm: dq, dk (the type of dqn and dkn), dq_weight, dk_weight (fp32 [D])
+    from dqn [B,T,Hq,D] and dkn [B,T,Hkv,D], the dq and dk of attn_bwd with qk_rotated=True
+    (bf16 or fp32, contiguous).  dq and dk may be given: slices of a fused projection's
+    gradient, or dqn and dkn themselves."""
+    B, T, Hq, D = q.shape
+    Hkv, dev, dt = k.shape[2], q.device, dqn.dtype
+    _need(k.shape == (B, T, Hkv, D), "k must be [B, T, Hkv, D] like q")
+    _need(dt in (torch.bfloat16, torch.float32), "dqn and dkn must be bfloat16 or float32")
+    qs, ks = _head_rows(q, "q"), _head_rows(k, "k", device=dev)
+    _vector(q_weight, D, "q_weight", dev)
+    _vector(k_weight, D, "k_weight", dev)
+    for t, like, name in ((dqn, q, "dqn"), (dkn, k, "dkn")):
+        _need(t.dtype == dt and t.device == dev and t.shape == like.shape and t.is_contiguous(),
+              "%s must be contiguous, of the shape of its input and of one type with the other" % name)
+    made = []
+    if dq is None:
+        dq = torch.empty(q.shape, dtype=dt, device=dev)
+        made.append(dq)
+    if dk is None:
+        dk = torch.empty(k.shape, dtype=dt, device=dev)
+        made.append(dk)
+    _need(dq.shape == q.shape and dk.shape == k.shape, "dq and dk must have the shapes of q and k")
+    dqs, dks = _head_rows(dq, "dq", dt, dev), _head_rows(dk, "dk", dt, dev)
+    dw = torch.empty((2, D), dtype=torch.float32, device=dev)
+    made.append(dw)
+    if workspace is None:
+        n = int(lib().ne_attn_qk_norm_bwd_workspace_size(B, T, Hq, Hkv, D))
+        _need(n > 0, "unsupported shape")
+        workspace = torch.empty(n, dtype=torch.uint8, device=dev)
+        made.append(workspace)
+    _need(workspace.dtype == torch.uint8 and workspace.device == dev, "workspace must be uint8 on the call's device")
+    p = dw.data_ptr()
+    _run("ne_attn_qk_norm_bwd", dev, stream, made, q.data_ptr(), k.data_ptr(), q_weight.data_ptr(),
+         k_weight.data_ptr(), dqn.data_ptr(), dkn.data_ptr(), dq.data_ptr(), dk.data_ptr(), p, p + 4 * D,
+         B, T, Hq, Hkv, D, qs, ks, dqs, dks, eps, GRAD_FP32 if dt == torch.float32 else 0, workspace.data_ptr(),
+         workspace.numel())
+    return dq, dk, dw[0], dw[1]
+
+
+def paged_cache(num_pages, page_size, Hkv, D, device):
+    """Empty page pools [num_pages, Hkv, page_size, D]: rotated keys (fp16) and values (bf16)."""
+    shape = (num_pages, Hkv, page_size, D)
+    return (torch.zeros(shape, dtype=torch.float16, device=device),
+            torch.zeros(shape, dtype=torch.bfloat16, device=device))
+
+
+def _pools(k_pages, v_pages, Hkv, D, device):
+    """(number of pages, page size, page stride) of the two pools."""
+    P, H, page, d = k_pages.shape
+    _need(v_pages.shape == k_pages.shape and H == Hkv and d == D, "pools must be [num_pages, Hkv, page_size, D]")
+    _need(k_pages.dtype == torch.float16 and v_pages.dtype == torch.bfloat16 and k_pages.device == device
+          and v_pages.device == device, "pools must be float16 keys and bfloat16 values on the call's CUDA device")
+    stride = k_pages.stride(0) if P > 1 else Hkv * page * D
+    for t in (k_pages, v_pages):
+        s = t.stride()
+        _need(s[3] == 1 and s[2] == D and (H == 1 or s[1] == page * D) and (P == 1 or s[0] == stride),
+              "pools must be contiguous inside a page and have one page stride")
+    return P, page, stride
+
+
+def kv_append_paged(k_new, v_new, k_pages, v_pages, page_table, pos0, cu_new=None, k_weight=None, eps=1e-6,
+                    rope_base=10000.0, rope_half=False, stream=None):
+    """Writes new keys and values [N,Hkv,D] (bf16, rows may be strided) into a paged cache
+    (ne_attn_kv_append_paged).
+
+    page_table int32 [B, max_pages], pos0 int32 [B] (the first new position of each
+    sequence) and cu_new int32 [B + 1] (its rows; None: N / B each) are CUDA tensors.
+    k_weight [D]: the keys are normalised first.  Bad pages are found by check_status."""
+    N, Hkv, D = k_new.shape
+    dev = k_new.device
+    _need(v_new.shape == k_new.shape, "k_new and v_new must have one shape")
+    ks, vs = _head_rows(k_new, "k_new"), _head_rows(v_new, "v_new", device=dev)
+    P, page, stride = _pools(k_pages, v_pages, Hkv, D, dev)
+    B, width = page_table.shape
+    _int32(page_table, "page_table", dev, (B, width))
+    _int32(pos0, "pos0", dev, (B,))
+    if cu_new is not None:
+        _int32(cu_new, "cu_new", dev, (B + 1,))
+    if k_weight is not None:
+        _vector(k_weight, D, "k_weight", dev)
+    if N == 0:
+        return
+    _run("ne_attn_kv_append_paged", dev, stream, (), k_new.data_ptr(), v_new.data_ptr(), _optr(k_weight),
+         k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(), pos0.data_ptr(), _optr(cu_new), N, B, Hkv, D,
+         page, P, width, stride, ks, vs, eps, rope_base, ROPE_HALF if rope_half else 0)
+
+
+@functools.lru_cache(maxsize=256)
+def decode_paged_workspace_size(B, Tq, Hq, Hkv, D, prefix_len=0):
+    return int(lib().ne_attn_decode_paged_workspace_size(B, Tq, Hq, Hkv, D, prefix_len))
+
+
+def attn_decode_paged(q, k_pages, v_pages, page_table, kv_len, q_weight=None, eps=1e-6, rope_base=10000.0,
+                      prefix_table=None, prefix_len=0, o=None, lse=None, o_dtype=torch.bfloat16, workspace=None,
+                      rope_half=False, stream=None):
+    """o, lse for the newest Tq tokens q [B,Tq,Hq,D] (bf16) of every sequence over a paged
+    cache (ne_attn_decode_paged).
+
+    kv_len int32 [B] counts the cached positions, the new tokens' own included (0: an
+    idle slot, whose o is 0 and lse -inf).  q_weight [D]: the queries are normalised
+    first.  prefix_table int32 and prefix_len: the first prefix_len positions (whole
+    pages) of every sequence are these pages, read once for the batch."""
+    B, Tq, Hq, D = q.shape
+    Hkv, dev = k_pages.shape[1], q.device
+    qs = _head_rows(q, "q")
+    P, page, stride = _pools(k_pages, v_pages, Hkv, D, dev)
+    width = page_table.shape[1]
+    _int32(page_table, "page_table", dev, (B, width))
+    _int32(kv_len, "kv_len", dev, (B,))
+    if q_weight is not None:
+        _vector(q_weight, D, "q_weight", dev)
+    if prefix_len:
+        _need(prefix_table is not None and prefix_table.dim() == 1 and prefix_table.numel() * page >= prefix_len,
+              "prefix_table must hold the pages of prefix_len positions")
+        _int32(prefix_table, "prefix_table", dev, tuple(prefix_table.shape))
+    made = []
+    if o is None:
+        o = torch.empty((B, Tq, Hq, D), dtype=o_dtype, device=dev)
+        made.append(o)
+    if lse is None:
+        lse = torch.empty((B, Hq, Tq), dtype=torch.float32, device=dev)
+        made.append(lse)
+    _need(o.dtype in (torch.bfloat16, torch.float32) and o.device == dev and o.is_contiguous()
+          and o.shape == (B, Tq, Hq, D), "o must be a contiguous bfloat16 or float32 [B, Tq, Hq, D]")
+    _need(lse.dtype == torch.float32 and lse.device == dev and lse.is_contiguous() and lse.shape == (B, Hq, Tq),
+          "lse must be a contiguous float32 [B, Hq, Tq]")
+    if workspace is None:
+        n = decode_paged_workspace_size(B, Tq, Hq, Hkv, D, prefix_len)
+        workspace = torch.empty(max(n, 1), dtype=torch.uint8, device=dev)
+        made.append(workspace)
+    _need(workspace.dtype == torch.uint8 and workspace.device == dev, "workspace must be uint8 on the call's device")
+    flags = (O_FP32 if o.dtype == torch.float32 else 0) | (ROPE_HALF if rope_half else 0)
+    _run("ne_attn_decode_paged", dev, stream, made, q.data_ptr(), _optr(q_weight), k_pages.data_ptr(),
+         v_pages.data_ptr(), page_table.data_ptr(), kv_len.data_ptr(), _optr(prefix_table) if prefix_len else None,
+         o.data_ptr(), lse.data_ptr(), B, Tq, Hq, Hkv, D, page, P, width, stride, qs, prefix_len, eps, rope_base,
+         flags, workspace.data_ptr(), workspace.numel())
+    return o, lse
 
 
 class HostStepPipeline:

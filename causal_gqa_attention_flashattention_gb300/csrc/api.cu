@@ -154,10 +154,15 @@ int rope_table(DeviceState& d, int D, double base, int Tneed, cudaStream_t s, co
       *out = t.ptr;
       return NE_OK;
     }
+  // Building one allocates and waits for the build, so that a call on another
+  // stream may use it at once; neither can be done under stream capture.
+  cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(s, &cs) != cudaSuccess) return NE_ERR_CUDA;
+  if (cs != cudaStreamCaptureStatusNone) return NE_ERR_WORKSPACE;
   int Tcap = ((Tneed + 1023) / 1024) * 1024;
   float2* p = nullptr;
   if (cudaMalloc(&p, sizeof(float2) * (size_t)Tcap * (D / 2)) != cudaSuccess) return NE_ERR_CUDA;
-  if (launch_rope_table(p, Tcap, D, base, s) != cudaSuccess) {
+  if (launch_rope_table(p, Tcap, D, base, s) != cudaSuccess || cudaStreamSynchronize(s) != cudaSuccess) {
     cudaFree(p);
     return NE_ERR_CUDA;
   }
@@ -455,6 +460,49 @@ int check_decode_shape(int B, int Tq, int Tkv, int Tcap, int Hq, int Hkv, int D)
   return NE_OK;
 }
 
+
+// Rows of H * D values `stride` values apart, 16-byte steps.
+bool row_stride_ok(long long stride, int H, int D) {
+  return stride >= (long long)H * D && stride % 8 == 0 && stride < (1LL << 40);
+}
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+int log2_of(int v) {
+  int s = 0;
+  while ((1 << s) < v) s++;
+  return s;
+}
+
+// Weight-gradient partials [blocks, 2 D] of the query/key norms' backward, for the most blocks it launches.
+size_t qk_norm_bwd_ws_bytes(int D) { return ws_up(sizeof(float) * 2 * D * kQkNormMaxSms * kQkNormBlocksPerSm); }
+
+// Paged cache: page sizes, the pool's stride, and the longest sequence a table
+// row can hold (its positions index the rotary table).
+constexpr int kPagedMaxBatch = 4096;
+constexpr int kPagedMaxPositions = 1 << 20;
+int check_paged(int B, int Hq, int Hkv, int D, int page_size, int num_pages, int max_pages, long long page_stride) {
+  if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || num_pages < 1 || max_pages < 1) return NE_ERR_ARG;
+  if (D != 32 && D != 64) return NE_ERR_UNSUPPORTED;
+  if (page_size < 16 || page_size > 256 || (page_size & (page_size - 1)) != 0) return NE_ERR_UNSUPPORTED;
+  if (B > kPagedMaxBatch || Hq > 32767 || (long long)max_pages * page_size > kPagedMaxPositions)
+    return NE_ERR_UNSUPPORTED;
+  if (page_stride < (long long)Hkv * page_size * D || page_stride % 8 != 0) return NE_ERR_ARG;
+  if (page_stride >= (1LL << 39)) return NE_ERR_UNSUPPORTED;  // a tensor map's stride, in bytes
+  return NE_OK;
+}
+int check_decode_paged_rows(int B, int Tq, int Hq, int Hkv, int D) {
+  if ((long long)(Hq / Hkv) * Tq > kTile) return NE_ERR_UNSUPPORTED;
+  if ((long long)B * Tq * Hq * D >= (1LL << 31)) return NE_ERR_UNSUPPORTED;
+  return NE_OK;
+}
+
+// The current device, its state and its number of SMs.  Requires g_mu held.
+int device_and_sms(int* dev, DeviceState** d, int* nsm) {
+  int st = current_device(dev);
+  if (st != NE_OK) return st;
+  if ((st = device_state(*dev, d)) != NE_OK) return st;
+  if (cudaDeviceGetAttribute(nsm, cudaDevAttrMultiProcessorCount, *dev) != cudaSuccess || *nsm < 1) return NE_ERR_CUDA;
+  return NE_OK;
+}
 
 // RMSNorm + projection: the attention shape rules, C % 8 == 0 (16-byte rows),
 // and every row-major index within 2^31 elements.
@@ -958,6 +1006,8 @@ const char* ne_attn_status_string(int status) {
     case NE_ERR_SCRATCH_LIMIT:
       return "problem needs more scratch than the fixed NE_ATTN_STATIC_SCRATCH_BYTES array of "
              "ne_attn_bwd_noalloc holds; use ne_attn_bwd with a caller workspace";
+    case NE_ERR_PAGE:
+      return "a page table entry outside the pool, or a position outside the page table, was met on the device";
     default: return "unknown status";
   }
 }
@@ -1141,6 +1191,226 @@ int ne_attn_decode(const void* q, const void* k_cache, const void* v_cache, void
   }
   ProfScope prof(NE_ATTN_KERNEL_DECODE, s);
   return launch_decode(a, nsm, s) == cudaSuccess ? NE_OK : NE_ERR_CUDA;
+}
+
+// ------------------------------------------------------------------ query/key norms
+size_t ne_attn_qk_norm_bwd_workspace_size(int B, int T, int Hq, int Hkv, int D) {
+  if (check_shape(B, T, Hq, Hkv, D) != NE_OK) return 0;
+  return qk_norm_bwd_ws_bytes(D);
+}
+
+int ne_attn_qk_norm(const void* q, const void* k, const void* q_w, const void* k_w, int B, int T, int Hq, int Hkv,
+                    int D, long long q_stride, long long k_stride, float eps, float rope_base, int flags,
+                    void* workspace, size_t workspace_bytes, void* stream) {
+  if (!q || !k || !q_w || !k_w) return NE_ERR_ARG;
+  if ((flags & ~kFlagRopeHalf) != 0) return NE_ERR_ARG;
+  if (!(eps > 0.0f) || !std::isfinite(eps)) return NE_ERR_ARG;
+  if (!(rope_base > 1.0f) || !std::isfinite(rope_base)) return NE_ERR_ARG;
+  int st = check_shape(B, T, Hq, Hkv, D);
+  if (st != NE_OK) return st;
+  if (!row_stride_ok(q_stride, Hq, D) || !row_stride_ok(k_stride, Hkv, D)) return NE_ERR_ARG;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(q_w) || !aligned16(k_w)) return NE_ERR_ALIGN;
+  if (!workspace || workspace_bytes < fwd_ws_bytes(B, T, Hq, Hkv, D) ||
+      (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+    return NE_ERR_WORKSPACE;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  std::lock_guard<std::mutex> lock(g_mu);
+  int dev, nsm = 0;
+  DeviceState* d;
+  if ((st = device_and_sms(&dev, &d, &nsm)) != NE_OK) return st;
+  QkNormArgs a;
+  std::memset(&a, 0, sizeof(a));
+  if ((st = rope_table(*d, D, (double)rope_base, T, s, &a.rope)) != NE_OK) return st;
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.k = static_cast<const __nv_bfloat16*>(k);
+  a.qw = static_cast<const __nv_bfloat16*>(q_w);
+  a.kw = static_cast<const __nv_bfloat16*>(k_w);
+  a.qr = static_cast<__half*>(workspace);
+  a.kr = reinterpret_cast<__half*>(static_cast<unsigned char*>(workspace) + ws_up(2 * (size_t)B * T * Hq * D));
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.B = B;
+  a.T = T;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.rope_half = (flags & kFlagRopeHalf) ? 1 : 0;
+  a.eps = eps;
+  a.div_t = make_fastdiv((uint32_t)T);
+  const int per = qk_norm_heads_per_item(false);
+  a.div_hg = make_fastdiv((uint32_t)((Hq + Hkv + per - 1) / per));
+  ProfScope prof(NE_ATTN_KERNEL_QK_NORM, s);
+  return launch_qk_norm(a, D, nsm, s) == cudaSuccess ? NE_OK : NE_ERR_CUDA;
+}
+
+int ne_attn_qk_norm_bwd(const void* q, const void* k, const void* q_w, const void* k_w, const void* dqn,
+                        const void* dkn, void* dq, void* dk, float* dq_w, float* dk_w, int B, int T, int Hq, int Hkv,
+                        int D, long long q_stride, long long k_stride, long long dq_stride, long long dk_stride,
+                        float eps, int flags, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!q || !k || !q_w || !k_w || !dqn || !dkn || !dq || !dk || !dq_w || !dk_w) return NE_ERR_ARG;
+  if ((flags & ~kFlagGradFp32) != 0) return NE_ERR_ARG;
+  if (!(eps > 0.0f) || !std::isfinite(eps)) return NE_ERR_ARG;
+  int st = check_shape(B, T, Hq, Hkv, D);
+  if (st != NE_OK) return st;
+  if (!row_stride_ok(q_stride, Hq, D) || !row_stride_ok(k_stride, Hkv, D) || !row_stride_ok(dq_stride, Hq, D) ||
+      !row_stride_ok(dk_stride, Hkv, D))
+    return NE_ERR_ARG;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(q_w) || !aligned16(k_w) || !aligned16(dqn) || !aligned16(dkn) ||
+      !aligned16(dq) || !aligned16(dk) || !aligned16(dq_w) || !aligned16(dk_w))
+    return NE_ERR_ALIGN;
+  if (!workspace || workspace_bytes < qk_norm_bwd_ws_bytes(D) || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+    return NE_ERR_WORKSPACE;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  std::lock_guard<std::mutex> lock(g_mu);
+  int dev, nsm = 0;
+  DeviceState* d;
+  if ((st = device_and_sms(&dev, &d, &nsm)) != NE_OK) return st;
+  QkNormBwdArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.k = static_cast<const __nv_bfloat16*>(k);
+  a.qw = static_cast<const __nv_bfloat16*>(q_w);
+  a.kw = static_cast<const __nv_bfloat16*>(k_w);
+  a.gq = dqn;
+  a.gk = dkn;
+  a.dq = dq;
+  a.dk = dk;
+  a.part = static_cast<float*>(workspace);
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.dq_stride = dq_stride;
+  a.dk_stride = dk_stride;
+  a.B = B;
+  a.T = T;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.eps = eps;
+  const int per = qk_norm_heads_per_item(true);
+  a.div_hg = make_fastdiv((uint32_t)((Hq + Hkv + per - 1) / per));
+  const int blocks = qk_norm_bwd_blocks(B, T, (int)a.div_hg.d, D, nsm);
+  {
+    ProfScope prof(NE_ATTN_KERNEL_QK_NORM_BWD, s);
+    if (launch_qk_norm_bwd(a, D, (flags & kFlagGradFp32) != 0, blocks, s) != cudaSuccess) return NE_ERR_CUDA;
+  }
+  ProfScope prof(NE_ATTN_KERNEL_QK_NORM_DW, s);
+  return launch_qk_norm_dw(a, D, blocks, dq_w, dk_w, s) == cudaSuccess ? NE_OK : NE_ERR_CUDA;
+}
+
+// ------------------------------------------------------------------ paged cache
+int ne_attn_kv_append_paged(const void* k_new, const void* v_new, const void* k_w, void* k_pages, void* v_pages,
+                            const int* page_table, const int* pos0, const int* cu_new, int N, int B, int Hkv, int D,
+                            int page_size, int num_pages, int max_pages, long long page_stride, long long k_stride,
+                            long long v_stride, float eps, float rope_base, int flags, void* stream) {
+  if (!k_new || !v_new || !k_pages || !v_pages || !page_table || !pos0) return NE_ERR_ARG;
+  if ((flags & ~kFlagRopeHalf) != 0) return NE_ERR_ARG;
+  if (k_w && (!(eps > 0.0f) || !std::isfinite(eps))) return NE_ERR_ARG;
+  if (!(rope_base > 1.0f) || !std::isfinite(rope_base)) return NE_ERR_ARG;
+  if (N < 1 || (!cu_new && B >= 1 && N % B != 0)) return NE_ERR_ARG;
+  int st = check_paged(B, Hkv, Hkv, D, page_size, num_pages, max_pages, page_stride);
+  if (st != NE_OK) return st;
+  if ((long long)N * Hkv * D >= (1LL << 31)) return NE_ERR_UNSUPPORTED;
+  if (!row_stride_ok(k_stride, Hkv, D) || !row_stride_ok(v_stride, Hkv, D)) return NE_ERR_ARG;
+  if (!aligned16(k_new) || !aligned16(v_new) || !aligned16(k_pages) || !aligned16(v_pages) || (k_w && !aligned16(k_w)) ||
+      !aligned4(page_table) || !aligned4(pos0) || !aligned4(cu_new))
+    return NE_ERR_ALIGN;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  std::lock_guard<std::mutex> lock(g_mu);
+  int dev, nsm = 0;
+  DeviceState* d;
+  if ((st = device_and_sms(&dev, &d, &nsm)) != NE_OK) return st;
+  PagedAppendArgs a;
+  std::memset(&a, 0, sizeof(a));
+  if ((st = rope_table(*d, D, (double)rope_base, max_pages * page_size, s, &a.rope)) != NE_OK) return st;
+  a.k = static_cast<const __nv_bfloat16*>(k_new);
+  a.v = static_cast<const __nv_bfloat16*>(v_new);
+  a.kw = static_cast<const __nv_bfloat16*>(k_w);
+  a.kp = static_cast<__half*>(k_pages);
+  a.vp = static_cast<__nv_bfloat16*>(v_pages);
+  a.table = page_table;
+  a.pos0 = pos0;
+  a.cu = cu_new;
+  a.status = d->status;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.page_stride = page_stride;
+  a.N = N;
+  a.B = B;
+  a.Hkv = Hkv;
+  a.page_shift = log2_of(page_size);
+  a.num_pages = num_pages;
+  a.max_pages = max_pages;
+  a.rope_half = (flags & kFlagRopeHalf) ? 1 : 0;
+  a.eps = eps;
+  a.div_hkv = make_fastdiv((uint32_t)Hkv);
+  a.div_per = make_fastdiv((uint32_t)(cu_new ? 1 : N / B));
+  ProfScope prof(NE_ATTN_KERNEL_KV_APPEND_PAGED, s);
+  return launch_kv_append_paged(a, D, s) == cudaSuccess ? NE_OK : NE_ERR_CUDA;
+}
+
+size_t ne_attn_decode_paged_workspace_size(int B, int Tq, int Hq, int Hkv, int D, int prefix_len) {
+  if (check_paged(B, Hq, Hkv, D, 16, 1, 1, 16LL * Hkv * D) != NE_OK || Tq < 1 || prefix_len < 0) return 0;
+  if (check_decode_paged_rows(B, Tq, Hq, Hkv, D) != NE_OK) return 0;
+  return 256;
+}
+
+int ne_attn_decode_paged(const void* q, const void* q_w, const void* k_pages, const void* v_pages,
+                         const int* page_table, const int* kv_len, const int* prefix_table, void* o, float* lse, int B,
+                         int Tq, int Hq, int Hkv, int D, int page_size, int num_pages, int max_pages,
+                         long long page_stride, long long q_stride, int prefix_len, float eps, float rope_base,
+                         int flags, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!q || !k_pages || !v_pages || !page_table || !kv_len || !o) return NE_ERR_ARG;
+  if ((flags & ~(kFlagOFp32 | kFlagRopeHalf)) != 0) return NE_ERR_ARG;
+  if (q_w && (!(eps > 0.0f) || !std::isfinite(eps))) return NE_ERR_ARG;
+  if (!(rope_base > 1.0f) || !std::isfinite(rope_base)) return NE_ERR_ARG;
+  if (Tq < 1) return NE_ERR_ARG;
+  int st = check_paged(B, Hq, Hkv, D, page_size, num_pages, max_pages, page_stride);
+  if (st != NE_OK) return st;
+  if ((st = check_decode_paged_rows(B, Tq, Hq, Hkv, D)) != NE_OK) return st;
+  if (!row_stride_ok(q_stride, Hq, D)) return NE_ERR_ARG;
+  if (prefix_len < 0 || prefix_len % page_size != 0 || prefix_len > max_pages * page_size ||
+      (prefix_len > 0 && !prefix_table))
+    return NE_ERR_ARG;
+  if (!aligned16(q) || (q_w && !aligned16(q_w)) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(o) ||
+      !aligned4(lse) || !aligned4(page_table) || !aligned4(kv_len) || !aligned4(prefix_table))
+    return NE_ERR_ALIGN;
+  if (!workspace || workspace_bytes < ne_attn_decode_paged_workspace_size(B, Tq, Hq, Hkv, D, prefix_len) ||
+      (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+    return NE_ERR_WORKSPACE;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  std::lock_guard<std::mutex> lock(g_mu);
+  int dev, nsm = 0;
+  DeviceState* d;
+  if ((st = device_and_sms(&dev, &d, &nsm)) != NE_OK) return st;
+  PagedDecodeArgs a;
+  std::memset(&a, 0, sizeof(a));
+  if ((st = rope_table(*d, D, (double)rope_base, max_pages * page_size, s, &a.rope)) != NE_OK) return st;
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.qw = static_cast<const __nv_bfloat16*>(q_w);
+  a.kp = static_cast<const __half*>(k_pages);
+  a.vp = static_cast<const __nv_bfloat16*>(v_pages);
+  a.table = page_table;
+  a.len = kv_len;
+  a.prefix_table = prefix_table;
+  a.status = d->status;
+  a.o = o;
+  a.lse = lse;
+  a.q_stride = q_stride;
+  a.page_stride = page_stride;
+  a.B = B;
+  a.Tq = Tq;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.D = D;
+  a.G = Hq / Hkv;
+  a.page_shift = log2_of(page_size);
+  a.num_pages = num_pages;
+  a.max_pages = max_pages;
+  a.prefix_len = prefix_len;
+  a.rope_half = (flags & kFlagRopeHalf) ? 1 : 0;
+  a.o_fp32 = (flags & kFlagOFp32) ? 1 : 0;
+  a.eps = eps;
+  a.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)D));
+  ProfScope prof(NE_ATTN_KERNEL_DECODE_PAGED, s);
+  return launch_decode_paged(a, s) == cudaSuccess ? NE_OK : NE_ERR_CUDA;
 }
 
 int ne_attn_debug_fwd_schedule(int B, int Hkv, int G, int nt, int nsm, int* table, int capacity, int* grid,

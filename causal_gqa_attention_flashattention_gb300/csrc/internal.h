@@ -13,6 +13,7 @@ constexpr int kTile = 128;  // query rows / key rows per tile
 
 // Device-side status codes (mirror ne_status in include/ne_attn.h).
 constexpr int kStatusTimeout = -6;
+constexpr int kStatusPage = -8;
 
 // Flag bits shared with include/ne_attn.h.
 constexpr int kFlagOFp32 = 1;      // o is float32
@@ -173,6 +174,85 @@ struct QkvArgs {
   int rope_half;
   float eps;
 };
+
+// Norms of the query and key heads with the rotation, and their backward (see qk_norm.cu).
+struct QkNormArgs {
+  const __nv_bfloat16 *q, *k;    // [B, T, H, D], rows of one position q_stride / k_stride values apart
+  const __nv_bfloat16 *qw, *kw;  // [D]
+  __half *qr, *kr;               // [B, T, Hq, D], [B, T, Hkv, D] rotated
+  const float2* rope;
+  long long q_stride, k_stride;
+  int B, T, Hq, Hkv, rope_half;
+  float eps;
+  FastDiv div_t, div_hg;         // by T and by the head groups of a position
+};
+struct QkNormBwdArgs {
+  const __nv_bfloat16 *q, *k, *qw, *kw;
+  const void *gq, *gk;  // gradients of the normalised q, k [B, T, H, D], bf16 or fp32
+  void *dq, *dk;        // gradients of q, k (same type), rows dq_stride / dk_stride values apart
+  float* part;          // [blocks, 2 D] partial weight gradients (workspace)
+  long long q_stride, k_stride, dq_stride, dk_stride;
+  int B, T, Hq, Hkv;
+  float eps;
+  FastDiv div_hg;
+};
+constexpr int kQkNormMaxSms = 160, kQkNormBlocksPerSm = 4;  // bound the backward's partials
+
+// Append of new keys and values to a paged cache (see paged.cu).
+struct PagedAppendArgs {
+  const __nv_bfloat16 *k, *v, *kw;  // new rows [N, Hkv, D], k_stride / v_stride values apart; kw [D] or null
+  __half* kp;                       // [num_pages, Hkv, page, D] rotated keys, pages page_stride values apart
+  __nv_bfloat16* vp;
+  const int *table, *pos0, *cu;     // [B, max_pages], [B], [B + 1] or null (N / B rows for every sequence)
+  const float2* rope;
+  int* status;
+  long long k_stride, v_stride, page_stride;
+  int N, B, Hkv, page_shift, num_pages, max_pages, rope_half;
+  float eps;
+  FastDiv div_hkv, div_per;         // by Hkv and by N / B (cu null)
+};
+
+// Attention of the newest tokens over a paged cache (see paged.cu).
+struct PagedDecodeArgs {
+  const __nv_bfloat16 *q, *qw;  // [B, Tq, Hq, D], positions q_stride values apart; qw [D] or null
+  const __half* kp;
+  const __nv_bfloat16* vp;
+  const int *table, *len, *prefix_table;
+  const float2* rope;
+  int* status;
+  void* o;
+  float* lse;  // or null
+  long long q_stride, page_stride;
+  int B, Tq, Hq, Hkv, D, G, page_shift, num_pages, max_pages, prefix_len, rope_half, o_fp32;
+  float eps, scale_log2;
+};
+
+// Launch that may start before the kernel ahead of it in the stream ends; the
+// kernel calls pdl_wait before it touches what that one writes.
+#ifdef __CUDACC__
+template <typename... P, typename... A>
+cudaError_t launch_pdl(void (*k)(P...), int grid, int block, size_t smem, cudaStream_t s, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3((unsigned)block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at = {};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k, static_cast<P>(args)...);
+}
+#endif
+
+int qk_norm_heads_per_item(bool bwd);
+cudaError_t launch_qk_norm(const QkNormArgs& a, int D, int nsm, cudaStream_t s);
+int qk_norm_bwd_blocks(int B, int T, int hg, int D, int nsm);
+cudaError_t launch_qk_norm_bwd(const QkNormBwdArgs& a, int D, bool f32, int blocks, cudaStream_t s);
+cudaError_t launch_qk_norm_dw(const QkNormBwdArgs& a, int D, int blocks, float* dwq, float* dwk, cudaStream_t s);
+cudaError_t launch_kv_append_paged(const PagedAppendArgs& a, int D, cudaStream_t s);
+cudaError_t launch_decode_paged(const PagedDecodeArgs& a, cudaStream_t s);
 
 cudaError_t launch_qkv_prep(const QkvArgs& a, cudaStream_t s);
 cudaError_t launch_qkv_gemm(const QkvArgs& a, int BN, int grid, cudaStream_t s);

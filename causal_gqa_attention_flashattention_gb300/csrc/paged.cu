@@ -1,0 +1,220 @@
+// Paged key/value cache (sm_103a): appending new tokens, and the attention of
+// the newest tokens of every sequence over it.
+//
+// The pools hold num_pages pages of `page` positions, head-major inside a page
+// ([num_pages, Hkv, page, D]: rotated keys fp16, values bf16), so that a page of
+// one key/value head is one stretch of memory.  Position j of sequence b lies in
+// row j % page of page table[b, j / page].  Lengths, tables and the places of new
+// tokens are read on the device: a captured graph replays with new ones.  Every
+// table entry is checked against num_pages before it is used; a bad one is
+// recorded in the status word (kStatusPage) and never followed.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "internal.h"
+#include "ptx.cuh"
+#include "rope.cuh"
+
+namespace ne {
+namespace {
+
+constexpr float kLn2 = 0.69314718055994531f;
+
+__device__ __forceinline__ void record_page(int* status) { atomicCAS(status, 0, kStatusPage); }
+
+// ====================================================================== append
+// New row n belongs to the sequence s with cu[s] <= n < cu[s + 1] (rows at or
+// past cu[B] belong to none and are skipped) and to position pos0[s] + n - cu[s].
+// A thread takes one 16-byte chunk of a key row and of the value row; the D / 8
+// threads of a row are neighbouring lanes (the norm adds up squares by shuffles).
+template <int D>
+__global__ void __launch_bounds__(128) k_kv_append_paged(const PagedAppendArgs a) {
+  constexpr int kCPR = D / 8;
+  const int lane = threadIdx.x & 31;
+  const long long total = (long long)a.N * a.Hkv * kCPR;
+  const long long it = blockIdx.x * 128LL + threadIdx.x;
+  if ((it & ~31LL) >= total) return;  // whole warps leave: the rest shuffle together
+  const bool in = it < total;
+  const uint32_t row = (uint32_t)((in ? it : 0) / kCPR);
+  const int c = (int)(it % kCPR);
+  const uint32_t n = fdiv(row, a.div_hkv);
+  const uint32_t g = row - n * a.Hkv;
+  // the row's sequence and position
+  int s = 0, first = 0;
+  bool on = in;
+  if (a.cu) {
+    // last s with cu[s] <= n: 32 probes at a time for the warp's lowest row, then
+    // each lane steps on to its own
+    const int n0 = (int)__shfl_sync(0xffffffffu, n, 0);
+    int lo = 0, hi = a.B;  // the answer is in [lo, hi)
+    while (hi - lo > 1) {
+      const int step = (hi - lo + 31) / 32;
+      const int i = lo + lane * step;
+      const unsigned le = __ballot_sync(0xffffffffu, i < hi && (lane == 0 || a.cu[i] <= n0));
+      const int top = 31 - __clz((int)le);
+      lo += top * step;
+      hi = min(hi, lo + step);
+    }
+    s = lo;
+    while (s + 1 < a.B && a.cu[s + 1] <= (int)n) s++;
+    first = a.cu[s];
+    on = on && (int)n >= first && (int)n < a.cu[a.B];
+  } else {
+    s = (int)fdiv(n, a.div_per);
+    first = s * (int)a.div_per.d;
+  }
+  const int pos = on ? a.pos0[s] + ((int)n - first) : 0;
+  int page = -1;
+  if (on) {
+    const int slot = pos >> a.page_shift;
+    if (pos >= 0 && slot < a.max_pages) page = a.table[(size_t)s * a.max_pages + slot];
+    if (page < 0 || page >= a.num_pages) {
+      record_page(a.status);
+      on = false;
+    }
+  }
+  uint4 kv = make_uint4(0, 0, 0, 0), vv = kv;
+  if (on) {
+    kv = load_rope_chunk<D>(a.k + (size_t)n * a.k_stride + g * D, c, a.rope_half != 0);
+    vv = __ldg(reinterpret_cast<const uint4*>(a.v + (size_t)n * a.v_stride + g * D) + c);
+  }
+  const uint32_t w[4] = {kv.x, kv.y, kv.z, kv.w};
+  float x[8];
+#pragma unroll
+  for (int p = 0; p < 4; p++) {
+    x[2 * p] = bf_lo(w[p]);
+    x[2 * p + 1] = bf_hi(w[p]);
+  }
+  if (a.kw) {
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; i++) ss = fmaf(x[i], x[i], ss);
+#pragma unroll
+    for (int m = 1; m < kCPR; m <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
+    const float r = rsqrtf(fmaf(ss, 1.f / D, a.eps));
+    const uint4 wv = load_rope_chunk<D>(a.kw, c, a.rope_half != 0);
+    const uint32_t ww[4] = {wv.x, wv.y, wv.z, wv.w};
+#pragma unroll
+    for (int p = 0; p < 4; p++) {
+      x[2 * p] *= r * bf_lo(ww[p]);
+      x[2 * p + 1] *= r * bf_hi(ww[p]);
+    }
+  }
+  if (!on) return;
+  float4 c0, c1;
+  rope_coeffs<D>(a.rope, pos, c, c0, c1);
+  const float cs[4] = {c0.x, c0.z, c1.x, c1.z}, sn[4] = {c0.y, c0.w, c1.y, c1.w};
+  uint32_t o[4];
+#pragma unroll
+  for (int p = 0; p < 4; p++)
+    o[p] = pack_f16(fmaf(x[2 * p], cs[p], -x[2 * p + 1] * sn[p]), fmaf(x[2 * p], sn[p], x[2 * p + 1] * cs[p]));
+  const size_t dst = (size_t)page * a.page_stride +
+                     (((size_t)g << a.page_shift) + (pos & ((1 << a.page_shift) - 1))) * D;
+  reinterpret_cast<uint4*>(a.kp + dst)[c] = make_uint4(o[0], o[1], o[2], o[3]);
+  reinterpret_cast<uint4*>(a.vp + dst)[c] = vv;
+}
+
+// ====================================================================== attention
+// One block per (sequence, new token, query head), one key per thread at a time:
+// running maximum and sum, O in registers, the threads merged at the end.
+template <int D>
+__global__ void __launch_bounds__(128) k_decode_paged(const PagedDecodeArgs a) {
+  const int h = blockIdx.x % a.Hq, bt = blockIdx.x / a.Hq;
+  const int t = bt % a.Tq, b = bt / a.Tq, g = h / a.G, tid = threadIdx.x;
+  __shared__ float qs[D];
+  __shared__ float red[128];
+  __shared__ float acc[D];
+  int len = a.len[b];
+  const int cap = a.max_pages << a.page_shift;
+  if (len > cap) {
+    if (tid == 0) record_page(a.status);
+    len = cap;
+  }
+  const int pos = len - a.Tq + t;
+  if (tid < D / 2) {
+    const __nv_bfloat16* q = a.q + (size_t)bt * a.q_stride + h * D;
+    const int i0 = a.rope_half ? tid : 2 * tid, i1 = a.rope_half ? tid + D / 2 : 2 * tid + 1;
+    float x0 = __bfloat162float(q[i0]), x1 = __bfloat162float(q[i1]);
+    if (a.qw) {
+      float ss = 0.f;
+      for (int i = 0; i < D; i++) ss += __bfloat162float(q[i]) * __bfloat162float(q[i]);
+      const float r = rsqrtf(ss / D + a.eps);
+      x0 *= r * __bfloat162float(a.qw[i0]);
+      x1 *= r * __bfloat162float(a.qw[i1]);
+    }
+    const float2 cs = a.rope[(size_t)max(pos, 0) * (D / 2) + tid];
+    qs[2 * tid] = x0 * cs.x - x1 * cs.y;
+    qs[2 * tid + 1] = x0 * cs.y + x1 * cs.x;
+  }
+  __syncthreads();
+  float m = -INFINITY, l = 0.f, o[D];
+#pragma unroll
+  for (int i = 0; i < D; i++) o[i] = 0.f;
+  for (int j = tid; j <= pos; j += 128) {
+    const int slot = j >> a.page_shift;
+    const int page = j < a.prefix_len ? a.prefix_table[slot] : a.table[(size_t)b * a.max_pages + slot];
+    const bool ok = page >= 0 && page < a.num_pages;
+    if (!ok) record_page(a.status);
+    const size_t at = (size_t)(ok ? page : 0) * a.page_stride +
+                      (((size_t)g << a.page_shift) + (j & ((1 << a.page_shift) - 1))) * D;
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < D; i++) s = fmaf(qs[i], ok ? __half2float(a.kp[at + i]) : 0.f, s);
+    s *= a.scale_log2;
+    const float mn = fmaxf(m, s), al = exp2f(m - mn), p = exp2f(s - mn);
+    l = l * al + p;
+#pragma unroll
+    for (int i = 0; i < D; i++) o[i] = fmaf(p, ok ? __bfloat162float(a.vp[at + i]) : 0.f, o[i] * al);
+    m = mn;
+  }
+  red[tid] = m;
+  __syncthreads();
+  float M = -INFINITY;
+  for (int i = 0; i < 128; i++) M = fmaxf(M, red[i]);
+  __syncthreads();
+  const float w = m == -INFINITY ? 0.f : exp2f(m - M);
+  red[tid] = w * l;
+  if (tid < D) acc[tid] = 0.f;
+  __syncthreads();
+  float L = 0.f;
+  for (int i = 0; i < 128; i++) L += red[i];
+  for (int k = 0; k < 128; k++) {
+    if (tid == k) {
+#pragma unroll
+      for (int i = 0; i < D; i++) acc[i] += w * o[i];
+    }
+    __syncthreads();
+  }
+  if (tid < D) {
+    const float v = L > 0.f ? acc[tid] / L : 0.f;
+    const size_t at = ((size_t)bt * a.Hq + h) * D + tid;
+    if (a.o_fp32)
+      static_cast<float*>(a.o)[at] = v;
+    else
+      static_cast<__nv_bfloat16*>(a.o)[at] = __float2bfloat16_rn(v);
+  }
+  if (tid == 0 && a.lse) a.lse[((size_t)b * a.Hq + h) * a.Tq + t] = L > 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
+}
+
+}  // namespace
+
+cudaError_t launch_kv_append_paged(const PagedAppendArgs& a, int D, cudaStream_t s) {
+  const long long n = (long long)a.N * a.Hkv * (D / 8);
+  const unsigned grid = (unsigned)((n + 127) / 128);
+  if (D == 64)
+    k_kv_append_paged<64><<<grid, 128, 0, s>>>(a);
+  else
+    k_kv_append_paged<32><<<grid, 128, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_decode_paged(const PagedDecodeArgs& a, cudaStream_t s) {
+  const unsigned grid = (unsigned)(a.B * a.Tq * a.Hq);
+  if (a.D == 64)
+    k_decode_paged<64><<<grid, 128, 0, s>>>(a);
+  else
+    k_decode_paged<32><<<grid, 128, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace ne

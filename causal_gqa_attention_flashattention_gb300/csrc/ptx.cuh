@@ -432,6 +432,14 @@ __device__ __forceinline__ void regs_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+// ------------------------------------------------------------------ dependent launches
+// A kernel launched by launch_pdl may start while the kernel before it in the
+// stream still runs.  pdl_wait holds until that kernel has finished and its
+// writes are visible; without a launch attribute it returns at once.  pdl_launch
+// lets the next kernel start once every block has called it or ended.
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // ------------------------------------------------------------------ misc math
 __device__ __forceinline__ float ex2(float x) {
   float y;

@@ -26,7 +26,8 @@
  * 16-byte aligned; the caller owns every buffer.
  *
  * Every call is asynchronous on `stream` (a cudaStream_t; NULL is the legacy
- * default stream): no host synchronisation, no host<->device copies.  Argument
+ * default stream): no host synchronisation, no host<->device copies (but for
+ * the first call of a new table, below).  Argument
  * errors are detected on the host and returned before anything is launched.
  * A kernel whose internal pipeline wait exceeds its time limit stops, frees
  * its tensor memory and records NE_ERR_DEVICE_TIMEOUT in a device status word
@@ -36,9 +37,10 @@
  * cos/sin of t * theta_i for t below the largest T seen so far, built on the
  * device in double precision; and, per forward shape, the table of work items
  * of each CTA of the persistent forward kernel (built on the host, copied once).
- * The first call that needs a new or larger table allocates it with
- * cudaMalloc, so make one call per shape (with the largest T) before capturing
- * calls in a CUDA graph.  Calls that pass no workspace use a buffer of the
+ * The first call that needs a new or larger table allocates it with cudaMalloc
+ * and waits for its build, so make one call per shape (with the largest T)
+ * before capturing calls in a CUDA graph (a captured call that needs a new
+ * rotary table returns NE_ERR_WORKSPACE).  Calls that pass no workspace use a buffer of the
  * library's per stream (see ne_attn_fwd_ex).  Nothing else is allocated.
  */
 #ifndef NE_ATTN_H
@@ -58,7 +60,9 @@ typedef enum {
   NE_ERR_CUDA = -4,           /* a CUDA runtime/driver call or a launch failed */
   NE_ERR_WORKSPACE = -5,      /* workspace missing, too small or not 256-byte aligned */
   NE_ERR_DEVICE_TIMEOUT = -6, /* a kernel gave up on a pipeline wait (see above) */
-  NE_ERR_SCRATCH_LIMIT = -7   /* ne_attn_bwd_noalloc: problem too large for its fixed scratch */
+  NE_ERR_SCRATCH_LIMIT = -7,  /* ne_attn_bwd_noalloc: problem too large for its fixed scratch */
+  NE_ERR_PAGE = -8            /* a kernel met a page table entry outside the pool, or a position outside
+                                 the page table (read by ne_attn_check_status) */
 } ne_status;
 
 /* Flag bits for ne_attn_fwd_ex, ne_attn_bwd and the workspace-size queries. */
@@ -294,11 +298,115 @@ int ne_attn_qkv_rmsnorm(const void* x, const void* norm_w, const void* w_qkv, vo
                         int flags, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * Norms of the query and key heads with the rotary embedding in the same pass,
+ * for models that normalise each head before attention: for x = q[b,t,h,:] (or
+ * k[b,t,g,:]) and the weight w = q_w (k_w) [D], shared by the heads,
+ *
+ *   n_d = x_d w_d / sqrt(mean_d x_d^2 + eps),   the attention then sees R_t n
+ *
+ * q [B,T,Hq,D] and k [B,T,Hkv,D] are bfloat16, q_w and k_w [D] bfloat16.  The
+ * heads of a position are contiguous; positions lie q_stride (k_stride) values
+ * apart (b * T + t rows; at least H * D, a multiple of 8), so q and k may be
+ * slices of a fused projection's rows.  Writes the rotated q and k (fp16) into
+ * the first ne_attn_fwd_workspace_size(.., 0) bytes of `workspace` (required,
+ * 256-byte aligned), where ne_attn_fwd_ex and ne_attn_bwd take them with
+ * NE_ATTN_QK_ROTATED (q and k NULL, same workspace and rotary layout).  That
+ * backward's dq and dk are the gradients of the normalised, un-rotated n.
+ * flags: NE_ATTN_ROPE_HALF or 0.  One streaming kernel.
+ */
+int ne_attn_qk_norm(const void* q, const void* k, const void* q_w, const void* k_w, int B, int T, int Hq, int Hkv,
+                    int D, long long q_stride, long long k_stride, float eps, float rope_base, int flags,
+                    void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Backward of the norms: from dqn [B,T,Hq,D] and dkn [B,T,Hkv,D] (contiguous, as
+ * ne_attn_bwd writes dq and dk), with xh = x / sqrt(mean x^2 + eps):
+ *   dx = (w dn - xh mean_d(w dn xh)) / sqrt(mean x^2 + eps)   per row,
+ *   dw = sum over every batch, position and head of dn xh     (float32 [D]).
+ * q, k, q_w, k_w, eps as given to ne_attn_qk_norm.  flags: NE_ATTN_GRAD_FP32
+ * (dqn, dkn, dq, dk are float32, else bfloat16).  dq and dk have row strides of
+ * their own and may be the buffers of dqn and dkn (with the contiguous stride).
+ * The rotary layout does not enter.  The workspace
+ * (ne_attn_qk_norm_bwd_workspace_size bytes, 256-byte aligned) is required.
+ * Two kernels: the rows, with the weight gradients summed per block in fp32;
+ * then the blocks' sums in a fixed order (bitwise reproducible).
+ */
+size_t ne_attn_qk_norm_bwd_workspace_size(int B, int T, int Hq, int Hkv, int D);
+int ne_attn_qk_norm_bwd(const void* q, const void* k, const void* q_w, const void* k_w, const void* dqn,
+                        const void* dkn, void* dq, void* dk, float* dq_w, float* dk_w, int B, int T, int Hq, int Hkv,
+                        int D, long long q_stride, long long k_stride, long long dq_stride, long long dk_stride,
+                        float eps, int flags, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Paged key/value cache.  The pools hold num_pages pages of page_size positions:
+ *   k_pages : [num_pages, Hkv, page_size, D] fp16, the rotated keys
+ *   v_pages : [num_pages, Hkv, page_size, D] bfloat16
+ * with consecutive pages page_stride values apart in both pools (at least
+ * Hkv * page_size * D, a multiple of 8: the pools of several layers may be
+ * interleaved page by page).  Position j of sequence b lies in row
+ * j % page_size of page page_table[b, j / page_size].  page_table [B, max_pages],
+ * the lengths and the places of new tokens are int32 arrays in device memory and
+ * are read when the kernels run, so a captured CUDA graph replays with new ones.
+ * page_size is 16, 32, 64, 128 or 256; B <= 4096; max_pages * page_size <= 2^20.
+ * Table entries that a call needs are checked against num_pages on the device: a
+ * page outside the pool, or a position outside the table, is recorded as
+ * NE_ERR_PAGE in the status word and never followed.  The table entries of
+ * positions that a call does not reach are not used and may hold anything.
+ *
+ * ne_attn_kv_append_paged writes the new rows k_new, v_new [N, Hkv, D] (bfloat16,
+ * rows k_stride / v_stride values apart) of a ragged batch: rows cu_new[b] ..
+ * cu_new[b+1] - 1 belong to sequence b and go to its positions pos0[b],
+ * pos0[b] + 1, ...; rows at or past cu_new[B] are padding and are not read.
+ * cu_new [B + 1] rises from 0; with cu_new = NULL every sequence has N / B rows.
+ * Each key is normalised with k_w [D] as in ne_attn_qk_norm (k_w = NULL: not),
+ * rotated at its position and stored as fp16; each value is copied.  A row
+ * whose place is bad (see above) is not written.  No two rows may have one
+ * place.  flags: NE_ATTN_ROPE_HALF or 0, as later given to ne_attn_decode_paged.
+ * One streaming kernel.
+ */
+int ne_attn_kv_append_paged(const void* k_new, const void* v_new, const void* k_w, void* k_pages, void* v_pages,
+                            const int* page_table, const int* pos0, const int* cu_new, int N, int B, int Hkv, int D,
+                            int page_size, int num_pages, int max_pages, long long page_stride, long long k_stride,
+                            long long v_stride, float eps, float rope_base, int flags, void* stream);
+
+/*
+ * Attention of the newest tokens over a paged cache.  kv_len[b] positions of
+ * sequence b are in the cache, the new ones included; its Tq queries
+ * q[b] [Tq, Hq, D] (bfloat16, positions q_stride values apart; normalised here
+ * with q_w [D] unless NULL, and rotated) sit at positions kv_len[b] - Tq ..
+ * kv_len[b] - 1 and each attends to the positions up to its own.  Writes
+ * o [B,Tq,Hq,D] (bfloat16, or float32 with NE_ATTN_O_FP32) and, unless NULL,
+ * lse [B,Hq,Tq].  A query before position 0 (kv_len[b] < Tq; kv_len[b] <= 0 is
+ * an idle slot of the batch) sees no key: o = 0, lse = -infinity.  A length
+ * past the table is cut to it and recorded as NE_ERR_PAGE; the keys and values
+ * of a bad page count as zeros.
+ *
+ * Shared prefix: with prefix_len > 0 (a multiple of page_size, at most
+ * max_pages * page_size) positions 0 .. prefix_len - 1 of every sequence are the
+ * pages prefix_table[0 .. prefix_len / page_size - 1] (device, int32), and the
+ * first prefix_len / page_size entries of the page_table's rows are not used.
+ * The prefix is then read once for the whole batch, its rows in tiles over all
+ * sequences.  The result is that of the same call with those pages in every
+ * sequence's own table and prefix_len = 0, up to rounding.
+ *
+ * Requires (Hq / Hkv) * Tq <= 128 and the workspace
+ * (ne_attn_decode_paged_workspace_size bytes, 256-byte aligned); calls that may
+ * run at the same time need workspaces of their own.
+ */
+size_t ne_attn_decode_paged_workspace_size(int B, int Tq, int Hq, int Hkv, int D, int prefix_len);
+int ne_attn_decode_paged(const void* q, const void* q_w, const void* k_pages, const void* v_pages,
+                         const int* page_table, const int* kv_len, const int* prefix_table, void* o, float* lse, int B,
+                         int Tq, int Hq, int Hkv, int D, int page_size, int num_pages, int max_pages,
+                         long long page_stride, long long q_stride, int prefix_len, float eps, float rope_base,
+                         int flags, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Synchronises `stream`, then returns and clears the device status word of
- * the current device: NE_OK, NE_ERR_DEVICE_TIMEOUT, or NE_ERR_CUDA if the
- * synchronisation itself failed.  The pages have no counterpart to this
- * call; it reports the one failure the kernels detect themselves, a pipeline
- * wait that gave up, while the GPU context stays usable.
+ * the current device: NE_OK, NE_ERR_DEVICE_TIMEOUT, NE_ERR_PAGE, or NE_ERR_CUDA
+ * if the synchronisation itself failed.  The pages have no counterpart to this
+ * call; it reports the failures the kernels detect themselves, a pipeline
+ * wait that gave up and a bad page of a paged cache, while the GPU context
+ * stays usable.
  */
 int ne_attn_check_status(void* stream);
 
@@ -333,7 +441,12 @@ const char* ne_attn_status_string(int status);
 #define NE_ATTN_KERNEL_DECODE_AUX 7 /* query rotation and packing */
 #define NE_ATTN_KERNEL_QKV_PREP 8   /* RMSNorm row statistics and the weight fold */
 #define NE_ATTN_KERNEL_QKV 9        /* the projection GEMM with the rotary epilogue */
-#define NE_ATTN_NUM_KERNEL_KINDS 10
+#define NE_ATTN_KERNEL_QK_NORM 10       /* query/key norms with the rotation */
+#define NE_ATTN_KERNEL_QK_NORM_BWD 11   /* their backward over the rows */
+#define NE_ATTN_KERNEL_QK_NORM_DW 12    /* the weight gradients' last sum */
+#define NE_ATTN_KERNEL_KV_APPEND_PAGED 13
+#define NE_ATTN_KERNEL_DECODE_PAGED 14  /* the sweep over a paged cache */
+#define NE_ATTN_NUM_KERNEL_KINDS 15
 int ne_attn_profile_start(int capacity);
 int ne_attn_profile_stop(double* total_ms, long long* launches);
 int ne_attn_profile_detach(void);

@@ -1,0 +1,392 @@
+"""Paged key/value cache on the GPU: append and decode against the fp64 definitions
+(oracle/paged.py), and both together against the framework's own attention.
+
+Bounds.  Append: values bit by bit; keys as the norms' forward (test_gpu_qk_norm).
+Decode without a shared prefix carries q as two fp16 parts (2^-22) and the weights
+as two bf16 parts (2^-17), sums in fp32: with M = max_j sum_i |q_i k_ji| / sqrt(D) a
+logit is off by at most d = M (2^-18 for the norm and rotation + 2^-21 for the parts
+and the fp32 sum of D terms), a weight by 2 d + 2^-16 (exp2, parts) relative, so
+  |o error| <= (2 d + 2^-14) A + the output's rounding,  A = sum_j p_j |v_j|
+(2^-14: the weights' 2^-16 and the fp32 sums over up to thousands of keys), and
+  |lse error| <= d + 2^-14 + 2^-22 |lse|.
+With a shared prefix the rows may go through the tiles of the default precision: q as
+one fp16 (2^-11) and the weights as one bf16 (2^-8): d = M 2^-10.9, 2^-8 + 2^-14 in
+place of 2^-14.
+"""
+import numpy as np
+import pytest
+
+import _harness as H
+from causal_gqa_attention_flashattention_gb300 import inputs
+from oracle import paged
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+EPS = 1e-6
+BASE = 10000.0
+
+
+@pytest.fixture(scope="module")
+def nb():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from causal_gqa_attention_flashattention_gb300 import binding
+    binding.lib()
+    return binding
+
+
+def bf16(x):
+    bits = inputs.bf16_round_bits(np.asarray(x, dtype=np.float32))
+    return H.to_device(bits), inputs.bf16_bits_to_f64(bits)
+
+
+def i32(x):
+    return torch.tensor(np.asarray(x, dtype=np.int64), dtype=torch.int32, device="cuda")
+
+
+# ------------------------------------------------------------------ append
+APPENDS = [
+    # new rows per sequence, past, Hkv, D, page, norm, half
+    ([1], [0], 1, 32, 16, False, False),
+    ([1, 1, 1, 1, 1], [0, 15, 16, 17, 100], 4, 64, 16, True, False),
+    ([3, 0, 40, 1, 0, 0, 130], [5, 7, 0, 255, 9, 1, 31], 2, 64, 32, True, True),
+    ([0, 0, 5], [0, 0, 3], 3, 32, 128, True, False),
+    ([200, 33], [250, 0], 4, 64, 256, False, True),
+    ([(i * 7) % 4 for i in range(300)], [i % 50 for i in range(300)], 1, 32, 64, True, False),
+]
+
+
+@pytest.mark.parametrize("case", APPENDS, ids=lambda c: "%d_%dx%d_p%d" % (len(c[0]), c[2], c[3], c[4]))
+@pytest.mark.parametrize("pad", [0, 9])
+def test_append(nb, case, pad):
+    new, past, Hkv, D, page, norm, half = case
+    rng = np.random.default_rng(1)
+    B = len(new)
+    cu = np.concatenate([[0], np.cumsum(new)])
+    N = int(cu[-1]) + pad
+    need = [-(-(a + b) // page) for a, b in zip(past, new)]
+    width = max(need) + 1
+    P = sum(need) + 5
+    perm = rng.permutation(P)
+    table = np.full((B, width), 2 ** 30)  # entries not reached may hold anything
+    at = 0
+    for b in range(B):
+        table[b, :need[b]] = perm[at:at + need[b]]
+        at += need[b]
+    # rows strided: keys and values side by side, as a projection gives them
+    kv, fkv = bf16(rng.standard_normal((N, 2 * Hkv, D)))
+    k, v = kv[:, :Hkv], kv[:, Hkv:]
+    kw, fkw = bf16(1 + 0.3 * rng.standard_normal(D))
+    # the pools of two layers interleaved page by page; the other layer stays as it was
+    kp = torch.full((P, 2, Hkv, page, D), 7.0, dtype=torch.float16, device="cuda")
+    vp = torch.full((P, 2, Hkv, page, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    nb.kv_append_paged(k, v, kp[:, 1], vp[:, 1], i32(table), i32(past), cu_new=i32(cu), k_weight=kw if norm else None,
+                       eps=EPS, rope_base=BASE, rope_half=half)
+    nb.check_status()
+    gk, gv = H.to_f64(kp), H.to_f64(vp)
+    assert (gk[:, 0] == 7).all() and (gv[:, 0] == 7).all()
+    rows = paged.places(table, past, cu, page)
+    wk, wv, tol = np.full(gk[:, 1].shape, 7.0), np.full(gk[:, 1].shape, 7.0), np.zeros(gk[:, 1].shape)
+    if rows:
+        idx = np.array([r[0] for r in rows])
+        n = paged.rms_heads(fkv[idx, :Hkv], fkw if norm else None, EPS)
+        y = paged.rope_at(n, [r[3] for r in rows], BASE, half)
+        pair = np.stack((n[..., :D // 2], n[..., D // 2:]), -1) if half else n.reshape(*n.shape[:-1], D // 2, 2)
+        d = np.repeat(np.linalg.norm(pair, axis=-1), 2, -1) * 2.0 ** -19
+        for i, (r, pg, slot, _) in enumerate(rows):
+            wk[pg, :, slot], wv[pg, :, slot] = y[i], fkv[r, Hkv:]
+            tol[pg, :, slot] = (np.abs(y[i]) + d[i]) * 2.0 ** -11 + d[i] + 2.0 ** -25
+    assert (gv[:, 1] == wv).all()
+    assert (np.abs(gk[:, 1] - wk) <= tol).all()
+
+
+def test_append_even_rows(nb):
+    """cu_new = None: N / B rows for every sequence."""
+    k, v = torch.randn((6, 2, 64), device="cuda").bfloat16(), torch.randn((6, 2, 64), device="cuda").bfloat16()
+    table, pos0 = i32([[1, 2], [0, 3]]), i32([14, 3])
+    a, b = nb.paged_cache(4, 16, 2, 64, "cuda"), nb.paged_cache(4, 16, 2, 64, "cuda")
+    nb.kv_append_paged(k, v, *a, table, pos0)
+    nb.kv_append_paged(k, v, *b, table, pos0, cu_new=i32([0, 3, 6]))
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1]) and (a[1][2, :, 0] == v[2]).all()
+
+
+@pytest.mark.parametrize("bad", [-1, 4, 2 ** 31 - 1, -2 ** 31])
+def test_append_bad_places(nb, bad):
+    """A page outside the pool and a position outside the table: not written, reported."""
+    k, v = torch.ones((3, 1, 32), device="cuda").bfloat16(), torch.ones((3, 1, 32), device="cuda").bfloat16()
+    kp, vp = nb.paged_cache(4, 16, 1, 32, "cuda")
+    nb.kv_append_paged(k, v, kp, vp, i32([[0, 1], [bad, 2], [3, 3]]), i32([0, 5, 32]))
+    assert nb.status_of_last_kernels() == -8
+    assert (vp[0, :, 0] == 1).all() and float(vp.float().sum()) == 32.0
+    nb.kv_append_paged(k[:1], v[:1], kp, vp, i32([[0, 1]]), i32([-1]))
+    assert nb.status_of_last_kernels() == -8
+    nb.kv_append_paged(k[:1], v[:1], kp, vp, i32([[0, 1]]), i32([1]))
+    nb.check_status()
+
+
+# ------------------------------------------------------------------ decode
+def setup(lens, Tq, Hq, Hkv, D, page, seed, prefix=0, scale=1.0, layers=1):
+    """Pools whose unreached rows and pages are NaN, and tables whose unreached entries are wild."""
+    rng = np.random.default_rng(seed)
+    B, shared = len(lens), prefix // page
+    own = [max(0, -(-n // page) - shared) if n > 0 else 0 for n in lens]
+    P = shared + sum(own) + 2
+    perm = rng.permutation(P)
+    width = shared + max(own + [0]) + 1
+    table = np.full((B, width), -2 ** 31)
+    kp, vp = np.full((P, Hkv, page, D), np.nan), np.full((P, Hkv, page, D), np.nan)
+    ptable = perm[:shared]
+    reach = max(0, min(prefix, max(lens)))
+    for i, pg in enumerate(ptable):
+        n = min(page, max(0, reach - i * page))
+        kp[pg, :, :n] = rng.standard_normal((Hkv, n, D)) * scale
+        vp[pg, :, :n] = rng.standard_normal((Hkv, n, D))
+    at = shared
+    for b in range(B):
+        table[b, shared:shared + own[b]] = perm[at:at + own[b]]
+        for i in range(own[b]):
+            n = min(page, lens[b] - prefix - i * page)
+            kp[perm[at + i], :, :n] = rng.standard_normal((Hkv, n, D)) * scale
+            vp[perm[at + i], :, :n] = rng.standard_normal((Hkv, n, D))
+        at += own[b]
+    k16 = kp.astype(np.float16)
+    dvp = torch.from_numpy(vp.astype(np.float32)).cuda().bfloat16()
+    q, fq = bf16(rng.standard_normal((B, Tq, Hq, D)) * scale)
+    qw, fqw = bf16(1 + 0.3 * rng.standard_normal(D))
+    return dict(q=q, qw=qw, kp=torch.from_numpy(k16).cuda(), vp=dvp, table=i32(table), lens=i32(lens),
+                ptable=i32(ptable) if shared else None, fq=fq, fqw=fqw, fk=k16.astype(np.float64),
+                fv=dvp.float().cpu().numpy().astype(np.float64), ftable=table, flens=lens, fptable=list(ptable))
+
+
+def check(nb, s, got, norm, half, prefix=0):
+    o, lse = got
+    nb.check_status()
+    ro, rl, A, M = paged.decode_paged(s["fq"], s["fqw"] if norm else None, s["fk"], s["fv"], s["ftable"], s["flens"], BASE,
+                                      EPS, half, s["fptable"], bounds=True)
+    d = M * (2.0 ** -10.9 if prefix else 2.0 ** -18 + 2.0 ** -21)
+    w = 2.0 ** -14 + (2.0 ** -8 if prefix else 0)
+    go, gl = H.to_f64(o), lse.cpu().numpy().astype(np.float64)
+    tol = (2 * d[..., None] + w) * A
+    if o.dtype == torch.bfloat16:
+        tol = tol + (np.abs(ro) + tol) * 2.0 ** -8
+    err = np.abs(go - ro)
+    assert (err <= tol + 1e-37).all(), float((err / (tol + 1e-37)).max())
+    empty = np.isneginf(rl)
+    assert (np.isneginf(gl) == empty).all() and np.isfinite(gl[~empty]).all()
+    dl = np.moveaxis(d, 1, 2)
+    ltol = dl + w + 2.0 ** -22 * np.abs(np.where(empty, 0, rl))
+    assert (np.abs(np.where(empty, 0, gl) - np.where(empty, 0, rl)) <= ltol).all()
+
+
+DECODES = [
+    # lens, Tq, Hq, Hkv, D, page, norm, half, fp32 o
+    ([1], 1, 1, 1, 32, 16, False, False, False),
+    ([129], 1, 12, 4, 64, 16, False, False, True),
+    ([0, 1, 127, 128, 129, 255, 256, 257, 1000], 1, 12, 4, 64, 16, True, False, False),
+    ([16, 17, 0, 31, 33, 5000], 1, 4, 2, 32, 16, True, True, True),
+    ([700, 3, 64, 65], 1, 8, 1, 64, 64, False, True, False),
+    ([3, 1, 2, 900, 0, 130], 3, 12, 4, 64, 32, True, False, True),      # queries before position 0
+    ([1111, 5, 6], 5, 4, 2, 32, 128, True, False, False),
+    ([300, 17], 16, 4, 2, 64, 256, False, False, True),                 # 32 rows
+    ([515, 40], 10, 16, 4, 64, 64, True, False, False),                 # 40 rows
+    ([200, 128, 1], 32, 12, 4, 64, 16, False, False, True),             # 96 rows
+    ([300, 128], 128, 2, 2, 32, 32, True, True, False),                 # 128 rows
+    ([40000], 1, 16, 4, 64, 128, False, False, True),                   # one long context over every SM
+    ([(i * 37) % 400 for i in range(200)], 1, 6, 3, 64, 16, True, False, False),
+]
+
+
+@pytest.mark.parametrize("case", DECODES, ids=lambda c: "b%d_t%d_%dx%dx%d_p%d" % (len(c[0]), c[1], c[2], c[3], c[4], c[5]))
+def test_decode(nb, case):
+    lens, Tq, Hq, Hkv, D, page, norm, half, o32 = case
+    s = setup(lens, Tq, Hq, Hkv, D, page, seed=len(lens) + Tq)
+    n = nb.decode_paged_workspace_size(len(lens), Tq, Hq, Hkv, D)
+    ws = torch.full((n + 512,), 0xFF, dtype=torch.uint8, device="cuda")
+    call = lambda: nb.attn_decode_paged(s["q"], s["kp"], s["vp"], s["table"], s["lens"], q_weight=s["qw"] if norm else None,
+                                        eps=EPS, rope_base=BASE, o_dtype=torch.float32 if o32 else torch.bfloat16,
+                                        workspace=ws, rope_half=half)
+    got = call()
+    check(nb, s, got, norm, half)
+    assert (ws[n:] == 0xFF).all()
+    again = call()  # on the used workspace, bit by bit
+    assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
+
+
+PREFIXES = [
+    # own lengths past the prefix (None: idle), prefix, Tq, Hq, Hkv, D, page, norm, half, fp32 o
+    ([1, 1], 16, 1, 4, 2, 32, 16, False, False, True),
+    ([1, None, 17, 128, 129, 300], 256, 1, 12, 4, 64, 64, True, False, False),
+    ([5, 2, 70], 128, 2, 6, 3, 64, 32, True, True, True),
+    ([(i * 13) % 90 + 1 for i in range(70)], 1024, 1, 12, 4, 64, 16, False, False, False),   # 210 rows a head
+    ([3, 4, 500, 9], 768, 3, 8, 1, 32, 256, True, False, False),
+    ([(i * 5) % 40 + 3 for i in range(140)], 640, 3, 4, 2, 64, 128, False, True, False),      # 840 rows a head
+]
+
+
+@pytest.mark.parametrize("case", PREFIXES, ids=lambda c: "b%d_p%d_t%d_%dx%dx%d" % (len(c[0]), c[1], c[2], c[3], c[4], c[5]))
+def test_shared_prefix(nb, case):
+    own, prefix, Tq, Hq, Hkv, D, page, norm, half, o32 = case
+    lens = [0 if x is None else prefix + x for x in own]
+    s = setup(lens, Tq, Hq, Hkv, D, page, seed=prefix + Tq, prefix=prefix)
+    kw = dict(q_weight=s["qw"] if norm else None, eps=EPS, rope_base=BASE, rope_half=half,
+              o_dtype=torch.float32 if o32 else torch.bfloat16)
+    call = lambda: nb.attn_decode_paged(s["q"], s["kp"], s["vp"], s["table"], s["lens"], prefix_table=s["ptable"],
+                                        prefix_len=prefix, **kw)
+    got = call()
+    check(nb, s, got, norm, half, prefix)
+    again = call()
+    assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
+
+
+def test_prefix_longer_than_a_sequence(nb):
+    """Sequences that end inside the shared pages, at and before their last position, see their own part."""
+    prefix, page = 256, 32
+    lens = [300, 256, 255, 33, 1, 0, 2, 257]
+    s = setup(lens, 2, 12, 4, 64, page, seed=5, prefix=prefix)
+    got = nb.attn_decode_paged(s["q"], s["kp"], s["vp"], s["table"], s["lens"], prefix_table=s["ptable"], prefix_len=prefix,
+                               rope_base=BASE, o_dtype=torch.float32)
+    check(nb, s, got, False, False, prefix)
+
+
+def test_prefix_only(nb):
+    """No sequence has a position of its own past the shared pages."""
+    s = setup([64, 64, 0, 64], 1, 4, 2, 64, 16, seed=6, prefix=64)
+    got = nb.attn_decode_paged(s["q"], s["kp"], s["vp"], s["table"], s["lens"], prefix_table=s["ptable"], prefix_len=64,
+                               rope_base=BASE, o_dtype=torch.float32)
+    check(nb, s, got, False, False, 64)
+
+
+def test_large_logits(nb):
+    """Logits of a few hundred: one key takes the whole weight, the maximum moves a lot."""
+    s = setup([700, 129, 2], 2, 12, 4, 64, 16, seed=8, scale=6.0)
+    got = nb.attn_decode_paged(s["q"], s["kp"], s["vp"], s["table"], s["lens"], rope_base=BASE, o_dtype=torch.float32)
+    check(nb, s, got, False, False)
+
+
+def test_strided_queries_and_pools(nb):
+    """q inside a fused projection's rows, two layers' pools interleaved."""
+    s = setup([100, 37, 260], 1, 12, 4, 64, 16, seed=12)
+    want = nb.attn_decode_paged(s["q"], s["kp"], s["vp"], s["table"], s["lens"], rope_base=BASE)
+    rows = torch.randn((3, 1, 20, 64), device="cuda").bfloat16()
+    rows[:, :, :12] = s["q"]
+    kp = torch.full((s["kp"].shape[0], 3, *s["kp"].shape[1:]), float("nan"), dtype=torch.float16, device="cuda")
+    vp = torch.full(kp.shape, float("nan"), dtype=torch.bfloat16, device="cuda")
+    kp[:, 1], vp[:, 1] = s["kp"], s["vp"]
+    got = nb.attn_decode_paged(rows[:, :, :12], kp[:, 1], vp[:, 1], s["table"], s["lens"], rope_base=BASE)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_bad_pages_and_lengths(nb):
+    """A bad page counts as zeros, a length past the table is cut to it; both are reported, and
+    the other sequences keep their results."""
+    s = setup([100, 90, 64], 1, 4, 2, 64, 16, seed=13)
+    args = (s["q"], s["kp"], s["vp"])
+    want = nb.attn_decode_paged(*args, s["table"], s["lens"], rope_base=BASE)
+    nb.check_status()
+    for bad in (-1, s["kp"].shape[0], 2 ** 31 - 1, -2 ** 31):
+        t = s["table"].clone()
+        t[1, 2] = bad
+        got = nb.attn_decode_paged(*args, t, s["lens"], rope_base=BASE)
+        assert nb.status_of_last_kernels() == -8
+        assert torch.isfinite(got[0].float()).all()
+        for b in (0, 2):
+            assert torch.equal(got[0][b], want[0][b]) and torch.equal(got[1][b], want[1][b])
+    width = s["table"].shape[1]
+    lens = s["lens"].clone()
+    lens[2] = width * 16 + 1000
+    t = s["table"].clone()
+    t[2] = t[2, 0]
+    got = nb.attn_decode_paged(*args, t, lens, rope_base=BASE)
+    assert nb.status_of_last_kernels() == -8
+    lens[2] = width * 16
+    cut = nb.attn_decode_paged(*args, t, lens, rope_base=BASE)
+    nb.check_status()
+    assert torch.equal(got[0], cut[0]) and torch.equal(got[1], cut[1])
+    lens[0] = -5
+    got = nb.attn_decode_paged(*args, t, lens, rope_base=BASE)
+    nb.check_status()
+    assert (got[0][0] == 0).all() and torch.isneginf(got[1][0]).all()
+    p = nb.attn_decode_paged(*args, s["table"], s["lens"], rope_base=BASE, prefix_table=i32([0, 10 ** 6]), prefix_len=32)
+    assert nb.status_of_last_kernels() == -8 and torch.isfinite(p[0].float()).all()
+
+
+def test_streams_and_graphs(nb):
+    """Another stream; a graph replayed with longer sequences; two graphs on one workspace in turn."""
+    Tq, Hq, Hkv, D, page = 1, 12, 4, 64, 16
+    s = setup([700, 300, 129, 40], Tq, Hq, Hkv, D, page, seed=21)
+    full = [700, 300, 129, 40]
+    call = lambda lens, **kw: nb.attn_decode_paged(s["q"], s["kp"], s["vp"], s["table"], lens, rope_base=BASE, **kw)
+    wants = {k: call(i32([max(0, n - k) for n in full])) for k in (0, 1, 39, 200)}
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    got = call(s["lens"], stream=st)
+    st.synchronize()
+    assert torch.equal(got[0], wants[0][0])
+    ws = torch.empty(nb.decode_paged_workspace_size(4, Tq, Hq, Hkv, D), dtype=torch.uint8, device="cuda")
+    lens = [i32([1, 1, 1, 1]), i32([1, 1, 1, 1])]
+    graphs, outs = [], []
+    for i in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(call(lens[i], workspace=ws))
+        graphs.append(g)
+    for k in (200, 39, 1, 0):
+        for i in range(2):
+            lens[i].copy_(i32([max(0, n - k) for n in full]))
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        for o in outs:
+            assert torch.equal(o[0], wants[k][0]) and torch.equal(o[1], wants[k][1])
+
+
+def test_far_pages(nb):
+    """Pages past 2^31 values into the pool."""
+    Hkv, page, D = 4, 16, 64
+    one = Hkv * page * D
+    P = 2 ** 31 // one + 40
+    if torch.cuda.mem_get_info()[0] < 12 << 30:
+        pytest.skip("needs 9 GB of device memory")
+    kp = torch.empty((P, Hkv, page, D), dtype=torch.float16, device="cuda")
+    vp = torch.empty((P, Hkv, page, D), dtype=torch.bfloat16, device="cuda")
+    s = setup([50, 33], 1, 12, 4, 64, page, seed=30)
+    n = s["kp"].shape[0]
+    kp[P - n:], vp[P - n:] = s["kp"], s["vp"]
+    table = torch.where(s["table"] >= 0, s["table"] + (P - n), s["table"])
+    want = nb.attn_decode_paged(s["q"], s["kp"], s["vp"], s["table"], s["lens"], rope_base=BASE)
+    got = nb.attn_decode_paged(s["q"], kp, vp, table, s["lens"], rope_base=BASE)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    k, v = torch.randn((2, Hkv, D), device="cuda").bfloat16(), torch.randn((2, Hkv, D), device="cuda").bfloat16()
+    nb.kv_append_paged(k, v, kp, vp, table, i32([49, 32]))
+    nb.check_status()
+    assert torch.equal(vp[int(table[0, 3]), :, 1], v[0]) and torch.equal(vp[int(table[1, 2]), :, 0], v[1])
+
+
+@pytest.mark.parametrize("half", [False, True])
+def test_serving_chain(nb, half):
+    """Prompts appended in two parts, then tokens one by one, with norms: every decode equals the
+    rows of the training path (norm, rotation, attention) over the whole sequence, to its bounds."""
+    B, T, Hq, Hkv, D, page = 2, 150, 12, 4, 64, 32
+    rng = np.random.default_rng(40)
+    q, _ = bf16(rng.standard_normal((B, T, Hq, D)))
+    k, _ = bf16(rng.standard_normal((B, T, Hkv, D)))
+    v, _ = bf16(rng.standard_normal((B, T, Hkv, D)))
+    qw, _ = bf16(1 + 0.2 * rng.standard_normal(D))
+    kw, _ = bf16(1 + 0.2 * rng.standard_normal(D))
+    ws = nb.qk_norm(q, k, qw, kw, eps=EPS, rope_base=BASE, rope_half=half)
+    o, lse = nb.attn_fwd(None, None, v, BASE, workspace=ws, qk_rotated=True, Hq=Hq, rope_half=half)
+    kp, vp = nb.paged_cache(12, page, Hkv, D, "cuda")
+    table = i32([[3, 11, 0, 7, 9], [2, 5, 10, 1, 4]])
+    put = lambda lo, hi: nb.kv_append_paged(k[:, lo:hi].reshape(-1, Hkv, D), v[:, lo:hi].reshape(-1, Hkv, D), kp, vp, table,
+                                            i32([lo] * B), k_weight=kw, eps=EPS, rope_base=BASE, rope_half=half)
+    put(0, 61)
+    put(61, 140)
+    for t in range(140, T):
+        put(t, t + 1)
+        got = nb.attn_decode_paged(q[:, t:t + 1], kp, vp, table, i32([t + 1] * B), q_weight=qw, eps=EPS, rope_base=BASE,
+                                   rope_half=half)
+        rel, mx = H.errors(H.to_f64(got[0]), H.to_f64(o[:, t:t + 1]))
+        assert rel <= H.REL_L2_TOL and mx <= H.MAX_ABS_TOL
+        assert float((got[1][:, :, 0] - lse[:, :, t]).abs().max()) <= H.LSE_ABS_TOL
+    nb.check_status()
