@@ -371,12 +371,12 @@ def qkv_rmsnorm(x, norm_w, w_qkv, Hq, Hkv, D, eps=1e-5, rope_base=10000.0, rotat
 def rotated_qk(workspace, B, T, Hq, Hkv, D):
     """Views of the rotated fp16 q [B,T,Hq,D] and k [B,T,Hkv,D] at the start of a
     forward / backward / projection workspace (NE_ATTN_QK_ROTATED layout)."""
-    def up(n):
-        return (n + 255) // 256 * 256
-    nq, nk = 2 * B * T * Hq * D, 2 * B * T * Hkv * D
-    qr = workspace[:nq].view(torch.float16).view(B, T, Hq, D)
-    kr = workspace[up(nq):up(nq) + nk].view(torch.float16).view(B, T, Hkv, D)
-    return qr, kr
+    n, nk = B * T * Hq * D, B * T * Hkv * D
+    at = (n + 127) // 128 * 128  # each array starts on 256 bytes
+    w = workspace[:2 * (at + nk)].view(torch.float16)
+    first = w.storage_offset()
+    return (w.as_strided((B, T, Hq, D), (T * Hq * D, Hq * D, D, 1), first),
+            w.as_strided((B, T, Hkv, D), (T * Hkv * D, Hkv * D, D, 1), first + at))
 
 
 # ------------------------------------------------------------------ query/key norms, paged cache
@@ -392,8 +392,11 @@ def _run(name, device, stream, temps, *args):
     if device.index != torch.cuda.current_device():
         with torch.cuda.device(device):
             return _run(name, device, stream, temps, *args)
-    s = torch.cuda.current_stream() if stream is None else stream
-    _check(name, getattr(lib(), name)(*args, s.cuda_stream))
+    # the current stream's handle without a Stream object around it (2.9 us a call)
+    s = torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
+    st = getattr(_lib or lib(), name)(*args, s)
+    if st != NE_OK:
+        raise NeAttnError(name, st)
     if stream is not None:
         for t in temps:
             t.record_stream(stream)
@@ -407,8 +410,8 @@ def _head_rows(t, name, dtype=torch.bfloat16, device=None):
     """Row stride (values between positions) of t [B, T, H, D] or [N, H, D]: heads
     contiguous, positions evenly spaced."""
     s, n = t.stride(), t.shape
-    _need(t.dtype == dtype and t.is_cuda and (device is None or t.device == device),
-          "%s must be %s on the call's CUDA device" % (name, dtype))
+    if t.dtype != dtype or not t.is_cuda or (device is not None and t.device != device):
+        raise ValueError("%s must be %s on the call's CUDA device" % (name, dtype))
     H, D = n[-2], n[-1]
     ok = s[-1] == 1 and (H == 1 or s[-2] == D)
     if len(n) == 3:
@@ -416,18 +419,19 @@ def _head_rows(t, name, dtype=torch.bfloat16, device=None):
     else:
         row = s[1] if n[1] > 1 else (s[0] if n[0] > 1 else H * D)
         ok = ok and (n[0] == 1 or n[1] == 1 or s[0] == n[1] * s[1])
-    _need(ok, "%s: the heads of a position must be contiguous and the positions evenly spaced" % name)
+    if not ok:
+        raise ValueError("%s: the heads of a position must be contiguous and the positions evenly spaced" % name)
     return row
 
 
 def _vector(t, D, name, device):
-    _need(t.dtype == torch.bfloat16 and t.device == device and t.shape == (D,) and t.is_contiguous(),
-          "%s must be a contiguous bfloat16 [%d] on the call's device" % (name, D))
+    if t.dtype != torch.bfloat16 or t.device != device or t.shape != (D,) or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous bfloat16 [%d] on the call's device" % (name, D))
 
 
 def _int32(t, name, device, shape):
-    _need(t.dtype == torch.int32 and t.device == device and t.is_contiguous() and tuple(t.shape) == shape,
-          "%s must be a contiguous int32 %s on the call's device" % (name, list(shape)))
+    if t.dtype != torch.int32 or t.device != device or t.shape != shape or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous int32 %s on the call's device" % (name, list(shape)))
 
 
 def qk_norm(q, k, q_weight, k_weight, eps=1e-6, rope_base=10000.0, rope_half=False, workspace=None, stream=None):
@@ -573,7 +577,7 @@ def attn_decode_paged(q, k_pages, v_pages, page_table, kv_len, q_weight=None, ep
     if prefix_len:
         _need(prefix_table is not None and prefix_table.dim() == 1 and prefix_table.numel() * page >= prefix_len,
               "prefix_table must hold the pages of prefix_len positions")
-        _int32(prefix_table, "prefix_table", dev, tuple(prefix_table.shape))
+        _int32(prefix_table, "prefix_table", dev, prefix_table.shape)
     made = []
     if o is None:
         o = torch.empty((B, Tq, Hq, D), dtype=o_dtype, device=dev)

@@ -495,6 +495,33 @@ int check_decode_paged_rows(int B, int Tq, int Hq, int Hkv, int D) {
   return NE_OK;
 }
 
+// Decode workspace: the split segments' O, their (maximum, sum), the counters.
+struct PagedWs {
+  size_t part_o, part_ml, done, total;
+};
+PagedWs paged_ws(int R, int D) {
+  PagedWs w;
+  w.part_o = 0;
+  w.part_ml = ws_up((size_t)2 * kPagedMaxBlocks * R * D * 4);
+  w.done = w.part_ml + ws_up((size_t)2 * kPagedMaxBlocks * R * 8);
+  w.total = w.done + ws_up((size_t)kPagedMaxBlocks * 4);
+  return w;
+}
+
+// 4-D map over a page pool, {D, page, Hkv, num_pages} (pages page_stride values
+// apart); box = `rows` positions of one head of one page, all D.
+int make_map_pages(CUtensorMap* m, const void* ptr, int num_pages, int Hkv, int page, int D, long long page_stride,
+                   int rows, CUtensorMapDataType dt) {
+  cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)page, (cuuint64_t)Hkv, (cuuint64_t)num_pages};
+  cuuint64_t strides[3] = {(cuuint64_t)D * 2, (cuuint64_t)page * D * 2, (cuuint64_t)page_stride * 2};
+  cuuint32_t box[4] = {(cuuint32_t)D, (cuuint32_t)rows, 1, 1};
+  cuuint32_t es[4] = {1, 1, 1, 1};
+  CUresult r = g_encode(m, dt, 4, const_cast<void*>(ptr), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        D == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? NE_OK : NE_ERR_CUDA;
+}
+
 // The current device, its state and its number of SMs.  Requires g_mu held.
 int device_and_sms(int* dev, DeviceState** d, int* nsm) {
   int st = current_device(dev);
@@ -1349,7 +1376,7 @@ int ne_attn_kv_append_paged(const void* k_new, const void* v_new, const void* k_
 size_t ne_attn_decode_paged_workspace_size(int B, int Tq, int Hq, int Hkv, int D, int prefix_len) {
   if (check_paged(B, Hq, Hkv, D, 16, 1, 1, 16LL * Hkv * D) != NE_OK || Tq < 1 || prefix_len < 0) return 0;
   if (check_decode_paged_rows(B, Tq, Hq, Hkv, D) != NE_OK) return 0;
-  return 256;
+  return paged_ws((Hq / Hkv) * Tq, D).total;
 }
 
 int ne_attn_decode_paged(const void* q, const void* q_w, const void* k_pages, const void* v_pages,
@@ -1385,8 +1412,6 @@ int ne_attn_decode_paged(const void* q, const void* q_w, const void* k_pages, co
   if ((st = rope_table(*d, D, (double)rope_base, max_pages * page_size, s, &a.rope)) != NE_OK) return st;
   a.q = static_cast<const __nv_bfloat16*>(q);
   a.qw = static_cast<const __nv_bfloat16*>(q_w);
-  a.kp = static_cast<const __half*>(k_pages);
-  a.vp = static_cast<const __nv_bfloat16*>(v_pages);
   a.table = page_table;
   a.len = kv_len;
   a.prefix_table = prefix_table;
@@ -1394,13 +1419,13 @@ int ne_attn_decode_paged(const void* q, const void* q_w, const void* k_pages, co
   a.o = o;
   a.lse = lse;
   a.q_stride = q_stride;
-  a.page_stride = page_stride;
   a.B = B;
   a.Tq = Tq;
   a.Hq = Hq;
   a.Hkv = Hkv;
   a.D = D;
   a.G = Hq / Hkv;
+  a.R = a.G * Tq;
   a.page_shift = log2_of(page_size);
   a.num_pages = num_pages;
   a.max_pages = max_pages;
@@ -1409,8 +1434,23 @@ int ne_attn_decode_paged(const void* q, const void* q_w, const void* k_pages, co
   a.o_fp32 = (flags & kFlagOFp32) ? 1 : 0;
   a.eps = eps;
   a.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)D));
+  const PagedWs w = paged_ws(a.R, D);
+  unsigned char* ws = static_cast<unsigned char*>(workspace);
+  a.part_o = reinterpret_cast<float*>(ws + w.part_o);
+  a.part_ml = reinterpret_cast<float2*>(ws + w.part_ml);
+  a.done = reinterpret_cast<unsigned*>(ws + w.done);
+  a.min_tiles = 1;
+  int mt = 1;
+  paged_rows(a.R, &mt, &a.tiles, &a.MG);
+  const int rows = page_size < (D == 64 ? 128 : 256) ? page_size : (D == 64 ? 128 : 256);
+  if ((st = make_map_pages(&a.map_k, k_pages, num_pages, Hkv, page_size, D, page_stride, rows,
+                           CU_TENSOR_MAP_DATA_TYPE_FLOAT16)) != NE_OK)
+    return st;
+  if ((st = make_map_pages(&a.map_v, v_pages, num_pages, Hkv, page_size, D, page_stride, rows,
+                           CU_TENSOR_MAP_DATA_TYPE_BFLOAT16)) != NE_OK)
+    return st;
   ProfScope prof(NE_ATTN_KERNEL_DECODE_PAGED, s);
-  return launch_decode_paged(a, s) == cudaSuccess ? NE_OK : NE_ERR_CUDA;
+  return launch_decode_paged(a, mt, nsm, s) == cudaSuccess ? NE_OK : NE_ERR_CUDA;
 }
 
 int ne_attn_debug_fwd_schedule(int B, int Hkv, int G, int nt, int nsm, int* table, int capacity, int* grid,

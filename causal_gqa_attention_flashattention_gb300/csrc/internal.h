@@ -213,17 +213,23 @@ struct PagedAppendArgs {
 };
 
 // Attention of the newest tokens over a paged cache (see paged.cu).
+constexpr int kPagedMaxBlocks = 160;  // blocks of the sweep: bounds its partial results
 struct PagedDecodeArgs {
+  CUtensorMap map_k, map_v;     // pools {D, page, Hkv, num_pages}, box D x min(page, tile) rows
   const __nv_bfloat16 *q, *qw;  // [B, Tq, Hq, D], positions q_stride values apart; qw [D] or null
-  const __half* kp;
-  const __nv_bfloat16* vp;
   const int *table, *len, *prefix_table;
   const float2* rope;
   int* status;
   void* o;
-  float* lse;  // or null
-  long long q_stride, page_stride;
-  int B, Tq, Hq, Hkv, D, G, page_shift, num_pages, max_pages, prefix_len, rope_half, o_fp32;
+  float* lse;       // or null
+  float* part_o;    // [2 blocks, R, D] unnormalised O of a block's first and last segment (workspace)
+  float2* part_ml;  // [2 blocks, R] their maximum (log2 units) and sum
+  unsigned* done;   // [blocks] segments finished of the (sequence, head) that starts in a block
+  long long q_stride;
+  int B, Tq, Hq, Hkv, D, G, R, page_shift, num_pages, max_pages, prefix_len, rope_half, o_fp32;
+  int base;         // positions before the part of every sequence that the sweep reads (a shared prefix read elsewhere)
+  int tiles, MG;    // packed row tiles (8 rows each) and the groups of warps that share them
+  int stages, min_tiles;
   float eps, scale_log2;
 };
 
@@ -252,7 +258,8 @@ int qk_norm_bwd_blocks(int B, int T, int hg, int D, int nsm);
 cudaError_t launch_qk_norm_bwd(const QkNormBwdArgs& a, int D, bool f32, int blocks, cudaStream_t s);
 cudaError_t launch_qk_norm_dw(const QkNormBwdArgs& a, int D, int blocks, float* dwq, float* dwk, cudaStream_t s);
 cudaError_t launch_kv_append_paged(const PagedAppendArgs& a, int D, cudaStream_t s);
-cudaError_t launch_decode_paged(const PagedDecodeArgs& a, cudaStream_t s);
+void paged_rows(int R, int* mt, int* tiles, int* mg);
+cudaError_t launch_decode_paged(const PagedDecodeArgs& a, int mt, int nsm, cudaStream_t s);
 
 cudaError_t launch_qkv_prep(const QkvArgs& a, cudaStream_t s);
 cudaError_t launch_qkv_gemm(const QkvArgs& a, int BN, int grid, cudaStream_t s);

@@ -19,6 +19,7 @@ namespace ne {
 namespace {
 
 constexpr float kLn2 = 0.69314718055994531f;
+constexpr int kSmemMax = 232448;
 
 __device__ __forceinline__ void record_page(int* status) { atomicCAS(status, 0, kStatusPage); }
 
@@ -115,85 +116,601 @@ __global__ void __launch_bounds__(128) k_kv_append_paged(const PagedAppendArgs a
 }
 
 // ====================================================================== attention
-// One block per (sequence, new token, query head), one key per thread at a time:
-// running maximum and sum, O in registers, the threads merged at the end.
+// Work: the key tiles (kTK positions) of every (sequence, key/value head), laid end
+// to end in that order, cut into one equal stretch for each block.  Every block
+// works the stretches out for itself from the lengths, so nothing is planned on the
+// host and a captured graph follows the lengths it finds.  A segment, the part of
+// one (sequence, head) in one block's stretch, that is not the whole of it leaves
+// its unnormalised O, running maximum and sum; the block that finishes a (sequence,
+// head) last adds the segments in order: the result does not depend on which one.
+//
+// Rows: the R = Tq * G queries of a key/value head (row t * G + g).  A matrix tile of
+// 16 rows holds 8 of them twice: rows 0-7 the high fp16 part of the rotated query,
+// rows 8-15 its remainder, so that one m16n8k16 product gives both parts of a score
+// in one thread; the same goes for the weights' two bf16 parts in P V.  With at most
+// 8 rows (one token of most models) that precision is free: the tile has 16 rows
+// anyway.  mma.sync and not tcgen05: with so few rows the sweep is bound by the bytes
+// of the cache, and a warp that owns its 16 keys end to end (scores, weights, P V in
+// registers) needs no hand-off between warps per tile.
 template <int D>
-__global__ void __launch_bounds__(128) k_decode_paged(const PagedDecodeArgs a) {
-  const int h = blockIdx.x % a.Hq, bt = blockIdx.x / a.Hq;
-  const int t = bt % a.Tq, b = bt / a.Tq, g = h / a.G, tid = threadIdx.x;
-  __shared__ float qs[D];
-  __shared__ float red[128];
-  __shared__ float acc[D];
-  int len = a.len[b];
+struct Sweep {
+  static constexpr int kTK = D == 64 ? 128 : 256;  // positions of a tile
+  static constexpr uint32_t kSpan = D * 2;
+  static constexpr int kHalf = kTK * (int)kSpan;   // bytes of a tile's keys (as many of values)
+  static constexpr int kStage = 2 * kHalf;
+  static constexpr int kSlices = kTK / 16;
+  static constexpr int kMaxStages = 6;
+};
+constexpr int kSweepWarps = 8;                       // consumers; then the producer and the query warp
+constexpr int kSweepThreads = (kSweepWarps + 4) * 32;  // whole warpgroups: two warps of the third stay idle
+constexpr int kBarBytes = 256;
+
+// Shared memory behind the ring, in bytes (tiles: packed row tiles, mt: of one warp).
+struct SweepSmem {
+  int q, scratch, ml, cum, len, bars, total;
+};
+__host__ __device__ inline SweepSmem sweep_smem(int D, int stages, int tiles, int mt, int B) {
+  SweepSmem m;
+  m.q = stages * 32768;
+  m.scratch = m.q + 2 * tiles * 16 * D * 2;
+  m.ml = m.scratch + kSweepWarps * mt * 8 * D * 4;
+  m.cum = m.ml + kSweepWarps * mt * 8 * 8;
+  m.len = m.cum + (B + 1) * 4;
+  m.bars = (m.len + B * 4 + 15) / 16 * 16;
+  m.total = m.bars + kBarBytes + 1024;
+  return m;
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_b16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// The block's place in the work: tiles [w, end) of all, as segments.
+struct SegWalk {
+  const int *cum, *len;  // shared memory: tiles before sequence b (one head), positions of b's own part
+  int Hkv, B;
+  long long W, w, end;
+  int G;                 // blocks that take part
+  int b, g, n0, n1, nt;  // the segment: key tiles [n0, n1) of nt
+  long long s0;          // the (sequence, head)'s first tile among all
+  __device__ long long start(long long c) const { return c * W / G; }
+  __device__ int owner(long long x) const { return (int)(((x + 1) * G - 1) / W); }
+  __device__ void init(int block, int grid, int min_tiles) {
+    W = (long long)cum[B] * Hkv;
+    const long long most = W / min_tiles;
+    G = most < 1 ? 1 : (most < grid ? (int)most : grid);
+    w = block < G ? start(block) : 0;
+    end = block < G ? start(block + 1) : 0;
+    int lo = 0, hi = B;  // the sequence of tile w: last b with Hkv * cum[b] <= w
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if ((long long)cum[mid] * Hkv <= w)
+        lo = mid;
+      else
+        hi = mid;
+    }
+    b = lo;
+    n1 = 0;
+  }
+  __device__ bool next() {
+    if (w >= end) return false;
+    while ((long long)cum[b + 1] * Hkv <= w) b++;
+    nt = cum[b + 1] - cum[b];
+    const long long off = w - (long long)cum[b] * Hkv;
+    g = (int)(off / nt);
+    n0 = (int)(off - (long long)g * nt);
+    s0 = w - n0;
+    n1 = (int)(end - w < nt - n0 ? n0 + (end - w) : nt);
+    w += n1 - n0;
+    return true;
+  }
+};
+
+// Rotated (and normalised) query row chunk as fp16 high and low parts.
+template <int D>
+__device__ __forceinline__ void query_chunk(const PagedDecodeArgs& a, int b, int g, int r, int c, int pos0, uint4& hi,
+                                            uint4& lo) {
+  constexpr int kCPR = D / 8;
+  const bool on = r < a.R;
+  const int t = on ? r / a.G : 0, gg = r - t * a.G;
+  uint4 v = make_uint4(0, 0, 0, 0);
+  if (on) v = load_rope_chunk<D>(a.q + (size_t)(b * a.Tq + t) * a.q_stride + (g * a.G + gg) * D, c, a.rope_half != 0);
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  float x[8];
+#pragma unroll
+  for (int p = 0; p < 4; p++) {
+    x[2 * p] = bf_lo(w[p]);
+    x[2 * p + 1] = bf_hi(w[p]);
+  }
+  if (a.qw) {
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; i++) ss = fmaf(x[i], x[i], ss);
+#pragma unroll
+    for (int m = 1; m < kCPR; m <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
+    const float rs = rsqrtf(fmaf(ss, 1.f / D, a.eps));
+    const uint4 wv = load_rope_chunk<D>(a.qw, c, a.rope_half != 0);
+    const uint32_t ww[4] = {wv.x, wv.y, wv.z, wv.w};
+#pragma unroll
+    for (int p = 0; p < 4; p++) {
+      x[2 * p] *= rs * bf_lo(ww[p]);
+      x[2 * p + 1] *= rs * bf_hi(ww[p]);
+    }
+  }
+  float4 c0, c1;
+  rope_coeffs<D>(a.rope, max(pos0 + t, 0), c, c0, c1);
+  const float cs[4] = {c0.x, c0.z, c1.x, c1.z}, sn[4] = {c0.y, c0.w, c1.y, c1.w};
+  uint32_t h[4], l[4];
+#pragma unroll
+  for (int p = 0; p < 4; p++) {
+    const float y0 = fmaf(x[2 * p], cs[p], -x[2 * p + 1] * sn[p]), y1 = fmaf(x[2 * p], sn[p], x[2 * p + 1] * cs[p]);
+    h[p] = pack_f16(y0, y1);
+    l[p] = pack_f16(y0 - f16_lo(h[p]), y1 - f16_hi(h[p]));
+  }
+  if (!on) {
+#pragma unroll
+    for (int p = 0; p < 4; p++) h[p] = l[p] = 0;
+  }
+  hi = make_uint4(h[0], h[1], h[2], h[3]);
+  lo = make_uint4(l[0], l[1], l[2], l[3]);
+}
+
+// All consumer warps meet (an mbarrier and not bar.sync: a warp that gave up must
+// not leave the others waiting for ever).
+__device__ __forceinline__ bool meet(uint64_t* bar, int& phase, volatile int* abort) {
+  warp_arrive(bar);
+  const bool ok = __all_sync(0xffffffffu, mbar_wait(bar, phase & 1, abort));
+  phase++;
+  return ok;
+}
+
+// Row r of (sequence b, head g), columns 4 q .. 4 q + 3: normalise and write.
+template <int D>
+__device__ __forceinline__ void write_row(const PagedDecodeArgs& a, int b, int g, int r, int q, float4 v, float M, float L) {
+  const int t = r / a.G, h = g * a.G + (r - t * a.G);
+  const float inv = L > 0.f ? 1.f / L : 0.f;
+  const size_t at = (((size_t)b * a.Tq + t) * a.Hq + h) * D + 4 * q;
+  v = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+  if (a.o_fp32)
+    *reinterpret_cast<float4*>(static_cast<float*>(a.o) + at) = v;
+  else
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.o) + at) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+  if (q == 0 && a.lse) a.lse[((size_t)b * a.Hq + h) * a.Tq + t] = L > 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
+}
+
+template <int D, int MT>
+__device__ bool sweep_consume(const PagedDecodeArgs& a, SegWalk sw, uint8_t* smem, const SweepSmem& L, uint64_t* full,
+                              uint64_t* empty, uint64_t* q_full, uint64_t* q_empty, uint64_t* gbar, volatile int* flag,
+                              volatile int* abort, int warp, int lane) {
+  using C = Sweep<D>;
+  constexpr int KS = D / 16;
+  const int KG = kSweepWarps / a.MG, mg = warp / KG, kg = warp - mg * KG;
+  const uint32_t ring = smem_u32(smem);
+  const float sl2 = a.scale_log2;
+  // this lane's ldmatrix row and chunk parity (keys, values and queries alike)
+  const uint32_t lrow = lane & 15, lchk = lane >> 4;
+  float* scratch = reinterpret_cast<float*>(smem + L.scratch);
+  float2* ml = reinterpret_cast<float2*>(smem + L.ml);
+  int st = 0, ph = 0, gphase = 0, seg = 0;
+  bool waited = false;
+  for (; sw.next(); seg++) {
+    const int own = sw.len[sw.b], total = own + a.base;
+    const int pos0 = total - a.Tq - a.base;  // row 0's position, counted from the own part's start
+    const int qs = seg & 1;
+    if (!__all_sync(0xffffffffu, mbar_wait(q_full + qs, (seg >> 1) & 1, abort))) return false;
+    const uint32_t qbase = smem_u32(smem + L.q) + (uint32_t)((qs * a.tiles + mg * MT) * 16) * C::kSpan;
+    uint32_t qf[MT <= 2 ? MT : 1][KS][4];
+    if (MT <= 2) {
+#pragma unroll
+      for (int m = 0; m < MT; m++)
+#pragma unroll
+        for (int k = 0; k < KS; k++)
+          ldsm4(qf[m <= 1 || MT <= 2 ? m : 0][k], qbase + m * 16 * C::kSpan + swz(lrow, 2 * k + lchk, C::kSpan));
+      warp_arrive(q_empty + qs);
+    }
+    float o[MT][2 * KS][4], mx[MT], ls[MT];
+    int lim[MT];  // last visible position of this lane's row, from the own part's start
+#pragma unroll
+    for (int m = 0; m < MT; m++) {
+      mx[m] = -INFINITY;
+      ls[m] = 0.f;
+      const int r = (mg * MT + m) * 8 + (lane >> 2);
+      lim[m] = r < a.R ? pos0 + r / a.G : own - 1;
+#pragma unroll
+      for (int i = 0; i < 2 * KS; i++)
+#pragma unroll
+        for (int e = 0; e < 4; e++) o[m][i][e] = 0.f;
+    }
+    for (int n = sw.n0; n < sw.n1; n++) {
+      if (!__all_sync(0xffffffffu, mbar_wait(full + st, ph, abort))) return false;
+      const uint32_t kb = ring + st * C::kStage, vb = kb + C::kHalf;
+      for (int sl = kg; sl < C::kSlices; sl += KG) {
+        const int j0 = n * C::kTK + sl * 16;
+        if (j0 >= own) break;
+        const uint32_t at = (uint32_t)sl * 16 * C::kSpan;
+        uint32_t kf[KS][4], vf[KS][4];
+#pragma unroll
+        for (int k = 0; k < KS; k++) ldsm4(kf[k], kb + at + swz(lrow, 2 * k + lchk, C::kSpan));
+#pragma unroll
+        for (int k = 0; k < KS; k++) ldsm4t(vf[k], vb + at + swz(lrow, 2 * k + lchk, C::kSpan));
+        const bool edge = j0 + 16 > pos0 + 1;  // some row does not see every key of the slice
+        if (j0 + 16 > own) {
+          // what lies behind the last position may be anything: its weight is 0, but
+          // 0 times a NaN is not
+          const int v0 = own - j0 - (lane & 3) * 2;
+          const uint32_t m0 = (v0 > 0 ? 0xffffu : 0u) | (v0 > 1 ? 0xffff0000u : 0u);
+          const uint32_t m1 = (v0 > 8 ? 0xffffu : 0u) | (v0 > 9 ? 0xffff0000u : 0u);
+#pragma unroll
+          for (int k = 0; k < KS; k++) {
+            vf[k][0] &= m0;
+            vf[k][1] &= m1;
+            vf[k][2] &= m0;
+            vf[k][3] &= m1;
+          }
+        }
+#pragma unroll
+        for (int m = 0; m < MT; m++) {
+          float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int k = 0; k < KS; k++) {
+            uint32_t qt[4];
+            if (MT <= 2) {
+#pragma unroll
+              for (int e = 0; e < 4; e++) qt[e] = qf[MT <= 2 ? m : 0][k][e];
+            } else {
+              ldsm4(qt, qbase + m * 16 * C::kSpan + swz(lrow, 2 * k + lchk, C::kSpan));
+            }
+            mma_f16(s0, qt, kf[k][0], kf[k][2]);
+            mma_f16(s1, qt, kf[k][1], kf[k][3]);
+          }
+          // keys (lane & 3) * 2 + {0, 1} and those + 8, row lane / 4: high + low part
+          float x[4] = {s0[0] + s0[2], s0[1] + s0[3], s1[0] + s1[2], s1[1] + s1[3]};
+          if (edge) {
+            const int k0 = j0 + (lane & 3) * 2;
+#pragma unroll
+            for (int e = 0; e < 4; e++)
+              if (k0 + (e & 1) + (e >> 1) * 8 > lim[m]) x[e] = -INFINITY;
+          }
+          float t = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+          t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
+          t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
+          // O and the sum follow the maximum only when it grew by more than 2^8
+          const bool grow = mx[m] == -INFINITY ? t > -INFINITY : __fmul_rn(t, sl2) > __fmul_rn(mx[m], sl2) + 8.f;
+          if (__any_sync(0xffffffffu, grow)) {
+            const float to = grow ? t : mx[m];
+            const float al = grow && mx[m] != -INFINITY ? ex2(__fmul_rn(mx[m], sl2) - __fmul_rn(t, sl2)) : 1.f;
+            mx[m] = to;
+            ls[m] *= al;
+#pragma unroll
+            for (int i = 0; i < 2 * KS; i++)
+#pragma unroll
+              for (int e = 0; e < 4; e++) o[m][i][e] *= al;
+          }
+          const float mu = mx[m] == -INFINITY ? 0.f : __fmul_rn(mx[m], sl2);
+          float p[4];
+#pragma unroll
+          for (int e = 0; e < 4; e++) p[e] = ex2(fmaf(x[e], sl2, -mu));
+          ls[m] += (p[0] + p[1]) + (p[2] + p[3]);
+          uint32_t pa[4];
+          pa[0] = pack_bf16(p[0], p[1]);
+          pa[2] = pack_bf16(p[2], p[3]);
+          pa[1] = pack_bf16(p[0] - bf_lo(pa[0]), p[1] - bf_hi(pa[0]));
+          pa[3] = pack_bf16(p[2] - bf_lo(pa[2]), p[3] - bf_hi(pa[2]));
+#pragma unroll
+          for (int k = 0; k < KS; k++) {
+            mma_b16(o[m][2 * k], pa, vf[k][0], vf[k][1]);
+            mma_b16(o[m][2 * k + 1], pa, vf[k][2], vf[k][3]);
+          }
+        }
+      }
+      warp_arrive(empty + st);
+      if (++st == a.stages) {
+        st = 0;
+        ph ^= 1;
+      }
+    }
+    if (MT > 2) warp_arrive(q_empty + qs);
+    // the warps' parts meet in shared memory
+#pragma unroll
+    for (int m = 0; m < MT; m++) {
+      float l = ls[m];
+      l += __shfl_xor_sync(0xffffffffu, l, 1);
+      l += __shfl_xor_sync(0xffffffffu, l, 2);
+      const int row = (warp * MT + m) * 8 + (lane >> 2);
+      if ((lane & 3) == 0) ml[row] = make_float2(mx[m] == -INFINITY ? -INFINITY : __fmul_rn(mx[m], sl2), l);
+#pragma unroll
+      for (int i = 0; i < 2 * KS; i++)
+        *reinterpret_cast<float2*>(scratch + row * D + i * 8 + (lane & 3) * 2) =
+            make_float2(o[m][i][0] + o[m][i][2], o[m][i][1] + o[m][i][3]);
+    }
+    if (!meet(gbar, gphase, abort)) return false;
+    if (!waited) {
+      pdl_wait();  // the workspace's counters are cleared by the kernel before
+      waited = true;
+    }
+    const bool whole = sw.n0 == 0 && sw.n1 == sw.nt;
+    const int c0 = whole ? 0 : sw.owner(sw.s0), c1 = whole ? 0 : sw.owner(sw.s0 + sw.nt - 1);
+    const int slot = 2 * (int)blockIdx.x + (sw.s0 <= sw.start(blockIdx.x) ? 0 : 1);
+    const int tid = warp * 32 + lane;
+    for (int i = tid; i < a.R * (D / 4); i += kSweepWarps * 32) {
+      const int r = i / (D / 4), q = i % (D / 4), tile = r >> 3, w0 = (tile / MT) * KG;
+      const int at = (w0 * MT + tile % MT) * 8 + (r & 7);
+      float M = -INFINITY;
+      for (int k = 0; k < KG; k++) M = fmaxf(M, ml[at + k * MT * 8].x);
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      float S = 0.f;
+      for (int k = 0; k < KG; k++) {
+        const float2 z = ml[at + k * MT * 8];
+        if (z.y == 0.f) continue;  // no visible key
+        const float f = ex2(z.x - M);
+        const float4 u = *reinterpret_cast<const float4*>(scratch + (at + k * MT * 8) * D + 4 * q);
+        S = fmaf(f, z.y, S);
+        v = make_float4(fmaf(f, u.x, v.x), fmaf(f, u.y, v.y), fmaf(f, u.z, v.z), fmaf(f, u.w, v.w));
+      }
+      if (whole) {
+        write_row<D>(a, sw.b, sw.g, r, q, v, M, S);
+      } else {
+        *reinterpret_cast<float4*>(a.part_o + ((size_t)slot * a.R + r) * D + 4 * q) = v;
+        if (q == 0) a.part_ml[(size_t)slot * a.R + r] = make_float2(M, S);
+      }
+    }
+    if (!whole) __threadfence();
+    if (!meet(gbar, gphase, abort)) return false;
+    if (whole) continue;
+    if (tid == 0) {
+      *flag = atomicAdd(a.done + c0, 1u) == (unsigned)(c1 - c0) ? 1 : 0;
+      __threadfence();
+    }
+    if (!meet(gbar, gphase, abort)) return false;
+    if (*flag) {
+      __threadfence();
+      const int first = 2 * c0 + (sw.s0 <= sw.start(c0) ? 0 : 1);
+      for (int i = tid; i < a.R * (D / 4); i += kSweepWarps * 32) {
+        const int r = i / (D / 4), q = i % (D / 4);
+        float M = -INFINITY;
+        for (int c = c0; c <= c1; c++) M = fmaxf(M, __ldcg(&a.part_ml[(size_t)(c == c0 ? first : 2 * c) * a.R + r].x));
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        float S = 0.f;
+        for (int c = c0; c <= c1; c++) {
+          const size_t at = (size_t)(c == c0 ? first : 2 * c) * a.R + r;
+          const float2 z = __ldcg(&a.part_ml[at]);
+          if (z.y == 0.f) continue;
+          const float f = ex2(z.x - M);
+          const float4 u = __ldcg(reinterpret_cast<const float4*>(a.part_o + at * D + 4 * q));
+          S = fmaf(f, z.y, S);
+          v = make_float4(fmaf(f, u.x, v.x), fmaf(f, u.y, v.y), fmaf(f, u.z, v.z), fmaf(f, u.w, v.w));
+        }
+        write_row<D>(a, sw.b, sw.g, r, q, v, M, S);
+      }
+      // flag is written again only after the next segment's first meeting
+    }
+  }
+  return true;
+}
+
+template <int D, int MT>
+__global__ void __launch_bounds__(kSweepThreads, 1) k_paged_sweep(const __grid_constant__ PagedDecodeArgs a) {
+  using C = Sweep<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  const SweepSmem L = sweep_smem(D, a.stages, a.tiles, MT, a.B);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L.bars);
+  uint64_t* empty = full + C::kMaxStages;
+  uint64_t* q_full = empty + C::kMaxStages;  // [2]
+  uint64_t* q_empty = q_full + 2;            // [2]
+  uint64_t* gbar = q_empty + 2;
+  volatile int* abort = reinterpret_cast<volatile int*>(gbar + 1);
+  volatile int* flag = abort + 1;
+  int* wsum = const_cast<int*>(abort) + 2;   // [12] the scan's warp totals
+  int* cum = reinterpret_cast<int*>(smem + L.cum);
+  int* len = reinterpret_cast<int*>(smem + L.len);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    *abort = 0;
+    for (int i = 0; i < a.stages; i++) {
+      mbar_init(full + i, 1);
+      mbar_init(empty + i, kSweepWarps);
+    }
+    for (int i = 0; i < 2; i++) {
+      mbar_init(q_full + i, 1);
+      mbar_init(q_empty + i, kSweepWarps);
+    }
+    mbar_init(gbar, kSweepWarps);
+    fence_mbar_init();
+    cum[0] = 0;
+  }
+  // lengths of the own parts and the running count of their tiles
   const int cap = a.max_pages << a.page_shift;
-  if (len > cap) {
-    if (tid == 0) record_page(a.status);
-    len = cap;
-  }
-  const int pos = len - a.Tq + t;
-  if (tid < D / 2) {
-    const __nv_bfloat16* q = a.q + (size_t)bt * a.q_stride + h * D;
-    const int i0 = a.rope_half ? tid : 2 * tid, i1 = a.rope_half ? tid + D / 2 : 2 * tid + 1;
-    float x0 = __bfloat162float(q[i0]), x1 = __bfloat162float(q[i1]);
-    if (a.qw) {
-      float ss = 0.f;
-      for (int i = 0; i < D; i++) ss += __bfloat162float(q[i]) * __bfloat162float(q[i]);
-      const float r = rsqrtf(ss / D + a.eps);
-      x0 *= r * __bfloat162float(a.qw[i0]);
-      x1 *= r * __bfloat162float(a.qw[i1]);
+  int before = 0;
+  for (int b0 = 0; b0 < a.B; b0 += kSweepThreads) {
+    const int b = b0 + tid;
+    int own = 0, nt = 0;
+    if (b < a.B) {
+      int n = a.len[b];
+      if (n > cap) {
+        if (blockIdx.x == 0) record_page(a.status);
+        n = cap;
+      }
+      own = max(n - a.base, 0);
+      if (n < 0) own = 0;
+      len[b] = n > 0 ? n - a.base : -a.base;  // signed: rows of a sequence inside the prefix see none of its own part
+      nt = max(1, (own + C::kTK - 1) / C::kTK);
     }
-    const float2 cs = a.rope[(size_t)max(pos, 0) * (D / 2) + tid];
-    qs[2 * tid] = x0 * cs.x - x1 * cs.y;
-    qs[2 * tid + 1] = x0 * cs.y + x1 * cs.x;
-  }
-  __syncthreads();
-  float m = -INFINITY, l = 0.f, o[D];
+    int x = nt;
 #pragma unroll
-  for (int i = 0; i < D; i++) o[i] = 0.f;
-  for (int j = tid; j <= pos; j += 128) {
-    const int slot = j >> a.page_shift;
-    const int page = j < a.prefix_len ? a.prefix_table[slot] : a.table[(size_t)b * a.max_pages + slot];
-    const bool ok = page >= 0 && page < a.num_pages;
-    if (!ok) record_page(a.status);
-    const size_t at = (size_t)(ok ? page : 0) * a.page_stride +
-                      (((size_t)g << a.page_shift) + (j & ((1 << a.page_shift) - 1))) * D;
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < D; i++) s = fmaf(qs[i], ok ? __half2float(a.kp[at + i]) : 0.f, s);
-    s *= a.scale_log2;
-    const float mn = fmaxf(m, s), al = exp2f(m - mn), p = exp2f(s - mn);
-    l = l * al + p;
-#pragma unroll
-    for (int i = 0; i < D; i++) o[i] = fmaf(p, ok ? __bfloat162float(a.vp[at + i]) : 0.f, o[i] * al);
-    m = mn;
-  }
-  red[tid] = m;
-  __syncthreads();
-  float M = -INFINITY;
-  for (int i = 0; i < 128; i++) M = fmaxf(M, red[i]);
-  __syncthreads();
-  const float w = m == -INFINITY ? 0.f : exp2f(m - M);
-  red[tid] = w * l;
-  if (tid < D) acc[tid] = 0.f;
-  __syncthreads();
-  float L = 0.f;
-  for (int i = 0; i < 128; i++) L += red[i];
-  for (int k = 0; k < 128; k++) {
-    if (tid == k) {
-#pragma unroll
-      for (int i = 0; i < D; i++) acc[i] += w * o[i];
+    for (int m = 1; m < 32; m <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, m);
+      if (lane >= m) x += y;
     }
+    if (lane == 31) wsum[warp] = x;
+    __syncthreads();
+    int all = 0;
+    for (int i = 0; i < kSweepThreads / 32; i++) {
+      if (i < warp) x += wsum[i];
+      all += wsum[i];
+    }
+    if (b < a.B) cum[b + 1] = before + x;
+    before += all;
     __syncthreads();
   }
-  if (tid < D) {
-    const float v = L > 0.f ? acc[tid] / L : 0.f;
-    const size_t at = ((size_t)bt * a.Hq + h) * D + tid;
-    if (a.o_fp32)
-      static_cast<float*>(a.o)[at] = v;
-    else
-      static_cast<__nv_bfloat16*>(a.o)[at] = __float2bfloat16_rn(v);
+  SegWalk sw;
+  sw.cum = cum;
+  sw.len = len;
+  sw.Hkv = a.Hkv;
+  sw.B = a.B;
+  sw.init(blockIdx.x, gridDim.x, a.min_tiles);
+  const volatile int never = 0;
+  // registers: 384 x 168 at launch; 256 x 216 for the consumers, 128 x 72 for the others
+  if (warp < kSweepWarps) {
+    regs_inc<216>();
+    const bool ok = sweep_consume<D, MT>(a, sw, smem, L, full, empty, q_full, q_empty, gbar, flag, abort, warp, lane);
+    if (!ok && lane == 0) {
+      *abort = 1;
+      atomicCAS(a.status, 0, kStatusTimeout);
+    }
+    return;
   }
-  if (tid == 0 && a.lse) a.lse[((size_t)b * a.Hq + h) * a.Tq + t] = L > 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
+  regs_dec<72>();
+  if (warp == kSweepWarps) {
+    // ------------------------------------------------------------ keys and values
+    // Lane i loads page i of a tile; the page numbers come 32 at a time.
+    const int prows = min(1 << a.page_shift, C::kTK), per = C::kTK / prows;
+    const uint32_t pbytes = (uint32_t)prows * C::kSpan;
+    const int shared = a.prefix_len >> a.page_shift;
+    if (lane == 0) {
+      prefetch_tmap(&a.map_k);
+      prefetch_tmap(&a.map_v);
+    }
+    int st = 0, ph = 1;  // the first round finds every stage empty
+    int issued = 0;
+    bool ok = true;
+    while (ok && sw.next()) {
+      const int own = sw.len[sw.b];
+      const int* row = a.table + (size_t)sw.b * a.max_pages;
+      const int p0 = a.base >> a.page_shift;
+      const int np = own > 0 ? (own + (1 << a.page_shift) - 1) >> a.page_shift : 0;  // own pages
+      int win = -1, id = 0;
+      for (int n = sw.n0; n < sw.n1; n++) {
+        const int first = (n * C::kTK) >> a.page_shift;  // own page of the tile's first position
+        const int have = max(0, min(per, np - first));
+        if (have > 0 && (first >> 5) != win) {
+          win = first >> 5;
+          const int i = p0 + win * 32 + lane;
+          id = 0;
+          if (i - p0 < np) {
+            id = i < shared ? a.prefix_table[i] : row[i];
+            if (id < 0 || id >= a.num_pages) {
+              record_page(a.status);
+              id = a.num_pages;  // past the pool: the copy fills with zeros
+            }
+          }
+        }
+        const int mine = __shfl_sync(0xffffffffu, id, (first & 31) + (lane < per ? lane : 0));
+        ok = __all_sync(0xffffffffu, mbar_wait(empty + st, ph, abort));
+        if (!ok) break;
+        if (lane == 0) {
+          if (have > 0)
+            mbar_arrive_expect_tx(full + st, 2u * have * pbytes);
+          else
+            mbar_arrive(full + st);
+        }
+        __syncwarp();
+        if (lane < have) {
+          const int off = (n * C::kTK) & ((1 << a.page_shift) - 1);  // a tile inside a larger page
+          uint8_t* dst = smem + st * C::kStage + lane * pbytes;
+          tma_load_4d(dst, &a.map_k, full + st, 0, off, sw.g, mine);
+          tma_load_4d(dst + C::kHalf, &a.map_v, full + st, 0, off, sw.g, mine);
+        }
+        issued++;
+        if (++st == a.stages) {
+          st = 0;
+          ph ^= 1;
+        }
+      }
+    }
+    if (!ok) {
+      if (lane == 0) {
+        *abort = 1;
+        atomicCAS(a.status, 0, kStatusTimeout);
+      }
+      // let every copy issued above land before the block can exit
+      if (lane == 0)
+        for (int x = max(0, issued - a.stages); x < issued; x++)
+          mbar_wait(full + x % a.stages, (x / a.stages) & 1, &never);
+    }
+  } else if (warp == kSweepWarps + 1) {
+    // ------------------------------------------------------------ queries
+    constexpr int kCPR = D / 8, kRows = 32 / kCPR;
+    const int c = lane % kCPR;
+    bool ok = true;
+    for (int seg = 0; ok && sw.next(); seg++) {
+      const int qs = seg & 1;
+      if (seg >= 2) ok = __all_sync(0xffffffffu, mbar_wait(q_empty + qs, ((seg >> 1) - 1) & 1, abort));
+      if (!ok) break;
+      const int pos0 = sw.len[sw.b] + a.base - a.Tq;
+      uint8_t* q = smem + L.q + qs * a.tiles * 16 * C::kSpan;
+      for (int r0 = 0; r0 < a.tiles * 8; r0 += kRows) {
+        const int r = r0 + lane / kCPR;
+        uint4 hi, lo;
+        query_chunk<D>(a, sw.b, sw.g, r, c, pos0, hi, lo);
+        uint8_t* tile = q + (r >> 3) * 16 * C::kSpan;
+        *reinterpret_cast<uint4*>(tile + swz(r & 7, c, C::kSpan)) = hi;
+        *reinterpret_cast<uint4*>(tile + swz((r & 7) + 8, c, C::kSpan)) = lo;
+      }
+      warp_arrive(q_full + qs);
+    }
+    if (!ok && lane == 0) {
+      *abort = 1;
+      atomicCAS(a.status, 0, kStatusTimeout);
+    }
+  }
+}
+
+// The counters of the (sequence, head)s that several blocks share.
+__global__ void k_paged_clear(unsigned* done, int n) {
+  pdl_launch();
+  for (int i = threadIdx.x; i < n; i += blockDim.x) done[i] = 0u;
+}
+
+template <int D, int MT>
+cudaError_t launch_sweep_t(const PagedDecodeArgs& a, int nsm, cudaStream_t s) {
+  static bool attr_set[64] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!attr_set[dev]) {
+    cudaError_t e = cudaFuncSetAttribute(k_paged_sweep<D, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
+    if (e != cudaSuccess) return e;
+    attr_set[dev] = true;
+  }
+  PagedDecodeArgs b = a;
+  b.stages = Sweep<D>::kMaxStages;
+  while (b.stages > 2 && sweep_smem(D, b.stages, b.tiles, MT, b.B).total > kSmemMax) b.stages--;
+  const int bytes = sweep_smem(D, b.stages, b.tiles, MT, b.B).total;
+  if (bytes > kSmemMax) return cudaErrorInvalidValue;
+  k_paged_clear<<<1, 256, 0, s>>>(b.done, kPagedMaxBlocks);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  return launch_pdl(k_paged_sweep<D, MT>, nsm < kPagedMaxBlocks ? nsm : kPagedMaxBlocks, kSweepThreads, (size_t)bytes, s, b);
 }
 
 }  // namespace
@@ -208,13 +725,16 @@ cudaError_t launch_kv_append_paged(const PagedAppendArgs& a, int D, cudaStream_t
   return cudaGetLastError();
 }
 
-cudaError_t launch_decode_paged(const PagedDecodeArgs& a, cudaStream_t s) {
-  const unsigned grid = (unsigned)(a.B * a.Tq * a.Hq);
+void paged_rows(int R, int* mt, int* tiles, int* mg) {
+  *mt = R <= 8 ? 1 : (R <= 16 ? 2 : 4);
+  *mg = R <= 32 ? 1 : (R <= 64 ? 2 : 4);
+  *tiles = *mt * *mg;
+}
+
+cudaError_t launch_decode_paged(const PagedDecodeArgs& a, int mt, int nsm, cudaStream_t s) {
   if (a.D == 64)
-    k_decode_paged<64><<<grid, 128, 0, s>>>(a);
-  else
-    k_decode_paged<32><<<grid, 128, 0, s>>>(a);
-  return cudaGetLastError();
+    return mt == 1 ? launch_sweep_t<64, 1>(a, nsm, s) : (mt == 2 ? launch_sweep_t<64, 2>(a, nsm, s) : launch_sweep_t<64, 4>(a, nsm, s));
+  return mt == 1 ? launch_sweep_t<32, 1>(a, nsm, s) : (mt == 2 ? launch_sweep_t<32, 2>(a, nsm, s) : launch_sweep_t<32, 4>(a, nsm, s));
 }
 
 }  // namespace ne
