@@ -489,6 +489,10 @@ int check_paged(int B, int Hq, int Hkv, int D, int page_size, int num_pages, int
   if (page_stride >= (1LL << 39)) return NE_ERR_UNSUPPORTED;  // a tensor map's stride, in bytes
   return NE_OK;
 }
+// The sweep counts key tiles of every (sequence, head) in 32 bits.
+int check_paged_tiles(int B, int Hkv, int page_size, int max_pages) {
+  return (long long)B * Hkv * (((long long)max_pages * page_size + 127) / 128) < (1LL << 30) ? NE_OK : NE_ERR_UNSUPPORTED;
+}
 int check_decode_paged_rows(int B, int Tq, int Hq, int Hkv, int D) {
   if ((long long)(Hq / Hkv) * Tq > kTile) return NE_ERR_UNSUPPORTED;
   if ((long long)B * Tq * Hq * D >= (1LL << 31)) return NE_ERR_UNSUPPORTED;
@@ -1392,6 +1396,7 @@ int ne_attn_decode_paged(const void* q, const void* q_w, const void* k_pages, co
   int st = check_paged(B, Hq, Hkv, D, page_size, num_pages, max_pages, page_stride);
   if (st != NE_OK) return st;
   if ((st = check_decode_paged_rows(B, Tq, Hq, Hkv, D)) != NE_OK) return st;
+  if ((st = check_paged_tiles(B, Hkv, page_size, max_pages)) != NE_OK) return st;
   if (!row_stride_ok(q_stride, Hq, D)) return NE_ERR_ARG;
   if (prefix_len < 0 || prefix_len % page_size != 0 || prefix_len > max_pages * page_size ||
       (prefix_len > 0 && !prefix_table))
@@ -1439,7 +1444,6 @@ int ne_attn_decode_paged(const void* q, const void* q_w, const void* k_pages, co
   a.part_o = reinterpret_cast<float*>(ws + w.part_o);
   a.part_ml = reinterpret_cast<float2*>(ws + w.part_ml);
   a.done = reinterpret_cast<unsigned*>(ws + w.done);
-  a.min_tiles = 1;
   int mt = 1;
   paged_rows(a.R, &mt, &a.tiles, &a.MG);
   const int rows = page_size < (D == 64 ? 128 : 256) ? page_size : (D == 64 ? 128 : 256);

@@ -229,7 +229,7 @@ struct PagedDecodeArgs {
   int B, Tq, Hq, Hkv, D, G, R, page_shift, num_pages, max_pages, prefix_len, rope_half, o_fp32;
   int base;         // positions before the part of every sequence that the sweep reads (a shared prefix read elsewhere)
   int tiles, MG;    // packed row tiles (8 rows each) and the groups of warps that share them
-  int stages, min_tiles;
+  int stages;
   float eps, scale_log2;
 };
 

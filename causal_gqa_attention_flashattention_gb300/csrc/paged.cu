@@ -141,20 +141,25 @@ struct Sweep {
   static constexpr int kSlices = kTK / 16;
   static constexpr int kMaxStages = 6;
 };
-constexpr int kSweepWarps = 8;                       // consumers; then the producer and the query warp
-constexpr int kSweepThreads = (kSweepWarps + 4) * 32;  // whole warpgroups: two warps of the third stay idle
-constexpr int kBarBytes = 256;
+// Consumer warps: 16 where the accumulators leave each at most 104 registers, else 8.
+// They work in groups of eight on alternate tiles: a warp's tile is one chain of dependent
+// instructions (about 1200 cycles), and four chains per scheduler hide it where two
+// do not.
+constexpr int sweep_warps(int D, int mt) { return mt * D <= 64 ? 16 : 8; }
+constexpr int sweep_threads(int D, int mt) { return (sweep_warps(D, mt) + 4) * 32; }  // the last warpgroup: producer, queries, two idle
+constexpr int kBarBytes = 384;
+constexpr int kWholeTiles = 8;  // a (sequence, head) of at most this many tiles is never split
 
 // Shared memory behind the ring, in bytes (tiles: packed row tiles, mt: of one warp).
 struct SweepSmem {
   int q, scratch, ml, cum, len, bars, total;
 };
-__host__ __device__ inline SweepSmem sweep_smem(int D, int stages, int tiles, int mt, int B) {
-  SweepSmem m;
+__host__ __device__ constexpr SweepSmem sweep_smem(int D, int stages, int tiles, int mt, int B) {
+  SweepSmem m = {};
   m.q = stages * 32768;
   m.scratch = m.q + 2 * tiles * 16 * D * 2;
-  m.ml = m.scratch + kSweepWarps * mt * 8 * D * 4;
-  m.cum = m.ml + kSweepWarps * mt * 8 * 8;
+  m.ml = m.scratch + sweep_warps(D, mt) * mt * 8 * D * 4;
+  m.cum = m.ml + sweep_warps(D, mt) * mt * 8 * 8;
   m.len = m.cum + (B + 1) * 4;
   m.bars = (m.len + B * 4 + 15) / 16 * 16;
   m.total = m.bars + kBarBytes + 1024;
@@ -188,38 +193,52 @@ __device__ __forceinline__ void mma_b16(float (&d)[4], const uint32_t (&a)[4], u
 struct SegWalk {
   const int *cum, *len;  // shared memory: tiles before sequence b (one head), positions of b's own part
   int Hkv, B;
-  long long W, w, end;
+  int W, w, end, s_first;
   int G;                 // blocks that take part
   int b, g, n0, n1, nt;  // the segment: key tiles [n0, n1) of nt
-  long long s0;          // the (sequence, head)'s first tile among all
-  __device__ long long start(long long c) const { return c * W / G; }
-  __device__ int owner(long long x) const { return (int)(((x + 1) * G - 1) / W); }
-  __device__ void init(int block, int grid, int min_tiles) {
-    W = (long long)cum[B] * Hkv;
-    const long long most = W / min_tiles;
-    G = most < 1 ? 1 : (most < grid ? (int)most : grid);
-    w = block < G ? start(block) : 0;
-    end = block < G ? start(block + 1) : 0;
-    int lo = 0, hi = B;  // the sequence of tile w: last b with Hkv * cum[b] <= w
+  int s0;                // the (sequence, head)'s first tile among all
+  // A block's stretch starts at c W / G, moved to the nearer end of a (sequence, head) of at
+  // most kWholeTiles tiles it would cut: joining a cut one costs about 3 us at the end,
+  // as much as five tiles, moving the boundary at most half the tiles.  Inside longer ones
+  // the boundaries stay, so owner() needs the unmoved starts only.
+  __device__ int find(int x) const {  // last b with Hkv * cum[b] <= x
+    int lo = 0, hi = B;
     while (hi - lo > 1) {
       const int mid = (lo + hi) / 2;
-      if ((long long)cum[mid] * Hkv <= w)
+      if (cum[mid] * Hkv <= x)
         lo = mid;
       else
         hi = mid;
     }
-    b = lo;
+    return lo;
+  }
+  __device__ int start(int c) const {
+    const int x = (int)((long long)c * W / G);
+    if (x >= W) return W;
+    const int i = find(x), n = cum[i + 1] - cum[i];
+    const int off = (x - cum[i] * Hkv) % n;
+    if (n > kWholeTiles || off == 0) return x;
+    return 2 * off < n ? x - off : x - off + n;
+  }
+  __device__ int owner(int x) const { return (int)(((x + 1LL) * G - 1) / W); }
+  __device__ void init(int block, int grid) {
+    W = cum[B] * Hkv;
+    G = W < grid ? W : grid;
+    w = block < G ? start(block) : 0;
+    end = block < G ? start(block + 1) : 0;
+    s_first = w;
+    b = find(w < W ? w : W - 1);
     n1 = 0;
   }
   __device__ bool next() {
     if (w >= end) return false;
-    while ((long long)cum[b + 1] * Hkv <= w) b++;
+    while (cum[b + 1] * Hkv <= w) b++;
     nt = cum[b + 1] - cum[b];
-    const long long off = w - (long long)cum[b] * Hkv;
-    g = (int)(off / nt);
-    n0 = (int)(off - (long long)g * nt);
+    const int off = w - cum[b] * Hkv;
+    g = off / nt;
+    n0 = off - g * nt;
     s0 = w - n0;
-    n1 = (int)(end - w < nt - n0 ? n0 + (end - w) : nt);
+    n1 = min(nt, n0 + (end - w));
     w += n1 - n0;
     return true;
   }
@@ -297,20 +316,35 @@ __device__ __forceinline__ void write_row(const PagedDecodeArgs& a, int b, int g
   if (q == 0 && a.lse) a.lse[((size_t)b * a.Hq + h) * a.Tq + t] = L > 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
 }
 
+// Adds the part (maximum z in log2 units, sum, O) to (M, S, v); a sum of 0 saw no key.
+__device__ __forceinline__ void merge4(float& M, float& S, float4& v, float z, float zs, float4 u) {
+  const float top = fmaxf(M, z);
+  const float f = S != 0.f ? ex2(M - top) : 0.f, g = zs != 0.f ? ex2(z - top) : 0.f;
+  M = top;
+  S = S * f + zs * g;
+  v.x = f == 0.f ? u.x * g : (g == 0.f ? v.x * f : fmaf(u.x, g, v.x * f));
+  v.y = f == 0.f ? u.y * g : (g == 0.f ? v.y * f : fmaf(u.y, g, v.y * f));
+  v.z = f == 0.f ? u.z * g : (g == 0.f ? v.z * f : fmaf(u.z, g, v.z * f));
+  v.w = f == 0.f ? u.w * g : (g == 0.f ? v.w * f : fmaf(u.w, g, v.w * f));
+}
+
 template <int D, int MT>
 __device__ bool sweep_consume(const PagedDecodeArgs& a, SegWalk sw, uint8_t* smem, const SweepSmem& L, uint64_t* full,
                               uint64_t* empty, uint64_t* q_full, uint64_t* q_empty, uint64_t* gbar, volatile int* flag,
                               volatile int* abort, int warp, int lane) {
   using C = Sweep<D>;
   constexpr int KS = D / 16;
-  const int KG = kSweepWarps / a.MG, mg = warp / KG, kg = warp - mg * KG;
+  constexpr int kWarps = sweep_warps(D, MT), kGroups = kWarps / 8;
+  const int grp = warp >> 3;                    // takes every kGroups-th tile
+  const int KG = MT < 4 ? 8 : 8 / a.MG;         // warps over a tile's keys; the rest share the row tiles out
+  const int mg = (warp & 7) / KG, kg = (warp & 7) - mg * KG;
   const uint32_t ring = smem_u32(smem);
   const float sl2 = a.scale_log2;
   // this lane's ldmatrix row and chunk parity (keys, values and queries alike)
   const uint32_t lrow = lane & 15, lchk = lane >> 4;
   float* scratch = reinterpret_cast<float*>(smem + L.scratch);
   float2* ml = reinterpret_cast<float2*>(smem + L.ml);
-  int st = 0, ph = 0, gphase = 0, seg = 0;
+  int st = 0, ph = 0, gphase = 0, seg = 0, turn = 0;
   bool waited = false;
   for (; sw.next(); seg++) {
     const int own = sw.len[sw.b], total = own + a.base;
@@ -341,6 +375,15 @@ __device__ bool sweep_consume(const PagedDecodeArgs& a, SegWalk sw, uint8_t* sme
         for (int e = 0; e < 4; e++) o[m][i][e] = 0.f;
     }
     for (int n = sw.n0; n < sw.n1; n++) {
+      const bool mine = kGroups == 1 || turn == grp;
+      if (kGroups > 1) turn = turn + 1 == kGroups ? 0 : turn + 1;
+      if (!mine) {
+        if (++st == a.stages) {
+          st = 0;
+          ph ^= 1;
+        }
+        continue;
+      }
       if (!__all_sync(0xffffffffu, mbar_wait(full + st, ph, abort))) return false;
       const uint32_t kb = ring + st * C::kStage, vb = kb + C::kHalf;
       for (int sl = kg; sl < C::kSlices; sl += KG) {
@@ -449,20 +492,23 @@ __device__ bool sweep_consume(const PagedDecodeArgs& a, SegWalk sw, uint8_t* sme
     }
     const bool whole = sw.n0 == 0 && sw.n1 == sw.nt;
     const int c0 = whole ? 0 : sw.owner(sw.s0), c1 = whole ? 0 : sw.owner(sw.s0 + sw.nt - 1);
-    const int slot = 2 * (int)blockIdx.x + (sw.s0 <= sw.start(blockIdx.x) ? 0 : 1);
+    const int slot = 2 * (int)blockIdx.x + (sw.s0 <= sw.s_first ? 0 : 1);
     const int tid = warp * 32 + lane;
-    for (int i = tid; i < a.R * (D / 4); i += kSweepWarps * 32) {
+    for (int i = tid; i < a.R * (D / 4); i += kWarps * 32) {
       const int r = i / (D / 4), q = i % (D / 4), tile = r >> 3, w0 = (tile / MT) * KG;
       const int at = (w0 * MT + tile % MT) * 8 + (r & 7);
+      // the row's warps: KG of each group of eight
+      const int parts = KG * kGroups;
       float M = -INFINITY;
-      for (int k = 0; k < KG; k++) M = fmaxf(M, ml[at + k * MT * 8].x);
+      for (int k = 0; k < parts; k++) M = fmaxf(M, ml[at + (k % KG + k / KG * 8) * MT * 8].x);
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
       float S = 0.f;
-      for (int k = 0; k < KG; k++) {
-        const float2 z = ml[at + k * MT * 8];
+      for (int k = 0; k < parts; k++) {
+        const int from = at + (k % KG + k / KG * 8) * MT * 8;
+        const float2 z = ml[from];
         if (z.y == 0.f) continue;  // no visible key
         const float f = ex2(z.x - M);
-        const float4 u = *reinterpret_cast<const float4*>(scratch + (at + k * MT * 8) * D + 4 * q);
+        const float4 u = *reinterpret_cast<const float4*>(scratch + from * D + 4 * q);
         S = fmaf(f, z.y, S);
         v = make_float4(fmaf(f, u.x, v.x), fmaf(f, u.y, v.y), fmaf(f, u.z, v.z), fmaf(f, u.w, v.w));
       }
@@ -482,24 +528,31 @@ __device__ bool sweep_consume(const PagedDecodeArgs& a, SegWalk sw, uint8_t* sme
     }
     if (!meet(gbar, gphase, abort)) return false;
     if (*flag) {
+      // Item i is four columns of a row; kSplit neighbouring lanes share its segments and add up
+      // by shuffles (each its own in order, then lane by lane: the same sum every time).
       __threadfence();
+      constexpr int kSplit = 8;
       const int first = 2 * c0 + (sw.s0 <= sw.start(c0) ? 0 : 1);
-      for (int i = tid; i < a.R * (D / 4); i += kSweepWarps * 32) {
+      const int sub = tid % kSplit, items = a.R * (D / 4);
+      for (int i0 = 0; i0 < items; i0 += kWarps * 32 / kSplit) {
+        const int i = min(i0 + tid / kSplit, items - 1);
         const int r = i / (D / 4), q = i % (D / 4);
-        float M = -INFINITY;
-        for (int c = c0; c <= c1; c++) M = fmaxf(M, __ldcg(&a.part_ml[(size_t)(c == c0 ? first : 2 * c) * a.R + r].x));
+        float M = -INFINITY, S = 0.f;
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        float S = 0.f;
-        for (int c = c0; c <= c1; c++) {
+        for (int c = c0 + sub; c <= c1; c += kSplit) {
           const size_t at = (size_t)(c == c0 ? first : 2 * c) * a.R + r;
           const float2 z = __ldcg(&a.part_ml[at]);
-          if (z.y == 0.f) continue;
-          const float f = ex2(z.x - M);
           const float4 u = __ldcg(reinterpret_cast<const float4*>(a.part_o + at * D + 4 * q));
-          S = fmaf(f, z.y, S);
-          v = make_float4(fmaf(f, u.x, v.x), fmaf(f, u.y, v.y), fmaf(f, u.z, v.z), fmaf(f, u.w, v.w));
+          merge4(M, S, v, z.x, z.y, u);
         }
-        write_row<D>(a, sw.b, sw.g, r, q, v, M, S);
+#pragma unroll
+        for (int m = 1; m < kSplit; m <<= 1) {
+          const float zm = __shfl_xor_sync(0xffffffffu, M, m), zs = __shfl_xor_sync(0xffffffffu, S, m);
+          const float4 u = make_float4(__shfl_xor_sync(0xffffffffu, v.x, m), __shfl_xor_sync(0xffffffffu, v.y, m),
+                                       __shfl_xor_sync(0xffffffffu, v.z, m), __shfl_xor_sync(0xffffffffu, v.w, m));
+          merge4(M, S, v, zm, zs, u);
+        }
+        if (sub == 0 && i0 + tid / kSplit < items) write_row<D>(a, sw.b, sw.g, r, q, v, M, S);
       }
       // flag is written again only after the next segment's first meeting
     }
@@ -508,8 +561,9 @@ __device__ bool sweep_consume(const PagedDecodeArgs& a, SegWalk sw, uint8_t* sme
 }
 
 template <int D, int MT>
-__global__ void __launch_bounds__(kSweepThreads, 1) k_paged_sweep(const __grid_constant__ PagedDecodeArgs a) {
+__global__ void __launch_bounds__(sweep_threads(D, MT), 1) k_paged_sweep(const __grid_constant__ PagedDecodeArgs a) {
   using C = Sweep<D>;
+  constexpr int kWarps = sweep_warps(D, MT), kThreads = sweep_threads(D, MT);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -521,7 +575,7 @@ __global__ void __launch_bounds__(kSweepThreads, 1) k_paged_sweep(const __grid_c
   uint64_t* gbar = q_empty + 2;
   volatile int* abort = reinterpret_cast<volatile int*>(gbar + 1);
   volatile int* flag = abort + 1;
-  int* wsum = const_cast<int*>(abort) + 2;   // [12] the scan's warp totals
+  int* wsum = const_cast<int*>(abort) + 2;   // [20] the scan's warp totals
   int* cum = reinterpret_cast<int*>(smem + L.cum);
   int* len = reinterpret_cast<int*>(smem + L.len);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -529,20 +583,20 @@ __global__ void __launch_bounds__(kSweepThreads, 1) k_paged_sweep(const __grid_c
     *abort = 0;
     for (int i = 0; i < a.stages; i++) {
       mbar_init(full + i, 1);
-      mbar_init(empty + i, kSweepWarps);
+      mbar_init(empty + i, 8);
     }
     for (int i = 0; i < 2; i++) {
       mbar_init(q_full + i, 1);
-      mbar_init(q_empty + i, kSweepWarps);
+      mbar_init(q_empty + i, kWarps);
     }
-    mbar_init(gbar, kSweepWarps);
+    mbar_init(gbar, kWarps);
     fence_mbar_init();
     cum[0] = 0;
   }
   // lengths of the own parts and the running count of their tiles
   const int cap = a.max_pages << a.page_shift;
   int before = 0;
-  for (int b0 = 0; b0 < a.B; b0 += kSweepThreads) {
+  for (int b0 = 0; b0 < a.B; b0 += kThreads) {
     const int b = b0 + tid;
     int own = 0, nt = 0;
     if (b < a.B) {
@@ -565,7 +619,7 @@ __global__ void __launch_bounds__(kSweepThreads, 1) k_paged_sweep(const __grid_c
     if (lane == 31) wsum[warp] = x;
     __syncthreads();
     int all = 0;
-    for (int i = 0; i < kSweepThreads / 32; i++) {
+    for (int i = 0; i < kThreads / 32; i++) {
       if (i < warp) x += wsum[i];
       all += wsum[i];
     }
@@ -578,11 +632,15 @@ __global__ void __launch_bounds__(kSweepThreads, 1) k_paged_sweep(const __grid_c
   sw.len = len;
   sw.Hkv = a.Hkv;
   sw.B = a.B;
-  sw.init(blockIdx.x, gridDim.x, a.min_tiles);
+  sw.init(blockIdx.x, gridDim.x);
   const volatile int never = 0;
-  // registers: 384 x 168 at launch; 256 x 216 for the consumers, 128 x 72 for the others
-  if (warp < kSweepWarps) {
-    regs_inc<216>();
+  // Registers at launch, and what the consumers and the others then hold: 640 x 96 = 512 x 104 +
+  // 128 x 64, or 384 x 168 = 256 x 216 + 128 x 72.
+  if (warp < kWarps) {
+    if (kWarps == 16)
+      regs_inc<104>();
+    else
+      regs_inc<216>();
     const bool ok = sweep_consume<D, MT>(a, sw, smem, L, full, empty, q_full, q_empty, gbar, flag, abort, warp, lane);
     if (!ok && lane == 0) {
       *abort = 1;
@@ -590,8 +648,11 @@ __global__ void __launch_bounds__(kSweepThreads, 1) k_paged_sweep(const __grid_c
     }
     return;
   }
-  regs_dec<72>();
-  if (warp == kSweepWarps) {
+  if (kWarps == 16)
+    regs_dec<64>();
+  else
+    regs_dec<72>();
+  if (warp == kWarps) {
     // ------------------------------------------------------------ keys and values
     // Lane i loads page i of a tile; the page numbers come 32 at a time.
     const int prows = min(1 << a.page_shift, C::kTK), per = C::kTK / prows;
@@ -658,7 +719,7 @@ __global__ void __launch_bounds__(kSweepThreads, 1) k_paged_sweep(const __grid_c
         for (int x = max(0, issued - a.stages); x < issued; x++)
           mbar_wait(full + x % a.stages, (x / a.stages) & 1, &never);
     }
-  } else if (warp == kSweepWarps + 1) {
+  } else if (warp == kWarps + 1) {
     // ------------------------------------------------------------ queries
     constexpr int kCPR = D / 8, kRows = 32 / kCPR;
     const int c = lane % kCPR;
@@ -704,13 +765,17 @@ cudaError_t launch_sweep_t(const PagedDecodeArgs& a, int nsm, cudaStream_t s) {
   }
   PagedDecodeArgs b = a;
   b.stages = Sweep<D>::kMaxStages;
-  while (b.stages > 2 && sweep_smem(D, b.stages, b.tiles, MT, b.B).total > kSmemMax) b.stages--;
+  // An even ring with two groups of consumers: every stage then belongs to one of them.  In an
+  // odd one a group could wait for a stage's next round while the other's round has not yet
+  // landed, and a parity wait would take the round before that for it.
+  constexpr int kGroups = sweep_warps(D, MT) / 8;
+  while (b.stages > 2 && sweep_smem(D, b.stages, b.tiles, MT, b.B).total > kSmemMax) b.stages -= kGroups;
   const int bytes = sweep_smem(D, b.stages, b.tiles, MT, b.B).total;
   if (bytes > kSmemMax) return cudaErrorInvalidValue;
   k_paged_clear<<<1, 256, 0, s>>>(b.done, kPagedMaxBlocks);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  return launch_pdl(k_paged_sweep<D, MT>, nsm < kPagedMaxBlocks ? nsm : kPagedMaxBlocks, kSweepThreads, (size_t)bytes, s, b);
+  return launch_pdl(k_paged_sweep<D, MT>, nsm < kPagedMaxBlocks ? nsm : kPagedMaxBlocks, sweep_threads(D, MT), (size_t)bytes, s, b);
 }
 
 }  // namespace

@@ -389,7 +389,8 @@ int ne_attn_kv_append_paged(const void* k_new, const void* v_new, const void* k_
  * sequences.  The result is that of the same call with those pages in every
  * sequence's own table and prefix_len = 0, up to rounding.
  *
- * Requires (Hq / Hkv) * Tq <= 128 and the workspace
+ * Requires (Hq / Hkv) * Tq <= 128, B * Hkv * ceil(max_pages * page_size / 128)
+ * < 2^30 and the workspace
  * (ne_attn_decode_paged_workspace_size bytes, 256-byte aligned); calls that may
  * run at the same time need workspaces of their own.
  */
