@@ -221,7 +221,8 @@ def status_of_last_kernels(stream=None):
 
 
 KERNEL_KINDS = ("fwd", "bwd_prep", "bwd_dkdv", "bwd_dq", "fwd_rope", "kv_append", "decode", "decode_aux",
-                "qkv_prep", "qkv", "qk_norm", "qk_norm_bwd", "qk_norm_dw", "kv_append_paged", "decode_paged")
+                "qkv_prep", "qkv", "qk_norm", "qk_norm_bwd", "qk_norm_dw", "kv_append_paged", "decode_paged",
+                "decode_prefix")
 
 
 def profile_start(capacity):

@@ -493,22 +493,33 @@ int check_paged(int B, int Hq, int Hkv, int D, int page_size, int num_pages, int
 int check_paged_tiles(int B, int Hkv, int page_size, int max_pages) {
   return (long long)B * Hkv * (((long long)max_pages * page_size + 127) / 128) < (1LL << 30) ? NE_OK : NE_ERR_UNSUPPORTED;
 }
+// Whether a shared prefix goes through the prefix kernel: see ne_attn_decode_paged.
+bool prefix_shared(int B, int Hkv, int prefix_len) { return true; }
 int check_decode_paged_rows(int B, int Tq, int Hq, int Hkv, int D) {
   if ((long long)(Hq / Hkv) * Tq > kTile) return NE_ERR_UNSUPPORTED;
-  if ((long long)B * Tq * Hq * D >= (1LL << 31)) return NE_ERR_UNSUPPORTED;
+  if (((long long)B * Tq * Hq + (long long)Hkv * kTile) * D >= (1LL << 31)) return NE_ERR_UNSUPPORTED;
   return NE_OK;
 }
 
 // Decode workspace: the split segments' O, their (maximum, sum), the counters.
+// With a shared prefix then its packed queries and its segments' O and (maximum, sum).
 struct PagedWs {
-  size_t part_o, part_ml, done, total;
+  size_t part_o, part_ml, done, pq, pp_o, pp_ml, total;
 };
-PagedWs paged_ws(int R, int D) {
+int prefix_tiles(int B, int R) { return (int)(((long long)B * R + kTile - 1) / kTile); }
+PagedWs paged_ws(int B, int R, int Hkv, int D, bool prefix) {
   PagedWs w;
   w.part_o = 0;
   w.part_ml = ws_up((size_t)2 * kPagedMaxBlocks * R * D * 4);
   w.done = w.part_ml + ws_up((size_t)2 * kPagedMaxBlocks * R * 8);
   w.total = w.done + ws_up((size_t)kPagedMaxBlocks * 4);
+  w.pq = w.pp_o = w.pp_ml = w.total;
+  if (prefix) {
+    const size_t tiles = prefix_tiles(B, R), segs = kPagedMaxBlocks + (size_t)Hkv * ((tiles + 1) / 2);
+    w.pp_o = w.pq + ws_up((size_t)Hkv * tiles * kTile * D * 2);
+    w.pp_ml = w.pp_o + ws_up(segs * 2 * kTile * D * 4);
+    w.total = w.pp_ml + ws_up(segs * 2 * kTile * 8);
+  }
   return w;
 }
 
@@ -1380,7 +1391,7 @@ int ne_attn_kv_append_paged(const void* k_new, const void* v_new, const void* k_
 size_t ne_attn_decode_paged_workspace_size(int B, int Tq, int Hq, int Hkv, int D, int prefix_len) {
   if (check_paged(B, Hq, Hkv, D, 16, 1, 1, 16LL * Hkv * D) != NE_OK || Tq < 1 || prefix_len < 0) return 0;
   if (check_decode_paged_rows(B, Tq, Hq, Hkv, D) != NE_OK) return 0;
-  return paged_ws((Hq / Hkv) * Tq, D).total;
+  return paged_ws(B, (Hq / Hkv) * Tq, Hkv, D, prefix_len > 0).total;
 }
 
 int ne_attn_decode_paged(const void* q, const void* q_w, const void* k_pages, const void* v_pages,
@@ -1397,6 +1408,8 @@ int ne_attn_decode_paged(const void* q, const void* q_w, const void* k_pages, co
   if (st != NE_OK) return st;
   if ((st = check_decode_paged_rows(B, Tq, Hq, Hkv, D)) != NE_OK) return st;
   if ((st = check_paged_tiles(B, Hkv, page_size, max_pages)) != NE_OK) return st;
+  if ((long long)Hkv * prefix_tiles(B, (Hq / Hkv) * Tq) * ((prefix_len + 127LL) / 128) >= (1LL << 30))
+    return NE_ERR_UNSUPPORTED;
   if (!row_stride_ok(q_stride, Hq, D)) return NE_ERR_ARG;
   if (prefix_len < 0 || prefix_len % page_size != 0 || prefix_len > max_pages * page_size ||
       (prefix_len > 0 && !prefix_table))
@@ -1439,7 +1452,7 @@ int ne_attn_decode_paged(const void* q, const void* q_w, const void* k_pages, co
   a.o_fp32 = (flags & kFlagOFp32) ? 1 : 0;
   a.eps = eps;
   a.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)D));
-  const PagedWs w = paged_ws(a.R, D);
+  const PagedWs w = paged_ws(B, a.R, Hkv, D, prefix_len > 0);
   unsigned char* ws = static_cast<unsigned char*>(workspace);
   a.part_o = reinterpret_cast<float*>(ws + w.part_o);
   a.part_ml = reinterpret_cast<float2*>(ws + w.part_ml);
@@ -1453,6 +1466,30 @@ int ne_attn_decode_paged(const void* q, const void* q_w, const void* k_pages, co
   if ((st = make_map_pages(&a.map_v, v_pages, num_pages, Hkv, page_size, D, page_stride, rows,
                            CU_TENSOR_MAP_DATA_TYPE_BFLOAT16)) != NE_OK)
     return st;
+  if (prefix_len > 0 && prefix_shared(B, Hkv, prefix_len)) {
+    a.base = prefix_len;
+    PrefixArgs& p = a.pre;
+    p.q = reinterpret_cast<__half*>(ws + w.pq);
+    p.part_o = reinterpret_cast<float*>(ws + w.pp_o);
+    p.part_ml = reinterpret_cast<float2*>(ws + w.pp_ml);
+    p.tiles = prefix_tiles(B, a.R);
+    p.pairs = (p.tiles + 1) / 2;
+    p.ntk = (prefix_len + kTile - 1) / kTile;
+    p.W = Hkv * p.pairs * p.ntk;
+    const int most = nsm < kPagedMaxBlocks ? nsm : kPagedMaxBlocks;
+    p.blocks = p.W < most ? p.W : most;
+    const int prows = page_size < kTile ? page_size : kTile;
+    if ((st = make_map_bthd(&a.map_q, p.q, 1, Hkv * p.tiles * kTile, 1, D, CU_TENSOR_MAP_DATA_TYPE_FLOAT16)) != NE_OK)
+      return st;
+    if ((st = make_map_pages(&a.map_pk, k_pages, num_pages, Hkv, page_size, D, page_stride, prows,
+                             CU_TENSOR_MAP_DATA_TYPE_FLOAT16)) != NE_OK)
+      return st;
+    if ((st = make_map_pages(&a.map_pv, v_pages, num_pages, Hkv, page_size, D, page_stride, prows,
+                             CU_TENSOR_MAP_DATA_TYPE_BFLOAT16)) != NE_OK)
+      return st;
+    ProfScope prof(NE_ATTN_KERNEL_DECODE_PREFIX, s);
+    if (launch_prefix(a, s) != cudaSuccess) return NE_ERR_CUDA;
+  }
   ProfScope prof(NE_ATTN_KERNEL_DECODE_PAGED, s);
   return launch_decode_paged(a, mt, nsm, s) == cudaSuccess ? NE_OK : NE_ERR_CUDA;
 }

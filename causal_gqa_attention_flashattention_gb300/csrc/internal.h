@@ -214,8 +214,25 @@ struct PagedAppendArgs {
 
 // Attention of the newest tokens over a paged cache (see paged.cu).
 constexpr int kPagedMaxBlocks = 160;  // blocks of the sweep: bounds its partial results
+// The shared prefix's part of it (see paged_prefix.cu): key tiles of 128 positions over every
+// (key/value head, pair of 128-row tiles), in one line, block c's stretch [c W / blocks, ..).
+struct PrefixArgs {
+  __half* q;        // [Hkv, tiles * 128, D] packed rotated queries (workspace)
+  float* part_o;    // [blocks + Hkv * pairs, 2, 128, D] unnormalised O of segment (block c, (head, pair) s) at c + s
+  float2* part_ml;  // [.., 2, 128] maximum (log2 units) and sum of the rows
+  int tiles, pairs, ntk, W, blocks;
+};
+#ifdef __CUDACC__
+// The block whose stretch tile x lies in.
+__host__ __device__ inline int prefix_owner(const PrefixArgs& p, int x) {
+  return (int)(((x + 1LL) * p.blocks - 1) / p.W);
+}
+#endif
+
 struct PagedDecodeArgs {
   CUtensorMap map_k, map_v;     // pools {D, page, Hkv, num_pages}, box D x min(page, tile) rows
+  CUtensorMap map_q, map_pk, map_pv;  // prefix kernel: packed queries, the pools with its own tile
+  PrefixArgs pre;
   const __nv_bfloat16 *q, *qw;  // [B, Tq, Hq, D], positions q_stride values apart; qw [D] or null
   const int *table, *len, *prefix_table;
   const float2* rope;
@@ -227,7 +244,7 @@ struct PagedDecodeArgs {
   unsigned* done;   // [blocks] segments finished of the (sequence, head) that starts in a block
   long long q_stride;
   int B, Tq, Hq, Hkv, D, G, R, page_shift, num_pages, max_pages, prefix_len, rope_half, o_fp32;
-  int base;         // positions before the part of every sequence that the sweep reads (a shared prefix read elsewhere)
+  int base;         // shared positions that the prefix kernel reads (0: none, the sweep reads all)
   int tiles, MG;    // packed row tiles (8 rows each) and the groups of warps that share them
   int stages;
   float eps, scale_log2;
@@ -258,6 +275,7 @@ int qk_norm_bwd_blocks(int B, int T, int hg, int D, int nsm);
 cudaError_t launch_qk_norm_bwd(const QkNormBwdArgs& a, int D, bool f32, int blocks, cudaStream_t s);
 cudaError_t launch_qk_norm_dw(const QkNormBwdArgs& a, int D, int blocks, float* dwq, float* dwk, cudaStream_t s);
 cudaError_t launch_kv_append_paged(const PagedAppendArgs& a, int D, cudaStream_t s);
+cudaError_t launch_prefix(const PagedDecodeArgs& a, cudaStream_t s);
 void paged_rows(int R, int* mt, int* tiles, int* mg);
 cudaError_t launch_decode_paged(const PagedDecodeArgs& a, int mt, int nsm, cudaStream_t s);
 

@@ -12,6 +12,7 @@
 #include <cuda_fp16.h>
 
 #include "internal.h"
+#include "paged.cuh"
 #include "ptx.cuh"
 #include "rope.cuh"
 
@@ -20,8 +21,6 @@ namespace {
 
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr int kSmemMax = 232448;
-
-__device__ __forceinline__ void record_page(int* status) { atomicCAS(status, 0, kStatusPage); }
 
 // ====================================================================== append
 // New row n belongs to the sequence s with cu[s] <= n < cu[s + 1] (rows at or
@@ -191,7 +190,7 @@ __device__ __forceinline__ void mma_b16(float (&d)[4], const uint32_t (&a)[4], u
 
 // The block's place in the work: tiles [w, end) of all, as segments.
 struct SegWalk {
-  const int *cum, *len;  // shared memory: tiles before sequence b (one head), positions of b's own part
+  const int *cum, *len;  // shared memory: tiles before sequence b (one head), positions of b
   int Hkv, B;
   int W, w, end, s_first;
   int G;                 // blocks that take part
@@ -244,55 +243,6 @@ struct SegWalk {
   }
 };
 
-// Rotated (and normalised) query row chunk as fp16 high and low parts.
-template <int D>
-__device__ __forceinline__ void query_chunk(const PagedDecodeArgs& a, int b, int g, int r, int c, int pos0, uint4& hi,
-                                            uint4& lo) {
-  constexpr int kCPR = D / 8;
-  const bool on = r < a.R;
-  const int t = on ? r / a.G : 0, gg = r - t * a.G;
-  uint4 v = make_uint4(0, 0, 0, 0);
-  if (on) v = load_rope_chunk<D>(a.q + (size_t)(b * a.Tq + t) * a.q_stride + (g * a.G + gg) * D, c, a.rope_half != 0);
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  float x[8];
-#pragma unroll
-  for (int p = 0; p < 4; p++) {
-    x[2 * p] = bf_lo(w[p]);
-    x[2 * p + 1] = bf_hi(w[p]);
-  }
-  if (a.qw) {
-    float ss = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; i++) ss = fmaf(x[i], x[i], ss);
-#pragma unroll
-    for (int m = 1; m < kCPR; m <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
-    const float rs = rsqrtf(fmaf(ss, 1.f / D, a.eps));
-    const uint4 wv = load_rope_chunk<D>(a.qw, c, a.rope_half != 0);
-    const uint32_t ww[4] = {wv.x, wv.y, wv.z, wv.w};
-#pragma unroll
-    for (int p = 0; p < 4; p++) {
-      x[2 * p] *= rs * bf_lo(ww[p]);
-      x[2 * p + 1] *= rs * bf_hi(ww[p]);
-    }
-  }
-  float4 c0, c1;
-  rope_coeffs<D>(a.rope, max(pos0 + t, 0), c, c0, c1);
-  const float cs[4] = {c0.x, c0.z, c1.x, c1.z}, sn[4] = {c0.y, c0.w, c1.y, c1.w};
-  uint32_t h[4], l[4];
-#pragma unroll
-  for (int p = 0; p < 4; p++) {
-    const float y0 = fmaf(x[2 * p], cs[p], -x[2 * p + 1] * sn[p]), y1 = fmaf(x[2 * p], sn[p], x[2 * p + 1] * cs[p]);
-    h[p] = pack_f16(y0, y1);
-    l[p] = pack_f16(y0 - f16_lo(h[p]), y1 - f16_hi(h[p]));
-  }
-  if (!on) {
-#pragma unroll
-    for (int p = 0; p < 4; p++) h[p] = l[p] = 0;
-  }
-  hi = make_uint4(h[0], h[1], h[2], h[3]);
-  lo = make_uint4(l[0], l[1], l[2], l[3]);
-}
-
 // All consumer warps meet (an mbarrier and not bar.sync: a warp that gave up must
 // not leave the others waiting for ever).
 __device__ __forceinline__ bool meet(uint64_t* bar, int& phase, volatile int* abort) {
@@ -316,6 +266,12 @@ __device__ __forceinline__ void write_row(const PagedDecodeArgs& a, int b, int g
   if (q == 0 && a.lse) a.lse[((size_t)b * a.Hq + h) * a.Tq + t] = L > 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
 }
 
+// Positions of a sequence that the sweep leaves to the prefix kernel: the whole shared
+// prefix if the first query sees all of it, else none.
+__device__ __forceinline__ int sweep_base(const PagedDecodeArgs& a, int len) {
+  return a.base > 0 && len - a.Tq + 1 >= a.base ? a.base : 0;
+}
+
 // Adds the part (maximum z in log2 units, sum, O) to (M, S, v); a sum of 0 saw no key.
 __device__ __forceinline__ void merge4(float& M, float& S, float4& v, float z, float zs, float4 u) {
   const float top = fmaxf(M, z);
@@ -326,6 +282,35 @@ __device__ __forceinline__ void merge4(float& M, float& S, float4& v, float z, f
   v.y = f == 0.f ? u.y * g : (g == 0.f ? v.y * f : fmaf(u.y, g, v.y * f));
   v.z = f == 0.f ? u.z * g : (g == 0.f ? v.z * f : fmaf(u.z, g, v.z * f));
   v.w = f == 0.f ? u.w * g : (g == 0.f ? v.w * f : fmaf(u.w, g, v.w * f));
+}
+
+// Adds the shared prefix's parts of row r of (sequence b, head g), columns 4 q ..; the kSplit
+// neighbouring lanes of a row share them out (every lane of the warp calls this).
+template <int D, int kSplit>
+__device__ __forceinline__ void merge_prefix(const PagedDecodeArgs& a, int b, int g, int r, int q, int sub, float& M,
+                                             float& S, float4& v) {
+  const PrefixArgs& p = a.pre;
+  const int rho = b * a.R + r, tile = rho / kTile, s = g * p.pairs + (tile >> 1);
+  const int lo = prefix_owner(p, s * p.ntk), hi = prefix_owner(p, s * p.ntk + p.ntk - 1);
+  const size_t row = (size_t)(tile & 1) * kTile + (rho & (kTile - 1));
+  for (int c = lo + sub; c <= hi; c += kSplit) {
+    const size_t at = (size_t)(c + s) * 2 * kTile + row;
+    const float2 z = __ldcg(&p.part_ml[at]);
+    const float4 u = __ldcg(reinterpret_cast<const float4*>(p.part_o + at * D + 4 * q));
+    merge4(M, S, v, z.x, z.y, u);
+  }
+}
+
+// Sums the parts of kSplit neighbouring lanes, the same way every time.
+template <int kSplit>
+__device__ __forceinline__ void merge_lanes(float& M, float& S, float4& v) {
+#pragma unroll
+  for (int m = 1; m < kSplit; m <<= 1) {
+    const float zm = __shfl_xor_sync(0xffffffffu, M, m), zs = __shfl_xor_sync(0xffffffffu, S, m);
+    const float4 u = make_float4(__shfl_xor_sync(0xffffffffu, v.x, m), __shfl_xor_sync(0xffffffffu, v.y, m),
+                                 __shfl_xor_sync(0xffffffffu, v.z, m), __shfl_xor_sync(0xffffffffu, v.w, m));
+    merge4(M, S, v, zm, zs, u);
+  }
 }
 
 template <int D, int MT>
@@ -347,8 +332,8 @@ __device__ bool sweep_consume(const PagedDecodeArgs& a, SegWalk sw, uint8_t* sme
   int st = 0, ph = 0, gphase = 0, seg = 0, turn = 0;
   bool waited = false;
   for (; sw.next(); seg++) {
-    const int own = sw.len[sw.b], total = own + a.base;
-    const int pos0 = total - a.Tq - a.base;  // row 0's position, counted from the own part's start
+    const int total = sw.len[sw.b], base = sweep_base(a, total), own = total - base;
+    const int pos0 = own - a.Tq;  // row 0's position, counted from the own part's start
     const int qs = seg & 1;
     if (!__all_sync(0xffffffffu, mbar_wait(q_full + qs, (seg >> 1) & 1, abort))) return false;
     const uint32_t qbase = smem_u32(smem + L.q) + (uint32_t)((qs * a.tiles + mg * MT) * 16) * C::kSpan;
@@ -494,29 +479,30 @@ __device__ bool sweep_consume(const PagedDecodeArgs& a, SegWalk sw, uint8_t* sme
     const int c0 = whole ? 0 : sw.owner(sw.s0), c1 = whole ? 0 : sw.owner(sw.s0 + sw.nt - 1);
     const int slot = 2 * (int)blockIdx.x + (sw.s0 <= sw.s_first ? 0 : 1);
     const int tid = warp * 32 + lane;
-    for (int i = tid; i < a.R * (D / 4); i += kWarps * 32) {
+    // Item i is four columns of a row; kSplit neighbouring lanes share the parts it is made of (each
+    // its own in order, then lane by lane: the same sum every time).
+    constexpr int kSplit = 8;
+    const int sub = tid % kSplit, items = a.R * (D / 4);
+    const int parts = KG * kGroups;  // warps that hold a part of the row
+    for (int i0 = 0; i0 < items; i0 += kWarps * 32 / kSplit) {
+      const int i = min(i0 + tid / kSplit, items - 1);
       const int r = i / (D / 4), q = i % (D / 4), tile = r >> 3, w0 = (tile / MT) * KG;
-      const int at = (w0 * MT + tile % MT) * 8 + (r & 7);
-      // the row's warps: KG of each group of eight
-      const int parts = KG * kGroups;
-      float M = -INFINITY;
-      for (int k = 0; k < parts; k++) M = fmaxf(M, ml[at + (k % KG + k / KG * 8) * MT * 8].x);
+      float M = -INFINITY, S = 0.f;
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      float S = 0.f;
-      for (int k = 0; k < parts; k++) {
-        const int from = at + (k % KG + k / KG * 8) * MT * 8;
-        const float2 z = ml[from];
-        if (z.y == 0.f) continue;  // no visible key
-        const float f = ex2(z.x - M);
-        const float4 u = *reinterpret_cast<const float4*>(scratch + from * D + 4 * q);
-        S = fmaf(f, z.y, S);
-        v = make_float4(fmaf(f, u.x, v.x), fmaf(f, u.y, v.y), fmaf(f, u.z, v.z), fmaf(f, u.w, v.w));
+      for (int k = sub; k < parts; k += kSplit) {
+        const int from = ((w0 + k % KG + k / KG * 8) * MT + tile % MT) * 8 + (r & 7);
+        merge4(M, S, v, ml[from].x, ml[from].y, *reinterpret_cast<const float4*>(scratch + from * D + 4 * q));
       }
-      if (whole) {
-        write_row<D>(a, sw.b, sw.g, r, q, v, M, S);
-      } else {
-        *reinterpret_cast<float4*>(a.part_o + ((size_t)slot * a.R + r) * D + 4 * q) = v;
-        if (q == 0) a.part_ml[(size_t)slot * a.R + r] = make_float2(M, S);
+      // the prefix's parts join where the sequence's first own tile is
+      if (base > 0 && sw.n0 == 0) merge_prefix<D, kSplit>(a, sw.b, sw.g, r, q, sub, M, S, v);
+      merge_lanes<kSplit>(M, S, v);
+      if (sub == 0 && i0 + tid / kSplit < items) {
+        if (whole) {
+          write_row<D>(a, sw.b, sw.g, r, q, v, M, S);
+        } else {
+          *reinterpret_cast<float4*>(a.part_o + ((size_t)slot * a.R + r) * D + 4 * q) = v;
+          if (q == 0) a.part_ml[(size_t)slot * a.R + r] = make_float2(M, S);
+        }
       }
     }
     if (!whole) __threadfence();
@@ -528,12 +514,8 @@ __device__ bool sweep_consume(const PagedDecodeArgs& a, SegWalk sw, uint8_t* sme
     }
     if (!meet(gbar, gphase, abort)) return false;
     if (*flag) {
-      // Item i is four columns of a row; kSplit neighbouring lanes share its segments and add up
-      // by shuffles (each its own in order, then lane by lane: the same sum every time).
       __threadfence();
-      constexpr int kSplit = 8;
       const int first = 2 * c0 + (sw.s0 <= sw.start(c0) ? 0 : 1);
-      const int sub = tid % kSplit, items = a.R * (D / 4);
       for (int i0 = 0; i0 < items; i0 += kWarps * 32 / kSplit) {
         const int i = min(i0 + tid / kSplit, items - 1);
         const int r = i / (D / 4), q = i % (D / 4);
@@ -545,13 +527,7 @@ __device__ bool sweep_consume(const PagedDecodeArgs& a, SegWalk sw, uint8_t* sme
           const float4 u = __ldcg(reinterpret_cast<const float4*>(a.part_o + at * D + 4 * q));
           merge4(M, S, v, z.x, z.y, u);
         }
-#pragma unroll
-        for (int m = 1; m < kSplit; m <<= 1) {
-          const float zm = __shfl_xor_sync(0xffffffffu, M, m), zs = __shfl_xor_sync(0xffffffffu, S, m);
-          const float4 u = make_float4(__shfl_xor_sync(0xffffffffu, v.x, m), __shfl_xor_sync(0xffffffffu, v.y, m),
-                                       __shfl_xor_sync(0xffffffffu, v.z, m), __shfl_xor_sync(0xffffffffu, v.w, m));
-          merge4(M, S, v, zm, zs, u);
-        }
+        merge_lanes<kSplit>(M, S, v);
         if (sub == 0 && i0 + tid / kSplit < items) write_row<D>(a, sw.b, sw.g, r, q, v, M, S);
       }
       // flag is written again only after the next segment's first meeting
@@ -598,17 +574,16 @@ __global__ void __launch_bounds__(sweep_threads(D, MT), 1) k_paged_sweep(const _
   int before = 0;
   for (int b0 = 0; b0 < a.B; b0 += kThreads) {
     const int b = b0 + tid;
-    int own = 0, nt = 0;
+    int nt = 0;
     if (b < a.B) {
       int n = a.len[b];
       if (n > cap) {
         if (blockIdx.x == 0) record_page(a.status);
         n = cap;
       }
-      own = max(n - a.base, 0);
-      if (n < 0) own = 0;
-      len[b] = n > 0 ? n - a.base : -a.base;  // signed: rows of a sequence inside the prefix see none of its own part
-      nt = max(1, (own + C::kTK - 1) / C::kTK);
+      n = max(n, 0);
+      len[b] = n;
+      nt = max(1, (n - sweep_base(a, n) + C::kTK - 1) / C::kTK);  // one even where nothing is read: its rows are written
     }
     int x = nt;
 #pragma unroll
@@ -666,9 +641,9 @@ __global__ void __launch_bounds__(sweep_threads(D, MT), 1) k_paged_sweep(const _
     int issued = 0;
     bool ok = true;
     while (ok && sw.next()) {
-      const int own = sw.len[sw.b];
+      const int base = sweep_base(a, sw.len[sw.b]), own = sw.len[sw.b] - base;
       const int* row = a.table + (size_t)sw.b * a.max_pages;
-      const int p0 = a.base >> a.page_shift;
+      const int p0 = base >> a.page_shift;
       const int np = own > 0 ? (own + (1 << a.page_shift) - 1) >> a.page_shift : 0;  // own pages
       int win = -1, id = 0;
       for (int n = sw.n0; n < sw.n1; n++) {
@@ -728,7 +703,7 @@ __global__ void __launch_bounds__(sweep_threads(D, MT), 1) k_paged_sweep(const _
       const int qs = seg & 1;
       if (seg >= 2) ok = __all_sync(0xffffffffu, mbar_wait(q_empty + qs, ((seg >> 1) - 1) & 1, abort));
       if (!ok) break;
-      const int pos0 = sw.len[sw.b] + a.base - a.Tq;
+      const int pos0 = sw.len[sw.b] - a.Tq;
       uint8_t* q = smem + L.q + qs * a.tiles * 16 * C::kSpan;
       for (int r0 = 0; r0 < a.tiles * 8; r0 += kRows) {
         const int r = r0 + lane / kCPR;
@@ -772,9 +747,11 @@ cudaError_t launch_sweep_t(const PagedDecodeArgs& a, int nsm, cudaStream_t s) {
   while (b.stages > 2 && sweep_smem(D, b.stages, b.tiles, MT, b.B).total > kSmemMax) b.stages -= kGroups;
   const int bytes = sweep_smem(D, b.stages, b.tiles, MT, b.B).total;
   if (bytes > kSmemMax) return cudaErrorInvalidValue;
-  k_paged_clear<<<1, 256, 0, s>>>(b.done, kPagedMaxBlocks);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
+  if (b.base == 0) {  // with a shared prefix k_prefix_q has cleared them
+    k_paged_clear<<<1, 256, 0, s>>>(b.done, kPagedMaxBlocks);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
   return launch_pdl(k_paged_sweep<D, MT>, nsm < kPagedMaxBlocks ? nsm : kPagedMaxBlocks, sweep_threads(D, MT), (size_t)bytes, s, b);
 }
 

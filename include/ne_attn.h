@@ -447,7 +447,8 @@ const char* ne_attn_status_string(int status);
 #define NE_ATTN_KERNEL_QK_NORM_DW 12    /* the weight gradients' last sum */
 #define NE_ATTN_KERNEL_KV_APPEND_PAGED 13
 #define NE_ATTN_KERNEL_DECODE_PAGED 14  /* the sweep over a paged cache */
-#define NE_ATTN_NUM_KERNEL_KINDS 15
+#define NE_ATTN_KERNEL_DECODE_PREFIX 15 /* a shared prefix's queries and sweep */
+#define NE_ATTN_NUM_KERNEL_KINDS 16
 int ne_attn_profile_start(int capacity);
 int ne_attn_profile_stop(double* total_ms, long long* launches);
 int ne_attn_profile_detach(void);
