@@ -218,11 +218,21 @@ constexpr int kPagedMaxBlocks = 160;  // blocks of the sweep: bounds its partial
 // (key/value head, pair of 128-row tiles), in one line, block c's stretch [c W / blocks, ..).
 struct PrefixArgs {
   __half* q;        // [Hkv, tiles * 128, D] packed rotated queries (workspace)
-  float* part_o;    // [blocks + Hkv * pairs, 2, 128, D] unnormalised O of segment (block c, (head, pair) s) at c + s
-  float2* part_ml;  // [.., 2, 128] maximum (log2 units) and sum of the rows
+  float* part_o;    // unnormalised O of segment (block c, (head, pair) s), unit u: part prefix_part(c + s, u),
+                    // float4 prefix_quad of it
+  float2* part_ml;  // [part, 128] maximum (log2 units) and sum of the rows
+  float* o;         // [Hkv, tiles * 128, D] the segments joined, still unnormalised (workspace)
+  float2* ml;       // [Hkv, tiles * 128]
   int tiles, pairs, ntk, W, blocks;
 };
 #ifdef __CUDACC__
+__device__ __forceinline__ size_t prefix_part(int segment, int unit) { return (size_t)segment * 2 + unit; }
+// Columns 4 q .. of a row: the 32 rows of a warp lie side by side, so that the warp's stores
+// (and the loads of a sequence's neighbouring rows) are whole sectors.
+template <int D>
+__device__ __forceinline__ size_t prefix_quad(size_t part, int row, int q) {
+  return ((part * (kTile / 32) + row / 32) * (D / 4) + q) * 32 + row % 32;
+}
 // The block whose stretch tile x lies in.
 __host__ __device__ inline int prefix_owner(const PrefixArgs& p, int x) {
   return (int)(((x + 1LL) * p.blocks - 1) / p.W);

@@ -149,16 +149,20 @@ constexpr int sweep_threads(int D, int mt) { return (sweep_warps(D, mt) + 4) * 3
 constexpr int kBarBytes = 384;
 constexpr int kWholeTiles = 8;  // a (sequence, head) of at most this many tiles is never split
 
+// Buffers for the warps' parts of a finished segment, each with a finishing warp of its own.
+constexpr int sweep_bufs(int mt) { return mt < 4 ? 2 : 1; }
+
 // Shared memory behind the ring, in bytes (tiles: packed row tiles, mt: of one warp).
 struct SweepSmem {
   int q, scratch, ml, cum, len, bars, total;
 };
 __host__ __device__ constexpr SweepSmem sweep_smem(int D, int stages, int tiles, int mt, int B) {
   SweepSmem m = {};
+  const int rows = sweep_bufs(mt) * sweep_warps(D, mt) * mt * 8;
   m.q = stages * 32768;
   m.scratch = m.q + 2 * tiles * 16 * D * 2;
-  m.ml = m.scratch + sweep_warps(D, mt) * mt * 8 * D * 4;
-  m.cum = m.ml + sweep_warps(D, mt) * mt * 8 * 8;
+  m.ml = m.scratch + rows * D * 4;
+  m.cum = m.ml + rows * 8;
   m.len = m.cum + (B + 1) * 4;
   m.bars = (m.len + B * 4 + 15) / 16 * 16;
   m.total = m.bars + kBarBytes + 1024;
@@ -188,18 +192,15 @@ __device__ __forceinline__ void mma_b16(float (&d)[4], const uint32_t (&a)[4], u
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// The block's place in the work: tiles [w, end) of all, as segments.
-struct SegWalk {
-  const int *cum, *len;  // shared memory: tiles before sequence b (one head), positions of b
-  int Hkv, B;
-  int W, w, end, s_first;
-  int G;                 // blocks that take part
-  int b, g, n0, n1, nt;  // the segment: key tiles [n0, n1) of nt
-  int s0;                // the (sequence, head)'s first tile among all
-  // A block's stretch starts at c W / G, moved to the nearer end of a (sequence, head) of at
-  // most kWholeTiles tiles it would cut: joining a cut one costs about 3 us at the end,
-  // as much as five tiles, moving the boundary at most half the tiles.  Inside longer ones
-  // the boundaries stay, so owner() needs the unmoved starts only.
+// The division of the W tiles among G blocks, and one block's stretch [w, end).
+struct SweepPlan {
+  int W, G, base, rem;  // the first rem blocks have base + 1 tiles, the others base
+  int w, end;           // the block's tiles, boundaries moved as below
+  int b, g, n0;         // its first tile: sequence, head, key tile
+};
+struct Tiles {
+  const int* cum;  // shared memory: tiles before sequence b (one head)
+  int B, Hkv;
   __device__ int find(int x) const {  // last b with Hkv * cum[b] <= x
     int lo = 0, hi = B;
     while (hi - lo > 1) {
@@ -211,46 +212,54 @@ struct SegWalk {
     }
     return lo;
   }
-  __device__ int start(int c) const {
-    const int x = (int)((long long)c * W / G);
-    if (x >= W) return W;
+  // A block's stretch starts at tile x = c base + min(c, rem), moved to the nearer end of a
+  // (sequence, head) of at most kWholeTiles tiles it would cut: joining a cut one costs about
+  // 3 us at the end, as much as five tiles, moving the boundary at most half the tiles.
+  // Inside longer ones the boundaries stay, so owner() needs the unmoved starts only.
+  __device__ int start(const SweepPlan& p, int c) const {
+    const int x = c * p.base + min(c, p.rem);
+    if (x >= p.W) return p.W;
     const int i = find(x), n = cum[i + 1] - cum[i];
+    if (n > kWholeTiles) return x;
     const int off = (x - cum[i] * Hkv) % n;
-    if (n > kWholeTiles || off == 0) return x;
     return 2 * off < n ? x - off : x - off + n;
   }
-  __device__ int owner(int x) const { return (int)(((x + 1LL) * G - 1) / W); }
-  __device__ void init(int block, int grid) {
-    W = cum[B] * Hkv;
-    G = W < grid ? W : grid;
-    w = block < G ? start(block) : 0;
-    end = block < G ? start(block + 1) : 0;
-    s_first = w;
-    b = find(w < W ? w : W - 1);
-    n1 = 0;
+  // The block with tile x of a (sequence, head) that is cut.
+  __device__ int owner(const SweepPlan& p, int x) const {
+    const int big = p.rem * (p.base + 1);
+    return x < big ? x / (p.base + 1) : p.rem + (x - big) / p.base;
+  }
+};
+// Walks a block's stretch segment by segment.
+struct SegWalk {
+  const int* cum;
+  int Hkv, w, end;
+  int b, g, n0, n1, nt;  // the segment: key tiles [n0, n1) of nt
+  __device__ void init(const int* c, int hkv, const volatile SweepPlan* p) {
+    cum = c;
+    Hkv = hkv;
+    w = p->w;
+    end = p->end;
+    b = p->b;
+    g = p->g;
+    n0 = p->n0;
+    nt = -1;
   }
   __device__ bool next() {
     if (w >= end) return false;
-    while (cum[b + 1] * Hkv <= w) b++;
+    if (nt >= 0) {  // the segment before ended with its (sequence, head)
+      n0 = 0;
+      if (++g == Hkv) {
+        g = 0;
+        b++;
+      }
+    }
     nt = cum[b + 1] - cum[b];
-    const int off = w - cum[b] * Hkv;
-    g = off / nt;
-    n0 = off - g * nt;
-    s0 = w - n0;
     n1 = min(nt, n0 + (end - w));
     w += n1 - n0;
     return true;
   }
 };
-
-// All consumer warps meet (an mbarrier and not bar.sync: a warp that gave up must
-// not leave the others waiting for ever).
-__device__ __forceinline__ bool meet(uint64_t* bar, int& phase, volatile int* abort) {
-  warp_arrive(bar);
-  const bool ok = __all_sync(0xffffffffu, mbar_wait(bar, phase & 1, abort));
-  phase++;
-  return ok;
-}
 
 // Row r of (sequence b, head g), columns 4 q .. 4 q + 3: normalise and write.
 template <int D>
@@ -272,54 +281,29 @@ __device__ __forceinline__ int sweep_base(const PagedDecodeArgs& a, int len) {
   return a.base > 0 && len - a.Tq + 1 >= a.base ? a.base : 0;
 }
 
-// Adds the part (maximum z in log2 units, sum, O) to (M, S, v); a sum of 0 saw no key.
-__device__ __forceinline__ void merge4(float& M, float& S, float4& v, float z, float zs, float4 u) {
-  const float top = fmaxf(M, z);
-  const float f = S != 0.f ? ex2(M - top) : 0.f, g = zs != 0.f ? ex2(z - top) : 0.f;
-  M = top;
-  S = S * f + zs * g;
-  v.x = f == 0.f ? u.x * g : (g == 0.f ? v.x * f : fmaf(u.x, g, v.x * f));
-  v.y = f == 0.f ? u.y * g : (g == 0.f ? v.y * f : fmaf(u.y, g, v.y * f));
-  v.z = f == 0.f ? u.z * g : (g == 0.f ? v.z * f : fmaf(u.z, g, v.z * f));
-  v.w = f == 0.f ? u.w * g : (g == 0.f ? v.w * f : fmaf(u.w, g, v.w * f));
-}
-
-// Adds the shared prefix's parts of row r of (sequence b, head g), columns 4 q ..; the kSplit
-// neighbouring lanes of a row share them out (every lane of the warp calls this).
-template <int D, int kSplit>
-__device__ __forceinline__ void merge_prefix(const PagedDecodeArgs& a, int b, int g, int r, int q, int sub, float& M,
-                                             float& S, float4& v) {
-  const PrefixArgs& p = a.pre;
-  const int rho = b * a.R + r, tile = rho / kTile, s = g * p.pairs + (tile >> 1);
-  const int lo = prefix_owner(p, s * p.ntk), hi = prefix_owner(p, s * p.ntk + p.ntk - 1);
-  const size_t row = (size_t)(tile & 1) * kTile + (rho & (kTile - 1));
-  for (int c = lo + sub; c <= hi; c += kSplit) {
-    const size_t at = (size_t)(c + s) * 2 * kTile + row;
-    const float2 z = __ldcg(&p.part_ml[at]);
-    const float4 u = __ldcg(reinterpret_cast<const float4*>(p.part_o + at * D + 4 * q));
-    merge4(M, S, v, z.x, z.y, u);
+// A row's parts (maximum z in log2 units, sum, O), some lanes each with a few: the maximum of
+// all, then sums of the rescaled parts.  A part with sum 0 saw no key and its O is not looked at.
+struct RowSum {
+  float M = -INFINITY, S = 0.f;
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  __device__ void add(float top, float2 z, const float4& u) {
+    if (z.y == 0.f) return;
+    const float f = ex2(z.x - top);
+    S = fmaf(f, z.y, S);
+    v = make_float4(fmaf(f, u.x, v.x), fmaf(f, u.y, v.y), fmaf(f, u.z, v.z), fmaf(f, u.w, v.w));
   }
-}
+};
 
-// Sums the parts of kSplit neighbouring lanes, the same way every time.
-template <int kSplit>
-__device__ __forceinline__ void merge_lanes(float& M, float& S, float4& v) {
-#pragma unroll
-  for (int m = 1; m < kSplit; m <<= 1) {
-    const float zm = __shfl_xor_sync(0xffffffffu, M, m), zs = __shfl_xor_sync(0xffffffffu, S, m);
-    const float4 u = make_float4(__shfl_xor_sync(0xffffffffu, v.x, m), __shfl_xor_sync(0xffffffffu, v.y, m),
-                                 __shfl_xor_sync(0xffffffffu, v.z, m), __shfl_xor_sync(0xffffffffu, v.w, m));
-    merge4(M, S, v, zm, zs, u);
-  }
-}
+struct SweepBars {
+  uint64_t *full, *empty, *q_full, *q_empty, *parts_full, *parts_empty, *fin;
+};
 
 template <int D, int MT>
-__device__ bool sweep_consume(const PagedDecodeArgs& a, SegWalk sw, uint8_t* smem, const SweepSmem& L, uint64_t* full,
-                              uint64_t* empty, uint64_t* q_full, uint64_t* q_empty, uint64_t* gbar, volatile int* flag,
-                              volatile int* abort, int warp, int lane) {
+__device__ bool sweep_consume(const PagedDecodeArgs& a, SegWalk sw, const int* len, uint8_t* smem, const SweepSmem& L,
+                              const SweepBars& bar, const volatile int* abort, int warp, int lane) {
   using C = Sweep<D>;
   constexpr int KS = D / 16;
-  constexpr int kWarps = sweep_warps(D, MT), kGroups = kWarps / 8;
+  constexpr int kWarps = sweep_warps(D, MT), kGroups = kWarps / 8, kBufs = sweep_bufs(MT);
   const int grp = warp >> 3;                    // takes every kGroups-th tile
   const int KG = MT < 4 ? 8 : 8 / a.MG;         // warps over a tile's keys; the rest share the row tiles out
   const int mg = (warp & 7) / KG, kg = (warp & 7) - mg * KG;
@@ -327,15 +311,12 @@ __device__ bool sweep_consume(const PagedDecodeArgs& a, SegWalk sw, uint8_t* sme
   const float sl2 = a.scale_log2;
   // this lane's ldmatrix row and chunk parity (keys, values and queries alike)
   const uint32_t lrow = lane & 15, lchk = lane >> 4;
-  float* scratch = reinterpret_cast<float*>(smem + L.scratch);
-  float2* ml = reinterpret_cast<float2*>(smem + L.ml);
-  int st = 0, ph = 0, gphase = 0, seg = 0, turn = 0;
-  bool waited = false;
+  int st = 0, ph = 0, seg = 0, turn = 0;
   for (; sw.next(); seg++) {
-    const int total = sw.len[sw.b], base = sweep_base(a, total), own = total - base;
+    const int total = len[sw.b], own = total - sweep_base(a, total);
     const int pos0 = own - a.Tq;  // row 0's position, counted from the own part's start
     const int qs = seg & 1;
-    if (!__all_sync(0xffffffffu, mbar_wait(q_full + qs, (seg >> 1) & 1, abort))) return false;
+    if (!__all_sync(0xffffffffu, mbar_wait(bar.q_full + qs, (seg >> 1) & 1, abort))) return false;
     const uint32_t qbase = smem_u32(smem + L.q) + (uint32_t)((qs * a.tiles + mg * MT) * 16) * C::kSpan;
     uint32_t qf[MT <= 2 ? MT : 1][KS][4];
     if (MT <= 2) {
@@ -344,7 +325,7 @@ __device__ bool sweep_consume(const PagedDecodeArgs& a, SegWalk sw, uint8_t* sme
 #pragma unroll
         for (int k = 0; k < KS; k++)
           ldsm4(qf[m <= 1 || MT <= 2 ? m : 0][k], qbase + m * 16 * C::kSpan + swz(lrow, 2 * k + lchk, C::kSpan));
-      warp_arrive(q_empty + qs);
+      warp_arrive(bar.q_empty + qs);
     }
     float o[MT][2 * KS][4], mx[MT], ls[MT];
     int lim[MT];  // last visible position of this lane's row, from the own part's start
@@ -369,7 +350,7 @@ __device__ bool sweep_consume(const PagedDecodeArgs& a, SegWalk sw, uint8_t* sme
         }
         continue;
       }
-      if (!__all_sync(0xffffffffu, mbar_wait(full + st, ph, abort))) return false;
+      if (!__all_sync(0xffffffffu, mbar_wait(bar.full + st, ph, abort))) return false;
       const uint32_t kb = ring + st * C::kStage, vb = kb + C::kHalf;
       for (int sl = kg; sl < C::kSlices; sl += KG) {
         const int j0 = n * C::kTK + sl * 16;
@@ -450,14 +431,18 @@ __device__ bool sweep_consume(const PagedDecodeArgs& a, SegWalk sw, uint8_t* sme
           }
         }
       }
-      warp_arrive(empty + st);
+      warp_arrive(bar.empty + st);
       if (++st == a.stages) {
         st = 0;
         ph ^= 1;
       }
     }
-    if (MT > 2) warp_arrive(q_empty + qs);
-    // the warps' parts meet in shared memory
+    if (MT > 2) warp_arrive(bar.q_empty + qs);
+    // the warps' parts go to shared memory, where a finishing warp joins them
+    const int buf = seg % kBufs, use = seg / kBufs;
+    if (use > 0 && !__all_sync(0xffffffffu, mbar_wait(bar.parts_empty + buf, (use - 1) & 1, abort))) return false;
+    float* scratch = reinterpret_cast<float*>(smem + L.scratch) + buf * kWarps * MT * 8 * D;
+    float2* ml = reinterpret_cast<float2*>(smem + L.ml) + buf * kWarps * MT * 8;
 #pragma unroll
     for (int m = 0; m < MT; m++) {
       float l = ls[m];
@@ -470,67 +455,127 @@ __device__ bool sweep_consume(const PagedDecodeArgs& a, SegWalk sw, uint8_t* sme
         *reinterpret_cast<float2*>(scratch + row * D + i * 8 + (lane & 3) * 2) =
             make_float2(o[m][i][0] + o[m][i][2], o[m][i][1] + o[m][i][3]);
     }
-    if (!meet(gbar, gphase, abort)) return false;
+    warp_arrive(bar.parts_full + buf);
+  }
+  return true;
+}
+
+// Finishing warp f: joins the consumers' parts of every kBufs-th segment (and the shared
+// prefix's part, where the sequence's own first tile is).  A whole (sequence, head) is written
+// out; a segment leaves its part in the workspace and is counted, and the block that counts
+// the last one notes it in todo[first or second segment of the block] for its consumers.
+template <int D, int MT>
+__device__ bool sweep_finish(const PagedDecodeArgs& a, SegWalk sw, const Tiles& tl, const SweepPlan& plan, const int* len,
+                             uint8_t* smem, const SweepSmem& L, const SweepBars& bar, volatile int* todo,
+                             const volatile int* abort, int f, int lane) {
+  constexpr int kWarps = sweep_warps(D, MT), kGroups = kWarps / 8, kBufs = sweep_bufs(MT);
+  const int KG = MT < 4 ? 8 : 8 / a.MG, parts = KG * kGroups;  // warps that hold a part of a row
+  const float* scratch = reinterpret_cast<const float*>(smem + L.scratch) + f * kWarps * MT * 8 * D;
+  const float2* ml = reinterpret_cast<const float2*>(smem + L.ml) + f * kWarps * MT * 8;
+  const int first = sw.w;
+  bool waited = false;
+  for (int seg = 0; sw.next(); seg++) {
+    if (seg % kBufs != f) continue;
+    if (!__all_sync(0xffffffffu, mbar_wait(bar.parts_full + f, (seg / kBufs) & 1, abort))) return false;
     if (!waited) {
-      pdl_wait();  // the workspace's counters are cleared by the kernel before
+      pdl_wait();  // the kernels before clear the workspace's counters and leave the prefix's parts
       waited = true;
     }
     const bool whole = sw.n0 == 0 && sw.n1 == sw.nt;
-    const int c0 = whole ? 0 : sw.owner(sw.s0), c1 = whole ? 0 : sw.owner(sw.s0 + sw.nt - 1);
-    const int slot = 2 * (int)blockIdx.x + (sw.s0 <= sw.s_first ? 0 : 1);
-    const int tid = warp * 32 + lane;
-    // Item i is four columns of a row; kSplit neighbouring lanes share the parts it is made of (each
-    // its own in order, then lane by lane: the same sum every time).
-    constexpr int kSplit = 8;
-    const int sub = tid % kSplit, items = a.R * (D / 4);
-    const int parts = KG * kGroups;  // warps that hold a part of the row
-    for (int i0 = 0; i0 < items; i0 += kWarps * 32 / kSplit) {
-      const int i = min(i0 + tid / kSplit, items - 1);
-      const int r = i / (D / 4), q = i % (D / 4), tile = r >> 3, w0 = (tile / MT) * KG;
-      float M = -INFINITY, S = 0.f;
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int k = sub; k < parts; k += kSplit) {
-        const int from = ((w0 + k % KG + k / KG * 8) * MT + tile % MT) * 8 + (r & 7);
-        merge4(M, S, v, ml[from].x, ml[from].y, *reinterpret_cast<const float4*>(scratch + from * D + 4 * q));
+    const int s0 = tl.cum[sw.b] * tl.Hkv + sw.g * sw.nt, slot = s0 <= first ? 0 : 1;
+    const bool pre = sw.n0 == 0 && sweep_base(a, len[sw.b]) > 0;
+    const int items = a.R * (D / 4);
+    for (int i = lane; i < items; i += 32) {
+      const int r = i / (D / 4), q = i % (D / 4), tile = r >> 3;
+      const int at0 = ((tile / MT) * KG * MT + tile % MT) * 8 + (r & 7);
+      const auto at = [&](int k) { return at0 + (k % KG + k / KG * 8) * MT * 8; };
+      float2 zp = make_float2(-INFINITY, 0.f);
+      float4 up = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (pre) {
+        const size_t row = (size_t)sw.g * a.pre.tiles * kTile + (size_t)sw.b * a.R + r;
+        zp = __ldcg(a.pre.ml + row);
+        up = __ldcg(reinterpret_cast<const float4*>(a.pre.o + row * D) + q);
       }
-      // the prefix's parts join where the sequence's first own tile is
-      if (base > 0 && sw.n0 == 0) merge_prefix<D, kSplit>(a, sw.b, sw.g, r, q, sub, M, S, v);
-      merge_lanes<kSplit>(M, S, v);
-      if (sub == 0 && i0 + tid / kSplit < items) {
-        if (whole) {
-          write_row<D>(a, sw.b, sw.g, r, q, v, M, S);
-        } else {
-          *reinterpret_cast<float4*>(a.part_o + ((size_t)slot * a.R + r) * D + 4 * q) = v;
-          if (q == 0) a.part_ml[(size_t)slot * a.R + r] = make_float2(M, S);
-        }
+      RowSum x;
+      x.M = zp.x;
+#pragma unroll 4
+      for (int k = 0; k < parts; k++) x.M = fmaxf(x.M, ml[at(k)].x);
+      x.add(x.M, zp, up);
+#pragma unroll 4
+      for (int k = 0; k < parts; k++) x.add(x.M, ml[at(k)], *reinterpret_cast<const float4*>(scratch + at(k) * D + 4 * q));
+      if (whole) {
+        write_row<D>(a, sw.b, sw.g, r, q, x.v, x.M, x.S);
+      } else {
+        const size_t at1 = (size_t)(2 * blockIdx.x + slot) * a.R + r;
+        *reinterpret_cast<float4*>(a.part_o + at1 * D + 4 * q) = x.v;
+        if (q == 0) a.part_ml[at1] = make_float2(x.M, x.S);
       }
     }
-    if (!whole) __threadfence();
-    if (!meet(gbar, gphase, abort)) return false;
+    warp_arrive(bar.parts_empty + f);
     if (whole) continue;
-    if (tid == 0) {
-      *flag = atomicAdd(a.done + c0, 1u) == (unsigned)(c1 - c0) ? 1 : 0;
+    __threadfence();
+    __syncwarp();
+    if (lane == 0) {
+      const int c0 = tl.owner(plan, s0), c1 = tl.owner(plan, s0 + sw.nt - 1);
+      if (atomicAdd(a.done + c0, 1u) == (unsigned)(c1 - c0)) todo[slot] = sw.b * tl.Hkv + sw.g;
       __threadfence();
     }
-    if (!meet(gbar, gphase, abort)) return false;
-    if (*flag) {
-      __threadfence();
-      const int first = 2 * c0 + (sw.s0 <= sw.start(c0) ? 0 : 1);
-      for (int i0 = 0; i0 < items; i0 += kWarps * 32 / kSplit) {
-        const int i = min(i0 + tid / kSplit, items - 1);
-        const int r = i / (D / 4), q = i % (D / 4);
-        float M = -INFINITY, S = 0.f;
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int c = c0 + sub; c <= c1; c += kSplit) {
-          const size_t at = (size_t)(c == c0 ? first : 2 * c) * a.R + r;
-          const float2 z = __ldcg(&a.part_ml[at]);
-          const float4 u = __ldcg(reinterpret_cast<const float4*>(a.part_o + at * D + 4 * q));
-          merge4(M, S, v, z.x, z.y, u);
+    __syncwarp();
+  }
+  warp_arrive(bar.fin);
+  return true;
+}
+
+// The (sequence, head)s whose last segment this block counted: their segments in order, kSplit
+// neighbouring lanes to four columns of a row (each its own share, then lane by lane: the same
+// sum whichever block does it).
+template <int D, int MT>
+__device__ bool sweep_join(const PagedDecodeArgs& a, const Tiles& tl, const SweepPlan& plan, const SweepBars& bar,
+                           const volatile int* todo, const volatile int* abort, int tid) {
+  constexpr int kThreads = sweep_warps(D, MT) * 32, kSplit = 8, kAhead = 4;
+  if (!__all_sync(0xffffffffu, mbar_wait(bar.fin, 0, abort))) return false;
+  for (int k = 0; k < 2; k++) {
+    const int sh = todo[k];
+    if (sh < 0) continue;
+    __threadfence();
+    const int b = sh / tl.Hkv, g = sh - b * tl.Hkv, nt = tl.cum[b + 1] - tl.cum[b];
+    const int s0 = tl.cum[b] * tl.Hkv + g * nt;
+    const int c0 = tl.owner(plan, s0), c1 = tl.owner(plan, s0 + nt - 1);
+    const int first = 2 * c0 + (s0 <= tl.start(plan, c0) ? 0 : 1);
+    const int sub = tid % kSplit, items = a.R * (D / 4);
+    for (int i0 = 0; i0 < items; i0 += kThreads / kSplit) {
+      const int i = min(i0 + tid / kSplit, items - 1);
+      const int r = i / (D / 4), q = i % (D / 4);
+      const auto at = [&](int c) { return (size_t)(c == c0 ? first : 2 * c) * a.R + r; };
+      float top = -INFINITY;
+      for (int c = c0 + sub; c <= c1; c += kSplit) top = fmaxf(top, __ldcg(a.part_ml + at(c)).x);
+#pragma unroll
+      for (int m = 1; m < kSplit; m <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
+      RowSum x;
+      for (int c = c0 + sub; c <= c1; c += kSplit * kAhead) {
+        float2 z[kAhead];
+        float4 u[kAhead];
+#pragma unroll
+        for (int e = 0; e < kAhead; e++) {
+          z[e] = make_float2(-INFINITY, 0.f);
+          u[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (c + e * kSplit <= c1) {
+            z[e] = __ldcg(a.part_ml + at(c + e * kSplit));
+            u[e] = __ldcg(reinterpret_cast<const float4*>(a.part_o + at(c + e * kSplit) * D) + q);
+          }
         }
-        merge_lanes<kSplit>(M, S, v);
-        if (sub == 0 && i0 + tid / kSplit < items) write_row<D>(a, sw.b, sw.g, r, q, v, M, S);
+#pragma unroll
+        for (int e = 0; e < kAhead; e++) x.add(top, z[e], u[e]);
       }
-      // flag is written again only after the next segment's first meeting
+#pragma unroll
+      for (int m = 1; m < kSplit; m <<= 1) {
+        x.S += __shfl_xor_sync(0xffffffffu, x.S, m);
+        x.v.x += __shfl_xor_sync(0xffffffffu, x.v.x, m);
+        x.v.y += __shfl_xor_sync(0xffffffffu, x.v.y, m);
+        x.v.z += __shfl_xor_sync(0xffffffffu, x.v.z, m);
+        x.v.w += __shfl_xor_sync(0xffffffffu, x.v.w, m);
+      }
+      if (sub == 0 && i0 + tid / kSplit < items) write_row<D>(a, b, g, r, q, x.v, top, x.S);
     }
   }
   return true;
@@ -539,37 +584,48 @@ __device__ bool sweep_consume(const PagedDecodeArgs& a, SegWalk sw, uint8_t* sme
 template <int D, int MT>
 __global__ void __launch_bounds__(sweep_threads(D, MT), 1) k_paged_sweep(const __grid_constant__ PagedDecodeArgs a) {
   using C = Sweep<D>;
-  constexpr int kWarps = sweep_warps(D, MT), kThreads = sweep_threads(D, MT);
+  constexpr int kWarps = sweep_warps(D, MT), kThreads = sweep_threads(D, MT), kBufs = sweep_bufs(MT);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   const SweepSmem L = sweep_smem(D, a.stages, a.tiles, MT, a.B);
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L.bars);
-  uint64_t* empty = full + C::kMaxStages;
-  uint64_t* q_full = empty + C::kMaxStages;  // [2]
-  uint64_t* q_empty = q_full + 2;            // [2]
-  uint64_t* gbar = q_empty + 2;
-  volatile int* abort = reinterpret_cast<volatile int*>(gbar + 1);
-  volatile int* flag = abort + 1;
-  int* wsum = const_cast<int*>(abort) + 2;   // [20] the scan's warp totals
+  SweepBars bar;
+  bar.full = reinterpret_cast<uint64_t*>(smem + L.bars);
+  bar.empty = bar.full + C::kMaxStages;
+  bar.q_full = bar.empty + C::kMaxStages;   // [2]
+  bar.q_empty = bar.q_full + 2;             // [2]
+  bar.parts_full = bar.q_empty + 2;         // [2] a segment's parts are in shared memory
+  bar.parts_empty = bar.parts_full + 2;     // [2] and have been read
+  bar.fin = bar.parts_empty + 2;            // the finishing warps are done
+  volatile int* abort = reinterpret_cast<volatile int*>(bar.fin + 1);
+  volatile int* todo = abort + 1;                              // [2]
+  volatile SweepPlan* splan = reinterpret_cast<volatile SweepPlan*>(const_cast<int*>(abort) + 3);
+  int* wsum = const_cast<int*>(abort) + 12;                    // [20] the scan's warp totals
   int* cum = reinterpret_cast<int*>(smem + L.cum);
   int* len = reinterpret_cast<int*>(smem + L.len);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     *abort = 0;
+    todo[0] = todo[1] = -1;
     for (int i = 0; i < a.stages; i++) {
-      mbar_init(full + i, 1);
-      mbar_init(empty + i, 8);
+      mbar_init(bar.full + i, 1);
+      mbar_init(bar.empty + i, 8);
     }
     for (int i = 0; i < 2; i++) {
-      mbar_init(q_full + i, 1);
-      mbar_init(q_empty + i, kWarps);
+      mbar_init(bar.q_full + i, 1);
+      mbar_init(bar.q_empty + i, kWarps);
+      mbar_init(bar.parts_full + i, kWarps);
+      mbar_init(bar.parts_empty + i, 1);
     }
-    mbar_init(gbar, kWarps);
+    mbar_init(bar.fin, kBufs);
     fence_mbar_init();
     cum[0] = 0;
   }
-  // lengths of the own parts and the running count of their tiles
+  if (warp == kWarps && lane == 0) {
+    prefetch_tmap(&a.map_k);
+    prefetch_tmap(&a.map_v);
+  }
+  // lengths, and the running count of the tiles of the parts read here
   const int cap = a.max_pages << a.page_shift;
   int before = 0;
   for (int b0 = 0; b0 < a.B; b0 += kThreads) {
@@ -586,28 +642,61 @@ __global__ void __launch_bounds__(sweep_threads(D, MT), 1) k_paged_sweep(const _
       nt = max(1, (n - sweep_base(a, n) + C::kTK - 1) / C::kTK);  // one even where nothing is read: its rows are written
     }
     int x = nt;
+    if (b0 + warp * 32 < a.B) {
 #pragma unroll
-    for (int m = 1; m < 32; m <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, x, m);
-      if (lane >= m) x += y;
+      for (int m = 1; m < 32; m <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, m);
+        if (lane >= m) x += y;
+      }
     }
     if (lane == 31) wsum[warp] = x;
     __syncthreads();
-    int all = 0;
-    for (int i = 0; i < kThreads / 32; i++) {
-      if (i < warp) x += wsum[i];
-      all += wsum[i];
+    if (b0 + warp * 32 < a.B) {
+      int low = lane < warp ? wsum[lane] : 0;  // at most 20 warps
+#pragma unroll
+      for (int m = 16; m; m >>= 1) low += __shfl_xor_sync(0xffffffffu, low, m);
+      if (b < a.B) cum[b + 1] = before + low + x;
     }
-    if (b < a.B) cum[b + 1] = before + x;
-    before += all;
-    __syncthreads();
+    if (b0 + kThreads < a.B) {
+      for (int i = 0; i < kThreads / 32; i++) before += wsum[i];
+      __syncthreads();
+    }
   }
+  __syncthreads();
+  Tiles tl;
+  tl.cum = cum;
+  tl.B = a.B;
+  tl.Hkv = a.Hkv;
+  // one warp divides the work (a division costs every warp its issue slots)
+  if (warp == 0) {
+    SweepPlan p;
+    p.W = cum[a.B] * a.Hkv;
+    p.G = min(p.W, (int)gridDim.x);
+    p.base = p.W / p.G;
+    p.rem = p.W - p.base * p.G;
+    const int c = (int)blockIdx.x + (lane & 1);
+    const int x = c <= p.G ? tl.start(p, min(c, p.G)) : p.W;
+    p.w = __shfl_sync(0xffffffffu, x, 0);
+    p.end = __shfl_sync(0xffffffffu, x, 1);
+    if (lane == 0) {
+      p.b = tl.find(min(p.w, p.W - 1));
+      const int nt = cum[p.b + 1] - cum[p.b], off = p.w - cum[p.b] * a.Hkv;
+      p.g = off / nt;
+      p.n0 = off - p.g * nt;
+      splan->W = p.W;
+      splan->G = p.G;
+      splan->base = p.base;
+      splan->rem = p.rem;
+      splan->w = p.w;
+      splan->end = p.end;
+      splan->b = p.b;
+      splan->g = p.g;
+      splan->n0 = p.n0;
+    }
+  }
+  __syncthreads();
   SegWalk sw;
-  sw.cum = cum;
-  sw.len = len;
-  sw.Hkv = a.Hkv;
-  sw.B = a.B;
-  sw.init(blockIdx.x, gridDim.x);
+  sw.init(cum, a.Hkv, splan);
   const volatile int never = 0;
   // Registers at launch, and what the consumers and the others then hold: 640 x 96 = 512 x 104 +
   // 128 x 64, or 384 x 168 = 256 x 216 + 128 x 72.
@@ -616,7 +705,14 @@ __global__ void __launch_bounds__(sweep_threads(D, MT), 1) k_paged_sweep(const _
       regs_inc<104>();
     else
       regs_inc<216>();
-    const bool ok = sweep_consume<D, MT>(a, sw, smem, L, full, empty, q_full, q_empty, gbar, flag, abort, warp, lane);
+    bool ok = sweep_consume<D, MT>(a, sw, len, smem, L, bar, abort, warp, lane);
+    if (ok) {
+      SweepPlan p;
+      p.W = splan->W;
+      p.base = splan->base;
+      p.rem = splan->rem;
+      ok = sweep_join<D, MT>(a, tl, p, bar, todo, abort, tid);
+    }
     if (!ok && lane == 0) {
       *abort = 1;
       atomicCAS(a.status, 0, kStatusTimeout);
@@ -627,21 +723,17 @@ __global__ void __launch_bounds__(sweep_threads(D, MT), 1) k_paged_sweep(const _
     regs_dec<64>();
   else
     regs_dec<72>();
+  bool ok = true;
   if (warp == kWarps) {
     // ------------------------------------------------------------ keys and values
     // Lane i loads page i of a tile; the page numbers come 32 at a time.
     const int prows = min(1 << a.page_shift, C::kTK), per = C::kTK / prows;
     const uint32_t pbytes = (uint32_t)prows * C::kSpan;
     const int shared = a.prefix_len >> a.page_shift;
-    if (lane == 0) {
-      prefetch_tmap(&a.map_k);
-      prefetch_tmap(&a.map_v);
-    }
     int st = 0, ph = 1;  // the first round finds every stage empty
     int issued = 0;
-    bool ok = true;
     while (ok && sw.next()) {
-      const int base = sweep_base(a, sw.len[sw.b]), own = sw.len[sw.b] - base;
+      const int base = sweep_base(a, len[sw.b]), own = len[sw.b] - base;
       const int* row = a.table + (size_t)sw.b * a.max_pages;
       const int p0 = base >> a.page_shift;
       const int np = own > 0 ? (own + (1 << a.page_shift) - 1) >> a.page_shift : 0;  // own pages
@@ -662,20 +754,20 @@ __global__ void __launch_bounds__(sweep_threads(D, MT), 1) k_paged_sweep(const _
           }
         }
         const int mine = __shfl_sync(0xffffffffu, id, (first & 31) + (lane < per ? lane : 0));
-        ok = __all_sync(0xffffffffu, mbar_wait(empty + st, ph, abort));
+        ok = __all_sync(0xffffffffu, mbar_wait(bar.empty + st, ph, abort));
         if (!ok) break;
         if (lane == 0) {
           if (have > 0)
-            mbar_arrive_expect_tx(full + st, 2u * have * pbytes);
+            mbar_arrive_expect_tx(bar.full + st, 2u * have * pbytes);
           else
-            mbar_arrive(full + st);
+            mbar_arrive(bar.full + st);
         }
         __syncwarp();
         if (lane < have) {
           const int off = (n * C::kTK) & ((1 << a.page_shift) - 1);  // a tile inside a larger page
           uint8_t* dst = smem + st * C::kStage + lane * pbytes;
-          tma_load_4d(dst, &a.map_k, full + st, 0, off, sw.g, mine);
-          tma_load_4d(dst + C::kHalf, &a.map_v, full + st, 0, off, sw.g, mine);
+          tma_load_4d(dst, &a.map_k, bar.full + st, 0, off, sw.g, mine);
+          tma_load_4d(dst + C::kHalf, &a.map_v, bar.full + st, 0, off, sw.g, mine);
         }
         issued++;
         if (++st == a.stages) {
@@ -684,41 +776,49 @@ __global__ void __launch_bounds__(sweep_threads(D, MT), 1) k_paged_sweep(const _
         }
       }
     }
-    if (!ok) {
-      if (lane == 0) {
-        *abort = 1;
-        atomicCAS(a.status, 0, kStatusTimeout);
-      }
-      // let every copy issued above land before the block can exit
-      if (lane == 0)
-        for (int x = max(0, issued - a.stages); x < issued; x++)
-          mbar_wait(full + x % a.stages, (x / a.stages) & 1, &never);
-    }
+    // let every copy issued above land before the block can exit
+    if (!ok && lane == 0)
+      for (int x = max(0, issued - a.stages); x < issued; x++)
+        mbar_wait(bar.full + x % a.stages, (x / a.stages) & 1, &never);
   } else if (warp == kWarps + 1) {
-    // ------------------------------------------------------------ queries
+    // ------------------------------------------------------------ queries, two passes of rows at a time
     constexpr int kCPR = D / 8, kRows = 32 / kCPR;
     const int c = lane % kCPR;
-    bool ok = true;
+    const bool norm = a.qw != nullptr;
+    uint4 wv = make_uint4(0, 0, 0, 0);
+    if (norm) wv = load_rope_chunk<D>(a.qw, c, a.rope_half != 0);
     for (int seg = 0; ok && sw.next(); seg++) {
       const int qs = seg & 1;
-      if (seg >= 2) ok = __all_sync(0xffffffffu, mbar_wait(q_empty + qs, ((seg >> 1) - 1) & 1, abort));
+      if (seg >= 2) ok = __all_sync(0xffffffffu, mbar_wait(bar.q_empty + qs, ((seg >> 1) - 1) & 1, abort));
       if (!ok) break;
-      const int pos0 = sw.len[sw.b] - a.Tq;
+      const int pos0 = len[sw.b] - a.Tq;
       uint8_t* q = smem + L.q + qs * a.tiles * 16 * C::kSpan;
-      for (int r0 = 0; r0 < a.tiles * 8; r0 += kRows) {
-        const int r = r0 + lane / kCPR;
+      for (int r0 = 0; r0 < a.tiles * 8; r0 += 2 * kRows) {
+        const int r = r0 + lane / kCPR, r2 = r + kRows;
+        const QueryChunk x = query_load<D>(a, sw.b, sw.g, r, c, pos0), y = query_load<D>(a, sw.b, sw.g, r2, c, pos0);
         uint4 hi, lo;
-        query_chunk<D>(a, sw.b, sw.g, r, c, pos0, hi, lo);
-        uint8_t* tile = q + (r >> 3) * 16 * C::kSpan;
-        *reinterpret_cast<uint4*>(tile + swz(r & 7, c, C::kSpan)) = hi;
-        *reinterpret_cast<uint4*>(tile + swz((r & 7) + 8, c, C::kSpan)) = lo;
+        query_finish<D>(a, x, norm, wv, hi, lo);
+        *reinterpret_cast<uint4*>(q + (r >> 3) * 16 * C::kSpan + swz(r & 7, c, C::kSpan)) = hi;
+        *reinterpret_cast<uint4*>(q + (r >> 3) * 16 * C::kSpan + swz((r & 7) + 8, c, C::kSpan)) = lo;
+        query_finish<D>(a, y, norm, wv, hi, lo);
+        if (r2 < a.tiles * 8) {
+          *reinterpret_cast<uint4*>(q + (r2 >> 3) * 16 * C::kSpan + swz(r2 & 7, c, C::kSpan)) = hi;
+          *reinterpret_cast<uint4*>(q + (r2 >> 3) * 16 * C::kSpan + swz((r2 & 7) + 8, c, C::kSpan)) = lo;
+        }
       }
-      warp_arrive(q_full + qs);
+      warp_arrive(bar.q_full + qs);
     }
-    if (!ok && lane == 0) {
-      *abort = 1;
-      atomicCAS(a.status, 0, kStatusTimeout);
-    }
+  } else if (warp - kWarps - 2 < kBufs) {
+    // ------------------------------------------------------------ finished segments
+    SweepPlan p;
+    p.W = splan->W;
+    p.base = splan->base;
+    p.rem = splan->rem;
+    ok = sweep_finish<D, MT>(a, sw, tl, p, len, smem, L, bar, todo, abort, warp - kWarps - 2, lane);
+  }
+  if (!ok && lane == 0) {
+    *abort = 1;
+    atomicCAS(a.status, 0, kStatusTimeout);
   }
 }
 

@@ -11,8 +11,8 @@
 //               prefix, laid end to end over (head, pair of row tiles) and cut into one
 //               equal stretch per block; each segment leaves its unnormalised O and its
 //               rows' maximum and sum
-// The sweep over the sequences' own pages (paged.cu) joins these parts with its own:
-//   O = sum_s 2^(m_s - m) O_s / sum_s 2^(m_s - m) l_s.
+//   k_prefix_join  the segments of every row: O = sum_s 2^(m_s - m) O_s, l likewise
+// The sweep over the sequences' own pages (paged.cu) takes the joined part in with its own.
 //
 // A sequence takes part if its first query sees the whole prefix, so no score is
 // masked here but for the columns behind the prefix in its last tile; the sweep
@@ -48,8 +48,11 @@ __global__ void __launch_bounds__(128) k_prefix_q(const PagedDecodeArgs a) {
   int pos0 = 0;
   const bool in = b < a.B && it < n;
   if (in) pos0 = min(a.len[b], a.max_pages << a.page_shift) - a.Tq;
-  uint4 hi, lo;
-  query_chunk<D>(a, in ? b : 0, g, in ? r : a.R, c, pos0, hi, lo);  // row R: zeros
+  const bool norm = a.qw != nullptr;
+  uint4 wv = make_uint4(0, 0, 0, 0), hi, lo;
+  if (norm) wv = load_rope_chunk<D>(a.qw, c, a.rope_half != 0);
+  const QueryChunk x = query_load<D>(a, in ? b : 0, g, in ? r : a.R, c, pos0);  // row R: zeros
+  query_finish<D>(a, x, norm, wv, hi, lo);
   if (it < n) reinterpret_cast<uint4*>(a.pre.q)[it] = hi;
 }
 
@@ -418,21 +421,21 @@ __global__ void __launch_bounds__(384, 1) k_prefix(const __grid_constant__ Paged
         pdl_wait();  // everything before in the stream is done with the workspace
         waited = true;
       }
-      const size_t row = (size_t)((blockIdx.x + sg.s) * 2 + u) * kTile + r;
+      const size_t part = prefix_part(blockIdx.x + sg.s, u);
+      float4* dst = reinterpret_cast<float4*>(p.part_o) + prefix_quad<D>(part, r, 0);
 #pragma unroll
       for (int c = 0; c < D / 32; c++) {
         uint32_t w[32];
         tmem_ld32(obuf + c * 32, w);
         tmem_wait_ld();
-        float4* dst = reinterpret_cast<float4*>(p.part_o + row * D + c * 32);
 #pragma unroll
         for (int e = 0; e < 8; e++)
-          dst[e] = make_float4(__uint_as_float(w[4 * e]), __uint_as_float(w[4 * e + 1]), __uint_as_float(w[4 * e + 2]),
-                               __uint_as_float(w[4 * e + 3]));
+          dst[(c * 8 + e) * 32] = make_float4(__uint_as_float(w[4 * e]), __uint_as_float(w[4 * e + 1]),
+                                              __uint_as_float(w[4 * e + 2]), __uint_as_float(w[4 * e + 3]));
       }
       tc_fence_before();
       warp_arrive(o_free + u);
-      p.part_ml[row] = make_float2(m_use, l_run);
+      p.part_ml[part * kTile + r] = make_float2(m_use, l_run);
     }
     if (!ok) {
       *abort = 1;
@@ -447,6 +450,41 @@ __global__ void __launch_bounds__(384, 1) k_prefix(const __grid_constant__ Paged
     tmem_relinquish();
     tmem_dealloc(tmem, C::kTmemCols);
   }
+}
+
+// ====================================================================== the segments of a tile joined
+// A thread takes four columns of a row: the maximum over the row's segments, then the sum of
+// the rescaled parts, in order.  32 neighbouring rows of one column quad lie side by side in a
+// segment (prefix_quad); the result is row by row.
+template <int D>
+__global__ void __launch_bounds__(128) k_prefix_join(const __grid_constant__ PagedDecodeArgs a) {
+  const PrefixArgs& p = a.pre;
+  pdl_wait();
+  pdl_launch();
+  const int lane = threadIdx.x & 31;
+  const long long w = blockIdx.x * 4LL + threadIdx.x / 32;  // (head, tile, 32 rows, quad)
+  const int q = (int)(w % (D / 4)), r32 = (int)(w / (D / 4) % (kTile / 32));
+  const long long gt = w / (D / 4) / (kTile / 32);
+  const int g = (int)(gt / p.tiles), tile = (int)(gt - (long long)g * p.tiles);
+  if (g >= a.Hkv) return;
+  const int row = r32 * 32 + lane, s = g * p.pairs + (tile >> 1), u = tile & 1;
+  const int lo = prefix_owner(p, s * p.ntk), hi = prefix_owner(p, s * p.ntk + p.ntk - 1);
+  float top = -INFINITY;
+  for (int c = lo; c <= hi; c++) top = fmaxf(top, __ldcg(p.part_ml + prefix_part(c + s, u) * kTile + row).x);
+  float S = 0.f;
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+  for (int c = lo; c <= hi; c++) {
+    const size_t part = prefix_part(c + s, u);
+    const float2 z = __ldcg(p.part_ml + part * kTile + row);
+    const float4 x = __ldcg(reinterpret_cast<const float4*>(p.part_o) + prefix_quad<D>(part, row, q));
+    const float f = ex2(z.x - top);
+    S = fmaf(f, z.y, S);
+    v = make_float4(fmaf(f, x.x, v.x), fmaf(f, x.y, v.y), fmaf(f, x.z, v.z), fmaf(f, x.w, v.w));
+  }
+  const size_t out = (size_t)gt * kTile + row;
+  reinterpret_cast<float4*>(p.o)[out * (D / 4) + q] = v;
+  if (q == 0) p.ml[out] = make_float2(top, S);
 }
 
 template <int D>
@@ -464,7 +502,10 @@ cudaError_t launch_t(const PagedDecodeArgs& a, cudaStream_t s) {
   k_prefix_q<D><<<(unsigned)((n + 127) / 128), 128, 0, s>>>(a);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  return launch_pdl(k_prefix<D>, a.pre.blocks, C::kThreads, (size_t)C::kSmemBytes, s, a);
+  e = launch_pdl(k_prefix<D>, a.pre.blocks, C::kThreads, (size_t)C::kSmemBytes, s, a);
+  if (e != cudaSuccess) return e;
+  const long long warps = (long long)a.Hkv * a.pre.tiles * (kTile / 32) * (D / 4);
+  return launch_pdl(k_prefix_join<D>, (int)((warps + 3) / 4), 128, 0, s, a);
 }
 
 }  // namespace
