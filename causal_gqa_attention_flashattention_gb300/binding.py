@@ -6,7 +6,6 @@ library has not been built, or its kernels cannot run on this device, the
 calls raise; there is no other implementation to fall back to.
 """
 import ctypes
-import functools
 import os
 
 import torch
@@ -15,6 +14,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_build", "libneattn.so")
 
 NE_OK = 0
+ERR_WORKSPACE = -5
 O_FP32 = 1       # flag bits, see include/ne_attn.h
 GRAD_FP32 = 2
 PRECISE_QK = 4
@@ -221,7 +221,7 @@ def status_of_last_kernels(stream=None):
 
 
 KERNEL_KINDS = ("fwd", "bwd_prep", "bwd_dkdv", "bwd_dq", "fwd_rope", "kv_append", "decode", "decode_aux",
-                "qkv_prep", "qkv", "qk_norm", "qk_norm_bwd", "qk_norm_dw", "kv_append_paged", "decode_paged",
+                "qkv_prep", "qkv", "qk_norm", "qk_norm_bwd", "kv_append_paged", "decode_paged",
                 "decode_prefix")
 
 
@@ -372,9 +372,10 @@ def qkv_rmsnorm(x, norm_w, w_qkv, Hq, Hkv, D, eps=1e-5, rope_base=10000.0, rotat
 def rotated_qk(workspace, B, T, Hq, Hkv, D):
     """Views of the rotated fp16 q [B,T,Hq,D] and k [B,T,Hkv,D] at the start of a
     forward / backward / projection workspace (NE_ATTN_QK_ROTATED layout)."""
-    n, nk = B * T * Hq * D, B * T * Hkv * D
-    at = (n + 127) // 128 * 128  # each array starts on 256 bytes
-    w = workspace[:2 * (at + nk)].view(torch.float16)
+    at = (B * T * Hq * D + 127) // 128 * 128  # each array starts on 256 bytes
+    if workspace.numel() % 2:
+        workspace = workspace[:-1]
+    w = workspace.view(torch.float16)
     first = w.storage_offset()
     return (w.as_strided((B, T, Hq, D), (T * Hq * D, Hq * D, D, 1), first),
             w.as_strided((B, T, Hkv, D), (T * Hkv * D, Hkv * D, D, 1), first + at))
@@ -435,6 +436,22 @@ def _int32(t, name, device, shape):
         raise ValueError("%s must be a contiguous int32 %s on the call's device" % (name, list(shape)))
 
 
+def _with_workspace(call, workspace, made, device, size):
+    """call(pointer, bytes) with the caller's workspace; without one with NULL (the library's
+    own for the stream) or, where a capture needs one, a tensor of the capture's own."""
+    if workspace is not None:
+        _need(workspace.dtype == torch.uint8 and workspace.device == device, "workspace must be uint8 on the call's device")
+        return call(workspace.data_ptr(), workspace.numel())
+    try:
+        return call(None, 0)
+    except NeAttnError as e:
+        if e.status != ERR_WORKSPACE:
+            raise
+    workspace = torch.empty(size(), dtype=torch.uint8, device=device)
+    made.append(workspace)
+    return call(workspace.data_ptr(), workspace.numel())
+
+
 def qk_norm(q, k, q_weight, k_weight, eps=1e-6, rope_base=10000.0, rope_half=False, workspace=None, stream=None):
     """RMS norm of every head of q [B,T,Hq,D] and k [B,T,Hkv,D] (bf16) with weights
     [D], then the rotary embedding, in one pass (ne_attn_qk_norm).
@@ -487,20 +504,18 @@ def qk_norm_bwd(q, k, q_weight, k_weight, dqn, dkn, eps=1e-6, dq=None, dk=None, 
         made.append(dk)
     _need(dq.shape == q.shape and dk.shape == k.shape, "dq and dk must have the shapes of q and k")
     dqs, dks = _head_rows(dq, "dq", dt, dev), _head_rows(dk, "dk", dt, dev)
-    dw = torch.empty((2, D), dtype=torch.float32, device=dev)
-    made.append(dw)
-    if workspace is None:
-        n = int(lib().ne_attn_qk_norm_bwd_workspace_size(B, T, Hq, Hkv, D))
-        _need(n > 0, "unsupported shape")
-        workspace = torch.empty(n, dtype=torch.uint8, device=dev)
-        made.append(workspace)
-    _need(workspace.dtype == torch.uint8 and workspace.device == dev, "workspace must be uint8 on the call's device")
-    p = dw.data_ptr()
-    _run("ne_attn_qk_norm_bwd", dev, stream, made, q.data_ptr(), k.data_ptr(), q_weight.data_ptr(),
-         k_weight.data_ptr(), dqn.data_ptr(), dkn.data_ptr(), dq.data_ptr(), dk.data_ptr(), p, p + 4 * D,
-         B, T, Hq, Hkv, D, qs, ks, dqs, dks, eps, GRAD_FP32 if dt == torch.float32 else 0, workspace.data_ptr(),
-         workspace.numel())
-    return dq, dk, dw[0], dw[1]
+    dqw = torch.empty(D, dtype=torch.float32, device=dev)
+    dkw = torch.empty(D, dtype=torch.float32, device=dev)
+    made += (dqw, dkw)
+    flags = GRAD_FP32 if dt == torch.float32 else 0
+
+    def call(ws, size):
+        _run("ne_attn_qk_norm_bwd", dev, stream, made, q.data_ptr(), k.data_ptr(), q_weight.data_ptr(),
+             k_weight.data_ptr(), dqn.data_ptr(), dkn.data_ptr(), dq.data_ptr(), dk.data_ptr(), dqw.data_ptr(),
+             dkw.data_ptr(), B, T, Hq, Hkv, D, qs, ks, dqs, dks, eps, flags, ws, size)
+
+    _with_workspace(call, workspace, made, dev, lambda: int(lib().ne_attn_qk_norm_bwd_workspace_size(B, T, Hq, Hkv, D)))
+    return dq, dk, dqw, dkw
 
 
 def paged_cache(num_pages, page_size, Hkv, D, device):
@@ -551,7 +566,6 @@ def kv_append_paged(k_new, v_new, k_pages, v_pages, page_table, pos0, cu_new=Non
          page, P, width, stride, ks, vs, eps, rope_base, ROPE_HALF if rope_half else 0)
 
 
-@functools.lru_cache(maxsize=256)
 def decode_paged_workspace_size(B, Tq, Hq, Hkv, D, prefix_len=0):
     return int(lib().ne_attn_decode_paged_workspace_size(B, Tq, Hq, Hkv, D, prefix_len))
 
@@ -590,16 +604,15 @@ def attn_decode_paged(q, k_pages, v_pages, page_table, kv_len, q_weight=None, ep
           and o.shape == (B, Tq, Hq, D), "o must be a contiguous bfloat16 or float32 [B, Tq, Hq, D]")
     _need(lse.dtype == torch.float32 and lse.device == dev and lse.is_contiguous() and lse.shape == (B, Hq, Tq),
           "lse must be a contiguous float32 [B, Hq, Tq]")
-    if workspace is None:
-        n = decode_paged_workspace_size(B, Tq, Hq, Hkv, D, prefix_len)
-        workspace = torch.empty(max(n, 1), dtype=torch.uint8, device=dev)
-        made.append(workspace)
-    _need(workspace.dtype == torch.uint8 and workspace.device == dev, "workspace must be uint8 on the call's device")
     flags = (O_FP32 if o.dtype == torch.float32 else 0) | (ROPE_HALF if rope_half else 0)
-    _run("ne_attn_decode_paged", dev, stream, made, q.data_ptr(), _optr(q_weight), k_pages.data_ptr(),
-         v_pages.data_ptr(), page_table.data_ptr(), kv_len.data_ptr(), _optr(prefix_table) if prefix_len else None,
-         o.data_ptr(), lse.data_ptr(), B, Tq, Hq, Hkv, D, page, P, width, stride, qs, prefix_len, eps, rope_base,
-         flags, workspace.data_ptr(), workspace.numel())
+    ptable = prefix_table.data_ptr() if prefix_len else None
+
+    def call(ws, size):
+        _run("ne_attn_decode_paged", dev, stream, made, q.data_ptr(), _optr(q_weight), k_pages.data_ptr(),
+             v_pages.data_ptr(), page_table.data_ptr(), kv_len.data_ptr(), ptable, o.data_ptr(), lse.data_ptr(),
+             B, Tq, Hq, Hkv, D, page, P, width, stride, qs, prefix_len, eps, rope_base, flags, ws, size)
+
+    _with_workspace(call, workspace, made, dev, lambda: decode_paged_workspace_size(B, Tq, Hq, Hkv, D, prefix_len))
     return o, lse
 
 

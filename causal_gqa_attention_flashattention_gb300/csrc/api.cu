@@ -99,6 +99,17 @@ struct FwdScratch {
   size_t bytes;
 };
 
+// Library-owned workspace and counters of one stream, for the calls that join partial results
+// (ne_attn_decode_paged, ne_attn_qk_norm_bwd) and are given no workspace.  The counters are 0
+// between calls.  Keyed by the stream's id, which unlike its handle is never used again.
+struct JoinScratch {
+  unsigned long long stream;
+  unsigned* counters;
+  void* ptr;
+  size_t bytes;
+};
+constexpr size_t kCounterBytes = 1024;
+
 struct DeviceState {
   bool init = false;
   bool supported = false;
@@ -106,6 +117,7 @@ struct DeviceState {
   std::vector<RopeTable> tables;
   std::vector<FwdSchedule> scheds;
   std::vector<FwdScratch> fwd_scratch;
+  std::vector<JoinScratch> join_scratch;
   unsigned char* static_scratch = nullptr;  // device address of g_static_scratch (set on first use)
 };
 
@@ -294,6 +306,45 @@ int fwd_scratch(DeviceState& d, cudaStream_t s, size_t need, void** out) {
   return NE_OK;
 }
 
+// The same for JoinScratch.  Requires g_mu held.
+int join_scratch(DeviceState& d, cudaStream_t s, size_t need, void** ws, unsigned** counters) {
+  cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(s, &cs) != cudaSuccess) return NE_ERR_CUDA;
+  // a graph may run on any stream: it needs a workspace of its own
+  if (cs != cudaStreamCaptureStatusNone) return NE_ERR_WORKSPACE;
+  unsigned long long id = 0;
+  if (cudaStreamGetId(s, &id) != cudaSuccess) return NE_ERR_CUDA;
+  JoinScratch* f = nullptr;
+  for (auto& x : d.join_scratch)
+    if (x.stream == id) f = &x;
+  if (!f) {
+    JoinScratch x = {id, nullptr, nullptr, 0};
+    if (cudaMalloc(&x.counters, kCounterBytes) != cudaSuccess) return NE_ERR_CUDA;
+    if (cudaMemsetAsync(x.counters, 0, kCounterBytes, s) != cudaSuccess) {
+      cudaFree(x.counters);
+      return NE_ERR_CUDA;
+    }
+    d.join_scratch.push_back(x);
+    f = &d.join_scratch.back();
+  }
+  if (f->bytes < need) {
+    if (f->ptr) {
+      // cudaFree waits for the device to finish the work that may still read it
+      if (cudaFree(f->ptr) != cudaSuccess) return NE_ERR_CUDA;
+      f->ptr = nullptr;
+      f->bytes = 0;
+    }
+    if (cudaMalloc(&f->ptr, need) != cudaSuccess) {
+      f->ptr = nullptr;
+      return NE_ERR_CUDA;
+    }
+    f->bytes = need;
+  }
+  *ws = f->ptr;
+  *counters = f->counters;
+  return NE_OK;
+}
+
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // 4-D map over a [B, T, H, D] bf16 tensor; box = one head, 128 rows, all D.
@@ -473,10 +524,16 @@ int log2_of(int v) {
 }
 
 // Weight-gradient partials [blocks, 2 D] of the query/key norms' backward, for the most blocks it launches.
-size_t qk_norm_bwd_ws_bytes(int D) { return ws_up(sizeof(float) * 2 * D * kQkNormMaxSms * kQkNormBlocksPerSm); }
+// Then the counters (256 bytes).
+constexpr int kQkNormMaxBlocks = kQkNormMaxSms * kQkNormBlocksPerSm;
+constexpr int kQkNormMaxGroups = (kQkNormMaxBlocks + kQkNormGroup - 1) / kQkNormGroup;
+static_assert((1 + kQkNormMaxGroups) * sizeof(unsigned) <= 256, "counters");
+size_t qk_norm_bwd_part_bytes(int D) { return ws_up(sizeof(float) * 2 * D * (kQkNormMaxBlocks + kQkNormMaxGroups)); }
+size_t qk_norm_bwd_ws_bytes(int D) { return qk_norm_bwd_part_bytes(D) + 256; }
 
 // Paged cache: page sizes, the pool's stride, and the longest sequence a table
 // row can hold (its positions index the rotary table).
+static_assert(kPagedMaxBlocks * sizeof(unsigned) <= kCounterBytes, "counters of one stream");
 constexpr int kPagedMaxBatch = 4096;
 constexpr int kPagedMaxPositions = 1 << 20;
 int check_paged(int B, int Hq, int Hkv, int D, int page_size, int num_pages, int max_pages, long long page_stride) {
@@ -1037,6 +1094,13 @@ int ne_attn_check_status(void* stream) {
   int word = 0, zero = 0;
   if (cudaMemcpyFromSymbol(&word, g_status_word, sizeof(int)) != cudaSuccess) return NE_ERR_CUDA;
   if (word != 0 && cudaMemcpyToSymbol(g_status_word, &zero, sizeof(int)) != cudaSuccess) return NE_ERR_CUDA;
+  if (word == kStatusTimeout) {
+    // a kernel that gave up may have left its stream's counters half way
+    std::lock_guard<std::mutex> lock(g_mu);
+    if (!d->join_scratch.empty() && cudaDeviceSynchronize() != cudaSuccess) return NE_ERR_CUDA;
+    for (auto& x : d->join_scratch)
+      if (cudaMemset(x.counters, 0, kCounterBytes) != cudaSuccess) return NE_ERR_CUDA;
+  }
   return word == 0 ? NE_OK : word;
 }
 
@@ -1303,7 +1367,7 @@ int ne_attn_qk_norm_bwd(const void* q, const void* k, const void* q_w, const voi
   if (!aligned16(q) || !aligned16(k) || !aligned16(q_w) || !aligned16(k_w) || !aligned16(dqn) || !aligned16(dkn) ||
       !aligned16(dq) || !aligned16(dk) || !aligned16(dq_w) || !aligned16(dk_w))
     return NE_ERR_ALIGN;
-  if (!workspace || workspace_bytes < qk_norm_bwd_ws_bytes(D) || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+  if (workspace && (workspace_bytes < qk_norm_bwd_ws_bytes(D) || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0))
     return NE_ERR_WORKSPACE;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   std::lock_guard<std::mutex> lock(g_mu);
@@ -1320,7 +1384,6 @@ int ne_attn_qk_norm_bwd(const void* q, const void* k, const void* q_w, const voi
   a.gk = dkn;
   a.dq = dq;
   a.dk = dk;
-  a.part = static_cast<float*>(workspace);
   a.q_stride = q_stride;
   a.k_stride = k_stride;
   a.dq_stride = dq_stride;
@@ -1333,12 +1396,18 @@ int ne_attn_qk_norm_bwd(const void* q, const void* k, const void* q_w, const voi
   const int per = qk_norm_heads_per_item(true);
   a.div_hg = make_fastdiv((uint32_t)((Hq + Hkv + per - 1) / per));
   const int blocks = qk_norm_bwd_blocks(B, T, (int)a.div_hg.d, D, nsm);
-  {
-    ProfScope prof(NE_ATTN_KERNEL_QK_NORM_BWD, s);
-    if (launch_qk_norm_bwd(a, D, (flags & kFlagGradFp32) != 0, blocks, s) != cudaSuccess) return NE_ERR_CUDA;
+  a.dqw = dq_w;
+  a.dkw = dk_w;
+  void* ws = workspace;
+  if (!ws) {
+    if ((st = join_scratch(*d, s, qk_norm_bwd_part_bytes(D), &ws, &a.done)) != NE_OK) return st;
+  } else {
+    a.done = reinterpret_cast<unsigned*>(static_cast<unsigned char*>(ws) + qk_norm_bwd_part_bytes(D));
+    if (cudaMemsetAsync(a.done, 0, 256, s) != cudaSuccess) return NE_ERR_CUDA;
   }
-  ProfScope prof(NE_ATTN_KERNEL_QK_NORM_DW, s);
-  return launch_qk_norm_dw(a, D, blocks, dq_w, dk_w, s) == cudaSuccess ? NE_OK : NE_ERR_CUDA;
+  a.part = static_cast<float*>(ws);
+  ProfScope prof(NE_ATTN_KERNEL_QK_NORM_BWD, s);
+  return launch_qk_norm_bwd(a, D, (flags & kFlagGradFp32) != 0, blocks, s) == cudaSuccess ? NE_OK : NE_ERR_CUDA;
 }
 
 // ------------------------------------------------------------------ paged cache
@@ -1421,8 +1490,8 @@ int ne_attn_decode_paged(const void* q, const void* q_w, const void* k_pages, co
   if (!aligned16(q) || (q_w && !aligned16(q_w)) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(o) ||
       !aligned4(lse) || !aligned4(page_table) || !aligned4(kv_len) || !aligned4(prefix_table))
     return NE_ERR_ALIGN;
-  if (!workspace || workspace_bytes < ne_attn_decode_paged_workspace_size(B, Tq, Hq, Hkv, D, prefix_len) ||
-      (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+  if (workspace && (workspace_bytes < ne_attn_decode_paged_workspace_size(B, Tq, Hq, Hkv, D, prefix_len) ||
+                    (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0))
     return NE_ERR_WORKSPACE;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   std::lock_guard<std::mutex> lock(g_mu);
@@ -1457,10 +1526,16 @@ int ne_attn_decode_paged(const void* q, const void* q_w, const void* k_pages, co
   a.eps = eps;
   a.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)D));
   const PagedWs w = paged_ws(B, a.R, Hkv, D, prefix_len > 0);
-  unsigned char* ws = static_cast<unsigned char*>(workspace);
+  void* wsp = workspace;
+  if (!wsp) {
+    if ((st = join_scratch(*d, s, w.total, &wsp, &a.done)) != NE_OK) return st;
+    a.own_counters = 1;
+  } else {
+    a.done = reinterpret_cast<unsigned*>(static_cast<unsigned char*>(wsp) + w.done);
+  }
+  unsigned char* ws = static_cast<unsigned char*>(wsp);
   a.part_o = reinterpret_cast<float*>(ws + w.part_o);
   a.part_ml = reinterpret_cast<float2*>(ws + w.part_ml);
-  a.done = reinterpret_cast<unsigned*>(ws + w.done);
   int mt = 1;
   paged_rows(a.R, &mt, &a.tiles, &a.MG);
   const int rows = page_size < (D == 64 ? 128 : 256) ? page_size : (D == 64 ? 128 : 256);

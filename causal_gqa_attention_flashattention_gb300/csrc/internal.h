@@ -190,13 +190,17 @@ struct QkNormBwdArgs {
   const __nv_bfloat16 *q, *k, *qw, *kw;
   const void *gq, *gk;  // gradients of the normalised q, k [B, T, H, D], bf16 or fp32
   void *dq, *dk;        // gradients of q, k (same type), rows dq_stride / dk_stride values apart
-  float* part;          // [blocks, 2 D] partial weight gradients (workspace)
+  float* part;          // [blocks + groups, 2 D] partial weight gradients (workspace)
+  unsigned* done;       // [1 + groups] groups, and blocks of a group, that have left theirs; 0 before and
+                        // after (workspace or the library's)
+  float *dqw, *dkw;     // [D]
   long long q_stride, k_stride, dq_stride, dk_stride;
   int B, T, Hq, Hkv;
   float eps;
   FastDiv div_hg;
 };
 constexpr int kQkNormMaxSms = 160, kQkNormBlocksPerSm = 4;  // bound the backward's partials
+constexpr int kQkNormGroup = 32;                            // blocks whose partials are added first
 
 // Append of new keys and values to a paged cache (see paged.cu).
 struct PagedAppendArgs {
@@ -251,12 +255,13 @@ struct PagedDecodeArgs {
   float* lse;       // or null
   float* part_o;    // [2 blocks, R, D] unnormalised O of a block's first and last segment (workspace)
   float2* part_ml;  // [2 blocks, R] their maximum (log2 units) and sum
-  unsigned* done;   // [blocks] segments finished of the (sequence, head) that starts in a block
+  unsigned* done;   // [blocks] segments finished of the (sequence, head) whose first one is the block's
   long long q_stride;
   int B, Tq, Hq, Hkv, D, G, R, page_shift, num_pages, max_pages, prefix_len, rope_half, o_fp32;
   int base;         // shared positions that the prefix kernel reads (0: none, the sweep reads all)
   int tiles, MG;    // packed row tiles (8 rows each) and the groups of warps that share them
   int stages;
+  int own_counters; // done is the library's: 0 before and after every call
   float eps, scale_log2;
 };
 
@@ -283,7 +288,6 @@ int qk_norm_heads_per_item(bool bwd);
 cudaError_t launch_qk_norm(const QkNormArgs& a, int D, int nsm, cudaStream_t s);
 int qk_norm_bwd_blocks(int B, int T, int hg, int D, int nsm);
 cudaError_t launch_qk_norm_bwd(const QkNormBwdArgs& a, int D, bool f32, int blocks, cudaStream_t s);
-cudaError_t launch_qk_norm_dw(const QkNormBwdArgs& a, int D, int blocks, float* dwq, float* dwk, cudaStream_t s);
 cudaError_t launch_kv_append_paged(const PagedAppendArgs& a, int D, cudaStream_t s);
 cudaError_t launch_prefix(const PagedDecodeArgs& a, cudaStream_t s);
 void paged_rows(int R, int* mt, int* tiles, int* mg);

@@ -140,12 +140,11 @@ struct Sweep {
   static constexpr int kSlices = kTK / 16;
   static constexpr int kMaxStages = 6;
 };
-// Consumer warps: 16 where the accumulators leave each at most 104 registers, else 8.
-// They work in groups of eight on alternate tiles: a warp's tile is one chain of dependent
-// instructions (about 1200 cycles), and four chains per scheduler hide it where two
-// do not.
-constexpr int sweep_warps(int D, int mt) { return mt * D <= 64 ? 16 : 8; }
-constexpr int sweep_threads(int D, int mt) { return (sweep_warps(D, mt) + 4) * 32; }  // the last warpgroup: producer, queries, two idle
+// Eight consumer warps, then a warpgroup of the producer, the queries and two finishing warps.
+// (Sixteen consumers in two groups on alternate tiles measured slower: a short context 8.4 us
+// against 7.4, 16 contexts around 8192 positions 31.9 against 31.4.)
+constexpr int kWarps = 8;
+constexpr int kSweepThreads = (kWarps + 4) * 32;
 constexpr int kBarBytes = 384;
 constexpr int kWholeTiles = 8;  // a (sequence, head) of at most this many tiles is never split
 
@@ -158,7 +157,7 @@ struct SweepSmem {
 };
 __host__ __device__ constexpr SweepSmem sweep_smem(int D, int stages, int tiles, int mt, int B) {
   SweepSmem m = {};
-  const int rows = sweep_bufs(mt) * sweep_warps(D, mt) * mt * 8;
+  const int rows = sweep_bufs(mt) * kWarps * mt * 8;
   m.q = stages * 32768;
   m.scratch = m.q + 2 * tiles * 16 * D * 2;
   m.ml = m.scratch + rows * D * 4;
@@ -201,6 +200,17 @@ struct SweepPlan {
 struct Tiles {
   const int* cum;  // shared memory: tiles before sequence b (one head)
   int B, Hkv;
+  // the same by a whole warp for one x: 32 probes at a time
+  __device__ int find_warp(int x, int lane) const {
+    int lo = 0, hi = B;
+    while (hi - lo > 1) {
+      const int step = (hi - lo + 31) >> 5, i = lo + lane * step;
+      const unsigned le = __ballot_sync(0xffffffffu, i < hi && cum[i] * Hkv <= x);
+      lo += (31 - __clz((int)le)) * step;
+      hi = min(hi, lo + step);
+    }
+    return lo;
+  }
   __device__ int find(int x) const {  // last b with Hkv * cum[b] <= x
     int lo = 0, hi = B;
     while (hi - lo > 1) {
@@ -218,8 +228,10 @@ struct Tiles {
   // Inside longer ones the boundaries stay, so owner() needs the unmoved starts only.
   __device__ int start(const SweepPlan& p, int c) const {
     const int x = c * p.base + min(c, p.rem);
-    if (x >= p.W) return p.W;
-    const int i = find(x), n = cum[i + 1] - cum[i];
+    return x >= p.W ? p.W : moved(x, find(x));
+  }
+  __device__ int moved(int x, int i) const {  // x in sequence i
+    const int n = cum[i + 1] - cum[i];
     if (n > kWholeTiles) return x;
     const int off = (x - cum[i] * Hkv) % n;
     return 2 * off < n ? x - off : x - off + n;
@@ -282,13 +294,12 @@ __device__ __forceinline__ int sweep_base(const PagedDecodeArgs& a, int len) {
 }
 
 // A row's parts (maximum z in log2 units, sum, O), some lanes each with a few: the maximum of
-// all, then sums of the rescaled parts.  A part with sum 0 saw no key and its O is not looked at.
+// all, then sums of the rescaled parts (0 where a part's sum is 0: the row saw none of its keys).
 struct RowSum {
   float M = -INFINITY, S = 0.f;
   float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
   __device__ void add(float top, float2 z, const float4& u) {
-    if (z.y == 0.f) return;
-    const float f = ex2(z.x - top);
+    const float f = z.y == 0.f ? 0.f : ex2(z.x - top);
     S = fmaf(f, z.y, S);
     v = make_float4(fmaf(f, u.x, v.x), fmaf(f, u.y, v.y), fmaf(f, u.z, v.z), fmaf(f, u.w, v.w));
   }
@@ -303,15 +314,14 @@ __device__ bool sweep_consume(const PagedDecodeArgs& a, SegWalk sw, const int* l
                               const SweepBars& bar, const volatile int* abort, int warp, int lane) {
   using C = Sweep<D>;
   constexpr int KS = D / 16;
-  constexpr int kWarps = sweep_warps(D, MT), kGroups = kWarps / 8, kBufs = sweep_bufs(MT);
-  const int grp = warp >> 3;                    // takes every kGroups-th tile
-  const int KG = MT < 4 ? 8 : 8 / a.MG;         // warps over a tile's keys; the rest share the row tiles out
-  const int mg = (warp & 7) / KG, kg = (warp & 7) - mg * KG;
+  constexpr int kBufs = sweep_bufs(MT);
+  const int KG = MT < 4 ? kWarps : kWarps / a.MG;  // warps over a tile's keys; the rest share the row tiles out
+  const int mg = warp / KG, kg = warp - mg * KG;
   const uint32_t ring = smem_u32(smem);
   const float sl2 = a.scale_log2;
   // this lane's ldmatrix row and chunk parity (keys, values and queries alike)
   const uint32_t lrow = lane & 15, lchk = lane >> 4;
-  int st = 0, ph = 0, seg = 0, turn = 0;
+  int st = 0, ph = 0, seg = 0;
   for (; sw.next(); seg++) {
     const int total = len[sw.b], own = total - sweep_base(a, total);
     const int pos0 = own - a.Tq;  // row 0's position, counted from the own part's start
@@ -341,15 +351,6 @@ __device__ bool sweep_consume(const PagedDecodeArgs& a, SegWalk sw, const int* l
         for (int e = 0; e < 4; e++) o[m][i][e] = 0.f;
     }
     for (int n = sw.n0; n < sw.n1; n++) {
-      const bool mine = kGroups == 1 || turn == grp;
-      if (kGroups > 1) turn = turn + 1 == kGroups ? 0 : turn + 1;
-      if (!mine) {
-        if (++st == a.stages) {
-          st = 0;
-          ph ^= 1;
-        }
-        continue;
-      }
       if (!__all_sync(0xffffffffu, mbar_wait(bar.full + st, ph, abort))) return false;
       const uint32_t kb = ring + st * C::kStage, vb = kb + C::kHalf;
       for (int sl = kg; sl < C::kSlices; sl += KG) {
@@ -460,6 +461,25 @@ __device__ bool sweep_consume(const PagedDecodeArgs& a, SegWalk sw, const int* l
   return true;
 }
 
+// Counts a segment, the last one (number `last`) back to 0: its part is visible before the
+// count, and the parts of those counted before are visible after it.
+__device__ __forceinline__ bool count_segment(unsigned* done, unsigned last) {
+  unsigned old;
+  asm volatile("atom.inc.acq_rel.gpu.global.u32 %0, [%1], %2;" : "=r"(old) : "l"(done), "r"(last) : "memory");
+  return old == last;
+}
+
+// The joined shared prefix of row r of (sequence b, head g): columns 4 q .. and 4 (q + D / 8) ..
+template <int D>
+__device__ __forceinline__ void load_prefix(const PagedDecodeArgs& a, int b, int g, int r, int q, float2& z, float4& u0,
+                                            float4& u1) {
+  const size_t row = (size_t)g * a.pre.tiles * kTile + (size_t)b * a.R + r;
+  z = __ldcg(a.pre.ml + row);
+  const float4* o = reinterpret_cast<const float4*>(a.pre.o + row * D) + q;
+  u0 = __ldcg(o);
+  u1 = __ldcg(o + D / 8);
+}
+
 // Finishing warp f: joins the consumers' parts of every kBufs-th segment (and the shared
 // prefix's part, where the sequence's own first tile is).  A whole (sequence, head) is written
 // out; a segment leaves its part in the workspace and is counted, and the block that counts
@@ -468,57 +488,63 @@ template <int D, int MT>
 __device__ bool sweep_finish(const PagedDecodeArgs& a, SegWalk sw, const Tiles& tl, const SweepPlan& plan, const int* len,
                              uint8_t* smem, const SweepSmem& L, const SweepBars& bar, volatile int* todo,
                              const volatile int* abort, int f, int lane) {
-  constexpr int kWarps = sweep_warps(D, MT), kGroups = kWarps / 8, kBufs = sweep_bufs(MT);
-  const int KG = MT < 4 ? 8 : 8 / a.MG, parts = KG * kGroups;  // warps that hold a part of a row
+  constexpr int kBufs = sweep_bufs(MT);
+  const int parts = MT < 4 ? kWarps : kWarps / a.MG;  // warps that hold a part of a row
   const float* scratch = reinterpret_cast<const float*>(smem + L.scratch) + f * kWarps * MT * 8 * D;
   const float2* ml = reinterpret_cast<const float2*>(smem + L.ml) + f * kWarps * MT * 8;
   const int first = sw.w;
   bool waited = false;
   for (int seg = 0; sw.next(); seg++) {
     if (seg % kBufs != f) continue;
-    if (!__all_sync(0xffffffffu, mbar_wait(bar.parts_full + f, (seg / kBufs) & 1, abort))) return false;
     if (!waited) {
       pdl_wait();  // the kernels before clear the workspace's counters and leave the prefix's parts
       waited = true;
     }
+    const bool pre = sw.n0 == 0 && sweep_base(a, len[sw.b]) > 0;
+    float2 zp = make_float2(-INFINITY, 0.f);
+    float4 up0 = make_float4(0.f, 0.f, 0.f, 0.f), up1 = up0;
+    if (pre && lane < a.R * (D / 8)) load_prefix<D>(a, sw.b, sw.g, lane / (D / 8), lane % (D / 8), zp, up0, up1);
+    if (!__all_sync(0xffffffffu, mbar_wait(bar.parts_full + f, (seg / kBufs) & 1, abort))) return false;
     const bool whole = sw.n0 == 0 && sw.n1 == sw.nt;
     const int s0 = tl.cum[sw.b] * tl.Hkv + sw.g * sw.nt, slot = s0 <= first ? 0 : 1;
-    const bool pre = sw.n0 == 0 && sweep_base(a, len[sw.b]) > 0;
-    const int items = a.R * (D / 4);
+    // a lane takes columns 4 q .. and 4 (q + D / 8) .. of a row
+    constexpr int kQ = D / 8;
+    const int items = a.R * kQ;
     for (int i = lane; i < items; i += 32) {
-      const int r = i / (D / 4), q = i % (D / 4), tile = r >> 3;
-      const int at0 = ((tile / MT) * KG * MT + tile % MT) * 8 + (r & 7);
-      const auto at = [&](int k) { return at0 + (k % KG + k / KG * 8) * MT * 8; };
-      float2 zp = make_float2(-INFINITY, 0.f);
-      float4 up = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (pre) {
-        const size_t row = (size_t)sw.g * a.pre.tiles * kTile + (size_t)sw.b * a.R + r;
-        zp = __ldcg(a.pre.ml + row);
-        up = __ldcg(reinterpret_cast<const float4*>(a.pre.o + row * D) + q);
-      }
-      RowSum x;
+      const int r = i / kQ, q = i % kQ, tile = r >> 3;
+      if (pre && i != lane) load_prefix<D>(a, sw.b, sw.g, r, q, zp, up0, up1);
+      const int at0 = ((tile / MT) * parts * MT + tile % MT) * 8 + (r & 7);
+      RowSum x, y;
       x.M = zp.x;
+#pragma unroll
+      for (int k = 0; k < kWarps; k++)
+        if (MT < 4 || k < parts) x.M = fmaxf(x.M, ml[at0 + k * MT * 8].x);
+      x.add(x.M, zp, up0);
+      y.add(x.M, zp, up1);
 #pragma unroll 4
-      for (int k = 0; k < parts; k++) x.M = fmaxf(x.M, ml[at(k)].x);
-      x.add(x.M, zp, up);
-#pragma unroll 4
-      for (int k = 0; k < parts; k++) x.add(x.M, ml[at(k)], *reinterpret_cast<const float4*>(scratch + at(k) * D + 4 * q));
+      for (int k = 0; k < parts; k++) {
+        const int from = at0 + k * MT * 8;
+        const float2 z = ml[from];
+        x.add(x.M, z, *reinterpret_cast<const float4*>(scratch + from * D + 4 * q));
+        y.add(x.M, z, *reinterpret_cast<const float4*>(scratch + from * D + 4 * (q + kQ)));
+      }
       if (whole) {
         write_row<D>(a, sw.b, sw.g, r, q, x.v, x.M, x.S);
+        write_row<D>(a, sw.b, sw.g, r, q + kQ, y.v, x.M, x.S);
       } else {
         const size_t at1 = (size_t)(2 * blockIdx.x + slot) * a.R + r;
-        *reinterpret_cast<float4*>(a.part_o + at1 * D + 4 * q) = x.v;
+        float4* to = reinterpret_cast<float4*>(a.part_o + at1 * D) + q;
+        to[0] = x.v;
+        to[kQ] = y.v;
         if (q == 0) a.part_ml[at1] = make_float2(x.M, x.S);
       }
     }
     warp_arrive(bar.parts_empty + f);
     if (whole) continue;
-    __threadfence();
-    __syncwarp();
+    __syncwarp();  // the other lanes' parts before lane 0's release
     if (lane == 0) {
       const int c0 = tl.owner(plan, s0), c1 = tl.owner(plan, s0 + sw.nt - 1);
-      if (atomicAdd(a.done + c0, 1u) == (unsigned)(c1 - c0)) todo[slot] = sw.b * tl.Hkv + sw.g;
-      __threadfence();
+      if (count_segment(a.done + c0, (unsigned)(c1 - c0))) todo[slot] = sw.b * tl.Hkv + sw.g;
     }
     __syncwarp();
   }
@@ -532,7 +558,7 @@ __device__ bool sweep_finish(const PagedDecodeArgs& a, SegWalk sw, const Tiles& 
 template <int D, int MT>
 __device__ bool sweep_join(const PagedDecodeArgs& a, const Tiles& tl, const SweepPlan& plan, const SweepBars& bar,
                            const volatile int* todo, const volatile int* abort, int tid) {
-  constexpr int kThreads = sweep_warps(D, MT) * 32, kSplit = 8, kAhead = 4;
+  constexpr int kThreads = kWarps * 32, kSplit = 4, kAhead = 5;
   if (!__all_sync(0xffffffffu, mbar_wait(bar.fin, 0, abort))) return false;
   for (int k = 0; k < 2; k++) {
     const int sh = todo[k];
@@ -582,9 +608,9 @@ __device__ bool sweep_join(const PagedDecodeArgs& a, const Tiles& tl, const Swee
 }
 
 template <int D, int MT>
-__global__ void __launch_bounds__(sweep_threads(D, MT), 1) k_paged_sweep(const __grid_constant__ PagedDecodeArgs a) {
+__global__ void __launch_bounds__(kSweepThreads, 1) k_paged_sweep(const __grid_constant__ PagedDecodeArgs a) {
   using C = Sweep<D>;
-  constexpr int kWarps = sweep_warps(D, MT), kThreads = sweep_threads(D, MT), kBufs = sweep_bufs(MT);
+  constexpr int kThreads = kSweepThreads, kBufs = sweep_bufs(MT);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -600,16 +626,18 @@ __global__ void __launch_bounds__(sweep_threads(D, MT), 1) k_paged_sweep(const _
   volatile int* abort = reinterpret_cast<volatile int*>(bar.fin + 1);
   volatile int* todo = abort + 1;                              // [2]
   volatile SweepPlan* splan = reinterpret_cast<volatile SweepPlan*>(const_cast<int*>(abort) + 3);
-  int* wsum = const_cast<int*>(abort) + 12;                    // [20] the scan's warp totals
+  int* wsum = const_cast<int*>(abort) + 12;                    // [12] the scan's warp totals
   int* cum = reinterpret_cast<int*>(smem + L.cum);
   int* len = reinterpret_cast<int*>(smem + L.len);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  int n_first = 0;
+  if (tid < a.B) n_first = a.len[tid];
   if (tid == 0) {
     *abort = 0;
     todo[0] = todo[1] = -1;
     for (int i = 0; i < a.stages; i++) {
       mbar_init(bar.full + i, 1);
-      mbar_init(bar.empty + i, 8);
+      mbar_init(bar.empty + i, kWarps);
     }
     for (int i = 0; i < 2; i++) {
       mbar_init(bar.q_full + i, 1);
@@ -632,7 +660,7 @@ __global__ void __launch_bounds__(sweep_threads(D, MT), 1) k_paged_sweep(const _
     const int b = b0 + tid;
     int nt = 0;
     if (b < a.B) {
-      int n = a.len[b];
+      int n = b0 == 0 ? n_first : a.len[b];
       if (n > cap) {
         if (blockIdx.x == 0) record_page(a.status);
         n = cap;
@@ -652,7 +680,7 @@ __global__ void __launch_bounds__(sweep_threads(D, MT), 1) k_paged_sweep(const _
     if (lane == 31) wsum[warp] = x;
     __syncthreads();
     if (b0 + warp * 32 < a.B) {
-      int low = lane < warp ? wsum[lane] : 0;  // at most 20 warps
+      int low = lane < warp ? wsum[lane] : 0;  // at most 12 warps
 #pragma unroll
       for (int m = 16; m; m >>= 1) low += __shfl_xor_sync(0xffffffffu, low, m);
       if (b < a.B) cum[b + 1] = before + low + x;
@@ -674,12 +702,16 @@ __global__ void __launch_bounds__(sweep_threads(D, MT), 1) k_paged_sweep(const _
     p.G = min(p.W, (int)gridDim.x);
     p.base = p.W / p.G;
     p.rem = p.W - p.base * p.G;
-    const int c = (int)blockIdx.x + (lane & 1);
-    const int x = c <= p.G ? tl.start(p, min(c, p.G)) : p.W;
-    p.w = __shfl_sync(0xffffffffu, x, 0);
-    p.end = __shfl_sync(0xffffffffu, x, 1);
+    // tiles of this block and the next one's first, with the sequences they are in
+    const int c = min((int)blockIdx.x, p.G), x0 = min(c * p.base + min(c, p.rem), p.W - 1);
+    const int x1 = min(x0 + p.base + (c < p.rem ? 1 : 0), p.W);
+    const int b0 = tl.find_warp(x0, lane), b1 = tl.find_warp(min(x1, p.W - 1), lane);
+    p.w = c < p.G ? tl.moved(x0, b0) : p.W;
+    p.end = c < p.G && x1 < p.W ? tl.moved(x1, b1) : p.W;
+    p.b = b0;
+    if (p.w == (cum[b0 + 1]) * a.Hkv) p.b++;  // moved to the next sequence's first tile
     if (lane == 0) {
-      p.b = tl.find(min(p.w, p.W - 1));
+      if (p.b == a.B) p.b--;  // nothing left
       const int nt = cum[p.b + 1] - cum[p.b], off = p.w - cum[p.b] * a.Hkv;
       p.g = off / nt;
       p.n0 = off - p.g * nt;
@@ -698,13 +730,9 @@ __global__ void __launch_bounds__(sweep_threads(D, MT), 1) k_paged_sweep(const _
   SegWalk sw;
   sw.init(cum, a.Hkv, splan);
   const volatile int never = 0;
-  // Registers at launch, and what the consumers and the others then hold: 640 x 96 = 512 x 104 +
-  // 128 x 64, or 384 x 168 = 256 x 216 + 128 x 72.
+  // registers: 384 x 168 at launch; 256 x 216 for the consumers, 128 x 72 for the others
   if (warp < kWarps) {
-    if (kWarps == 16)
-      regs_inc<104>();
-    else
-      regs_inc<216>();
+    regs_inc<216>();
     bool ok = sweep_consume<D, MT>(a, sw, len, smem, L, bar, abort, warp, lane);
     if (ok) {
       SweepPlan p;
@@ -719,10 +747,7 @@ __global__ void __launch_bounds__(sweep_threads(D, MT), 1) k_paged_sweep(const _
     }
     return;
   }
-  if (kWarps == 16)
-    regs_dec<64>();
-  else
-    regs_dec<72>();
+  regs_dec<72>();
   bool ok = true;
   if (warp == kWarps) {
     // ------------------------------------------------------------ keys and values
@@ -840,19 +865,20 @@ cudaError_t launch_sweep_t(const PagedDecodeArgs& a, int nsm, cudaStream_t s) {
   }
   PagedDecodeArgs b = a;
   b.stages = Sweep<D>::kMaxStages;
-  // An even ring with two groups of consumers: every stage then belongs to one of them.  In an
-  // odd one a group could wait for a stage's next round while the other's round has not yet
-  // landed, and a parity wait would take the round before that for it.
-  constexpr int kGroups = sweep_warps(D, MT) / 8;
-  while (b.stages > 2 && sweep_smem(D, b.stages, b.tiles, MT, b.B).total > kSmemMax) b.stages -= kGroups;
+  while (b.stages > 2 && sweep_smem(D, b.stages, b.tiles, MT, b.B).total > kSmemMax) b.stages--;
   const int bytes = sweep_smem(D, b.stages, b.tiles, MT, b.B).total;
   if (bytes > kSmemMax) return cudaErrorInvalidValue;
+  const int grid = nsm < kPagedMaxBlocks ? nsm : kPagedMaxBlocks;
+  if (b.base == 0 && b.own_counters) {  // they are 0 before and after every call
+    k_paged_sweep<D, MT><<<grid, kSweepThreads, (size_t)bytes, s>>>(b);
+    return cudaGetLastError();
+  }
   if (b.base == 0) {  // with a shared prefix k_prefix_q has cleared them
     k_paged_clear<<<1, 256, 0, s>>>(b.done, kPagedMaxBlocks);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
-  return launch_pdl(k_paged_sweep<D, MT>, nsm < kPagedMaxBlocks ? nsm : kPagedMaxBlocks, sweep_threads(D, MT), (size_t)bytes, s, b);
+  return launch_pdl(k_paged_sweep<D, MT>, grid, kSweepThreads, (size_t)bytes, s, b);
 }
 
 }  // namespace

@@ -105,10 +105,50 @@ __global__ void __launch_bounds__(kThreads) k_qk_norm(const QkNormArgs a) {
   }
 }
 
+// Whether this block is the last of n to count itself (the counter goes back to 0); what the
+// block wrote before is visible to the last one after.
+__device__ __forceinline__ bool last_to_count(unsigned* done, unsigned n) {
+  __shared__ bool last;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    unsigned old;
+    asm volatile("atom.inc.acq_rel.gpu.global.u32 %0, [%1], %2;" : "=r"(old) : "l"(done), "r"(n - 1) : "memory");
+    last = old == n - 1;
+  }
+  __syncthreads();
+  return last;
+}
+
+// Sum of n partial rows of 2 D values, n at most 4 kOver, in a fixed order; true for the first
+// 2 D / 4 threads, which then have a quad each in t.
+template <int D>
+__device__ __forceinline__ bool add_partials(const float* part, unsigned n, float4& t) {
+  constexpr unsigned kQuads = 2 * D / 4, kOver = kThreads / kQuads;
+  __shared__ float4 red4[kOver][kQuads];
+  const unsigned q = threadIdx.x % kQuads, o = threadIdx.x / kQuads;
+  float4 u[4];
+#pragma unroll
+  for (unsigned k = 0; k < 4; k++)
+    u[k] = o + k * kOver < n ? __ldcg(reinterpret_cast<const float4*>(part) + (size_t)(o + k * kOver) * kQuads + q)
+                             : make_float4(0.f, 0.f, 0.f, 0.f);
+  red4[o][q] = make_float4((u[0].x + u[1].x) + (u[2].x + u[3].x), (u[0].y + u[1].y) + (u[2].y + u[3].y),
+                           (u[0].z + u[1].z) + (u[2].z + u[3].z), (u[0].w + u[1].w) + (u[2].w + u[3].w));
+  __syncthreads();
+  if (threadIdx.x >= kQuads) return false;
+  t = red4[0][q];
+#pragma unroll
+  for (unsigned k = 1; k < kOver; k++) {
+    const float4 x = red4[k][q];
+    t = make_float4(t.x + x.x, t.y + x.y, t.z + x.z, t.w + x.w);
+  }
+  return true;
+}
+static_assert(kQkNormGroup <= 32 && kQkNormMaxSms * kQkNormBlocksPerSm <= 32 * kQkNormGroup, "partials of a sum");
+
 // Backward.  dw is summed in fp32: over the rows of a thread, over the threads of
 // a block that share a chunk (in a fixed order), one partial per block and weight
-// in the workspace; k_qk_norm_dw adds the blocks in order.  Nothing is atomic, so
-// the result is bitwise reproducible.
+// in the workspace, added in two steps by the blocks that end last, always in the
+// same order: the result does not depend on which ones, and is bitwise reproducible.
 template <int D, bool F32>
 __global__ void __launch_bounds__(kThreads) k_qk_norm_bwd(const QkNormBwdArgs a) {
   constexpr int kCPR = D / 8;
@@ -211,28 +251,18 @@ __global__ void __launch_bounds__(kThreads) k_qk_norm_bwd(const QkNormBwdArgs a)
     for (int w = 0; w < kThreads / 32; w++) s += red[w][threadIdx.x];
     a.part[(size_t)blockIdx.x * 2 * D + threadIdx.x] = s;
   }
-}
-
-// dw[j] = sum over the blocks of part[block][j]: a block takes eight columns
-// (one 32-byte sector of every partial row), 32 threads per column.
-template <int D>
-__global__ void __launch_bounds__(256) k_qk_norm_dw(const float* part, int blocks, float* dwq, float* dwk) {
-  pdl_wait();  // the partials of the pass before
-  const int col = blockIdx.x * 8 + threadIdx.x % 8, k = threadIdx.x / 8;
-  float s = 0.f;
-  for (int b = k; b < blocks; b += 32) s += part[(size_t)b * 2 * D + col];
-  __shared__ float red[32][8];
-  red[k][threadIdx.x % 8] = s;
-  __syncthreads();
-  if (threadIdx.x < 8) {
-    s = 0.f;
-#pragma unroll
-    for (int i = 0; i < 32; i++) s += red[i][threadIdx.x];
-    if (col < D)
-      dwq[col] = s;
-    else
-      dwk[col - D] = s;
-  }
+  // the last of kQkNormGroup neighbouring blocks adds their partials in order, the last of those
+  // blocks the groups' sums
+  const unsigned grp = blockIdx.x / kQkNormGroup, groups = (gridDim.x + kQkNormGroup - 1) / kQkNormGroup;
+  const unsigned b0 = grp * kQkNormGroup, nb = min((unsigned)kQkNormGroup, gridDim.x - b0);
+  float4 t;
+  if (!last_to_count(a.done + 1 + grp, nb)) return;
+  const bool mine = add_partials<D>(a.part + (size_t)b0 * 2 * D, nb, t);
+  float4* sums = reinterpret_cast<float4*>(a.part + (size_t)gridDim.x * 2 * D);
+  if (mine) sums[(size_t)grp * (2 * D / 4) + threadIdx.x] = t;
+  if (!last_to_count(a.done, groups)) return;
+  if (add_partials<D>(reinterpret_cast<const float*>(sums), groups, t))
+    *reinterpret_cast<float4*>((threadIdx.x < D / 4 ? a.dqw : a.dkw - D) + 4 * threadIdx.x) = t;
 }
 
 int blocks_for(long long threads, int most) {
@@ -270,11 +300,6 @@ cudaError_t launch_qk_norm_bwd(const QkNormBwdArgs& a, int D, bool f32, int bloc
       k_qk_norm_bwd<32, false><<<blocks, kThreads, 0, s>>>(a);
   }
   return cudaGetLastError();
-}
-
-cudaError_t launch_qk_norm_dw(const QkNormBwdArgs& a, int D, int blocks, float* dwq, float* dwk, cudaStream_t s) {
-  if (D == 64) return launch_pdl(k_qk_norm_dw<64>, 2 * D / 8, 256, 0, s, (const float*)a.part, blocks, dwq, dwk);
-  return launch_pdl(k_qk_norm_dw<32>, 2 * D / 8, 256, 0, s, (const float*)a.part, blocks, dwq, dwk);
 }
 
 }  // namespace ne

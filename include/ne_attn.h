@@ -327,9 +327,11 @@ int ne_attn_qk_norm(const void* q, const void* k, const void* q_w, const void* k
  * (dqn, dkn, dq, dk are float32, else bfloat16).  dq and dk have row strides of
  * their own and may be the buffers of dqn and dkn (with the contiguous stride).
  * The rotary layout does not enter.  The workspace
- * (ne_attn_qk_norm_bwd_workspace_size bytes, 256-byte aligned) is required.
- * Two kernels: the rows, with the weight gradients summed per block in fp32;
- * then the blocks' sums in a fixed order (bitwise reproducible).
+ * (ne_attn_qk_norm_bwd_workspace_size bytes, 256-byte aligned) may be NULL: the
+ * library then uses one of its own per stream, except under stream capture
+ * (NE_ERR_WORKSPACE).  One streaming kernel: the weight gradients are summed per
+ * block in fp32, and by the block that ends last in a fixed order (bitwise
+ * reproducible).
  */
 size_t ne_attn_qk_norm_bwd_workspace_size(int B, int T, int Hq, int Hkv, int D);
 int ne_attn_qk_norm_bwd(const void* q, const void* k, const void* q_w, const void* k_w, const void* dqn,
@@ -390,9 +392,12 @@ int ne_attn_kv_append_paged(const void* k_new, const void* v_new, const void* k_
  * sequence's own table and prefix_len = 0, up to rounding.
  *
  * Requires (Hq / Hkv) * Tq <= 128, B * Hkv * ceil(max_pages * page_size / 128)
- * < 2^30 and the workspace
- * (ne_attn_decode_paged_workspace_size bytes, 256-byte aligned); calls that may
- * run at the same time need workspaces of their own.
+ * < 2^30.  The workspace (ne_attn_decode_paged_workspace_size bytes, 256-byte
+ * aligned) may be NULL: the library then uses one of its own per stream, grown
+ * with cudaMalloc when a larger shape arrives, except under stream capture
+ * (NE_ERR_WORKSPACE: a graph may run on any stream).  Calls and graphs that may
+ * run at the same time need workspaces of their own.  The result is bitwise
+ * reproducible.
  */
 size_t ne_attn_decode_paged_workspace_size(int B, int Tq, int Hq, int Hkv, int D, int prefix_len);
 int ne_attn_decode_paged(const void* q, const void* q_w, const void* k_pages, const void* v_pages,
@@ -443,12 +448,11 @@ const char* ne_attn_status_string(int status);
 #define NE_ATTN_KERNEL_QKV_PREP 8   /* RMSNorm row statistics and the weight fold */
 #define NE_ATTN_KERNEL_QKV 9        /* the projection GEMM with the rotary epilogue */
 #define NE_ATTN_KERNEL_QK_NORM 10       /* query/key norms with the rotation */
-#define NE_ATTN_KERNEL_QK_NORM_BWD 11   /* their backward over the rows */
-#define NE_ATTN_KERNEL_QK_NORM_DW 12    /* the weight gradients' last sum */
-#define NE_ATTN_KERNEL_KV_APPEND_PAGED 13
-#define NE_ATTN_KERNEL_DECODE_PAGED 14  /* the sweep over a paged cache */
-#define NE_ATTN_KERNEL_DECODE_PREFIX 15 /* a shared prefix's queries and sweep */
-#define NE_ATTN_NUM_KERNEL_KINDS 16
+#define NE_ATTN_KERNEL_QK_NORM_BWD 11   /* their backward */
+#define NE_ATTN_KERNEL_KV_APPEND_PAGED 12
+#define NE_ATTN_KERNEL_DECODE_PAGED 13  /* the sweep over a paged cache */
+#define NE_ATTN_KERNEL_DECODE_PREFIX 14 /* a shared prefix's queries and sweep */
+#define NE_ATTN_NUM_KERNEL_KINDS 15
 int ne_attn_profile_start(int capacity);
 int ne_attn_profile_stop(double* total_ms, long long* launches);
 int ne_attn_profile_detach(void);

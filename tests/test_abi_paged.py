@@ -63,7 +63,7 @@ def test_qk_norm_bwd(libne, mem):
         assert f(**{name: p + 8}) == -2
     assert f(eps=-1.0) == -1 and f(flags=16) == -1 and f(flags=1) == -1
     assert f(dqs=120) == -1 and f(dks=60) == -1 and f(qs=132) == -1
-    assert f(ws=None) == -5 and f(bytes=n - 1) == -5 and f(ws=p + 128) == -5
+    assert f(bytes=n - 1) == -5 and f(ws=p + 128) == -5
 
 
 def test_kv_append_paged(libne, mem):
@@ -110,7 +110,7 @@ def test_decode_paged(libne, mem):
     assert f(prefix=16) == -1                    # needs its table
     assert f(prefix=-16, ptable=p) == -1 and f(prefix=24, ptable=p) == -1 and f(prefix=64, ptable=p) == -1
     assert f(eps=0.0) == -1 and f(base=float("inf")) == -1 and f(flags=2) == -1 and f(flags=4) == -1
-    assert f(ws=None) == -5 and f(bytes=n - 1) == -5 and f(ws=p + 64) == -5
+    assert f(bytes=n - 1) == -5 and f(ws=p + 64) == -5
 
 
 def test_status_text(libne):
