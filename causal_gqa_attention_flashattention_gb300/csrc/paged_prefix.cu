@@ -453,8 +453,7 @@ __global__ void __launch_bounds__(384, 1) k_prefix(const __grid_constant__ Paged
 }
 
 // ====================================================================== the segments of a tile joined
-// A thread takes four columns of a row: the maximum over the row's segments, then the sum of
-// the rescaled parts, in order.  32 neighbouring rows of one column quad lie side by side in a
+// A thread takes four columns of a row and its segments in order, rescaling as the maximum grows.  32 neighbouring rows of one column quad lie side by side in a
 // segment (prefix_quad); the result is row by row.
 template <int D>
 __global__ void __launch_bounds__(128) k_prefix_join(const __grid_constant__ PagedDecodeArgs a) {
@@ -469,18 +468,32 @@ __global__ void __launch_bounds__(128) k_prefix_join(const __grid_constant__ Pag
   if (g >= a.Hkv) return;
   const int row = r32 * 32 + lane, s = g * p.pairs + (tile >> 1), u = tile & 1;
   const int lo = prefix_owner(p, s * p.ntk), hi = prefix_owner(p, s * p.ntk + p.ntk - 1);
-  float top = -INFINITY;
-  for (int c = lo; c <= hi; c++) top = fmaxf(top, __ldcg(p.part_ml + prefix_part(c + s, u) * kTile + row).x);
-  float S = 0.f;
+  // eight segments' loads under way at a time
+  constexpr int kAhead = 8;
+  float top = -INFINITY, S = 0.f;
   float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-  for (int c = lo; c <= hi; c++) {
-    const size_t part = prefix_part(c + s, u);
-    const float2 z = __ldcg(p.part_ml + part * kTile + row);
-    const float4 x = __ldcg(reinterpret_cast<const float4*>(p.part_o) + prefix_quad<D>(part, row, q));
-    const float f = ex2(z.x - top);
-    S = fmaf(f, z.y, S);
-    v = make_float4(fmaf(f, x.x, v.x), fmaf(f, x.y, v.y), fmaf(f, x.z, v.z), fmaf(f, x.w, v.w));
+  for (int c0 = lo; c0 <= hi; c0 += kAhead) {
+    float2 z[kAhead];
+    float4 x[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; k++) {
+      const size_t part = prefix_part(min(c0 + k, hi) + s, u);
+      z[k] = __ldcg(p.part_ml + part * kTile + row);
+      x[k] = __ldcg(reinterpret_cast<const float4*>(p.part_o) + prefix_quad<D>(part, row, q));
+    }
+    float t = top;
+#pragma unroll
+    for (int k = 0; k < kAhead; k++) t = fmaxf(t, z[k].x);
+    const float r = top == -INFINITY ? 0.f : ex2(top - t);
+    S *= r;
+    v = make_float4(v.x * r, v.y * r, v.z * r, v.w * r);
+    top = t;
+#pragma unroll
+    for (int k = 0; k < kAhead; k++) {
+      const float f = c0 + k <= hi ? ex2(z[k].x - top) : 0.f;
+      S = fmaf(f, z[k].y, S);
+      v = make_float4(fmaf(f, x[k].x, v.x), fmaf(f, x[k].y, v.y), fmaf(f, x[k].z, v.z), fmaf(f, x[k].w, v.w));
+    }
   }
   const size_t out = (size_t)gt * kTile + row;
   reinterpret_cast<float4*>(p.o)[out * (D / 4) + q] = v;
