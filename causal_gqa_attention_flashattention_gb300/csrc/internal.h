@@ -261,6 +261,7 @@ struct PagedDecodeArgs {
   int base;         // shared positions that the prefix kernel reads (0: none, the sweep reads all)
   int tiles, MG;    // packed row tiles (8 rows each) and the groups of warps that share them
   int stages;
+  FastDiv div_grid; // by the sweep's blocks
   int own_counters; // done is the library's: 0 before and after every call
   float eps, scale_log2;
 };

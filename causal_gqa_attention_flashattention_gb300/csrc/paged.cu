@@ -298,6 +298,13 @@ __device__ __forceinline__ int sweep_base(const PagedDecodeArgs& a, int len) {
 struct RowSum {
   float M = -INFINITY, S = 0.f;
   float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  // to the maximum `top`, which is at least M
+  __device__ void raise(float top) {
+    const float f = S == 0.f ? 0.f : ex2(M - top);
+    M = top;
+    S *= f;
+    v = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
+  }
   __device__ void add(float top, float2 z, const float4& u) {
     const float f = z.y == 0.f ? 0.f : ex2(z.x - top);
     S = fmaf(f, z.y, S);
@@ -309,6 +316,126 @@ struct SweepBars {
   uint64_t *full, *empty, *q_full, *q_empty, *parts_full, *parts_empty, *fin;
 };
 
+// What a consumer warp holds of a segment: MT row tiles' queries (in registers for at most two
+// of them, else read from shared memory as they are used), O, running maximum and sum.
+template <int D, int MT>
+struct SweepState {
+  static constexpr int KS = D / 16, kQ = MT <= 2 ? MT : 1;
+  uint32_t q[kQ][KS][4], qbase;
+  float o[MT][2 * KS][4], mx[MT], ls[MT];
+  int lim[MT];      // last visible position of this lane's row, from the own part's start
+  int own, pos0;    // positions of the own part; row 0's position
+};
+// Slices of 16 keys that a warp takes together: two where the registers allow it, which gives
+// its chain of dependent steps (scores, maximum, weights, P V) something to overlap with.
+template <int D, int MT>
+constexpr int kSlicesAtOnce = MT * D <= 128 ? 2 : 1;
+
+// N slices (keys at kb, values at vb, first position j0) into the state.
+template <int D, int MT, int N>
+__device__ __forceinline__ void sweep_slices(SweepState<D, MT>& w, const uint32_t (&kb)[N], const uint32_t (&vb)[N],
+                                             const int (&j0)[N], float sl2, int lane) {
+  constexpr int KS = D / 16;
+  constexpr uint32_t kSpan = Sweep<D>::kSpan;
+  // this lane's ldmatrix row and chunk parity (keys, values and queries alike)
+  const uint32_t lrow = lane & 15, lchk = lane >> 4;
+  uint32_t kf[N][KS][4], vf[N][KS][4];
+#pragma unroll
+  for (int i = 0; i < N; i++)
+#pragma unroll
+    for (int k = 0; k < KS; k++) ldsm4(kf[i][k], kb[i] + swz(lrow, 2 * k + lchk, kSpan));
+#pragma unroll
+  for (int i = 0; i < N; i++) {
+#pragma unroll
+    for (int k = 0; k < KS; k++) ldsm4t(vf[i][k], vb[i] + swz(lrow, 2 * k + lchk, kSpan));
+    if (j0[i] + 16 > w.own) {
+      // what lies behind the last position may be anything: its weight is 0, but 0 times a
+      // NaN is not
+      const int v0 = w.own - j0[i] - (lane & 3) * 2;
+      const uint32_t m0 = (v0 > 0 ? 0xffffu : 0u) | (v0 > 1 ? 0xffff0000u : 0u);
+      const uint32_t m1 = (v0 > 8 ? 0xffffu : 0u) | (v0 > 9 ? 0xffff0000u : 0u);
+#pragma unroll
+      for (int k = 0; k < KS; k++) {
+        vf[i][k][0] &= m0;
+        vf[i][k][1] &= m1;
+        vf[i][k][2] &= m0;
+        vf[i][k][3] &= m1;
+      }
+    }
+  }
+#pragma unroll
+  for (int m = 0; m < MT; m++) {
+    float sa[N][4], sb[N][4];
+#pragma unroll
+    for (int i = 0; i < N; i++)
+#pragma unroll
+      for (int e = 0; e < 4; e++) sa[i][e] = sb[i][e] = 0.f;
+#pragma unroll
+    for (int k = 0; k < KS; k++) {
+      uint32_t qt[4];
+      if (MT <= 2) {
+#pragma unroll
+        for (int e = 0; e < 4; e++) qt[e] = w.q[MT <= 2 ? m : 0][k][e];
+      } else {
+        ldsm4(qt, w.qbase + m * 16 * kSpan + swz(lrow, 2 * k + lchk, kSpan));
+      }
+#pragma unroll
+      for (int i = 0; i < N; i++) {
+        mma_f16(sa[i], qt, kf[i][k][0], kf[i][k][2]);
+        mma_f16(sb[i], qt, kf[i][k][1], kf[i][k][3]);
+      }
+    }
+    // keys (lane & 3) * 2 + {0, 1} and those + 8, row lane / 4: high + low part
+    float x[N][4], t = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < N; i++) {
+      x[i][0] = sa[i][0] + sa[i][2];
+      x[i][1] = sa[i][1] + sa[i][3];
+      x[i][2] = sb[i][0] + sb[i][2];
+      x[i][3] = sb[i][1] + sb[i][3];
+      if (j0[i] + 16 > w.pos0 + 1) {  // some row does not see every key of the slice
+        const int k0 = j0[i] + (lane & 3) * 2;
+#pragma unroll
+        for (int e = 0; e < 4; e++)
+          if (k0 + (e & 1) + (e >> 1) * 8 > w.lim[m]) x[i][e] = -INFINITY;
+      }
+      t = fmaxf(t, fmaxf(fmaxf(x[i][0], x[i][1]), fmaxf(x[i][2], x[i][3])));
+    }
+    t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
+    t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
+    // O and the sum follow the maximum only when it grew by more than 2^8
+    const float mx = w.mx[m];
+    const bool grow = mx == -INFINITY ? t > -INFINITY : __fmul_rn(t, sl2) > __fmul_rn(mx, sl2) + 8.f;
+    if (__any_sync(0xffffffffu, grow)) {
+      const float al = grow && mx != -INFINITY ? ex2(__fmul_rn(mx, sl2) - __fmul_rn(t, sl2)) : 1.f;
+      w.mx[m] = grow ? t : mx;
+      w.ls[m] *= al;
+#pragma unroll
+      for (int i = 0; i < 2 * KS; i++)
+#pragma unroll
+        for (int e = 0; e < 4; e++) w.o[m][i][e] *= al;
+    }
+    const float mu = w.mx[m] == -INFINITY ? 0.f : __fmul_rn(w.mx[m], sl2);
+#pragma unroll
+    for (int i = 0; i < N; i++) {
+      float p[4];
+#pragma unroll
+      for (int e = 0; e < 4; e++) p[e] = ex2(fmaf(x[i][e], sl2, -mu));
+      w.ls[m] += (p[0] + p[1]) + (p[2] + p[3]);
+      uint32_t pa[4];
+      pa[0] = pack_bf16(p[0], p[1]);
+      pa[2] = pack_bf16(p[2], p[3]);
+      pa[1] = pack_bf16(p[0] - bf_lo(pa[0]), p[1] - bf_hi(pa[0]));
+      pa[3] = pack_bf16(p[2] - bf_lo(pa[2]), p[3] - bf_hi(pa[2]));
+#pragma unroll
+      for (int k = 0; k < KS; k++) {
+        mma_b16(w.o[m][2 * k], pa, vf[i][k][0], vf[i][k][1]);
+        mma_b16(w.o[m][2 * k + 1], pa, vf[i][k][2], vf[i][k][3]);
+      }
+    }
+  }
+}
+
 template <int D, int MT>
 __device__ bool sweep_consume(const PagedDecodeArgs& a, SegWalk sw, const int* len, uint8_t* smem, const SweepSmem& L,
                               const SweepBars& bar, const volatile int* abort, int warp, int lane) {
@@ -319,124 +446,87 @@ __device__ bool sweep_consume(const PagedDecodeArgs& a, SegWalk sw, const int* l
   const int mg = warp / KG, kg = warp - mg * KG;
   const uint32_t ring = smem_u32(smem);
   const float sl2 = a.scale_log2;
-  // this lane's ldmatrix row and chunk parity (keys, values and queries alike)
   const uint32_t lrow = lane & 15, lchk = lane >> 4;
   int st = 0, ph = 0, seg = 0;
+  const auto turn = [&]() {
+    if (++st == a.stages) {
+      st = 0;
+      ph ^= 1;
+    }
+  };
   for (; sw.next(); seg++) {
-    const int total = len[sw.b], own = total - sweep_base(a, total);
-    const int pos0 = own - a.Tq;  // row 0's position, counted from the own part's start
+    SweepState<D, MT> w;
+    const int total = len[sw.b];
+    w.own = total - sweep_base(a, total);
+    w.pos0 = w.own - a.Tq;
     const int qs = seg & 1;
     if (!__all_sync(0xffffffffu, mbar_wait(bar.q_full + qs, (seg >> 1) & 1, abort))) return false;
-    const uint32_t qbase = smem_u32(smem + L.q) + (uint32_t)((qs * a.tiles + mg * MT) * 16) * C::kSpan;
-    uint32_t qf[MT <= 2 ? MT : 1][KS][4];
+    w.qbase = smem_u32(smem + L.q) + (uint32_t)((qs * a.tiles + mg * MT) * 16) * C::kSpan;
     if (MT <= 2) {
 #pragma unroll
-      for (int m = 0; m < MT; m++)
+      for (int m = 0; m < w.kQ; m++)
 #pragma unroll
         for (int k = 0; k < KS; k++)
-          ldsm4(qf[m <= 1 || MT <= 2 ? m : 0][k], qbase + m * 16 * C::kSpan + swz(lrow, 2 * k + lchk, C::kSpan));
+          ldsm4(w.q[m][k], w.qbase + m * 16 * C::kSpan + swz(lrow, 2 * k + lchk, C::kSpan));
       warp_arrive(bar.q_empty + qs);
     }
-    float o[MT][2 * KS][4], mx[MT], ls[MT];
-    int lim[MT];  // last visible position of this lane's row, from the own part's start
 #pragma unroll
     for (int m = 0; m < MT; m++) {
-      mx[m] = -INFINITY;
-      ls[m] = 0.f;
+      w.mx[m] = -INFINITY;
+      w.ls[m] = 0.f;
       const int r = (mg * MT + m) * 8 + (lane >> 2);
-      lim[m] = r < a.R ? pos0 + r / a.G : own - 1;
+      w.lim[m] = r < a.R ? w.pos0 + r / a.G : w.own - 1;
 #pragma unroll
       for (int i = 0; i < 2 * KS; i++)
 #pragma unroll
-        for (int e = 0; e < 4; e++) o[m][i][e] = 0.f;
+        for (int e = 0; e < 4; e++) w.o[m][i][e] = 0.f;
     }
     for (int n = sw.n0; n < sw.n1; n++) {
       if (!__all_sync(0xffffffffu, mbar_wait(bar.full + st, ph, abort))) return false;
-      const uint32_t kb = ring + st * C::kStage, vb = kb + C::kHalf;
-      for (int sl = kg; sl < C::kSlices; sl += KG) {
+      const uint32_t kb = ring + st * C::kStage;
+      if constexpr (kSlicesAtOnce<D, MT> == 2 && C::kSlices == kWarps && MT < 4) {
+        // one slice of a tile for each warp: two tiles at a time
+        const uint32_t at = (uint32_t)kg * 16 * C::kSpan;
+        const int j0 = n * C::kTK + kg * 16, st0 = st;
+        turn();
+        if (n + 1 < sw.n1) {
+          if (!__all_sync(0xffffffffu, mbar_wait(bar.full + st, ph, abort))) return false;
+          const uint32_t kb2 = ring + st * C::kStage;
+          if (j0 < w.own) {
+            const uint32_t k2[2] = {kb + at, kb2 + at}, v2[2] = {k2[0] + C::kHalf, k2[1] + C::kHalf};
+            const int j2[2] = {j0, j0 + C::kTK};
+            sweep_slices<D, MT, 2>(w, k2, v2, j2, sl2, lane);
+          }
+          warp_arrive(bar.empty + st0);
+          warp_arrive(bar.empty + st);
+          turn();
+          n++;
+        } else {
+          if (j0 < w.own) {
+            const uint32_t k1[1] = {kb + at}, v1[1] = {kb + at + C::kHalf};
+            const int j1[1] = {j0};
+            sweep_slices<D, MT, 1>(w, k1, v1, j1, sl2, lane);
+          }
+          warp_arrive(bar.empty + st0);
+        }
+        continue;
+      }
+      constexpr int N = kSlicesAtOnce<D, MT>;
+      for (int sl = kg; sl < C::kSlices; sl += N * KG) {
         const int j0 = n * C::kTK + sl * 16;
-        if (j0 >= own) break;
-        const uint32_t at = (uint32_t)sl * 16 * C::kSpan;
-        uint32_t kf[KS][4], vf[KS][4];
+        if (j0 >= w.own) break;
+        uint32_t kn[N], vn[N];
+        int jn[N];
 #pragma unroll
-        for (int k = 0; k < KS; k++) ldsm4(kf[k], kb + at + swz(lrow, 2 * k + lchk, C::kSpan));
-#pragma unroll
-        for (int k = 0; k < KS; k++) ldsm4t(vf[k], vb + at + swz(lrow, 2 * k + lchk, C::kSpan));
-        const bool edge = j0 + 16 > pos0 + 1;  // some row does not see every key of the slice
-        if (j0 + 16 > own) {
-          // what lies behind the last position may be anything: its weight is 0, but
-          // 0 times a NaN is not
-          const int v0 = own - j0 - (lane & 3) * 2;
-          const uint32_t m0 = (v0 > 0 ? 0xffffu : 0u) | (v0 > 1 ? 0xffff0000u : 0u);
-          const uint32_t m1 = (v0 > 8 ? 0xffffu : 0u) | (v0 > 9 ? 0xffff0000u : 0u);
-#pragma unroll
-          for (int k = 0; k < KS; k++) {
-            vf[k][0] &= m0;
-            vf[k][1] &= m1;
-            vf[k][2] &= m0;
-            vf[k][3] &= m1;
-          }
+        for (int i = 0; i < N; i++) {
+          kn[i] = kb + (uint32_t)(sl + i * KG) * 16 * C::kSpan;
+          vn[i] = kn[i] + C::kHalf;
+          jn[i] = j0 + i * KG * 16;
         }
-#pragma unroll
-        for (int m = 0; m < MT; m++) {
-          float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int k = 0; k < KS; k++) {
-            uint32_t qt[4];
-            if (MT <= 2) {
-#pragma unroll
-              for (int e = 0; e < 4; e++) qt[e] = qf[MT <= 2 ? m : 0][k][e];
-            } else {
-              ldsm4(qt, qbase + m * 16 * C::kSpan + swz(lrow, 2 * k + lchk, C::kSpan));
-            }
-            mma_f16(s0, qt, kf[k][0], kf[k][2]);
-            mma_f16(s1, qt, kf[k][1], kf[k][3]);
-          }
-          // keys (lane & 3) * 2 + {0, 1} and those + 8, row lane / 4: high + low part
-          float x[4] = {s0[0] + s0[2], s0[1] + s0[3], s1[0] + s1[2], s1[1] + s1[3]};
-          if (edge) {
-            const int k0 = j0 + (lane & 3) * 2;
-#pragma unroll
-            for (int e = 0; e < 4; e++)
-              if (k0 + (e & 1) + (e >> 1) * 8 > lim[m]) x[e] = -INFINITY;
-          }
-          float t = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
-          t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
-          t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
-          // O and the sum follow the maximum only when it grew by more than 2^8
-          const bool grow = mx[m] == -INFINITY ? t > -INFINITY : __fmul_rn(t, sl2) > __fmul_rn(mx[m], sl2) + 8.f;
-          if (__any_sync(0xffffffffu, grow)) {
-            const float to = grow ? t : mx[m];
-            const float al = grow && mx[m] != -INFINITY ? ex2(__fmul_rn(mx[m], sl2) - __fmul_rn(t, sl2)) : 1.f;
-            mx[m] = to;
-            ls[m] *= al;
-#pragma unroll
-            for (int i = 0; i < 2 * KS; i++)
-#pragma unroll
-              for (int e = 0; e < 4; e++) o[m][i][e] *= al;
-          }
-          const float mu = mx[m] == -INFINITY ? 0.f : __fmul_rn(mx[m], sl2);
-          float p[4];
-#pragma unroll
-          for (int e = 0; e < 4; e++) p[e] = ex2(fmaf(x[e], sl2, -mu));
-          ls[m] += (p[0] + p[1]) + (p[2] + p[3]);
-          uint32_t pa[4];
-          pa[0] = pack_bf16(p[0], p[1]);
-          pa[2] = pack_bf16(p[2], p[3]);
-          pa[1] = pack_bf16(p[0] - bf_lo(pa[0]), p[1] - bf_hi(pa[0]));
-          pa[3] = pack_bf16(p[2] - bf_lo(pa[2]), p[3] - bf_hi(pa[2]));
-#pragma unroll
-          for (int k = 0; k < KS; k++) {
-            mma_b16(o[m][2 * k], pa, vf[k][0], vf[k][1]);
-            mma_b16(o[m][2 * k + 1], pa, vf[k][2], vf[k][3]);
-          }
-        }
+        sweep_slices<D, MT, N>(w, kn, vn, jn, sl2, lane);
       }
       warp_arrive(bar.empty + st);
-      if (++st == a.stages) {
-        st = 0;
-        ph ^= 1;
-      }
+      turn();
     }
     if (MT > 2) warp_arrive(bar.q_empty + qs);
     // the warps' parts go to shared memory, where a finishing warp joins them
@@ -446,15 +536,15 @@ __device__ bool sweep_consume(const PagedDecodeArgs& a, SegWalk sw, const int* l
     float2* ml = reinterpret_cast<float2*>(smem + L.ml) + buf * kWarps * MT * 8;
 #pragma unroll
     for (int m = 0; m < MT; m++) {
-      float l = ls[m];
+      float l = w.ls[m];
       l += __shfl_xor_sync(0xffffffffu, l, 1);
       l += __shfl_xor_sync(0xffffffffu, l, 2);
       const int row = (warp * MT + m) * 8 + (lane >> 2);
-      if ((lane & 3) == 0) ml[row] = make_float2(mx[m] == -INFINITY ? -INFINITY : __fmul_rn(mx[m], sl2), l);
+      if ((lane & 3) == 0) ml[row] = make_float2(w.mx[m] == -INFINITY ? -INFINITY : __fmul_rn(w.mx[m], sl2), l);
 #pragma unroll
       for (int i = 0; i < 2 * KS; i++)
         *reinterpret_cast<float2*>(scratch + row * D + i * 8 + (lane & 3) * 2) =
-            make_float2(o[m][i][0] + o[m][i][2], o[m][i][1] + o[m][i][3]);
+            make_float2(w.o[m][i][0] + w.o[m][i][2], w.o[m][i][1] + w.o[m][i][3]);
     }
     warp_arrive(bar.parts_full + buf);
   }
@@ -558,7 +648,7 @@ __device__ bool sweep_finish(const PagedDecodeArgs& a, SegWalk sw, const Tiles& 
 template <int D, int MT>
 __device__ bool sweep_join(const PagedDecodeArgs& a, const Tiles& tl, const SweepPlan& plan, const SweepBars& bar,
                            const volatile int* todo, const volatile int* abort, int tid) {
-  constexpr int kThreads = kWarps * 32, kSplit = 4, kAhead = 5;
+  constexpr int kThreads = kWarps * 32, kSplit = 4, kAhead = 10;
   if (!__all_sync(0xffffffffu, mbar_wait(bar.fin, 0, abort))) return false;
   for (int k = 0; k < 2; k++) {
     const int sh = todo[k];
@@ -573,10 +663,6 @@ __device__ bool sweep_join(const PagedDecodeArgs& a, const Tiles& tl, const Swee
       const int i = min(i0 + tid / kSplit, items - 1);
       const int r = i / (D / 4), q = i % (D / 4);
       const auto at = [&](int c) { return (size_t)(c == c0 ? first : 2 * c) * a.R + r; };
-      float top = -INFINITY;
-      for (int c = c0 + sub; c <= c1; c += kSplit) top = fmaxf(top, __ldcg(a.part_ml + at(c)).x);
-#pragma unroll
-      for (int m = 1; m < kSplit; m <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
       RowSum x;
       for (int c = c0 + sub; c <= c1; c += kSplit * kAhead) {
         float2 z[kAhead];
@@ -590,9 +676,17 @@ __device__ bool sweep_join(const PagedDecodeArgs& a, const Tiles& tl, const Swee
             u[e] = __ldcg(reinterpret_cast<const float4*>(a.part_o + at(c + e * kSplit) * D) + q);
           }
         }
+        float top = x.M;
+#pragma unroll
+        for (int e = 0; e < kAhead; e++) top = fmaxf(top, z[e].x);
+        x.raise(top);
 #pragma unroll
         for (int e = 0; e < kAhead; e++) x.add(top, z[e], u[e]);
       }
+      float top = x.M;
+#pragma unroll
+      for (int m = 1; m < kSplit; m <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
+      x.raise(top);
 #pragma unroll
       for (int m = 1; m < kSplit; m <<= 1) {
         x.S += __shfl_xor_sync(0xffffffffu, x.S, m);
@@ -700,7 +794,7 @@ __global__ void __launch_bounds__(kSweepThreads, 1) k_paged_sweep(const __grid_c
     SweepPlan p;
     p.W = cum[a.B] * a.Hkv;
     p.G = min(p.W, (int)gridDim.x);
-    p.base = p.W / p.G;
+    p.base = p.W == p.G ? 1 : (int)fdiv((uint32_t)p.W, a.div_grid);
     p.rem = p.W - p.base * p.G;
     // tiles of this block and the next one's first, with the sequences they are in
     const int c = min((int)blockIdx.x, p.G), x0 = min(c * p.base + min(c, p.rem), p.W - 1);
@@ -713,8 +807,10 @@ __global__ void __launch_bounds__(kSweepThreads, 1) k_paged_sweep(const __grid_c
     if (lane == 0) {
       if (p.b == a.B) p.b--;  // nothing left
       const int nt = cum[p.b + 1] - cum[p.b], off = p.w - cum[p.b] * a.Hkv;
-      p.g = off / nt;
+      p.g = (int)__fdividef((float)off, (float)nt);  // within one of off / nt
       p.n0 = off - p.g * nt;
+      while (p.n0 < 0) p.g--, p.n0 += nt;
+      while (p.n0 >= nt) p.g++, p.n0 -= nt;
       splan->W = p.W;
       splan->G = p.G;
       splan->base = p.base;
@@ -869,6 +965,7 @@ cudaError_t launch_sweep_t(const PagedDecodeArgs& a, int nsm, cudaStream_t s) {
   const int bytes = sweep_smem(D, b.stages, b.tiles, MT, b.B).total;
   if (bytes > kSmemMax) return cudaErrorInvalidValue;
   const int grid = nsm < kPagedMaxBlocks ? nsm : kPagedMaxBlocks;
+  b.div_grid = make_fastdiv((uint32_t)grid);
   if (b.base == 0 && b.own_counters) {  // they are 0 before and after every call
     k_paged_sweep<D, MT><<<grid, kSweepThreads, (size_t)bytes, s>>>(b);
     return cudaGetLastError();
