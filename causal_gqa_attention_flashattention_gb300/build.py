@@ -15,7 +15,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libneattn.so")
 SOURCES = ["api.cu", "attn_fwd.cu", "attn_bwd.cu", "attn_decode.cu", "qkv_proj.cu", "qk_norm.cu", "paged.cu",
            "paged_prefix.cu"]
-HEADERS = ["ptx.cuh", "rope.cuh", "internal.h", "paged.cuh"]
+HEADERS = ["ptx.cuh", "rope.cuh", "internal.h", "paged.cuh", "paged_sweep.cuh", "paged_prefix.cuh"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr"]

@@ -550,9 +550,6 @@ int check_paged(int B, int Hq, int Hkv, int D, int page_size, int num_pages, int
 int check_paged_tiles(int B, int Hkv, int page_size, int max_pages) {
   return (long long)B * Hkv * (((long long)max_pages * page_size + 127) / 128) < (1LL << 30) ? NE_OK : NE_ERR_UNSUPPORTED;
 }
-constexpr int kPrefixMinTiles = 4;  // key tiles of a prefix block, where there are not enough for all
-// Whether a shared prefix goes through the prefix kernel: see ne_attn_decode_paged.
-bool prefix_shared(int B, int Hkv, int prefix_len) { return true; }
 int check_decode_paged_rows(int B, int Tq, int Hq, int Hkv, int D) {
   if ((long long)(Hq / Hkv) * Tq > kTile) return NE_ERR_UNSUPPORTED;
   if (((long long)B * Tq * Hq + (long long)Hkv * kTile) * D >= (1LL << 31)) return NE_ERR_UNSUPPORTED;
@@ -560,10 +557,9 @@ int check_decode_paged_rows(int B, int Tq, int Hq, int Hkv, int D) {
 }
 
 // Decode workspace: the split segments' O, their (maximum, sum), the counters.
-// With a shared prefix then its packed queries, its segments' O and (maximum, sum), and the
-// same joined.
+// With a shared prefix then its segments' O and (maximum, sum), and the sequences' own.
 struct PagedWs {
-  size_t part_o, part_ml, done, pq, pp_o, pp_ml, pj_o, pj_ml, total;
+  size_t part_o, part_ml, done, pp_o, pp_ml, po, pml, cut, total;
 };
 int prefix_tiles(int B, int R) { return (int)(((long long)B * R + kTile - 1) / kTile); }
 PagedWs paged_ws(int B, int R, int Hkv, int D, bool prefix) {
@@ -572,14 +568,14 @@ PagedWs paged_ws(int B, int R, int Hkv, int D, bool prefix) {
   w.part_ml = ws_up((size_t)2 * kPagedMaxBlocks * R * D * 4);
   w.done = w.part_ml + ws_up((size_t)2 * kPagedMaxBlocks * R * 8);
   w.total = w.done + ws_up((size_t)kPagedMaxBlocks * 4);
-  w.pq = w.pp_o = w.pp_ml = w.pj_o = w.pj_ml = w.total;
+  w.pp_o = w.pp_ml = w.po = w.pml = w.cut = w.total;
   if (prefix) {
     const size_t tiles = prefix_tiles(B, R), segs = kPagedMaxBlocks + (size_t)Hkv * ((tiles + 1) / 2);
-    w.pp_o = w.pq + ws_up((size_t)Hkv * tiles * kTile * D * 2);
     w.pp_ml = w.pp_o + ws_up(segs * 2 * kTile * D * 4);
-    w.pj_o = w.pp_ml + ws_up(segs * 2 * kTile * 8);
-    w.pj_ml = w.pj_o + ws_up((size_t)Hkv * tiles * kTile * D * 4);
-    w.total = w.pj_ml + ws_up((size_t)Hkv * tiles * kTile * 8);
+    w.po = w.pp_ml + ws_up(segs * 2 * kTile * 8);
+    w.pml = w.po + ws_up((size_t)Hkv * tiles * kTile * D * 4);
+    w.cut = w.pml + ws_up((size_t)Hkv * tiles * kTile * 8);
+    w.total = w.cut + 256;
   }
   return w;
 }
@@ -1545,24 +1541,19 @@ int ne_attn_decode_paged(const void* q, const void* q_w, const void* k_pages, co
   if ((st = make_map_pages(&a.map_v, v_pages, num_pages, Hkv, page_size, D, page_stride, rows,
                            CU_TENSOR_MAP_DATA_TYPE_BFLOAT16)) != NE_OK)
     return st;
-  if (prefix_len > 0 && prefix_shared(B, Hkv, prefix_len)) {
+  if (prefix_len > 0 && nsm > 1) {
     a.base = prefix_len;
     PrefixArgs& p = a.pre;
-    p.q = reinterpret_cast<__half*>(ws + w.pq);
     p.part_o = reinterpret_cast<float*>(ws + w.pp_o);
     p.part_ml = reinterpret_cast<float2*>(ws + w.pp_ml);
-    p.o = reinterpret_cast<float*>(ws + w.pj_o);
-    p.ml = reinterpret_cast<float2*>(ws + w.pj_ml);
+    p.o = reinterpret_cast<float*>(ws + w.po);
+    p.ml = reinterpret_cast<float2*>(ws + w.pml);
+    p.cut = reinterpret_cast<int*>(ws + w.cut);
     p.tiles = prefix_tiles(B, a.R);
     p.pairs = (p.tiles + 1) / 2;
     p.ntk = (prefix_len + kTile - 1) / kTile;
     p.W = Hkv * p.pairs * p.ntk;
-    const int most = nsm < kPagedMaxBlocks ? nsm : kPagedMaxBlocks;
-    const int want = (p.W + kPrefixMinTiles - 1) / kPrefixMinTiles;
-    p.blocks = want < most ? want : most;
     const int prows = page_size < kTile ? page_size : kTile;
-    if ((st = make_map_bthd(&a.map_q, p.q, 1, Hkv * p.tiles * kTile, 1, D, CU_TENSOR_MAP_DATA_TYPE_FLOAT16)) != NE_OK)
-      return st;
     if ((st = make_map_pages(&a.map_pk, k_pages, num_pages, Hkv, page_size, D, page_stride, prows,
                              CU_TENSOR_MAP_DATA_TYPE_FLOAT16)) != NE_OK)
       return st;
@@ -1570,7 +1561,7 @@ int ne_attn_decode_paged(const void* q, const void* q_w, const void* k_pages, co
                              CU_TENSOR_MAP_DATA_TYPE_BFLOAT16)) != NE_OK)
       return st;
     ProfScope prof(NE_ATTN_KERNEL_DECODE_PREFIX, s);
-    if (launch_prefix(a, s) != cudaSuccess) return NE_ERR_CUDA;
+    return launch_decode_prefix(a, mt, nsm, s) == cudaSuccess ? NE_OK : NE_ERR_CUDA;
   }
   ProfScope prof(NE_ATTN_KERNEL_DECODE_PAGED, s);
   return launch_decode_paged(a, mt, nsm, s) == cudaSuccess ? NE_OK : NE_ERR_CUDA;

@@ -221,13 +221,13 @@ constexpr int kPagedMaxBlocks = 160;  // blocks of the sweep: bounds its partial
 // The shared prefix's part of it (see paged_prefix.cu): key tiles of 128 positions over every
 // (key/value head, pair of 128-row tiles), in one line, block c's stretch [c W / blocks, ..).
 struct PrefixArgs {
-  __half* q;        // [Hkv, tiles * 128, D] packed rotated queries (workspace)
   float* part_o;    // unnormalised O of segment (block c, (head, pair) s), unit u: part prefix_part(c + s, u),
-                    // float4 prefix_quad of it
+                    // float4 prefix_quad of it (workspace)
   float2* part_ml;  // [part, 128] maximum (log2 units) and sum of the rows
-  float* o;         // [Hkv, tiles * 128, D] the segments joined, still unnormalised (workspace)
+  float* o;         // [Hkv, tiles * 128, D] the sequences' own parts, unnormalised (workspace)
   float2* ml;       // [Hkv, tiles * 128]
-  int tiles, pairs, ntk, W, blocks;
+  int* cut;         // blocks that took the prefix (workspace)
+  int tiles, pairs, ntk, W;
 };
 #ifdef __CUDACC__
 __device__ __forceinline__ size_t prefix_part(int segment, int unit) { return (size_t)segment * 2 + unit; }
@@ -237,15 +237,21 @@ template <int D>
 __device__ __forceinline__ size_t prefix_quad(size_t part, int row, int q) {
   return ((part * (kTile / 32) + row / 32) * (D / 4) + q) * 32 + row % 32;
 }
-// The block whose stretch tile x lies in.
-__host__ __device__ inline int prefix_owner(const PrefixArgs& p, int x) {
-  return (int)(((x + 1LL) * p.blocks - 1) / p.W);
-}
+// The prefix's W tiles cut among its blocks: the first rem have base + 1.
+struct PrefixCut {
+  int W, base, rem;
+  __device__ PrefixCut(int W_, int blocks) : W(W_), base(W_ / blocks), rem(W_ - base * blocks) {}
+  __device__ int start(int c) const { return c * base + min(c, rem); }
+  __device__ int owner(int x) const {  // the block with tile x
+    const int big = rem * (base + 1);
+    return x < big ? x / (base + 1) : rem + (x - big) / base;
+  }
+};
 #endif
 
 struct PagedDecodeArgs {
   CUtensorMap map_k, map_v;     // pools {D, page, Hkv, num_pages}, box D x min(page, tile) rows
-  CUtensorMap map_q, map_pk, map_pv;  // prefix kernel: packed queries, the pools with its own tile
+  CUtensorMap map_pk, map_pv;   // the same with the prefix's tile of 128 positions
   PrefixArgs pre;
   const __nv_bfloat16 *q, *qw;  // [B, Tq, Hq, D], positions q_stride values apart; qw [D] or null
   const int *table, *len, *prefix_table;
@@ -290,9 +296,9 @@ cudaError_t launch_qk_norm(const QkNormArgs& a, int D, int nsm, cudaStream_t s);
 int qk_norm_bwd_blocks(int B, int T, int hg, int D, int nsm);
 cudaError_t launch_qk_norm_bwd(const QkNormBwdArgs& a, int D, bool f32, int blocks, cudaStream_t s);
 cudaError_t launch_kv_append_paged(const PagedAppendArgs& a, int D, cudaStream_t s);
-cudaError_t launch_prefix(const PagedDecodeArgs& a, cudaStream_t s);
 void paged_rows(int R, int* mt, int* tiles, int* mg);
 cudaError_t launch_decode_paged(const PagedDecodeArgs& a, int mt, int nsm, cudaStream_t s);
+cudaError_t launch_decode_prefix(const PagedDecodeArgs& a, int mt, int nsm, cudaStream_t s);
 
 cudaError_t launch_qkv_prep(const QkvArgs& a, cudaStream_t s);
 cudaError_t launch_qkv_gemm(const QkvArgs& a, int BN, int grid, cudaStream_t s);

@@ -12,15 +12,10 @@
 #include <cuda_fp16.h>
 
 #include "internal.h"
-#include "paged.cuh"
-#include "ptx.cuh"
-#include "rope.cuh"
+#include "paged_sweep.cuh"
 
 namespace ne {
 namespace {
-
-constexpr float kLn2 = 0.69314718055994531f;
-constexpr int kSmemMax = 232448;
 
 // ====================================================================== append
 // New row n belongs to the sequence s with cu[s] <= n < cu[s + 1] (rows at or
@@ -114,870 +109,6 @@ __global__ void __launch_bounds__(128) k_kv_append_paged(const PagedAppendArgs a
   reinterpret_cast<uint4*>(a.vp + dst)[c] = vv;
 }
 
-// ====================================================================== attention
-// Work: the key tiles (kTK positions) of every (sequence, key/value head), laid end
-// to end in that order, cut into one equal stretch for each block.  Every block
-// works the stretches out for itself from the lengths, so nothing is planned on the
-// host and a captured graph follows the lengths it finds.  A segment, the part of
-// one (sequence, head) in one block's stretch, that is not the whole of it leaves
-// its unnormalised O, running maximum and sum; the block that finishes a (sequence,
-// head) last adds the segments in order: the result does not depend on which one.
-//
-// Rows: the R = Tq * G queries of a key/value head (row t * G + g).  A matrix tile of
-// 16 rows holds 8 of them twice: rows 0-7 the high fp16 part of the rotated query,
-// rows 8-15 its remainder, so that one m16n8k16 product gives both parts of a score
-// in one thread; the same goes for the weights' two bf16 parts in P V.  With at most
-// 8 rows (one token of most models) that precision is free: the tile has 16 rows
-// anyway.  mma.sync and not tcgen05: with so few rows the sweep is bound by the bytes
-// of the cache, and a warp that owns its 16 keys end to end (scores, weights, P V in
-// registers) needs no hand-off between warps per tile.
-template <int D>
-struct Sweep {
-  static constexpr int kTK = D == 64 ? 128 : 256;  // positions of a tile
-  static constexpr uint32_t kSpan = D * 2;
-  static constexpr int kHalf = kTK * (int)kSpan;   // bytes of a tile's keys (as many of values)
-  static constexpr int kStage = 2 * kHalf;
-  static constexpr int kSlices = kTK / 16;
-  static constexpr int kMaxStages = 6;
-};
-// Eight consumer warps, then a warpgroup of the producer, the queries and two finishing warps.
-// (Sixteen consumers in two groups on alternate tiles measured slower: a short context 8.4 us
-// against 7.4, 16 contexts around 8192 positions 31.9 against 31.4.)
-constexpr int kWarps = 8;
-constexpr int kSweepThreads = (kWarps + 4) * 32;
-constexpr int kBarBytes = 384;
-constexpr int kWholeTiles = 8;  // a (sequence, head) of at most this many tiles is never split
-
-// Buffers for the warps' parts of a finished segment, each with a finishing warp of its own.
-constexpr int sweep_bufs(int mt) { return mt < 4 ? 2 : 1; }
-
-// Shared memory behind the ring, in bytes (tiles: packed row tiles, mt: of one warp).
-struct SweepSmem {
-  int q, scratch, ml, cum, len, bars, total;
-};
-__host__ __device__ constexpr SweepSmem sweep_smem(int D, int stages, int tiles, int mt, int B) {
-  SweepSmem m = {};
-  const int rows = sweep_bufs(mt) * kWarps * mt * 8;
-  m.q = stages * 32768;
-  m.scratch = m.q + 2 * tiles * 16 * D * 2;
-  m.ml = m.scratch + rows * D * 4;
-  m.cum = m.ml + rows * 8;
-  m.len = m.cum + (B + 1) * 4;
-  m.bars = (m.len + B * 4 + 15) / 16 * 16;
-  m.total = m.bars + kBarBytes + 1024;
-  return m;
-}
-
-__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ void mma_b16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-// The division of the W tiles among G blocks, and one block's stretch [w, end).
-struct SweepPlan {
-  int W, G, base, rem;  // the first rem blocks have base + 1 tiles, the others base
-  int w, end;           // the block's tiles, boundaries moved as below
-  int b, g, n0;         // its first tile: sequence, head, key tile
-};
-struct Tiles {
-  const int* cum;  // shared memory: tiles before sequence b (one head)
-  int B, Hkv;
-  // the same by a whole warp for one x: 32 probes at a time
-  __device__ int find_warp(int x, int lane) const {
-    int lo = 0, hi = B;
-    while (hi - lo > 1) {
-      const int step = (hi - lo + 31) >> 5, i = lo + lane * step;
-      const unsigned le = __ballot_sync(0xffffffffu, i < hi && cum[i] * Hkv <= x);
-      lo += (31 - __clz((int)le)) * step;
-      hi = min(hi, lo + step);
-    }
-    return lo;
-  }
-  __device__ int find(int x) const {  // last b with Hkv * cum[b] <= x
-    int lo = 0, hi = B;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) / 2;
-      if (cum[mid] * Hkv <= x)
-        lo = mid;
-      else
-        hi = mid;
-    }
-    return lo;
-  }
-  // A block's stretch starts at tile x = c base + min(c, rem), moved to the nearer end of a
-  // (sequence, head) of at most kWholeTiles tiles it would cut: joining a cut one costs about
-  // 3 us at the end, as much as five tiles, moving the boundary at most half the tiles.
-  // Inside longer ones the boundaries stay, so owner() needs the unmoved starts only.
-  __device__ int start(const SweepPlan& p, int c) const {
-    const int x = c * p.base + min(c, p.rem);
-    return x >= p.W ? p.W : moved(x, find(x));
-  }
-  __device__ int moved(int x, int i) const {  // x in sequence i
-    const int n = cum[i + 1] - cum[i];
-    if (n > kWholeTiles) return x;
-    const int off = (x - cum[i] * Hkv) % n;
-    return 2 * off < n ? x - off : x - off + n;
-  }
-  // The block with tile x of a (sequence, head) that is cut.
-  __device__ int owner(const SweepPlan& p, int x) const {
-    const int big = p.rem * (p.base + 1);
-    return x < big ? x / (p.base + 1) : p.rem + (x - big) / p.base;
-  }
-};
-// Walks a block's stretch segment by segment.
-struct SegWalk {
-  const int* cum;
-  int Hkv, w, end;
-  int b, g, n0, n1, nt;  // the segment: key tiles [n0, n1) of nt
-  __device__ void init(const int* c, int hkv, const volatile SweepPlan* p) {
-    cum = c;
-    Hkv = hkv;
-    w = p->w;
-    end = p->end;
-    b = p->b;
-    g = p->g;
-    n0 = p->n0;
-    nt = -1;
-  }
-  __device__ bool next() {
-    if (w >= end) return false;
-    if (nt >= 0) {  // the segment before ended with its (sequence, head)
-      n0 = 0;
-      if (++g == Hkv) {
-        g = 0;
-        b++;
-      }
-    }
-    nt = cum[b + 1] - cum[b];
-    n1 = min(nt, n0 + (end - w));
-    w += n1 - n0;
-    return true;
-  }
-};
-
-// Row r of (sequence b, head g), columns 4 q .. 4 q + 3: normalise and write.
-template <int D>
-__device__ __forceinline__ void write_row(const PagedDecodeArgs& a, int b, int g, int r, int q, float4 v, float M, float L) {
-  const int t = r / a.G, h = g * a.G + (r - t * a.G);
-  const float inv = L > 0.f ? 1.f / L : 0.f;
-  const size_t at = (((size_t)b * a.Tq + t) * a.Hq + h) * D + 4 * q;
-  v = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
-  if (a.o_fp32)
-    *reinterpret_cast<float4*>(static_cast<float*>(a.o) + at) = v;
-  else
-    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.o) + at) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
-  if (q == 0 && a.lse) a.lse[((size_t)b * a.Hq + h) * a.Tq + t] = L > 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
-}
-
-// Positions of a sequence that the sweep leaves to the prefix kernel: the whole shared
-// prefix if the first query sees all of it, else none.
-__device__ __forceinline__ int sweep_base(const PagedDecodeArgs& a, int len) {
-  return a.base > 0 && len - a.Tq + 1 >= a.base ? a.base : 0;
-}
-
-// A row's parts (maximum z in log2 units, sum, O), some lanes each with a few: the maximum of
-// all, then sums of the rescaled parts (0 where a part's sum is 0: the row saw none of its keys).
-struct RowSum {
-  float M = -INFINITY, S = 0.f;
-  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-  // to the maximum `top`, which is at least M
-  __device__ void raise(float top) {
-    const float f = S == 0.f ? 0.f : ex2(M - top);
-    M = top;
-    S *= f;
-    v = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
-  }
-  __device__ void add(float top, float2 z, const float4& u) {
-    const float f = z.y == 0.f ? 0.f : ex2(z.x - top);
-    S = fmaf(f, z.y, S);
-    v = make_float4(fmaf(f, u.x, v.x), fmaf(f, u.y, v.y), fmaf(f, u.z, v.z), fmaf(f, u.w, v.w));
-  }
-};
-
-struct SweepBars {
-  uint64_t *full, *empty, *q_full, *q_empty, *parts_full, *parts_empty, *fin;
-};
-
-// What a consumer warp holds of a segment: MT row tiles' queries (in registers for at most two
-// of them, else read from shared memory as they are used), O, running maximum and sum.
-template <int D, int MT>
-struct SweepState {
-  static constexpr int KS = D / 16, kQ = MT <= 2 ? MT : 1;
-  uint32_t q[kQ][KS][4], qbase;
-  float o[MT][2 * KS][4], mx[MT], ls[MT];
-  int lim[MT];      // last visible position of this lane's row, from the own part's start
-  int own, pos0;    // positions of the own part; row 0's position
-};
-// Slices of 16 keys that a warp takes together: two where the registers allow it, which gives
-// its chain of dependent steps (scores, maximum, weights, P V) something to overlap with.
-template <int D, int MT>
-constexpr int kSlicesAtOnce = MT * D <= 128 ? 2 : 1;
-
-// N slices (keys at kb, values at vb, first position j0) into the state.
-template <int D, int MT, int N>
-__device__ __forceinline__ void sweep_slices(SweepState<D, MT>& w, const uint32_t (&kb)[N], const uint32_t (&vb)[N],
-                                             const int (&j0)[N], float sl2, int lane) {
-  constexpr int KS = D / 16;
-  constexpr uint32_t kSpan = Sweep<D>::kSpan;
-  // this lane's ldmatrix row and chunk parity (keys, values and queries alike)
-  const uint32_t lrow = lane & 15, lchk = lane >> 4;
-  uint32_t kf[N][KS][4], vf[N][KS][4];
-#pragma unroll
-  for (int i = 0; i < N; i++)
-#pragma unroll
-    for (int k = 0; k < KS; k++) ldsm4(kf[i][k], kb[i] + swz(lrow, 2 * k + lchk, kSpan));
-#pragma unroll
-  for (int i = 0; i < N; i++) {
-#pragma unroll
-    for (int k = 0; k < KS; k++) ldsm4t(vf[i][k], vb[i] + swz(lrow, 2 * k + lchk, kSpan));
-    if (j0[i] + 16 > w.own) {
-      // what lies behind the last position may be anything: its weight is 0, but 0 times a
-      // NaN is not
-      const int v0 = w.own - j0[i] - (lane & 3) * 2;
-      const uint32_t m0 = (v0 > 0 ? 0xffffu : 0u) | (v0 > 1 ? 0xffff0000u : 0u);
-      const uint32_t m1 = (v0 > 8 ? 0xffffu : 0u) | (v0 > 9 ? 0xffff0000u : 0u);
-#pragma unroll
-      for (int k = 0; k < KS; k++) {
-        vf[i][k][0] &= m0;
-        vf[i][k][1] &= m1;
-        vf[i][k][2] &= m0;
-        vf[i][k][3] &= m1;
-      }
-    }
-  }
-#pragma unroll
-  for (int m = 0; m < MT; m++) {
-    float sa[N][4], sb[N][4];
-#pragma unroll
-    for (int i = 0; i < N; i++)
-#pragma unroll
-      for (int e = 0; e < 4; e++) sa[i][e] = sb[i][e] = 0.f;
-#pragma unroll
-    for (int k = 0; k < KS; k++) {
-      uint32_t qt[4];
-      if (MT <= 2) {
-#pragma unroll
-        for (int e = 0; e < 4; e++) qt[e] = w.q[MT <= 2 ? m : 0][k][e];
-      } else {
-        ldsm4(qt, w.qbase + m * 16 * kSpan + swz(lrow, 2 * k + lchk, kSpan));
-      }
-#pragma unroll
-      for (int i = 0; i < N; i++) {
-        mma_f16(sa[i], qt, kf[i][k][0], kf[i][k][2]);
-        mma_f16(sb[i], qt, kf[i][k][1], kf[i][k][3]);
-      }
-    }
-    // keys (lane & 3) * 2 + {0, 1} and those + 8, row lane / 4: high + low part
-    float x[N][4], t = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < N; i++) {
-      x[i][0] = sa[i][0] + sa[i][2];
-      x[i][1] = sa[i][1] + sa[i][3];
-      x[i][2] = sb[i][0] + sb[i][2];
-      x[i][3] = sb[i][1] + sb[i][3];
-      if (j0[i] + 16 > w.pos0 + 1) {  // some row does not see every key of the slice
-        const int k0 = j0[i] + (lane & 3) * 2;
-#pragma unroll
-        for (int e = 0; e < 4; e++)
-          if (k0 + (e & 1) + (e >> 1) * 8 > w.lim[m]) x[i][e] = -INFINITY;
-      }
-      t = fmaxf(t, fmaxf(fmaxf(x[i][0], x[i][1]), fmaxf(x[i][2], x[i][3])));
-    }
-    t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
-    t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
-    // O and the sum follow the maximum only when it grew by more than 2^8
-    const float mx = w.mx[m];
-    const bool grow = mx == -INFINITY ? t > -INFINITY : __fmul_rn(t, sl2) > __fmul_rn(mx, sl2) + 8.f;
-    if (__any_sync(0xffffffffu, grow)) {
-      const float al = grow && mx != -INFINITY ? ex2(__fmul_rn(mx, sl2) - __fmul_rn(t, sl2)) : 1.f;
-      w.mx[m] = grow ? t : mx;
-      w.ls[m] *= al;
-#pragma unroll
-      for (int i = 0; i < 2 * KS; i++)
-#pragma unroll
-        for (int e = 0; e < 4; e++) w.o[m][i][e] *= al;
-    }
-    const float mu = w.mx[m] == -INFINITY ? 0.f : __fmul_rn(w.mx[m], sl2);
-#pragma unroll
-    for (int i = 0; i < N; i++) {
-      float p[4];
-#pragma unroll
-      for (int e = 0; e < 4; e++) p[e] = ex2(fmaf(x[i][e], sl2, -mu));
-      w.ls[m] += (p[0] + p[1]) + (p[2] + p[3]);
-      uint32_t pa[4];
-      pa[0] = pack_bf16(p[0], p[1]);
-      pa[2] = pack_bf16(p[2], p[3]);
-      pa[1] = pack_bf16(p[0] - bf_lo(pa[0]), p[1] - bf_hi(pa[0]));
-      pa[3] = pack_bf16(p[2] - bf_lo(pa[2]), p[3] - bf_hi(pa[2]));
-#pragma unroll
-      for (int k = 0; k < KS; k++) {
-        mma_b16(w.o[m][2 * k], pa, vf[i][k][0], vf[i][k][1]);
-        mma_b16(w.o[m][2 * k + 1], pa, vf[i][k][2], vf[i][k][3]);
-      }
-    }
-  }
-}
-
-template <int D, int MT>
-__device__ bool sweep_consume(const PagedDecodeArgs& a, SegWalk sw, const int* len, uint8_t* smem, const SweepSmem& L,
-                              const SweepBars& bar, const volatile int* abort, int warp, int lane) {
-  using C = Sweep<D>;
-  constexpr int KS = D / 16;
-  constexpr int kBufs = sweep_bufs(MT);
-  const int KG = MT < 4 ? kWarps : kWarps / a.MG;  // warps over a tile's keys; the rest share the row tiles out
-  const int mg = warp / KG, kg = warp - mg * KG;
-  const uint32_t ring = smem_u32(smem);
-  const float sl2 = a.scale_log2;
-  const uint32_t lrow = lane & 15, lchk = lane >> 4;
-  int st = 0, ph = 0, seg = 0;
-  const auto turn = [&]() {
-    if (++st == a.stages) {
-      st = 0;
-      ph ^= 1;
-    }
-  };
-  for (; sw.next(); seg++) {
-    SweepState<D, MT> w;
-    const int total = len[sw.b];
-    w.own = total - sweep_base(a, total);
-    w.pos0 = w.own - a.Tq;
-    const int qs = seg & 1;
-    if (!__all_sync(0xffffffffu, mbar_wait(bar.q_full + qs, (seg >> 1) & 1, abort))) return false;
-    w.qbase = smem_u32(smem + L.q) + (uint32_t)((qs * a.tiles + mg * MT) * 16) * C::kSpan;
-    if (MT <= 2) {
-#pragma unroll
-      for (int m = 0; m < w.kQ; m++)
-#pragma unroll
-        for (int k = 0; k < KS; k++)
-          ldsm4(w.q[m][k], w.qbase + m * 16 * C::kSpan + swz(lrow, 2 * k + lchk, C::kSpan));
-      warp_arrive(bar.q_empty + qs);
-    }
-#pragma unroll
-    for (int m = 0; m < MT; m++) {
-      w.mx[m] = -INFINITY;
-      w.ls[m] = 0.f;
-      const int r = (mg * MT + m) * 8 + (lane >> 2);
-      w.lim[m] = r < a.R ? w.pos0 + r / a.G : w.own - 1;
-#pragma unroll
-      for (int i = 0; i < 2 * KS; i++)
-#pragma unroll
-        for (int e = 0; e < 4; e++) w.o[m][i][e] = 0.f;
-    }
-    for (int n = sw.n0; n < sw.n1; n++) {
-      if (!__all_sync(0xffffffffu, mbar_wait(bar.full + st, ph, abort))) return false;
-      const uint32_t kb = ring + st * C::kStage;
-      if constexpr (kSlicesAtOnce<D, MT> == 2 && C::kSlices == kWarps && MT < 4) {
-        // one slice of a tile for each warp: two tiles at a time
-        const uint32_t at = (uint32_t)kg * 16 * C::kSpan;
-        const int j0 = n * C::kTK + kg * 16, st0 = st;
-        turn();
-        if (n + 1 < sw.n1) {
-          if (!__all_sync(0xffffffffu, mbar_wait(bar.full + st, ph, abort))) return false;
-          const uint32_t kb2 = ring + st * C::kStage;
-          if (j0 < w.own) {
-            const uint32_t k2[2] = {kb + at, kb2 + at}, v2[2] = {k2[0] + C::kHalf, k2[1] + C::kHalf};
-            const int j2[2] = {j0, j0 + C::kTK};
-            sweep_slices<D, MT, 2>(w, k2, v2, j2, sl2, lane);
-          }
-          warp_arrive(bar.empty + st0);
-          warp_arrive(bar.empty + st);
-          turn();
-          n++;
-        } else {
-          if (j0 < w.own) {
-            const uint32_t k1[1] = {kb + at}, v1[1] = {kb + at + C::kHalf};
-            const int j1[1] = {j0};
-            sweep_slices<D, MT, 1>(w, k1, v1, j1, sl2, lane);
-          }
-          warp_arrive(bar.empty + st0);
-        }
-        continue;
-      }
-      constexpr int N = kSlicesAtOnce<D, MT>;
-      for (int sl = kg; sl < C::kSlices; sl += N * KG) {
-        const int j0 = n * C::kTK + sl * 16;
-        if (j0 >= w.own) break;
-        uint32_t kn[N], vn[N];
-        int jn[N];
-#pragma unroll
-        for (int i = 0; i < N; i++) {
-          kn[i] = kb + (uint32_t)(sl + i * KG) * 16 * C::kSpan;
-          vn[i] = kn[i] + C::kHalf;
-          jn[i] = j0 + i * KG * 16;
-        }
-        sweep_slices<D, MT, N>(w, kn, vn, jn, sl2, lane);
-      }
-      warp_arrive(bar.empty + st);
-      turn();
-    }
-    if (MT > 2) warp_arrive(bar.q_empty + qs);
-    // the warps' parts go to shared memory, where a finishing warp joins them
-    const int buf = seg % kBufs, use = seg / kBufs;
-    if (use > 0 && !__all_sync(0xffffffffu, mbar_wait(bar.parts_empty + buf, (use - 1) & 1, abort))) return false;
-    float* scratch = reinterpret_cast<float*>(smem + L.scratch) + buf * kWarps * MT * 8 * D;
-    float2* ml = reinterpret_cast<float2*>(smem + L.ml) + buf * kWarps * MT * 8;
-#pragma unroll
-    for (int m = 0; m < MT; m++) {
-      float l = w.ls[m];
-      l += __shfl_xor_sync(0xffffffffu, l, 1);
-      l += __shfl_xor_sync(0xffffffffu, l, 2);
-      const int row = (warp * MT + m) * 8 + (lane >> 2);
-      if ((lane & 3) == 0) ml[row] = make_float2(w.mx[m] == -INFINITY ? -INFINITY : __fmul_rn(w.mx[m], sl2), l);
-#pragma unroll
-      for (int i = 0; i < 2 * KS; i++)
-        *reinterpret_cast<float2*>(scratch + row * D + i * 8 + (lane & 3) * 2) =
-            make_float2(w.o[m][i][0] + w.o[m][i][2], w.o[m][i][1] + w.o[m][i][3]);
-    }
-    warp_arrive(bar.parts_full + buf);
-  }
-  return true;
-}
-
-// Counts a segment, the last one (number `last`) back to 0: its part is visible before the
-// count, and the parts of those counted before are visible after it.
-__device__ __forceinline__ bool count_segment(unsigned* done, unsigned last) {
-  unsigned old;
-  asm volatile("atom.inc.acq_rel.gpu.global.u32 %0, [%1], %2;" : "=r"(old) : "l"(done), "r"(last) : "memory");
-  return old == last;
-}
-
-// The joined shared prefix of row r of (sequence b, head g): columns 4 q .. and 4 (q + D / 8) ..
-template <int D>
-__device__ __forceinline__ void load_prefix(const PagedDecodeArgs& a, int b, int g, int r, int q, float2& z, float4& u0,
-                                            float4& u1) {
-  const size_t row = (size_t)g * a.pre.tiles * kTile + (size_t)b * a.R + r;
-  z = __ldcg(a.pre.ml + row);
-  const float4* o = reinterpret_cast<const float4*>(a.pre.o + row * D) + q;
-  u0 = __ldcg(o);
-  u1 = __ldcg(o + D / 8);
-}
-
-// Finishing warp f: joins the consumers' parts of every kBufs-th segment (and the shared
-// prefix's part, where the sequence's own first tile is).  A whole (sequence, head) is written
-// out; a segment leaves its part in the workspace and is counted, and the block that counts
-// the last one notes it in todo[first or second segment of the block] for its consumers.
-template <int D, int MT>
-__device__ bool sweep_finish(const PagedDecodeArgs& a, SegWalk sw, const Tiles& tl, const SweepPlan& plan, const int* len,
-                             uint8_t* smem, const SweepSmem& L, const SweepBars& bar, volatile int* todo,
-                             const volatile int* abort, int f, int lane) {
-  constexpr int kBufs = sweep_bufs(MT);
-  const int parts = MT < 4 ? kWarps : kWarps / a.MG;  // warps that hold a part of a row
-  const float* scratch = reinterpret_cast<const float*>(smem + L.scratch) + f * kWarps * MT * 8 * D;
-  const float2* ml = reinterpret_cast<const float2*>(smem + L.ml) + f * kWarps * MT * 8;
-  const int first = sw.w;
-  bool waited = false;
-  for (int seg = 0; sw.next(); seg++) {
-    if (seg % kBufs != f) continue;
-    if (!waited) {
-      pdl_wait();  // the kernels before clear the workspace's counters and leave the prefix's parts
-      waited = true;
-    }
-    const bool pre = sw.n0 == 0 && sweep_base(a, len[sw.b]) > 0;
-    float2 zp = make_float2(-INFINITY, 0.f);
-    float4 up0 = make_float4(0.f, 0.f, 0.f, 0.f), up1 = up0;
-    if (pre && lane < a.R * (D / 8)) load_prefix<D>(a, sw.b, sw.g, lane / (D / 8), lane % (D / 8), zp, up0, up1);
-    if (!__all_sync(0xffffffffu, mbar_wait(bar.parts_full + f, (seg / kBufs) & 1, abort))) return false;
-    const bool whole = sw.n0 == 0 && sw.n1 == sw.nt;
-    const int s0 = tl.cum[sw.b] * tl.Hkv + sw.g * sw.nt, slot = s0 <= first ? 0 : 1;
-    // a lane takes columns 4 q .. and 4 (q + D / 8) .. of a row
-    constexpr int kQ = D / 8;
-    const int items = a.R * kQ;
-    for (int i = lane; i < items; i += 32) {
-      const int r = i / kQ, q = i % kQ, tile = r >> 3;
-      if (pre && i != lane) load_prefix<D>(a, sw.b, sw.g, r, q, zp, up0, up1);
-      const int at0 = ((tile / MT) * parts * MT + tile % MT) * 8 + (r & 7);
-      RowSum x, y;
-      x.M = zp.x;
-#pragma unroll
-      for (int k = 0; k < kWarps; k++)
-        if (MT < 4 || k < parts) x.M = fmaxf(x.M, ml[at0 + k * MT * 8].x);
-      x.add(x.M, zp, up0);
-      y.add(x.M, zp, up1);
-#pragma unroll 4
-      for (int k = 0; k < parts; k++) {
-        const int from = at0 + k * MT * 8;
-        const float2 z = ml[from];
-        x.add(x.M, z, *reinterpret_cast<const float4*>(scratch + from * D + 4 * q));
-        y.add(x.M, z, *reinterpret_cast<const float4*>(scratch + from * D + 4 * (q + kQ)));
-      }
-      if (whole) {
-        write_row<D>(a, sw.b, sw.g, r, q, x.v, x.M, x.S);
-        write_row<D>(a, sw.b, sw.g, r, q + kQ, y.v, x.M, x.S);
-      } else {
-        const size_t at1 = (size_t)(2 * blockIdx.x + slot) * a.R + r;
-        float4* to = reinterpret_cast<float4*>(a.part_o + at1 * D) + q;
-        to[0] = x.v;
-        to[kQ] = y.v;
-        if (q == 0) a.part_ml[at1] = make_float2(x.M, x.S);
-      }
-    }
-    warp_arrive(bar.parts_empty + f);
-    if (whole) continue;
-    __syncwarp();  // the other lanes' parts before lane 0's release
-    if (lane == 0) {
-      const int c0 = tl.owner(plan, s0), c1 = tl.owner(plan, s0 + sw.nt - 1);
-      if (count_segment(a.done + c0, (unsigned)(c1 - c0))) todo[slot] = sw.b * tl.Hkv + sw.g;
-    }
-    __syncwarp();
-  }
-  warp_arrive(bar.fin);
-  return true;
-}
-
-// The (sequence, head)s whose last segment this block counted: their segments in order, kSplit
-// neighbouring lanes to four columns of a row (each its own share, then lane by lane: the same
-// sum whichever block does it).
-template <int D, int MT>
-__device__ bool sweep_join(const PagedDecodeArgs& a, const Tiles& tl, const SweepPlan& plan, const SweepBars& bar,
-                           const volatile int* todo, const volatile int* abort, int tid) {
-  constexpr int kThreads = kWarps * 32, kSplit = 4, kAhead = 10;
-  if (!__all_sync(0xffffffffu, mbar_wait(bar.fin, 0, abort))) return false;
-  for (int k = 0; k < 2; k++) {
-    const int sh = todo[k];
-    if (sh < 0) continue;
-    __threadfence();
-    const int b = sh / tl.Hkv, g = sh - b * tl.Hkv, nt = tl.cum[b + 1] - tl.cum[b];
-    const int s0 = tl.cum[b] * tl.Hkv + g * nt;
-    const int c0 = tl.owner(plan, s0), c1 = tl.owner(plan, s0 + nt - 1);
-    const int first = 2 * c0 + (s0 <= tl.start(plan, c0) ? 0 : 1);
-    const int sub = tid % kSplit, items = a.R * (D / 4);
-    for (int i0 = 0; i0 < items; i0 += kThreads / kSplit) {
-      const int i = min(i0 + tid / kSplit, items - 1);
-      const int r = i / (D / 4), q = i % (D / 4);
-      const auto at = [&](int c) { return (size_t)(c == c0 ? first : 2 * c) * a.R + r; };
-      RowSum x;
-      for (int c = c0 + sub; c <= c1; c += kSplit * kAhead) {
-        float2 z[kAhead];
-        float4 u[kAhead];
-#pragma unroll
-        for (int e = 0; e < kAhead; e++) {
-          z[e] = make_float2(-INFINITY, 0.f);
-          u[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (c + e * kSplit <= c1) {
-            z[e] = __ldcg(a.part_ml + at(c + e * kSplit));
-            u[e] = __ldcg(reinterpret_cast<const float4*>(a.part_o + at(c + e * kSplit) * D) + q);
-          }
-        }
-        float top = x.M;
-#pragma unroll
-        for (int e = 0; e < kAhead; e++) top = fmaxf(top, z[e].x);
-        x.raise(top);
-#pragma unroll
-        for (int e = 0; e < kAhead; e++) x.add(top, z[e], u[e]);
-      }
-      float top = x.M;
-#pragma unroll
-      for (int m = 1; m < kSplit; m <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
-      x.raise(top);
-#pragma unroll
-      for (int m = 1; m < kSplit; m <<= 1) {
-        x.S += __shfl_xor_sync(0xffffffffu, x.S, m);
-        x.v.x += __shfl_xor_sync(0xffffffffu, x.v.x, m);
-        x.v.y += __shfl_xor_sync(0xffffffffu, x.v.y, m);
-        x.v.z += __shfl_xor_sync(0xffffffffu, x.v.z, m);
-        x.v.w += __shfl_xor_sync(0xffffffffu, x.v.w, m);
-      }
-      if (sub == 0 && i0 + tid / kSplit < items) write_row<D>(a, b, g, r, q, x.v, top, x.S);
-    }
-  }
-  return true;
-}
-
-template <int D, int MT>
-__global__ void __launch_bounds__(kSweepThreads, 1) k_paged_sweep(const __grid_constant__ PagedDecodeArgs a) {
-  using C = Sweep<D>;
-  constexpr int kThreads = kSweepThreads, kBufs = sweep_bufs(MT);
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~static_cast<uintptr_t>(1023));
-  const SweepSmem L = sweep_smem(D, a.stages, a.tiles, MT, a.B);
-  SweepBars bar;
-  bar.full = reinterpret_cast<uint64_t*>(smem + L.bars);
-  bar.empty = bar.full + C::kMaxStages;
-  bar.q_full = bar.empty + C::kMaxStages;   // [2]
-  bar.q_empty = bar.q_full + 2;             // [2]
-  bar.parts_full = bar.q_empty + 2;         // [2] a segment's parts are in shared memory
-  bar.parts_empty = bar.parts_full + 2;     // [2] and have been read
-  bar.fin = bar.parts_empty + 2;            // the finishing warps are done
-  volatile int* abort = reinterpret_cast<volatile int*>(bar.fin + 1);
-  volatile int* todo = abort + 1;                              // [2]
-  volatile SweepPlan* splan = reinterpret_cast<volatile SweepPlan*>(const_cast<int*>(abort) + 3);
-  int* wsum = const_cast<int*>(abort) + 12;                    // [12] the scan's warp totals
-  int* cum = reinterpret_cast<int*>(smem + L.cum);
-  int* len = reinterpret_cast<int*>(smem + L.len);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  int n_first = 0;
-  if (tid < a.B) n_first = a.len[tid];
-  if (tid == 0) {
-    *abort = 0;
-    todo[0] = todo[1] = -1;
-    for (int i = 0; i < a.stages; i++) {
-      mbar_init(bar.full + i, 1);
-      mbar_init(bar.empty + i, kWarps);
-    }
-    for (int i = 0; i < 2; i++) {
-      mbar_init(bar.q_full + i, 1);
-      mbar_init(bar.q_empty + i, kWarps);
-      mbar_init(bar.parts_full + i, kWarps);
-      mbar_init(bar.parts_empty + i, 1);
-    }
-    mbar_init(bar.fin, kBufs);
-    fence_mbar_init();
-    cum[0] = 0;
-  }
-  if (warp == kWarps && lane == 0) {
-    prefetch_tmap(&a.map_k);
-    prefetch_tmap(&a.map_v);
-  }
-  // lengths, and the running count of the tiles of the parts read here
-  const int cap = a.max_pages << a.page_shift;
-  int before = 0;
-  for (int b0 = 0; b0 < a.B; b0 += kThreads) {
-    const int b = b0 + tid;
-    int nt = 0;
-    if (b < a.B) {
-      int n = b0 == 0 ? n_first : a.len[b];
-      if (n > cap) {
-        if (blockIdx.x == 0) record_page(a.status);
-        n = cap;
-      }
-      n = max(n, 0);
-      len[b] = n;
-      nt = max(1, (n - sweep_base(a, n) + C::kTK - 1) / C::kTK);  // one even where nothing is read: its rows are written
-    }
-    int x = nt;
-    if (b0 + warp * 32 < a.B) {
-#pragma unroll
-      for (int m = 1; m < 32; m <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, m);
-        if (lane >= m) x += y;
-      }
-    }
-    if (lane == 31) wsum[warp] = x;
-    __syncthreads();
-    if (b0 + warp * 32 < a.B) {
-      int low = lane < warp ? wsum[lane] : 0;  // at most 12 warps
-#pragma unroll
-      for (int m = 16; m; m >>= 1) low += __shfl_xor_sync(0xffffffffu, low, m);
-      if (b < a.B) cum[b + 1] = before + low + x;
-    }
-    if (b0 + kThreads < a.B) {
-      for (int i = 0; i < kThreads / 32; i++) before += wsum[i];
-      __syncthreads();
-    }
-  }
-  __syncthreads();
-  Tiles tl;
-  tl.cum = cum;
-  tl.B = a.B;
-  tl.Hkv = a.Hkv;
-  // one warp divides the work (a division costs every warp its issue slots)
-  if (warp == 0) {
-    SweepPlan p;
-    p.W = cum[a.B] * a.Hkv;
-    p.G = min(p.W, (int)gridDim.x);
-    p.base = p.W == p.G ? 1 : (int)fdiv((uint32_t)p.W, a.div_grid);
-    p.rem = p.W - p.base * p.G;
-    // tiles of this block and the next one's first, with the sequences they are in
-    const int c = min((int)blockIdx.x, p.G), x0 = min(c * p.base + min(c, p.rem), p.W - 1);
-    const int x1 = min(x0 + p.base + (c < p.rem ? 1 : 0), p.W);
-    const int b0 = tl.find_warp(x0, lane), b1 = tl.find_warp(min(x1, p.W - 1), lane);
-    p.w = c < p.G ? tl.moved(x0, b0) : p.W;
-    p.end = c < p.G && x1 < p.W ? tl.moved(x1, b1) : p.W;
-    p.b = b0;
-    if (p.w == (cum[b0 + 1]) * a.Hkv) p.b++;  // moved to the next sequence's first tile
-    if (lane == 0) {
-      if (p.b == a.B) p.b--;  // nothing left
-      const int nt = cum[p.b + 1] - cum[p.b], off = p.w - cum[p.b] * a.Hkv;
-      p.g = (int)__fdividef((float)off, (float)nt);  // within one of off / nt
-      p.n0 = off - p.g * nt;
-      while (p.n0 < 0) p.g--, p.n0 += nt;
-      while (p.n0 >= nt) p.g++, p.n0 -= nt;
-      splan->W = p.W;
-      splan->G = p.G;
-      splan->base = p.base;
-      splan->rem = p.rem;
-      splan->w = p.w;
-      splan->end = p.end;
-      splan->b = p.b;
-      splan->g = p.g;
-      splan->n0 = p.n0;
-    }
-  }
-  __syncthreads();
-  SegWalk sw;
-  sw.init(cum, a.Hkv, splan);
-  const volatile int never = 0;
-  // registers: 384 x 168 at launch; 256 x 216 for the consumers, 128 x 72 for the others
-  if (warp < kWarps) {
-    regs_inc<216>();
-    bool ok = sweep_consume<D, MT>(a, sw, len, smem, L, bar, abort, warp, lane);
-    if (ok) {
-      SweepPlan p;
-      p.W = splan->W;
-      p.base = splan->base;
-      p.rem = splan->rem;
-      ok = sweep_join<D, MT>(a, tl, p, bar, todo, abort, tid);
-    }
-    if (!ok && lane == 0) {
-      *abort = 1;
-      atomicCAS(a.status, 0, kStatusTimeout);
-    }
-    return;
-  }
-  regs_dec<72>();
-  bool ok = true;
-  if (warp == kWarps) {
-    // ------------------------------------------------------------ keys and values
-    // Lane i loads page i of a tile; the page numbers come 32 at a time.
-    const int prows = min(1 << a.page_shift, C::kTK), per = C::kTK / prows;
-    const uint32_t pbytes = (uint32_t)prows * C::kSpan;
-    const int shared = a.prefix_len >> a.page_shift;
-    int st = 0, ph = 1;  // the first round finds every stage empty
-    int issued = 0;
-    while (ok && sw.next()) {
-      const int base = sweep_base(a, len[sw.b]), own = len[sw.b] - base;
-      const int* row = a.table + (size_t)sw.b * a.max_pages;
-      const int p0 = base >> a.page_shift;
-      const int np = own > 0 ? (own + (1 << a.page_shift) - 1) >> a.page_shift : 0;  // own pages
-      int win = -1, id = 0;
-      for (int n = sw.n0; n < sw.n1; n++) {
-        const int first = (n * C::kTK) >> a.page_shift;  // own page of the tile's first position
-        const int have = max(0, min(per, np - first));
-        if (have > 0 && (first >> 5) != win) {
-          win = first >> 5;
-          const int i = p0 + win * 32 + lane;
-          id = 0;
-          if (i - p0 < np) {
-            id = i < shared ? a.prefix_table[i] : row[i];
-            if (id < 0 || id >= a.num_pages) {
-              record_page(a.status);
-              id = a.num_pages;  // past the pool: the copy fills with zeros
-            }
-          }
-        }
-        const int mine = __shfl_sync(0xffffffffu, id, (first & 31) + (lane < per ? lane : 0));
-        ok = __all_sync(0xffffffffu, mbar_wait(bar.empty + st, ph, abort));
-        if (!ok) break;
-        if (lane == 0) {
-          if (have > 0)
-            mbar_arrive_expect_tx(bar.full + st, 2u * have * pbytes);
-          else
-            mbar_arrive(bar.full + st);
-        }
-        __syncwarp();
-        if (lane < have) {
-          const int off = (n * C::kTK) & ((1 << a.page_shift) - 1);  // a tile inside a larger page
-          uint8_t* dst = smem + st * C::kStage + lane * pbytes;
-          tma_load_4d(dst, &a.map_k, bar.full + st, 0, off, sw.g, mine);
-          tma_load_4d(dst + C::kHalf, &a.map_v, bar.full + st, 0, off, sw.g, mine);
-        }
-        issued++;
-        if (++st == a.stages) {
-          st = 0;
-          ph ^= 1;
-        }
-      }
-    }
-    // let every copy issued above land before the block can exit
-    if (!ok && lane == 0)
-      for (int x = max(0, issued - a.stages); x < issued; x++)
-        mbar_wait(bar.full + x % a.stages, (x / a.stages) & 1, &never);
-  } else if (warp == kWarps + 1) {
-    // ------------------------------------------------------------ queries, two passes of rows at a time
-    constexpr int kCPR = D / 8, kRows = 32 / kCPR;
-    const int c = lane % kCPR;
-    const bool norm = a.qw != nullptr;
-    uint4 wv = make_uint4(0, 0, 0, 0);
-    if (norm) wv = load_rope_chunk<D>(a.qw, c, a.rope_half != 0);
-    for (int seg = 0; ok && sw.next(); seg++) {
-      const int qs = seg & 1;
-      if (seg >= 2) ok = __all_sync(0xffffffffu, mbar_wait(bar.q_empty + qs, ((seg >> 1) - 1) & 1, abort));
-      if (!ok) break;
-      const int pos0 = len[sw.b] - a.Tq;
-      uint8_t* q = smem + L.q + qs * a.tiles * 16 * C::kSpan;
-      for (int r0 = 0; r0 < a.tiles * 8; r0 += 2 * kRows) {
-        const int r = r0 + lane / kCPR, r2 = r + kRows;
-        const QueryChunk x = query_load<D>(a, sw.b, sw.g, r, c, pos0), y = query_load<D>(a, sw.b, sw.g, r2, c, pos0);
-        uint4 hi, lo;
-        query_finish<D>(a, x, norm, wv, hi, lo);
-        *reinterpret_cast<uint4*>(q + (r >> 3) * 16 * C::kSpan + swz(r & 7, c, C::kSpan)) = hi;
-        *reinterpret_cast<uint4*>(q + (r >> 3) * 16 * C::kSpan + swz((r & 7) + 8, c, C::kSpan)) = lo;
-        query_finish<D>(a, y, norm, wv, hi, lo);
-        if (r2 < a.tiles * 8) {
-          *reinterpret_cast<uint4*>(q + (r2 >> 3) * 16 * C::kSpan + swz(r2 & 7, c, C::kSpan)) = hi;
-          *reinterpret_cast<uint4*>(q + (r2 >> 3) * 16 * C::kSpan + swz((r2 & 7) + 8, c, C::kSpan)) = lo;
-        }
-      }
-      warp_arrive(bar.q_full + qs);
-    }
-  } else if (warp - kWarps - 2 < kBufs) {
-    // ------------------------------------------------------------ finished segments
-    SweepPlan p;
-    p.W = splan->W;
-    p.base = splan->base;
-    p.rem = splan->rem;
-    ok = sweep_finish<D, MT>(a, sw, tl, p, len, smem, L, bar, todo, abort, warp - kWarps - 2, lane);
-  }
-  if (!ok && lane == 0) {
-    *abort = 1;
-    atomicCAS(a.status, 0, kStatusTimeout);
-  }
-}
-
-// The counters of the (sequence, head)s that several blocks share.
-__global__ void k_paged_clear(unsigned* done, int n) {
-  pdl_launch();
-  for (int i = threadIdx.x; i < n; i += blockDim.x) done[i] = 0u;
-}
-
-template <int D, int MT>
-cudaError_t launch_sweep_t(const PagedDecodeArgs& a, int nsm, cudaStream_t s) {
-  static bool attr_set[64] = {};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  if (!attr_set[dev]) {
-    cudaError_t e = cudaFuncSetAttribute(k_paged_sweep<D, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
-    if (e != cudaSuccess) return e;
-    attr_set[dev] = true;
-  }
-  PagedDecodeArgs b = a;
-  b.stages = Sweep<D>::kMaxStages;
-  while (b.stages > 2 && sweep_smem(D, b.stages, b.tiles, MT, b.B).total > kSmemMax) b.stages--;
-  const int bytes = sweep_smem(D, b.stages, b.tiles, MT, b.B).total;
-  if (bytes > kSmemMax) return cudaErrorInvalidValue;
-  const int grid = nsm < kPagedMaxBlocks ? nsm : kPagedMaxBlocks;
-  b.div_grid = make_fastdiv((uint32_t)grid);
-  if (b.base == 0 && b.own_counters) {  // they are 0 before and after every call
-    k_paged_sweep<D, MT><<<grid, kSweepThreads, (size_t)bytes, s>>>(b);
-    return cudaGetLastError();
-  }
-  if (b.base == 0) {  // with a shared prefix k_prefix_q has cleared them
-    k_paged_clear<<<1, 256, 0, s>>>(b.done, kPagedMaxBlocks);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-  }
-  return launch_pdl(k_paged_sweep<D, MT>, grid, kSweepThreads, (size_t)bytes, s, b);
-}
-
 }  // namespace
 
 cudaError_t launch_kv_append_paged(const PagedAppendArgs& a, int D, cudaStream_t s) {
@@ -997,9 +128,7 @@ void paged_rows(int R, int* mt, int* tiles, int* mg) {
 }
 
 cudaError_t launch_decode_paged(const PagedDecodeArgs& a, int mt, int nsm, cudaStream_t s) {
-  if (a.D == 64)
-    return mt == 1 ? launch_sweep_t<64, 1>(a, nsm, s) : (mt == 2 ? launch_sweep_t<64, 2>(a, nsm, s) : launch_sweep_t<64, 4>(a, nsm, s));
-  return mt == 1 ? launch_sweep_t<32, 1>(a, nsm, s) : (mt == 2 ? launch_sweep_t<32, 2>(a, nsm, s) : launch_sweep_t<32, 4>(a, nsm, s));
+  return launch_sweep<false>(a, mt, nsm, s);
 }
 
 }  // namespace ne

@@ -7,6 +7,9 @@
 
 namespace ne {
 
+constexpr float kPagedLn2 = 0.69314718055994531f;
+constexpr int kSmemMax = 232448;
+
 __device__ __forceinline__ void record_page(int* status) { atomicCAS(status, 0, kStatusPage); }
 
 // Chunk c (8 values) of query row r of (sequence b, key/value head g) on its way to the
@@ -63,6 +66,26 @@ __device__ __forceinline__ void query_finish(const PagedDecodeArgs& a, const Que
   }
   hi = make_uint4(h[0], h[1], h[2], h[3]);
   lo = make_uint4(l[0], l[1], l[2], l[3]);
+}
+
+// Row r of (sequence b, head g), columns 4 q .. 4 q + 3: normalise and write.
+template <int D>
+__device__ __forceinline__ void write_row(const PagedDecodeArgs& a, int b, int g, int r, int q, float4 v, float M, float L) {
+  const int t = r / a.G, h = g * a.G + (r - t * a.G);
+  const float inv = L > 0.f ? 1.f / L : 0.f;
+  const size_t at = (((size_t)b * a.Tq + t) * a.Hq + h) * D + 4 * q;
+  v = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+  if (a.o_fp32)
+    *reinterpret_cast<float4*>(static_cast<float*>(a.o) + at) = v;
+  else
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.o) + at) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+  if (q == 0 && a.lse) a.lse[((size_t)b * a.Hq + h) * a.Tq + t] = L > 0.f ? (M + log2f(L)) * kPagedLn2 : -INFINITY;
+}
+
+// Positions of a sequence that the sweep leaves to the prefix kernel: the whole shared
+// prefix if the first query sees all of it, else none.
+__device__ __forceinline__ int sweep_base(const PagedDecodeArgs& a, int len) {
+  return a.base > 0 && len - a.Tq + 1 >= a.base ? a.base : 0;
 }
 
 }  // namespace ne

@@ -451,7 +451,7 @@ const char* ne_attn_status_string(int status);
 #define NE_ATTN_KERNEL_QK_NORM_BWD 11   /* their backward */
 #define NE_ATTN_KERNEL_KV_APPEND_PAGED 12
 #define NE_ATTN_KERNEL_DECODE_PAGED 13  /* the sweep over a paged cache */
-#define NE_ATTN_KERNEL_DECODE_PREFIX 14 /* a shared prefix's queries and sweep */
+#define NE_ATTN_KERNEL_DECODE_PREFIX 14 /* the same with a shared prefix, and the join */
 #define NE_ATTN_NUM_KERNEL_KINDS 15
 int ne_attn_profile_start(int capacity);
 int ne_attn_profile_stop(double* total_ms, long long* launches);
