@@ -523,12 +523,10 @@ int log2_of(int v) {
   return s;
 }
 
-// Weight-gradient partials [blocks, 2 D] of the query/key norms' backward, for the most blocks it launches.
+// Weight-gradient partials [blocks + groups, D] of the query/key norms' backward, for the most it launches.
 // Then the counters (256 bytes).
-constexpr int kQkNormMaxBlocks = kQkNormMaxSms * kQkNormBlocksPerSm;
-constexpr int kQkNormMaxGroups = (kQkNormMaxBlocks + kQkNormGroup - 1) / kQkNormGroup;
-static_assert((1 + kQkNormMaxGroups) * sizeof(unsigned) <= 256, "counters");
-size_t qk_norm_bwd_part_bytes(int D) { return ws_up(sizeof(float) * 2 * D * (kQkNormMaxBlocks + kQkNormMaxGroups)); }
+static_assert((2 + kQkNormMaxGroups) * sizeof(unsigned) <= 256, "counters");
+size_t qk_norm_bwd_part_bytes(int D) { return ws_up(sizeof(float) * D * (kQkNormMaxBlocks + kQkNormMaxGroups)); }
 size_t qk_norm_bwd_ws_bytes(int D) { return qk_norm_bwd_part_bytes(D) + 256; }
 
 // Paged cache: page sizes, the pool's stride, and the longest sequence a table
@@ -1342,10 +1340,11 @@ int ne_attn_qk_norm(const void* q, const void* k, const void* q_w, const void* k
   a.rope_half = (flags & kFlagRopeHalf) ? 1 : 0;
   a.eps = eps;
   a.div_t = make_fastdiv((uint32_t)T);
-  const int per = qk_norm_heads_per_item(false);
-  a.div_hg = make_fastdiv((uint32_t)((Hq + Hkv + per - 1) / per));
+  a.div_hq = make_fastdiv((uint32_t)Hq);
+  a.div_hkv = make_fastdiv((uint32_t)Hkv);
+  const int blocks = qk_norm_blocks(B, T, Hq, Hkv, D, nsm, false, &a.nbq);
   ProfScope prof(NE_ATTN_KERNEL_QK_NORM, s);
-  return launch_qk_norm(a, D, nsm, s) == cudaSuccess ? NE_OK : NE_ERR_CUDA;
+  return launch_qk_norm(a, D, blocks, s) == cudaSuccess ? NE_OK : NE_ERR_CUDA;
 }
 
 int ne_attn_qk_norm_bwd(const void* q, const void* k, const void* q_w, const void* k_w, const void* dqn,
@@ -1389,9 +1388,9 @@ int ne_attn_qk_norm_bwd(const void* q, const void* k, const void* q_w, const voi
   a.Hq = Hq;
   a.Hkv = Hkv;
   a.eps = eps;
-  const int per = qk_norm_heads_per_item(true);
-  a.div_hg = make_fastdiv((uint32_t)((Hq + Hkv + per - 1) / per));
-  const int blocks = qk_norm_bwd_blocks(B, T, (int)a.div_hg.d, D, nsm);
+  a.div_hq = make_fastdiv((uint32_t)Hq);
+  a.div_hkv = make_fastdiv((uint32_t)Hkv);
+  const int blocks = qk_norm_blocks(B, T, Hq, Hkv, D, nsm, true, &a.nbq);
   a.dqw = dq_w;
   a.dkw = dk_w;
   void* ws = workspace;

@@ -184,23 +184,27 @@ struct QkNormArgs {
   long long q_stride, k_stride;
   int B, T, Hq, Hkv, rope_half;
   float eps;
-  FastDiv div_t, div_hg;         // by T and by the head groups of a position
+  int nbq;                       // blocks that work on q; the others on k
+  FastDiv div_t, div_hq, div_hkv;
 };
 struct QkNormBwdArgs {
   const __nv_bfloat16 *q, *k, *qw, *kw;
   const void *gq, *gk;  // gradients of the normalised q, k [B, T, H, D], bf16 or fp32
   void *dq, *dk;        // gradients of q, k (same type), rows dq_stride / dk_stride values apart
-  float* part;          // [blocks + groups, 2 D] partial weight gradients (workspace)
-  unsigned* done;       // [1 + groups] groups, and blocks of a group, that have left theirs; 0 before and
-                        // after (workspace or the library's)
+  float* part;          // [blocks + groups, D] partial weight gradients (workspace)
+  unsigned* done;       // [2 + groups] groups of a side, and blocks of a group, that have left theirs; 0
+                        // before and after (workspace or the library's)
   float *dqw, *dkw;     // [D]
   long long q_stride, k_stride, dq_stride, dk_stride;
   int B, T, Hq, Hkv;
   float eps;
-  FastDiv div_hg;
+  int nbq;              // blocks that work on q; the others on k
+  FastDiv div_hq, div_hkv;
 };
-constexpr int kQkNormMaxSms = 160, kQkNormBlocksPerSm = 4;  // bound the backward's partials
-constexpr int kQkNormGroup = 32;                            // blocks whose partials are added first
+constexpr int kQkNormMaxSms = 160, kQkNormBlocksPerSm = 3, kQkNormFwdBlocksPerSm = 5;
+constexpr int kQkNormMaxBlocks = kQkNormMaxSms * kQkNormBlocksPerSm;  // bounds the backward's partials
+constexpr int kQkNormGroup = 32;  // blocks whose partials are added first
+constexpr int kQkNormMaxGroups = kQkNormMaxBlocks / kQkNormGroup + 2;
 
 // Append of new keys and values to a paged cache (see paged.cu).
 struct PagedAppendArgs {
@@ -291,9 +295,8 @@ cudaError_t launch_pdl(void (*k)(P...), int grid, int block, size_t smem, cudaSt
 }
 #endif
 
-int qk_norm_heads_per_item(bool bwd);
-cudaError_t launch_qk_norm(const QkNormArgs& a, int D, int nsm, cudaStream_t s);
-int qk_norm_bwd_blocks(int B, int T, int hg, int D, int nsm);
+int qk_norm_blocks(int B, int T, int Hq, int Hkv, int D, int nsm, bool bwd, int* nbq);
+cudaError_t launch_qk_norm(const QkNormArgs& a, int D, int blocks, cudaStream_t s);
 cudaError_t launch_qk_norm_bwd(const QkNormBwdArgs& a, int D, bool f32, int blocks, cudaStream_t s);
 cudaError_t launch_kv_append_paged(const PagedAppendArgs& a, int D, cudaStream_t s);
 void paged_rows(int R, int* mt, int* tiles, int* mg);

@@ -52,10 +52,11 @@ inline int prefix_smem(int D, int B) {
   return (kPagedHead0 + (2 * B + 1) * 4 + 1023) / 1024 * 1024 + (D == 64 ? PreCfg<64>::kBytes : PreCfg<32>::kBytes) + 1024;
 }
 
-// The blocks that take the prefix, of all: their share of the work, at what a block of each kind
-// takes for a tile (1.2 us for a pair of row tiles, 0.55 us for a tile of the sweep, measured).
+// The blocks that take the prefix, of all: their share of the work, a tile of a pair of row tiles
+// counted as 1.64 of the sweep's (measured: 64 sequences on 8192 positions 24.5, 19.9 and 23.1 us
+// at 1.27, 1.64 and 2.18; 128 on 16384 41.9, 39.6 and 42.4 us).
 __device__ __forceinline__ int prefix_blocks(const PagedDecodeArgs& a, int sweep_tiles, int blocks) {
-  const float mine = 1.2f * (float)a.pre.W, theirs = 0.55f * (float)sweep_tiles;
+  const float mine = 1.64f * (float)a.pre.W, theirs = (float)sweep_tiles;
   const int P = __float2int_rn((float)blocks * __fdiv_rn(mine, mine + theirs));
   return max(1, min(min(P, blocks - 1), a.pre.W));
 }

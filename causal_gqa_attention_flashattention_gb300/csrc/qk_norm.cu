@@ -41,66 +41,74 @@ __device__ __forceinline__ float row_sum(float s) {
 }
 
 constexpr int kThreads = 256;
-constexpr int kHeads = 4;  // heads of one position per thread: one read of its table row serves them
+constexpr int kAtOnce = 2;  // rows a thread has under way
 
-// A thread takes chunk c of up to kHeads heads of one position; the D / 8
-// threads of a row are neighbouring lanes and add up their squares by shuffles.
-// The chunk index is the same for every item of a thread (the grid's stride is a
-// multiple of D / 8), so its weights stay in registers.
+// A block works on q or on k (the first nbq blocks on q): one weight, a thread takes the same
+// chunk of every row it gets, so its part of the weight stays in registers.  Few registers, and
+// as many blocks as the SMs hold at once, carry these kernels: with four heads of a position per
+// thread (one read of its table row for them, both weights in registers) the forward took 15.0 us
+// at 16 x 512 positions, 12/4 heads, D = 64, with two heads 11.6 us, in this form 8.5 us (33.6 MB,
+// 3.9 TB/s); the backward 28.3 us, in this form 17.1 us (50 MB, with the sums of dw).
+template <int D>
+struct Side {
+  bool isq;
+  const __nv_bfloat16 *x, *w;
+  long long stride;
+  uint32_t H, n, first, step;  // heads; row chunks; this thread's first chunk and the distance to its next
+};
+template <int D, typename Args>
+__device__ __forceinline__ Side<D> side_of(const Args& a) {
+  Side<D> s;
+  s.isq = blockIdx.x < (uint32_t)a.nbq;
+  s.x = s.isq ? a.q : a.k;
+  s.w = s.isq ? a.qw : a.kw;
+  s.stride = s.isq ? a.q_stride : a.k_stride;
+  s.H = s.isq ? a.Hq : a.Hkv;
+  s.n = (uint32_t)a.B * a.T * s.H * (D / 8);
+  const uint32_t blk = s.isq ? blockIdx.x : blockIdx.x - a.nbq;
+  s.first = blk * kThreads + threadIdx.x;
+  s.step = (s.isq ? a.nbq : gridDim.x - a.nbq) * kThreads;
+  return s;
+}
+
+// The D / 8 threads of a row are neighbouring lanes and add up their squares by shuffles: whole
+// warps run together, lanes past the end take part in the shuffles only.
 template <int D>
 __global__ void __launch_bounds__(kThreads) k_qk_norm(const QkNormArgs a) {
   constexpr int kCPR = D / 8;
-  const uint32_t H = a.Hq + a.Hkv;
-  const uint32_t n = (uint32_t)a.B * a.T * a.div_hg.d * kCPR;
+  const Side<D> s = side_of<D>(a);
+  const FastDiv div_h = s.isq ? a.div_hq : a.div_hkv;
+  uint4* out = reinterpret_cast<uint4*>(s.isq ? a.qr : a.kr);
   const int c = (int)(threadIdx.x % kCPR);
   const bool half = a.rope_half != 0;
-  float wq[8], wk[8];
-  unpack8(load_rope_chunk<D>(a.qw, c, half), wq);
-  unpack8(load_rope_chunk<D>(a.kw, c, half), wk);
-  // whole warps run together: lanes past the end take part in the shuffles only
-  for (uint32_t it = blockIdx.x * kThreads + threadIdx.x; (it & ~31u) < n; it += gridDim.x * kThreads) {
-    const bool on = it < n;
-    const uint32_t row = (on ? it : 0u) / kCPR;
-    const uint32_t bt = fdiv(row, a.div_hg);
-    const uint32_t h0 = (row - bt * a.div_hg.d) * kHeads;
-    const uint32_t t = bt - fdiv(bt, a.div_t) * a.T;
-    float x[kHeads][8], ss[kHeads];
+  float w[8];
+  unpack8(load_rope_chunk<D>(s.w, c, half), w);
+  for (uint32_t it = s.first; (it & ~31u) < s.n; it += kAtOnce * s.step) {
+    uint4 v[kAtOnce];
+    float4 c0[kAtOnce], c1[kAtOnce];
 #pragma unroll
-    for (int e = 0; e < kHeads; e++) {
-      const uint32_t h = h0 + e;
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (on && h < H)
-        v = load_rope_chunk<D>(h < (uint32_t)a.Hq ? a.q + (size_t)bt * a.q_stride + h * D
-                                                  : a.k + (size_t)bt * a.k_stride + (h - a.Hq) * D,
-                               c, half);
-      unpack8(v, x[e]);
+    for (int e = 0; e < kAtOnce; e++) {
+      const uint32_t i = it + e * s.step, row = (i < s.n ? i : 0u) / kCPR;
+      const uint32_t bt = fdiv(row, div_h), h = row - bt * s.H, t = bt - fdiv(bt, a.div_t) * a.T;
+      v[e] = load_rope_chunk<D>(s.x + (size_t)bt * s.stride + h * D, c, half);
+      rope_coeffs<D>(a.rope, (int)t, c, c0[e], c1[e]);
     }
-    float4 c0, c1;
-    rope_coeffs<D>(a.rope, (int)t, c, c0, c1);
 #pragma unroll
-    for (int e = 0; e < kHeads; e++) {
-      float s = 0.f;
+    for (int e = 0; e < kAtOnce; e++) {
+      const uint32_t i = it + e * s.step;
+      float x[8], ss = 0.f;
+      unpack8(v[e], x);
 #pragma unroll
-      for (int i = 0; i < 8; i++) s = fmaf(x[e][i], x[e][i], s);
-      ss[e] = row_sum<kCPR>(s);
-    }
-    const float cs[4] = {c0.x, c0.z, c1.x, c1.z}, sn[4] = {c0.y, c0.w, c1.y, c1.w};
-#pragma unroll
-    for (int e = 0; e < kHeads; e++) {
-      const uint32_t h = h0 + e;
-      if (!on || h >= H) continue;
-      const bool isq = h < (uint32_t)a.Hq;
-      const float r = rsqrtf(fmaf(ss[e], 1.f / D, a.eps));
+      for (int j = 0; j < 8; j++) ss = fmaf(x[j], x[j], ss);
+      const float r = rsqrtf(fmaf(row_sum<kCPR>(ss), 1.f / D, a.eps));
+      const float cs[4] = {c0[e].x, c0[e].z, c1[e].x, c1[e].z}, sn[4] = {c0[e].y, c0[e].w, c1[e].y, c1[e].w};
       uint32_t o[4];
 #pragma unroll
       for (int p = 0; p < 4; p++) {
-        const float x0 = x[e][2 * p] * r * (isq ? wq[2 * p] : wk[2 * p]);
-        const float x1 = x[e][2 * p + 1] * r * (isq ? wq[2 * p + 1] : wk[2 * p + 1]);
+        const float x0 = x[2 * p] * r * w[2 * p], x1 = x[2 * p + 1] * r * w[2 * p + 1];
         o[p] = pack_f16(fmaf(x0, cs[p], -x1 * sn[p]), fmaf(x0, sn[p], x1 * cs[p]));
       }
-      uint4* dst = isq ? reinterpret_cast<uint4*>(a.qr) + ((size_t)bt * a.Hq + h) * kCPR
-                       : reinterpret_cast<uint4*>(a.kr) + ((size_t)bt * a.Hkv + (h - a.Hq)) * kCPR;
-      dst[c] = make_uint4(o[0], o[1], o[2], o[3]);
+      if (i < s.n) out[i] = make_uint4(o[0], o[1], o[2], o[3]);
     }
   }
 }
@@ -119,20 +127,21 @@ __device__ __forceinline__ bool last_to_count(unsigned* done, unsigned n) {
   return last;
 }
 
-// Sum of n partial rows of 2 D values, n at most 4 kOver, in a fixed order; true for the first
-// 2 D / 4 threads, which then have a quad each in t.
+// Sum of n <= 32 partial rows of D values, in a fixed order; true for the first D / 4 threads,
+// which then have a quad each in t.
 template <int D>
 __device__ __forceinline__ bool add_partials(const float* part, unsigned n, float4& t) {
-  constexpr unsigned kQuads = 2 * D / 4, kOver = kThreads / kQuads;
+  constexpr unsigned kQuads = D / 4, kOver = kThreads / kQuads, kEach = (32 + kOver - 1) / kOver;
   __shared__ float4 red4[kOver][kQuads];
   const unsigned q = threadIdx.x % kQuads, o = threadIdx.x / kQuads;
-  float4 u[4];
+  float4 u = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-  for (unsigned k = 0; k < 4; k++)
-    u[k] = o + k * kOver < n ? __ldcg(reinterpret_cast<const float4*>(part) + (size_t)(o + k * kOver) * kQuads + q)
-                             : make_float4(0.f, 0.f, 0.f, 0.f);
-  red4[o][q] = make_float4((u[0].x + u[1].x) + (u[2].x + u[3].x), (u[0].y + u[1].y) + (u[2].y + u[3].y),
-                           (u[0].z + u[1].z) + (u[2].z + u[3].z), (u[0].w + u[1].w) + (u[2].w + u[3].w));
+  for (unsigned k = 0; k < kEach; k++)
+    if (o + k * kOver < n) {
+      const float4 x = __ldcg(reinterpret_cast<const float4*>(part) + (size_t)(o + k * kOver) * kQuads + q);
+      u = make_float4(u.x + x.x, u.y + x.y, u.z + x.z, u.w + x.w);
+    }
+  red4[o][q] = u;
   __syncthreads();
   if (threadIdx.x >= kQuads) return false;
   t = red4[0][q];
@@ -143,148 +152,138 @@ __device__ __forceinline__ bool add_partials(const float* part, unsigned n, floa
   }
   return true;
 }
-static_assert(kQkNormGroup <= 32 && kQkNormMaxSms * kQkNormBlocksPerSm <= 32 * kQkNormGroup, "partials of a sum");
+static_assert(kQkNormGroup <= 32 && kQkNormMaxBlocks <= 32 * kQkNormGroup, "partials of a sum");
 
 // Backward.  dw is summed in fp32: over the rows of a thread, over the threads of
-// a block that share a chunk (in a fixed order), one partial per block and weight
-// in the workspace, added in two steps by the blocks that end last, always in the
+// a block that share a chunk (in a fixed order), one partial per block in the
+// workspace, added in two steps by the blocks that end last, always in the
 // same order: the result does not depend on which ones, and is bitwise reproducible.
 template <int D, bool F32>
 __global__ void __launch_bounds__(kThreads) k_qk_norm_bwd(const QkNormBwdArgs a) {
   constexpr int kCPR = D / 8;
-  constexpr int kPer = 2;  // heads per thread
-  const uint32_t H = a.Hq + a.Hkv;
-  const uint32_t n = (uint32_t)a.B * a.T * a.div_hg.d * kCPR;
+  const Side<D> s = side_of<D>(a);
+  const FastDiv div_h = s.isq ? a.div_hq : a.div_hkv;
+  const void* gp = s.isq ? a.gq : a.gk;
+  void* dp = s.isq ? a.dq : a.dk;
+  const long long d_stride = s.isq ? a.dq_stride : a.dk_stride;
   const int c = (int)(threadIdx.x % kCPR);
-  float wq[8], wk[8], dwq[8], dwk[8];
-  unpack8(__ldg(reinterpret_cast<const uint4*>(a.qw) + c), wq);
-  unpack8(__ldg(reinterpret_cast<const uint4*>(a.kw) + c), wk);
+  float w[8], dw[8];
+  unpack8(__ldg(reinterpret_cast<const uint4*>(s.w) + c), w);
 #pragma unroll
-  for (int i = 0; i < 8; i++) dwq[i] = dwk[i] = 0.f;
-  for (uint32_t it = blockIdx.x * kThreads + threadIdx.x; (it & ~31u) < n; it += gridDim.x * kThreads) {
-    const bool on = it < n;
-    const uint32_t row = (on ? it : 0u) / kCPR;
-    const uint32_t bt = fdiv(row, a.div_hg);
-    const uint32_t h0 = (row - bt * a.div_hg.d) * kPer;
-    float x[kPer][8], g[kPer][8];
+  for (int j = 0; j < 8; j++) dw[j] = 0.f;
+  for (uint32_t it = s.first; (it & ~31u) < s.n; it += kAtOnce * s.step) {
+    uint4 v[kAtOnce], g0[kAtOnce], g1[kAtOnce];
+    size_t to[kAtOnce];
 #pragma unroll
-    for (int e = 0; e < kPer; e++) {
-      const uint32_t h = h0 + e;
-      const bool isq = h < (uint32_t)a.Hq;
-      uint4 v = make_uint4(0, 0, 0, 0);
-#pragma unroll
-      for (int i = 0; i < 8; i++) g[e][i] = 0.f;
-      if (on && h < H) {
-        v = __ldg(reinterpret_cast<const uint4*>(isq ? a.q + (size_t)bt * a.q_stride + h * D
-                                                     : a.k + (size_t)bt * a.k_stride + (h - a.Hq) * D) + c);
-        const size_t gi = isq ? ((size_t)bt * a.Hq + h) * D + 8 * c : ((size_t)bt * a.Hkv + (h - a.Hq)) * D + 8 * c;
-        const void* gp = isq ? a.gq : a.gk;
-        if (F32) {  // plain loads: dq may be the same buffer as gq
-          const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(gp) + gi);
-          const float4 u = p[0], w = p[1];
-          g[e][0] = u.x, g[e][1] = u.y, g[e][2] = u.z, g[e][3] = u.w;
-          g[e][4] = w.x, g[e][5] = w.y, g[e][6] = w.z, g[e][7] = w.w;
-        } else {
-          unpack8(*reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(gp) + gi), g[e]);
-        }
+    for (int e = 0; e < kAtOnce; e++) {
+      const uint32_t i = it + e * s.step, row = (i < s.n ? i : 0u) / kCPR;
+      const uint32_t bt = fdiv(row, div_h), h = row - bt * s.H;
+      v[e] = __ldg(reinterpret_cast<const uint4*>(s.x + (size_t)bt * s.stride + h * D) + c);
+      // plain loads: dq may be the same buffer as gq
+      g0[e] = g1[e] = make_uint4(0, 0, 0, 0);
+      if (i < s.n) {
+        const uint4* p = static_cast<const uint4*>(gp) + (size_t)i * (F32 ? 2 : 1);
+        g0[e] = p[0];
+        if (F32) g1[e] = p[1];
       }
-      unpack8(v, x[e]);
+      to[e] = (size_t)bt * d_stride + h * D + 8 * c;
     }
 #pragma unroll
-    for (int e = 0; e < kPer; e++) {
-      const uint32_t h = h0 + e;
-      const bool isq = h < (uint32_t)a.Hq;
+    for (int e = 0; e < kAtOnce; e++) {
+      float x[8], g[8];
+      unpack8(v[e], x);
+      if (F32) {
+        const uint32_t u[8] = {g0[e].x, g0[e].y, g0[e].z, g0[e].w, g1[e].x, g1[e].y, g1[e].z, g1[e].w};
+#pragma unroll
+        for (int j = 0; j < 8; j++) g[j] = __uint_as_float(u[j]);
+      } else {
+        unpack8(g0[e], g);
+      }
       float s1 = 0.f, s2 = 0.f;
 #pragma unroll
-      for (int i = 0; i < 8; i++) {
-        s1 = fmaf(x[e][i], x[e][i], s1);
-        s2 = fmaf(g[e][i] * (isq ? wq[i] : wk[i]), x[e][i], s2);
+      for (int j = 0; j < 8; j++) {
+        s1 = fmaf(x[j], x[j], s1);
+        s2 = fmaf(g[j] * w[j], x[j], s2);
       }
       s1 = row_sum<kCPR>(s1);
       s2 = row_sum<kCPR>(s2);
-      if (!on || h >= H) continue;
+      if (it + e * s.step >= s.n) continue;
       const float r = rsqrtf(fmaf(s1, 1.f / D, a.eps));
       const float m = s2 * r * (1.f / D);  // mean(w g xh)
       float d[8];
 #pragma unroll
-      for (int i = 0; i < 8; i++) {
-        const float xh = x[e][i] * r;
-        d[i] = r * fmaf(-xh, m, g[e][i] * (isq ? wq[i] : wk[i]));
-        if (isq)
-          dwq[i] = fmaf(g[e][i], xh, dwq[i]);
-        else
-          dwk[i] = fmaf(g[e][i], xh, dwk[i]);
+      for (int j = 0; j < 8; j++) {
+        const float xh = x[j] * r;
+        d[j] = r * fmaf(-xh, m, g[j] * w[j]);
+        dw[j] = fmaf(g[j], xh, dw[j]);
       }
-      const size_t di = isq ? (size_t)bt * a.dq_stride + h * D + 8 * c : (size_t)bt * a.dk_stride + (h - a.Hq) * D + 8 * c;
-      void* dp = isq ? a.dq : a.dk;
       if (F32) {
-        float4* p = reinterpret_cast<float4*>(static_cast<float*>(dp) + di);
+        float4* p = reinterpret_cast<float4*>(static_cast<float*>(dp) + to[e]);
         p[0] = make_float4(d[0], d[1], d[2], d[3]);
         p[1] = make_float4(d[4], d[5], d[6], d[7]);
       } else {
-        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(dp) + di) =
+        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(dp) + to[e]) =
             make_uint4(pack_bf16(d[0], d[1]), pack_bf16(d[2], d[3]), pack_bf16(d[4], d[5]), pack_bf16(d[6], d[7]));
       }
     }
   }
   // the block's dw: lanes of a warp with the same chunk, then the warps
-  __shared__ float red[kThreads / 32][2 * D];
+  __shared__ float red[kThreads / 32][D];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
 #pragma unroll
-  for (int i = 0; i < 8; i++)
+  for (int j = 0; j < 8; j++)
 #pragma unroll
-    for (int m = kCPR; m < 32; m <<= 1) {
-      dwq[i] += __shfl_xor_sync(0xffffffffu, dwq[i], m);
-      dwk[i] += __shfl_xor_sync(0xffffffffu, dwk[i], m);
-    }
+    for (int m = kCPR; m < 32; m <<= 1) dw[j] += __shfl_xor_sync(0xffffffffu, dw[j], m);
   if (lane < kCPR) {
 #pragma unroll
-    for (int i = 0; i < 8; i++) {
-      red[warp][8 * c + i] = dwq[i];
-      red[warp][D + 8 * c + i] = dwk[i];
-    }
+    for (int j = 0; j < 8; j++) red[warp][8 * c + j] = dw[j];
   }
   __syncthreads();
-  if (threadIdx.x < 2 * D) {
-    float s = 0.f;
+  if (threadIdx.x < D) {
+    float t = 0.f;
 #pragma unroll
-    for (int w = 0; w < kThreads / 32; w++) s += red[w][threadIdx.x];
-    a.part[(size_t)blockIdx.x * 2 * D + threadIdx.x] = s;
+    for (int k = 0; k < kThreads / 32; k++) t += red[k][threadIdx.x];
+    a.part[(size_t)blockIdx.x * D + threadIdx.x] = t;
   }
-  // the last of kQkNormGroup neighbouring blocks adds their partials in order, the last of those
-  // blocks the groups' sums
-  const unsigned grp = blockIdx.x / kQkNormGroup, groups = (gridDim.x + kQkNormGroup - 1) / kQkNormGroup;
-  const unsigned b0 = grp * kQkNormGroup, nb = min((unsigned)kQkNormGroup, gridDim.x - b0);
+  // the last of kQkNormGroup neighbouring blocks of a side adds their partials in order, the last of
+  // those blocks the groups' sums
+  const unsigned first = s.isq ? 0 : a.nbq, count = s.isq ? a.nbq : gridDim.x - a.nbq;
+  const unsigned grp = (blockIdx.x - first) / kQkNormGroup, groups = (count + kQkNormGroup - 1) / kQkNormGroup;
+  const unsigned b0 = grp * kQkNormGroup, nb = min((unsigned)kQkNormGroup, count - b0);
+  const unsigned g0 = s.isq ? 0 : (a.nbq + kQkNormGroup - 1) / kQkNormGroup;  // the side's first group
   float4 t;
-  if (!last_to_count(a.done + 1 + grp, nb)) return;
-  const bool mine = add_partials<D>(a.part + (size_t)b0 * 2 * D, nb, t);
-  float4* sums = reinterpret_cast<float4*>(a.part + (size_t)gridDim.x * 2 * D);
-  if (mine) sums[(size_t)grp * (2 * D / 4) + threadIdx.x] = t;
-  if (!last_to_count(a.done, groups)) return;
-  if (add_partials<D>(reinterpret_cast<const float*>(sums), groups, t))
-    *reinterpret_cast<float4*>((threadIdx.x < D / 4 ? a.dqw : a.dkw - D) + 4 * threadIdx.x) = t;
-}
-
-int blocks_for(long long threads, int most) {
-  const long long b = (threads + kThreads - 1) / kThreads;
-  return (int)(b < most ? b : most);
+  if (!last_to_count(a.done + 2 + g0 + grp, nb)) return;
+  float* sums = a.part + (size_t)(gridDim.x + g0) * D;
+  if (add_partials<D>(a.part + (size_t)(first + b0) * D, nb, t))
+    reinterpret_cast<float4*>(sums + (size_t)grp * D)[threadIdx.x] = t;
+  if (!last_to_count(a.done + (s.isq ? 0 : 1), groups)) return;
+  if (add_partials<D>(sums, groups, t)) reinterpret_cast<float4*>(s.isq ? a.dqw : a.dkw)[threadIdx.x] = t;
 }
 
 }  // namespace
 
-int qk_norm_heads_per_item(bool bwd) { return bwd ? 2 : kHeads; }
-
-cudaError_t launch_qk_norm(const QkNormArgs& a, int D, int nsm, cudaStream_t s) {
-  const int grid = blocks_for((long long)a.B * a.T * a.div_hg.d * (D / 8), nsm * 8);
-  if (D == 64)
-    k_qk_norm<64><<<grid, kThreads, 0, s>>>(a);
-  else
-    k_qk_norm<32><<<grid, kThreads, 0, s>>>(a);
-  return cudaGetLastError();
+// Blocks of q and of both: as many as the rows need or the SMs hold, in proportion to the heads.
+int qk_norm_blocks(int B, int T, int Hq, int Hkv, int D, int nsm, bool bwd, int* nbq) {
+  const auto need = [&](int H) {
+    const long long chunks = (long long)B * T * H * (D / 8);
+    return (int)((chunks + kThreads * kAtOnce - 1) / (kThreads * kAtOnce));
+  };
+  const int nq = need(Hq), nk = need(Hkv);
+  int most = (nsm < kQkNormMaxSms ? nsm : kQkNormMaxSms) * (bwd ? kQkNormBlocksPerSm : kQkNormFwdBlocksPerSm);
+  if (nq + nk <= most) {
+    *nbq = nq;
+    return nq + nk;
+  }
+  *nbq = (int)((long long)most * Hq / (Hq + Hkv));
+  return most;
 }
 
-int qk_norm_bwd_blocks(int B, int T, int hg, int D, int nsm) {
-  return blocks_for((long long)B * T * hg * (D / 8), (nsm < kQkNormMaxSms ? nsm : kQkNormMaxSms) * kQkNormBlocksPerSm);
+cudaError_t launch_qk_norm(const QkNormArgs& a, int D, int blocks, cudaStream_t s) {
+  if (D == 64)
+    k_qk_norm<64><<<blocks, kThreads, 0, s>>>(a);
+  else
+    k_qk_norm<32><<<blocks, kThreads, 0, s>>>(a);
+  return cudaGetLastError();
 }
 
 cudaError_t launch_qk_norm_bwd(const QkNormBwdArgs& a, int D, bool f32, int blocks, cudaStream_t s) {
