@@ -14,8 +14,8 @@
 // A sequence takes part if its first query sees the whole prefix, so no score is
 // masked here but for the columns behind the prefix in its last tile; the sweep
 // reads the prefix pages itself for one that does not.
-// Precision: q as one fp16, the weights as one bf16, as the forward (2^-11 and 2^-8
-// at most, at random over the keys).
+// Precision: q as two fp16 parts (two products; with one the LSE is off by 1e-5), the
+// weights as one bf16, as the forward (2^-8 at most, at random over the keys).
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -36,15 +36,15 @@ struct PreCfg {
   static constexpr uint32_t kSpan = D * 2;
   static constexpr uint32_t kSwz = D == 64 ? kSw128 : kSw64;
   static constexpr uint32_t kSBO = 8 * kSpan;
-  static constexpr int kQSlots = 4;  // two segments' worth of row tiles
+  static constexpr int kQSlots = 4;  // high and low part of each unit's row tile
   static constexpr int kStages = 4;
   static constexpr uint32_t kColO = 0, kColS = 128, kColP = 384;  // unit u: O at 64u, S at 128 + 128u, P at 384 + 64u
   static constexpr uint32_t kTmemCols = 512;
   static constexpr int kThreads = 384;
-  static constexpr int kOffK = kQSlots * kTileBytes;  // Q slots first: unit u has 2 u and 2 u + 1
+  static constexpr int kOffK = kQSlots * kTileBytes;  // Q first: unit u at 2 u and 2 u + 1
   static constexpr int kOffV = kOffK + kStages * kTileBytes;
   static constexpr int kOffBar = kOffV + kStages * kTileBytes;
-  static constexpr int kNumBars = 2 * kQSlots + 2 * kStages + 14 + 3;
+  static constexpr int kNumBars = 4 + 2 * kStages + 14 + 3;
   static constexpr int kBytes = kOffBar + kNumBars * 8 + 16;
 };
 
@@ -80,7 +80,8 @@ struct PreSeg {
   __device__ int units(const PrefixArgs& p) const { return 2 * (s % p.pairs) + 1 < p.tiles ? 2 : 1; }
 };
 
-// A row of the packed tile, normalised and rotated to fp16, into the swizzled tile at dst.
+// A row of the packed tile, normalised and rotated, as fp16 high and low parts into the swizzled
+// tiles at dst and behind it.
 template <int D>
 __device__ __forceinline__ void pack_query_row(const PagedDecodeArgs& a, int g, int rho, uint8_t* dst, int r) {
   constexpr int kCPR = D / 8;
@@ -112,13 +113,16 @@ __device__ __forceinline__ void pack_query_row(const PagedDecodeArgs& a, int g, 
     if (a.qw) wv = load_rope_chunk<D>(a.qw, c, half);
     const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w}, ww[4] = {wv.x, wv.y, wv.z, wv.w};
     const float cs[4] = {c0.x, c0.z, c1.x, c1.z}, sn[4] = {c0.y, c0.w, c1.y, c1.w};
-    uint32_t h[4];
+    uint32_t h[4], l[4];
 #pragma unroll
     for (int p = 0; p < 4; p++) {
       const float x0 = bf_lo(w[p]) * (rs * bf_lo(ww[p])), x1 = bf_hi(w[p]) * (rs * bf_hi(ww[p]));
-      h[p] = on ? pack_f16(fmaf(x0, cs[p], -x1 * sn[p]), fmaf(x0, sn[p], x1 * cs[p])) : 0u;
+      const float y0 = fmaf(x0, cs[p], -x1 * sn[p]), y1 = fmaf(x0, sn[p], x1 * cs[p]);
+      h[p] = on ? pack_f16(y0, y1) : 0u;
+      l[p] = on ? pack_f16(y0 - f16_lo(h[p]), y1 - f16_hi(h[p])) : 0u;
     }
     *reinterpret_cast<uint4*>(dst + swz(r, c, D * 2)) = make_uint4(h[0], h[1], h[2], h[3]);
+    *reinterpret_cast<uint4*>(dst + PreCfg<D>::kTileBytes + swz(r, c, D * 2)) = make_uint4(l[0], l[1], l[2], l[3]);
   }
 }
 
@@ -129,9 +133,9 @@ __device__ void prefix_role(const PagedDecodeArgs& a, uint8_t* smem, int P, int 
   constexpr int S = C::kStages;
   constexpr int TB = C::kTileBytes;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
-  uint64_t* q_full = bars;                  // [4] Q slots: a warpgroup's 128 rows are packed
-  uint64_t* q_empty = q_full + 4;           // [4] the slot's last S has completed
-  uint64_t* kv_full = q_empty + 4;          // [S]
+  uint64_t* q_full = bars;                  // [2] per unit: its 128 rows are packed
+  uint64_t* q_empty = q_full + 2;           // [2] the segment's last S has completed
+  uint64_t* kv_full = q_empty + 2;          // [S]
   uint64_t* kv_empty = kv_full + S;         // [S] both O += P V issuers are done with the stage
   uint64_t* s_full = kv_empty + S;          // [2] per unit
   uint64_t* s_read = s_full + 2;            // [2] the unit's warpgroup holds its scores in registers
@@ -146,7 +150,7 @@ __device__ void prefix_role(const PagedDecodeArgs& a, uint8_t* smem, int P, int 
 
   if (tid == 0) {
     *abort = 0;
-    for (int k = 0; k < C::kQSlots; k++) {
+    for (int k = 0; k < 2; k++) {
       mbar_init(q_full + k, 4);
       mbar_init(q_empty + k, 1);
     }
@@ -240,15 +244,15 @@ __device__ void prefix_role(const PagedDecodeArgs& a, uint8_t* smem, int P, int 
           const int st = g % S;
           if (!(ok = mbar_wait(kv_full + st, (g / S) & 1, abort))) break;
           for (int u = 0; u < nu; u++) {
-            const int sl = 2 * u + (e[u] & 1);
-            if (n == sg.n0 && !(ok = mbar_wait(q_full + sl, (e[u] >> 1) & 1, abort))) break;
+            if (n == sg.n0 && !(ok = mbar_wait(q_full + u, e[u] & 1, abort))) break;
             // the unit's previous scores are in its warpgroup's registers
             if (m[u] > 0 && !(ok = mbar_wait(s_read + u, (m[u] - 1) & 1, abort))) break;
             tc_fence_after();
-            mma_ss_chain<D / 16>(tmem + C::kColS + 128u * u, dQ0 + (uint64_t)(sl * tstep), kStepK,
-                                 dK0 + (uint64_t)(st * tstep), kStepK, idS, 0u);
+            const uint64_t dq = dQ0 + (uint64_t)(2 * u * tstep), dk = dK0 + (uint64_t)(st * tstep);
+            mma_ss_chain<D / 16>(tmem + C::kColS + 128u * u, dq, kStepK, dk, kStepK, idS, 0u);
+            mma_ss_chain<D / 16>(tmem + C::kColS + 128u * u, dq + (uint64_t)tstep, kStepK, dk, kStepK, idS, 1u);
             mma_commit(s_full + u);
-            if (n + 1 == sg.n1) mma_commit(q_empty + sl);
+            if (n + 1 == sg.n1) mma_commit(q_empty + u);
             m[u]++;
           }
         }
@@ -320,12 +324,11 @@ __device__ void prefix_role(const PagedDecodeArgs& a, uint8_t* smem, int P, int 
     while (ok && sg.next(p)) {
       if (u >= sg.units(p)) continue;
       {
-        const int sl = 2 * u + (e & 1);
-        if (e >= 2) ok = __all_sync(0xffffffffu, mbar_wait(q_empty + sl, ((e >> 1) - 1) & 1, abort));
+        if (e >= 1) ok = __all_sync(0xffffffffu, mbar_wait(q_empty + u, (e - 1) & 1, abort));
         if (!ok) break;
-        pack_query_row<D>(a, sg.s / p.pairs, (2 * (sg.s % p.pairs) + u) * kTile + r, smem + sl * TB, r);
+        pack_query_row<D>(a, sg.s / p.pairs, (2 * (sg.s % p.pairs) + u) * kTile + r, smem + 2 * u * TB, r);
         fence_proxy_async_smem();
-        warp_arrive(q_full + sl);
+        warp_arrive(q_full + u);
         e++;
       }
       float r_run = 0.f, l_run = 0.f;  // running maximum (raw logit units) and sum of the row
