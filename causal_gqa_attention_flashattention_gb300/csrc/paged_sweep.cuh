@@ -847,7 +847,8 @@ cudaError_t launch_sweep_t(const PagedDecodeArgs& a, int nsm, cudaStream_t s) {
   }
   PagedDecodeArgs b = a;
   b.stages = Sweep<D>::kMaxStages;
-  while (b.stages > 2 && sweep_smem(D, b.stages, b.tiles, MT, b.B).total > kSmemMax) b.stages--;
+  const int least = MT < 4 ? 2 : 1;  // two tiles at a time, or one
+  while (b.stages > least && sweep_smem(D, b.stages, b.tiles, MT, b.B).total > kSmemMax) b.stages--;
   int bytes = sweep_smem(D, b.stages, b.tiles, MT, b.B).total;
   if constexpr (PREFIX) bytes = bytes > prefix_smem(D, b.B) ? bytes : prefix_smem(D, b.B);
   if (bytes > kSmemMax) return cudaErrorInvalidValue;

@@ -9,9 +9,8 @@ and the fp32 sum of D terms), a weight by 2 d + 2^-16 (exp2, parts) relative, so
   |o error| <= (2 d + 2^-14) A + the output's rounding,  A = sum_j p_j |v_j|
 (2^-14: the weights' 2^-16 and the fp32 sums over up to thousands of keys), and
   |lse error| <= d + 2^-14 + 2^-22 |lse|.
-With a shared prefix the rows may go through the tiles of the default precision: q as
-one fp16 (2^-11) and the weights as one bf16 (2^-8): d = M 2^-10.9, 2^-8 + 2^-14 in
-place of 2^-14.
+With a shared prefix its weights are one bf16 (2^-8): 2^-8 + 2^-14 in place of 2^-14
+for o; the sums, and so the LSE, keep their bound.
 """
 import numpy as np
 import pytest
@@ -164,7 +163,7 @@ def check(nb, s, got, norm, half, prefix=0):
     nb.check_status()
     ro, rl, A, M = paged.decode_paged(s["fq"], s["fqw"] if norm else None, s["fk"], s["fv"], s["ftable"], s["flens"], BASE,
                                       EPS, half, s["fptable"], bounds=True)
-    d = M * (2.0 ** -10.9 if prefix else 2.0 ** -18 + 2.0 ** -21)
+    d = M * (2.0 ** -18 + 2.0 ** -21)
     w = 2.0 ** -14 + (2.0 ** -8 if prefix else 0)
     go, gl = H.to_f64(o), lse.cpu().numpy().astype(np.float64)
     tol = (2 * d[..., None] + w) * A
@@ -175,7 +174,7 @@ def check(nb, s, got, norm, half, prefix=0):
     empty = np.isneginf(rl)
     assert (np.isneginf(gl) == empty).all() and np.isfinite(gl[~empty]).all()
     dl = np.moveaxis(d, 1, 2)
-    ltol = dl + w + 2.0 ** -22 * np.abs(np.where(empty, 0, rl))
+    ltol = dl + 2.0 ** -14 + 2.0 ** -22 * np.abs(np.where(empty, 0, rl))
     assert (np.abs(np.where(empty, 0, gl) - np.where(empty, 0, rl)) <= ltol).all()
 
 
@@ -255,6 +254,48 @@ def test_prefix_only(nb):
     got = nb.attn_decode_paged(s["q"], s["kp"], s["vp"], s["table"], s["lens"], prefix_table=s["ptable"], prefix_len=64,
                                rope_base=BASE, o_dtype=torch.float32)
     check(nb, s, got, False, False, 64)
+
+
+def test_many_sequences(nb):
+    """More sequences than the sweep has threads, one of them long enough to be cut among blocks."""
+    lens = [(i * 29) % 75 for i in range(900)]
+    lens[417] = 6000
+    s = setup(lens, 2, 6, 3, 32, 16, seed=14)
+    got = nb.attn_decode_paged(s["q"], s["kp"], s["vp"], s["table"], s["lens"], q_weight=s["qw"], rope_base=BASE)
+    check(nb, s, got, True, False)
+
+
+def test_most_sequences_and_rows(nb):
+    """The largest batch with the most rows, against the same sequences in smaller batches (short
+    ones are never cut, so the results are the same bit by bit)."""
+    B, Tq = 4096, 128
+    lens = [(i * 61) % 200 for i in range(B)]
+    lens[4095] = 200
+    pages, D = 16, 64
+    P = 64
+    g = torch.Generator(device="cuda").manual_seed(2)
+    kp = torch.randn((P, 1, pages, D), generator=g, device="cuda").half()
+    vp = torch.randn((P, 1, pages, D), generator=g, device="cuda").bfloat16()
+    table = torch.randint(0, P, (B, 13), generator=g, device="cuda", dtype=torch.int32)
+    q = torch.randn((B, Tq, 1, D), generator=g, device="cuda").bfloat16()
+    n = i32(lens)
+    o, lse = nb.attn_decode_paged(q, kp, vp, table, n, rope_base=BASE)
+    nb.check_status()
+    for lo, hi in ((0, 1500), (1500, 4096)):
+        a, b = nb.attn_decode_paged(q[lo:hi], kp, vp, table[lo:hi], n[lo:hi], rope_base=BASE)
+        assert torch.equal(a, o[lo:hi]) and torch.equal(b, lse[lo:hi])
+
+
+def test_keys_after_a_query_do_not_matter(nb):
+    """Infinite and NaN keys at the positions of later new tokens."""
+    s = setup([300, 33], 3, 4, 2, 64, 16, seed=15)
+    args = (s["vp"], s["table"], s["lens"])
+    want = nb.attn_decode_paged(s["q"], s["kp"], *args, rope_base=BASE)
+    kp = s["kp"].clone()
+    for b, n in enumerate((300, 33)):
+        kp[int(s["table"][b, (n - 1) // 16]), :, (n - 1) % 16] = float("nan") if b else float("inf")
+    got = nb.attn_decode_paged(s["q"], kp, *args, rope_base=BASE)
+    assert torch.equal(got[0][:, :2], want[0][:, :2]) and torch.equal(got[1][:, :, :2], want[1][:, :, :2])
 
 
 def test_large_logits(nb):
@@ -339,6 +380,79 @@ def test_streams_and_graphs(nb):
         torch.cuda.synchronize()
         for o in outs:
             assert torch.equal(o[0], wants[k][0]) and torch.equal(o[1], wants[k][1])
+
+
+def test_two_streams_at_once(nb):
+    """Calls that run side by side on streams of their own, with the library's workspaces."""
+    lens = [5000, 2000, 40, 3000]
+    sets = [setup(lens, 1, 12, 4, 64, 16, seed=50 + i) for i in range(2)]
+    call = lambda s, **kw: nb.attn_decode_paged(s["q"], s["kp"], s["vp"], s["table"], s["lens"], rope_base=BASE, **kw)
+    wants = [call(s) for s in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    outs = [[], []]
+    for _ in range(20):
+        for i in range(2):
+            outs[i].append(call(sets[i], stream=streams[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for o in outs[i]:
+            assert torch.equal(o[0], wants[i][0]) and torch.equal(o[1], wants[i][1])
+
+
+def test_step_in_a_graph(nb):
+    """Append and decode over a shared prefix captured together and replayed as the sequences grow."""
+    B, Hq, Hkv, D, page, prefix = 5, 12, 4, 64, 32, 128
+    g = torch.Generator(device="cuda").manual_seed(9)
+    r = lambda *s: torch.randn(s, generator=g, device="cuda")
+    kp, vp = r(40, Hkv, page, D).half(), r(40, Hkv, page, D).bfloat16()
+    table = torch.randperm(40, generator=g, device="cuda")[:35].to(torch.int32).view(B, 7).contiguous()
+    shared = table[0, :4].clone()
+    table[:, :4] = shared
+    q, k, v = r(B, 1, Hq, D).bfloat16(), r(B, Hkv, D).bfloat16(), r(B, Hkv, D).bfloat16()
+    kw, qw = torch.ones(D, device="cuda").bfloat16(), (1 + 0.1 * r(D)).bfloat16()
+    pos = i32([130, 128, 140, 131, 200])
+    n = pos + 1
+
+    def step(kp, vp, n, pos):
+        nb.kv_append_paged(k, v, kp, vp, table, pos, k_weight=kw, rope_base=BASE)
+        return nb.attn_decode_paged(q, kp, vp, table, n, q_weight=qw, rope_base=BASE, prefix_table=shared, prefix_len=prefix)
+
+    eager_k, eager_v = kp.clone(), vp.clone()
+    step(eager_k.clone(), eager_v.clone(), n, pos)  # tables of the shape exist before the capture
+    gpos, gn = torch.zeros_like(pos), torch.zeros_like(n)
+    gpos.copy_(pos)
+    gn.copy_(n)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step(kp, vp, gn, gpos)
+    for i in range(4):
+        for t, x in ((k, r(B, Hkv, D)), (v, r(B, Hkv, D)), (q, r(B, 1, Hq, D))):
+            t.copy_(x)
+        gpos.copy_(pos + i)
+        gn.copy_(n + i)
+        graph.replay()
+        want = step(eager_k, eager_v, n + i, pos + i)
+        torch.cuda.synchronize()
+        assert torch.equal(kp, eager_k) and torch.equal(vp, eager_v)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_kernel_kinds(nb):
+    """Every launch of the new calls is counted under its kind."""
+    s = setup([100, 90], 1, 4, 2, 64, 16, seed=3, prefix=64)
+    nb.profile_start(64)
+    nb.attn_decode_paged(s["q"], s["kp"], s["vp"], s["table"], s["lens"], prefix_table=s["ptable"], prefix_len=64)
+    nb.attn_decode_paged(s["q"], s["kp"], s["vp"], s["table"].clamp(0), s["lens"])
+    nb.kv_append_paged(s["q"][:, 0, :2].contiguous(), s["q"][:, 0, 2:].contiguous(), s["kp"], s["vp"], s["table"], i32([99, 89]))
+    q = torch.randn((1, 4, 2, 32), device="cuda").bfloat16()
+    w = torch.ones(32, device="cuda").bfloat16()
+    nb.qk_norm(q, q, w, w)
+    nb.qk_norm_bwd(q, q, w, w, q, q)
+    got = nb.profile_stop()
+    assert {k: v[1] for k, v in got.items() if v[1]} == dict(decode_prefix=1, decode_paged=1, kv_append_paged=1, qk_norm=1,
+                                                             qk_norm_bwd=1)
+    assert all(got[k][0] > 0 for k in ("decode_prefix", "decode_paged", "kv_append_paged", "qk_norm", "qk_norm_bwd"))
 
 
 def test_far_pages(nb):
