@@ -436,20 +436,20 @@ def _int32(t, name, device, shape):
         raise ValueError("%s must be a contiguous int32 %s on the call's device" % (name, list(shape)))
 
 
-def _with_workspace(call, workspace, made, device, size):
-    """call(pointer, bytes) with the caller's workspace; without one with NULL (the library's
-    own for the stream) or, where a capture needs one, a tensor of the capture's own."""
-    if workspace is not None:
-        _need(workspace.dtype == torch.uint8 and workspace.device == device, "workspace must be uint8 on the call's device")
-        return call(workspace.data_ptr(), workspace.numel())
-    try:
-        return call(None, 0)
-    except NeAttnError as e:
-        if e.status != ERR_WORKSPACE:
-            raise
-    workspace = torch.empty(size(), dtype=torch.uint8, device=device)
-    made.append(workspace)
-    return call(workspace.data_ptr(), workspace.numel())
+def _run_ws(name, device, stream, made, args, workspace, size):
+    """_run with the workspace as the last arguments: the caller's; without one NULL (the
+    library's own for the stream) or, where a capture needs one, a tensor of the capture's own."""
+    if workspace is None:
+        try:
+            return _run(name, device, stream, made, *args, None, 0)
+        except NeAttnError as e:
+            if e.status != ERR_WORKSPACE:
+                raise
+        workspace = torch.empty(size(), dtype=torch.uint8, device=device)
+        made.append(workspace)
+    elif workspace.dtype != torch.uint8 or workspace.device != device:
+        raise ValueError("workspace must be uint8 on the call's device")
+    _run(name, device, stream, made, *args, workspace.data_ptr(), workspace.numel())
 
 
 def qk_norm(q, k, q_weight, k_weight, eps=1e-6, rope_base=10000.0, rope_half=False, workspace=None, stream=None):
@@ -507,14 +507,11 @@ def qk_norm_bwd(q, k, q_weight, k_weight, dqn, dkn, eps=1e-6, dq=None, dk=None, 
     dqw = torch.empty(D, dtype=torch.float32, device=dev)
     dkw = torch.empty(D, dtype=torch.float32, device=dev)
     made += (dqw, dkw)
-    flags = GRAD_FP32 if dt == torch.float32 else 0
-
-    def call(ws, size):
-        _run("ne_attn_qk_norm_bwd", dev, stream, made, q.data_ptr(), k.data_ptr(), q_weight.data_ptr(),
-             k_weight.data_ptr(), dqn.data_ptr(), dkn.data_ptr(), dq.data_ptr(), dk.data_ptr(), dqw.data_ptr(),
-             dkw.data_ptr(), B, T, Hq, Hkv, D, qs, ks, dqs, dks, eps, flags, ws, size)
-
-    _with_workspace(call, workspace, made, dev, lambda: int(lib().ne_attn_qk_norm_bwd_workspace_size(B, T, Hq, Hkv, D)))
+    args = (q.data_ptr(), k.data_ptr(), q_weight.data_ptr(), k_weight.data_ptr(), dqn.data_ptr(), dkn.data_ptr(),
+            dq.data_ptr(), dk.data_ptr(), dqw.data_ptr(), dkw.data_ptr(), B, T, Hq, Hkv, D, qs, ks, dqs, dks, eps,
+            GRAD_FP32 if dt == torch.float32 else 0)
+    _run_ws("ne_attn_qk_norm_bwd", dev, stream, made, args, workspace,
+            lambda: int(lib().ne_attn_qk_norm_bwd_workspace_size(B, T, Hq, Hkv, D)))
     return dq, dk, dqw, dkw
 
 
@@ -527,15 +524,21 @@ def paged_cache(num_pages, page_size, Hkv, D, device):
 
 def _pools(k_pages, v_pages, Hkv, D, device):
     """(number of pages, page size, page stride) of the two pools."""
-    P, H, page, d = k_pages.shape
-    _need(v_pages.shape == k_pages.shape and H == Hkv and d == D, "pools must be [num_pages, Hkv, page_size, D]")
-    _need(k_pages.dtype == torch.float16 and v_pages.dtype == torch.bfloat16 and k_pages.device == device
-          and v_pages.device == device, "pools must be float16 keys and bfloat16 values on the call's CUDA device")
-    stride = k_pages.stride(0) if P > 1 else Hkv * page * D
-    for t in (k_pages, v_pages):
-        s = t.stride()
-        _need(s[3] == 1 and s[2] == D and (H == 1 or s[1] == page * D) and (P == 1 or s[0] == stride),
-              "pools must be contiguous inside a page and have one page stride")
+    shape = k_pages.shape
+    P, H, page, d = shape
+    if v_pages.shape != shape or H != Hkv or d != D:
+        raise ValueError("pools must be [num_pages, Hkv, page_size, D]")
+    if (k_pages.dtype != torch.float16 or v_pages.dtype != torch.bfloat16 or k_pages.device != device
+            or v_pages.device != device):
+        raise ValueError("pools must be float16 keys and bfloat16 values on the call's CUDA device")
+    sk, sv = k_pages.stride(), v_pages.stride()
+    stride = sk[0] if P > 1 else H * page * D
+    inner = (page * D, D, 1)
+    if sk[1:] != inner or sv != sk:
+        # strides of dimensions of one do not matter
+        for t in (sk, sv):
+            if t[3] != 1 or t[2] != D or (H > 1 and t[1] != page * D) or (P > 1 and t[0] != stride):
+                raise ValueError("pools must be contiguous inside a page and have one page stride")
     return P, page, stride
 
 
@@ -597,22 +600,22 @@ def attn_decode_paged(q, k_pages, v_pages, page_table, kv_len, q_weight=None, ep
     if o is None:
         o = torch.empty((B, Tq, Hq, D), dtype=o_dtype, device=dev)
         made.append(o)
+    elif o.device != dev or not o.is_contiguous() or o.shape != (B, Tq, Hq, D):
+        raise ValueError("o must be a contiguous [B, Tq, Hq, D] on the call's device")
     if lse is None:
         lse = torch.empty((B, Hq, Tq), dtype=torch.float32, device=dev)
         made.append(lse)
-    _need(o.dtype in (torch.bfloat16, torch.float32) and o.device == dev and o.is_contiguous()
-          and o.shape == (B, Tq, Hq, D), "o must be a contiguous bfloat16 or float32 [B, Tq, Hq, D]")
-    _need(lse.dtype == torch.float32 and lse.device == dev and lse.is_contiguous() and lse.shape == (B, Hq, Tq),
-          "lse must be a contiguous float32 [B, Hq, Tq]")
-    flags = (O_FP32 if o.dtype == torch.float32 else 0) | (ROPE_HALF if rope_half else 0)
-    ptable = prefix_table.data_ptr() if prefix_len else None
-
-    def call(ws, size):
-        _run("ne_attn_decode_paged", dev, stream, made, q.data_ptr(), _optr(q_weight), k_pages.data_ptr(),
-             v_pages.data_ptr(), page_table.data_ptr(), kv_len.data_ptr(), ptable, o.data_ptr(), lse.data_ptr(),
-             B, Tq, Hq, Hkv, D, page, P, width, stride, qs, prefix_len, eps, rope_base, flags, ws, size)
-
-    _with_workspace(call, workspace, made, dev, lambda: decode_paged_workspace_size(B, Tq, Hq, Hkv, D, prefix_len))
+    elif lse.dtype != torch.float32 or lse.device != dev or not lse.is_contiguous() or lse.shape != (B, Hq, Tq):
+        raise ValueError("lse must be a contiguous float32 [B, Hq, Tq] on the call's device")
+    fp32 = o.dtype == torch.float32
+    if not fp32 and o.dtype != torch.bfloat16:
+        raise ValueError("o must be bfloat16 or float32")
+    args = (q.data_ptr(), None if q_weight is None else q_weight.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
+            page_table.data_ptr(), kv_len.data_ptr(), prefix_table.data_ptr() if prefix_len else None, o.data_ptr(),
+            lse.data_ptr(), B, Tq, Hq, Hkv, D, page, P, width, stride, qs, prefix_len, eps, rope_base,
+            (O_FP32 if fp32 else 0) | (ROPE_HALF if rope_half else 0))
+    _run_ws("ne_attn_decode_paged", dev, stream, made, args, workspace,
+            lambda: decode_paged_workspace_size(B, Tq, Hq, Hkv, D, prefix_len))
     return o, lse
 
 
