@@ -532,7 +532,7 @@ size_t qk_norm_bwd_ws_bytes(int D) { return qk_norm_bwd_part_bytes(D) + 256; }
 // Paged cache: page sizes, the pool's stride, and the longest sequence a table
 // row can hold (its positions index the rotary table).
 static_assert(kPagedMaxBlocks * sizeof(unsigned) <= kCounterBytes, "counters of one stream");
-constexpr int kPagedMaxBatch = 4096;
+constexpr int kPagedMaxBatch = 2048;  // lengths and tile counts of the sweep in shared memory
 constexpr int kPagedMaxPositions = 1 << 20;
 int check_paged(int B, int Hq, int Hkv, int D, int page_size, int num_pages, int max_pages, long long page_stride) {
   if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || num_pages < 1 || max_pages < 1) return NE_ERR_ARG;
@@ -1533,13 +1533,9 @@ int ne_attn_decode_paged(const void* q, const void* q_w, const void* k_pages, co
   a.part_ml = reinterpret_cast<float2*>(ws + w.part_ml);
   int mt = 1;
   paged_rows(a.R, &mt, &a.tiles, &a.MG);
-  const int rows = page_size < (D == 64 ? 128 : 256) ? page_size : (D == 64 ? 128 : 256);
-  if ((st = make_map_pages(&a.map_k, k_pages, num_pages, Hkv, page_size, D, page_stride, rows,
-                           CU_TENSOR_MAP_DATA_TYPE_FLOAT16)) != NE_OK)
-    return st;
-  if ((st = make_map_pages(&a.map_v, v_pages, num_pages, Hkv, page_size, D, page_stride, rows,
-                           CU_TENSOR_MAP_DATA_TYPE_BFLOAT16)) != NE_OK)
-    return st;
+  a.kp = static_cast<const __half*>(k_pages);
+  a.vp = static_cast<const __nv_bfloat16*>(v_pages);
+  a.page_stride = page_stride;
   if (prefix_len > 0 && nsm > 1) {
     a.base = prefix_len;
     PrefixArgs& p = a.pre;

@@ -254,8 +254,10 @@ struct PrefixCut {
 #endif
 
 struct PagedDecodeArgs {
-  CUtensorMap map_k, map_v;     // pools {D, page, Hkv, num_pages}, box D x min(page, tile) rows
-  CUtensorMap map_pk, map_pv;   // the same with the prefix's tile of 128 positions
+  CUtensorMap map_pk, map_pv;   // prefix: pools {D, page, Hkv, num_pages}, box D x min(page, 128) rows
+  const __half* kp;             // pools, pages page_stride values apart
+  const __nv_bfloat16* vp;
+  long long page_stride;
   PrefixArgs pre;
   const __nv_bfloat16 *q, *qw;  // [B, Tq, Hq, D], positions q_stride values apart; qw [D] or null
   const int *table, *len, *prefix_table;
@@ -270,7 +272,6 @@ struct PagedDecodeArgs {
   int B, Tq, Hq, Hkv, D, G, R, page_shift, num_pages, max_pages, prefix_len, rope_half, o_fp32;
   int base;         // shared positions that the prefix kernel reads (0: none, the sweep reads all)
   int tiles, MG;    // packed row tiles (8 rows each) and the groups of warps that share them
-  int stages;
   FastDiv div_grid; // by the sweep's blocks
   int own_counters; // done is the library's: 0 before and after every call
   float eps, scale_log2;

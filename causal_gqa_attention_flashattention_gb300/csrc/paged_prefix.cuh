@@ -56,7 +56,7 @@ inline int prefix_smem(int D, int B) {
 // counted as 1.64 of the sweep's (measured: 64 sequences on 8192 positions 24.5, 19.9 and 23.1 us
 // at 1.27, 1.64 and 2.18; 128 on 16384 41.9, 39.6 and 42.4 us).
 __device__ __forceinline__ int prefix_blocks(const PagedDecodeArgs& a, int sweep_tiles, int blocks) {
-  const float mine = 1.64f * (float)a.pre.W, theirs = (float)sweep_tiles;
+  const float mine = 1.64f * (float)a.pre.W, theirs = (float)sweep_tiles * (a.D == 64 ? 1.f : 0.5f);
   const int P = __float2int_rn((float)blocks * __fdiv_rn(mine, mine + theirs));
   return max(1, min(min(P, blocks - 1), a.pre.W));
 }

@@ -33,22 +33,23 @@ namespace {
 // registers) needs no hand-off between warps per tile.
 template <int D>
 struct Sweep {
-  static constexpr int kTK = D == 64 ? 128 : 256;  // positions of a tile
   static constexpr uint32_t kSpan = D * 2;
-  static constexpr int kHalf = kTK * (int)kSpan;   // bytes of a tile's keys (as many of values)
-  static constexpr int kStage = 2 * kHalf;
-  static constexpr int kSlices = kTK / 16;
-  static constexpr int kMaxStages = 6;
+  static constexpr int kSlot = 2 * 16 * (int)kSpan;  // 16 keys and their values
 };
-// Eight consumer warps, then a warpgroup of the producer, the queries and two finishing warps.
+constexpr int kTK = 128;  // positions of a tile: a slice of 16 for each consumer warp
+// Slices that a consumer warp has room for.
+template <int D, int MT>
+constexpr int kDepth = D == 64 ? (MT == 1 ? 5 : (MT == 2 ? 4 : 3)) : (MT < 4 ? 8 : 6);
+// Eight consumer warps, then a warpgroup of the queries, two finishing warps and an idle one.
 // (Sixteen consumers in two groups on alternate tiles measured slower: a short context 8.4 us
 // against 7.4, 16 contexts around 8192 positions 31.9 against 31.4.)
 constexpr int kWarps = 8;
 constexpr int kSweepThreads = (kWarps + 4) * 32;
-constexpr int kWholeTiles = 8;  // a (sequence, head) of at most this many tiles is never split
+// A (sequence, head) of at most this many tiles is never split.
+constexpr int whole_tiles(int D) { return D == 64 ? 8 : 16; }
 
 // Buffers for the warps' parts of a finished segment, each with a finishing warp of its own.
-constexpr int sweep_bufs(int mt) { return mt < 4 ? 2 : 1; }
+constexpr int sweep_bufs(int D, int mt) { return D * mt <= 64 ? 2 : 1; }
 
 // Shared memory: barriers, the block's plan and the sequences' lengths first, then (from a
 // 1024-byte boundary) the ring and what else a role keeps.  tiles: packed row tiles, mt: of one warp.
@@ -57,12 +58,14 @@ __host__ __device__ constexpr int paged_head(int B) { return (kOffCum + (2 * B +
 struct SweepSmem {
   int ring, q, scratch, ml, total;
 };
-__host__ __device__ constexpr SweepSmem sweep_smem(int D, int stages, int tiles, int mt, int B) {
+// Query tiles of two segments, where there are not too many.
+__host__ __device__ constexpr int sweep_qbufs(int tiles) { return tiles <= 8 ? 2 : 1; }
+__host__ __device__ constexpr SweepSmem sweep_smem(int D, int depth, int tiles, int mt, int B) {
   SweepSmem m = {};
-  const int rows = sweep_bufs(mt) * kWarps * mt * 8;
+  const int rows = sweep_bufs(D, mt) * kWarps * mt * 8;
   m.ring = paged_head(B);
-  m.q = m.ring + stages * 32768;
-  m.scratch = m.q + 2 * tiles * 16 * D * 2;
+  m.q = m.ring + kWarps * depth * 2 * 16 * D * 2;
+  m.scratch = m.q + sweep_qbufs(tiles) * tiles * 16 * D * 2;
   m.ml = m.scratch + rows * D * 4;
   m.total = m.ml + rows * 8 + 1024;
   return m;
@@ -79,6 +82,16 @@ __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(addr)
                : "memory");
+}
+// 16 bytes global -> shared past L1; n = 0 reads nothing and writes zeros.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, uint32_t n) {
+  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Until all but the newest N groups of this thread have landed.
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -99,7 +112,7 @@ struct SweepPlan {
 };
 struct Tiles {
   const int* cum;  // shared memory: tiles before sequence b (one head)
-  int B, Hkv;
+  int B, Hkv, whole;
   // the same by a whole warp for one x: 32 probes at a time
   __device__ int find_warp(int x, int lane) const {
     int lo = 0, hi = B;
@@ -123,7 +136,7 @@ struct Tiles {
     return lo;
   }
   // A block's stretch starts at tile x = c base + min(c, rem), moved to the nearer end of a
-  // (sequence, head) of at most kWholeTiles tiles it would cut: joining a cut one costs about
+  // (sequence, head) of at most `whole` tiles it would cut: joining a cut one costs about
   // 3 us at the end, as much as five tiles, moving the boundary at most half the tiles.
   // Inside longer ones the boundaries stay, so owner() needs the unmoved starts only.
   __device__ int start(const SweepPlan& p, int c) const {
@@ -132,7 +145,7 @@ struct Tiles {
   }
   __device__ int moved(int x, int i) const {  // x in sequence i
     const int n = cum[i + 1] - cum[i];
-    if (n > kWholeTiles) return x;
+    if (n > whole) return x;
     const int off = (x - cum[i] * Hkv) % n;
     return 2 * off < n ? x - off : x - off + n;
   }
@@ -193,7 +206,7 @@ struct RowSum {
 };
 
 struct SweepBars {
-  uint64_t *full, *empty, *q_full, *q_empty, *parts_full, *parts_empty, *fin;
+  uint64_t *q_full, *q_empty, *parts_full, *parts_empty, *fin;
 };
 
 // What a consumer warp holds of a segment: MT row tiles' queries (in registers for at most two
@@ -321,26 +334,97 @@ __device__ bool sweep_consume(const PagedDecodeArgs& a, SegWalk sw, const int* l
                               const SweepBars& bar, const volatile int* abort, int warp, int lane) {
   using C = Sweep<D>;
   constexpr int KS = D / 16;
-  constexpr int kBufs = sweep_bufs(MT);
+  constexpr int kBufs = sweep_bufs(D, MT);
   const int KG = MT < 4 ? kWarps : kWarps / a.MG;  // warps over a tile's keys; the rest share the row tiles out
   const int mg = warp / KG, kg = warp - mg * KG;
-  const uint32_t ring = smem_u32(smem + L.ring);
   const float sl2 = a.scale_log2;
   const uint32_t lrow = lane & 15, lchk = lane >> 4;
-  int st = 0, ph = 0, seg = 0;
-  const auto turn = [&]() {
-    if (++st == a.stages) {
-      st = 0;
-      ph ^= 1;
-    }
+  constexpr int S = kDepth<D, MT>, kN = kSlicesAtOnce<D, MT>;
+  constexpr int kCPR = D / 8, kCopies = 16 * kCPR / 32;  // 16-byte chunks of a row; of a slice, per lane
+  const int lm = MT < 4 ? 0 : (a.MG == 1 ? 0 : (a.MG == 2 ? 1 : 2));  // log2 of a tile's slices per warp
+  const uint32_t ring = smem_u32(smem + L.ring) + (uint32_t)warp * S * C::kSlot;
+  // Slice k of a segment is 16 positions from place(segment, k).  The warp copies its own slices,
+  // S ahead of the one it works on: no other warp reads them, so a copy needs no barrier, and a
+  // slice lies in one page, so small pages cost nothing (with tiled copies by a producer warp,
+  // pages of 16 took 0.87 us a tile and larger ones 0.70).
+  const auto slices = [&](const SegWalk& s) { return (s.n1 - s.n0) << lm; };
+  const auto place = [&](const SegWalk& s, int k) {
+    return (s.n0 + (k >> lm)) * kTK + (kg + (k & ((1 << lm) - 1)) * KG) * 16;
   };
+  // Page numbers come 32 slices at a time, one to a lane and a window ahead: -1 where nothing is
+  // to be read, -2 for a bad page.
+  const auto window = [&](const SegWalk& s, int k0) {
+    const int base = sweep_base(a, len[s.b]), own = len[s.b] - base, k = k0 + lane;
+    int id = -1;
+    if (k < slices(s)) {
+      const int j0 = place(s, k);
+      if (j0 < own) {
+        const int i = (base + j0) >> a.page_shift;
+        id = i < (a.prefix_len >> a.page_shift) ? a.prefix_table[i] : a.table[(size_t)s.b * a.max_pages + i];
+        if (id < 0 || id >= a.num_pages) {
+          record_page(a.status);
+          id = -2;
+        }
+      }
+    }
+    return id;
+  };
+  SegWalk is = sw, ls = sw;  // the segment being copied, and that of the window after this one
+  bool ion = is.next(), lon = ls.next();
+  int ik = 0, iw = 0, lk = 0, islot = 0, id = -1, nid = -1;
+  const auto look = [&]() {
+    if (!lon) return;
+    if (lk + 32 < slices(ls)) {
+      lk += 32;
+    } else {
+      lon = ls.next();
+      lk = 0;
+    }
+    nid = lon ? window(ls, lk) : -1;
+  };
+  if (ion) id = window(is, 0);
+  look();
+  const auto issue = [&]() {
+    if (ion && (ik - iw == 32 || ik == slices(is))) {
+      is = ls;
+      ion = lon;
+      ik = iw = lk;
+      id = nid;
+      look();
+    }
+    if (ion) {
+      const int page = __shfl_sync(0xffffffffu, id, ik - iw);
+      if (page != -1) {
+        const int j0 = place(is, ik);
+        const size_t at = (size_t)max(page, 0) * a.page_stride +
+                          (((size_t)is.g << a.page_shift) + (j0 & ((1 << a.page_shift) - 1))) * D + lane * 8;
+        const uint32_t n = page < 0 ? 0u : 16u, to = ring + islot * C::kSlot;
+#pragma unroll
+        for (int i = 0; i < kCopies; i++) {
+          const uint32_t row = i * (32 / kCPR) + lane / kCPR, off = swz(row, lane % kCPR, C::kSpan);
+          copy16(to + off, a.kp + at + i * 256, n);
+          copy16(to + C::kSlot / 2 + off, a.vp + at + i * 256, n);
+        }
+      }
+      ik++;
+    }
+    copy_commit();
+    islot = islot + 1 == S ? 0 : islot + 1;
+  };
+#pragma unroll 1
+  for (int i = 0; i < S; i++) issue();
+  int cslot = 0, seg = 0;
+  const int qbufs = sweep_qbufs(a.tiles);
   for (; sw.next(); seg++) {
     SweepState<D, MT> w;
     const int total = len[sw.b];
     w.own = total - sweep_base(a, total);
     w.pos0 = w.own - a.Tq;
-    const int qs = seg & 1;
-    if (!__all_sync(0xffffffffu, mbar_wait(bar.q_full + qs, (seg >> 1) & 1, abort))) return false;
+    const int qs = qbufs == 2 ? seg & 1 : 0;
+    if (!__all_sync(0xffffffffu, mbar_wait(bar.q_full + qs, (qbufs == 2 ? seg >> 1 : seg) & 1, abort))) {
+      copy_wait<0>();
+      return false;
+    }
     w.qbase = smem_u32(smem + L.q) + (uint32_t)((qs * a.tiles + mg * MT) * 16) * C::kSpan;
     if (MT <= 2) {
 #pragma unroll
@@ -361,57 +445,45 @@ __device__ bool sweep_consume(const PagedDecodeArgs& a, SegWalk sw, const int* l
 #pragma unroll
         for (int e = 0; e < 4; e++) w.o[m][i][e] = 0.f;
     }
-    for (int n = sw.n0; n < sw.n1; n++) {
-      if (!__all_sync(0xffffffffu, mbar_wait(bar.full + st, ph, abort))) return false;
-      const uint32_t kb = ring + st * C::kStage;
-      if constexpr (kSlicesAtOnce<D, MT> == 2 && C::kSlices == kWarps && MT < 4) {
-        // one slice of a tile for each warp: two tiles at a time
-        const uint32_t at = (uint32_t)kg * 16 * C::kSpan;
-        const int j0 = n * C::kTK + kg * 16, st0 = st;
-        turn();
-        if (n + 1 < sw.n1) {
-          if (!__all_sync(0xffffffffu, mbar_wait(bar.full + st, ph, abort))) return false;
-          const uint32_t kb2 = ring + st * C::kStage;
-          if (j0 < w.own) {
-            const uint32_t k2[2] = {kb + at, kb2 + at}, v2[2] = {k2[0] + C::kHalf, k2[1] + C::kHalf};
-            const int j2[2] = {j0, j0 + C::kTK};
-            sweep_slices<D, MT, 2>(w, k2, v2, j2, sl2, lane);
-          }
-          warp_arrive(bar.empty + st0);
-          warp_arrive(bar.empty + st);
-          turn();
-          n++;
-        } else {
-          if (j0 < w.own) {
-            const uint32_t k1[1] = {kb + at}, v1[1] = {kb + at + C::kHalf};
-            const int j1[1] = {j0};
-            sweep_slices<D, MT, 1>(w, k1, v1, j1, sl2, lane);
-          }
-          warp_arrive(bar.empty + st0);
+    const int cnt = slices(sw);
+    for (int k = 0; k < cnt;) {
+      const int j0 = place(sw, k);
+      const uint32_t k0 = ring + cslot * C::kSlot;
+      cslot = cslot + 1 == S ? 0 : cslot + 1;
+      if (kN == 2 && k + 1 < cnt) {
+        const uint32_t k1 = ring + cslot * C::kSlot;
+        cslot = cslot + 1 == S ? 0 : cslot + 1;
+        copy_wait<S - 2>();
+        __syncwarp();
+        if (j0 < w.own) {
+          const uint32_t kb[2] = {k0, k1}, vb[2] = {k0 + C::kSlot / 2, k1 + C::kSlot / 2};
+          const int jn[2] = {j0, place(sw, k + 1)};
+          sweep_slices<D, MT, 2>(w, kb, vb, jn, sl2, lane);
         }
-        continue;
-      }
-      constexpr int N = kSlicesAtOnce<D, MT>;
-      for (int sl = kg; sl < C::kSlices; sl += N * KG) {
-        const int j0 = n * C::kTK + sl * 16;
-        if (j0 >= w.own) break;
-        uint32_t kn[N], vn[N];
-        int jn[N];
-#pragma unroll
-        for (int i = 0; i < N; i++) {
-          kn[i] = kb + (uint32_t)(sl + i * KG) * 16 * C::kSpan;
-          vn[i] = kn[i] + C::kHalf;
-          jn[i] = j0 + i * KG * 16;
+        __syncwarp();
+        issue();
+        issue();
+        k += 2;
+      } else {
+        copy_wait<S - 1>();
+        __syncwarp();
+        if (j0 < w.own) {
+          const uint32_t kb[1] = {k0}, vb[1] = {k0 + C::kSlot / 2};
+          const int jn[1] = {j0};
+          sweep_slices<D, MT, 1>(w, kb, vb, jn, sl2, lane);
         }
-        sweep_slices<D, MT, N>(w, kn, vn, jn, sl2, lane);
+        __syncwarp();
+        issue();
+        k++;
       }
-      warp_arrive(bar.empty + st);
-      turn();
     }
     if (MT > 2) warp_arrive(bar.q_empty + qs);
     // the warps' parts go to shared memory, where a finishing warp joins them
     const int buf = seg % kBufs, use = seg / kBufs;
-    if (use > 0 && !__all_sync(0xffffffffu, mbar_wait(bar.parts_empty + buf, (use - 1) & 1, abort))) return false;
+    if (use > 0 && !__all_sync(0xffffffffu, mbar_wait(bar.parts_empty + buf, (use - 1) & 1, abort))) {
+      copy_wait<0>();
+      return false;
+    }
     float* scratch = reinterpret_cast<float*>(smem + L.scratch) + buf * kWarps * MT * 8 * D;
     float2* ml = reinterpret_cast<float2*>(smem + L.ml) + buf * kWarps * MT * 8;
 #pragma unroll
@@ -428,6 +500,7 @@ __device__ bool sweep_consume(const PagedDecodeArgs& a, SegWalk sw, const int* l
     }
     warp_arrive(bar.parts_full + buf);
   }
+  copy_wait<0>();
   return true;
 }
 
@@ -459,7 +532,7 @@ template <int D, int MT, bool PREFIX>
 __device__ bool sweep_finish(const PagedDecodeArgs& a, SegWalk sw, const Tiles& tl, const SweepPlan& plan, const int* len,
                              uint8_t* smem, const SweepSmem& L, const SweepBars& bar, volatile int* todo,
                              const volatile int* abort, int blk, int f, int lane) {
-  constexpr int kBufs = sweep_bufs(MT);
+  constexpr int kBufs = sweep_bufs(D, MT);
   const int parts = MT < 4 ? kWarps : kWarps / a.MG;  // warps that hold a part of a row
   const float* scratch = reinterpret_cast<const float*>(smem + L.scratch) + f * kWarps * MT * 8 * D;
   const float2* ml = reinterpret_cast<const float2*>(smem + L.ml) + f * kWarps * MT * 8;
@@ -579,16 +652,13 @@ __device__ bool sweep_join(const PagedDecodeArgs& a, const Tiles& tl, const Swee
 // by the tensor cores and exponentials, the other by HBM, and they run side by side.
 template <int D, int MT, bool PREFIX>
 __global__ void __launch_bounds__(kSweepThreads, 1) k_paged_sweep(const __grid_constant__ PagedDecodeArgs a) {
-  using C = Sweep<D>;
-  constexpr int kThreads = kSweepThreads, kBufs = sweep_bufs(MT);
+  constexpr int kThreads = kSweepThreads, kBufs = sweep_bufs(D, MT);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  const SweepSmem L = sweep_smem(D, a.stages, a.tiles, MT, a.B);
+  const SweepSmem L = sweep_smem(D, kDepth<D, MT>, a.tiles, MT, a.B);
   SweepBars bar;
-  bar.full = reinterpret_cast<uint64_t*>(smem);
-  bar.empty = bar.full + C::kMaxStages;
-  bar.q_full = bar.empty + C::kMaxStages;   // [2]
+  bar.q_full = reinterpret_cast<uint64_t*>(smem);  // [2]
   bar.q_empty = bar.q_full + 2;             // [2]
   bar.parts_full = bar.q_empty + 2;         // [2] a segment's parts are in shared memory
   bar.parts_empty = bar.parts_full + 2;     // [2] and have been read
@@ -617,7 +687,7 @@ __global__ void __launch_bounds__(kSweepThreads, 1) k_paged_sweep(const __grid_c
       }
       n = max(n, 0);
       len[b] = n;
-      nt = max(1, (n - sweep_base(a, n) + C::kTK - 1) / C::kTK);  // one even where nothing is read: its rows are written
+      nt = max(1, (n - sweep_base(a, n) + kTK - 1) / kTK);  // one even where nothing is read: its rows are written
     }
     int x = nt;
     if (b0 + warp * 32 < a.B) {
@@ -654,10 +724,6 @@ __global__ void __launch_bounds__(kSweepThreads, 1) k_paged_sweep(const __grid_c
   if (tid == 32) {
     *abort = 0;
     todo[0] = todo[1] = -1;
-    for (int i = 0; i < a.stages; i++) {
-      mbar_init(bar.full + i, 1);
-      mbar_init(bar.empty + i, kWarps);
-    }
     for (int i = 0; i < 2; i++) {
       mbar_init(bar.q_full + i, 1);
       mbar_init(bar.q_empty + i, kWarps);
@@ -667,14 +733,11 @@ __global__ void __launch_bounds__(kSweepThreads, 1) k_paged_sweep(const __grid_c
     mbar_init(bar.fin, kBufs);
     fence_mbar_init();
   }
-  if (warp == kWarps && lane == 0) {
-    prefetch_tmap(&a.map_k);
-    prefetch_tmap(&a.map_v);
-  }
   Tiles tl;
   tl.cum = cum;
   tl.B = a.B;
   tl.Hkv = a.Hkv;
+  tl.whole = whole_tiles(D);
   // one warp divides the work (a division costs every warp its issue slots)
   if (warp == 0) {
     SweepPlan p;
@@ -711,7 +774,6 @@ __global__ void __launch_bounds__(kSweepThreads, 1) k_paged_sweep(const __grid_c
   __syncthreads();
   SegWalk sw;
   sw.init(cum, a.Hkv, splan);
-  const volatile int never = 0;
   // registers: 384 x 168 at launch; 256 x 216 for the consumers, 128 x 72 for the others
   if (warp < kWarps) {
     regs_inc<216>();
@@ -732,96 +794,42 @@ __global__ void __launch_bounds__(kSweepThreads, 1) k_paged_sweep(const __grid_c
   regs_dec<72>();
   bool ok = true;
   if (warp == kWarps) {
-    // ------------------------------------------------------------ keys and values
-    // Lane i loads page i of a tile; the page numbers come 32 at a time.
-    const int prows = min(1 << a.page_shift, C::kTK), per = C::kTK / prows;
-    const uint32_t pbytes = (uint32_t)prows * C::kSpan;
-    const int shared = a.prefix_len >> a.page_shift;
-    int st = 0, ph = 1;  // the first round finds every stage empty
-    int issued = 0;
-    while (ok && sw.next()) {
-      const int base = sweep_base(a, len[sw.b]), own = len[sw.b] - base;
-      const int* row = a.table + (size_t)sw.b * a.max_pages;
-      const int p0 = base >> a.page_shift;
-      const int np = own > 0 ? (own + (1 << a.page_shift) - 1) >> a.page_shift : 0;  // own pages
-      int win = -1, id = 0;
-      for (int n = sw.n0; n < sw.n1; n++) {
-        const int first = (n * C::kTK) >> a.page_shift;  // own page of the tile's first position
-        const int have = max(0, min(per, np - first));
-        if (have > 0 && (first >> 5) != win) {
-          win = first >> 5;
-          const int i = p0 + win * 32 + lane;
-          id = 0;
-          if (i - p0 < np) {
-            id = i < shared ? a.prefix_table[i] : row[i];
-            if (id < 0 || id >= a.num_pages) {
-              record_page(a.status);
-              id = a.num_pages;  // past the pool: the copy fills with zeros
-            }
-          }
-        }
-        const int mine = __shfl_sync(0xffffffffu, id, (first & 31) + (lane < per ? lane : 0));
-        ok = __all_sync(0xffffffffu, mbar_wait(bar.empty + st, ph, abort));
-        if (!ok) break;
-        if (lane == 0) {
-          if (have > 0)
-            mbar_arrive_expect_tx(bar.full + st, 2u * have * pbytes);
-          else
-            mbar_arrive(bar.full + st);
-        }
-        __syncwarp();
-        if (lane < have) {
-          const int off = (n * C::kTK) & ((1 << a.page_shift) - 1);  // a tile inside a larger page
-          uint8_t* dst = smem + L.ring + st * C::kStage + lane * pbytes;
-          tma_load_4d(dst, &a.map_k, bar.full + st, 0, off, sw.g, mine);
-          tma_load_4d(dst + C::kHalf, &a.map_v, bar.full + st, 0, off, sw.g, mine);
-        }
-        issued++;
-        if (++st == a.stages) {
-          st = 0;
-          ph ^= 1;
-        }
-      }
-    }
-    // let every copy issued above land before the block can exit
-    if (!ok && lane == 0)
-      for (int x = max(0, issued - a.stages); x < issued; x++)
-        mbar_wait(bar.full + x % a.stages, (x / a.stages) & 1, &never);
-  } else if (warp == kWarps + 1) {
     // ------------------------------------------------------------ queries, two passes of rows at a time
     constexpr int kCPR = D / 8, kRows = 32 / kCPR;
     const int c = lane % kCPR;
     const bool norm = a.qw != nullptr;
+    const int qbufs = sweep_qbufs(a.tiles);
+    constexpr uint32_t kSpan = Sweep<D>::kSpan;
     uint4 wv = make_uint4(0, 0, 0, 0);
     if (norm) wv = load_rope_chunk<D>(a.qw, c, a.rope_half != 0);
     for (int seg = 0; ok && sw.next(); seg++) {
-      const int qs = seg & 1;
-      if (seg >= 2) ok = __all_sync(0xffffffffu, mbar_wait(bar.q_empty + qs, ((seg >> 1) - 1) & 1, abort));
+      const int qs = qbufs == 2 ? seg & 1 : 0, use = qbufs == 2 ? seg >> 1 : seg;
+      if (use > 0) ok = __all_sync(0xffffffffu, mbar_wait(bar.q_empty + qs, (use - 1) & 1, abort));
       if (!ok) break;
       const int pos0 = len[sw.b] - a.Tq;
-      uint8_t* q = smem + L.q + qs * a.tiles * 16 * C::kSpan;
+      uint8_t* q = smem + L.q + qs * a.tiles * 16 * kSpan;
       for (int r0 = 0; r0 < a.tiles * 8; r0 += 2 * kRows) {
         const int r = r0 + lane / kCPR, r2 = r + kRows;
         const QueryChunk x = query_load<D>(a, sw.b, sw.g, r, c, pos0), y = query_load<D>(a, sw.b, sw.g, r2, c, pos0);
         uint4 hi, lo;
         query_finish<D>(a, x, norm, wv, hi, lo);
-        *reinterpret_cast<uint4*>(q + (r >> 3) * 16 * C::kSpan + swz(r & 7, c, C::kSpan)) = hi;
-        *reinterpret_cast<uint4*>(q + (r >> 3) * 16 * C::kSpan + swz((r & 7) + 8, c, C::kSpan)) = lo;
+        *reinterpret_cast<uint4*>(q + (r >> 3) * 16 * kSpan + swz(r & 7, c, kSpan)) = hi;
+        *reinterpret_cast<uint4*>(q + (r >> 3) * 16 * kSpan + swz((r & 7) + 8, c, kSpan)) = lo;
         query_finish<D>(a, y, norm, wv, hi, lo);
         if (r2 < a.tiles * 8) {
-          *reinterpret_cast<uint4*>(q + (r2 >> 3) * 16 * C::kSpan + swz(r2 & 7, c, C::kSpan)) = hi;
-          *reinterpret_cast<uint4*>(q + (r2 >> 3) * 16 * C::kSpan + swz((r2 & 7) + 8, c, C::kSpan)) = lo;
+          *reinterpret_cast<uint4*>(q + (r2 >> 3) * 16 * kSpan + swz(r2 & 7, c, kSpan)) = hi;
+          *reinterpret_cast<uint4*>(q + (r2 >> 3) * 16 * kSpan + swz((r2 & 7) + 8, c, kSpan)) = lo;
         }
       }
       warp_arrive(bar.q_full + qs);
     }
-  } else if (warp - kWarps - 2 < kBufs) {
+  } else if (warp - kWarps - 1 < kBufs) {
     // ------------------------------------------------------------ finished segments
     SweepPlan p;
     p.W = splan->W;
     p.base = splan->base;
     p.rem = splan->rem;
-    ok = sweep_finish<D, MT, PREFIX>(a, sw, tl, p, len, smem, L, bar, todo, abort, blk, warp - kWarps - 2, lane);
+    ok = sweep_finish<D, MT, PREFIX>(a, sw, tl, p, len, smem, L, bar, todo, abort, blk, warp - kWarps - 1, lane);
   }
   if (!ok && lane == 0) {
     *abort = 1;
@@ -846,10 +854,7 @@ cudaError_t launch_sweep_t(const PagedDecodeArgs& a, int nsm, cudaStream_t s) {
     attr_set[dev] = true;
   }
   PagedDecodeArgs b = a;
-  b.stages = Sweep<D>::kMaxStages;
-  const int least = MT < 4 ? 2 : 1;  // two tiles at a time, or one
-  while (b.stages > least && sweep_smem(D, b.stages, b.tiles, MT, b.B).total > kSmemMax) b.stages--;
-  int bytes = sweep_smem(D, b.stages, b.tiles, MT, b.B).total;
+  int bytes = sweep_smem(D, kDepth<D, MT>, b.tiles, MT, b.B).total;
   if constexpr (PREFIX) bytes = bytes > prefix_smem(D, b.B) ? bytes : prefix_smem(D, b.B);
   if (bytes > kSmemMax) return cudaErrorInvalidValue;
   const int grid = nsm < kPagedMaxBlocks ? nsm : kPagedMaxBlocks;

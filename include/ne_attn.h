@@ -349,7 +349,7 @@ int ne_attn_qk_norm_bwd(const void* q, const void* k, const void* q_w, const voi
  * j % page_size of page page_table[b, j / page_size].  page_table [B, max_pages],
  * the lengths and the places of new tokens are int32 arrays in device memory and
  * are read when the kernels run, so a captured CUDA graph replays with new ones.
- * page_size is 16, 32, 64, 128 or 256; B <= 4096; max_pages * page_size <= 2^20.
+ * page_size is 16, 32, 64, 128 or 256; B <= 2048; max_pages * page_size <= 2^20.
  * Table entries that a call needs are checked against num_pages on the device: a
  * page outside the pool, or a position outside the table, is recorded as
  * NE_ERR_PAGE in the status word and never followed.  The table entries of

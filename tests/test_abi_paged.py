@@ -80,7 +80,7 @@ def test_kv_append_paged(libne, mem):
     assert f(cu=None) == -1                      # 5 rows do not divide into 2 sequences
     assert f(N=0) == -1 and f(B=0) == -1 and f(P=0) == -1 and f(width=0) == -1
     assert f(page=8) == -3 and f(page=48) == -3 and f(page=512) == -3 and f(D=48) == -3
-    assert f(B=4097) == -3 and f(width=(1 << 16) + 1) == -3
+    assert f(B=2049) == -3 and f(width=(1 << 16) + 1) == -3
     assert f(pstride=1023) == -1 and f(pstride=1028) == -1 and f(pstride=1 << 40) == -3
     assert f(ks=60) == -1 and f(vs=72 + 4) == -1
     assert f(eps=0.0) == -1 and f(base=0.5) == -1 and f(flags=1) == -1
@@ -108,6 +108,8 @@ def test_decode_paged(libne, mem):
     assert f(Tq=0) == -1 and f(Tq=65) == -3 and f(Hq=3) == -1 and f(B=0) == -1 and f(B=5000) == -3
     assert f(page=24) == -3 and f(D=128) == -3 and f(qs=120) == -1 and f(pstride=1000) == -1
     assert f(prefix=16) == -1                    # needs its table
+    # more key tiles than the sweep counts
+    assert f(B=2048, Hq=64, Hkv=64, page=256, width=4096, pstride=64 * 256 * 32, qs=64 * 32) == -3
     assert f(prefix=-16, ptable=p) == -1 and f(prefix=24, ptable=p) == -1 and f(prefix=64, ptable=p) == -1
     assert f(eps=0.0) == -1 and f(base=float("inf")) == -1 and f(flags=2) == -1 and f(flags=4) == -1
     assert f(bytes=n - 1) == -5 and f(ws=p + 64) == -5
