@@ -241,14 +241,23 @@ template <int D>
 __device__ __forceinline__ size_t prefix_quad(size_t part, int row, int q) {
   return ((part * (kTile / 32) + row / 32) * (D / 4) + q) * 32 + row % 32;
 }
-// The prefix's W tiles cut among its blocks: the first rem have base + 1.
+// The prefix's tiles, `ntk` of each of its segs (head, pair)s, cut among its blocks: with at least a
+// block for each (head, pair) (blocks is then a multiple of segs) every one is cut for itself, else
+// all of them in one line.
 struct PrefixCut {
-  int W, base, rem;
-  __device__ PrefixCut(int W_, int blocks) : W(W_), base(W_ / blocks), rem(W_ - base * blocks) {}
-  __device__ int start(int c) const { return c * base + min(c, rem); }
+  int ntk, per, base, rem;  // per: blocks of a (head, pair), 0: in one line; the first rem blocks have base + 1
+  __device__ PrefixCut(int ntk_, int segs, int blocks) : ntk(ntk_), per(blocks >= segs ? blocks / segs : 0) {
+    const int n = per ? per : blocks, tiles = per ? ntk : ntk * segs;
+    base = tiles / n;
+    rem = tiles - base * n;
+  }
+  __device__ int start(int c) const {
+    const int s = per ? c / per : 0, i = c - s * per;
+    return s * ntk + i * base + min(i, rem);
+  }
   __device__ int owner(int x) const {  // the block with tile x
-    const int big = rem * (base + 1);
-    return x < big ? x / (base + 1) : rem + (x - big) / base;
+    const int s = per ? x / ntk : 0, y = x - s * ntk, big = rem * (base + 1);
+    return s * per + (y < big ? y / (base + 1) : rem + (y - big) / base);
   }
 };
 #endif

@@ -23,7 +23,7 @@ __global__ void __launch_bounds__(128) k_prefix_join(const __grid_constant__ Pag
   const int rho = tile * kTile + row, b = rho / a.R, r = rho - b * a.R;
   if (b >= a.B) return;
   if (sweep_base(a, max(0, min(a.len[b], a.max_pages << a.page_shift))) == 0) return;  // the sweep has written it
-  const PrefixCut cut(p.W, max(1, min(__ldcg(p.cut), min(kPagedMaxBlocks, p.W))));
+  const PrefixCut cut(p.ntk, a.Hkv * p.pairs, max(1, min(__ldcg(p.cut), min(kPagedMaxBlocks, p.W))));
   const int lo = cut.owner(s * p.ntk), hi = cut.owner(s * p.ntk + p.ntk - 1);
   const size_t own = (size_t)gt * kTile + row;
   const float2 zo = __ldcg(p.ml + own);

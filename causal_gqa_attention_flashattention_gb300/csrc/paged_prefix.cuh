@@ -53,19 +53,24 @@ inline int prefix_smem(int D, int B) {
 }
 
 // The blocks that take the prefix, of all: their share of the work, a tile of a pair of row tiles
-// counted as 1.64 of the sweep's (measured: 64 sequences on 8192 positions 24.5, 19.9 and 23.1 us
-// at 1.27, 1.64 and 2.18; 128 on 16384 41.9, 39.6 and 42.4 us).
+// counted as 1.5 of the sweep's (measured: 64 sequences on 8192 positions 21.4, 21.2, 22.9 us at 1.4,
+// 1.64, 1.9; 128 on 16384 38.8, 39.3, 44.1 us).
 __device__ __forceinline__ int prefix_blocks(const PagedDecodeArgs& a, int sweep_tiles, int blocks) {
-  const float mine = 1.64f * (float)a.pre.W, theirs = (float)sweep_tiles * (a.D == 64 ? 1.f : 0.5f);
-  const int P = __float2int_rn((float)blocks * __fdiv_rn(mine, mine + theirs));
-  return max(1, min(min(P, blocks - 1), a.pre.W));
+  const float mine = 1.5f * (float)a.pre.W, theirs = (float)sweep_tiles * (a.D == 64 ? 1.f : 0.5f);
+  const int P = max(1, min(min(__float2int_rn((float)blocks * __fdiv_rn(mine, mine + theirs)), blocks - 1), a.pre.W));
+  // the same number for every (head, pair), so that no block has parts of two (which costs it
+  // a second packing and a second epilogue, about 4 us)
+  const int segs = a.Hkv * a.pre.pairs;
+  if (P < segs) return P;
+  const int up = (P + segs / 2) / segs * segs;
+  return up < blocks && up <= a.pre.W ? up : P / segs * segs;
 }
 
 struct PreSeg {
   int w, end;       // tiles of the block's stretch that are left
   int s, n0, n1;    // the segment: (head, pair) s, key tiles [n0, n1)
   __device__ void init(const PrefixArgs& p, int block, int blocks) {
-    const PrefixCut cut(p.W, blocks);
+    const PrefixCut cut(p.ntk, p.W / p.ntk, blocks);
     w = cut.start(block);
     end = cut.start(block + 1);
   }
