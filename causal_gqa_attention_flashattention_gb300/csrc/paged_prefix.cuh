@@ -88,17 +88,22 @@ struct PreSeg {
 // A row of the packed tile, normalised and rotated, as fp16 high and low parts into the swizzled
 // tiles at dst and behind it.
 template <int D>
-__device__ __forceinline__ void pack_query_row(const PagedDecodeArgs& a, int g, int rho, uint8_t* dst, int r) {
+__device__ __forceinline__ void pack_query_row(const PagedDecodeArgs& a, const int* len, int g, int rho, uint8_t* dst,
+                                               int r) {
   constexpr int kCPR = D / 8;
   const int b = rho / a.R, rr = rho - b * a.R;
   const bool on = b < a.B;
   const int t = on ? rr / a.G : 0, gg = rr - t * a.G;
   const bool half = a.rope_half != 0;
   const __nv_bfloat16* row = a.q + (size_t)(on ? b * a.Tq + t : 0) * a.q_stride + (on ? g * a.G + gg : 0) * D;
-  const int pos = on ? max(min(a.len[b], a.max_pages << a.page_shift) - a.Tq + t, 0) : 0;
+  const int pos = on ? max(len[b] - a.Tq + t, 0) : 0;
   uint4 v[kCPR];
+  float4 c0[kCPR], c1[kCPR];
 #pragma unroll
-  for (int c = 0; c < kCPR; c++) v[c] = load_rope_chunk<D>(row, c, half);
+  for (int c = 0; c < kCPR; c++) {
+    v[c] = load_rope_chunk<D>(row, c, half);
+    rope_coeffs<D>(a.rope, pos, c, c0[c], c1[c]);
+  }
   float rs = 1.f;
   if (a.qw) {
     float ss = 0.f;
@@ -112,12 +117,10 @@ __device__ __forceinline__ void pack_query_row(const PagedDecodeArgs& a, int g, 
   }
 #pragma unroll
   for (int c = 0; c < kCPR; c++) {
-    float4 c0, c1;
-    rope_coeffs<D>(a.rope, pos, c, c0, c1);
     uint4 wv = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);  // ones
     if (a.qw) wv = load_rope_chunk<D>(a.qw, c, half);
     const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w}, ww[4] = {wv.x, wv.y, wv.z, wv.w};
-    const float cs[4] = {c0.x, c0.z, c1.x, c1.z}, sn[4] = {c0.y, c0.w, c1.y, c1.w};
+    const float cs[4] = {c0[c].x, c0[c].z, c1[c].x, c1[c].z}, sn[4] = {c0[c].y, c0[c].w, c1[c].y, c1[c].w};
     uint32_t h[4], l[4];
 #pragma unroll
     for (int p = 0; p < 4; p++) {
@@ -131,9 +134,10 @@ __device__ __forceinline__ void pack_query_row(const PagedDecodeArgs& a, int g, 
   }
 }
 
-// Block pb of P of the prefix's part; smem: behind the block's head, 1024-byte aligned.
+// Block pb of P of the prefix's part; len: the sequences' lengths in shared memory, smem: behind the
+// block's head, 1024-byte aligned.
 template <int D>
-__device__ void prefix_role(const PagedDecodeArgs& a, uint8_t* smem, int P, int tid) {
+__device__ void prefix_role(const PagedDecodeArgs& a, const int* len, uint8_t* smem, int P, int tid) {
   using C = PreCfg<D>;
   constexpr int S = C::kStages;
   constexpr int TB = C::kTileBytes;
@@ -331,7 +335,7 @@ __device__ void prefix_role(const PagedDecodeArgs& a, uint8_t* smem, int P, int 
       {
         if (e >= 1) ok = __all_sync(0xffffffffu, mbar_wait(q_empty + u, (e - 1) & 1, abort));
         if (!ok) break;
-        pack_query_row<D>(a, sg.s / p.pairs, (2 * (sg.s % p.pairs) + u) * kTile + r, smem + 2 * u * TB, r);
+        pack_query_row<D>(a, len, sg.s / p.pairs, (2 * (sg.s % p.pairs) + u) * kTile + r, smem + 2 * u * TB, r);
         fence_proxy_async_smem();
         warp_arrive(q_full + u);
         e++;
