@@ -387,21 +387,21 @@ def _need(ok, what):
         raise ValueError(what)
 
 
-def _run(name, device, stream, temps, *args):
-    """Calls library function `name` with the launch stream as its last argument,
-    on `device` (the current one or not).  `temps`, tensors the call allocated on
-    the current stream, are kept from reuse until the work on another stream is done."""
+def _on(stream, call, *args, **kw):
+    """The call with `stream` as the current stream: what it allocates then belongs to it."""
+    with torch.cuda.stream(stream):
+        return call(*args, **kw)
+
+
+def _run(name, device, *args):
+    """Calls library function `name` with `device`'s current stream as its last argument."""
     if device.index != torch.cuda.current_device():
         with torch.cuda.device(device):
-            return _run(name, device, stream, temps, *args)
+            return _run(name, device, *args)
     # the current stream's handle without a Stream object around it (2.9 us a call)
-    s = torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
-    st = getattr(_lib or lib(), name)(*args, s)
+    st = getattr(_lib or lib(), name)(*args, torch._C._cuda_getCurrentRawStream(device.index))
     if st != NE_OK:
         raise NeAttnError(name, st)
-    if stream is not None:
-        for t in temps:
-            t.record_stream(stream)
 
 
 def _optr(t):
@@ -436,20 +436,19 @@ def _int32(t, name, device, shape):
         raise ValueError("%s must be a contiguous int32 %s on the call's device" % (name, list(shape)))
 
 
-def _run_ws(name, device, stream, made, args, workspace, size):
+def _run_ws(name, device, args, workspace, size):
     """_run with the workspace as the last arguments: the caller's; without one NULL (the
     library's own for the stream) or, where a capture needs one, a tensor of the capture's own."""
     if workspace is None:
         try:
-            return _run(name, device, stream, made, *args, None, 0)
+            return _run(name, device, *args, None, 0)
         except NeAttnError as e:
             if e.status != ERR_WORKSPACE:
                 raise
         workspace = torch.empty(size(), dtype=torch.uint8, device=device)
-        made.append(workspace)
     elif workspace.dtype != torch.uint8 or workspace.device != device:
         raise ValueError("workspace must be uint8 on the call's device")
-    _run(name, device, stream, made, *args, workspace.data_ptr(), workspace.numel())
+    _run(name, device, *args, workspace.data_ptr(), workspace.numel())
 
 
 def qk_norm(q, k, q_weight, k_weight, eps=1e-6, rope_base=10000.0, rope_half=False, workspace=None, stream=None):
@@ -461,20 +460,20 @@ def qk_norm(q, k, q_weight, k_weight, eps=1e-6, rope_base=10000.0, rope_half=Fal
     fwd_workspace_size bytes; allocated if None), which is returned: attn_fwd and
     attn_bwd take it with qk_rotated=True (q and k then None), rotated_qk views it.
     """
+    if stream is not None:
+        return _on(stream, qk_norm, q, k, q_weight, k_weight, eps, rope_base, rope_half, workspace)
     B, T, Hq, D = q.shape
     Hkv, dev = k.shape[2], q.device
     _need(k.shape == (B, T, Hkv, D), "k must be [B, T, Hkv, D] like q")
     qs, ks = _head_rows(q, "q"), _head_rows(k, "k", device=dev)
     _vector(q_weight, D, "q_weight", dev)
     _vector(k_weight, D, "k_weight", dev)
-    temps = ()
     if workspace is None:
         n = fwd_workspace_size(B, T, Hq, Hkv, D)
         _need(n > 0, "unsupported shape")
         workspace = torch.empty(n, dtype=torch.uint8, device=dev)
-        temps = (workspace,)
     _need(workspace.dtype == torch.uint8 and workspace.device == dev, "workspace must be uint8 on the call's device")
-    _run("ne_attn_qk_norm", dev, stream, temps, q.data_ptr(), k.data_ptr(), q_weight.data_ptr(), k_weight.data_ptr(),
+    _run("ne_attn_qk_norm", dev, q.data_ptr(), k.data_ptr(), q_weight.data_ptr(), k_weight.data_ptr(),
          B, T, Hq, Hkv, D, qs, ks, eps, rope_base, ROPE_HALF if rope_half else 0, workspace.data_ptr(),
          workspace.numel())
     return workspace
@@ -485,6 +484,8 @@ def qk_norm_bwd(q, k, q_weight, k_weight, dqn, dkn, eps=1e-6, dq=None, dk=None, 
     from dqn [B,T,Hq,D] and dkn [B,T,Hkv,D], the dq and dk of attn_bwd with qk_rotated=True
     (bf16 or fp32, contiguous).  dq and dk may be given: slices of a fused projection's
     gradient, or dqn and dkn themselves."""
+    if stream is not None:
+        return _on(stream, qk_norm_bwd, q, k, q_weight, k_weight, dqn, dkn, eps, dq, dk, workspace)
     B, T, Hq, D = q.shape
     Hkv, dev, dt = k.shape[2], q.device, dqn.dtype
     _need(k.shape == (B, T, Hkv, D), "k must be [B, T, Hkv, D] like q")
@@ -495,22 +496,18 @@ def qk_norm_bwd(q, k, q_weight, k_weight, dqn, dkn, eps=1e-6, dq=None, dk=None, 
     for t, like, name in ((dqn, q, "dqn"), (dkn, k, "dkn")):
         _need(t.dtype == dt and t.device == dev and t.shape == like.shape and t.is_contiguous(),
               "%s must be contiguous, of the shape of its input and of one type with the other" % name)
-    made = []
     if dq is None:
         dq = torch.empty(q.shape, dtype=dt, device=dev)
-        made.append(dq)
     if dk is None:
         dk = torch.empty(k.shape, dtype=dt, device=dev)
-        made.append(dk)
     _need(dq.shape == q.shape and dk.shape == k.shape, "dq and dk must have the shapes of q and k")
     dqs, dks = _head_rows(dq, "dq", dt, dev), _head_rows(dk, "dk", dt, dev)
     dqw = torch.empty(D, dtype=torch.float32, device=dev)
     dkw = torch.empty(D, dtype=torch.float32, device=dev)
-    made += (dqw, dkw)
     args = (q.data_ptr(), k.data_ptr(), q_weight.data_ptr(), k_weight.data_ptr(), dqn.data_ptr(), dkn.data_ptr(),
             dq.data_ptr(), dk.data_ptr(), dqw.data_ptr(), dkw.data_ptr(), B, T, Hq, Hkv, D, qs, ks, dqs, dks, eps,
             GRAD_FP32 if dt == torch.float32 else 0)
-    _run_ws("ne_attn_qk_norm_bwd", dev, stream, made, args, workspace,
+    _run_ws("ne_attn_qk_norm_bwd", dev, args, workspace,
             lambda: int(lib().ne_attn_qk_norm_bwd_workspace_size(B, T, Hq, Hkv, D)))
     return dq, dk, dqw, dkw
 
@@ -550,6 +547,9 @@ def kv_append_paged(k_new, v_new, k_pages, v_pages, page_table, pos0, cu_new=Non
     page_table int32 [B, max_pages], pos0 int32 [B] (the first new position of each
     sequence) and cu_new int32 [B + 1] (its rows; None: N / B each) are CUDA tensors.
     k_weight [D]: the keys are normalised first.  Bad pages are found by check_status."""
+    if stream is not None:
+        return _on(stream, kv_append_paged, k_new, v_new, k_pages, v_pages, page_table, pos0, cu_new, k_weight, eps,
+                   rope_base, rope_half)
     N, Hkv, D = k_new.shape
     dev = k_new.device
     _need(v_new.shape == k_new.shape, "k_new and v_new must have one shape")
@@ -564,7 +564,7 @@ def kv_append_paged(k_new, v_new, k_pages, v_pages, page_table, pos0, cu_new=Non
         _vector(k_weight, D, "k_weight", dev)
     if N == 0:
         return
-    _run("ne_attn_kv_append_paged", dev, stream, (), k_new.data_ptr(), v_new.data_ptr(), _optr(k_weight),
+    _run("ne_attn_kv_append_paged", dev, k_new.data_ptr(), v_new.data_ptr(), _optr(k_weight),
          k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(), pos0.data_ptr(), _optr(cu_new), N, B, Hkv, D,
          page, P, width, stride, ks, vs, eps, rope_base, ROPE_HALF if rope_half else 0)
 
@@ -583,6 +583,9 @@ def attn_decode_paged(q, k_pages, v_pages, page_table, kv_len, q_weight=None, ep
     idle slot, whose o is 0 and lse -inf).  q_weight [D]: the queries are normalised
     first.  prefix_table int32 and prefix_len: the first prefix_len positions (whole
     pages) of every sequence are these pages, read once for the batch."""
+    if stream is not None:
+        return _on(stream, attn_decode_paged, q, k_pages, v_pages, page_table, kv_len, q_weight, eps, rope_base,
+                   prefix_table, prefix_len, o, lse, o_dtype, workspace, rope_half)
     B, Tq, Hq, D = q.shape
     Hkv, dev = k_pages.shape[1], q.device
     qs = _head_rows(q, "q")
@@ -596,15 +599,12 @@ def attn_decode_paged(q, k_pages, v_pages, page_table, kv_len, q_weight=None, ep
         _need(prefix_table is not None and prefix_table.dim() == 1 and prefix_table.numel() * page >= prefix_len,
               "prefix_table must hold the pages of prefix_len positions")
         _int32(prefix_table, "prefix_table", dev, prefix_table.shape)
-    made = []
     if o is None:
         o = torch.empty((B, Tq, Hq, D), dtype=o_dtype, device=dev)
-        made.append(o)
     elif o.device != dev or not o.is_contiguous() or o.shape != (B, Tq, Hq, D):
         raise ValueError("o must be a contiguous [B, Tq, Hq, D] on the call's device")
     if lse is None:
         lse = torch.empty((B, Hq, Tq), dtype=torch.float32, device=dev)
-        made.append(lse)
     elif lse.dtype != torch.float32 or lse.device != dev or not lse.is_contiguous() or lse.shape != (B, Hq, Tq):
         raise ValueError("lse must be a contiguous float32 [B, Hq, Tq] on the call's device")
     fp32 = o.dtype == torch.float32
@@ -614,7 +614,7 @@ def attn_decode_paged(q, k_pages, v_pages, page_table, kv_len, q_weight=None, ep
             page_table.data_ptr(), kv_len.data_ptr(), prefix_table.data_ptr() if prefix_len else None, o.data_ptr(),
             lse.data_ptr(), B, Tq, Hq, Hkv, D, page, P, width, stride, qs, prefix_len, eps, rope_base,
             (O_FP32 if fp32 else 0) | (ROPE_HALF if rope_half else 0))
-    _run_ws("ne_attn_decode_paged", dev, stream, made, args, workspace,
+    _run_ws("ne_attn_decode_paged", dev, args, workspace,
             lambda: decode_paged_workspace_size(B, Tq, Hq, Hkv, D, prefix_len))
     return o, lse
 

@@ -359,7 +359,7 @@ int ne_attn_qk_norm_bwd(const void* q, const void* k, const void* q_w, const voi
  * rows k_stride / v_stride values apart) of a ragged batch: rows cu_new[b] ..
  * cu_new[b+1] - 1 belong to sequence b and go to its positions pos0[b],
  * pos0[b] + 1, ...; rows at or past cu_new[B] are padding and are not read.
- * cu_new [B + 1] rises from 0; with cu_new = NULL every sequence has N / B rows.
+ * cu_new [B + 1] rises from 0 (entries never fall); with cu_new = NULL every sequence has N / B rows.
  * Each key is normalised with k_w [D] as in ne_attn_qk_norm (k_w = NULL: not),
  * rotated at its position and stored as fp16; each value is copied.  A row
  * whose place is bad (see above) is not written.  No two rows may have one
@@ -382,6 +382,11 @@ int ne_attn_kv_append_paged(const void* k_new, const void* v_new, const void* k_
  * an idle slot of the batch) sees no key: o = 0, lse = -infinity.  A length
  * past the table is cut to it and recorded as NE_ERR_PAGE; the keys and values
  * of a bad page count as zeros.
+ *
+ * The keys and values of every position below kv_len must be numbers: a weight of
+ * 0 times an infinity or a NaN in v is NaN for all queries that share its tile (an
+ * infinite or NaN key does harm only where it is visible).  Rotated queries and keys
+ * are fp16: their values must stay below 65504.
  *
  * Shared prefix: with prefix_len > 0 (a multiple of page_size, at most
  * max_pages * page_size) positions 0 .. prefix_len - 1 of every sequence are the

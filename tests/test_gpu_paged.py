@@ -219,6 +219,10 @@ PREFIXES = [
     ([5, 2, 70], 128, 2, 6, 3, 64, 32, True, True, True),
     ([(i * 13) % 90 + 1 for i in range(70)], 1024, 1, 12, 4, 64, 16, False, False, False),   # 210 rows a head
     ([3, 4, 500, 9], 768, 3, 8, 1, 32, 256, True, False, False),
+    ([2, 40, 9, 8], 80, 1, 12, 4, 64, 16, False, True, True),            # tiles that end inside the prefix
+    ([1, 7, 33], 416, 4, 6, 2, 64, 32, True, False, True),
+    ([12, 31], 704, 1, 8, 1, 32, 64, True, False, False),
+    ([600, 2, 77], 128, 12, 8, 2, 64, 16, False, False, True),           # 48 rows a sequence
     ([(i * 5) % 40 + 3 for i in range(140)], 640, 3, 4, 2, 64, 128, False, True, False),      # 840 rows a head
 ]
 
