@@ -1398,11 +1398,10 @@ int ne_attn_qk_norm_bwd(const void* q, const void* k, const void* q_w, const voi
     if ((st = join_scratch(*d, s, qk_norm_bwd_part_bytes(D), &ws, &a.done)) != NE_OK) return st;
   } else {
     a.done = reinterpret_cast<unsigned*>(static_cast<unsigned char*>(ws) + qk_norm_bwd_part_bytes(D));
-    if (cudaMemsetAsync(a.done, 0, 256, s) != cudaSuccess) return NE_ERR_CUDA;
   }
   a.part = static_cast<float*>(ws);
   ProfScope prof(NE_ATTN_KERNEL_QK_NORM_BWD, s);
-  return launch_qk_norm_bwd(a, D, (flags & kFlagGradFp32) != 0, blocks, s) == cudaSuccess ? NE_OK : NE_ERR_CUDA;
+  return launch_qk_norm_bwd(a, D, (flags & kFlagGradFp32) != 0, blocks, workspace != nullptr, s) == cudaSuccess ? NE_OK : NE_ERR_CUDA;
 }
 
 // ------------------------------------------------------------------ paged cache

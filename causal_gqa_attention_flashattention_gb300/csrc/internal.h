@@ -307,7 +307,7 @@ cudaError_t launch_pdl(void (*k)(P...), int grid, int block, size_t smem, cudaSt
 
 int qk_norm_blocks(int B, int T, int Hq, int Hkv, int D, int nsm, bool bwd, int* nbq);
 cudaError_t launch_qk_norm(const QkNormArgs& a, int D, int blocks, cudaStream_t s);
-cudaError_t launch_qk_norm_bwd(const QkNormBwdArgs& a, int D, bool f32, int blocks, cudaStream_t s);
+cudaError_t launch_qk_norm_bwd(const QkNormBwdArgs& a, int D, bool f32, int blocks, bool clear, cudaStream_t s);
 cudaError_t launch_kv_append_paged(const PagedAppendArgs& a, int D, cudaStream_t s);
 void paged_rows(int R, int* mt, int* tiles, int* mg);
 cudaError_t launch_decode_paged(const PagedDecodeArgs& a, int mt, int nsm, cudaStream_t s);

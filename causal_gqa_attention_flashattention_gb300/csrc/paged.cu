@@ -35,9 +35,16 @@ __global__ void __launch_bounds__(128) k_kv_append_paged(const PagedAppendArgs a
   const int c = (int)(it % kCPR);
   const uint32_t n = fdiv(row, a.div_hkv);
   const uint32_t g = row - n * a.Hkv;
+  // the row itself first: its loads are under way while its place is looked up
+  bool on = in && (!a.cu || (int)n < a.cu[a.B]);
+  uint4 kv = make_uint4(0, 0, 0, 0), vv = kv, wv = kv;
+  if (on) {
+    kv = load_rope_chunk<D>(a.k + (size_t)n * a.k_stride + g * D, c, a.rope_half != 0);
+    vv = __ldg(reinterpret_cast<const uint4*>(a.v + (size_t)n * a.v_stride + g * D) + c);
+  }
+  if (a.kw) wv = load_rope_chunk<D>(a.kw, c, a.rope_half != 0);
   // the row's sequence and position
   int s = 0, first = 0;
-  bool on = in;
   if (a.cu) {
     // last s with cu[s] <= n: 32 probes at a time for the warp's lowest row, then
     // each lane steps on to its own
@@ -54,7 +61,7 @@ __global__ void __launch_bounds__(128) k_kv_append_paged(const PagedAppendArgs a
     s = lo;
     while (s + 1 < a.B && a.cu[s + 1] <= (int)n) s++;
     first = a.cu[s];
-    on = on && (int)n >= first && (int)n < a.cu[a.B];
+    on = on && (int)n >= first;
   } else {
     s = (int)fdiv(n, a.div_per);
     first = s * (int)a.div_per.d;
@@ -69,11 +76,8 @@ __global__ void __launch_bounds__(128) k_kv_append_paged(const PagedAppendArgs a
       on = false;
     }
   }
-  uint4 kv = make_uint4(0, 0, 0, 0), vv = kv;
-  if (on) {
-    kv = load_rope_chunk<D>(a.k + (size_t)n * a.k_stride + g * D, c, a.rope_half != 0);
-    vv = __ldg(reinterpret_cast<const uint4*>(a.v + (size_t)n * a.v_stride + g * D) + c);
-  }
+  float4 c0 = make_float4(0.f, 0.f, 0.f, 0.f), c1 = c0;
+  if (on) rope_coeffs<D>(a.rope, pos, c, c0, c1);
   const uint32_t w[4] = {kv.x, kv.y, kv.z, kv.w};
   float x[8];
 #pragma unroll
@@ -88,7 +92,6 @@ __global__ void __launch_bounds__(128) k_kv_append_paged(const PagedAppendArgs a
 #pragma unroll
     for (int m = 1; m < kCPR; m <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
     const float r = rsqrtf(fmaf(ss, 1.f / D, a.eps));
-    const uint4 wv = load_rope_chunk<D>(a.kw, c, a.rope_half != 0);
     const uint32_t ww[4] = {wv.x, wv.y, wv.z, wv.w};
 #pragma unroll
     for (int p = 0; p < 4; p++) {
@@ -97,8 +100,6 @@ __global__ void __launch_bounds__(128) k_kv_append_paged(const PagedAppendArgs a
     }
   }
   if (!on) return;
-  float4 c0, c1;
-  rope_coeffs<D>(a.rope, pos, c, c0, c1);
   const float cs[4] = {c0.x, c0.z, c1.x, c1.z}, sn[4] = {c0.y, c0.w, c1.y, c1.w};
   uint32_t o[4];
 #pragma unroll

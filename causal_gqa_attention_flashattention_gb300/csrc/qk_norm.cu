@@ -243,6 +243,7 @@ __global__ void __launch_bounds__(kThreads) k_qk_norm_bwd(const QkNormBwdArgs a)
     float t = 0.f;
 #pragma unroll
     for (int k = 0; k < kThreads / 32; k++) t += red[k][threadIdx.x];
+    pdl_wait();  // where the kernel before clears the workspace's counters
     a.part[(size_t)blockIdx.x * D + threadIdx.x] = t;
   }
   // the last of kQkNormGroup neighbouring blocks of a side adds their partials in order, the last of
@@ -259,6 +260,13 @@ __global__ void __launch_bounds__(kThreads) k_qk_norm_bwd(const QkNormBwdArgs a)
   if (!last_to_count(a.done + (s.isq ? 0 : 1), groups)) return;
   if (add_partials<D>(sums, groups, t)) reinterpret_cast<float4*>(s.isq ? a.dqw : a.dkw)[threadIdx.x] = t;
 }
+
+// The counters of a caller's workspace.
+__global__ void k_qk_norm_clear(unsigned* done) {
+  pdl_launch();
+  if (threadIdx.x < 2 + kQkNormMaxGroups) done[threadIdx.x] = 0u;
+}
+static_assert(2 + kQkNormMaxGroups <= 64, "threads of the clear");
 
 }  // namespace
 
@@ -286,19 +294,16 @@ cudaError_t launch_qk_norm(const QkNormArgs& a, int D, int blocks, cudaStream_t 
   return cudaGetLastError();
 }
 
-cudaError_t launch_qk_norm_bwd(const QkNormBwdArgs& a, int D, bool f32, int blocks, cudaStream_t s) {
-  if (D == 64) {
-    if (f32)
-      k_qk_norm_bwd<64, true><<<blocks, kThreads, 0, s>>>(a);
-    else
-      k_qk_norm_bwd<64, false><<<blocks, kThreads, 0, s>>>(a);
-  } else {
-    if (f32)
-      k_qk_norm_bwd<32, true><<<blocks, kThreads, 0, s>>>(a);
-    else
-      k_qk_norm_bwd<32, false><<<blocks, kThreads, 0, s>>>(a);
+cudaError_t launch_qk_norm_bwd(const QkNormBwdArgs& a, int D, bool f32, int blocks, bool clear, cudaStream_t s) {
+  const auto k = D == 64 ? (f32 ? k_qk_norm_bwd<64, true> : k_qk_norm_bwd<64, false>)
+                         : (f32 ? k_qk_norm_bwd<32, true> : k_qk_norm_bwd<32, false>);
+  if (!clear) {
+    k<<<blocks, kThreads, 0, s>>>(a);
+    return cudaGetLastError();
   }
-  return cudaGetLastError();
+  k_qk_norm_clear<<<1, 64, 0, s>>>(a.done);
+  const cudaError_t e = cudaGetLastError();
+  return e != cudaSuccess ? e : launch_pdl(k, blocks, kThreads, 0, s, a);
 }
 
 }  // namespace ne
