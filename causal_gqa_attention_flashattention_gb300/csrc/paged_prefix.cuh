@@ -305,7 +305,9 @@ __device__ void prefix_role(const PagedDecodeArgs& a, const int* len, uint8_t* s
             mma_commit(kv_empty + st);  // V by this PV; K by this unit's S, complete before its P existed
             m++;
           } else {
-            mbar_arrive(kv_empty + st);  // the segment has one unit
+            // the segment has one unit: once for each use of the stage, so not before the stage is full
+            if (!(ok = mbar_wait(kv_full + st, (g / S) & 1, abort))) break;
+            mbar_arrive(kv_empty + st);
           }
         }
         if (act) e++;

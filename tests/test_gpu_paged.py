@@ -224,6 +224,10 @@ PREFIXES = [
     ([12, 31], 704, 1, 8, 1, 32, 64, True, False, False),
     ([600, 2, 77], 128, 12, 8, 2, 64, 16, False, False, True),           # 48 rows a sequence
     ([(i * 5) % 40 + 3 for i in range(140)], 640, 3, 4, 2, 64, 128, False, True, False),      # 840 rows a head
+    # an odd number of row tiles, and blocks that take many key tiles for the last one alone
+    ([3, None, 40, 9], 16384, 1, 8, 8, 64, 64, True, False, True),
+    ([11], 65536, 3, 6, 2, 32, 256, False, True, True),
+    ([(i * 11) % 50 + 1 for i in range(100)], 10240, 1, 12, 4, 64, 16, False, False, False),  # 300 rows a head
 ]
 
 
