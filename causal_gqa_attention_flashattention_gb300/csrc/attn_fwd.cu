@@ -833,7 +833,10 @@ __global__ void __launch_bounds__(384, 1) k_attn_fwd4(const __grid_constant__ Fw
             mma_commit(kv_empty + st);  // V by this PV; K by this unit's S, complete before its P existed
             n++;
           } else {
-            mbar_arrive(kv_empty + st);  // this unit does not use the stage
+            // this unit does not use the stage: one arrival for each of its uses, so not before it is full
+            // (items of one unit in a row would otherwise free a stage that the other unit still reads)
+            if (!(ok = mbar_wait(kv_full + st, (g / S) & 1, abort))) break;
+            mbar_arrive(kv_empty + st);
           }
         }
         if (act) e++;
