@@ -157,7 +157,10 @@ struct Tiles {
   __device__ int moved(int x, int i) const {  // x in sequence i
     const int n = cum[i + 1] - cum[i];
     if (n > whole) return x;
-    const int off = (x - cum[i] * Hkv) % n;
+    const int y = x - cum[i] * Hkv;
+    int off = y - (int)__fdividef((float)y, (float)n) * n;  // y mod n, the quotient within one
+    off += off < 0 ? n : 0;
+    off -= off >= n ? n : 0;
     return 2 * off < n ? x - off : x - off + n;
   }
   // The block with tile x of a (sequence, head) that is cut.
@@ -750,23 +753,22 @@ __global__ void __launch_bounds__(kSweepThreads, 1) k_paged_sweep(const __grid_c
   tl.B = a.B;
   tl.Hkv = a.Hkv;
   tl.whole = whole_tiles(D);
-  // one warp divides the work (a division costs every warp its issue slots)
-  if (warp == 0) {
+  // two warps divide the work (a division costs every warp its issue slots): the block's first tile
+  // and the next block's
+  if (warp < 2) {
     SweepPlan p;
     p.W = cum[a.B] * a.Hkv;
     p.G = min(p.W, nblk);
     p.base = p.W == p.G ? 1 : (PREFIX ? p.W / p.G : (int)fdiv((uint32_t)p.W, a.div_grid));
     p.rem = p.W - p.base * p.G;
-    // tiles of this block and the next one's first, with the sequences they are in
-    const int c = min(blk, p.G), x0 = min(c * p.base + min(c, p.rem), p.W - 1);
-    const int x1 = min(x0 + p.base + (c < p.rem ? 1 : 0), p.W);
-    const int b0 = tl.find_warp(x0, lane), b1 = tl.find_warp(min(x1, p.W - 1), lane);
-    p.w = c < p.G ? tl.moved(x0, b0) : p.W;
-    p.end = c < p.G && x1 < p.W ? tl.moved(x1, b1) : p.W;
-    p.b = b0;
-    if (p.w == (cum[b0 + 1]) * a.Hkv) p.b++;  // moved to the next sequence's first tile
-    if (lane == 0) {
-      if (p.b == a.B) p.b--;  // nothing left
+    const int c = blk + warp, x = c * p.base + min(c, p.rem);
+    const bool any = blk < p.G && x < p.W;
+    p.b = tl.find_warp(min(x, p.W - 1), lane);
+    p.w = any ? tl.moved(x, p.b) : p.W;
+    if (lane == 0 && warp == 1) splan->end = p.w;
+    if (lane == 0 && warp == 0) {
+      if (p.w == cum[p.b + 1] * a.Hkv) p.b++;  // moved to the next sequence's first tile
+      if (p.b == a.B) p.b--;                   // nothing left
       const int nt = cum[p.b + 1] - cum[p.b], off = p.w - cum[p.b] * a.Hkv;
       p.g = (int)__fdividef((float)off, (float)nt);  // within one of off / nt
       p.n0 = off - p.g * nt;
@@ -777,7 +779,6 @@ __global__ void __launch_bounds__(kSweepThreads, 1) k_paged_sweep(const __grid_c
       splan->base = p.base;
       splan->rem = p.rem;
       splan->w = p.w;
-      splan->end = p.end;
       splan->b = p.b;
       splan->g = p.g;
       splan->n0 = p.n0;
