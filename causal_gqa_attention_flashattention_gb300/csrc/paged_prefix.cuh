@@ -53,17 +53,18 @@ inline int prefix_smem(int D, int B) {
 }
 
 // The blocks that take the prefix, of all: their share of the work, a tile of a pair of row tiles
-// counted as 1.5 of the sweep's (measured: 64 sequences on 8192 positions 21.4, 21.2, 22.9 us at 1.4,
-// 1.64, 1.9; 128 on 16384 38.8, 39.3, 44.1 us).
+// counted as 2 of the sweep's (measured: 128 sequences on 16384 positions 35.1, 37.9, 37.2 us at 2, 1.75,
+// 2.25; 60 on 8192 with D = 32 18.6, 18.3, 18.5).
 __device__ __forceinline__ int prefix_blocks(const PagedDecodeArgs& a, int sweep_tiles, int blocks) {
-  const float mine = 1.5f * (float)a.pre.W, theirs = (float)sweep_tiles * (a.D == 64 ? 1.f : 0.5f);
+  const float mine = 2.f * (float)a.pre.W, theirs = (float)sweep_tiles * (a.D == 64 ? 1.f : 0.5f);
   const int P = max(1, min(min(__float2int_rn((float)blocks * __fdiv_rn(mine, mine + theirs)), blocks - 1), a.pre.W));
   // the same number for every (head, pair), so that no block has parts of two (which costs it
   // a second packing and a second epilogue, about 4 us)
   const int segs = a.Hkv * a.pre.pairs;
   if (P < segs) return P;
-  const int up = (P + segs / 2) / segs * segs;
-  return up < blocks && up <= a.pre.W ? up : P / segs * segs;
+  const int most = min(blocks - 1, a.pre.W) / segs;
+  const int k = max(1, min((P + segs / 2) / segs, most)), n = (a.pre.ntk + k - 1) / k;
+  return segs * ((a.pre.ntk + n - 1) / n);  // fewer, where the busiest of them then has no more tiles
 }
 
 struct PreSeg {

@@ -47,8 +47,15 @@ constexpr int kDepth = D == 64 ? (MT < 4 ? 4 : 3) : (MT < 4 ? 8 : 6);
 // against 7.4, 16 contexts around 8192 positions 31.9 against 31.4.)
 constexpr int kWarps = 8;
 constexpr int kSweepThreads = (kWarps + 4) * 32;
-// A (sequence, head) of at most this many tiles is never split.
+// What a segment costs beside its tiles (queries, its parts' way out), in tiles of the sweep: blocks get
+// equal shares of both (128 sequences up to 1000 long 20.9 us, without it 22.4; 8 around 1700 11.5, 12.9).
+constexpr int seg_cost(int D) { return D == 64 ? 1 : 2; }
+// Joining a cut (sequence, head) costs about 3 us at the end, as much as five tiles.  One of at
+// most so many tiles is never cut (32 sequences up to 1500 long 14.3 us, with 4 for 8 15.0) ...
 constexpr int whole_tiles(int D) { return D == 64 ? 8 : 16; }
+// ... and a boundary moves by so many to an end of a longer one (those 32 sequences 13.4 us, with 2
+// 14.3, with 0 15.1; 64 up to 4000 long 29.8, 29.2, 31.2).
+constexpr int max_slack(int D) { return D == 64 ? 3 : 6; }
 
 // Buffers for the warps' parts of a finished segment, each with a finishing warp of its own.
 constexpr int sweep_bufs(int D, int mt) { return D * mt <= 64 ? 2 : 1; }
@@ -115,16 +122,18 @@ __device__ __forceinline__ void mma_b16(float (&d)[4], const uint32_t (&a)[4], u
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// The division of the W tiles among G blocks, and one block's stretch [w, end).
+// The work: a (sequence, head) of n tiles takes `over` + n places of a line, (sequence, head) by
+// (sequence, head), tile i of one at s0 the place s0 + over + i; G blocks have equal stretches of it.
 struct SweepPlan {
-  int W, G, base, rem;  // the first rem blocks have base + 1 tiles, the others base
-  int w, end;           // the block's tiles, boundaries moved as below
+  int W, G, base, rem;  // the first rem blocks have base + 1, the others base
+  int slack;            // tiles by which a boundary moves to spare a cut
+  int w, end;           // the block's stretch, boundaries moved as below
   int b, g, n0;         // its first tile: sequence, head, key tile
 };
 struct Tiles {
-  const int* cum;  // shared memory: tiles before sequence b (one head)
-  int B, Hkv, whole;
-  // the same by a whole warp for one x: 32 probes at a time
+  const int* cum;  // shared memory: the cost of one head before sequence b
+  int B, Hkv, over, whole;
+  // the last b with Hkv * cum[b] <= x, by a whole warp: 32 probes at a time
   __device__ int find_warp(int x, int lane) const {
     int lo = 0, hi = B;
     while (hi - lo > 1) {
@@ -135,48 +144,38 @@ struct Tiles {
     }
     return lo;
   }
-  __device__ int find(int x) const {  // last b with Hkv * cum[b] <= x
-    int lo = 0, hi = B;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) / 2;
-      if (cum[mid] * Hkv <= x)
-        lo = mid;
-      else
-        hi = mid;
-    }
-    return lo;
-  }
-  // A block's stretch starts at tile x = c base + min(c, rem), moved to the nearer end of a
-  // (sequence, head) of at most `whole` tiles it would cut: joining a cut one costs about
-  // 3 us at the end, as much as five tiles, moving the boundary at most half the tiles.
-  // Inside longer ones the boundaries stay, so owner() needs the unmoved starts only.
-  __device__ int start(const SweepPlan& p, int c) const {
-    const int x = c * p.base + min(c, p.rem);
-    return x >= p.W ? p.W : moved(x, find(x));
-  }
-  __device__ int moved(int x, int i) const {  // x in sequence i
-    const int n = cum[i + 1] - cum[i];
-    if (n > whole) return x;
-    const int y = x - cum[i] * Hkv;
+  // The boundary x, in sequence i: at an end of its (sequence, head) if that is at most `slack` tiles away
+  // or the whole has at most `whole`, else as it is.
+  __device__ int moved(int x, int i, int slack) const {
+    const int n = cum[i + 1] - cum[i], y = x - cum[i] * Hkv;
     int off = y - (int)__fdividef((float)y, (float)n) * n;  // y mod n, the quotient within one
     off += off < 0 ? n : 0;
     off -= off >= n ? n : 0;
-    return 2 * off < n ? x - off : x - off + n;
+    const int up = n - off, down = off - over;
+    if (n - over <= whole) slack = n;
+    if (down <= slack && down <= up) return x - off;
+    return up <= slack ? x + up : x;
   }
-  // The block with tile x of a (sequence, head) that is cut.
-  __device__ int owner(const SweepPlan& p, int x) const {
+  __device__ int nt(int b) const { return cum[b + 1] - cum[b] - over; }
+  // The block whose unmoved stretch has x.
+  __device__ int at(const SweepPlan& p, int x) const {
     const int big = p.rem * (p.base + 1);
     return x < big ? x / (p.base + 1) : p.rem + (x - big) / p.base;
   }
+  // The first and last block of a (sequence, head) of n tiles that is cut, so has more than 2 slack
+  // + 1 of them: the boundaries within `slack` of its ends have moved there.
+  __device__ int first(const SweepPlan& p, int s0) const { return at(p, s0 + over + p.slack); }
+  __device__ int last(const SweepPlan& p, int s0, int n) const { return at(p, s0 + over + n - 1 - p.slack); }
 };
 // Walks a block's stretch segment by segment.
+template <int OVER>
 struct SegWalk {
   const int* cum;
   int Hkv, w, end;
   int b, g, n0, n1, nt;  // the segment: key tiles [n0, n1) of nt
-  __device__ void init(const int* c, int hkv, const volatile SweepPlan* p) {
-    cum = c;
-    Hkv = hkv;
+  __device__ void init(const Tiles& t, const volatile SweepPlan* p) {
+    cum = t.cum;
+    Hkv = t.Hkv;
     w = p->w;
     end = p->end;
     b = p->b;
@@ -185,15 +184,16 @@ struct SegWalk {
     nt = -1;
   }
   __device__ bool next() {
-    if (w >= end) return false;
-    if (nt >= 0) {  // the segment before ended with its (sequence, head)
+    if (nt >= 0) {  // the segment before ended with its (sequence, head), or the stretch with it
       n0 = 0;
       if (++g == Hkv) {
         g = 0;
         b++;
       }
     }
-    nt = cum[b + 1] - cum[b];
+    if (n0 == 0) w += OVER;
+    if (w >= end) return false;
+    nt = cum[b + 1] - cum[b] - OVER;
     n1 = min(nt, n0 + (end - w));
     w += n1 - n0;
     return true;
@@ -344,7 +344,7 @@ __device__ __forceinline__ void sweep_slices(SweepState<D, MT>& w, const uint32_
 }
 
 template <int D, int MT>
-__device__ bool sweep_consume(const PagedDecodeArgs& a, SegWalk sw, const int* len, uint8_t* smem, const SweepSmem& L,
+__device__ bool sweep_consume(const PagedDecodeArgs& a, SegWalk<seg_cost(D)> sw, const int* len, uint8_t* smem, const SweepSmem& L,
                               const SweepBars& bar, const volatile int* abort, int warp, int lane) {
   using C = Sweep<D>;
   constexpr int KS = D / 16;
@@ -362,13 +362,13 @@ __device__ bool sweep_consume(const PagedDecodeArgs& a, SegWalk sw, const int* l
   // S ahead of the one it works on: no other warp reads them, so a copy needs no barrier, and a
   // slice lies in one page, so small pages cost nothing (with tiled copies by a producer warp,
   // pages of 16 took 0.87 us a tile and larger ones 0.70).
-  const auto slices = [&](const SegWalk& s) { return (s.n1 - s.n0) << lm; };
-  const auto place = [&](const SegWalk& s, int k) {
+  const auto slices = [&](const auto& s) { return (s.n1 - s.n0) << lm; };
+  const auto place = [&](const auto& s, int k) {
     return (s.n0 + (k >> lm)) * kTK + (kg + (k & ((1 << lm) - 1)) * KG) * 16;
   };
   // Page numbers come 32 slices at a time, one to a lane and a window ahead: -1 where nothing is
   // to be read, -2 for a bad page.
-  const auto window = [&](const SegWalk& s, int k0) {
+  const auto window = [&](const auto& s, int k0) {
     const int base = sweep_base(a, len[s.b]), own = len[s.b] - base, k = k0 + lane;
     int id = -1;
     if (k < slices(s)) {
@@ -384,7 +384,7 @@ __device__ bool sweep_consume(const PagedDecodeArgs& a, SegWalk sw, const int* l
     }
     return id;
   };
-  SegWalk is = sw, ls = sw;  // the segment being copied, and that of the window after this one
+  SegWalk<seg_cost(D)> is = sw, ls = sw;  // the segment being copied, and that of the window after this one
   bool ion = is.next(), lon = ls.next();
   int ik = 0, iw = 0, lk = 0, islot = 0, id = -1, nid = -1;
   const auto look = [&]() {
@@ -544,14 +544,13 @@ __device__ __forceinline__ void put_row(const PagedDecodeArgs& a, bool prefix, i
 // head) is written out; a segment leaves its part in the workspace and is counted, and the block that counts
 // the last one notes it in todo[first or second segment of the block] for its consumers.
 template <int D, int MT, bool PREFIX>
-__device__ bool sweep_finish(const PagedDecodeArgs& a, SegWalk sw, const Tiles& tl, const SweepPlan& plan, const int* len,
+__device__ bool sweep_finish(const PagedDecodeArgs& a, SegWalk<seg_cost(D)> sw, const Tiles& tl, const SweepPlan& plan, const int* len,
                              uint8_t* smem, const SweepSmem& L, const SweepBars& bar, volatile int* todo,
                              const volatile int* abort, int blk, int f, int lane) {
   constexpr int kBufs = sweep_bufs(D, MT);
   const int parts = MT < 4 ? kWarps : kWarps / a.MG;  // warps that hold a part of a row
   const float* scratch = reinterpret_cast<const float*>(smem + L.scratch) + f * kWarps * MT * 8 * D;
   const float2* ml = reinterpret_cast<const float2*>(smem + L.ml) + f * kWarps * MT * 8;
-  const int first = sw.w;
   bool waited = false;
   for (int seg = 0; sw.next(); seg++) {
     if (seg % kBufs != f) continue;
@@ -561,7 +560,7 @@ __device__ bool sweep_finish(const PagedDecodeArgs& a, SegWalk sw, const Tiles& 
     }
     if (!__all_sync(0xffffffffu, mbar_wait(bar.parts_full + f, (seg / kBufs) & 1, abort))) return false;
     const bool whole = sw.n0 == 0 && sw.n1 == sw.nt;
-    const int s0 = tl.cum[sw.b] * tl.Hkv + sw.g * sw.nt, slot = s0 <= first ? 0 : 1;
+    const int slot = sw.n0 > 0 ? 0 : 1;  // a block's first segment is the only one that begins inside
     const bool pre = PREFIX && sweep_base(a, len[sw.b]) > 0;
     // a lane takes columns 4 q .. and 4 (q + D / 8) .. of a row
     constexpr int kQ = D / 8;
@@ -595,7 +594,8 @@ __device__ bool sweep_finish(const PagedDecodeArgs& a, SegWalk sw, const Tiles& 
     if (whole) continue;
     __syncwarp();  // the other lanes' parts before lane 0's release
     if (lane == 0) {
-      const int c0 = tl.owner(plan, s0), c1 = tl.owner(plan, s0 + sw.nt - 1);
+      const int s0 = tl.cum[sw.b] * tl.Hkv + sw.g * (sw.nt + tl.over);
+      const int c0 = tl.first(plan, s0), c1 = tl.last(plan, s0, sw.nt);
       if (count_segment(a.done + c0, (unsigned)(c1 - c0))) todo[slot] = sw.b * tl.Hkv + sw.g;
     }
     __syncwarp();
@@ -616,15 +616,14 @@ __device__ bool sweep_join(const PagedDecodeArgs& a, const Tiles& tl, const Swee
     const int sh = todo[k];
     if (sh < 0) continue;
     __threadfence();
-    const int b = sh / tl.Hkv, g = sh - b * tl.Hkv, nt = tl.cum[b + 1] - tl.cum[b];
-    const int s0 = tl.cum[b] * tl.Hkv + g * nt;
-    const int c0 = tl.owner(plan, s0), c1 = tl.owner(plan, s0 + nt - 1);
-    const int first = 2 * c0 + (s0 <= tl.start(plan, c0) ? 0 : 1);
+    const int b = sh / tl.Hkv, g = sh - b * tl.Hkv, nt = tl.nt(b);
+    const int s0 = tl.cum[b] * tl.Hkv + g * (nt + tl.over);
+    const int c0 = tl.first(plan, s0), c1 = tl.last(plan, s0, nt);
     const int sub = tid % kSplit, items = a.R * (D / 4);
     for (int i0 = 0; i0 < items; i0 += kThreads / kSplit) {
       const int i = min(i0 + tid / kSplit, items - 1);
       const int r = i / (D / 4), q = i % (D / 4);
-      const auto at = [&](int c) { return (size_t)(c == c0 ? first : 2 * c) * a.R + r; };
+      const auto at = [&](int c) { return (size_t)(2 * c + (c == c0 ? 1 : 0)) * a.R + r; };
       RowSum x;
       for (int c = c0 + sub; c <= c1; c += kSplit * kAhead) {
         float2 z[kAhead];
@@ -681,7 +680,7 @@ __global__ void __launch_bounds__(kSweepThreads, 1) k_paged_sweep(const __grid_c
   volatile int* abort = reinterpret_cast<volatile int*>(smem + kOffVars);
   volatile int* todo = abort + 1;                              // [2]
   volatile SweepPlan* splan = reinterpret_cast<volatile SweepPlan*>(const_cast<int*>(abort) + 3);
-  int* wsum = const_cast<int*>(abort) + 12;                    // [12] the scan's warp totals
+  int* wsum = const_cast<int*>(abort) + 16;                    // [12] the scan's warp totals
   int* cum = reinterpret_cast<int*>(smem + kOffCum);
   int* len = cum + a.B + 1;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -702,7 +701,7 @@ __global__ void __launch_bounds__(kSweepThreads, 1) k_paged_sweep(const __grid_c
       }
       n = max(n, 0);
       len[b] = n;
-      nt = max(1, (n - sweep_base(a, n) + kTK - 1) / kTK);  // one even where nothing is read: its rows are written
+      nt = seg_cost(D) + max(1, (n - sweep_base(a, n) + kTK - 1) / kTK);  // one even where nothing is read: its rows are written
     }
     int x = nt;
     if (b0 + warp * 32 < a.B) {
@@ -752,6 +751,7 @@ __global__ void __launch_bounds__(kSweepThreads, 1) k_paged_sweep(const __grid_c
   tl.cum = cum;
   tl.B = a.B;
   tl.Hkv = a.Hkv;
+  tl.over = seg_cost(D);
   tl.whole = whole_tiles(D);
   // two warps divide the work (a division costs every warp its issue slots): the block's first tile
   // and the next block's
@@ -764,16 +764,19 @@ __global__ void __launch_bounds__(kSweepThreads, 1) k_paged_sweep(const __grid_c
     const int c = blk + warp, x = c * p.base + min(c, p.rem);
     const bool any = blk < p.G && x < p.W;
     p.b = tl.find_warp(min(x, p.W - 1), lane);
-    p.w = any ? tl.moved(x, p.b) : p.W;
+    p.slack = min(max_slack(D), p.base / 2);
+    p.w = any ? tl.moved(x, p.b, p.slack) : p.W;
     if (lane == 0 && warp == 1) splan->end = p.w;
     if (lane == 0 && warp == 0) {
       if (p.w == cum[p.b + 1] * a.Hkv) p.b++;  // moved to the next sequence's first tile
       if (p.b == a.B) p.b--;                   // nothing left
-      const int nt = cum[p.b + 1] - cum[p.b], off = p.w - cum[p.b] * a.Hkv;
-      p.g = (int)__fdividef((float)off, (float)nt);  // within one of off / nt
-      p.n0 = off - p.g * nt;
-      while (p.n0 < 0) p.g--, p.n0 += nt;
-      while (p.n0 >= nt) p.g++, p.n0 -= nt;
+      const int n = cum[p.b + 1] - cum[p.b], off = p.w - cum[p.b] * a.Hkv;
+      p.g = (int)__fdividef((float)off, (float)n);  // within one of off / n
+      p.n0 = off - p.g * n;
+      while (p.n0 < 0) p.g--, p.n0 += n;
+      while (p.n0 >= n) p.g++, p.n0 -= n;
+      p.n0 = max(p.n0 - tl.over, 0);
+      splan->slack = p.slack;
       splan->W = p.W;
       splan->G = p.G;
       splan->base = p.base;
@@ -785,8 +788,8 @@ __global__ void __launch_bounds__(kSweepThreads, 1) k_paged_sweep(const __grid_c
     }
   }
   __syncthreads();
-  SegWalk sw;
-  sw.init(cum, a.Hkv, splan);
+  SegWalk<seg_cost(D)> sw;
+  sw.init(tl, splan);
   // registers: 384 x 168 at launch; 256 x 216 for the consumers, 128 x 72 for the others
   if (warp < kWarps) {
     regs_inc<216>();
@@ -796,6 +799,7 @@ __global__ void __launch_bounds__(kSweepThreads, 1) k_paged_sweep(const __grid_c
       p.W = splan->W;
       p.base = splan->base;
       p.rem = splan->rem;
+      p.slack = splan->slack;
       ok = sweep_join<D, MT, PREFIX>(a, tl, p, len, bar, todo, abort, tid);
     }
     if (!ok && lane == 0) {
@@ -842,6 +846,7 @@ __global__ void __launch_bounds__(kSweepThreads, 1) k_paged_sweep(const __grid_c
     p.W = splan->W;
     p.base = splan->base;
     p.rem = splan->rem;
+    p.slack = splan->slack;
     ok = sweep_finish<D, MT, PREFIX>(a, sw, tl, p, len, smem, L, bar, todo, abort, blk, warp - kWarps - 1, lane);
   }
   if (!ok && lane == 0) {
