@@ -1511,6 +1511,8 @@ int ne_attn_decode_paged(const void* q, const void* q_w, const void* k_pages, co
   a.D = D;
   a.G = Hq / Hkv;
   a.R = a.G * Tq;
+  a.div_r = make_fastdiv((uint32_t)a.R);
+  a.div_g = make_fastdiv((uint32_t)a.G);
   a.page_shift = log2_of(page_size);
   a.num_pages = num_pages;
   a.max_pages = max_pages;

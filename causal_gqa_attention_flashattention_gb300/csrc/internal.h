@@ -255,9 +255,12 @@ struct PrefixCut {
     const int s = per ? c / per : 0, i = c - s * per;
     return s * ntk + i * base + min(i, rem);
   }
-  __device__ int owner(int x) const {  // the block with tile x
-    const int s = per ? x / ntk : 0, y = x - s * ntk, big = rem * (base + 1);
-    return s * per + (y < big ? y / (base + 1) : rem + (y - big) / base);
+  // the first and last block of the (head, pair) s
+  __device__ int first(int s) const { return per ? s * per : at(s * ntk); }
+  __device__ int last(int s) const { return per ? s * per + min(per, ntk) - 1 : at(s * ntk + ntk - 1); }
+  __device__ int at(int x) const {  // the block with tile x of the one line
+    const int big = rem * (base + 1);
+    return x < big ? x / (base + 1) : rem + (x - big) / base;
   }
 };
 #endif
@@ -282,6 +285,7 @@ struct PagedDecodeArgs {
   int base;         // shared positions that the prefix kernel reads (0: none, the sweep reads all)
   int tiles, MG;    // packed row tiles (8 rows each) and the groups of warps that share them
   FastDiv div_grid; // by the sweep's blocks
+  FastDiv div_r, div_g;  // by R, G
   int own_counters; // done is the library's: 0 before and after every call
   float eps, scale_log2;
 };
@@ -290,9 +294,9 @@ struct PagedDecodeArgs {
 // kernel calls pdl_wait before it touches what that one writes.
 #ifdef __CUDACC__
 template <typename... P, typename... A>
-cudaError_t launch_pdl(void (*k)(P...), int grid, int block, size_t smem, cudaStream_t s, A... args) {
+cudaError_t launch_pdl(void (*k)(P...), dim3 grid, int block, size_t smem, cudaStream_t s, A... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3((unsigned)block);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;

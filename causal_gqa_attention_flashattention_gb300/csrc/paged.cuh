@@ -23,7 +23,7 @@ template <int D>
 __device__ __forceinline__ QueryChunk query_load(const PagedDecodeArgs& a, int b, int g, int r, int c, int pos0) {
   QueryChunk x;
   x.on = r < a.R;
-  const int t = x.on ? r / a.G : 0, gg = r - t * a.G;
+  const int t = x.on ? (int)fdiv((uint32_t)r, a.div_g) : 0, gg = r - t * a.G;
   x.v = make_uint4(0, 0, 0, 0);
   if (x.on) x.v = load_rope_chunk<D>(a.q + (size_t)(b * a.Tq + t) * a.q_stride + (g * a.G + gg) * D, c, a.rope_half != 0);
   rope_coeffs<D>(a.rope, max(pos0 + t, 0), c, x.c0, x.c1);
@@ -71,7 +71,7 @@ __device__ __forceinline__ void query_finish(const PagedDecodeArgs& a, const Que
 // Row r of (sequence b, head g), columns 4 q .. 4 q + 3: normalise and write.
 template <int D>
 __device__ __forceinline__ void write_row(const PagedDecodeArgs& a, int b, int g, int r, int q, float4 v, float M, float L) {
-  const int t = r / a.G, h = g * a.G + (r - t * a.G);
+  const int t = (int)fdiv((uint32_t)r, a.div_g), h = g * a.G + (r - t * a.G);
   const float inv = L > 0.f ? 1.f / L : 0.f;
   const size_t at = (((size_t)b * a.Tq + t) * a.Hq + h) * D + 4 * q;
   v = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);

@@ -12,22 +12,20 @@ namespace {
 template <int D>
 __global__ void __launch_bounds__(128) k_prefix_join(const __grid_constant__ PagedDecodeArgs a) {
   const PrefixArgs& p = a.pre;
-  pdl_wait();
-  const int lane = threadIdx.x & 31;
-  const long long w = blockIdx.x * 4LL + threadIdx.x / 32;  // (head, tile, 32 rows, quad)
-  const int q = (int)(w % (D / 4)), r32 = (int)(w / (D / 4) % (kTile / 32));
-  const long long gt = w / (D / 4) / (kTile / 32);
-  const int g = (int)(gt / p.tiles), tile = (int)(gt - (long long)g * p.tiles);
-  if (g >= a.Hkv) return;
+  const int lane = threadIdx.x & 31, tile = blockIdx.y, g = blockIdx.z;
+  const int w = blockIdx.x * 4 + threadIdx.x / 32, q = w % (D / 4), r32 = w / (D / 4);
   const int row = r32 * 32 + lane, s = g * p.pairs + (tile >> 1), u = tile & 1;
-  const int rho = tile * kTile + row, b = rho / a.R, r = rho - b * a.R;
+  const int rho = tile * kTile + row, b = (int)fdiv((uint32_t)rho, a.div_r), r = rho - b * a.R;
   if (b >= a.B) return;
-  if (sweep_base(a, max(0, min(a.len[b], a.max_pages << a.page_shift))) == 0) return;  // the sweep has written it
-  const PrefixCut cut(p.ntk, a.Hkv * p.pairs, max(1, min(__ldcg(p.cut), min(kPagedMaxBlocks, p.W))));
-  const int lo = cut.owner(s * p.ntk), hi = cut.owner(s * p.ntk + p.ntk - 1);
-  const size_t own = (size_t)gt * kTile + row;
+  const int len = max(0, min(a.len[b], a.max_pages << a.page_shift));
+  pdl_wait();
+  const int blocks = __ldcg(p.cut);
+  const size_t own = ((size_t)g * p.tiles + tile) * kTile + row;
   const float2 zo = __ldcg(p.ml + own);
   const float4 xo = __ldcg(reinterpret_cast<const float4*>(p.o + own * D) + q);
+  if (sweep_base(a, len) == 0) return;  // the sweep has written it
+  const PrefixCut cut(p.ntk, a.Hkv * p.pairs, max(1, min(blocks, min(kPagedMaxBlocks, p.W))));
+  const int lo = cut.first(s), hi = cut.last(s);
   // eight segments' loads under way at a time
   constexpr int kAhead = 8;
   float top = -INFINITY, S = 0.f;
@@ -63,8 +61,7 @@ __global__ void __launch_bounds__(128) k_prefix_join(const __grid_constant__ Pag
 
 template <int D>
 cudaError_t launch_join(const PagedDecodeArgs& a, cudaStream_t s) {
-  const long long warps = (long long)a.Hkv * a.pre.tiles * (kTile / 32) * (D / 4);
-  return launch_pdl(k_prefix_join<D>, (int)((warps + 3) / 4), 128, 0, s, a);
+  return launch_pdl(k_prefix_join<D>, dim3(kTile / 32 * (D / 4) / 4, a.pre.tiles, a.Hkv), 128, 0, s, a);
 }
 
 }  // namespace

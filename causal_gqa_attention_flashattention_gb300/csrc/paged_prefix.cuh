@@ -86,52 +86,30 @@ struct PreSeg {
   __device__ int units(const PrefixArgs& p) const { return 2 * (s % p.pairs) + 1 < p.tiles ? 2 : 1; }
 };
 
-// A row of the packed tile, normalised and rotated, as fp16 high and low parts into the swizzled
-// tiles at dst and behind it.
+// Rows r0 .. r0 + 31 of a packed tile whose first row is rho0, normalised and rotated, as fp16 high and low
+// parts into the swizzled tiles at dst and behind it.  D / 8 neighbouring lanes to a row, so that a
+// load takes whole lines (a lane to a row took 3 us more), all of the warp's rows under way at once.
 template <int D>
-__device__ __forceinline__ void pack_query_row(const PagedDecodeArgs& a, const int* len, int g, int rho, uint8_t* dst,
-                                               int r) {
-  constexpr int kCPR = D / 8;
-  const int b = rho / a.R, rr = rho - b * a.R;
-  const bool on = b < a.B;
-  const int t = on ? rr / a.G : 0, gg = rr - t * a.G;
-  const bool half = a.rope_half != 0;
-  const __nv_bfloat16* row = a.q + (size_t)(on ? b * a.Tq + t : 0) * a.q_stride + (on ? g * a.G + gg : 0) * D;
-  const int pos = on ? max(len[b] - a.Tq + t, 0) : 0;
-  uint4 v[kCPR];
-  float4 c0[kCPR], c1[kCPR];
+__device__ __forceinline__ void pack_query_rows(const PagedDecodeArgs& a, const int* len, int g, int rho0, uint8_t* dst,
+                                                int r0, int lane) {
+  constexpr int kCPR = D / 8, kRows = 32 / kCPR, kPasses = 32 / kRows;
+  const int c = lane % kCPR;
+  uint4 wv = make_uint4(0, 0, 0, 0);
+  if (a.qw) wv = load_rope_chunk<D>(a.qw, c, a.rope_half != 0);
+  QueryChunk x[kPasses];
 #pragma unroll
-  for (int c = 0; c < kCPR; c++) {
-    v[c] = load_rope_chunk<D>(row, c, half);
-    rope_coeffs<D>(a.rope, pos, c, c0[c], c1[c]);
-  }
-  float rs = 1.f;
-  if (a.qw) {
-    float ss = 0.f;
-#pragma unroll
-    for (int c = 0; c < kCPR; c++) {
-      const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
-#pragma unroll
-      for (int p = 0; p < 4; p++) ss = fmaf(bf_lo(w[p]), bf_lo(w[p]), fmaf(bf_hi(w[p]), bf_hi(w[p]), ss));
-    }
-    rs = rsqrtf(fmaf(ss, 1.f / D, a.eps));
+  for (int i = 0; i < kPasses; i++) {
+    const int rho = rho0 + r0 + i * kRows + lane / kCPR, b = (int)fdiv((uint32_t)rho, a.div_r);
+    const bool on = b < a.B;
+    x[i] = query_load<D>(a, on ? b : 0, g, on ? rho - b * a.R : a.R, c, on ? len[b] - a.Tq : 0);
   }
 #pragma unroll
-  for (int c = 0; c < kCPR; c++) {
-    uint4 wv = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);  // ones
-    if (a.qw) wv = load_rope_chunk<D>(a.qw, c, half);
-    const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w}, ww[4] = {wv.x, wv.y, wv.z, wv.w};
-    const float cs[4] = {c0[c].x, c0[c].z, c1[c].x, c1[c].z}, sn[4] = {c0[c].y, c0[c].w, c1[c].y, c1[c].w};
-    uint32_t h[4], l[4];
-#pragma unroll
-    for (int p = 0; p < 4; p++) {
-      const float x0 = bf_lo(w[p]) * (rs * bf_lo(ww[p])), x1 = bf_hi(w[p]) * (rs * bf_hi(ww[p]));
-      const float y0 = fmaf(x0, cs[p], -x1 * sn[p]), y1 = fmaf(x0, sn[p], x1 * cs[p]);
-      h[p] = on ? pack_f16(y0, y1) : 0u;
-      l[p] = on ? pack_f16(y0 - f16_lo(h[p]), y1 - f16_hi(h[p])) : 0u;
-    }
-    *reinterpret_cast<uint4*>(dst + swz(r, c, D * 2)) = make_uint4(h[0], h[1], h[2], h[3]);
-    *reinterpret_cast<uint4*>(dst + PreCfg<D>::kTileBytes + swz(r, c, D * 2)) = make_uint4(l[0], l[1], l[2], l[3]);
+  for (int i = 0; i < kPasses; i++) {
+    const int r = r0 + i * kRows + lane / kCPR;
+    uint4 hi, lo;
+    query_finish<D>(a, x[i], a.qw != nullptr, wv, hi, lo);
+    *reinterpret_cast<uint4*>(dst + swz(r, c, D * 2)) = hi;
+    *reinterpret_cast<uint4*>(dst + PreCfg<D>::kTileBytes + swz(r, c, D * 2)) = lo;
   }
 }
 
@@ -338,7 +316,7 @@ __device__ void prefix_role(const PagedDecodeArgs& a, const int* len, uint8_t* s
       {
         if (e >= 1) ok = __all_sync(0xffffffffu, mbar_wait(q_empty + u, (e - 1) & 1, abort));
         if (!ok) break;
-        pack_query_row<D>(a, len, sg.s / p.pairs, (2 * (sg.s % p.pairs) + u) * kTile + r, smem + 2 * u * TB, r);
+        pack_query_rows<D>(a, len, sg.s / p.pairs, (2 * (sg.s % p.pairs) + u) * kTile, smem + 2 * u * TB, q4 * 32, lane);
         fence_proxy_async_smem();
         warp_arrive(q_full + u);
         e++;

@@ -454,7 +454,7 @@ __device__ bool sweep_consume(const PagedDecodeArgs& a, SegWalk<seg_cost(D)> sw,
       w.mx[m] = -INFINITY;
       w.ls[m] = 0.f;
       const int r = (mg * MT + m) * 8 + (lane >> 2);
-      w.lim[m] = r < a.R ? w.pos0 + r / a.G : w.own - 1;
+      w.lim[m] = r < a.R ? w.pos0 + (int)fdiv((uint32_t)r, a.div_g) : w.own - 1;
 #pragma unroll
       for (int i = 0; i < 2 * KS; i++)
 #pragma unroll
