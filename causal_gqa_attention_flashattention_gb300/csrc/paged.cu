@@ -22,7 +22,7 @@ namespace {
 // past cu[B] belong to none and are skipped) and to position pos0[s] + n - cu[s].
 // A thread takes one 16-byte chunk of a key row and of the value row; the D / 8
 // threads of a row are neighbouring lanes (the norm adds up squares by shuffles).  Bound by the
-// bytes: 23 prompts with 17,000 rows of four heads (34.9 MB) take 9.1 us, a step of 64 tokens 3.3 us.
+// bytes: 23 prompts with 17,000 rows of four heads (34.9 MB) take 9.3 us, a step of 64 tokens 3.1 us.
 template <int D>
 __global__ void __launch_bounds__(128) k_kv_append_paged(const PagedAppendArgs a) {
   constexpr int kCPR = D / 8;

@@ -31,8 +31,8 @@ namespace {
 // of the cache, and a warp that owns its 16 keys end to end (copies, scores, weights,
 // P V in registers) needs no hand-off between warps per tile.  It works two tiles off in
 // 0.7 us, HBM delivers them in 1.4 us (7.1 TB/s over a long context); the contiguous cache's
-// tcgen05 sweep takes 0.9 us for one.  16 contexts around 8192 positions (127 MB) 28.2 us,
-// one of 131001 29.3 us; a short context 7.8 us, the chain of lengths, table, page and join.
+// tcgen05 sweep takes 0.9 us for one.  16 contexts around 8192 positions (127 MB) 28.0 us,
+// one of 131001 29.3 us; a short context 7.3 us, the chain of lengths, table, page and join.
 template <int D>
 struct Sweep {
   static constexpr uint32_t kSpan = D * 2;

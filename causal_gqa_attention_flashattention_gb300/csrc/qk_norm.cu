@@ -47,8 +47,8 @@ constexpr int kAtOnce = 2;  // rows a thread has under way
 // chunk of every row it gets, so its part of the weight stays in registers.  Few registers, and
 // as many blocks as the SMs hold at once, carry these kernels: with four heads of a position per
 // thread (one read of its table row for them, both weights in registers) the forward took 15.0 us
-// at 16 x 512 positions, 12/4 heads, D = 64, with two heads 11.6 us, in this form 8.5 us (33.6 MB,
-// 3.9 TB/s); the backward 28.3 us, in this form 17.1 us (50 MB, with the sums of dw).
+// at 16 x 512 positions, 12/4 heads, D = 64, with two heads 11.6 us, in this form 8.1 us (33.6 MB,
+// 4.1 TB/s); the backward 28.3 us, in this form 14.3 us (50 MB, with the sums of dw).
 template <int D>
 struct Side {
   bool isq;
