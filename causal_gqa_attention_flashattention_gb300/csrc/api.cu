@@ -109,6 +109,7 @@ struct JoinScratch {
   size_t bytes;
 };
 constexpr size_t kCounterBytes = 1024;
+constexpr size_t kJoinStreams = 64;  // streams that have one at a time
 
 struct DeviceState {
   bool init = false;
@@ -317,6 +318,15 @@ int join_scratch(DeviceState& d, cudaStream_t s, size_t need, void** ws, unsigne
   JoinScratch* f = nullptr;
   for (auto& x : d.join_scratch)
     if (x.stream == id) f = &x;
+  if (!f && d.join_scratch.size() >= kJoinStreams) {
+    // a program that keeps making streams: the oldest one's go (cudaFree waits for the device)
+    JoinScratch& x = d.join_scratch.front();
+    if (x.ptr && cudaFree(x.ptr) != cudaSuccess) return NE_ERR_CUDA;
+    x.ptr = nullptr;
+    x.bytes = 0;
+    if (cudaFree(x.counters) != cudaSuccess) return NE_ERR_CUDA;
+    d.join_scratch.erase(d.join_scratch.begin());
+  }
   if (!f) {
     JoinScratch x = {id, nullptr, nullptr, 0};
     if (cudaMalloc(&x.counters, kCounterBytes) != cudaSuccess) return NE_ERR_CUDA;

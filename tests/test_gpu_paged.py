@@ -390,6 +390,34 @@ def test_streams_and_graphs(nb):
             assert torch.equal(o[0], wants[k][0]) and torch.equal(o[1], wants[k][1])
 
 
+def test_many_streams(nb):
+    """More streams than the library keeps workspaces for, each used once, then the first again."""
+    import ctypes
+    s = setup([700, 3000, 40], 1, 8, 2, 64, 32, seed=12)
+    call = lambda: nb.attn_decode_paged(s["q"], s["kp"], s["vp"], s["table"], s["lens"], o_dtype=torch.float32)
+    want = call()
+    rt, handles = torch.cuda.cudart(), []
+    torch.cuda.synchronize()
+    for _ in range(70):
+        h = ctypes.c_void_p()
+        assert int(rt.cudaStreamCreate(ctypes.addressof(h))) == 0
+        handles.append(h.value)
+    try:
+        for h in handles + handles[:3]:
+            stream = torch.cuda.ExternalStream(h)
+            with torch.cuda.stream(stream):
+                got = call()
+            stream.synchronize()
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    finally:
+        torch.cuda.synchronize()
+        for h in handles:
+            rt.cudaStreamDestroy(h)
+    got = call()
+    assert torch.equal(got[0], want[0])
+    nb.check_status()
+
+
 def test_two_streams_at_once(nb):
     """Calls that run side by side on streams of their own, with the library's workspaces."""
     lens = [5000, 2000, 40, 3000]
