@@ -59,6 +59,9 @@ constexpr int max_slack(int D) { return D == 64 ? 3 : 6; }
 
 // Buffers for the warps' parts of a finished segment, each with a finishing warp of its own.
 constexpr int sweep_bufs(int D, int mt) { return D * mt <= 64 ? 2 : 1; }
+// Warps that pack queries: with more than 8 rows those that do not finish segments (one of them alone
+// takes about 1 us for 8 rows, in front of the block's first tile).
+constexpr int query_warps(int D, int mt) { return mt == 1 ? 1 : 4 - sweep_bufs(D, mt); }
 
 // Shared memory: barriers, the block's plan and the sequences' lengths first, then (from a
 // 1024-byte boundary) the ring and what else a role keeps.  tiles: packed row tiles, mt: of one warp.
@@ -220,23 +223,76 @@ struct RowSum {
 };
 
 struct SweepBars {
-  uint64_t *q_full, *q_empty, *parts_full, *parts_empty, *fin;
+  uint64_t *q_full, *q_empty, *parts_full, *parts_empty, *fin, *stored;
 };
 
-// What a consumer warp holds of a segment: MT row tiles' queries (in registers for at most two
-// of them, else read from shared memory as they are used), O, running maximum and sum.
+// What a consumer warp holds of a segment: its rows' queries (in registers for at most 16 rows, else
+// read from shared memory as they are used), O, running maximum and sum.  Up to 8 rows they are
+// twice in one matrix tile, high and low parts; with more a tile has 16 rows, and the parts are
+// two products into the same sums, which halves O's registers (28 rows 67 us with pairs of
+// 8, NN in this form).
 template <int D, int MT>
 struct SweepState {
-  static constexpr int KS = D / 16, kQ = MT <= 2 ? MT : 1;
-  uint32_t q[kQ][KS][4], qbase;
-  float o[MT][2 * KS][4], mx[MT], ls[MT];
-  int lim[MT];      // last visible position of this lane's row, from the own part's start
+  static constexpr int KS = D / 16;
+  static constexpr bool kTwice = MT == 1;
+  static constexpr int MF = kTwice ? 1 : MT / 2;      // matrix tiles
+  static constexpr int kParts = kTwice ? 1 : 2, kH = kTwice ? 1 : 2;  // products of a score; rows of a lane in a tile
+  static constexpr bool kQRegs = MT <= 2;
+  uint32_t q[kQRegs ? MF : 1][kParts][KS][4], qbase;
+  float o[MF][2 * KS][4], mx[MF][kH], ls[MF][kH];
+  int lim[MF][kH];  // last visible position of this lane's rows, from the own part's start
   int own, pos0;    // positions of the own part; row 0's position
+
+  // Part p of the queries of tile m, columns 16 k ..: rows 8 .. 15 of the fragment come from the low
+  // parts behind the eight rows, or from the next eight rows.
+  __device__ __forceinline__ uint32_t q_at(int m, int p, int k, int lane) const {
+    constexpr uint32_t kSpan = Sweep<D>::kSpan;
+    const uint32_t lrow = lane & 15, lchk = lane >> 4;
+    if (kTwice) return qbase + swz(lrow, 2 * k + lchk, kSpan);
+    return qbase + (2 * m + (lrow >> 3)) * 16 * kSpan + swz((lrow & 7) + 8 * p, 2 * k + lchk, kSpan);
+  }
+  __device__ __forceinline__ void begin(const PagedDecodeArgs& a, int mg, int lane) {
+#pragma unroll
+    for (int m = 0; m < MF; m++) {
+#pragma unroll
+      for (int h = 0; h < kH; h++) {
+        mx[m][h] = -INFINITY;
+        ls[m][h] = 0.f;
+        const int r = (mg * MT + kH * m + h) * 8 + (lane >> 2);
+        lim[m][h] = r < a.R ? pos0 + (int)fdiv((uint32_t)r, a.div_g) : own - 1;
+      }
+#pragma unroll
+      for (int i = 0; i < 2 * KS; i++)
+#pragma unroll
+        for (int e = 0; e < 4; e++) o[m][i][e] = 0.f;
+    }
+  }
+  // The segment's parts: row (lane / 4) of each eight, maximum in log2 units.
+  __device__ __forceinline__ void store(float* scratch, float2* ml, int warp, float sl2, int lane) {
+#pragma unroll
+    for (int m = 0; m < MF; m++)
+#pragma unroll
+      for (int h = 0; h < kH; h++) {
+        float l = ls[m][h];
+        l += __shfl_xor_sync(0xffffffffu, l, 1);
+        l += __shfl_xor_sync(0xffffffffu, l, 2);
+        const int row = (warp * MT + kH * m + h) * 8 + (lane >> 2);
+        if ((lane & 3) == 0) ml[row] = make_float2(mx[m][h] == -INFINITY ? -INFINITY : __fmul_rn(mx[m][h], sl2), l);
+#pragma unroll
+        for (int i = 0; i < 2 * KS; i++)
+          *reinterpret_cast<float2*>(scratch + row * D + i * 8 + (lane & 3) * 2) =
+              kTwice ? make_float2(o[m][i][0] + o[m][i][2], o[m][i][1] + o[m][i][3])
+                     : make_float2(o[m][i][2 * h], o[m][i][2 * h + 1]);
+      }
+  }
 };
 // Slices of 16 keys that a warp takes together: two where the registers allow it, which gives
 // its chain of dependent steps (scores, maximum, weights, P V) something to overlap with.
 template <int D, int MT>
-constexpr int kSlicesAtOnce = MT * D <= 128 ? 2 : 1;
+#ifndef NSL
+#define NSL (MT * D <= 128 ? 2 : 1)
+#endif
+constexpr int kSlicesAtOnce = NSL;
 
 // N slices (keys at kb, values at vb, first position j0) into the state.
 template <int D, int MT, int N>
@@ -270,82 +326,177 @@ __device__ __forceinline__ void sweep_slices(SweepState<D, MT>& w, const uint32_
       }
     }
   }
+  using W = SweepState<D, MT>;
+  constexpr int kH = W::kH, kV = 4 * kH;  // rows and values of a slice per lane
 #pragma unroll
-  for (int m = 0; m < MT; m++) {
+  for (int m = 0; m < W::MF; m++) {
     float sa[N][4], sb[N][4];
 #pragma unroll
     for (int i = 0; i < N; i++)
 #pragma unroll
       for (int e = 0; e < 4; e++) sa[i][e] = sb[i][e] = 0.f;
 #pragma unroll
-    for (int k = 0; k < KS; k++) {
-      uint32_t qt[4];
-      if (MT <= 2) {
+    for (int k = 0; k < KS; k++)
 #pragma unroll
-        for (int e = 0; e < 4; e++) qt[e] = w.q[MT <= 2 ? m : 0][k][e];
-      } else {
-        ldsm4(qt, w.qbase + m * 16 * kSpan + swz(lrow, 2 * k + lchk, kSpan));
-      }
+      for (int p = 0; p < W::kParts; p++) {
+        uint32_t qt[4];
+        if (W::kQRegs) {
 #pragma unroll
-      for (int i = 0; i < N; i++) {
-        mma_f16(sa[i], qt, kf[i][k][0], kf[i][k][2]);
-        mma_f16(sb[i], qt, kf[i][k][1], kf[i][k][3]);
+          for (int e = 0; e < 4; e++) qt[e] = w.q[W::kQRegs ? m : 0][p][k][e];
+        } else {
+          ldsm4(qt, w.q_at(m, p, k, lane));
+        }
+#pragma unroll
+        for (int i = 0; i < N; i++) {
+          mma_f16(sa[i], qt, kf[i][k][0], kf[i][k][2]);
+          mma_f16(sb[i], qt, kf[i][k][1], kf[i][k][3]);
+        }
       }
-    }
-    // keys (lane & 3) * 2 + {0, 1} and those + 8, row lane / 4: high + low part
-    float x[N][4], t = -INFINITY;
+    // row h, keys (lane & 3) * 2 + {0, 1} and those + 8 at 4 h .. 4 h + 3
+    float x[N][kV], t[kH];
+#pragma unroll
+    for (int h = 0; h < kH; h++) t[h] = -INFINITY;
 #pragma unroll
     for (int i = 0; i < N; i++) {
-      x[i][0] = sa[i][0] + sa[i][2];
-      x[i][1] = sa[i][1] + sa[i][3];
-      x[i][2] = sb[i][0] + sb[i][2];
-      x[i][3] = sb[i][1] + sb[i][3];
+      if (W::kTwice) {  // high + low part
+        x[i][0] = sa[i][0] + sa[i][2];
+        x[i][1] = sa[i][1] + sa[i][3];
+        x[i][2] = sb[i][0] + sb[i][2];
+        x[i][3] = sb[i][1] + sb[i][3];
+      } else {
+#pragma unroll
+        for (int e = 0; e < kV; e++) x[i][e] = (e & 2 ? sb : sa)[i][(e >> 2) * 2 + (e & 1)];
+      }
       if (j0[i] + 16 > w.pos0 + 1) {  // some row does not see every key of the slice
         const int k0 = j0[i] + (lane & 3) * 2;
 #pragma unroll
-        for (int e = 0; e < 4; e++)
-          if (k0 + (e & 1) + (e >> 1) * 8 > w.lim[m]) x[i][e] = -INFINITY;
+        for (int e = 0; e < kV; e++)
+          if (k0 + (e & 1) + ((e >> 1) & 1) * 8 > w.lim[m][e >> 2]) x[i][e] = -INFINITY;
       }
-      t = fmaxf(t, fmaxf(fmaxf(x[i][0], x[i][1]), fmaxf(x[i][2], x[i][3])));
+#pragma unroll
+      for (int h = 0; h < kH; h++)
+        t[h] = fmaxf(t[h], fmaxf(fmaxf(x[i][4 * h], x[i][4 * h + 1]), fmaxf(x[i][4 * h + 2], x[i][4 * h + 3])));
     }
-    t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
-    t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
     // O and the sum follow the maximum only when it grew by more than 2^8
-    const float mx = w.mx[m];
-    const bool grow = mx == -INFINITY ? t > -INFINITY : __fmul_rn(t, sl2) > __fmul_rn(mx, sl2) + 8.f;
-    if (__any_sync(0xffffffffu, grow)) {
-      const float al = grow && mx != -INFINITY ? ex2(__fmul_rn(mx, sl2) - __fmul_rn(t, sl2)) : 1.f;
-      w.mx[m] = grow ? t : mx;
-      w.ls[m] *= al;
+    bool grow[kH], any = false;
 #pragma unroll
-      for (int i = 0; i < 2 * KS; i++)
-#pragma unroll
-        for (int e = 0; e < 4; e++) w.o[m][i][e] *= al;
+    for (int h = 0; h < kH; h++) {
+      t[h] = fmaxf(t[h], __shfl_xor_sync(0xffffffffu, t[h], 1));
+      t[h] = fmaxf(t[h], __shfl_xor_sync(0xffffffffu, t[h], 2));
+      const float mx = w.mx[m][h];
+      grow[h] = mx == -INFINITY ? t[h] > -INFINITY : __fmul_rn(t[h], sl2) > __fmul_rn(mx, sl2) + 8.f;
+      any = any || grow[h];
     }
-    const float mu = w.mx[m] == -INFINITY ? 0.f : __fmul_rn(w.mx[m], sl2);
+    if (__any_sync(0xffffffffu, any)) {
+#pragma unroll
+      for (int h = 0; h < kH; h++) {
+        const float mx = w.mx[m][h];
+        const float al = grow[h] && mx != -INFINITY ? ex2(__fmul_rn(mx, sl2) - __fmul_rn(t[h], sl2)) : 1.f;
+        w.mx[m][h] = grow[h] ? t[h] : mx;
+        w.ls[m][h] *= al;
+#pragma unroll
+        for (int i = 0; i < 2 * KS; i++)
+#pragma unroll
+          for (int e = 0; e < 4; e++)
+            if (W::kTwice || (e >> 1) == h) w.o[m][i][e] *= al;
+      }
+    }
+    float mu[kH];
+#pragma unroll
+    for (int h = 0; h < kH; h++) mu[h] = w.mx[m][h] == -INFINITY ? 0.f : __fmul_rn(w.mx[m][h], sl2);
 #pragma unroll
     for (int i = 0; i < N; i++) {
-      float p[4];
+      float p[kV];
 #pragma unroll
-      for (int e = 0; e < 4; e++) p[e] = ex2(fmaf(x[i][e], sl2, -mu));
-      w.ls[m] += (p[0] + p[1]) + (p[2] + p[3]);
-      uint32_t pa[4];
-      pa[0] = pack_bf16(p[0], p[1]);
-      pa[2] = pack_bf16(p[2], p[3]);
-      pa[1] = pack_bf16(p[0] - bf_lo(pa[0]), p[1] - bf_hi(pa[0]));
-      pa[3] = pack_bf16(p[2] - bf_lo(pa[2]), p[3] - bf_hi(pa[2]));
+      for (int e = 0; e < kV; e++) p[e] = ex2(fmaf(x[i][e], sl2, -mu[e >> 2]));
 #pragma unroll
-      for (int k = 0; k < KS; k++) {
-        mma_b16(w.o[m][2 * k], pa, vf[i][k][0], vf[i][k][1]);
-        mma_b16(w.o[m][2 * k + 1], pa, vf[i][k][2], vf[i][k][3]);
+      for (int h = 0; h < kH; h++) w.ls[m][h] += (p[4 * h] + p[4 * h + 1]) + (p[4 * h + 2] + p[4 * h + 3]);
+      // the weights' bf16 high parts and remainders, by row and eight keys
+      uint32_t hi[2 * kH], lo[2 * kH];
+#pragma unroll
+      for (int e = 0; e < 2 * kH; e++) {
+        hi[e] = pack_bf16(p[2 * e], p[2 * e + 1]);
+        lo[e] = pack_bf16(p[2 * e] - bf_lo(hi[e]), p[2 * e + 1] - bf_hi(hi[e]));
+      }
+      if constexpr (W::kTwice) {
+        const uint32_t pa[4] = {hi[0], lo[0], hi[1], lo[1]};
+#pragma unroll
+        for (int k = 0; k < KS; k++) {
+          mma_b16(w.o[m][2 * k], pa, vf[i][k][0], vf[i][k][1]);
+          mma_b16(w.o[m][2 * k + 1], pa, vf[i][k][2], vf[i][k][3]);
+        }
+      } else {
+        const uint32_t ph[4] = {hi[0], hi[kH], hi[1], hi[kH + 1]}, pl[4] = {lo[0], lo[kH], lo[1], lo[kH + 1]};
+#pragma unroll
+        for (int k = 0; k < KS; k++) {
+          mma_b16(w.o[m][2 * k], ph, vf[i][k][0], vf[i][k][1]);
+          mma_b16(w.o[m][2 * k + 1], ph, vf[i][k][2], vf[i][k][3]);
+        }
+#pragma unroll
+        for (int k = 0; k < KS; k++) {
+          mma_b16(w.o[m][2 * k], pl, vf[i][k][0], vf[i][k][1]);
+          mma_b16(w.o[m][2 * k + 1], pl, vf[i][k][2], vf[i][k][3]);
+        }
       }
     }
   }
 }
 
-template <int D, int MT>
+// A finished row: written out, or (prefix) kept as the sequence's own part for k_prefix_join.
+template <int D, bool PREFIX>
+__device__ __forceinline__ void put_row(const PagedDecodeArgs& a, bool prefix, int b, int g, int r, int q, float4 v,
+                                        float M, float S) {
+  if (PREFIX && prefix) {
+    const size_t row = (size_t)g * a.pre.tiles * kTile + (size_t)b * a.R + r;
+    reinterpret_cast<float4*>(a.pre.o + row * D)[q] = v;
+    if (q == 0) a.pre.ml[row] = make_float2(M, S);
+  } else {
+    write_row<D>(a, b, g, r, q, v, M, S);
+  }
+}
+
+// Joins the consumers' parts of a segment, thread t of n: a whole (sequence, head) is written out, a
+// part of one left in the workspace.
+template <int D, int MT, bool PREFIX>
+__device__ __forceinline__ void join_warps(const PagedDecodeArgs& a, const SegWalk<seg_cost(D)>& sw, const int* len,
+                                           const float* scratch, const float2* ml, int blk, int t, int n) {
+  const int parts = MT < 4 ? kWarps : kWarps / a.MG;  // warps that hold a part of a row
+  const bool whole = sw.n0 == 0 && sw.n1 == sw.nt;
+  const int slot = sw.n0 > 0 ? 0 : 1;  // a block's first segment is the only one that begins inside
+  const bool pre = PREFIX && sweep_base(a, len[sw.b]) > 0;
+  // a thread takes columns 4 q .. and 4 (q + D / 8) .. of a row
+  constexpr int kQ = D / 8;
+  const int items = a.R * kQ;
+  for (int i = t; i < items; i += n) {
+    const int r = i / kQ, q = i % kQ, tile = r >> 3;
+    const int at0 = ((tile / MT) * parts * MT + tile % MT) * 8 + (r & 7);
+    RowSum x, y;
+#pragma unroll
+    for (int k = 0; k < kWarps; k++)
+      if (MT < 4 || k < parts) x.M = fmaxf(x.M, ml[at0 + k * MT * 8].x);
+#pragma unroll 4
+    for (int k = 0; k < parts; k++) {
+      const int from = at0 + k * MT * 8;
+      const float2 z = ml[from];
+      x.add(x.M, z, *reinterpret_cast<const float4*>(scratch + from * D + 4 * q));
+      y.add(x.M, z, *reinterpret_cast<const float4*>(scratch + from * D + 4 * (q + kQ)));
+    }
+    if (whole) {
+      put_row<D, PREFIX>(a, pre, sw.b, sw.g, r, q, x.v, x.M, x.S);
+      put_row<D, PREFIX>(a, pre, sw.b, sw.g, r, q + kQ, y.v, x.M, x.S);
+    } else {
+      const size_t at1 = (size_t)(2 * blk + slot) * a.R + r;
+      float4* to = reinterpret_cast<float4*>(a.part_o + at1 * D) + q;
+      to[0] = x.v;
+      to[kQ] = y.v;
+      if (q == 0) a.part_ml[at1] = make_float2(x.M, x.S);
+    }
+  }
+}
+
+template <int D, int MT, bool PREFIX>
 __device__ bool sweep_consume(const PagedDecodeArgs& a, SegWalk<seg_cost(D)> sw, const int* len, uint8_t* smem, const SweepSmem& L,
-                              const SweepBars& bar, const volatile int* abort, int warp, int lane) {
+                              const SweepBars& bar, const volatile int* abort, int blk, int warp, int lane) {
   using C = Sweep<D>;
   constexpr int KS = D / 16;
   constexpr int kBufs = sweep_bufs(D, MT);
@@ -353,7 +504,6 @@ __device__ bool sweep_consume(const PagedDecodeArgs& a, SegWalk<seg_cost(D)> sw,
   const int mg = warp / KG, kg = warp - mg * KG;
   const uint64_t policy = evict_first();
   const float sl2 = a.scale_log2;
-  const uint32_t lrow = lane & 15, lchk = lane >> 4;
   constexpr int S = kDepth<D, MT>, kN = kSlicesAtOnce<D, MT>;
   constexpr int kCPR = D / 8, kCopies = 16 * kCPR / 32;  // 16-byte chunks of a row; of a slice, per lane
   const int lm = MT < 4 ? 0 : (a.MG == 1 ? 0 : (a.MG == 2 ? 1 : 2));  // log2 of a tile's slices per warp
@@ -441,25 +591,16 @@ __device__ bool sweep_consume(const PagedDecodeArgs& a, SegWalk<seg_cost(D)> sw,
       return false;
     }
     w.qbase = smem_u32(smem + L.q) + (uint32_t)((qs * a.tiles + mg * MT) * 16) * C::kSpan;
-    if (MT <= 2) {
+    if (w.kQRegs) {
 #pragma unroll
-      for (int m = 0; m < w.kQ; m++)
+      for (int m = 0; m < w.MF; m++)
 #pragma unroll
-        for (int k = 0; k < KS; k++)
-          ldsm4(w.q[m][k], w.qbase + m * 16 * C::kSpan + swz(lrow, 2 * k + lchk, C::kSpan));
+        for (int p = 0; p < w.kParts; p++)
+#pragma unroll
+          for (int k = 0; k < KS; k++) ldsm4(w.q[w.kQRegs ? m : 0][p][k], w.q_at(m, p, k, lane));
       warp_arrive(bar.q_empty + qs);
     }
-#pragma unroll
-    for (int m = 0; m < MT; m++) {
-      w.mx[m] = -INFINITY;
-      w.ls[m] = 0.f;
-      const int r = (mg * MT + m) * 8 + (lane >> 2);
-      w.lim[m] = r < a.R ? w.pos0 + (int)fdiv((uint32_t)r, a.div_g) : w.own - 1;
-#pragma unroll
-      for (int i = 0; i < 2 * KS; i++)
-#pragma unroll
-        for (int e = 0; e < 4; e++) w.o[m][i][e] = 0.f;
-    }
+    w.begin(a, mg, lane);
     const int cnt = slices(sw);
     for (int k = 0; k < cnt;) {
       const int j0 = place(sw, k);
@@ -492,8 +633,8 @@ __device__ bool sweep_consume(const PagedDecodeArgs& a, SegWalk<seg_cost(D)> sw,
         k++;
       }
     }
-    if (MT > 2) warp_arrive(bar.q_empty + qs);
-    // the warps' parts go to shared memory, where a finishing warp joins them
+    if (!w.kQRegs) warp_arrive(bar.q_empty + qs);
+    // the warps' parts go to shared memory, where they are joined
     const int buf = seg % kBufs, use = seg / kBufs;
     if (use > 0 && !__all_sync(0xffffffffu, mbar_wait(bar.parts_empty + buf, (use - 1) & 1, abort))) {
       copy_wait<0>();
@@ -501,17 +642,14 @@ __device__ bool sweep_consume(const PagedDecodeArgs& a, SegWalk<seg_cost(D)> sw,
     }
     float* scratch = reinterpret_cast<float*>(smem + L.scratch) + buf * kWarps * MT * 8 * D;
     float2* ml = reinterpret_cast<float2*>(smem + L.ml) + buf * kWarps * MT * 8;
-#pragma unroll
-    for (int m = 0; m < MT; m++) {
-      float l = w.ls[m];
-      l += __shfl_xor_sync(0xffffffffu, l, 1);
-      l += __shfl_xor_sync(0xffffffffu, l, 2);
-      const int row = (warp * MT + m) * 8 + (lane >> 2);
-      if ((lane & 3) == 0) ml[row] = make_float2(w.mx[m] == -INFINITY ? -INFINITY : __fmul_rn(w.mx[m], sl2), l);
-#pragma unroll
-      for (int i = 0; i < 2 * KS; i++)
-        *reinterpret_cast<float2*>(scratch + row * D + i * 8 + (lane & 3) * 2) =
-            make_float2(w.o[m][i][0] + w.o[m][i][2], w.o[m][i][1] + w.o[m][i][3]);
+    w.store(scratch, ml, warp, sl2, lane);
+    if (kBufs == 1) {
+      warp_arrive(bar.stored);
+      if (!__all_sync(0xffffffffu, mbar_wait(bar.stored, seg & 1, abort))) {
+        copy_wait<0>();
+        return false;
+      }
+      join_warps<D, MT, PREFIX>(a, sw, len, scratch, ml, blk, warp * 32 + lane, kWarps * 32);
     }
     warp_arrive(bar.parts_full + buf);
   }
@@ -527,28 +665,15 @@ __device__ __forceinline__ bool count_segment(unsigned* done, unsigned last) {
   return old == last;
 }
 
-// A finished row: written out, or (prefix) kept as the sequence's own part for k_prefix_join.
-template <int D, bool PREFIX>
-__device__ __forceinline__ void put_row(const PagedDecodeArgs& a, bool prefix, int b, int g, int r, int q, float4 v,
-                                        float M, float S) {
-  if (PREFIX && prefix) {
-    const size_t row = (size_t)g * a.pre.tiles * kTile + (size_t)b * a.R + r;
-    reinterpret_cast<float4*>(a.pre.o + row * D)[q] = v;
-    if (q == 0) a.pre.ml[row] = make_float2(M, S);
-  } else {
-    write_row<D>(a, b, g, r, q, v, M, S);
-  }
-}
-
-// Finishing warp f: joins the consumers' parts of every kBufs-th segment.  A whole (sequence,
-// head) is written out; a segment leaves its part in the workspace and is counted, and the block that counts
-// the last one notes it in todo[first or second segment of the block] for its consumers.
+// Finishing warp f: joins the consumers' parts of every kBufs-th segment (with one buffer, more rows,
+// the consumers do that themselves: one warp took 2.6 us for 32 rows).  A part of a (sequence, head) is
+// counted, and the block that counts the last one notes it in todo[first or second cut segment of the
+// block] for its consumers.
 template <int D, int MT, bool PREFIX>
-__device__ bool sweep_finish(const PagedDecodeArgs& a, SegWalk<seg_cost(D)> sw, const Tiles& tl, const SweepPlan& plan, const int* len,
-                             uint8_t* smem, const SweepSmem& L, const SweepBars& bar, volatile int* todo,
+__device__ bool sweep_finish(const PagedDecodeArgs& a, SegWalk<seg_cost(D)> sw, const Tiles& tl, const SweepPlan& plan,
+                             const int* len, uint8_t* smem, const SweepSmem& L, const SweepBars& bar, volatile int* todo,
                              const volatile int* abort, int blk, int f, int lane) {
   constexpr int kBufs = sweep_bufs(D, MT);
-  const int parts = MT < 4 ? kWarps : kWarps / a.MG;  // warps that hold a part of a row
   const float* scratch = reinterpret_cast<const float*>(smem + L.scratch) + f * kWarps * MT * 8 * D;
   const float2* ml = reinterpret_cast<const float2*>(smem + L.ml) + f * kWarps * MT * 8;
   bool waited = false;
@@ -559,44 +684,14 @@ __device__ bool sweep_finish(const PagedDecodeArgs& a, SegWalk<seg_cost(D)> sw, 
       waited = true;
     }
     if (!__all_sync(0xffffffffu, mbar_wait(bar.parts_full + f, (seg / kBufs) & 1, abort))) return false;
-    const bool whole = sw.n0 == 0 && sw.n1 == sw.nt;
-    const int slot = sw.n0 > 0 ? 0 : 1;  // a block's first segment is the only one that begins inside
-    const bool pre = PREFIX && sweep_base(a, len[sw.b]) > 0;
-    // a lane takes columns 4 q .. and 4 (q + D / 8) .. of a row
-    constexpr int kQ = D / 8;
-    const int items = a.R * kQ;
-    for (int i = lane; i < items; i += 32) {
-      const int r = i / kQ, q = i % kQ, tile = r >> 3;
-      const int at0 = ((tile / MT) * parts * MT + tile % MT) * 8 + (r & 7);
-      RowSum x, y;
-#pragma unroll
-      for (int k = 0; k < kWarps; k++)
-        if (MT < 4 || k < parts) x.M = fmaxf(x.M, ml[at0 + k * MT * 8].x);
-#pragma unroll 4
-      for (int k = 0; k < parts; k++) {
-        const int from = at0 + k * MT * 8;
-        const float2 z = ml[from];
-        x.add(x.M, z, *reinterpret_cast<const float4*>(scratch + from * D + 4 * q));
-        y.add(x.M, z, *reinterpret_cast<const float4*>(scratch + from * D + 4 * (q + kQ)));
-      }
-      if (whole) {
-        put_row<D, PREFIX>(a, pre, sw.b, sw.g, r, q, x.v, x.M, x.S);
-        put_row<D, PREFIX>(a, pre, sw.b, sw.g, r, q + kQ, y.v, x.M, x.S);
-      } else {
-        const size_t at1 = (size_t)(2 * blk + slot) * a.R + r;
-        float4* to = reinterpret_cast<float4*>(a.part_o + at1 * D) + q;
-        to[0] = x.v;
-        to[kQ] = y.v;
-        if (q == 0) a.part_ml[at1] = make_float2(x.M, x.S);
-      }
-    }
+    if (kBufs == 2) join_warps<D, MT, PREFIX>(a, sw, len, scratch, ml, blk, lane, 32);
     warp_arrive(bar.parts_empty + f);
-    if (whole) continue;
+    if (sw.n0 == 0 && sw.n1 == sw.nt) continue;
     __syncwarp();  // the other lanes' parts before lane 0's release
     if (lane == 0) {
       const int s0 = tl.cum[sw.b] * tl.Hkv + sw.g * (sw.nt + tl.over);
       const int c0 = tl.first(plan, s0), c1 = tl.last(plan, s0, sw.nt);
-      if (count_segment(a.done + c0, (unsigned)(c1 - c0))) todo[slot] = sw.b * tl.Hkv + sw.g;
+      if (count_segment(a.done + c0, (unsigned)(c1 - c0))) todo[sw.n0 > 0 ? 0 : 1] = sw.b * tl.Hkv + sw.g;
     }
     __syncwarp();
   }
@@ -604,13 +699,13 @@ __device__ bool sweep_finish(const PagedDecodeArgs& a, SegWalk<seg_cost(D)> sw, 
   return true;
 }
 
-// The (sequence, head)s whose last segment this block counted: their segments in order, kSplit
-// neighbouring lanes to four columns of a row (each its own share, then lane by lane: the same
-// sum whichever block does it).
+// The (sequence, head)s whose last segment this block counted: their segments in order, up to four
+// neighbouring lanes to four columns of a row, as the threads suffice for all rows at once (each its
+// own share, then lane by lane: the same sum whichever block does it).
 template <int D, int MT, bool PREFIX>
 __device__ bool sweep_join(const PagedDecodeArgs& a, const Tiles& tl, const SweepPlan& plan, const int* len,
                            const SweepBars& bar, const volatile int* todo, const volatile int* abort, int tid) {
-  constexpr int kThreads = kWarps * 32, kSplit = 4, kAhead = 4;
+  constexpr int kThreads = kWarps * 32, kAhead = 4;
   if (!__all_sync(0xffffffffu, mbar_wait(bar.fin, 0, abort))) return false;
   for (int k = 0; k < 2; k++) {
     const int sh = todo[k];
@@ -619,22 +714,23 @@ __device__ bool sweep_join(const PagedDecodeArgs& a, const Tiles& tl, const Swee
     const int b = sh / tl.Hkv, g = sh - b * tl.Hkv, nt = tl.nt(b);
     const int s0 = tl.cum[b] * tl.Hkv + g * (nt + tl.over);
     const int c0 = tl.first(plan, s0), c1 = tl.last(plan, s0, nt);
-    const int sub = tid % kSplit, items = a.R * (D / 4);
-    for (int i0 = 0; i0 < items; i0 += kThreads / kSplit) {
-      const int i = min(i0 + tid / kSplit, items - 1);
+    const int items = a.R * (D / 4), lg = items <= kThreads / 4 ? 2 : (items <= kThreads / 2 ? 1 : 0);
+    const int split = 1 << lg, sub = tid & (split - 1);
+    for (int i0 = 0; i0 < items; i0 += kThreads >> lg) {
+      const int i = min(i0 + (tid >> lg), items - 1);
       const int r = i / (D / 4), q = i % (D / 4);
       const auto at = [&](int c) { return (size_t)(2 * c + (c == c0 ? 1 : 0)) * a.R + r; };
       RowSum x;
-      for (int c = c0 + sub; c <= c1; c += kSplit * kAhead) {
+      for (int c = c0 + sub; c <= c1; c += kAhead << lg) {
         float2 z[kAhead];
         float4 u[kAhead];
 #pragma unroll
         for (int e = 0; e < kAhead; e++) {
           z[e] = make_float2(-INFINITY, 0.f);
           u[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (c + e * kSplit <= c1) {
-            z[e] = __ldcg(a.part_ml + at(c + e * kSplit));
-            u[e] = __ldcg(reinterpret_cast<const float4*>(a.part_o + at(c + e * kSplit) * D) + q);
+          if (c + (e << lg) <= c1) {
+            z[e] = __ldcg(a.part_ml + at(c + (e << lg)));
+            u[e] = __ldcg(reinterpret_cast<const float4*>(a.part_o + at(c + (e << lg)) * D) + q);
           }
         }
         float top = x.M;
@@ -645,18 +741,16 @@ __device__ bool sweep_join(const PagedDecodeArgs& a, const Tiles& tl, const Swee
         for (int e = 0; e < kAhead; e++) x.add(top, z[e], u[e]);
       }
       float top = x.M;
-#pragma unroll
-      for (int m = 1; m < kSplit; m <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
+      for (int m = 1; m < split; m <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
       x.raise(top);
-#pragma unroll
-      for (int m = 1; m < kSplit; m <<= 1) {
+      for (int m = 1; m < split; m <<= 1) {
         x.S += __shfl_xor_sync(0xffffffffu, x.S, m);
         x.v.x += __shfl_xor_sync(0xffffffffu, x.v.x, m);
         x.v.y += __shfl_xor_sync(0xffffffffu, x.v.y, m);
         x.v.z += __shfl_xor_sync(0xffffffffu, x.v.z, m);
         x.v.w += __shfl_xor_sync(0xffffffffu, x.v.w, m);
       }
-      if (sub == 0 && i0 + tid / kSplit < items) put_row<D, PREFIX>(a, PREFIX && sweep_base(a, len[b]) > 0, b, g, r, q, x.v, top, x.S);
+      if (sub == 0 && i0 + (tid >> lg) < items) put_row<D, PREFIX>(a, PREFIX && sweep_base(a, len[b]) > 0, b, g, r, q, x.v, top, x.S);
     }
   }
   return true;
@@ -677,6 +771,7 @@ __global__ void __launch_bounds__(kSweepThreads, 1) k_paged_sweep(const __grid_c
   bar.parts_full = bar.q_empty + 2;         // [2] a segment's parts are in shared memory
   bar.parts_empty = bar.parts_full + 2;     // [2] and have been read
   bar.fin = bar.parts_empty + 2;            // the finishing warps are done
+  bar.stored = bar.fin + 1;                 // one buffer: all consumers' parts are in it
   volatile int* abort = reinterpret_cast<volatile int*>(smem + kOffVars);
   volatile int* todo = abort + 1;                              // [2]
   volatile SweepPlan* splan = reinterpret_cast<volatile SweepPlan*>(const_cast<int*>(abort) + 3);
@@ -739,12 +834,13 @@ __global__ void __launch_bounds__(kSweepThreads, 1) k_paged_sweep(const __grid_c
     *abort = 0;
     todo[0] = todo[1] = -1;
     for (int i = 0; i < 2; i++) {
-      mbar_init(bar.q_full + i, 1);
+      mbar_init(bar.q_full + i, query_warps(D, MT));
       mbar_init(bar.q_empty + i, kWarps);
       mbar_init(bar.parts_full + i, kWarps);
       mbar_init(bar.parts_empty + i, 1);
     }
     mbar_init(bar.fin, kBufs);
+    mbar_init(bar.stored, kWarps);
     fence_mbar_init();
   }
   Tiles tl;
@@ -793,7 +889,7 @@ __global__ void __launch_bounds__(kSweepThreads, 1) k_paged_sweep(const __grid_c
   // registers: 384 x 168 at launch; 256 x 216 for the consumers, 128 x 72 for the others
   if (warp < kWarps) {
     regs_inc<216>();
-    bool ok = sweep_consume<D, MT>(a, sw, len, smem, L, bar, abort, warp, lane);
+    bool ok = sweep_consume<D, MT, PREFIX>(a, sw, len, smem, L, bar, abort, blk, warp, lane);
     if (ok) {
       SweepPlan p;
       p.W = splan->W;
@@ -810,7 +906,8 @@ __global__ void __launch_bounds__(kSweepThreads, 1) k_paged_sweep(const __grid_c
   }
   regs_dec<72>();
   bool ok = true;
-  if (warp == kWarps) {
+  const int qw = warp == kWarps ? 0 : warp - kWarps - kBufs;
+  if (warp == kWarps || (qw > 0 && qw < query_warps(D, MT))) {
     // ------------------------------------------------------------ queries, two passes of rows at a time
     constexpr int kCPR = D / 8, kRows = 32 / kCPR;
     const int c = lane % kCPR;
@@ -825,7 +922,7 @@ __global__ void __launch_bounds__(kSweepThreads, 1) k_paged_sweep(const __grid_c
       if (!ok) break;
       const int pos0 = len[sw.b] - a.Tq;
       uint8_t* q = smem + L.q + qs * a.tiles * 16 * kSpan;
-      for (int r0 = 0; r0 < a.tiles * 8; r0 += 2 * kRows) {
+      for (int r0 = qw * 2 * kRows; r0 < a.tiles * 8; r0 += query_warps(D, MT) * 2 * kRows) {
         const int r = r0 + lane / kCPR, r2 = r + kRows;
         const QueryChunk x = query_load<D>(a, sw.b, sw.g, r, c, pos0), y = query_load<D>(a, sw.b, sw.g, r2, c, pos0);
         uint4 hi, lo;
