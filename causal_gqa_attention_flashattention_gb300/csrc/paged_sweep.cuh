@@ -22,27 +22,29 @@ namespace {
 // its unnormalised O, running maximum and sum; the block that finishes a (sequence,
 // head) last adds the segments in order: the result does not depend on which one.
 //
-// Rows: the R = Tq * G queries of a key/value head (row t * G + g).  A matrix tile of
-// 16 rows holds 8 of them twice: rows 0-7 the high fp16 part of the rotated query,
+// Rows: the R = Tq * G queries of a key/value head (row t * G + g).  With at most 8 a
+// matrix tile of 16 rows holds them twice: rows 0-7 the high fp16 part of the rotated query,
 // rows 8-15 its remainder, so that one m16n8k16 product gives both parts of a score
-// in one thread; the same goes for the weights' two bf16 parts in P V.  With at most
-// 8 rows (one token of most models) that precision is free: the tile has 16 rows
-// anyway.  mma.sync and not tcgen05: with so few rows the sweep is bound by the bytes
+// in one thread; the same goes for the weights' two bf16 parts in P V.  That
+// precision is free: the tile has 16 rows anyway.  With more rows the parts are two products of
+// a tile of 16 rows each.  mma.sync and not tcgen05: with so few rows the sweep is bound by the bytes
 // of the cache, and a warp that owns its 16 keys end to end (copies, scores, weights,
 // P V in registers) needs no hand-off between warps per tile.  It works two tiles off in
 // 0.7 us, HBM delivers them in 1.4 us (7.1 TB/s over a long context); the contiguous cache's
 // tcgen05 sweep takes 0.9 us for one.  16 contexts around 8192 positions (127 MB) 28.0 us,
-// one of 131001 29.3 us; a short context 7.3 us, the chain of lengths, table, page and join.
+// one of 131001 29.0 us; a short context 7.2 us, the chain of lengths, table, page and join.  The
+// 16 contexts with 16 rows take 30.5 us, with 32 (bound by the products) 45.9, with 64 81.
 template <int D>
 struct Sweep {
   static constexpr uint32_t kSpan = D * 2;
   static constexpr int kSlot = 2 * 16 * (int)kSpan;  // 16 keys and their values
 };
 constexpr int kTK = 128;  // positions of a tile: a slice of 16 for each consumer warp
-// Slices that a consumer warp has room for.
+// Slices that a consumer warp has room for (more than 16 rows are bound by the products: 32 rows of
+// 64 columns 45.9 us with two, 47.4 with three; of 32 columns 34.9 with four, 34.3 with six).
 template <int D, int MT>
-constexpr int kDepth = D == 64 ? (MT < 4 ? 4 : 3) : (MT < 4 ? 8 : 6);
-// Eight consumer warps, then a warpgroup of the queries, two finishing warps and an idle one.
+constexpr int kDepth = D == 64 ? (MT < 4 ? 4 : 2) : (MT < 4 ? 8 : 6);
+// Eight consumer warps, then a warpgroup for the queries and the finished segments.
 // (Sixteen consumers in two groups on alternate tiles measured slower: a short context 8.4 us
 // against 7.4, 16 contexts around 8192 positions 31.9 against 31.4.)
 constexpr int kWarps = 8;
@@ -229,8 +231,8 @@ struct SweepBars {
 // What a consumer warp holds of a segment: its rows' queries (in registers for at most 16 rows, else
 // read from shared memory as they are used), O, running maximum and sum.  Up to 8 rows they are
 // twice in one matrix tile, high and low parts; with more a tile has 16 rows, and the parts are
-// two products into the same sums, which halves O's registers (28 rows 67 us with pairs of
-// 8, NN in this form).
+// two products into the same sums, which halves O's registers (16 contexts around 8192, 32 rows: 56 us
+// for 69).
 template <int D, int MT>
 struct SweepState {
   static constexpr int KS = D / 16;
@@ -289,10 +291,7 @@ struct SweepState {
 // Slices of 16 keys that a warp takes together: two where the registers allow it, which gives
 // its chain of dependent steps (scores, maximum, weights, P V) something to overlap with.
 template <int D, int MT>
-#ifndef NSL
-#define NSL (MT * D <= 128 ? 2 : 1)
-#endif
-constexpr int kSlicesAtOnce = NSL;
+constexpr int kSlicesAtOnce = MT * D <= 128 ? 2 : 1;
 
 // N slices (keys at kb, values at vb, first position j0) into the state.
 template <int D, int MT, int N>
