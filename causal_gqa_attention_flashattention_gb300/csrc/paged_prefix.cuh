@@ -54,9 +54,12 @@ inline int prefix_smem(int D, int B) {
 
 // The blocks that take the prefix, of all: their share of the work, a tile of a pair of row tiles
 // counted as 2 of the sweep's (measured: 128 sequences on 16384 positions 35.1, 37.9, 37.2 us at 2, 1.75,
-// 2.25; 60 on 8192 with D = 32 18.6, 18.3, 18.5).
+// 2.25; 60 on 8192 with D = 32 18.6, 18.3, 18.5).  Above 16 rows the sweep is bound by its products, for
+// every 32 rows a tile counts three times (20 sequences of 32 rows on 4096 positions 20.9 us, with 2
+// 22.9, 4 21.9, 1 26.1; of 64 rows 28.4, 32.2, 33.2, 47.1).
 __device__ __forceinline__ int prefix_blocks(const PagedDecodeArgs& a, int sweep_tiles, int blocks) {
-  const float mine = 2.f * (float)a.pre.W, theirs = (float)sweep_tiles * (a.D == 64 ? 1.f : 0.5f);
+  const float mine = 2.f * (float)a.pre.W;
+  const float theirs = (float)sweep_tiles * (a.D == 64 ? 1.f : 0.5f) * (a.R > 16 ? 3.f * (float)a.MG : 1.f);
   const int P = max(1, min(min(__float2int_rn((float)blocks * __fdiv_rn(mine, mine + theirs)), blocks - 1), a.pre.W));
   // the same number for every (head, pair), so that no block has parts of two (which costs it
   // a second packing and a second epilogue, about 4 us)
