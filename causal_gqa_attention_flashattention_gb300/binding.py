@@ -393,13 +393,18 @@ def _on(stream, call, *args, **kw):
         return call(*args, **kw)
 
 
-def _run(name, device, *args):
-    """Calls library function `name` with `device`'s current stream as its last argument."""
-    if device.index != torch.cuda.current_device():
+def _call(name, device, args):
+    """Status of library function `name` with `device`'s current stream as its last argument."""
+    index = device.index
+    # no Python around the device and the stream: a call right after a launch finds the caches cold
+    if index != torch._C._cuda_getDevice():
         with torch.cuda.device(device):
-            return _run(name, device, *args)
-    # the current stream's handle without a Stream object around it (2.9 us a call)
-    st = getattr(_lib or lib(), name)(*args, torch._C._cuda_getCurrentRawStream(device.index))
+            return _call(name, device, args)
+    return getattr(_lib or lib(), name)(*args, torch._C._cuda_getCurrentRawStream(index))
+
+
+def _run(name, device, *args):
+    st = _call(name, device, args)
     if st != NE_OK:
         raise NeAttnError(name, st)
 
@@ -440,11 +445,11 @@ def _run_ws(name, device, args, workspace, size):
     """_run with the workspace as the last arguments: the caller's; without one NULL (the
     library's own for the stream) or, where a capture needs one, a tensor of the capture's own."""
     if workspace is None:
-        try:
-            return _run(name, device, *args, None, 0)
-        except NeAttnError as e:
-            if e.status != ERR_WORKSPACE:
-                raise
+        st = _call(name, device, args + (None, 0))
+        if st == NE_OK:
+            return
+        if st != ERR_WORKSPACE:
+            raise NeAttnError(name, st)
         workspace = torch.empty(size(), dtype=torch.uint8, device=device)
     elif workspace.dtype != torch.uint8 or workspace.device != device:
         raise ValueError("workspace must be uint8 on the call's device")
@@ -469,13 +474,14 @@ def qk_norm(q, k, q_weight, k_weight, eps=1e-6, rope_base=10000.0, rope_half=Fal
     _vector(q_weight, D, "q_weight", dev)
     _vector(k_weight, D, "k_weight", dev)
     if workspace is None:
-        n = fwd_workspace_size(B, T, Hq, Hkv, D)
-        _need(n > 0, "unsupported shape")
+        n = (B * T * Hq * D + 127) // 128 * 256 + (B * T * Hkv * D + 127) // 128 * 256  # as rotated_qk
         workspace = torch.empty(n, dtype=torch.uint8, device=dev)
-    _need(workspace.dtype == torch.uint8 and workspace.device == dev, "workspace must be uint8 on the call's device")
+    elif workspace.dtype != torch.uint8 or workspace.device != dev:
+        raise ValueError("workspace must be uint8 on the call's device")
+    else:
+        n = workspace.numel()
     _run("ne_attn_qk_norm", dev, q.data_ptr(), k.data_ptr(), q_weight.data_ptr(), k_weight.data_ptr(),
-         B, T, Hq, Hkv, D, qs, ks, eps, rope_base, ROPE_HALF if rope_half else 0, workspace.data_ptr(),
-         workspace.numel())
+         B, T, Hq, Hkv, D, qs, ks, eps, rope_base, ROPE_HALF if rope_half else 0, workspace.data_ptr(), n)
     return workspace
 
 
@@ -497,11 +503,15 @@ def qk_norm_bwd(q, k, q_weight, k_weight, dqn, dkn, eps=1e-6, dq=None, dk=None, 
         _need(t.dtype == dt and t.device == dev and t.shape == like.shape and t.is_contiguous(),
               "%s must be contiguous, of the shape of its input and of one type with the other" % name)
     if dq is None:
-        dq = torch.empty(q.shape, dtype=dt, device=dev)
+        dq, dqs = torch.empty(q.shape, dtype=dt, device=dev), Hq * D
+    else:
+        _need(dq.shape == q.shape, "dq must have the shape of q")
+        dqs = _head_rows(dq, "dq", dt, dev)
     if dk is None:
-        dk = torch.empty(k.shape, dtype=dt, device=dev)
-    _need(dq.shape == q.shape and dk.shape == k.shape, "dq and dk must have the shapes of q and k")
-    dqs, dks = _head_rows(dq, "dq", dt, dev), _head_rows(dk, "dk", dt, dev)
+        dk, dks = torch.empty(k.shape, dtype=dt, device=dev), Hkv * D
+    else:
+        _need(dk.shape == k.shape, "dk must have the shape of k")
+        dks = _head_rows(dk, "dk", dt, dev)
     dqw = torch.empty(D, dtype=torch.float32, device=dev)
     dkw = torch.empty(D, dtype=torch.float32, device=dev)
     args = (q.data_ptr(), k.data_ptr(), q_weight.data_ptr(), k_weight.data_ptr(), dqn.data_ptr(), dkn.data_ptr(),
@@ -603,12 +613,14 @@ def attn_decode_paged(q, k_pages, v_pages, page_table, kv_len, q_weight=None, ep
         o = torch.empty((B, Tq, Hq, D), dtype=o_dtype, device=dev)
     elif o.device != dev or not o.is_contiguous() or o.shape != (B, Tq, Hq, D):
         raise ValueError("o must be a contiguous [B, Tq, Hq, D] on the call's device")
+    else:
+        o_dtype = o.dtype
     if lse is None:
         lse = torch.empty((B, Hq, Tq), dtype=torch.float32, device=dev)
     elif lse.dtype != torch.float32 or lse.device != dev or not lse.is_contiguous() or lse.shape != (B, Hq, Tq):
         raise ValueError("lse must be a contiguous float32 [B, Hq, Tq] on the call's device")
-    fp32 = o.dtype == torch.float32
-    if not fp32 and o.dtype != torch.bfloat16:
+    fp32 = o_dtype == torch.float32
+    if not fp32 and o_dtype != torch.bfloat16:
         raise ValueError("o must be bfloat16 or float32")
     args = (q.data_ptr(), None if q_weight is None else q_weight.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
             page_table.data_ptr(), kv_len.data_ptr(), prefix_table.data_ptr() if prefix_len else None, o.data_ptr(),
