@@ -14,8 +14,13 @@
 // A sequence takes part if its first query sees the whole prefix, so no score is
 // masked here but for the columns behind the prefix in its last tile; the sweep
 // reads the prefix pages itself for one that does not.
-// Precision: q as two fp16 parts (two products; with one the LSE is off by 1e-5), the
-// weights as one bf16, as the forward (2^-8 at most, at random over the keys).
+// Precision: as the sweep's, so that a call gives the same o with and without a shared prefix: q as
+// two fp16 parts (two products; with one the LSE is off by 1e-5), the weights as two bf16
+// parts (2^-17; one part is 2^-9 off, and the call with a prefix then differs from the one without by
+// more than a bf16 o's rounding). Both parts of all 128 keys would not fit the tensor memory, so P
+// goes out in quarters of 32 keys through two buffers. 128 sequences on 16384 positions 40.4 us, with
+// one part in halves 34.8: a third each for the second part's arithmetic, its products and the
+// hand-offs (halves through one buffer 46.5 where quarters take 45.6).
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -38,7 +43,8 @@ struct PreCfg {
   static constexpr uint32_t kSBO = 8 * kSpan;
   static constexpr int kQSlots = 4;  // high and low part of each unit's row tile
   static constexpr int kStages = 4;
-  static constexpr uint32_t kColO = 0, kColS = 128, kColP = 384;  // unit u: O at 64u, S at 128 + 128u, P at 384 + 64u
+  static constexpr uint32_t kColO = 0, kColS = 128, kColP = 384;  // unit u: O at 64u, S at 128 + 128u, P at 384 + 64u:
+  // two buffers of 32 columns, a quarter's high parts and then its low parts in each
   static constexpr uint32_t kTmemCols = 512;
   static constexpr int kThreads = 384;
   static constexpr int kOffK = kQSlots * kTileBytes;  // Q first: unit u at 2 u and 2 u + 1
@@ -53,12 +59,12 @@ inline int prefix_smem(int D, int B) {
 }
 
 // The blocks that take the prefix, of all: their share of the work, a tile of a pair of row tiles
-// counted as 2 of the sweep's (measured: 128 sequences on 16384 positions 35.1, 37.9, 37.2 us at 2, 1.75,
-// 2.25; 60 on 8192 with D = 32 18.6, 18.3, 18.5).  Above 16 rows the sweep is bound by its products, for
-// every 32 rows a tile counts three times (20 sequences of 32 rows on 4096 positions 20.9 us, with 2
-// 22.9, 4 21.9, 1 26.1; of 64 rows 28.4, 32.2, 33.2, 47.1).
+// counted as 2.75 of the sweep's (measured: 128 sequences on 16384 positions 40.8 us, 45.5, 43.1, 40.9, 41.3
+// at 2, 2.5, 3, 3.5; 100 on 2048 21.3, 24.9, 21.3, 21.3, 21.3). Above 16 rows the sweep is bound by its
+// products, for every 32 rows a tile counts three times (40 sequences of 20 rows on 8192 positions 34.4 us,
+// with 1 52.9, 2 36.1, 4 37.7, 5 37.7; 20 of 64 rows on 4096 21.7, 22.0, 22.2, 21.6, 23.3).
 __device__ __forceinline__ int prefix_blocks(const PagedDecodeArgs& a, int sweep_tiles, int blocks) {
-  const float mine = 2.f * (float)a.pre.W;
+  const float mine = 2.75f * (float)a.pre.W;
   const float theirs = (float)sweep_tiles * (a.D == 64 ? 1.f : 0.5f) * (a.R > 16 ? 3.f * (float)a.MG : 1.f);
   const int P = max(1, min(min(__float2int_rn((float)blocks * __fdiv_rn(mine, mine + theirs)), blocks - 1), a.pre.W));
   // the same number for every (head, pair), so that no block has parts of two (which costs it
@@ -131,8 +137,8 @@ __device__ void prefix_role(const PagedDecodeArgs& a, const int* len, uint8_t* s
   uint64_t* kv_empty = kv_full + S;         // [S] both O += P V issuers are done with the stage
   uint64_t* s_full = kv_empty + S;          // [2] per unit
   uint64_t* s_read = s_full + 2;            // [2] the unit's warpgroup holds its scores in registers
-  uint64_t* p_ready = s_read + 2;           // [2][2] per unit and key half
-  uint64_t* pv_done = p_ready + 4;          // [2][2] per unit and key half
+  uint64_t* p_ready = s_read + 2;           // [2][2] per unit and P buffer: twice a tile
+  uint64_t* pv_done = p_ready + 4;          // [2][2] per unit and P buffer
   uint64_t* o_free = pv_done + 4;           // [2] the unit's O has been read out
   uint64_t* drain = o_free + 2;             // [3] one per issuing thread
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::kNumBars);
@@ -266,27 +272,27 @@ __device__ void prefix_role(const PagedDecodeArgs& a, const int* len, uint8_t* s
       constexpr uint32_t tstep = (uint32_t)TB >> 4;
       const uint64_t dV0 = smem_desc(smem_u32(smem + C::kOffV), 16, C::kSBO, C::kSwz);
       bool ok = true;
-      int g = 0, m = 0, e = 0;  // K/V stages, this unit's steps, this unit's segments
+      int g = 0, e = 0;  // K/V stages, this unit's segments
       while (ok && sg.next(p)) {
         const bool act = u < sg.units(p);
         for (int n = sg.n0; ok && n < sg.n1; n++, g++) {
           const int st = g % S;
           if (act) {
-            // keys 0..63 of P go out while the warpgroup still computes keys 64..127
-            if (!(ok = mbar_wait(p_ready + 2 * u, m & 1, abort))) break;
-            if (n == sg.n0 && e > 0 && !(ok = mbar_wait(o_free + u, (e - 1) & 1, abort))) break;
-            tc_fence_after();
+            // the first quarters of P go out while the warpgroup still computes the others: quarter j in
+            // buffer j & 1, the buffer's use 2 m + (j >> 1)
             const uint64_t dv = dV0 + (uint64_t)(st * tstep);
-            mma_ts_chain<4, false>(tmem + C::kColO + 64u * u, tmem + C::kColP + 64u * u, dv, kStepMN, idPV,
-                                   n > sg.n0 ? 1u : 0u);
-            mma_commit(pv_done + 2 * u);
-            if (!(ok = mbar_wait(p_ready + 2 * u + 1, m & 1, abort))) break;
-            tc_fence_after();
-            mma_ts_chain<4, false>(tmem + C::kColO + 64u * u, tmem + C::kColP + 64u * u + 32u,
-                                   dv + (uint64_t)(4 * kStepMN), kStepMN, idPV, 1u);
-            mma_commit(pv_done + 2 * u + 1);
+            for (int j = 0; ok && j < 4; j++) {
+              if (!(ok = mbar_wait(p_ready + 2 * u + (j & 1), j >> 1, abort))) break;
+              if (j == 0 && n == sg.n0 && e > 0 && !(ok = mbar_wait(o_free + u, (e - 1) & 1, abort))) break;
+              tc_fence_after();
+              const uint32_t pb = tmem + C::kColP + 64u * u + 32u * (j & 1);
+              const uint64_t dvj = dv + (uint64_t)(2 * j * kStepMN);
+              mma_ts_chain<2, false>(tmem + C::kColO + 64u * u, pb, dvj, kStepMN, idPV, n > sg.n0 || j > 0 ? 1u : 0u);
+              mma_ts_chain<2, false>(tmem + C::kColO + 64u * u, pb + 16u, dvj, kStepMN, idPV, 1u);
+              mma_commit(pv_done + 2 * u + (j & 1));
+            }
+            if (!ok) break;
             mma_commit(kv_empty + st);  // V by this PV; K by this unit's S, complete before its P existed
-            m++;
           } else {
             // the segment has one unit: once for each use of the stage, so not before the stage is full
             if (!(ok = mbar_wait(kv_full + st, (g / S) & 1, abort))) break;
@@ -359,7 +365,8 @@ __device__ void prefix_role(const PagedDecodeArgs& a, const int* len, uint8_t* s
           const float m_new = __fmul_rn(r_new, sl2);
           // lazy rescale: only when some row's maximum grew by more than 2^8
           if (__any_sync(0xffffffffu, m_new > m_old + 8.0f)) {
-            ok = __all_sync(0xffffffffu, mbar_wait(pv_done + 2 * u + 1, (m - 1) & 1, abort));
+            // the last quarter of the step before: use 2 m - 1 of the second buffer
+            ok = __all_sync(0xffffffffu, mbar_wait(pv_done + 2 * u + 1, 1, abort));
             if (!ok) break;
             tc_fence_after();
             r_use = r_new;
@@ -379,36 +386,40 @@ __device__ void prefix_role(const PagedDecodeArgs& a, const int* len, uint8_t* s
         }
         r_run = r_use;
         m_use = __fmul_rn(r_use, sl2);
-        if (m > 0) {  // keys 0..63 of the P buffer: read by the first half of the previous step's P V
-          ok = __all_sync(0xffffffffu, mbar_wait(pv_done + 2 * u, (m - 1) & 1, abort));
-          if (!ok) break;
-        }
-        tc_fence_after();
         uint64_t sum4[4] = {0ull, 0ull, 0ull, 0ull};
         const uint64_t sl2x2 = f2(sl2, sl2), negm = f2(-m_use, -m_use);
+        const uint64_t minus = f2(-1.f, -1.f);
 #pragma unroll
         for (int c = 0; c < 8; c++) {
-          if (c == 4) {
-            tmem_wait_st();
-            tc_fence_before();
-            warp_arrive(p_ready + 2 * u);
-            if (m > 0 && !__all_sync(0xffffffffu, mbar_wait(pv_done + 2 * u + 1, (m - 1) & 1, abort))) {
+          const int j = c >> 1, h = j & 1;  // quarter and its buffer
+          uint32_t ph[8], pl[8];
+#pragma unroll
+          for (int e = 0; e < 8; e++) {
+            const int k = 16 * c + 2 * e;
+            float x0, x1, l0, l1;
+            f2_split(f2_fma(f2(__uint_as_float(sc[k]), __uint_as_float(sc[k + 1])), sl2x2, negm), x0, x1);
+            const uint64_t pp = f2(ex2(x0), ex2(x1));
+            f2_split(pp, x0, x1);
+            ph[e] = pack_bf16(x0, x1);
+            f2_split(f2_fma(f2(bf_lo(ph[e]), bf_hi(ph[e])), minus, pp), l0, l1);
+            pl[e] = pack_bf16(l0, l1);
+            sum4[e & 3] = f2_add(sum4[e & 3], pp);
+          }
+          if ((c & 1) == 0) {
+            if (c > 0) {  // the quarter before: its stores have had 16 keys' time
+              tmem_wait_st();
+              tc_fence_before();
+              warp_arrive(p_ready + 2 * u + (h ^ 1));
+            }
+            // the buffer's use before, 2 m + (j >> 1) - 1, has been read
+            if ((j > 1 || m > 0) && !__all_sync(0xffffffffu, mbar_wait(pv_done + 2 * u + h, j > 1 ? 0 : 1, abort))) {
               ok = false;
               break;
             }
             tc_fence_after();
           }
-          uint32_t pk[8];
-#pragma unroll
-          for (int e = 0; e < 8; e++) {
-            const int k = 16 * c + 2 * e;
-            float x0, x1;
-            f2_split(f2_fma(f2(__uint_as_float(sc[k]), __uint_as_float(sc[k + 1])), sl2x2, negm), x0, x1);
-            const float p0 = ex2(x0), p1 = ex2(x1);
-            pk[e] = pack_bf16(p0, p1);
-            sum4[e & 3] = f2_add(sum4[e & 3], f2(p0, p1));
-          }
-          tmem_st8(pbuf + c * 8, pk);
+          tmem_st8(pbuf + 32 * h + 8 * (c & 1), ph);
+          tmem_st8(pbuf + 32 * h + 16 + 8 * (c & 1), pl);
         }
         if (!ok) break;
         tmem_wait_st();
@@ -424,7 +435,7 @@ __device__ void prefix_role(const PagedDecodeArgs& a, const int* len, uint8_t* s
       }
       if (!ok) break;
       // the segment's unnormalised O, maximum (log2 units) and sum
-      ok = __all_sync(0xffffffffu, mbar_wait(pv_done + 2 * u + 1, (m - 1) & 1, abort));
+      ok = __all_sync(0xffffffffu, mbar_wait(pv_done + 2 * u + 1, 1, abort));
       if (!ok) break;
       tc_fence_after();
       if (!waited) {
