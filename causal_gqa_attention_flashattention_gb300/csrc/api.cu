@@ -62,7 +62,7 @@ __global__ void k_timeout_probe(int* status, long long limit_ns) {
   __syncthreads();
   if (threadIdx.x == 0) {
     // Nothing arrives on `bar`: the wait must give up after limit_ns.
-    if (!mbar_wait(&bar, 0, &abort_flag, (unsigned long long)limit_ns)) atomicCAS(status, 0, kStatusTimeout);
+    if (!mbar_wait(&bar, 0, &abort_flag, (unsigned long long)limit_ns)) atomicExch(status, kStatusTimeout);
   }
 }
 
@@ -1097,15 +1097,20 @@ int ne_attn_check_status(void* stream) {
   }
   int word = 0, zero = 0;
   if (cudaMemcpyFromSymbol(&word, g_status_word, sizeof(int)) != cudaSuccess) return NE_ERR_CUDA;
-  if (word != 0 && cudaMemcpyToSymbol(g_status_word, &zero, sizeof(int)) != cudaSuccess) return NE_ERR_CUDA;
-  if (word == kStatusTimeout) {
-    // a kernel that gave up may have left its stream's counters half way
-    std::lock_guard<std::mutex> lock(g_mu);
-    if (!d->join_scratch.empty() && cudaDeviceSynchronize() != cudaSuccess) return NE_ERR_CUDA;
+  if (word == 0) return NE_OK;
+  // no other stream's kernel may record between the reading and the clearing, or start on counters
+  // that are being cleared
+  std::lock_guard<std::mutex> lock(g_mu);
+  if (cudaDeviceSynchronize() != cudaSuccess ||
+      cudaMemcpyFromSymbol(&word, g_status_word, sizeof(int)) != cudaSuccess ||
+      cudaMemcpyToSymbol(g_status_word, &zero, sizeof(int)) != cudaSuccess)
+    return NE_ERR_CUDA;
+  if (word == kStatusTimeout)  // a kernel that gave up may have left its stream's counters half way
     for (auto& x : d->join_scratch)
       if (cudaMemset(x.counters, 0, kCounterBytes) != cudaSuccess) return NE_ERR_CUDA;
-  }
-  return word == 0 ? NE_OK : word;
+  // the clears are on the legacy stream, which streams made not to block do not wait for
+  if (cudaDeviceSynchronize() != cudaSuccess) return NE_ERR_CUDA;
+  return word;
 }
 
 const char* ne_attn_status_string(int status) {

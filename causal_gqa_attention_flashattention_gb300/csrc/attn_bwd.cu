@@ -37,7 +37,7 @@ namespace {
 
 __device__ __forceinline__ void record_timeout(int* status, volatile int* abort) {
   *abort = 1;
-  atomicCAS(status, 0, kStatusTimeout);
+  atomicExch(status, kStatusTimeout);
 }
 
 // ====================================================================== pre-pass

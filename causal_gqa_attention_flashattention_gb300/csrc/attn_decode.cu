@@ -40,7 +40,7 @@ constexpr float kLn2 = 0.69314718055994531f;
 
 __device__ __forceinline__ void record_timeout(int* status, volatile int* abort) {
   *abort = 1;
-  atomicCAS(status, 0, kStatusTimeout);
+  atomicExch(status, kStatusTimeout);
 }
 
 // ====================================================================== cache append

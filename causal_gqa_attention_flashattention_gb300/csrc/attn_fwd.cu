@@ -60,7 +60,7 @@ struct FwdCfg {
 
 __device__ __forceinline__ void record_timeout(int* status, volatile int* abort) {
   *abort = 1;
-  atomicCAS(status, 0, kStatusTimeout);
+  atomicExch(status, kStatusTimeout);
 }
 
 // Rotates `ntiles` consecutive 128-row tiles in place (positions pos0 + row),
@@ -673,7 +673,7 @@ __global__ void __launch_bounds__(384, 1) k_attn_fwd4(const __grid_constant__ Fw
   uint8_t* smem = smem_raw;
   // the swizzled tiles need a 1024-byte aligned base; the declaration asks for it
   if (smem_u32(smem_raw) & 1023u) {
-    if (threadIdx.x == 0) atomicCAS(a.status, 0, kStatusTimeout);
+    if (threadIdx.x == 0) atomicExch(a.status, kStatusTimeout);
     return;
   }
   constexpr int S = C::kStages;

@@ -11,7 +11,8 @@ namespace ne {
 
 constexpr int kTile = 128;  // query rows / key rows per tile
 
-// Device-side status codes (mirror ne_status in include/ne_attn.h).
+// Device-side status codes (mirror ne_status in include/ne_attn.h). The word keeps the first bad page,
+// but a timeout takes its place: counters that the library keeps may then be half way.
 constexpr int kStatusTimeout = -6;
 constexpr int kStatusPage = -8;
 

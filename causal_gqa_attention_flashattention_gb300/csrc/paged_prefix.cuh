@@ -220,7 +220,7 @@ __device__ void prefix_role(const PagedDecodeArgs& a, const int* len, uint8_t* s
     }
     if (!ok && lane == 0) {
       *abort = 1;
-      atomicCAS(a.status, 0, kStatusTimeout);
+      atomicExch(a.status, kStatusTimeout);
     }
     // let every copy issued above land before the block can exit
     if (lane == 0) {
@@ -258,7 +258,7 @@ __device__ void prefix_role(const PagedDecodeArgs& a, const int* len, uint8_t* s
       }
       if (!ok) {
         *abort = 1;
-        atomicCAS(a.status, 0, kStatusTimeout);
+        atomicExch(a.status, kStatusTimeout);
       }
       mma_commit(drain);
       mbar_wait(drain, 0, &never);
@@ -303,7 +303,7 @@ __device__ void prefix_role(const PagedDecodeArgs& a, const int* len, uint8_t* s
       }
       if (!ok) {
         *abort = 1;
-        atomicCAS(a.status, 0, kStatusTimeout);
+        atomicExch(a.status, kStatusTimeout);
       }
       mma_commit(drain + 1 + u);
       mbar_wait(drain + 1 + u, 0, &never);
@@ -461,7 +461,7 @@ __device__ void prefix_role(const PagedDecodeArgs& a, const int* len, uint8_t* s
     }
     if (!ok) {
       *abort = 1;
-      atomicCAS(a.status, 0, kStatusTimeout);
+      atomicExch(a.status, kStatusTimeout);
     }
   }
 

@@ -899,7 +899,7 @@ __global__ void __launch_bounds__(kSweepThreads, 1) k_paged_sweep(const __grid_c
     }
     if (!ok && lane == 0) {
       *abort = 1;
-      atomicCAS(a.status, 0, kStatusTimeout);
+      atomicExch(a.status, kStatusTimeout);
     }
     return;
   }
@@ -947,7 +947,7 @@ __global__ void __launch_bounds__(kSweepThreads, 1) k_paged_sweep(const __grid_c
   }
   if (!ok && lane == 0) {
     *abort = 1;
-    atomicCAS(a.status, 0, kStatusTimeout);
+    atomicExch(a.status, kStatusTimeout);
   }
 }
 

@@ -417,7 +417,9 @@ int ne_attn_decode_paged(const void* q, const void* q_w, const void* k_pages, co
  * if the synchronisation itself failed.  The pages have no counterpart to this
  * call; it reports the failures the kernels detect themselves, a pipeline
  * wait that gave up and a bad page of a paged cache, while the GPU context
- * stays usable.
+ * stays usable.  A timeout takes the place of a bad page that was met before it.
+ * After a timeout the library's own workspaces are ready for use again once this
+ * call has returned it.
  */
 int ne_attn_check_status(void* stream);
 
