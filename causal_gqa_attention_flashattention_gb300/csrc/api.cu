@@ -84,6 +84,7 @@ struct RopeTable {
   double base;
   int Tcap;
   float2* ptr;
+  cudaEvent_t built;  // recorded behind its build; null once that is known to have ended
 };
 
 // Work items of the persistent forward, per CTA: see fwd_pair_schedule.
@@ -116,6 +117,7 @@ struct DeviceState {
   bool supported = false;
   int* status = nullptr;
   std::vector<RopeTable> tables;
+  cudaStream_t build_stream = nullptr;  // where they are built (made on first use)
   std::vector<FwdSchedule> scheds;
   std::vector<FwdScratch> fwd_scratch;
   std::vector<JoinScratch> join_scratch;
@@ -159,30 +161,65 @@ int device_state(int dev, DeviceState** out) {
   return NE_OK;
 }
 
-// Returns a table with at least Tneed rows for (D, base) on this device.
+// What another stream's capture forbids this thread (allocations, event queries) is allowed while one of
+// these lives: nothing here is work of a captured stream.
+struct RelaxedCapture {
+  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+  RelaxedCapture() { cudaThreadExchangeStreamCaptureMode(&mode); }
+  ~RelaxedCapture() { cudaThreadExchangeStreamCaptureMode(&mode); }
+};
+
+// Orders work on `s` behind the table's build.  The host waits only if `s` is being captured (a captured
+// stream cannot wait for an event from outside), and for the build alone.
+int await_rope_table(RopeTable& t, cudaStream_t s) {
+  if (!t.built) return NE_OK;
+  RelaxedCapture relaxed;
+  cudaError_t e = cudaEventQuery(t.built);
+  if (e == cudaErrorNotReady) {
+    cudaGetLastError();
+    cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(s, &cs) != cudaSuccess) return NE_ERR_CUDA;
+    if (cs == cudaStreamCaptureStatusNone) return cudaStreamWaitEvent(s, t.built, 0) == cudaSuccess ? NE_OK : NE_ERR_CUDA;
+    e = cudaEventSynchronize(t.built);
+  }
+  if (e != cudaSuccess) return NE_ERR_CUDA;
+  cudaEventDestroy(t.built);
+  t.built = nullptr;
+  return NE_OK;
+}
+
+// Returns a table with at least Tneed rows for (D, base) on this device, for use on `s`.
 // Requires g_mu held.
 int rope_table(DeviceState& d, int D, double base, int Tneed, cudaStream_t s, const float2** out) {
   for (auto& t : d.tables)
     if (t.D == D && t.base == base && t.Tcap >= Tneed) {
       *out = t.ptr;
-      return NE_OK;
+      return await_rope_table(t, s);
     }
-  // Building one allocates and waits for the build, so that a call on another
-  // stream may use it at once; neither can be done under stream capture.
-  cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
-  if (cudaStreamIsCapturing(s, &cs) != cudaSuccess) return NE_ERR_CUDA;
-  if (cs != cudaStreamCaptureStatusNone) return NE_ERR_WORKSPACE;
+  // Built on a stream of its own: behind nothing that is queued on `s`, so that a call on another
+  // stream that finds the table waits for the build alone; and outside a capture of `s`.
+  RelaxedCapture relaxed;
+  if (!d.build_stream && cudaStreamCreateWithFlags(&d.build_stream, cudaStreamNonBlocking) != cudaSuccess) {
+    d.build_stream = nullptr;
+    return NE_ERR_CUDA;
+  }
   int Tcap = ((Tneed + 1023) / 1024) * 1024;
-  float2* p = nullptr;
-  if (cudaMalloc(&p, sizeof(float2) * (size_t)Tcap * (D / 2)) != cudaSuccess) return NE_ERR_CUDA;
-  if (launch_rope_table(p, Tcap, D, base, s) != cudaSuccess || cudaStreamSynchronize(s) != cudaSuccess) {
-    cudaFree(p);
+  RopeTable t = {D, base, Tcap, nullptr, nullptr};
+  if (cudaMalloc(&t.ptr, sizeof(float2) * (size_t)Tcap * (D / 2)) != cudaSuccess) return NE_ERR_CUDA;
+  if (cudaEventCreateWithFlags(&t.built, cudaEventDisableTiming) != cudaSuccess) {
+    cudaFree(t.ptr);
+    return NE_ERR_CUDA;
+  }
+  if (launch_rope_table(t.ptr, Tcap, D, base, d.build_stream) != cudaSuccess ||
+      cudaEventRecord(t.built, d.build_stream) != cudaSuccess) {
+    cudaEventDestroy(t.built);
+    cudaFree(t.ptr);
     return NE_ERR_CUDA;
   }
   // Older, smaller tables stay allocated: kernels queued on other streams may still read them.
-  d.tables.push_back(RopeTable{D, base, Tcap, p});
-  *out = p;
-  return NE_OK;
+  d.tables.push_back(t);
+  *out = t.ptr;
+  return await_rope_table(d.tables.back(), s);
 }
 
 // The persistent forward's work items, built on the host once per shape.  A

@@ -27,7 +27,7 @@
  *
  * Every call is asynchronous on `stream` (a cudaStream_t; NULL is the legacy
  * default stream): no host synchronisation, no host<->device copies (but for
- * the first call of a new table, below).  Argument
+ * the first call of a new forward shape, below).  Argument
  * errors are detected on the host and returned before anything is launched.
  * A kernel whose internal pipeline wait exceeds its time limit stops, frees
  * its tensor memory and records NE_ERR_DEVICE_TIMEOUT in a device status word
@@ -37,10 +37,11 @@
  * cos/sin of t * theta_i for t below the largest T seen so far, built on the
  * device in double precision; and, per forward shape, the table of work items
  * of each CTA of the persistent forward kernel (built on the host, copied once).
- * The first call that needs a new or larger table allocates it with cudaMalloc
- * and waits for its build, so make one call per shape (with the largest T)
- * before capturing calls in a CUDA graph (a captured call that needs a new
- * rotary table returns NE_ERR_WORKSPACE).  Calls that pass no workspace use a buffer of the
+ * The first call that needs a new or larger table allocates it with cudaMalloc.
+ * A rotary table is built on a stream of the library's own, for which the calls'
+ * streams wait (under stream capture the host waits, for the build alone).  A work
+ * table is copied while the host waits, so make one forward call per shape
+ * before capturing calls in a CUDA graph.  Calls that pass no workspace use a buffer of the
  * library's per stream (see ne_attn_fwd_ex).  Nothing else is allocated.
  */
 #ifndef NE_ATTN_H
