@@ -188,14 +188,21 @@ int await_rope_table(RopeTable& t, cudaStream_t s) {
   return NE_OK;
 }
 
-// Returns a table with at least Tneed rows for (D, base) on this device, for use on `s`.
+// Returns a table with at least Tneed rows for (D, base) on this device, for use on `s`.  A table that is
+// outgrown is followed by one of twice its rows or more (up to kRopeGrowRows): the tables of one (D, base)
+// together are less than twice the last, and contexts that grow a little at a time build few.
 // Requires g_mu held.
+constexpr int kRopeGrowRows = 1 << 20;
 int rope_table(DeviceState& d, int D, double base, int Tneed, cudaStream_t s, const float2** out) {
-  for (auto& t : d.tables)
-    if (t.D == D && t.base == base && t.Tcap >= Tneed) {
+  int most = 0;
+  for (auto& t : d.tables) {
+    if (t.D != D || t.base != base) continue;
+    if (t.Tcap >= Tneed) {
       *out = t.ptr;
       return await_rope_table(t, s);
     }
+    if (t.Tcap > most) most = t.Tcap;
+  }
   // Built on a stream of its own: behind nothing that is queued on `s`, so that a call on another
   // stream that finds the table waits for the build alone; and outside a capture of `s`.
   RelaxedCapture relaxed;
@@ -203,14 +210,20 @@ int rope_table(DeviceState& d, int D, double base, int Tneed, cudaStream_t s, co
     d.build_stream = nullptr;
     return NE_ERR_CUDA;
   }
-  int Tcap = ((Tneed + 1023) / 1024) * 1024;
-  RopeTable t = {D, base, Tcap, nullptr, nullptr};
-  if (cudaMalloc(&t.ptr, sizeof(float2) * (size_t)Tcap * (D / 2)) != cudaSuccess) return NE_ERR_CUDA;
+  const int need = ((Tneed + 1023) / 1024) * 1024, grown = most < kRopeGrowRows / 2 ? 2 * most : kRopeGrowRows;
+  RopeTable t = {D, base, grown > need ? grown : need, nullptr, nullptr};
+  const auto bytes = [&] { return sizeof(float2) * (size_t)t.Tcap * (D / 2); };
+  if (cudaMalloc(&t.ptr, bytes()) != cudaSuccess) {
+    cudaGetLastError();
+    if (t.Tcap == need) return NE_ERR_CUDA;
+    t.Tcap = need;
+    if (cudaMalloc(&t.ptr, bytes()) != cudaSuccess) return NE_ERR_CUDA;
+  }
   if (cudaEventCreateWithFlags(&t.built, cudaEventDisableTiming) != cudaSuccess) {
     cudaFree(t.ptr);
     return NE_ERR_CUDA;
   }
-  if (launch_rope_table(t.ptr, Tcap, D, base, d.build_stream) != cudaSuccess ||
+  if (launch_rope_table(t.ptr, t.Tcap, D, base, d.build_stream) != cudaSuccess ||
       cudaEventRecord(t.built, d.build_stream) != cudaSuccess) {
     cudaEventDestroy(t.built);
     cudaFree(t.ptr);

@@ -1,6 +1,9 @@
 """Rotary tables that a call needs for the first time: the host does not wait for what is queued on
 the call's stream, calls on other streams see a finished table, and a captured call may need one too."""
+import numpy as np
 import pytest
+
+from oracle import paged
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -111,3 +114,26 @@ def test_capture_right_after_the_build(nb, bases):
         torch.cuda.synchronize()
         assert all(torch.equal(p, q) for p, q in zip(got, norm(nb, x, base)))
         assert torch.equal(first, step(nb, x, base))
+
+
+def test_growing_contexts_keep_few_tables(nb, bases):
+    """Contexts that grow by 2048 positions at a time up to 65536: tables of 2048, 4096, 8192, ... 65536
+    rows, 32 MB in all where one for each step would be 277 MB.  The keys are rotated as the oracle has
+    it, to the append's bound (the fp16 rounding and 2^-19 of the pair)."""
+    k = torch.randn((1, 1, 1, D), device="cuda").bfloat16()
+    kc, vc = nb.kv_cache(1, 65536, 1, D, "cuda")
+    put = lambda pos, base: nb.kv_append(k, k, kc, vc, pos, rope_base=base)
+    put(0, next(bases))
+    base = next(bases)
+    torch.cuda.synchronize()
+    free = torch.cuda.mem_get_info()[0]
+    last = [2048 * i - 1 for i in range(1, 33)]
+    for pos in last:
+        put(pos, base)
+    torch.cuda.synchronize()
+    assert free - torch.cuda.mem_get_info()[0] < 64 << 20
+    x = k[0].double().cpu().numpy()
+    want = paged.rope_at(np.repeat(x, len(last), 0), last, base)[:, 0]
+    pair = np.repeat(np.linalg.norm(x[0, 0].reshape(D // 2, 2), axis=-1), 2) * 2.0 ** -19
+    got = kc[0, 0, last].double().cpu().numpy()
+    assert (np.abs(got - want) <= (np.abs(want) + pair) * 2.0 ** -11 + pair + 2.0 ** -25).all()
