@@ -110,7 +110,7 @@ struct JoinScratch {
   size_t bytes;
 };
 constexpr size_t kCounterBytes = 1024;
-constexpr size_t kJoinStreams = 64;  // streams that have one at a time
+constexpr size_t kJoinStreams = 64;  // streams that have one at a time: those used last
 
 struct DeviceState {
   bool init = false;
@@ -365,11 +365,16 @@ int join_scratch(DeviceState& d, cudaStream_t s, size_t need, void** ws, unsigne
   if (cs != cudaStreamCaptureStatusNone) return NE_ERR_WORKSPACE;
   unsigned long long id = 0;
   if (cudaStreamGetId(s, &id) != cudaSuccess) return NE_ERR_CUDA;
+  // in the order of their last use: the stream used now goes to the end
   JoinScratch* f = nullptr;
-  for (auto& x : d.join_scratch)
-    if (x.stream == id) f = &x;
+  for (size_t i = d.join_scratch.size(); i-- > 0 && !f;)
+    if (d.join_scratch[i].stream == id) {
+      std::rotate(d.join_scratch.begin() + i, d.join_scratch.begin() + i + 1, d.join_scratch.end());
+      f = &d.join_scratch.back();
+    }
   if (!f && d.join_scratch.size() >= kJoinStreams) {
-    // a program that keeps making streams: the oldest one's go (cudaFree waits for the device)
+    // a program that keeps making streams: those of the one not used for longest go (cudaFree
+    // waits for the device)
     JoinScratch& x = d.join_scratch.front();
     if (x.ptr && cudaFree(x.ptr) != cudaSuccess) return NE_ERR_CUDA;
     x.ptr = nullptr;

@@ -403,7 +403,9 @@ int ne_attn_kv_append_paged(const void* k_new, const void* v_new, const void* k_
  * < 2^30.  The workspace (ne_attn_decode_paged_workspace_size bytes, 256-byte
  * aligned) may be NULL: the library then uses one of its own per stream, grown
  * with cudaMalloc when a larger shape arrives, except under stream capture
- * (NE_ERR_WORKSPACE: a graph may run on any stream).  Calls and graphs that may
+ * (NE_ERR_WORKSPACE: a graph may run on any stream).  64 streams have one at a time;
+ * for one more, the workspace of the stream not used for longest is freed, which
+ * waits for the device.  Calls and graphs that may
  * run at the same time need workspaces of their own.  The result is bitwise
  * reproducible.
  */
