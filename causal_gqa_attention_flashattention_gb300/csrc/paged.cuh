@@ -68,18 +68,19 @@ __device__ __forceinline__ void query_finish(const PagedDecodeArgs& a, const Que
   lo = make_uint4(l[0], l[1], l[2], l[3]);
 }
 
-// Row r of (sequence b, head g), columns 4 q .. 4 q + 3: normalise and write.
+// Row r of (sequence b, head g), columns 4 q .. 4 q + 3: normalise and write. L is 0 for a row that saw no
+// key, and only then; a NaN stays one in o and lse.
 template <int D>
 __device__ __forceinline__ void write_row(const PagedDecodeArgs& a, int b, int g, int r, int q, float4 v, float M, float L) {
   const int t = (int)fdiv((uint32_t)r, a.div_g), h = g * a.G + (r - t * a.G);
-  const float inv = L > 0.f ? 1.f / L : 0.f;
+  const float inv = L == 0.f ? 0.f : 1.f / L;
   const size_t at = (((size_t)b * a.Tq + t) * a.Hq + h) * D + 4 * q;
   v = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
   if (a.o_fp32)
     *reinterpret_cast<float4*>(static_cast<float*>(a.o) + at) = v;
   else
     *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.o) + at) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
-  if (q == 0 && a.lse) a.lse[((size_t)b * a.Hq + h) * a.Tq + t] = L > 0.f ? (M + log2f(L)) * kPagedLn2 : -INFINITY;
+  if (q == 0 && a.lse) a.lse[((size_t)b * a.Hq + h) * a.Tq + t] = L == 0.f ? -INFINITY : (M + log2f(L)) * kPagedLn2;
 }
 
 // Positions of a sequence that the sweep leaves to the prefix kernel: the whole shared
