@@ -441,6 +441,12 @@ def _int32(t, name, device, shape):
         raise ValueError("%s must be a contiguous int32 %s on the call's device" % (name, list(shape)))
 
 
+def _bytes(workspace, device):
+    # its size is counted in numel(): an expanded tensor has more of those than bytes
+    if workspace.dtype != torch.uint8 or workspace.device != device or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous uint8 on the call's device")
+
+
 def _run_ws(name, device, args, workspace, size):
     """_run with the workspace as the last arguments: the caller's; without one NULL (the
     library's own for the stream) or, where a capture needs one, a tensor of the capture's own."""
@@ -451,8 +457,8 @@ def _run_ws(name, device, args, workspace, size):
         if st != ERR_WORKSPACE:
             raise NeAttnError(name, st)
         workspace = torch.empty(size(), dtype=torch.uint8, device=device)
-    elif workspace.dtype != torch.uint8 or workspace.device != device:
-        raise ValueError("workspace must be uint8 on the call's device")
+    else:
+        _bytes(workspace, device)
     _run(name, device, *args, workspace.data_ptr(), workspace.numel())
 
 
@@ -476,9 +482,8 @@ def qk_norm(q, k, q_weight, k_weight, eps=1e-6, rope_base=10000.0, rope_half=Fal
     if workspace is None:
         n = (B * T * Hq * D + 127) // 128 * 256 + (B * T * Hkv * D + 127) // 128 * 256  # as rotated_qk
         workspace = torch.empty(n, dtype=torch.uint8, device=dev)
-    elif workspace.dtype != torch.uint8 or workspace.device != dev:
-        raise ValueError("workspace must be uint8 on the call's device")
     else:
+        _bytes(workspace, dev)
         n = workspace.numel()
     _run("ne_attn_qk_norm", dev, q.data_ptr(), k.data_ptr(), q_weight.data_ptr(), k_weight.data_ptr(),
          B, T, Hq, Hkv, D, qs, ks, eps, rope_base, ROPE_HALF if rope_half else 0, workspace.data_ptr(), n)
