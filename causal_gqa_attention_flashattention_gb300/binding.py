@@ -387,10 +387,12 @@ def _need(ok, what):
         raise ValueError(what)
 
 
-def _on(stream, call, *args, **kw):
-    """The call with `stream` as the current stream: what it allocates then belongs to it."""
+def _on(stream, call, x, *args):
+    """call(x, *args) with `stream`, of x's device, as the current stream: what it allocates then belongs to it."""
+    if stream.device != x.device:
+        raise ValueError("stream must be of the call's device")
     with torch.cuda.stream(stream):
-        return call(*args, **kw)
+        return call(x, *args)
 
 
 def _call(name, device, args):

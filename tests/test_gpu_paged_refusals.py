@@ -1,5 +1,7 @@
 """What the binding of the query/key norms and the paged calls refuses before the library is called,
 with tensors on the GPU."""
+import types
+
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -44,3 +46,14 @@ def test_workspaces(nb, name):
             call(workspace=ws)
     with pytest.raises(nb.NeAttnError):
         call(workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.parametrize("name", ["qk_norm", "qk_norm_bwd", "append", "decode"])
+def test_stream_of_another_device(nb, name):
+    """The call would run on its own device's current stream, not behind the work of the given one."""
+    call = calls(nb)[name]
+    with pytest.raises(ValueError):
+        call(stream=types.SimpleNamespace(device=torch.device("cuda", 1), cuda_stream=0))
+    call(stream=torch.cuda.Stream())
+    torch.cuda.synchronize()
+    nb.check_status()
