@@ -470,8 +470,10 @@ def qk_norm(q, k, q_weight, k_weight, eps=1e-6, rope_base=10000.0, rope_half=Fal
 
     q and k may be slices of a fused projection's rows.  The rotated fp16 q and k
     land at the start of `workspace` (a uint8 CUDA tensor of at least
-    fwd_workspace_size bytes; allocated if None), which is returned: attn_fwd and
-    attn_bwd take it with qk_rotated=True (q and k then None), rotated_qk views it.
+    fwd_workspace_size bytes; one of that size is allocated if None), which is
+    returned: attn_fwd takes it with qk_rotated=True (q and k then None), rotated_qk
+    views it.  attn_bwd needs more room: for training give alloc_workspace's, which
+    attn_fwd and attn_bwd then both take with qk_rotated=True.
     """
     if stream is not None:
         return _on(stream, qk_norm, q, k, q_weight, k_weight, eps, rope_base, rope_half, workspace)

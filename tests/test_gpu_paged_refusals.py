@@ -57,3 +57,17 @@ def test_stream_of_another_device(nb, name):
     call(stream=torch.cuda.Stream())
     torch.cuda.synchronize()
     nb.check_status()
+
+
+def test_workspace_for_training(nb):
+    """The workspace that qk_norm allocates is the forward's: the backward refuses it, and takes alloc_workspace's."""
+    bf = lambda *s: torch.randn(s, device="cuda").bfloat16()
+    B, T, Hq, Hkv, D = 1, 200, 4, 2, 64
+    q, k, v, do, w = bf(B, T, Hq, D), bf(B, T, Hkv, D), bf(B, T, Hkv, D), bf(B, T, Hq, D), bf(D)
+    short, enough = nb.qk_norm(q, k, w, w), nb.qk_norm(q, k, w, w, workspace=nb.alloc_workspace(B, T, Hq, Hkv, D))
+    out = [nb.attn_fwd(None, None, v, workspace=ws, qk_rotated=True, Hq=Hq) for ws in (short, enough)]
+    assert torch.equal(out[0][0], out[1][0]) and torch.equal(out[0][1], out[1][1])
+    with pytest.raises(nb.NeAttnError):
+        nb.attn_bwd(None, None, v, *out[0], do, workspace=short, qk_rotated=True)
+    assert all(torch.isfinite(g.float()).all() for g in nb.attn_bwd(None, None, v, *out[1], do, workspace=enough, qk_rotated=True))
+    nb.check_status()
