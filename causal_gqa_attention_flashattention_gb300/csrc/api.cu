@@ -117,7 +117,7 @@ struct DeviceState {
   bool supported = false;
   int* status = nullptr;
   std::vector<RopeTable> tables;
-  cudaStream_t build_stream = nullptr;  // where they are built (made on first use)
+  cudaStream_t build_stream = nullptr;  // where captured calls have theirs built (made on first use)
   std::vector<FwdSchedule> scheds;
   std::vector<FwdScratch> fwd_scratch;
   std::vector<JoinScratch> join_scratch;
@@ -170,7 +170,7 @@ struct RelaxedCapture {
 };
 
 // Orders work on `s` behind the table's build.  The host waits only if `s` is being captured (a captured
-// stream cannot wait for an event from outside), and for the build alone.
+// stream cannot wait for an event from outside).
 int await_rope_table(RopeTable& t, cudaStream_t s) {
   if (!t.built) return NE_OK;
   RelaxedCapture relaxed;
@@ -203,12 +203,19 @@ int rope_table(DeviceState& d, int D, double base, int Tneed, cudaStream_t s, co
     }
     if (t.Tcap > most) most = t.Tcap;
   }
-  // Built on a stream of its own: behind nothing that is queued on `s`, so that a call on another
-  // stream that finds the table waits for the build alone; and outside a capture of `s`.
+  // Built on `s`, calls on other streams wait for the event.  For a captured `s` on a stream of the
+  // library's, outside the capture; only then: work on one more stream makes every later kernel of a
+  // program's graphs start about 0.25 us later (a shared prefix's call of two 21.1 -> 21.6 us).
   RelaxedCapture relaxed;
-  if (!d.build_stream && cudaStreamCreateWithFlags(&d.build_stream, cudaStreamNonBlocking) != cudaSuccess) {
-    d.build_stream = nullptr;
-    return NE_ERR_CUDA;
+  cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(s, &cs) != cudaSuccess) return NE_ERR_CUDA;
+  cudaStream_t on = s;
+  if (cs != cudaStreamCaptureStatusNone) {
+    if (!d.build_stream && cudaStreamCreateWithFlags(&d.build_stream, cudaStreamNonBlocking) != cudaSuccess) {
+      d.build_stream = nullptr;
+      return NE_ERR_CUDA;
+    }
+    on = d.build_stream;
   }
   const int need = ((Tneed + 1023) / 1024) * 1024, grown = most < kRopeGrowRows / 2 ? 2 * most : kRopeGrowRows;
   RopeTable t = {D, base, grown > need ? grown : need, nullptr, nullptr};
@@ -223,8 +230,8 @@ int rope_table(DeviceState& d, int D, double base, int Tneed, cudaStream_t s, co
     cudaFree(t.ptr);
     return NE_ERR_CUDA;
   }
-  if (launch_rope_table(t.ptr, t.Tcap, D, base, d.build_stream) != cudaSuccess ||
-      cudaEventRecord(t.built, d.build_stream) != cudaSuccess) {
+  if (launch_rope_table(t.ptr, t.Tcap, D, base, on) != cudaSuccess ||
+      cudaEventRecord(t.built, on) != cudaSuccess) {
     cudaEventDestroy(t.built);
     cudaFree(t.ptr);
     return NE_ERR_CUDA;

@@ -38,11 +38,11 @@
  * device in double precision; and, per forward shape, the table of work items
  * of each CTA of the persistent forward kernel (built on the host, copied once).
  * The first call that needs a new or larger table allocates it with cudaMalloc.
- * A rotary table is built on a stream of the library's own, for which the calls'
- * streams wait (under stream capture the host waits, for the build alone); one that
- * is outgrown stays allocated and is followed by one of at least twice its rows (up
- * to 2^20, or what the call needs).  A work
- * table is copied while the host waits, so make one forward call per shape
+ * A rotary table is built on the stream of the call that needs it first, and other
+ * calls' streams wait for it (under stream capture it is built on a stream of the
+ * library's own, and the host waits); one that is outgrown stays allocated and is
+ * followed by one of at least twice its rows (up to 2^20, or what the call needs).
+ * A work table is copied while the host waits, so make one forward call per shape
  * before capturing calls in a CUDA graph.  Calls that pass no workspace use a buffer of the
  * library's per stream (see ne_attn_fwd_ex).  Nothing else is allocated.
  */
