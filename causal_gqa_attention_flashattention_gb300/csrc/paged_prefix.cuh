@@ -59,13 +59,15 @@ inline int prefix_smem(int D, int B) {
 }
 
 // The blocks that take the prefix, of all: their share of the work, a tile of a pair of row tiles
-// counted as 2.75 of the sweep's (measured: 128 sequences on 16384 positions 40.8 us, 45.5, 43.1, 40.9, 41.3
-// at 2, 2.5, 3, 3.5; 100 on 2048 21.3, 24.9, 21.3, 21.3, 21.3). Above 16 rows the sweep is bound by its
-// products, for every 32 rows a tile counts three times (40 sequences of 20 rows on 8192 positions 34.4 us,
-// with 1 52.9, 2 36.1, 4 37.7, 5 37.7; 20 of 64 rows on 4096 21.7, 22.0, 22.2, 21.6, 23.3).
+// counted as 3.25 of the sweep's (measured: 128 sequences on 16384 positions 40.1 us, with 3 42.3, with 3.5
+// 40.2; 100 on 2048 21.0, 24.5, 21.0), and a (sequence, head) as one tile more than in the sweep's own
+// plan, whose blocks share that cost alike (100 sequences of one own position on 131072 68.8 us, without
+// 100; 64 of up to 16 on 65536 46.7, 49.5; 128 of up to 20 on 1024 20.4, 18.7). Above 16 rows the sweep is
+// bound by its products, for every 32 rows a tile counts three times (40 sequences of 20 rows on 8192
+// positions 34.0 us, with 1 52.9, 2 36.1, 4 37.7, 5 37.7; 20 of 64 rows on 4096 21.3, 22.0, 22.2, 21.6, 23.3).
 __device__ __forceinline__ int prefix_blocks(const PagedDecodeArgs& a, int sweep_tiles, int blocks) {
-  const float mine = 2.75f * (float)a.pre.W;
-  const float theirs = (float)sweep_tiles * (a.D == 64 ? 1.f : 0.5f) * (a.R > 16 ? 3.f * (float)a.MG : 1.f);
+  const float mine = 3.25f * (float)a.pre.W;
+  const float theirs = ((float)sweep_tiles + (float)(a.B * a.Hkv)) * (a.D == 64 ? 1.f : 0.5f) * (a.R > 16 ? 3.f * (float)a.MG : 1.f);
   const int P = max(1, min(min(__float2int_rn((float)blocks * __fdiv_rn(mine, mine + theirs)), blocks - 1), a.pre.W));
   // the same number for every (head, pair), so that no block has parts of two (which costs it
   // a second packing and a second epilogue, about 4 us)
