@@ -92,3 +92,24 @@ def test_same_with_and_without(nb):
     two = nb.attn_decode_paged(s["q"], s["kp"], s["vp"], table, s["lens"], eps=EPS, rope_base=BASE, o_dtype=torch.float32)
     hold(nb, s, one, prefix)
     hold(nb, s, two, prefix)
+
+
+MANY = [
+    # own lengths, prefix, Tq, Hq, Hkv, D, page: more (head, pair of row tiles)s than blocks take the prefix
+    ([3, 70, 900], 640, 1, 200, 200, 32, 64),
+    ([5, 1], 400, 2, 180, 180, 64, 16),
+    ([(i * 7) % 60 + 4 for i in range(70)], 256, 4, 80, 40, 32, 128),     # 560 rows a head: 5 row tiles
+    ([4000, 3900, 17], 128, 1, 48, 24, 64, 64),
+]
+
+
+@pytest.mark.parametrize("case", MANY, ids=lambda c: "b%d_p%d_t%d_%dx%dx%d" % (len(c[0]), *c[1:6]))
+def test_many_heads(nb, case):
+    """The prefix's tiles of all heads lie in one line: a block has parts of several heads and row tiles."""
+    own, prefix, Tq, Hq, Hkv, D, page = case
+    s = setup([prefix + x for x in own], Tq, Hq, Hkv, D, page, seed=prefix, prefix=prefix, scale=1.5)
+    got = decode(nb, s, prefix)
+    hold(nb, s, got, prefix)
+    for _ in range(3):
+        again = decode(nb, s, prefix)
+        assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
