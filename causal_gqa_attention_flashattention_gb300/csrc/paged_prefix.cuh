@@ -18,7 +18,7 @@
 // two fp16 parts (two products; with one the LSE is off by 1e-5), the weights as two bf16
 // parts (2^-17; one part is 2^-9 off, and the call with a prefix then differs from the one without by
 // more than a bf16 o's rounding). Both parts of all 128 keys would not fit the tensor memory, so P
-// goes out in quarters of 32 keys through two buffers. 128 sequences on 16384 positions 40.4 us, with
+// goes out in quarters of 32 keys through two buffers. 128 sequences on 16384 positions 39.7 us, with
 // one part in halves 34.8: a third each for the second part's arithmetic, its products and the
 // hand-offs (halves through one buffer 46.5 where quarters take 45.6).
 #pragma once
@@ -100,7 +100,7 @@ struct PreSeg {
 // Rows r0 .. r0 + 31 of a packed tile whose first row is rho0, normalised and rotated, as fp16 high and low
 // parts into the swizzled tiles at dst and behind it.  D / 8 neighbouring lanes to a row, so that a
 // load takes whole lines (100 sequences on 2048 positions 23.9 us, with a lane to a row 25.4; 64 on 8192
-// 20.5, 20.2), all of the warp's rows under way at once.
+// 20.5, 20.2, each with one part of the weights), all of the warp's rows under way at once.
 template <int D>
 __device__ __forceinline__ void pack_query_rows(const PagedDecodeArgs& a, const int* len, int g, int rho0, uint8_t* dst,
                                                 int r0, int lane) {
