@@ -5,6 +5,7 @@ library.  PyTorch supplies device memory and the current stream.  If the
 library has not been built, or its kernels cannot run on this device, the
 calls raise; there is no other implementation to fall back to.
 """
+import collections
 import ctypes
 import os
 
@@ -89,6 +90,16 @@ def lib():
         L.ne_attn_decode_paged_workspace_size.restype = sz
         L.ne_attn_decode_paged.argtypes = [vp] * 9 + [i] * 8 + [ll, ll, i, f, f, i, vp, sz, vp]
         L.ne_attn_decode_paged.restype = i
+        L.ne_attn_paged_plan.argtypes = [vp] * 13 + [i] * 6 + [ll, vp]
+        L.ne_attn_paged_plan.restype = i
+        L.ne_attn_kv_append_slots.argtypes = [vp] * 7 + [i] * 6 + [ll] * 3 + [f, f, i, vp]
+        L.ne_attn_kv_append_slots.restype = i
+        L.ne_attn_decode_tree_workspace_size.argtypes = [i, i, i, i, i]
+        L.ne_attn_decode_tree_workspace_size.restype = sz
+        L.ne_attn_decode_tree.argtypes = [vp] * 10 + [i] * 8 + [ll] * 3 + [f, f, i, vp, sz, vp]
+        L.ne_attn_decode_tree.restype = i
+        L.ne_attn_kv_keep_paged.argtypes = [vp] * 8 + [i] * 8 + [ll, vp]
+        L.ne_attn_kv_keep_paged.restype = i
         _lib = L
     return _lib
 
@@ -222,7 +233,7 @@ def status_of_last_kernels(stream=None):
 
 KERNEL_KINDS = ("fwd", "bwd_prep", "bwd_dkdv", "bwd_dq", "fwd_rope", "kv_append", "decode", "decode_aux",
                 "qkv_prep", "qkv", "qk_norm", "qk_norm_bwd", "kv_append_paged", "decode_paged",
-                "decode_prefix")
+                "decode_prefix", "paged_plan", "decode_tree", "kv_keep")
 
 
 def profile_start(capacity):
@@ -592,6 +603,23 @@ def decode_paged_workspace_size(B, Tq, Hq, Hkv, D, prefix_len=0):
     return int(lib().ne_attn_decode_paged_workspace_size(B, Tq, Hq, Hkv, D, prefix_len))
 
 
+def _outputs(o, lse, o_dtype, B, Tq, Hq, D, dev):
+    if o is None:
+        o = torch.empty((B, Tq, Hq, D), dtype=o_dtype, device=dev)
+    elif o.device != dev or not o.is_contiguous() or o.shape != (B, Tq, Hq, D):
+        raise ValueError("o must be a contiguous [B, Tq, Hq, D] on the call's device")
+    else:
+        o_dtype = o.dtype
+    if lse is None:
+        lse = torch.empty((B, Hq, Tq), dtype=torch.float32, device=dev)
+    elif lse.dtype != torch.float32 or lse.device != dev or not lse.is_contiguous() or lse.shape != (B, Hq, Tq):
+        raise ValueError("lse must be a contiguous float32 [B, Hq, Tq] on the call's device")
+    fp32 = o_dtype == torch.float32
+    if not fp32 and o_dtype != torch.bfloat16:
+        raise ValueError("o must be bfloat16 or float32")
+    return o, lse, fp32
+
+
 def attn_decode_paged(q, k_pages, v_pages, page_table, kv_len, q_weight=None, eps=1e-6, rope_base=10000.0,
                       prefix_table=None, prefix_len=0, o=None, lse=None, o_dtype=torch.bfloat16, workspace=None,
                       rope_half=False, stream=None):
@@ -618,19 +646,7 @@ def attn_decode_paged(q, k_pages, v_pages, page_table, kv_len, q_weight=None, ep
         _need(prefix_table is not None and prefix_table.dim() == 1 and prefix_table.numel() * page >= prefix_len,
               "prefix_table must hold the pages of prefix_len positions")
         _int32(prefix_table, "prefix_table", dev, prefix_table.shape)
-    if o is None:
-        o = torch.empty((B, Tq, Hq, D), dtype=o_dtype, device=dev)
-    elif o.device != dev or not o.is_contiguous() or o.shape != (B, Tq, Hq, D):
-        raise ValueError("o must be a contiguous [B, Tq, Hq, D] on the call's device")
-    else:
-        o_dtype = o.dtype
-    if lse is None:
-        lse = torch.empty((B, Hq, Tq), dtype=torch.float32, device=dev)
-    elif lse.dtype != torch.float32 or lse.device != dev or not lse.is_contiguous() or lse.shape != (B, Hq, Tq):
-        raise ValueError("lse must be a contiguous float32 [B, Hq, Tq] on the call's device")
-    fp32 = o_dtype == torch.float32
-    if not fp32 and o_dtype != torch.bfloat16:
-        raise ValueError("o must be bfloat16 or float32")
+    o, lse, fp32 = _outputs(o, lse, o_dtype, B, Tq, Hq, D, dev)
     args = (q.data_ptr(), None if q_weight is None else q_weight.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
             page_table.data_ptr(), kv_len.data_ptr(), prefix_table.data_ptr() if prefix_len else None, o.data_ptr(),
             lse.data_ptr(), B, Tq, Hq, Hkv, D, page, P, width, stride, qs, prefix_len, eps, rope_base,
@@ -638,6 +654,174 @@ def attn_decode_paged(q, k_pages, v_pages, page_table, kv_len, q_weight=None, ep
     _run_ws("ne_attn_decode_paged", dev, args, workspace,
             lambda: decode_paged_workspace_size(B, Tq, Hq, Hkv, D, prefix_len))
     return o, lse
+
+
+# ------------------------------------------------------------------ drafted trees over the paged cache
+PagedPlan = collections.namedtuple("PagedPlan", "kv_len held span cu_new slots positions")
+
+
+def _tree(parents, B, device):
+    """(tokens, row stride) of parents int32 [B, Tq], or [Tq]: one tree for the batch."""
+    n, s = parents.shape, parents.stride()
+    if (parents.dtype != torch.int32 or parents.device != device or len(n) not in (1, 2)
+            or (len(n) == 2 and n[0] != B) or (n[-1] > 1 and s[-1] != 1)):
+        raise ValueError("parents must be int32 [B, Tq] or [Tq], rows contiguous, on the call's device")
+    if len(n) == 1 or B == 1:
+        return n[-1], 0
+    if s[0] != 0 and s[0] < n[1]:
+        raise ValueError("parents: rows must not overlap")
+    return n[1], s[0]
+
+
+def _out32(t, name, device, shape):
+    if t is None:
+        return torch.empty(shape, dtype=torch.int32, device=device)
+    _int32(t, name, device, shape)
+    return t
+
+
+def _apart(a, b, what):
+    # neither a byte of the one in the other
+    pa, pb = a.data_ptr(), b.data_ptr()
+    if pa < pb + 4 * b.numel() and pb < pa + 4 * a.numel():
+        raise ValueError("%s must not share memory" % what)
+
+
+def paged_plan(page_table, free_pages, held, free_span, kv_len, new_len, rows, page_size, parents=None, kv_len_out=None,
+               held_out=None, span_out=None, stream=None):
+    """Block tables and slot maps from lengths, on the device (ne_attn_paged_plan).
+
+    Sequence b has kv_len[b] positions, holds the first held[b] pages of its row of page_table [B, max_pages] and
+    is to have new_len[b] more; free_pages [num_pages] is a ring whose entries free_span = (first, count) are free.
+    All are int32 CUDA tensors; page_table and free_pages are changed in place.  rows: how many new rows the
+    call maps, those past the sum of new_len being padding.  parents [B, Tq] or [Tq]: the new tokens are trees.
+
+    Returns PagedPlan(kv_len [B], held [B], span [2], cu_new [B + 1], slots [rows], positions [rows]): the new
+    lengths and pages held (a sequence whose pages the ring no longer has keeps its old ones), where each
+    sequence's rows begin, and the place (-1: none) and rotary position of every row for kv_append_slots.
+    held_out and span_out may be held and free_span themselves, kv_len_out may not be kv_len."""
+    if stream is not None:
+        return _on(stream, paged_plan, page_table, free_pages, held, free_span, kv_len, new_len, rows, page_size, parents,
+                   kv_len_out, held_out, span_out)
+    B, width = page_table.shape
+    dev = page_table.device
+    _need(page_table.is_cuda, "page_table must be a CUDA tensor")
+    _int32(page_table, "page_table", dev, (B, width))
+    _need(free_pages.dim() == 1, "free_pages must be [num_pages]")
+    _int32(free_pages, "free_pages", dev, free_pages.shape)
+    for t, n, shape in ((held, "held", (B,)), (free_span, "free_span", (2,)), (kv_len, "kv_len", (B,)), (new_len, "new_len", (B,))):
+        _int32(t, n, dev, shape)
+    Tq, pstride = (0, 0) if parents is None else _tree(parents, B, dev)
+    if kv_len_out is not None:
+        _int32(kv_len_out, "kv_len_out", dev, (B,))
+        _apart(kv_len_out, kv_len, "kv_len_out and kv_len")
+    total = _out32(kv_len_out, "kv_len_out", dev, (B,))
+    got, span = _out32(held_out, "held_out", dev, (B,)), _out32(span_out, "span_out", dev, (2,))
+    cu = torch.empty(B + 1, dtype=torch.int32, device=dev)
+    slots = torch.empty(rows, dtype=torch.int32, device=dev)
+    positions = torch.empty(rows, dtype=torch.int32, device=dev)
+    _run("ne_attn_paged_plan", dev, page_table.data_ptr(), free_pages.data_ptr(), held.data_ptr(), free_span.data_ptr(),
+         kv_len.data_ptr(), new_len.data_ptr(), _optr(parents), got.data_ptr(), span.data_ptr(), total.data_ptr(),
+         cu.data_ptr(), slots.data_ptr(), positions.data_ptr(), rows, B, Tq, page_size, free_pages.numel(), width, pstride)
+    return PagedPlan(total, got, span, cu, slots, positions)
+
+
+def kv_append_slots(k_new, v_new, k_pages, v_pages, slots, positions, capacity, k_weight=None, eps=1e-6,
+                    rope_base=10000.0, rope_half=False, stream=None):
+    """Writes new keys and values [N,Hkv,D] (bf16, rows may be strided) to given places of a paged cache
+    (ne_attn_kv_append_slots): row n to slot slots[n] (int32 [N], negative: nowhere), its key normalised with k_weight
+    [D] unless None and rotated at positions[n] (int32 [N], below `capacity`).  paged_plan gives both.
+    Bad slots and positions are found by check_status."""
+    if stream is not None:
+        return _on(stream, kv_append_slots, k_new, v_new, k_pages, v_pages, slots, positions, capacity, k_weight, eps,
+                   rope_base, rope_half)
+    N, Hkv, D = k_new.shape
+    dev = k_new.device
+    _need(v_new.shape == k_new.shape, "k_new and v_new must have one shape")
+    ks, vs = _head_rows(k_new, "k_new"), _head_rows(v_new, "v_new", device=dev)
+    P, page, stride = _pools(k_pages, v_pages, Hkv, D, dev)
+    _int32(slots, "slots", dev, (N,))
+    _int32(positions, "positions", dev, (N,))
+    if k_weight is not None:
+        _vector(k_weight, D, "k_weight", dev)
+    if N == 0:
+        return
+    _run("ne_attn_kv_append_slots", dev, k_new.data_ptr(), v_new.data_ptr(), _optr(k_weight), k_pages.data_ptr(),
+         v_pages.data_ptr(), slots.data_ptr(), positions.data_ptr(), N, Hkv, D, page, P, capacity, stride, ks, vs, eps,
+         rope_base, ROPE_HALF if rope_half else 0)
+
+
+def decode_tree_workspace_size(B, Tq, Hq, Hkv, D):
+    return int(lib().ne_attn_decode_tree_workspace_size(B, Tq, Hq, Hkv, D))
+
+
+def attn_decode_tree(q, k_pages, v_pages, page_table, kv_len, parents, tree_len=None, q_weight=None, eps=1e-6,
+                     rope_base=10000.0, o=None, lse=None, o_dtype=torch.bfloat16, workspace=None, rope_half=False,
+                     stream=None):
+    """o, lse for a tree of drafted tokens q [B,Tq,Hq,D] (bf16) of every sequence over a paged cache
+    (ne_attn_decode_tree).
+
+    kv_len int32 [B] counts the cached positions, the tree's tree_len[b] own included (int32 [B]; None: Tq).  parents
+    int32 [B, Tq] or [Tq] (one tree for all): the token each hangs on, -1 for the context.  A token sees the
+    positions before the tree, its ancestors and itself; tokens past tree_len, and idle slots (kv_len 0), get o = 0
+    and lse = -inf.  q_weight [D]: the queries are normalised first."""
+    if stream is not None:
+        return _on(stream, attn_decode_tree, q, k_pages, v_pages, page_table, kv_len, parents, tree_len, q_weight, eps,
+                   rope_base, o, lse, o_dtype, workspace, rope_half)
+    B, Tq, Hq, D = q.shape
+    Hkv, dev = k_pages.shape[1], q.device
+    qs = _head_rows(q, "q")
+    P, page, stride = _pools(k_pages, v_pages, Hkv, D, dev)
+    width = page_table.shape[1]
+    _int32(page_table, "page_table", dev, (B, width))
+    _int32(kv_len, "kv_len", dev, (B,))
+    n, pstride = _tree(parents, B, dev)
+    _need(n == Tq, "parents must have a token for each of q's")
+    if tree_len is not None:
+        _int32(tree_len, "tree_len", dev, (B,))
+    if q_weight is not None:
+        _vector(q_weight, D, "q_weight", dev)
+    o, lse, fp32 = _outputs(o, lse, o_dtype, B, Tq, Hq, D, dev)
+    args = (q.data_ptr(), _optr(q_weight), k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(), kv_len.data_ptr(),
+            parents.data_ptr(), _optr(tree_len), o.data_ptr(), lse.data_ptr(), B, Tq, Hq, Hkv, D, page, P, width, stride, qs,
+            pstride, eps, rope_base, (O_FP32 if fp32 else 0) | (ROPE_HALF if rope_half else 0))
+    _run_ws("ne_attn_decode_tree", dev, args, workspace, lambda: decode_tree_workspace_size(B, Tq, Hq, Hkv, D))
+    return o, lse
+
+
+def kv_keep_paged(k_pages, v_pages, page_table, kv_len, tree_len, path, path_len, kv_len_out=None, stream=None):
+    """Keeps the accepted path of every sequence's tree (ne_attn_kv_keep_paged): the keys and values of its tokens
+    path[b, :path_len[b]] (int32 [B, width] and [B], rising) move to the positions right behind the context, in place.
+
+    kv_len int32 [B] counts the cached positions, the tree's tree_len (int32 [B], or one number for all) included;
+    returns the new lengths (kv_len_out if given, which may not be kv_len).  The pools of several layers with one
+    table may be passed as one [num_pages, layers * Hkv, page_size, D]."""
+    if stream is not None:
+        return _on(stream, kv_keep_paged, k_pages, v_pages, page_table, kv_len, tree_len, path, path_len, kv_len_out)
+    dev = k_pages.device
+    _need(k_pages.is_cuda, "pools must be CUDA tensors")
+    Hkv, D = k_pages.shape[1], k_pages.shape[3]
+    P, page, stride = _pools(k_pages, v_pages, Hkv, D, dev)
+    B, width = page_table.shape
+    _int32(page_table, "page_table", dev, (B, width))
+    _int32(kv_len, "kv_len", dev, (B,))
+    _need(path.dim() == 2, "path must be [B, width]")
+    _int32(path, "path", dev, (B, path.shape[1]))
+    _int32(path_len, "path_len", dev, (B,))
+    tokens, lens = 0, None
+    if isinstance(tree_len, torch.Tensor):
+        _int32(tree_len, "tree_len", dev, (B,))
+        lens = tree_len
+    else:
+        tokens = int(tree_len)
+    if kv_len_out is not None:
+        _int32(kv_len_out, "kv_len_out", dev, (B,))
+        _apart(kv_len_out, kv_len, "kv_len_out and kv_len")
+    out = _out32(kv_len_out, "kv_len_out", dev, (B,))
+    _run("ne_attn_kv_keep_paged", dev, k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(), kv_len.data_ptr(),
+         _optr(lens), path.data_ptr(), path_len.data_ptr(), out.data_ptr(), B, tokens, path.shape[1], Hkv, D, page, P, width,
+         stride)
+    return out
 
 
 class HostStepPipeline:

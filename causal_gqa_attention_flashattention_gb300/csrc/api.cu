@@ -626,6 +626,19 @@ int check_decode_paged_rows(int B, int Tq, int Hq, int Hkv, int D) {
   return NE_OK;
 }
 
+// The shape rules of a tree's attention: tokens as bits of a mask, 32-bit indices of rows.
+int check_tree(int B, int Tq, int Hq, int Hkv, int D) {
+  if (Tq < 1) return NE_ERR_ARG;
+  if (Tq > kTreeMax || (long long)B * Tq * Hq * D >= (1LL << 31)) return NE_ERR_UNSUPPORTED;
+  return NE_OK;
+}
+// Slots of the pool are counted in 32 bits.
+int check_slots(int page_size, int num_pages) {
+  if (num_pages < 1) return NE_ERR_ARG;
+  if (page_size < 16 || page_size > 256 || (page_size & (page_size - 1)) != 0) return NE_ERR_UNSUPPORTED;
+  return (long long)num_pages * page_size < (1LL << 31) ? NE_OK : NE_ERR_UNSUPPORTED;
+}
+
 // Decode workspace: the split segments' O, their (maximum, sum), the counters.
 // With a shared prefix then its segments' O and (maximum, sum), and the sequences' own.
 struct PagedWs {
@@ -1189,6 +1202,7 @@ const char* ne_attn_status_string(int status) {
              "ne_attn_bwd_noalloc holds; use ne_attn_bwd with a caller workspace";
     case NE_ERR_PAGE:
       return "a page table entry outside the pool, or a position outside the page table, was met on the device";
+    case NE_ERR_TREE: return "a drafted tree or a path in it that is not one was met on the device";
     default: return "unknown status";
   }
 }
@@ -1638,6 +1652,212 @@ int ne_attn_decode_paged(const void* q, const void* q_w, const void* k_pages, co
   }
   ProfScope prof(NE_ATTN_KERNEL_DECODE_PAGED, s);
   return launch_decode_paged(a, mt, nsm, s) == cudaSuccess ? NE_OK : NE_ERR_CUDA;
+}
+
+// ------------------------------------------------------------------ drafted trees over the paged cache
+int ne_attn_paged_plan(int* page_table, int* free_pages, const int* held, const int* free_span, const int* kv_len,
+                       const int* new_len, const int* parents, int* held_out, int* free_span_out, int* kv_len_out,
+                       int* cu_new, int* slots, int* positions, int N, int B, int Tq, int page_size, int num_pages,
+                       int max_pages, long long parent_stride, void* stream) {
+  if (!page_table || !free_pages || !held || !free_span || !kv_len || !new_len || !held_out || !free_span_out ||
+      !kv_len_out || !cu_new || !slots || !positions)
+    return NE_ERR_ARG;
+  if (B < 1 || N < 1 || max_pages < 1 || kv_len_out == kv_len) return NE_ERR_ARG;
+  int st = check_slots(page_size, num_pages);
+  if (st != NE_OK) return st;
+  if (B > kPagedMaxBatch || (long long)max_pages * page_size > kPagedMaxPositions || N > (1 << 30))
+    return NE_ERR_UNSUPPORTED;
+  if (parents) {
+    if (Tq < 1 || (parent_stride != 0 && parent_stride < Tq)) return NE_ERR_ARG;
+    if (Tq > kTreeMax) return NE_ERR_UNSUPPORTED;
+  }
+  const void* all[] = {page_table, free_pages, held, free_span, kv_len, new_len, parents, held_out, free_span_out,
+                       kv_len_out, cu_new, slots, positions};
+  for (const void* p : all)
+    if (!aligned4(p)) return NE_ERR_ALIGN;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  std::lock_guard<std::mutex> lock(g_mu);
+  int dev, nsm = 0;
+  DeviceState* d;
+  if ((st = device_and_sms(&dev, &d, &nsm)) != NE_OK) return st;
+  PagedPlanArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.table = page_table;
+  a.ring = free_pages;
+  a.held = held;
+  a.span = free_span;
+  a.len = kv_len;
+  a.add = new_len;
+  a.parents = parents;
+  a.held_out = held_out;
+  a.span_out = free_span_out;
+  a.len_out = kv_len_out;
+  a.cu = cu_new;
+  a.slots = slots;
+  a.positions = positions;
+  a.status = d->status;
+  a.parent_stride = parent_stride;
+  a.N = N;
+  a.B = B;
+  a.Tq = Tq;
+  a.page_shift = log2_of(page_size);
+  a.num_pages = num_pages;
+  a.max_pages = max_pages;
+  ProfScope prof(NE_ATTN_KERNEL_PAGED_PLAN, s);
+  return launch_paged_plan(a, s) == cudaSuccess ? NE_OK : NE_ERR_CUDA;
+}
+
+int ne_attn_kv_append_slots(const void* k_new, const void* v_new, const void* k_w, void* k_pages, void* v_pages,
+                            const int* slots, const int* positions, int N, int Hkv, int D, int page_size,
+                            int num_pages, int capacity, long long page_stride, long long k_stride,
+                            long long v_stride, float eps, float rope_base, int flags, void* stream) {
+  if (!k_new || !v_new || !k_pages || !v_pages || !slots || !positions) return NE_ERR_ARG;
+  if ((flags & ~kFlagRopeHalf) != 0) return NE_ERR_ARG;
+  if (k_w && (!(eps > 0.0f) || !std::isfinite(eps))) return NE_ERR_ARG;
+  if (!(rope_base > 1.0f) || !std::isfinite(rope_base)) return NE_ERR_ARG;
+  if (N < 1 || capacity < 1) return NE_ERR_ARG;
+  int st = check_paged(1, Hkv, Hkv, D, page_size, num_pages, 1, page_stride);
+  if (st != NE_OK) return st;
+  if ((st = check_slots(page_size, num_pages)) != NE_OK) return st;
+  if (capacity > kPagedMaxPositions || (long long)N * Hkv * D >= (1LL << 31)) return NE_ERR_UNSUPPORTED;
+  if (!row_stride_ok(k_stride, Hkv, D) || !row_stride_ok(v_stride, Hkv, D)) return NE_ERR_ARG;
+  if (!aligned16(k_new) || !aligned16(v_new) || !aligned16(k_pages) || !aligned16(v_pages) || (k_w && !aligned16(k_w)) ||
+      !aligned4(slots) || !aligned4(positions))
+    return NE_ERR_ALIGN;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  std::lock_guard<std::mutex> lock(g_mu);
+  int dev, nsm = 0;
+  DeviceState* d;
+  if ((st = device_and_sms(&dev, &d, &nsm)) != NE_OK) return st;
+  PagedAppendArgs a;
+  std::memset(&a, 0, sizeof(a));
+  if ((st = rope_table(*d, D, (double)rope_base, capacity, s, &a.rope)) != NE_OK) return st;
+  a.k = static_cast<const __nv_bfloat16*>(k_new);
+  a.v = static_cast<const __nv_bfloat16*>(v_new);
+  a.kw = static_cast<const __nv_bfloat16*>(k_w);
+  a.kp = static_cast<__half*>(k_pages);
+  a.vp = static_cast<__nv_bfloat16*>(v_pages);
+  a.slots = slots;
+  a.positions = positions;
+  a.capacity = capacity;
+  a.status = d->status;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.page_stride = page_stride;
+  a.N = N;
+  a.B = 1;
+  a.Hkv = Hkv;
+  a.page_shift = log2_of(page_size);
+  a.num_pages = num_pages;
+  a.rope_half = (flags & kFlagRopeHalf) ? 1 : 0;
+  a.eps = eps;
+  a.div_hkv = make_fastdiv((uint32_t)Hkv);
+  ProfScope prof(NE_ATTN_KERNEL_KV_APPEND_PAGED, s);
+  return launch_kv_append_slots(a, D, s) == cudaSuccess ? NE_OK : NE_ERR_CUDA;
+}
+
+size_t ne_attn_decode_tree_workspace_size(int B, int Tq, int Hq, int Hkv, int D) {
+  if (check_paged(B, Hq, Hkv, D, 16, 1, 1, 16LL * Hkv * D) != NE_OK || check_tree(B, Tq, Hq, Hkv, D) != NE_OK) return 0;
+  return 256;
+}
+
+int ne_attn_decode_tree(const void* q, const void* q_w, const void* k_pages, const void* v_pages,
+                        const int* page_table, const int* kv_len, const int* parents, const int* tree_len, void* o,
+                        float* lse, int B, int Tq, int Hq, int Hkv, int D, int page_size, int num_pages, int max_pages,
+                        long long page_stride, long long q_stride, long long parent_stride, float eps,
+                        float rope_base, int flags, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!q || !k_pages || !v_pages || !page_table || !kv_len || !parents || !o) return NE_ERR_ARG;
+  if ((flags & ~(kFlagOFp32 | kFlagRopeHalf)) != 0) return NE_ERR_ARG;
+  if (q_w && (!(eps > 0.0f) || !std::isfinite(eps))) return NE_ERR_ARG;
+  if (!(rope_base > 1.0f) || !std::isfinite(rope_base)) return NE_ERR_ARG;
+  int st = check_paged(B, Hq, Hkv, D, page_size, num_pages, max_pages, page_stride);
+  if (st != NE_OK) return st;
+  if ((st = check_tree(B, Tq, Hq, Hkv, D)) != NE_OK) return st;
+  if ((st = check_paged_tiles(B, Hkv, page_size, max_pages)) != NE_OK) return st;
+  if (!row_stride_ok(q_stride, Hq, D) || (parent_stride != 0 && parent_stride < Tq)) return NE_ERR_ARG;
+  if (!aligned16(q) || (q_w && !aligned16(q_w)) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(o) ||
+      !aligned4(lse) || !aligned4(page_table) || !aligned4(kv_len) || !aligned4(parents) || !aligned4(tree_len))
+    return NE_ERR_ALIGN;
+  if (workspace && (workspace_bytes < ne_attn_decode_tree_workspace_size(B, Tq, Hq, Hkv, D) ||
+                    (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0))
+    return NE_ERR_WORKSPACE;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  std::lock_guard<std::mutex> lock(g_mu);
+  int dev, nsm = 0;
+  DeviceState* d;
+  if ((st = device_and_sms(&dev, &d, &nsm)) != NE_OK) return st;
+  PagedTreeArgs a;
+  std::memset(&a, 0, sizeof(a));
+  if ((st = rope_table(*d, D, (double)rope_base, max_pages * page_size, s, &a.rope)) != NE_OK) return st;
+  a.kp = static_cast<const __half*>(k_pages);
+  a.vp = static_cast<const __nv_bfloat16*>(v_pages);
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.qw = static_cast<const __nv_bfloat16*>(q_w);
+  a.table = page_table;
+  a.len = kv_len;
+  a.parents = parents;
+  a.nodes = tree_len;
+  a.status = d->status;
+  a.o = o;
+  a.lse = lse;
+  a.page_stride = page_stride;
+  a.q_stride = q_stride;
+  a.parent_stride = parent_stride;
+  a.B = B;
+  a.Tq = Tq;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.D = D;
+  a.G = Hq / Hkv;
+  a.page_shift = log2_of(page_size);
+  a.num_pages = num_pages;
+  a.max_pages = max_pages;
+  a.rope_half = (flags & kFlagRopeHalf) ? 1 : 0;
+  a.o_fp32 = (flags & kFlagOFp32) ? 1 : 0;
+  a.eps = eps;
+  a.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)D));
+  ProfScope prof(NE_ATTN_KERNEL_DECODE_TREE, s);
+  return launch_decode_tree(a, s) == cudaSuccess ? NE_OK : NE_ERR_CUDA;
+}
+
+int ne_attn_kv_keep_paged(void* k_pages, void* v_pages, const int* page_table, const int* kv_len, const int* tree_len,
+                          const int* path, const int* path_len, int* kv_len_out, int B, int tokens, int width, int Hkv,
+                          int D, int page_size, int num_pages, int max_pages, long long page_stride, void* stream) {
+  if (!k_pages || !v_pages || !page_table || !kv_len || !path || !path_len || !kv_len_out || kv_len_out == kv_len)
+    return NE_ERR_ARG;
+  if (width < 1 || tokens < 0) return NE_ERR_ARG;
+  int st = check_paged(B, Hkv, Hkv, D, page_size, num_pages, max_pages, page_stride);
+  if (st != NE_OK) return st;
+  if (width > kTreeMax) return NE_ERR_UNSUPPORTED;
+  if (!aligned16(k_pages) || !aligned16(v_pages) || !aligned4(page_table) || !aligned4(kv_len) || !aligned4(tree_len) ||
+      !aligned4(path) || !aligned4(path_len) || !aligned4(kv_len_out))
+    return NE_ERR_ALIGN;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  std::lock_guard<std::mutex> lock(g_mu);
+  int dev, nsm = 0;
+  DeviceState* d;
+  if ((st = device_and_sms(&dev, &d, &nsm)) != NE_OK) return st;
+  PagedKeepArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.kp = static_cast<__half*>(k_pages);
+  a.vp = static_cast<__nv_bfloat16*>(v_pages);
+  a.table = page_table;
+  a.len = kv_len;
+  a.nodes = tree_len;
+  a.path = path;
+  a.count = path_len;
+  a.len_out = kv_len_out;
+  a.status = d->status;
+  a.page_stride = page_stride;
+  a.B = B;
+  a.Hkv = Hkv;
+  a.width = width;
+  a.tokens = tokens;
+  a.page_shift = log2_of(page_size);
+  a.num_pages = num_pages;
+  a.max_pages = max_pages;
+  ProfScope prof(NE_ATTN_KERNEL_KV_KEEP, s);
+  return launch_kv_keep(a, D, s) == cudaSuccess ? NE_OK : NE_ERR_CUDA;
 }
 
 int ne_attn_debug_fwd_schedule(int B, int Hkv, int G, int nt, int nsm, int* table, int capacity, int* grid,

@@ -15,6 +15,7 @@ constexpr int kTile = 128;  // query rows / key rows per tile
 // but a timeout takes its place: counters that the library keeps may then be half way.
 constexpr int kStatusTimeout = -6;
 constexpr int kStatusPage = -8;
+constexpr int kStatusTree = -9;
 
 // Flag bits shared with include/ne_attn.h.
 constexpr int kFlagOFp32 = 1;      // o is float32
@@ -219,6 +220,48 @@ struct PagedAppendArgs {
   int N, B, Hkv, page_shift, num_pages, max_pages, rope_half;
   float eps;
   FastDiv div_hkv, div_per;         // by Hkv and by N / B (cu null)
+  const int *slots, *positions;     // append to slots: [N] each; table, pos0 and cu are then not used
+  int capacity;                     // positions of the rotary table
+};
+
+// Block tables and slot maps from lengths (see paged_plan.cu).
+constexpr int kTreeMax = 64;  // tokens of a drafted tree: one bit each in a mask of ancestors
+struct PagedPlanArgs {
+  int *table, *ring;                           // [B, max_pages], [num_pages]
+  const int *held, *span, *len, *add;          // [B], [2] (first, count), [B], [B]
+  const int* parents;                          // [B, Tq] parent_stride apart, or null
+  int *held_out, *span_out, *len_out;          // the first two may be held and span
+  int *cu, *slots, *positions;                 // [B + 1], [N], [N]
+  int* status;
+  long long parent_stride;
+  int N, B, Tq, page_shift, num_pages, max_pages;
+};
+
+// The accepted path of a drafted tree moved behind the cached positions (see paged_plan.cu).
+struct PagedKeepArgs {
+  __half* kp;
+  __nv_bfloat16* vp;
+  const int *table, *len, *nodes, *path, *count;  // [B, max_pages], [B], [B] or null (all `tokens`), [B, width], [B]
+  int* len_out;                                   // [B]
+  int* status;
+  long long page_stride;
+  int B, Hkv, width, tokens, page_shift, num_pages, max_pages;
+};
+
+// Attention of a drafted tree over a paged cache (see paged_tree.cu).
+struct PagedTreeArgs {
+  const __half* kp;             // pools, pages page_stride values apart
+  const __nv_bfloat16* vp;
+  const __nv_bfloat16 *q, *qw;  // [B, Tq, Hq, D], positions q_stride values apart; qw [D] or null
+  const int *table, *len;       // [B, max_pages], [B]
+  const int *parents, *nodes;   // [B, Tq] rows parent_stride apart; [B] or null (all Tq)
+  const float2* rope;
+  int* status;
+  void* o;
+  float* lse;                   // or null
+  long long page_stride, q_stride, parent_stride;
+  int B, Tq, Hq, Hkv, D, G, page_shift, num_pages, max_pages, rope_half, o_fp32;
+  float eps, scale_log2;
 };
 
 // Attention of the newest tokens over a paged cache (see paged.cu).
@@ -314,6 +357,10 @@ int qk_norm_blocks(int B, int T, int Hq, int Hkv, int D, int nsm, bool bwd, int*
 cudaError_t launch_qk_norm(const QkNormArgs& a, int D, int blocks, cudaStream_t s);
 cudaError_t launch_qk_norm_bwd(const QkNormBwdArgs& a, int D, bool f32, int blocks, bool clear, cudaStream_t s);
 cudaError_t launch_kv_append_paged(const PagedAppendArgs& a, int D, cudaStream_t s);
+cudaError_t launch_kv_append_slots(const PagedAppendArgs& a, int D, cudaStream_t s);
+cudaError_t launch_paged_plan(const PagedPlanArgs& a, cudaStream_t s);
+cudaError_t launch_kv_keep(const PagedKeepArgs& a, int D, cudaStream_t s);
+cudaError_t launch_decode_tree(const PagedTreeArgs& a, cudaStream_t s);
 void paged_rows(int R, int* mt, int* tiles, int* mg);
 cudaError_t launch_decode_paged(const PagedDecodeArgs& a, int mt, int nsm, cudaStream_t s);
 cudaError_t launch_decode_prefix(const PagedDecodeArgs& a, int mt, int nsm, cudaStream_t s);

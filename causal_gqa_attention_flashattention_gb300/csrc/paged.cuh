@@ -11,6 +11,7 @@ constexpr float kPagedLn2 = 0.69314718055994531f;
 constexpr int kSmemMax = 232448;
 
 __device__ __forceinline__ void record_page(int* status) { atomicCAS(status, 0, kStatusPage); }
+__device__ __forceinline__ void record_tree(int* status) { atomicCAS(status, 0, kStatusTree); }
 
 // Chunk c (8 values) of query row r of (sequence b, key/value head g) on its way to the
 // tensor cores, in two steps so that a warp can have the loads of several rows under way.

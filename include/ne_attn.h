@@ -64,8 +64,10 @@ typedef enum {
   NE_ERR_WORKSPACE = -5,      /* workspace missing, too small or not 256-byte aligned */
   NE_ERR_DEVICE_TIMEOUT = -6, /* a kernel gave up on a pipeline wait (see above) */
   NE_ERR_SCRATCH_LIMIT = -7,  /* ne_attn_bwd_noalloc: problem too large for its fixed scratch */
-  NE_ERR_PAGE = -8            /* a kernel met a page table entry outside the pool, or a position outside
+  NE_ERR_PAGE = -8,           /* a kernel met a page table entry outside the pool, or a position outside
                                  the page table (read by ne_attn_check_status) */
+  NE_ERR_TREE = -9            /* a kernel met a parent that does not come before its token, a tree that does
+                                 not fit, or a path that is not one (read by ne_attn_check_status) */
 } ne_status;
 
 /* Flag bits for ne_attn_fwd_ex, ne_attn_bwd and the workspace-size queries. */
@@ -417,12 +419,88 @@ int ne_attn_decode_paged(const void* q, const void* q_w, const void* k_pages, co
                          int flags, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * Trees of drafted tokens over the paged cache.  A step of a batch that drafts: ne_attn_paged_plan gives
+ * every sequence the pages for its drafted tokens and every token its slot and rotary position;
+ * ne_attn_kv_append_slots writes their keys and values; ne_attn_decode_tree is their attention; once it is known which
+ * of them stay, ne_attn_kv_keep_paged moves those behind the cached positions, and the next plan takes back
+ * the pages that are left over.  Lengths, trees, tables and paths are int32 arrays in device memory, read when
+ * the kernels run, so a captured CUDA graph of the whole step replays with new ones.
+ *
+ * A tree has at most 64 tokens.  Token t of sequence b hangs on token parents[b, t] < t, or on the context
+ * (-1; several may); rows of parents lie parent_stride values apart (0: one tree for the whole batch, else at least Tq).  Its
+ * depth is the number of its ancestors, its rotary position ctx + depth, where ctx positions come
+ * before the tree; its place in the cache is position ctx + t.  A parent below -1 or not before its token
+ * counts as -1 and is recorded as NE_ERR_TREE.
+ *
+ * ne_attn_paged_plan: sequence b has kv_len[b] positions, holds pages page_table[b, 0 .. held[b] - 1], and is to
+ * have new_len[b] positions more (0 is fine; kv_len may have shrunk since its pages were given).  It then holds
+ * ceil((kv_len + new_len) / page_size) pages: those it lacks are taken from the front of the ring of free pages
+ * (entries free_span[0] .. + free_span[1] - 1 of free_pages [num_pages], modulo num_pages), in the order of the
+ * sequences and of their tables; those it no longer needs go to the back of the ring, in the same order, and serve
+ * the next call.  Pages are handed out as long as they last: from the first sequence whose need goes past
+ * them, every one that needs pages gets none of them, keeps what it holds, and its rows get no slots.
+ * Writes held_out [B], free_span_out [2] (these may be held and free_span), kv_len_out [B] (kv_len + new_len, or
+ * kv_len where refused; a buffer of its own), cu_new [B + 1] (the running sum of new_len, at most N), and for each of the N rows
+ * n = cu_new[b] + t: slots[n] = the place of position kv_len[b] + t in the pools, page * page_size + row of the page (-1
+ * where refused and at or past cu_new[B]), positions[n] = kv_len[b] + t, with parents (at most Tq new tokens a
+ * sequence) kv_len[b] + depth(t) (0 at or past cu_new[B]).
+ * A sequence with a negative or too large length or count (more than max_pages * page_size positions, more than
+ * N rows up to its last, more than Tq tokens of a tree) is refused and recorded as NE_ERR_PAGE, and so are all if
+ * free_span is not a part of the ring.  B <= 2048, num_pages * page_size < 2^31.  One block, for more than 4096 rows a second launch.
+ */
+int ne_attn_paged_plan(int* page_table, int* free_pages, const int* held, const int* free_span, const int* kv_len,
+                       const int* new_len, const int* parents, int* held_out, int* free_span_out, int* kv_len_out,
+                       int* cu_new, int* slots, int* positions, int N, int B, int Tq, int page_size, int num_pages,
+                       int max_pages, long long parent_stride, void* stream);
+
+/*
+ * ne_attn_kv_append_slots: as ne_attn_kv_append_paged, with the place and the rotary position of every row given: row n
+ * goes to row slots[n] % page_size of page slots[n] / page_size, its key rotated at positions[n].  Rows
+ * with a negative slot are not written.  A slot outside the pool or a position outside 0 .. capacity - 1 (capacity
+ * <= 2^20) is recorded as NE_ERR_PAGE and not written.  No two rows may have one slot.
+ */
+int ne_attn_kv_append_slots(const void* k_new, const void* v_new, const void* k_w, void* k_pages, void* v_pages,
+                            const int* slots, const int* positions, int N, int Hkv, int D, int page_size,
+                            int num_pages, int capacity, long long page_stride, long long k_stride,
+                            long long v_stride, float eps, float rope_base, int flags, void* stream);
+
+/*
+ * ne_attn_decode_tree: kv_len[b] positions of sequence b are in the cache, the last tree_len[b] of them (NULL: Tq)
+ * its tree's.  The query of token t < tree_len[b], q[b, t] (otherwise as in ne_attn_decode_paged), attends to the
+ * positions before the tree, to its ancestors and to itself.  o and lse as there; tokens at or past
+ * tree_len[b], and all of an idle slot (kv_len[b] <= 0 or below tree_len[b]), see no key: o = 0, lse =
+ * -infinity.  A kv_len past the table (NE_ERR_PAGE) or a tree_len outside 0 .. Tq (NE_ERR_TREE) makes the slot an idle
+ * one.  Bad pages, values that must be numbers, and workspaces as for ne_attn_decode_paged; B * Tq * Hq * D < 2^31.
+ * The result is bitwise reproducible.
+ */
+size_t ne_attn_decode_tree_workspace_size(int B, int Tq, int Hq, int Hkv, int D);
+int ne_attn_decode_tree(const void* q, const void* q_w, const void* k_pages, const void* v_pages,
+                        const int* page_table, const int* kv_len, const int* parents, const int* tree_len, void* o,
+                        float* lse, int B, int Tq, int Hq, int Hkv, int D, int page_size, int num_pages, int max_pages,
+                        long long page_stride, long long q_stride, long long parent_stride, float eps,
+                        float rope_base, int flags, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * ne_attn_kv_keep_paged: of the tree at the end of sequence b (tree_len[b] tokens, NULL: `tokens`) the path_len[b] tokens
+ * path[b, 0], path[b, 1], .. stay (path [B, width], width <= 64; rising, as a child comes after its parent): the keys
+ * and values of token path[b, i] move to position kv_len[b] - tree_len[b] + i, in place, whatever the
+ * overlap.  Writes kv_len_out[b] = kv_len[b] - tree_len[b] + path_len[b] (a buffer of its own; idle slots, with
+ * kv_len[b] below tree_len[b] or 0, keep max(kv_len, 0)).  A path that does not rise or leaves the tree
+ * is recorded as NE_ERR_TREE and none of it stays.  The moved keys keep the rotation of their depth, which
+ * is right for a path from the context on.  The pools of layers that share one table may be given as one, with all their heads:
+ * [num_pages, layers * Hkv, page_size, D].
+ */
+int ne_attn_kv_keep_paged(void* k_pages, void* v_pages, const int* page_table, const int* kv_len, const int* tree_len,
+                          const int* path, const int* path_len, int* kv_len_out, int B, int tokens, int width, int Hkv,
+                          int D, int page_size, int num_pages, int max_pages, long long page_stride, void* stream);
+
+/*
  * Synchronises `stream`, then returns and clears the device status word of
- * the current device: NE_OK, NE_ERR_DEVICE_TIMEOUT, NE_ERR_PAGE, or NE_ERR_CUDA
+ * the current device: NE_OK, NE_ERR_DEVICE_TIMEOUT, NE_ERR_PAGE, NE_ERR_TREE, or NE_ERR_CUDA
  * if the synchronisation itself failed.  The pages have no counterpart to this
  * call; it reports the failures the kernels detect themselves, a pipeline
- * wait that gave up and a bad page of a paged cache, while the GPU context
- * stays usable.  A timeout takes the place of a bad page that was met before it.
+ * wait that gave up, a bad page of a paged cache and a bad tree, while the GPU context
+ * stays usable.  The first of them is kept, but a timeout takes the place of one that was met before it.
  * After a timeout the library's own workspaces are ready for use again once this
  * call has returned it.
  */
@@ -464,7 +542,10 @@ const char* ne_attn_status_string(int status);
 #define NE_ATTN_KERNEL_KV_APPEND_PAGED 12
 #define NE_ATTN_KERNEL_DECODE_PAGED 13  /* the sweep over a paged cache */
 #define NE_ATTN_KERNEL_DECODE_PREFIX 14 /* the same with a shared prefix, and the join */
-#define NE_ATTN_NUM_KERNEL_KINDS 15
+#define NE_ATTN_KERNEL_PAGED_PLAN 15    /* block tables and slot maps */
+#define NE_ATTN_KERNEL_DECODE_TREE 16   /* a drafted tree over a paged cache */
+#define NE_ATTN_KERNEL_KV_KEEP 17       /* the accepted path moved */
+#define NE_ATTN_NUM_KERNEL_KINDS 18
 int ne_attn_profile_start(int capacity);
 int ne_attn_profile_stop(double* total_ms, long long* launches);
 int ne_attn_profile_detach(void);
