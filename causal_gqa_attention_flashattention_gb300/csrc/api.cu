@@ -632,6 +632,19 @@ int check_tree(int B, int Tq, int Hq, int Hkv, int D) {
   if (Tq > kTreeMax || (long long)B * Tq * Hq * D >= (1LL << 31)) return NE_ERR_UNSUPPORTED;
   return NE_OK;
 }
+// Its workspace: the cut (sequence, head)s' parts, their (maximum, sum), where they are.
+struct TreeWs {
+  size_t part_o, part_ml, cut, total;
+};
+TreeWs tree_ws(int R, int D) {
+  const size_t rows = std::min(R, 2 * kTile);
+  TreeWs w;
+  w.part_o = 0;
+  w.part_ml = ws_up(2 * kPagedMaxBlocks * rows * D * 4);
+  w.cut = w.part_ml + ws_up(2 * kPagedMaxBlocks * rows * 8);
+  w.total = w.cut + ws_up(kPagedMaxBlocks * sizeof(int4));
+  return w;
+}
 // Slots of the pool are counted in 32 bits.
 int check_slots(int page_size, int num_pages) {
   if (num_pages < 1) return NE_ERR_ARG;
@@ -1758,7 +1771,7 @@ int ne_attn_kv_append_slots(const void* k_new, const void* v_new, const void* k_
 
 size_t ne_attn_decode_tree_workspace_size(int B, int Tq, int Hq, int Hkv, int D) {
   if (check_paged(B, Hq, Hkv, D, 16, 1, 1, 16LL * Hkv * D) != NE_OK || check_tree(B, Tq, Hq, Hkv, D) != NE_OK) return 0;
-  return 256;
+  return tree_ws(Hq / Hkv * Tq, D).total;
 }
 
 int ne_attn_decode_tree(const void* q, const void* q_w, const void* k_pages, const void* v_pages,
@@ -1773,7 +1786,10 @@ int ne_attn_decode_tree(const void* q, const void* q_w, const void* k_pages, con
   int st = check_paged(B, Hq, Hkv, D, page_size, num_pages, max_pages, page_stride);
   if (st != NE_OK) return st;
   if ((st = check_tree(B, Tq, Hq, Hkv, D)) != NE_OK) return st;
-  if ((st = check_paged_tiles(B, Hkv, page_size, max_pages)) != NE_OK) return st;
+  const int pairs = tree_pairs(Hq / Hkv * Tq);
+  // tiles and segments' costs of every (sequence, head, pair of row tiles) in 32 bits
+  if ((long long)Hkv * pairs > (1 << 20) || (st = check_paged_tiles(B, Hkv * pairs, page_size, max_pages + 4096 / page_size)) != NE_OK)
+    return NE_ERR_UNSUPPORTED;
   if (!row_stride_ok(q_stride, Hq, D) || (parent_stride != 0 && parent_stride < Tq)) return NE_ERR_ARG;
   if (!aligned16(q) || (q_w && !aligned16(q_w)) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(o) ||
       !aligned4(lse) || !aligned4(page_table) || !aligned4(kv_len) || !aligned4(parents) || !aligned4(tree_len))
@@ -1789,8 +1805,6 @@ int ne_attn_decode_tree(const void* q, const void* q_w, const void* k_pages, con
   PagedTreeArgs a;
   std::memset(&a, 0, sizeof(a));
   if ((st = rope_table(*d, D, (double)rope_base, max_pages * page_size, s, &a.rope)) != NE_OK) return st;
-  a.kp = static_cast<const __half*>(k_pages);
-  a.vp = static_cast<const __nv_bfloat16*>(v_pages);
   a.q = static_cast<const __nv_bfloat16*>(q);
   a.qw = static_cast<const __nv_bfloat16*>(q_w);
   a.table = page_table;
@@ -1800,7 +1814,6 @@ int ne_attn_decode_tree(const void* q, const void* q_w, const void* k_pages, con
   a.status = d->status;
   a.o = o;
   a.lse = lse;
-  a.page_stride = page_stride;
   a.q_stride = q_stride;
   a.parent_stride = parent_stride;
   a.B = B;
@@ -1809,6 +1822,10 @@ int ne_attn_decode_tree(const void* q, const void* q_w, const void* k_pages, con
   a.Hkv = Hkv;
   a.D = D;
   a.G = Hq / Hkv;
+  a.R = a.G * Tq;
+  a.pairs = pairs;
+  a.rows = std::min(a.R, 2 * kTile);
+  a.div_g = make_fastdiv((uint32_t)a.G);
   a.page_shift = log2_of(page_size);
   a.num_pages = num_pages;
   a.max_pages = max_pages;
@@ -1816,8 +1833,23 @@ int ne_attn_decode_tree(const void* q, const void* q_w, const void* k_pages, con
   a.o_fp32 = (flags & kFlagOFp32) ? 1 : 0;
   a.eps = eps;
   a.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)D));
+  const TreeWs w = tree_ws(a.R, D);
+  void* wsp = workspace;
+  unsigned* counters = nullptr;
+  if (!wsp && (st = join_scratch(*d, s, w.total, &wsp, &counters)) != NE_OK) return st;
+  unsigned char* ws = static_cast<unsigned char*>(wsp);
+  a.part_o = reinterpret_cast<float*>(ws + w.part_o);
+  a.part_ml = reinterpret_cast<float2*>(ws + w.part_ml);
+  a.cut = reinterpret_cast<int4*>(ws + w.cut);
+  const int prows = page_size < kTile ? page_size : kTile;
+  if ((st = make_map_pages(&a.map_pk, k_pages, num_pages, Hkv, page_size, D, page_stride, prows,
+                           CU_TENSOR_MAP_DATA_TYPE_FLOAT16)) != NE_OK)
+    return st;
+  if ((st = make_map_pages(&a.map_pv, v_pages, num_pages, Hkv, page_size, D, page_stride, prows,
+                           CU_TENSOR_MAP_DATA_TYPE_BFLOAT16)) != NE_OK)
+    return st;
   ProfScope prof(NE_ATTN_KERNEL_DECODE_TREE, s);
-  return launch_decode_tree(a, s) == cudaSuccess ? NE_OK : NE_ERR_CUDA;
+  return launch_decode_tree(a, nsm, s) == cudaSuccess ? NE_OK : NE_ERR_CUDA;
 }
 
 int ne_attn_kv_keep_paged(void* k_pages, void* v_pages, const int* page_table, const int* kv_len, const int* tree_len,

@@ -248,10 +248,10 @@ struct PagedKeepArgs {
   int B, Hkv, width, tokens, page_shift, num_pages, max_pages;
 };
 
+
 // Attention of a drafted tree over a paged cache (see paged_tree.cu).
 struct PagedTreeArgs {
-  const __half* kp;             // pools, pages page_stride values apart
-  const __nv_bfloat16* vp;
+  CUtensorMap map_pk, map_pv;   // pools {D, page, Hkv, num_pages}, box D x min(page, 128) rows
   const __nv_bfloat16 *q, *qw;  // [B, Tq, Hq, D], positions q_stride values apart; qw [D] or null
   const int *table, *len;       // [B, max_pages], [B]
   const int *parents, *nodes;   // [B, Tq] rows parent_stride apart; [B] or null (all Tq)
@@ -259,10 +259,17 @@ struct PagedTreeArgs {
   int* status;
   void* o;
   float* lse;                   // or null
-  long long page_stride, q_stride, parent_stride;
-  int B, Tq, Hq, Hkv, D, G, page_shift, num_pages, max_pages, rope_half, o_fp32;
+  float* part_o;                // [2 blocks, rows, D] unnormalised O of a block's first and last segment (workspace)
+  float2* part_ml;              // [2 blocks, rows] their maximum (log2 units) and sum
+  int4* cut;                    // [blocks] the (sequence, head) that is cut and begins in the block: sequence (-1: none),
+                                // head, last block (workspace)
+  long long q_stride, parent_stride;
+  int B, Tq, Hq, Hkv, D, G, R, page_shift, num_pages, max_pages, rope_half, o_fp32;
+  int pairs, rows;              // pairs of 128-row tiles of a head's queries; rows of the largest
+  FastDiv div_g, div_grid;      // by G and the sweep's blocks
   float eps, scale_log2;
 };
+inline int tree_pairs(int R) { return (R + 2 * kTile - 1) / (2 * kTile); }
 
 // Attention of the newest tokens over a paged cache (see paged.cu).
 constexpr int kPagedMaxBlocks = 160;  // blocks of the sweep: bounds its partial results
@@ -360,7 +367,7 @@ cudaError_t launch_kv_append_paged(const PagedAppendArgs& a, int D, cudaStream_t
 cudaError_t launch_kv_append_slots(const PagedAppendArgs& a, int D, cudaStream_t s);
 cudaError_t launch_paged_plan(const PagedPlanArgs& a, cudaStream_t s);
 cudaError_t launch_kv_keep(const PagedKeepArgs& a, int D, cudaStream_t s);
-cudaError_t launch_decode_tree(const PagedTreeArgs& a, cudaStream_t s);
+cudaError_t launch_decode_tree(const PagedTreeArgs& a, int nsm, cudaStream_t s);
 void paged_rows(int R, int* mt, int* tiles, int* mg);
 cudaError_t launch_decode_paged(const PagedDecodeArgs& a, int mt, int nsm, cudaStream_t s);
 cudaError_t launch_decode_prefix(const PagedDecodeArgs& a, int mt, int nsm, cudaStream_t s);

@@ -20,21 +20,27 @@ struct QueryChunk {
   float4 c0, c1;
   bool on;
 };
+template <int D, class A>
+__device__ __forceinline__ QueryChunk query_load_at(const A& a, bool on, int b, int g, int r, int t, int c, int pos) {
+  QueryChunk x;
+  x.on = on;
+  x.v = make_uint4(0, 0, 0, 0);
+  if (on)
+    x.v = load_rope_chunk<D>(a.q + (size_t)(b * a.Tq + t) * a.q_stride + (g * a.G + (r - t * a.G)) * D, c, a.rope_half != 0);
+  rope_coeffs<D>(a.rope, max(pos, 0), c, x.c0, x.c1);
+  return x;
+}
 template <int D>
 __device__ __forceinline__ QueryChunk query_load(const PagedDecodeArgs& a, int b, int g, int r, int c, int pos0) {
-  QueryChunk x;
-  x.on = r < a.R;
-  const int t = x.on ? (int)fdiv((uint32_t)r, a.div_g) : 0, gg = r - t * a.G;
-  x.v = make_uint4(0, 0, 0, 0);
-  if (x.on) x.v = load_rope_chunk<D>(a.q + (size_t)(b * a.Tq + t) * a.q_stride + (g * a.G + gg) * D, c, a.rope_half != 0);
-  rope_coeffs<D>(a.rope, max(pos0 + t, 0), c, x.c0, x.c1);
-  return x;
+  const bool on = r < a.R;
+  const int t = on ? (int)fdiv((uint32_t)r, a.div_g) : 0;
+  return query_load_at<D>(a, on, b, g, r, t, c, pos0 + t);
 }
 // Normalises with the weight chunk w (where norm is set) and rotates in fp32; hi is the fp16
 // rounding, lo that of the remainder.  The D / 8 lanes of a row are neighbours (every lane of
 // the warp takes part); rows past the last come out as zeros.
-template <int D>
-__device__ __forceinline__ void query_finish(const PagedDecodeArgs& a, const QueryChunk& q, bool norm, const uint4& wv,
+template <int D, class A>
+__device__ __forceinline__ void query_finish(const A& a, const QueryChunk& q, bool norm, const uint4& wv,
                                              uint4& hi, uint4& lo) {
   const uint32_t w[4] = {q.v.x, q.v.y, q.v.z, q.v.w};
   float x[8];
@@ -71,8 +77,8 @@ __device__ __forceinline__ void query_finish(const PagedDecodeArgs& a, const Que
 
 // Row r of (sequence b, head g), columns 4 q .. 4 q + 3: normalise and write. L is 0 for a row that saw no
 // key, and only then; a NaN stays one in o and lse.
-template <int D>
-__device__ __forceinline__ void write_row(const PagedDecodeArgs& a, int b, int g, int r, int q, float4 v, float M, float L) {
+template <int D, class A>
+__device__ __forceinline__ void write_row(const A& a, int b, int g, int r, int q, float4 v, float M, float L) {
   const int t = (int)fdiv((uint32_t)r, a.div_g), h = g * a.G + (r - t * a.G);
   const float inv = L == 0.f ? 0.f : 1.f / L;
   const size_t at = (((size_t)b * a.Tq + t) * a.Hq + h) * D + 4 * q;

@@ -172,6 +172,76 @@ struct Tiles {
   __device__ int first(const SweepPlan& p, int s0) const { return at(p, s0 + over + p.slack); }
   __device__ int last(const SweepPlan& p, int s0, int n) const { return at(p, s0 + over + n - 1 - p.slack); }
 };
+// cum[0 .. B]: the running sum of cost(b), by the block's THREADS threads (wsum: a word for each warp).
+template <int THREADS, class F>
+__device__ __forceinline__ void running_costs(int B, int* cum, int* wsum, int tid, F cost) {
+  const int warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) cum[0] = 0;
+  int before = 0;
+  for (int b0 = 0; b0 < B; b0 += THREADS) {
+    const int b = b0 + tid;
+    int x = b < B ? cost(b) : 0;
+    if (b0 + warp * 32 < B) {
+#pragma unroll
+      for (int m = 1; m < 32; m <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, m);
+        if (lane >= m) x += y;
+      }
+    }
+    if (lane == 31) wsum[warp] = x;
+    __syncthreads();
+    if (b0 + warp * 32 < B) {
+      int low = lane < warp ? wsum[lane] : 0;  // at most 12 warps
+#pragma unroll
+      for (int m = 16; m; m >>= 1) low += __shfl_xor_sync(0xffffffffu, low, m);
+      if (b < B) cum[b + 1] = before + low + x;
+    }
+    if (b0 + THREADS < B) {
+      for (int i = 0; i < THREADS / 32; i++) before += wsum[i];
+      __syncthreads();
+    }
+  }
+  __syncthreads();
+}
+// Block blk of nblk: its stretch and its first tile, into splan (slack: see SweepPlan; div(W, G) = W / G).
+// Two warps divide the work (a division costs every warp its issue slots): the block's first tile and
+// the next block's.
+template <class F>
+__device__ __forceinline__ void divide_work(const Tiles& tl, volatile SweepPlan* splan, int blk, int nblk, int slack,
+                                            int warp, int lane, F div) {
+  if (warp < 2) {
+    SweepPlan p;
+    p.W = tl.cum[tl.B] * tl.Hkv;
+    p.G = min(p.W, nblk);
+    p.base = p.W == p.G ? 1 : div(p.W, p.G);
+    p.rem = p.W - p.base * p.G;
+    const int c = blk + warp, x = c * p.base + min(c, p.rem);
+    const bool any = blk < p.G && x < p.W;
+    p.b = tl.find_warp(min(x, p.W - 1), lane);
+    p.slack = min(slack, p.base / 2);
+    p.w = any ? tl.moved(x, p.b, p.slack) : p.W;
+    if (lane == 0 && warp == 1) splan->end = p.w;
+    if (lane == 0 && warp == 0) {
+      if (p.w == tl.cum[p.b + 1] * tl.Hkv) p.b++;  // moved to the next sequence's first tile
+      if (p.b == tl.B) p.b--;                      // nothing left
+      const int n = tl.cum[p.b + 1] - tl.cum[p.b], off = p.w - tl.cum[p.b] * tl.Hkv;
+      p.g = (int)__fdividef((float)off, (float)n);  // within one of off / n
+      p.n0 = off - p.g * n;
+      while (p.n0 < 0) p.g--, p.n0 += n;
+      while (p.n0 >= n) p.g++, p.n0 -= n;
+      p.n0 = max(p.n0 - tl.over, 0);
+      splan->slack = p.slack;
+      splan->W = p.W;
+      splan->G = p.G;
+      splan->base = p.base;
+      splan->rem = p.rem;
+      splan->w = p.w;
+      splan->b = p.b;
+      splan->g = p.g;
+      splan->n0 = p.n0;
+    }
+  }
+}
 // Walks a block's stretch segment by segment.
 template <int OVER>
 struct SegWalk {
@@ -778,47 +848,18 @@ __global__ void __launch_bounds__(kSweepThreads, 1) k_paged_sweep(const __grid_c
   int* cum = reinterpret_cast<int*>(smem + kOffCum);
   int* len = cum + a.B + 1;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  int n_first = 0;
-  if (tid < a.B) n_first = a.len[tid];
-  if (tid == 0) cum[0] = 0;
   // lengths, and the running count of the tiles of the parts read here
   const int cap = a.max_pages << a.page_shift;
-  int before = 0;
-  for (int b0 = 0; b0 < a.B; b0 += kThreads) {
-    const int b = b0 + tid;
-    int nt = 0;
-    if (b < a.B) {
-      int n = b0 == 0 ? n_first : a.len[b];
-      if (n > cap) {
-        if (blockIdx.x == 0) record_page(a.status);
-        n = cap;
-      }
-      n = max(n, 0);
-      len[b] = n;
-      nt = seg_cost(D) + max(1, (n - sweep_base(a, n) + kTK - 1) / kTK);  // one even where nothing is read: its rows are written
+  running_costs<kThreads>(a.B, cum, wsum, tid, [&](int b) {
+    int n = a.len[b];
+    if (n > cap) {
+      if (blockIdx.x == 0) record_page(a.status);
+      n = cap;
     }
-    int x = nt;
-    if (b0 + warp * 32 < a.B) {
-#pragma unroll
-      for (int m = 1; m < 32; m <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, m);
-        if (lane >= m) x += y;
-      }
-    }
-    if (lane == 31) wsum[warp] = x;
-    __syncthreads();
-    if (b0 + warp * 32 < a.B) {
-      int low = lane < warp ? wsum[lane] : 0;  // at most 12 warps
-#pragma unroll
-      for (int m = 16; m; m >>= 1) low += __shfl_xor_sync(0xffffffffu, low, m);
-      if (b < a.B) cum[b + 1] = before + low + x;
-    }
-    if (b0 + kThreads < a.B) {
-      for (int i = 0; i < kThreads / 32; i++) before += wsum[i];
-      __syncthreads();
-    }
-  }
-  __syncthreads();
+    n = max(n, 0);
+    len[b] = n;
+    return seg_cost(D) + max(1, (n - sweep_base(a, n) + kTK - 1) / kTK);  // one even where nothing is read: its rows are written
+  });
   int blk = (int)blockIdx.x, nblk = (int)gridDim.x;
   if constexpr (PREFIX) {
     const int P = prefix_blocks(a, cum[a.B] * a.Hkv, nblk);
@@ -848,40 +889,8 @@ __global__ void __launch_bounds__(kSweepThreads, 1) k_paged_sweep(const __grid_c
   tl.Hkv = a.Hkv;
   tl.over = seg_cost(D);
   tl.whole = whole_tiles(D);
-  // two warps divide the work (a division costs every warp its issue slots): the block's first tile
-  // and the next block's
-  if (warp < 2) {
-    SweepPlan p;
-    p.W = cum[a.B] * a.Hkv;
-    p.G = min(p.W, nblk);
-    p.base = p.W == p.G ? 1 : (PREFIX ? p.W / p.G : (int)fdiv((uint32_t)p.W, a.div_grid));
-    p.rem = p.W - p.base * p.G;
-    const int c = blk + warp, x = c * p.base + min(c, p.rem);
-    const bool any = blk < p.G && x < p.W;
-    p.b = tl.find_warp(min(x, p.W - 1), lane);
-    p.slack = min(max_slack(D), p.base / 2);
-    p.w = any ? tl.moved(x, p.b, p.slack) : p.W;
-    if (lane == 0 && warp == 1) splan->end = p.w;
-    if (lane == 0 && warp == 0) {
-      if (p.w == cum[p.b + 1] * a.Hkv) p.b++;  // moved to the next sequence's first tile
-      if (p.b == a.B) p.b--;                   // nothing left
-      const int n = cum[p.b + 1] - cum[p.b], off = p.w - cum[p.b] * a.Hkv;
-      p.g = (int)__fdividef((float)off, (float)n);  // within one of off / n
-      p.n0 = off - p.g * n;
-      while (p.n0 < 0) p.g--, p.n0 += n;
-      while (p.n0 >= n) p.g++, p.n0 -= n;
-      p.n0 = max(p.n0 - tl.over, 0);
-      splan->slack = p.slack;
-      splan->W = p.W;
-      splan->G = p.G;
-      splan->base = p.base;
-      splan->rem = p.rem;
-      splan->w = p.w;
-      splan->b = p.b;
-      splan->g = p.g;
-      splan->n0 = p.n0;
-    }
-  }
+  divide_work(tl, splan, blk, nblk, max_slack(D), warp, lane,
+              [&](int W, int G) { return PREFIX ? W / G : (int)fdiv((uint32_t)W, a.div_grid); });
   __syncthreads();
   SegWalk<seg_cost(D)> sw;
   sw.init(tl, splan);

@@ -3,11 +3,20 @@
 // Sequence b has len[b] positions in the cache, the last nodes[b] of them a tree: token t hangs on token
 // parents[t] < t, or on the context (-1).  With ctx = len - nodes and depth the number of ancestors,
 //   q^_t = R_(ctx + depth(t)) q_t,   s_tj = q^_t . k^_j / sqrt(D)
-// for j < ctx and for the positions ctx + u of t's ancestors u and of t itself; o and lse as ever.
-#include "internal.h"
-#include "paged.cuh"
-#include "ptx.cuh"
-#include "rope.cuh"
+// for j < ctx and for the positions ctx + u of t's ancestors u and of t itself; o and lse as ever.  A token's
+// ancestors and itself are a mask of 64 bits.
+//
+// The R = Tq * G queries of a key/value head fill tiles of 128 rows (row t * G + g).  The key tiles of every
+// (sequence, head, pair of row tiles) lie in one line that is cut into one equal stretch for each block, as
+// in the sweep of the paged decode, and each tile is worked off on the tensor cores: S = Q K^T and O += P V with
+// TMEM accumulators, q as two fp16 parts and the weights as two bf16 parts (the paged decode's precision: a
+// tree's rows are the decode's of the accepted path).  A step is one key tile for one row tile; two groups
+// of four softmax warps take the steps in turn, each with an O of its own.  With up to 128 rows the groups share the row
+// tile and take alternate key tiles (their two O are added at the end), with more each has one of the pair's.
+// Up to 64 (32) rows are 2 (4) times in the tile and each copy takes 64 (32) of a tile's 128 keys: its weights of
+// the others are zeros, so that no warp idles and a thread's chain is that much shorter.
+// A segment that is not the whole of its (sequence, head) leaves its parts to k_tree_join.
+#include "paged_sweep.cuh"
 
 namespace ne {
 namespace {
@@ -31,98 +40,720 @@ __device__ __forceinline__ TreeShape tree_shape(const PagedTreeArgs& a, int b, b
   return x;
 }
 
-// A warp to a query row (sequence, token, head), its lanes on the positions in turn.
+constexpr int kTreeThreads = 384;
+// A segment's cost beside its tiles, in tiles; a (sequence, head) of at most so many tiles is never cut; a
+// boundary moves by so many to an end of a longer one.
+constexpr int kTreeOver = 2, kTreeWhole = 4, kTreeSlack = 2;
+
 template <int D>
-__global__ void __launch_bounds__(128) k_tree_rows(const PagedTreeArgs a) {
-  __shared__ float sq[4][D];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long row = blockIdx.x * 4LL + warp;
-  if (row >= (long long)a.B * a.Tq * a.Hq) return;
-  const int h = (int)(row % a.Hq), t = (int)(row / a.Hq % a.Tq), b = (int)(row / a.Hq / a.Tq), g = h / a.G;
-  const TreeShape x = tree_shape(a, b, lane == 0);
-  const int len = x.len, ctx = x.len - x.nodes;
-  const bool live = t < x.nodes;
-  unsigned long long mask = 0;
-  int depth = -1;
-  if (live) {
-    for (int x = t; x >= 0;) {
-      mask |= 1ull << x;
-      depth++;
-      int p = a.parents[b * a.parent_stride + x];
-      if (p < -1 || p >= x) {
-        record_tree(a.status);
-        p = -1;
+struct TreeCfg {
+  static constexpr int kTileBytes = kTile * D * 2;
+  static constexpr uint32_t kSpan = D * 2;
+  static constexpr uint32_t kSwz = D == 64 ? kSw128 : kSw64;
+  static constexpr uint32_t kSBO = 8 * kSpan;
+  static constexpr int kStages = D == 64 ? 4 : 8;
+  static constexpr int kOffK = 4 * kTileBytes;  // Q first: two slots of (high, low), or a pair's two row tiles
+  static constexpr int kOffV = kOffK + kStages * kTileBytes;
+  static constexpr int kBytes = kOffV + kStages * kTileBytes;
+  static constexpr uint32_t kColO = 0, kColS = 128;  // group g: O at 64 g; step n: S, then P, at 128 + 128 (n % 3)
+};
+// What the query warp knows of a segment's tree.
+struct TreeInfo {
+  unsigned long long mask[kTreeMax];  // a token and its ancestors
+  int ctx, nodes;
+};
+constexpr int kTreeVars = 384, kTreePlan = 392, kTreeSums = 448, kTreeInfo = 512, kTreeMl = 1664;
+constexpr int kTreeCum = kTreeMl + 4 * kTile * 8;
+static_assert(kTreeInfo + 2 * sizeof(TreeInfo) <= kTreeMl && kTreePlan + sizeof(SweepPlan) <= kTreeSums, "head");
+static_assert((4 + 2 * TreeCfg<32>::kStages + 4 + 4 + 3 + 4 + 2 + 2) * 8 <= kTreeVars, "barriers");
+__host__ __device__ constexpr int tree_head(int B) { return (kTreeCum + (2 * B + 1) * 4 + 1023) / 1024 * 1024; }
+
+// The tile's bits of a mask over positions that begins `r` positions before position 0 of the tree (r < 0: in the
+// context, all ones): 32 columns from there.
+__device__ __forceinline__ uint32_t tree_word(unsigned long long mask, int r) {
+  if (r <= -32) return 0xffffffffu;
+  if (r < 0) return (uint32_t)(mask << -r) | ((1u << -r) - 1u);
+  return r < 64 ? (uint32_t)(mask >> r) : 0u;
+}
+__device__ __forceinline__ unsigned long long shfl64(unsigned long long x, int lane) {
+  return ((unsigned long long)__shfl_sync(0xffffffffu, (uint32_t)(x >> 32), lane) << 32) |
+         __shfl_sync(0xffffffffu, (uint32_t)x, lane);
+}
+
+// Tokens lane and lane + 32 of a tree: masks of ancestors by doubling (after k rounds a token's mask holds itself and
+// 2^k - 1 ancestors, `up` the next one).
+__device__ __forceinline__ void tree_masks(const int* parents, int nodes, int lane, int* status,
+                                           unsigned long long (&mask)[2]) {
+  int up[2];
+#pragma unroll
+  for (int h = 0; h < 2; h++) {
+    const int t = lane + 32 * h;
+    mask[h] = t < nodes ? 1ull << t : 0ull;
+    up[h] = t < nodes ? parents[t] : -1;
+    if (up[h] < -1 || up[h] >= t) {
+      record_tree(status);
+      up[h] = -1;
+    }
+  }
+#pragma unroll 1
+  while (__any_sync(0xffffffffu, up[0] >= 0 || up[1] >= 0)) {
+    unsigned long long m[2];
+    int u[2];
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+      const int s = up[h] & 31;
+      const bool high = up[h] >= 32;
+      const unsigned long long m0 = shfl64(mask[0], s), m1 = shfl64(mask[1], s);
+      const int u0 = __shfl_sync(0xffffffffu, up[0], s), u1 = __shfl_sync(0xffffffffu, up[1], s);
+      m[h] = up[h] < 0 ? 0 : (high ? m1 : m0);
+      u[h] = up[h] < 0 ? -1 : (high ? u1 : u0);
+    }
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+      mask[h] |= m[h];
+      up[h] = u[h];
+    }
+  }
+}
+
+// Columns 32 c .. of row `to` (bf16 or fp32), scaled.
+template <int N>
+__device__ __forceinline__ void put_columns(const PagedTreeArgs& a, size_t to, const float (&v)[N], float inv, bool live) {
+  if (a.o_fp32) {
+    float4* p = reinterpret_cast<float4*>(static_cast<float*>(a.o) + to);
+#pragma unroll
+    for (int e = 0; e < N / 4; e++)
+      p[e] = live ? make_float4(v[4 * e] * inv, v[4 * e + 1] * inv, v[4 * e + 2] * inv, v[4 * e + 3] * inv)
+                  : make_float4(0.f, 0.f, 0.f, 0.f);
+  } else {
+    uint4* p = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.o) + to);
+#pragma unroll
+    for (int e = 0; e < N / 8; e++)
+      p[e] = live ? make_uint4(pack_bf16(v[8 * e] * inv, v[8 * e + 1] * inv), pack_bf16(v[8 * e + 2] * inv, v[8 * e + 3] * inv),
+                               pack_bf16(v[8 * e + 4] * inv, v[8 * e + 5] * inv), pack_bf16(v[8 * e + 6] * inv, v[8 * e + 7] * inv))
+                  : make_uint4(0u, 0u, 0u, 0u);
+  }
+}
+
+// RT: row tiles of a pair (2: more than 128 rows), F: copies of the rows in the one tile.
+template <int D, int RT, int F>
+__global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_constant__ PagedTreeArgs a) {
+  using C = TreeCfg<D>;
+  constexpr int S = C::kStages, TB = C::kTileBytes, NC = kTile / F;  // NC: keys of a tile, and rows, of a copy
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* head = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint64_t* q_full = reinterpret_cast<uint64_t*>(head);  // [2] the slot's queries are packed
+  uint64_t* q_empty = q_full + 2;          // [2] the slot's segment has left it
+  uint64_t* kv_full = q_empty + 2;         // [S]
+  uint64_t* kv_empty = kv_full + S;        // [S] the last O += P V of the stage has completed
+  uint64_t* s_full = kv_empty + S;         // [group][2] the group's steps in turn
+  uint64_t* p_ready = s_full + 4;          // [group][2]
+  uint64_t* pv_done = p_ready + 4;         // [3] per buffer of S and P
+  uint64_t* part_full = pv_done + 3;       // [group][2] the other group's part of a segment that this one finishes
+  uint64_t* gsync = part_full + 4;         // [group]
+  uint64_t* drain = gsync + 2;             // [2] per issuing thread
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(head + kTreeVars);
+  volatile int* abort = reinterpret_cast<volatile int*>(head + kTreeVars) + 1;
+  volatile SweepPlan* splan = reinterpret_cast<volatile SweepPlan*>(head + kTreePlan);
+  int* wsum = reinterpret_cast<int*>(head + kTreeSums);
+  TreeInfo* info = reinterpret_cast<TreeInfo*>(head + kTreeInfo);  // [2] per slot
+  float2* ml_other = reinterpret_cast<float2*>(head + kTreeMl);    // [2][128] per slot
+  float2* ml_own = ml_other + 2 * kTile;                           // [2][128] per group
+  int* cum = reinterpret_cast<int*>(head + kTreeCum);
+  int* len = cum + a.B + 1;
+  uint8_t* smem = head + tree_head(a.B);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, blk = (int)blockIdx.x;
+  if (tid == 0) {
+    *abort = 0;
+    for (int k = 0; k < 2; k++) {
+      mbar_init(q_full + k, 1);
+      mbar_init(q_empty + k, 4);
+      mbar_init(gsync + k, 4);
+      mbar_init(drain + k, 1);
+    }
+    for (int k = 0; k < S; k++) {
+      mbar_init(kv_full + k, 1);
+      mbar_init(kv_empty + k, 1);
+    }
+    for (int k = 0; k < 4; k++) {
+      mbar_init(s_full + k, 2);
+      mbar_init(p_ready + k, 4);
+      mbar_init(part_full + k, 4);
+    }
+    for (int k = 0; k < 3; k++) mbar_init(pv_done + k, 1);
+    fence_mbar_init();
+  }
+  if (warp == 1) tmem_alloc(tmem_slot, 512);
+  running_costs<kTreeThreads>(a.B, cum, wsum, tid, [&](int b) {
+    const TreeShape x = tree_shape(a, b, blk == 0);
+    len[b] = x.len;
+    return kTreeOver + max(1, (x.len + kTile - 1) / kTile);  // one even where nothing is read: its rows are written
+  });
+  Tiles tl;
+  tl.cum = cum;
+  tl.B = a.B;
+  tl.Hkv = a.Hkv * a.pairs;
+  tl.over = kTreeOver;
+  tl.whole = kTreeWhole;
+  divide_work(tl, splan, blk, (int)gridDim.x, kTreeSlack, warp, lane,
+              [&](int W, int) { return (int)fdiv((uint32_t)W, a.div_grid); });
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const volatile int never = 0;
+  SegWalk<kTreeOver> sw;
+  sw.init(tl, splan);
+  const auto units = [&](const SegWalk<kTreeOver>& x) {  // row tiles of the segment's pair
+    return RT == 1 ? 1 : (2 * (x.g % a.pairs) * kTile + kTile < a.R ? 2 : 1);
+  };
+  const auto slot_of = [](int e) { return RT == 1 ? e & 1 : 0; };
+  const auto use_of = [](int e) { return RT == 1 ? e >> 1 : e; };
+  // registers: 384 x 168 at launch; 128 x 104 + 256 x 200
+  if (warp < 4) regs_dec<104>();
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      prefetch_tmap(&a.map_pk);
+      prefetch_tmap(&a.map_pv);
+    }
+    const uint64_t policy = evict_first();
+    const int prows = min(1 << a.page_shift, kTile), per = kTile / prows;
+    const uint32_t pbytes = (uint32_t)prows * C::kSpan;
+    // Page numbers 32 at a time, one to a lane, a window ahead: num_pages (outside the pool, read as zeros)
+    // for a bad page and behind the last position.
+    const auto window = [&](const SegWalk<kTreeOver>& s, int w) {
+      const int i = w * 32 + lane;
+      int id = a.num_pages;
+      if ((i << a.page_shift) < len[s.b]) {
+        id = a.table[(size_t)s.b * a.max_pages + i];
+        if (id < 0 || id >= a.num_pages) {
+          record_page(a.status);
+          id = a.num_pages;
+        }
       }
-      x = p;
+      return id;
+    };
+    const auto page_of = [&](int n) { return (n * kTile) >> a.page_shift; };
+    SegWalk<kTreeOver> ls = sw;  // the segment of the next window
+    bool lon = ls.next();
+    int lw = 0, id = 0, nid = 0;
+    if (lon) {
+      lw = page_of(ls.n0) >> 5;
+      nid = window(ls, lw);
     }
-    // the rotated query
-    const __nv_bfloat16* q = a.q + (size_t)(b * a.Tq + t) * a.q_stride + (size_t)h * D;
-    for (int i = lane; i < D / 2; i += 32) {
-      const int i0 = a.rope_half ? i : 2 * i, i1 = a.rope_half ? i + D / 2 : 2 * i + 1;
-      float x0 = __bfloat162float(q[i0]), x1 = __bfloat162float(q[i1]);
-      if (a.qw) {
-        float ss = 0.f;
-        for (int d = 0; d < D; d++) ss = fmaf(__bfloat162float(q[d]), __bfloat162float(q[d]), ss);
-        const float r = rsqrtf(fmaf(ss, 1.f / D, a.eps));
-        x0 *= r * __bfloat162float(a.qw[i0]);
-        x1 *= r * __bfloat162float(a.qw[i1]);
+    const auto look = [&]() {
+      id = nid;
+      if (!lon) return;
+      if (lw < page_of(ls.n1 - 1) >> 5) {
+        lw++;
+      } else {
+        lon = ls.next();
+        if (lon) lw = page_of(ls.n0) >> 5;
       }
-      const float2 cs = a.rope[(size_t)(ctx + depth) * (D / 2) + i];
-      sq[warp][2 * i] = x0 * cs.x - x1 * cs.y;
-      sq[warp][2 * i + 1] = x0 * cs.y + x1 * cs.x;
+      if (lon) nid = window(ls, lw);
+    };
+    bool ok = true;
+    int k = 0;  // stages handed out so far
+    while (ok && sw.next()) {
+      const int kvh = sw.g / a.pairs;
+      int win = -1;
+#pragma unroll 1
+      for (int n = sw.n0; ok && n < sw.n1; n++, k++) {
+        const int first = page_of(n);
+        if ((first >> 5) != win) {
+          win = first >> 5;
+          look();
+        }
+        const int mine = __shfl_sync(0xffffffffu, id, (first & 31) + (lane < per ? lane : 0));
+        const int st = k % S, use = k / S;
+        if (use > 0) ok = __all_sync(0xffffffffu, mbar_wait(kv_empty + st, (use - 1) & 1, abort));
+        if (!ok) break;
+        if (lane == 0) mbar_arrive_expect_tx(kv_full + st, 2 * TB);
+        __syncwarp();
+        if (lane < per) {
+          const int off = (n * kTile) & ((1 << a.page_shift) - 1);
+          uint8_t *dk = smem + C::kOffK + st * TB + lane * pbytes, *dv = smem + C::kOffV + st * TB + lane * pbytes;
+          if (RT == 1 || a.pairs == 1) {
+            tma_load_4d(dk, &a.map_pk, kv_full + st, 0, off, kvh, mine, policy);
+            tma_load_4d(dv, &a.map_pv, kv_full + st, 0, off, kvh, mine, policy);
+          } else {  // the other pairs read it too
+            tma_load_4d(dk, &a.map_pk, kv_full + st, 0, off, kvh, mine);
+            tma_load_4d(dv, &a.map_pv, kv_full + st, 0, off, kvh, mine);
+          }
+        }
+      }
+    }
+    if (!ok && lane == 0) {
+      *abort = 1;
+      atomicExch(a.status, kStatusTimeout);
+    }
+    // let every copy issued above land before the block can exit
+    if (lane == 0) {
+      for (int x = k - S < 0 ? 0 : k - S; x < k; x++) mbar_wait(kv_full + x % S, (x / S) & 1, &never);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ S = Q K^T issuer
+    if (lane == 0) {
+      constexpr uint32_t idS = idesc_fp16(128, 128, false, false);
+      constexpr uint32_t kStepK = 32 >> 4, tstep = (uint32_t)TB >> 4;
+      const uint64_t dQ0 = smem_desc(smem_u32(smem), 16, C::kSBO, C::kSwz);
+      const uint64_t dK0 = smem_desc(smem_u32(smem + C::kOffK), 16, C::kSBO, C::kSwz);
+      bool ok = true;
+      int n = 0, k = 0, e = 0;  // steps, stages, segments
+      while (ok && sw.next()) {
+        const int nu = units(sw), slot = slot_of(e);
+        if (!(ok = mbar_wait(q_full + slot, use_of(e) & 1, abort))) break;
+#pragma unroll 1
+        for (int i = sw.n0; ok && i < sw.n1; i++, k++) {
+          const int st = k % S;
+          if (!(ok = mbar_wait(kv_full + st, (k / S) & 1, abort))) break;
+#pragma unroll 1
+          for (int u = 0; u < nu; u++, n++) {
+            const int buf = n % 3, use = n / 3;
+            if (use > 0 && !(ok = mbar_wait(pv_done + buf, (use - 1) & 1, abort))) break;
+            tc_fence_after();
+            const uint64_t dq = dQ0 + (uint64_t)((RT == 1 ? 2 * slot : 2 * u) * tstep), dk = dK0 + (uint64_t)(st * tstep);
+            const uint32_t to = tmem + C::kColS + 128u * buf;
+            mma_ss_chain<D / 16>(to, dq, kStepK, dk, kStepK, idS, 0u);
+            mma_ss_chain<D / 16>(to, dq + (uint64_t)tstep, kStepK, dk, kStepK, idS, 1u);
+            uint64_t* full = s_full + 2 * (n & 1) + ((n >> 1) & 1);
+            mma_commit(full);
+            mbar_arrive(full);  // what this thread has seen (the tree of the slot) comes with it
+          }
+        }
+        e++;
+      }
+      if (!ok) {
+        *abort = 1;
+        atomicExch(a.status, kStatusTimeout);
+      }
+      mma_commit(drain);
+      mbar_wait(drain, 0, &never);
+    }
+  } else if (warp == 2) {
+    // ------------------------------------------------------------ O += P V issuer
+    if (lane == 0) {
+      constexpr uint32_t idPV = idesc_bf16(128, D, false, true);
+      constexpr uint32_t kStepMN = (16 * C::kSpan) >> 4, tstep = (uint32_t)TB >> 4;
+      const uint64_t dV0 = smem_desc(smem_u32(smem + C::kOffV), 16, C::kSBO, C::kSwz);
+      bool ok = true;
+      int n = 0, k = 0;
+      while (ok && sw.next()) {
+        const int nu = units(sw), first = n;
+#pragma unroll 1
+        for (int i = sw.n0; ok && i < sw.n1; i++, k++) {
+          const int st = k % S;
+#pragma unroll 1
+          for (int u = 0; u < nu; u++, n++) {
+            const int buf = n % 3;
+            // the group has also read the O of its last segment before it arrives for this one
+            if (!(ok = mbar_wait(p_ready + 2 * (n & 1) + ((n >> 1) & 1), (n >> 2) & 1, abort))) break;
+            tc_fence_after();
+            const uint64_t dv = dV0 + (uint64_t)(st * tstep);
+            const uint32_t o = tmem + C::kColO + 64u * (n & 1), p = tmem + C::kColS + 128u * buf;
+            mma_ts_chain<4, false>(o, p, dv, kStepMN, idPV, n - first >= 2 ? 1u : 0u);
+            mma_ts_chain<4, false>(o, p + 32u, dv + (uint64_t)(4 * kStepMN), kStepMN, idPV, 1u);
+            mma_ts_chain<4, false>(o, p + 64u, dv, kStepMN, idPV, 1u);
+            mma_ts_chain<4, false>(o, p + 96u, dv + (uint64_t)(4 * kStepMN), kStepMN, idPV, 1u);
+            mma_commit(pv_done + buf);
+          }
+          if (ok) mma_commit(kv_empty + st);  // V by these products, K by their scores, complete before
+        }
+      }
+      if (!ok) {
+        *abort = 1;
+        atomicExch(a.status, kStatusTimeout);
+      }
+      mma_commit(drain + 1);
+      mbar_wait(drain + 1, 0, &never);
+    }
+  } else if (warp == 3) {
+    // ------------------------------------------------------------ queries and trees, two segments ahead
+    constexpr int kCPR = D / 8, kRows = 32 / kCPR, kBatch = 4;
+    const int c = lane % kCPR;
+    uint4 wv = make_uint4(0, 0, 0, 0);
+    if (a.qw) wv = load_rope_chunk<D>(a.qw, c, a.rope_half != 0);
+    bool ok = true;
+    int4 cut = make_int4(-1, 0, 0, 0);
+    for (int e = 0; ok && sw.next(); e++) {
+      const int slot = slot_of(e), use = use_of(e), pr = sw.g % a.pairs, g = sw.g / a.pairs;
+      if (sw.n0 == 0 && sw.n1 < sw.nt) {
+        SweepPlan p;
+        p.base = splan->base;
+        p.rem = splan->rem;
+        p.slack = splan->slack;
+        cut = make_int4(sw.b, sw.g, tl.last(p, cum[sw.b] * tl.Hkv + sw.g * (sw.nt + tl.over), sw.nt), 0);
+      }
+      if (use > 0) ok = __all_sync(0xffffffffu, mbar_wait(q_empty + slot, (use - 1) & 1, abort));
+      if (!ok) break;
+      const int total = len[sw.b], nodes = total > 0 ? (a.nodes ? a.nodes[sw.b] : a.Tq) : 0, ctx = total - nodes;
+      unsigned long long mask[2];
+      tree_masks(a.parents + sw.b * a.parent_stride, nodes, lane, a.status, mask);
+      const int depth[2] = {__popcll(mask[0]) - 1, __popcll(mask[1]) - 1};
+      info[slot].mask[lane] = mask[0];
+      info[slot].mask[lane + 32] = mask[1];
+      if (lane == 0) {
+        info[slot].ctx = ctx;
+        info[slot].nodes = nodes;
+      }
+      uint8_t* q = smem + (RT == 1 ? 2 * slot : 0) * TB;
+      const int rows = RT == 1 ? NC : units(sw) * kTile;
+#pragma unroll 1
+      for (int r0 = 0; r0 < rows; r0 += kBatch * kRows) {
+        QueryChunk x[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; i++) {
+          const int r = pr * 2 * kTile + r0 + i * kRows + lane / kCPR;
+          const int t = r < a.R ? (int)fdiv((uint32_t)r, a.div_g) : 0;
+          const int d0 = __shfl_sync(0xffffffffu, depth[0], t & 31), d1 = __shfl_sync(0xffffffffu, depth[1], t & 31);
+          x[i] = query_load_at<D>(a, r < a.R && t < nodes, sw.b, g, r, t, c, ctx + (t < 32 ? d0 : d1));
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; i++) {
+          const int r = r0 + i * kRows + lane / kCPR;
+          uint4 hi, lo;
+          query_finish<D>(a, x[i], a.qw != nullptr, wv, hi, lo);
+          if (r < rows) {
+            uint8_t* to = q + (RT == 1 ? 0 : (r / kTile) * 2 * TB);
+#pragma unroll
+            for (int f = 0; f < F; f++) {
+              const uint32_t at = swz(r % kTile + f * NC, c, C::kSpan);
+              *reinterpret_cast<uint4*>(to + at) = hi;
+              *reinterpret_cast<uint4*>(to + TB + at) = lo;
+            }
+          }
+        }
+      }
+      fence_proxy_async_smem();
+      warp_arrive(q_full + slot);
+    }
+    if (lane == 0) a.cut[blk] = cut;
+    if (!ok && lane == 0) {
+      *abort = 1;
+      atomicExch(a.status, kStatusTimeout);
+    }
+  } else {
+    // ------------------------------------------------------------ softmax group
+    regs_inc<200>();
+    const int grp = (warp - 4) >> 2, q4 = warp & 3;
+    const int r = q4 * 32 + lane, f = r / NC, rr = r - f * NC;  // row of the tile: copy f of row rr
+    const uint32_t trow = tmem + ((uint32_t)(q4 * 32) << 16);
+    const uint32_t obuf = trow + C::kColO + 64u * grp;
+    const float sl2 = a.scale_log2;
+    bool ok = true;
+    int n = 0, kt = 0, joined0 = 0, joined1 = 0, syncs = 0;  // steps, stages; segments that each group finished with the other; group barriers
+    const auto group_sync = [&]() {
+      warp_arrive(gsync + grp);
+      return __all_sync(0xffffffffu, mbar_wait(gsync + grp, syncs++ & 1, abort));
+    };
+    for (int e = 0; ok && sw.next(); e++) {
+      const int nu = units(sw), slot = slot_of(e), first = n, end = first + (sw.n1 - sw.n0) * nu;
+      const int mine = first + ((first ^ grp) & 1);           // this group's first step
+      const bool joint = nu == 1 && end - first >= 2;         // both groups have a part of the same rows
+      const int last = (end - 1) & 1;                         // the group of the last step
+      const int k0 = kt;
+      n = end;
+      kt += sw.n1 - sw.n0;
+      const int turn = last ? joined1 : joined0;
+      if (joint) last ? joined1++ : joined0++;
+      if (mine >= end) continue;
+      const int total = len[sw.b], pr = sw.g % a.pairs, u = nu == 2 ? (mine - first) & 1 : 0;
+      const int row = pr * 2 * kTile + u * kTile + rr;        // row of the (sequence, head)
+      unsigned long long mask = 0;
+      int ctx = 0;
+      bool live = false;
+      float r_run = 0.f, l_run = 0.f, m_use = 0.f;
+      int s = mine;
+      for (; s < end; s += 2) {
+        const int buf = s % 3, tile = sw.n0 + (nu == 2 ? (s - first) >> 1 : s - first);
+        const uint32_t sbuf = trow + C::kColS + 128u * buf;
+        ok = __all_sync(0xffffffffu, mbar_wait(s_full + 2 * grp + ((s >> 1) & 1), (s >> 2) & 1, abort));
+        if (!ok) break;
+        tc_fence_after();
+        if (s == mine) {
+          ctx = info[slot].ctx;
+          const int t = row < a.R ? (int)fdiv((uint32_t)row, a.div_g) : kTreeMax;
+          live = t < info[slot].nodes;
+          if (live) mask = info[slot].mask[t];
+        }
+        uint32_t sc[NC];
+#pragma unroll
+        for (int c = 0; c < NC / 32; c++) tmem_ld32(sbuf + f * NC + c * 32, *reinterpret_cast<uint32_t(*)[32]>(sc + 32 * c));
+        tmem_wait_ld();
+        if (F > 1) {
+          // the weights of the keys that other copies take
+          const uint32_t z[16] = {0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+          for (int c = 0; c < 4; c++)
+            if (c / (4 / F) != f) {
+              tmem_st16(sbuf + 16 * c, z);
+              tmem_st16(sbuf + 64 + 16 * c, z);
+            }
+        }
+        if ((tile + 1) * kTile > ctx) {  // the tile ends in the tree or behind it
+#pragma unroll
+          for (int c = 0; c < NC / 32; c++) {
+            const uint32_t see = tree_word(mask, tile * kTile + f * NC + c * 32 - ctx);
+#pragma unroll
+            for (int x = 0; x < 32; x++)
+              if (!(see & (1u << x))) sc[32 * c + x] = 0xff800000u;
+          }
+          // what lies behind the last position may be anything: its weight is 0, but 0 times a NaN is not
+          if (u == 0 && r >= total - tile * kTile) {
+            uint4* v = reinterpret_cast<uint4*>(smem + C::kOffV + (k0 + tile - sw.n0) % S * TB + r * C::kSpan);
+#pragma unroll
+            for (int c = 0; c < D / 8; c++) v[c] = make_uint4(0u, 0u, 0u, 0u);
+            fence_proxy_async_smem();
+          }
+        }
+        float mx8[8];
+#pragma unroll
+        for (int x = 0; x < 8; x++) mx8[x] = -INFINITY;
+#pragma unroll
+        for (int x = 0; x < NC; x += 2)
+          mx8[(x >> 1) & 7] = fmax3(mx8[(x >> 1) & 7], __uint_as_float(sc[x]), __uint_as_float(sc[x + 1]));
+        const float mxr = fmaxf(fmaxf(fmaxf(mx8[0], mx8[1]), fmaxf(mx8[2], mx8[3])),
+                                fmaxf(fmaxf(mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])));
+        float r_use = mxr, alpha = 1.f;
+        if (s > mine) {
+          r_use = r_run;
+          const float r_new = fmaxf(r_run, mxr), m_old = __fmul_rn(r_run, sl2), m_new = __fmul_rn(r_new, sl2);
+          // O and the sum follow the maximum only when some row's grew by more than 2^8 (or came out of nothing)
+          if (__any_sync(0xffffffffu, m_new > m_old + 8.0f)) {
+            ok = __all_sync(0xffffffffu, mbar_wait(pv_done + (s - 2) % 3, ((s - 2) / 3) & 1, abort));
+            if (!ok) break;
+            tc_fence_after();
+            r_use = r_new;
+            alpha = r_run == -INFINITY ? 0.f : ex2(m_old - m_new);
+            uint32_t w[32];
+#pragma unroll
+            for (int c = 0; c < D / 32; c++) {
+              tmem_ld32(obuf + c * 32, w);
+              tmem_wait_ld();
+#pragma unroll
+              for (int x = 0; x < 32; x++) w[x] = __float_as_uint(__uint_as_float(w[x]) * alpha);
+              tmem_st32(obuf + c * 32, w);
+            }
+          }
+        }
+        r_run = r_use;
+        m_use = r_use == -INFINITY ? 0.f : __fmul_rn(r_use, sl2);
+        uint64_t sum4[4] = {0ull, 0ull, 0ull, 0ull};
+        const uint64_t sl2x2 = f2(sl2, sl2), negm = f2(-m_use, -m_use), minus = f2(-1.f, -1.f);
+#pragma unroll
+        for (int c = 0; c < NC / 16; c++) {
+          uint32_t ph[8], pl[8];
+#pragma unroll
+          for (int x = 0; x < 8; x++) {
+            const int k = 16 * c + 2 * x;
+            float x0, x1, l0, l1;
+            f2_split(f2_fma(f2(__uint_as_float(sc[k]), __uint_as_float(sc[k + 1])), sl2x2, negm), x0, x1);
+            const uint64_t pp = f2(ex2(x0), ex2(x1));
+            f2_split(pp, x0, x1);
+            ph[x] = pack_bf16(x0, x1);
+            f2_split(f2_fma(f2(bf_lo(ph[x]), bf_hi(ph[x])), minus, pp), l0, l1);
+            pl[x] = pack_bf16(l0, l1);
+            sum4[x & 3] = f2_add(sum4[x & 3], pp);
+          }
+          tmem_st8(sbuf + f * (NC / 2) + 8 * c, ph);
+          tmem_st8(sbuf + 64 + f * (NC / 2) + 8 * c, pl);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        warp_arrive(p_ready + 2 * grp + ((s >> 1) & 1));
+        float s0, s1, s2, s3, s4, s5, s6, s7;
+        f2_split(sum4[0], s0, s1);
+        f2_split(sum4[1], s2, s3);
+        f2_split(sum4[2], s4, s5);
+        f2_split(sum4[3], s6, s7);
+        const float l = ((s0 + s1) + (s2 + s3)) + ((s4 + s5) + (s6 + s7));
+        l_run = s > mine ? fmaf(l_run, alpha, l) : l;
+      }
+      if (!ok) break;
+      // the segment's unnormalised O, maximum (log2 units) and sum
+      ok = __all_sync(0xffffffffu, mbar_wait(pv_done + (s - 2) % 3, ((s - 2) / 3) & 1, abort));
+      if (!ok) break;
+      tc_fence_after();
+      float4* scratch = reinterpret_cast<float4*>(smem + 2 * slot * TB) + r * (D / 4);  // the slot's queries are no longer needed
+      const auto chunk = [&](int q) { return q ^ (r & 7); };
+      if (joint && grp != last) {
+        ok = __all_sync(0xffffffffu, mbar_wait(s_full + 2 * last + (((end - 1) >> 1) & 1), ((end - 1) >> 2) & 1, abort));
+        if (!ok) break;
+#pragma unroll
+        for (int c = 0; c < D / 32; c++) {
+          uint32_t w[32];
+          tmem_ld32(obuf + c * 32, w);
+          tmem_wait_ld();
+#pragma unroll
+          for (int q = 0; q < 8; q++)
+            scratch[chunk(c * 8 + q)] = make_float4(__uint_as_float(w[4 * q]), __uint_as_float(w[4 * q + 1]),
+                                                    __uint_as_float(w[4 * q + 2]), __uint_as_float(w[4 * q + 3]));
+        }
+        ml_other[slot * kTile + r] = make_float2(m_use, l_run);
+        tc_fence_before();
+        warp_arrive(part_full + 2 * last + (turn & 1));
+        continue;
+      }
+      const bool whole = sw.n0 == 0 && sw.n1 == sw.nt;
+      const size_t part = (size_t)(2 * blk + (sw.n0 > 0 ? 0 : 1)) * a.rows;
+      const int g = sw.g / a.pairs;
+      float M = m_use, L = l_run, mine_f = 1.f, other_f = 0.f;
+      if (joint) {
+        ok = __all_sync(0xffffffffu, mbar_wait(part_full + 2 * grp + (turn & 1), (turn >> 1) & 1, abort));
+        if (!ok) break;
+        const float2 z = ml_other[slot * kTile + r];
+        M = L == 0.f ? z.x : (z.y == 0.f ? M : fmaxf(M, z.x));
+        mine_f = L == 0.f ? 0.f : ex2(m_use - M);
+        other_f = z.y == 0.f ? 0.f : ex2(z.x - M);
+        L = fmaf(L, mine_f, z.y * other_f);
+      }
+#pragma unroll
+      for (int c = 0; c < D / 32; c++) {
+        uint32_t w[32];
+        float v[32];
+        tmem_ld32(obuf + c * 32, w);
+        tmem_wait_ld();
+#pragma unroll
+        for (int q = 0; q < 8; q++) {
+          float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (joint) y = scratch[chunk(c * 8 + q)];
+          v[4 * q] = fmaf(__uint_as_float(w[4 * q]), mine_f, y.x * other_f);
+          v[4 * q + 1] = fmaf(__uint_as_float(w[4 * q + 1]), mine_f, y.y * other_f);
+          v[4 * q + 2] = fmaf(__uint_as_float(w[4 * q + 2]), mine_f, y.z * other_f);
+          v[4 * q + 3] = fmaf(__uint_as_float(w[4 * q + 3]), mine_f, y.w * other_f);
+        }
+        if (F > 1) {
+#pragma unroll
+          for (int q = 0; q < 8; q++)
+            scratch[chunk(c * 8 + q)] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+        } else if (row < a.R) {
+          if (whole) {
+            const int t = (int)fdiv((uint32_t)row, a.div_g), h = g * a.G + (row - t * a.G);
+            put_columns(a, (((size_t)sw.b * a.Tq + t) * a.Hq + h) * D + c * 32, v, 1.f / L, live);
+          } else {
+            float4* to = reinterpret_cast<float4*>(a.part_o + (part + row - pr * 2 * kTile) * D) + c * 8;
+#pragma unroll
+            for (int q = 0; q < 8; q++) to[q] = live ? make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]) : make_float4(0.f, 0.f, 0.f, 0.f);
+          }
+        }
+      }
+      tc_fence_before();
+      if (F > 1) {
+        // the copies of a row: a thread takes four of its columns
+        ml_own[grp * kTile + r] = make_float2(M, L);
+        if (!(ok = group_sync())) break;
+        const float4* all = reinterpret_cast<const float4*>(smem + 2 * slot * TB);
+        for (int i = r; i < a.R * (D / 4); i += kTile) {
+          const int ro = i / (D / 4), q = i % (D / 4), t = (int)fdiv((uint32_t)ro, a.div_g);
+          RowSum x;
+#pragma unroll
+          for (int y = 0; y < F; y++) {
+            const float2 z = ml_own[grp * kTile + ro + y * NC];
+            if (z.y != 0.f) x.M = fmaxf(x.M, z.x);
+          }
+#pragma unroll
+          for (int y = 0; y < F; y++) {
+            const int at = ro + y * NC;
+            x.add(x.M, ml_own[grp * kTile + at], all[at * (D / 4) + (q ^ (at & 7))]);
+          }
+          if (t >= info[slot].nodes) x.S = 0.f, x.v = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (whole) {
+            write_row<D>(a, sw.b, g, ro, q, x.v, x.M, x.S);
+          } else {
+            reinterpret_cast<float4*>(a.part_o + (part + ro) * D)[q] = x.v;
+            if (q == 0) a.part_ml[part + ro] = make_float2(x.M, x.S);
+          }
+        }
+      } else if (row < a.R) {
+        if (!whole)
+          a.part_ml[part + row - pr * 2 * kTile] = make_float2(M, live ? L : 0.f);
+        else if (a.lse) {
+          const int t = (int)fdiv((uint32_t)row, a.div_g), h = g * a.G + (row - t * a.G);
+          a.lse[((size_t)sw.b * a.Hq + h) * a.Tq + t] = live ? (M + log2f(L)) * kPagedLn2 : -INFINITY;
+        }
+      }
+      if (grp == last) warp_arrive(q_empty + slot);
+    }
+    if (!ok) {
+      *abort = 1;
+      atomicExch(a.status, kStatusTimeout);
     }
   }
-  __syncwarp();
-  float m = -INFINITY, l = 0.f, o[D];
-#pragma unroll
-  for (int d = 0; d < D; d++) o[d] = 0.f;
-  for (int j = lane; j < (live ? len : 0); j += 32) {
-    if (j >= ctx && !((mask >> (j - ctx)) & 1)) continue;
-    const int page = a.table[(size_t)b * a.max_pages + (j >> a.page_shift)];
-    const bool there = page >= 0 && page < a.num_pages;
-    if (!there) record_page(a.status);
-    const size_t at = (size_t)(there ? page : 0) * a.page_stride + (((size_t)g << a.page_shift) + (j & ((1 << a.page_shift) - 1))) * D;
-    float s = 0.f;
-    if (there) {
-#pragma unroll
-      for (int d = 0; d < D; d++) s = fmaf(sq[warp][d], __half2float(a.kp[at + d]), s);
-    }
-    s *= a.scale_log2;
-    const float top = fmaxf(m, s), f = m == -INFINITY ? 0.f : ex2(m - top), p = ex2(s - top);
-    m = top;
-    l = fmaf(l, f, p);
-#pragma unroll
-    for (int d = 0; d < D; d++) o[d] = fmaf(o[d], f, there ? p * __bfloat162float(a.vp[at + d]) : 0.f);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) {
+    tmem_relinquish();
+    tmem_dealloc(tmem, 512);
   }
-  float top = m;
-  for (int x = 16; x; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-  const float f = m == -INFINITY && l == 0.f ? 0.f : ex2(m - top);
-  l *= f;
-  for (int x = 16; x; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  const size_t to = (size_t)row * D;
+}
+
+// The cut (sequence, head)s: block c has the one that begins in the sweep's block c, a thread four columns of a
+// row, its parts in order.
+template <int D>
+__global__ void __launch_bounds__(128) k_tree_join(const __grid_constant__ PagedTreeArgs a) {
+  pdl_wait();
+  const int c0 = blockIdx.x, q = threadIdx.x % (D / 4), row = blockIdx.y * (512 / D) + threadIdx.x / (D / 4);
+  const int4 cut = a.cut[c0];
+  if (cut.x < 0) return;
+  const int g = cut.y / a.pairs, r0 = cut.y % a.pairs * 2 * kTile;
+  if (row >= a.rows || r0 + row >= a.R) return;
+  constexpr int kAhead = 8;
+  RowSum x;
+  for (int c = c0; c <= cut.z; c += kAhead) {
+    float2 z[kAhead];
+    float4 v[kAhead];
 #pragma unroll
-  for (int d = 0; d < D; d++) {
-    float v = o[d] * f;
-    for (int x = 16; x; x >>= 1) v += __shfl_xor_sync(0xffffffffu, v, x);
-    if (lane == (d & 31)) {
-      if (a.o_fp32) static_cast<float*>(a.o)[to + d] = v * inv;
-      else static_cast<__nv_bfloat16*>(a.o)[to + d] = __float2bfloat16(v * inv);
+    for (int e = 0; e < kAhead; e++) {
+      const size_t at = (size_t)(2 * min(c + e, cut.z) + (c + e == c0 ? 1 : 0)) * a.rows + row;
+      z[e] = __ldcg(a.part_ml + at);
+      v[e] = __ldcg(reinterpret_cast<const float4*>(a.part_o + at * D) + q);
+      if (c + e > cut.z) z[e].y = 0.f;
     }
+    float top = x.M;
+#pragma unroll
+    for (int e = 0; e < kAhead; e++)
+      if (z[e].y != 0.f) top = fmaxf(top, z[e].x);
+    x.raise(top);
+#pragma unroll
+    for (int e = 0; e < kAhead; e++)
+      if (z[e].y != 0.f) x.add(top, z[e], v[e]);
   }
-  if (lane == 0 && a.lse) a.lse[((size_t)b * a.Hq + h) * a.Tq + t] = l == 0.f ? -INFINITY : (top + log2f(l)) * kPagedLn2;
+  write_row<D>(a, cut.x, g, r0 + row, q, x.v, x.M, x.S);
+}
+
+template <int D, int RT, int F>
+cudaError_t launch_tree_t(const PagedTreeArgs& a, int grid, cudaStream_t s) {
+  static bool attr_set[64] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!attr_set[dev]) {
+    const cudaError_t e = cudaFuncSetAttribute(k_tree_sweep<D, RT, F>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
+    if (e != cudaSuccess) return e;
+    attr_set[dev] = true;
+  }
+  const int bytes = tree_head(a.B) + TreeCfg<D>::kBytes + 1024;
+  if (bytes > kSmemMax) return cudaErrorInvalidValue;
+  k_tree_sweep<D, RT, F><<<grid, kTreeThreads, (size_t)bytes, s>>>(a);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  return launch_pdl(k_tree_join<D>, dim3((unsigned)grid, (unsigned)((a.rows + 512 / D - 1) / (512 / D))), 128, 0, s, a);
+}
+template <int D>
+cudaError_t launch_tree(const PagedTreeArgs& a, int grid, cudaStream_t s) {
+  if (a.R > kTile) return launch_tree_t<D, 2, 1>(a, grid, s);
+  if (a.R > 64) return launch_tree_t<D, 1, 1>(a, grid, s);
+  return a.R > 32 ? launch_tree_t<D, 1, 2>(a, grid, s) : launch_tree_t<D, 1, 4>(a, grid, s);
 }
 
 }  // namespace
 
-cudaError_t launch_decode_tree(const PagedTreeArgs& a, cudaStream_t s) {
-  const long long rows = (long long)a.B * a.Tq * a.Hq;
-  const unsigned grid = (unsigned)((rows + 3) / 4);
-  if (a.D == 64)
-    k_tree_rows<64><<<grid, 128, 0, s>>>(a);
-  else
-    k_tree_rows<32><<<grid, 128, 0, s>>>(a);
-  return cudaGetLastError();
+cudaError_t launch_decode_tree(const PagedTreeArgs& a, int nsm, cudaStream_t s) {
+  PagedTreeArgs b = a;
+  const int grid = nsm < kPagedMaxBlocks ? nsm : kPagedMaxBlocks;
+  b.div_grid = make_fastdiv((uint32_t)grid);
+  return b.D == 64 ? launch_tree<64>(b, grid, s) : launch_tree<32>(b, grid, s);
 }
 
 }  // namespace ne
