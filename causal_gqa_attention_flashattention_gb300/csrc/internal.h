@@ -250,8 +250,14 @@ struct PagedKeepArgs {
 
 
 // Attention of a drafted tree over a paged cache (see paged_tree.cu).
+struct TreeInfo {               // a sequence's tree
+  unsigned long long mask[kTreeMax];  // a token and its ancestors
+  int ctx, nodes, pad[2];
+};
 struct PagedTreeArgs {
   CUtensorMap map_pk, map_pv;   // pools {D, page, Hkv, num_pages}, box D x min(page, 128) rows
+  unsigned char* packed;        // [B, Hkv, tiles] queries as fp16 high and low parts, laid out as in shared memory (workspace)
+  TreeInfo* info;               // [B] (workspace)
   const __nv_bfloat16 *q, *qw;  // [B, Tq, Hq, D], positions q_stride values apart; qw [D] or null
   const int *table, *len;       // [B, max_pages], [B]
   const int *parents, *nodes;   // [B, Tq] rows parent_stride apart; [B] or null (all Tq)
@@ -265,11 +271,15 @@ struct PagedTreeArgs {
                                 // head, last block (workspace)
   long long q_stride, parent_stride;
   int B, Tq, Hq, Hkv, D, G, R, page_shift, num_pages, max_pages, rope_half, o_fp32;
-  int pairs, rows;              // pairs of 128-row tiles of a head's queries; rows of the largest
+  int tiles, pairs, rows;       // 128-row tiles of a head's queries, pairs of them, rows of the largest pair
   FastDiv div_g, div_grid;      // by G and the sweep's blocks
   float eps, scale_log2;
 };
-inline int tree_pairs(int R) { return (R + 2 * kTile - 1) / (2 * kTile); }
+inline int tree_tiles(int R) { return (R + kTile - 1) / kTile; }
+inline int tree_pairs(int R) { return (tree_tiles(R) + 1) / 2; }
+// Times that up to 64 rows are in their tile: each as the one that takes its weights' high parts and the one that
+// takes the low parts, up to 32 rows for each half of the keys.
+inline int tree_copies(int R) { return R > 64 ? 1 : (R > 32 ? 2 : 4); }
 
 // Attention of the newest tokens over a paged cache (see paged.cu).
 constexpr int kPagedMaxBlocks = 160;  // blocks of the sweep: bounds its partial results

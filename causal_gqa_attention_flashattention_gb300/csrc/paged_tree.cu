@@ -13,8 +13,12 @@
 // tree's rows are the decode's of the accepted path).  A step is one key tile for one row tile; two groups
 // of four softmax warps take the steps in turn, each with an O of its own.  With up to 128 rows the groups share the row
 // tile and take alternate key tiles (their two O are added at the end), with more each has one of the pair's.
-// Up to 64 (32) rows are 2 (4) times in the tile and each copy takes 64 (32) of a tile's 128 keys: its weights of
-// the others are zeros, so that no warp idles and a thread's chain is that much shorter.
+// A product of 128 rows and 64 columns takes the tensor cores as long as one of 128 columns (64 clocks for 16 keys), so
+// the two parts of the weights cost as much again as the two of the scores. Up to 64 rows are therefore twice in
+// their tile: the first copy's lanes hold the weights' high parts, the second's the low parts, and one product takes
+// both. Up to 32 rows are there four times, a pair of copies for each half of the tile's keys (its weights of the
+// other half are zeros), so that a thread has 64 scores and not 128.
+// k_tree_prep packs the queries (normalised, rotated, two parts, laid out as the sweep has them in shared memory) and the trees.
 // A segment that is not the whole of its (sequence, head) leaves its parts to k_tree_join.
 #include "paged_sweep.cuh"
 
@@ -57,12 +61,8 @@ struct TreeCfg {
   static constexpr int kBytes = kOffV + kStages * kTileBytes;
   static constexpr uint32_t kColO = 0, kColS = 128;  // group g: O at 64 g; step n: S, then P, at 128 + 128 (n % 3)
 };
-// What the query warp knows of a segment's tree.
-struct TreeInfo {
-  unsigned long long mask[kTreeMax];  // a token and its ancestors
-  int ctx, nodes;
-};
 constexpr int kTreeVars = 384, kTreePlan = 392, kTreeSums = 448, kTreeInfo = 512, kTreeMl = 1664;
+static_assert(sizeof(TreeInfo) % 16 == 0, "copied in one piece");
 constexpr int kTreeCum = kTreeMl + 4 * kTile * 8;
 static_assert(kTreeInfo + 2 * sizeof(TreeInfo) <= kTreeMl && kTreePlan + sizeof(SweepPlan) <= kTreeSums, "head");
 static_assert((4 + 2 * TreeCfg<32>::kStages + 4 + 4 + 3 + 4 + 2 + 2) * 8 <= kTreeVars, "barriers");
@@ -91,7 +91,7 @@ __device__ __forceinline__ void tree_masks(const int* parents, int nodes, int la
     mask[h] = t < nodes ? 1ull << t : 0ull;
     up[h] = t < nodes ? parents[t] : -1;
     if (up[h] < -1 || up[h] >= t) {
-      record_tree(status);
+      if (status) record_tree(status);
       up[h] = -1;
     }
   }
@@ -116,7 +116,47 @@ __device__ __forceinline__ void tree_masks(const int* parents, int nodes, int la
   }
 }
 
-// Columns 32 c .. of row `to` (bf16 or fp32), scaled.
+// Queries and trees: a thread takes a 16-byte chunk of a row of a (sequence, head); rows behind the last, and of tokens
+// that the tree does not have, are zeros. Every warp works the tree's masks out for itself while its
+// queries are on their way.
+template <int D>
+__global__ void __launch_bounds__(128) k_tree_prep(const __grid_constant__ PagedTreeArgs a, int rows) {
+  constexpr int kCPR = D / 8;
+  pdl_launch();
+  const int b = blockIdx.y, lane = threadIdx.x & 31, i = blockIdx.x * 128 + threadIdx.x;
+  const int c = i % kCPR, hr = i / kCPR, r = hr % (a.tiles * rows), g = hr / (a.tiles * rows);  // rows: of a tile, as packed
+  const bool in = g < a.Hkv && r < a.R;
+  const int t = in ? (int)fdiv((uint32_t)r, a.div_g) : 0;
+  QueryChunk x = {};
+  if (in) x.v = load_rope_chunk<D>(a.q + (size_t)(b * a.Tq + t) * a.q_stride + (g * a.G + (r - t * a.G)) * D, c, a.rope_half != 0);
+  uint4 wv = make_uint4(0, 0, 0, 0);
+  if (a.qw) wv = load_rope_chunk<D>(a.qw, c, a.rope_half != 0);
+  const TreeShape s = tree_shape(a, b, i == 0);
+  unsigned long long mask[2];
+  tree_masks(a.parents + b * a.parent_stride, s.nodes, lane, i < 32 ? a.status : nullptr, mask);
+  const int depth[2] = {__popcll(mask[0]) - 1, __popcll(mask[1]) - 1};
+  const int d0 = __shfl_sync(0xffffffffu, depth[0], t & 31), d1 = __shfl_sync(0xffffffffu, depth[1], t & 31);
+  x.on = in && t < s.nodes;
+  if (x.on) rope_coeffs<D>(a.rope, s.len - s.nodes + (t < 32 ? d0 : d1), c, x.c0, x.c1);
+  uint4 hi, lo;
+  query_finish<D>(a, x, a.qw != nullptr, wv, hi, lo);
+  if (g < a.Hkv) {
+    const size_t part = (size_t)rows * D * 2;
+    unsigned char* to = a.packed + (((size_t)b * a.Hkv + g) * a.tiles + r / rows) * 2 * part + swz(r % rows, c, D * 2);
+    *reinterpret_cast<uint4*>(to) = hi;
+    *reinterpret_cast<uint4*>(to + part) = lo;
+  }
+  if (i < 32) {
+    a.info[b].mask[lane] = mask[0];
+    a.info[b].mask[lane + 32] = mask[1];
+    if (lane == 0) {
+      a.info[b].ctx = s.len - s.nodes;
+      a.info[b].nodes = s.nodes;
+    }
+  }
+}
+
+// N values to place `to` of o (bf16 or fp32), scaled.
 template <int N>
 __device__ __forceinline__ void put_columns(const PagedTreeArgs& a, size_t to, const float (&v)[N], float inv, bool live) {
   if (a.o_fp32) {
@@ -135,11 +175,12 @@ __device__ __forceinline__ void put_columns(const PagedTreeArgs& a, size_t to, c
   }
 }
 
-// RT: row tiles of a pair (2: more than 128 rows), F: copies of the rows in the one tile.
+// RT: row tiles of a pair (2: more than 128 rows), F: copies of the rows in the one tile (see above).
 template <int D, int RT, int F>
 __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_constant__ PagedTreeArgs a) {
   using C = TreeCfg<D>;
-  constexpr int S = C::kStages, TB = C::kTileBytes, NC = kTile / F;  // NC: keys of a tile, and rows, of a copy
+  constexpr int S = C::kStages, TB = C::kTileBytes;
+  constexpr int NR = kTile / F, NC = F == 4 ? 64 : 128;  // rows of a copy, keys of a tile that it takes
   extern __shared__ uint8_t smem_raw[];
   uint8_t* head = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint64_t* q_full = reinterpret_cast<uint64_t*>(head);  // [2] the slot's queries are packed
@@ -354,8 +395,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
             const uint32_t o = tmem + C::kColO + 64u * (n & 1), p = tmem + C::kColS + 128u * buf;
             mma_ts_chain<4, false>(o, p, dv, kStepMN, idPV, n - first >= 2 ? 1u : 0u);
             mma_ts_chain<4, false>(o, p + 32u, dv + (uint64_t)(4 * kStepMN), kStepMN, idPV, 1u);
-            mma_ts_chain<4, false>(o, p + 64u, dv, kStepMN, idPV, 1u);
-            mma_ts_chain<4, false>(o, p + 96u, dv + (uint64_t)(4 * kStepMN), kStepMN, idPV, 1u);
+            if (F == 1) {
+              mma_ts_chain<4, false>(o, p + 64u, dv, kStepMN, idPV, 1u);
+              mma_ts_chain<4, false>(o, p + 96u, dv + (uint64_t)(4 * kStepMN), kStepMN, idPV, 1u);
+            }
             mma_commit(pv_done + buf);
           }
           if (ok) mma_commit(kv_empty + st);  // V by these products, K by their scores, complete before
@@ -370,74 +413,51 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
     }
   } else if (warp == 3) {
     // ------------------------------------------------------------ queries and trees, two segments ahead
-    constexpr int kCPR = D / 8, kRows = 32 / kCPR, kBatch = 4;
-    const int c = lane % kCPR;
-    uint4 wv = make_uint4(0, 0, 0, 0);
-    if (a.qw) wv = load_rope_chunk<D>(a.qw, c, a.rope_half != 0);
-    bool ok = true;
-    int4 cut = make_int4(-1, 0, 0, 0);
-    for (int e = 0; ok && sw.next(); e++) {
-      const int slot = slot_of(e), use = use_of(e), pr = sw.g % a.pairs, g = sw.g / a.pairs;
-      if (sw.n0 == 0 && sw.n1 < sw.nt) {
-        SweepPlan p;
-        p.base = splan->base;
-        p.rem = splan->rem;
-        p.slack = splan->slack;
-        cut = make_int4(sw.b, sw.g, tl.last(p, cum[sw.b] * tl.Hkv + sw.g * (sw.nt + tl.over), sw.nt), 0);
-      }
-      if (use > 0) ok = __all_sync(0xffffffffu, mbar_wait(q_empty + slot, (use - 1) & 1, abort));
-      if (!ok) break;
-      const int total = len[sw.b], nodes = total > 0 ? (a.nodes ? a.nodes[sw.b] : a.Tq) : 0, ctx = total - nodes;
-      unsigned long long mask[2];
-      tree_masks(a.parents + sw.b * a.parent_stride, nodes, lane, a.status, mask);
-      const int depth[2] = {__popcll(mask[0]) - 1, __popcll(mask[1]) - 1};
-      info[slot].mask[lane] = mask[0];
-      info[slot].mask[lane + 32] = mask[1];
-      if (lane == 0) {
-        info[slot].ctx = ctx;
-        info[slot].nodes = nodes;
-      }
-      uint8_t* q = smem + (RT == 1 ? 2 * slot : 0) * TB;
-      const int rows = RT == 1 ? NC : units(sw) * kTile;
-#pragma unroll 1
-      for (int r0 = 0; r0 < rows; r0 += kBatch * kRows) {
-        QueryChunk x[kBatch];
+    if (lane == 0) {
+      bool ok = true;
+      int k = -1;  // the last segment whose queries are on their way
+      int4 cut = make_int4(-1, 0, 0, 0);
+      SweepPlan p;
+      p.base = splan->base;
+      p.rem = splan->rem;
+      p.slack = splan->slack;
+      pdl_wait();  // k_tree_prep has written them
+      for (int e = 0; ok && sw.next(); e++) {
+        const int slot = slot_of(e), use = use_of(e), pr = sw.g % a.pairs, g = sw.g / a.pairs;
+        if (sw.n0 == 0 && sw.n1 < sw.nt)
+          cut = make_int4(sw.b, sw.g, tl.last(p, cum[sw.b] * tl.Hkv + sw.g * (sw.nt + tl.over), sw.nt), 0);
+        if (use > 0 && !(ok = mbar_wait(q_empty + slot, (use - 1) & 1, abort))) break;
+        const int nu = units(sw);
+        mbar_arrive_expect_tx(q_full + slot, (uint32_t)(nu * 2 * TB + sizeof(TreeInfo)));
+        bulk_load(info + slot, a.info + sw.b, sizeof(TreeInfo), q_full + slot);
+        constexpr uint32_t part = NR * C::kSpan;
+        for (int u = 0; u < nu; u++) {
+          const unsigned char* from = a.packed + (((size_t)sw.b * a.Hkv + g) * a.tiles + pr * 2 + u) * 2 * part;
+          uint8_t* to = smem + (RT == 1 ? 2 * slot : 2 * u) * TB;
 #pragma unroll
-        for (int i = 0; i < kBatch; i++) {
-          const int r = pr * 2 * kTile + r0 + i * kRows + lane / kCPR;
-          const int t = r < a.R ? (int)fdiv((uint32_t)r, a.div_g) : 0;
-          const int d0 = __shfl_sync(0xffffffffu, depth[0], t & 31), d1 = __shfl_sync(0xffffffffu, depth[1], t & 31);
-          x[i] = query_load_at<D>(a, r < a.R && t < nodes, sw.b, g, r, t, c, ctx + (t < 32 ? d0 : d1));
-        }
-#pragma unroll
-        for (int i = 0; i < kBatch; i++) {
-          const int r = r0 + i * kRows + lane / kCPR;
-          uint4 hi, lo;
-          query_finish<D>(a, x[i], a.qw != nullptr, wv, hi, lo);
-          if (r < rows) {
-            uint8_t* to = q + (RT == 1 ? 0 : (r / kTile) * 2 * TB);
-#pragma unroll
-            for (int f = 0; f < F; f++) {
-              const uint32_t at = swz(r % kTile + f * NC, c, C::kSpan);
-              *reinterpret_cast<uint4*>(to + at) = hi;
-              *reinterpret_cast<uint4*>(to + TB + at) = lo;
-            }
+          for (int f = 0; f < F; f++) {
+            bulk_load(to + f * part, from, part, q_full + slot);
+            bulk_load(to + TB + f * part, from + part, part, q_full + slot);
           }
         }
+        k = e;
       }
-      fence_proxy_async_smem();
-      warp_arrive(q_full + slot);
-    }
-    if (lane == 0) a.cut[blk] = cut;
-    if (!ok && lane == 0) {
-      *abort = 1;
-      atomicExch(a.status, kStatusTimeout);
+      a.cut[blk] = cut;
+      if (!ok) {
+        *abort = 1;
+        atomicExch(a.status, kStatusTimeout);
+      }
+      // let every copy issued above land before the block can exit: the last of each slot
+      if (RT == 1 && k > 0) mbar_wait(q_full + slot_of(k - 1), use_of(k - 1) & 1, &never);
+      if (k >= 0) mbar_wait(q_full + slot_of(k), use_of(k) & 1, &never);
     }
   } else {
     // ------------------------------------------------------------ softmax group
     regs_inc<200>();
     const int grp = (warp - 4) >> 2, q4 = warp & 3;
-    const int r = q4 * 32 + lane, f = r / NC, rr = r - f * NC;  // row of the tile: copy f of row rr
+    const int r = q4 * 32 + lane, rr = r % NR;  // row of the tile: of the copy that takes
+    const bool low = F > 1 && (r / NR) & 1;     // the weights' low parts (F == 1: both),
+    const int half = F == 4 ? r / 64 : 0;       // this half of the keys
     const uint32_t trow = tmem + ((uint32_t)(q4 * 32) << 16);
     const uint32_t obuf = trow + C::kColO + 64u * grp;
     const float sl2 = a.scale_log2;
@@ -479,22 +499,17 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
         }
         uint32_t sc[NC];
 #pragma unroll
-        for (int c = 0; c < NC / 32; c++) tmem_ld32(sbuf + f * NC + c * 32, *reinterpret_cast<uint32_t(*)[32]>(sc + 32 * c));
+        for (int c = 0; c < NC / 32; c++) tmem_ld32(sbuf + half * 64 + c * 32, *reinterpret_cast<uint32_t(*)[32]>(sc + 32 * c));
         tmem_wait_ld();
-        if (F > 1) {
-          // the weights of the keys that other copies take
+        if (F == 4) {  // the weights of the other half
           const uint32_t z[16] = {0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
-#pragma unroll
-          for (int c = 0; c < 4; c++)
-            if (c / (4 / F) != f) {
-              tmem_st16(sbuf + 16 * c, z);
-              tmem_st16(sbuf + 64 + 16 * c, z);
-            }
+          tmem_st16(sbuf + 32 * (1 - half), z);
+          tmem_st16(sbuf + 32 * (1 - half) + 16, z);
         }
         if ((tile + 1) * kTile > ctx) {  // the tile ends in the tree or behind it
 #pragma unroll
           for (int c = 0; c < NC / 32; c++) {
-            const uint32_t see = tree_word(mask, tile * kTile + f * NC + c * 32 - ctx);
+            const uint32_t see = tree_word(mask, tile * kTile + half * 64 + c * 32 - ctx);
 #pragma unroll
             for (int x = 0; x < 32; x++)
               if (!(see & (1u << x))) sc[32 * c + x] = 0xff800000u;
@@ -526,14 +541,14 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
             tc_fence_after();
             r_use = r_new;
             alpha = r_run == -INFINITY ? 0.f : ex2(m_old - m_new);
-            uint32_t w[32];
-#pragma unroll
-            for (int c = 0; c < D / 32; c++) {
-              tmem_ld32(obuf + c * 32, w);
+#pragma unroll 1
+            for (int c = 0; c < D / 16; c++) {
+              uint32_t w[16];
+              tmem_ld16(obuf + c * 16, w);
               tmem_wait_ld();
 #pragma unroll
-              for (int x = 0; x < 32; x++) w[x] = __float_as_uint(__uint_as_float(w[x]) * alpha);
-              tmem_st32(obuf + c * 32, w);
+              for (int x = 0; x < 16; x++) w[x] = __float_as_uint(__uint_as_float(w[x]) * alpha);
+              tmem_st16(obuf + c * 16, w);
             }
           }
         }
@@ -552,12 +567,20 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
             const uint64_t pp = f2(ex2(x0), ex2(x1));
             f2_split(pp, x0, x1);
             ph[x] = pack_bf16(x0, x1);
-            f2_split(f2_fma(f2(bf_lo(ph[x]), bf_hi(ph[x])), minus, pp), l0, l1);
-            pl[x] = pack_bf16(l0, l1);
+            if (F == 1 || low) {
+              f2_split(f2_fma(f2(bf_lo(ph[x]), bf_hi(ph[x])), minus, pp), l0, l1);
+              pl[x] = pack_bf16(l0, l1);
+            }
             sum4[x & 3] = f2_add(sum4[x & 3], pp);
           }
-          tmem_st8(sbuf + f * (NC / 2) + 8 * c, ph);
-          tmem_st8(sbuf + 64 + f * (NC / 2) + 8 * c, pl);
+          if (F == 1) {
+            tmem_st8(sbuf + 8 * c, ph);
+            tmem_st8(sbuf + 64 + 8 * c, pl);
+          } else if (low) {
+            tmem_st8(sbuf + half * 32 + 8 * c, pl);
+          } else {
+            tmem_st8(sbuf + half * 32 + 8 * c, ph);
+          }
         }
         tmem_wait_st();
         tc_fence_before();
@@ -575,19 +598,21 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
       ok = __all_sync(0xffffffffu, mbar_wait(pv_done + (s - 2) % 3, ((s - 2) / 3) & 1, abort));
       if (!ok) break;
       tc_fence_after();
-      float4* scratch = reinterpret_cast<float4*>(smem + 2 * slot * TB) + r * (D / 4);  // the slot's queries are no longer needed
-      const auto chunk = [&](int q) { return q ^ (r & 7); };
+      int lr = r;
+      asm volatile("" : "+r"(lr));  // addresses of this part are not kept in registers over the steps
+      float4* scratch = reinterpret_cast<float4*>(smem + 2 * slot * TB) + lr * (D / 4);  // the slot's queries are no longer needed
+      const auto chunk = [&](int q) { return q ^ (lr & 7); };
       if (joint && grp != last) {
         ok = __all_sync(0xffffffffu, mbar_wait(s_full + 2 * last + (((end - 1) >> 1) & 1), ((end - 1) >> 2) & 1, abort));
         if (!ok) break;
-#pragma unroll
-        for (int c = 0; c < D / 32; c++) {
-          uint32_t w[32];
-          tmem_ld32(obuf + c * 32, w);
+#pragma unroll 1
+        for (int c = 0; c < D / 16; c++) {
+          uint32_t w[16];
+          tmem_ld16(obuf + c * 16, w);
           tmem_wait_ld();
 #pragma unroll
-          for (int q = 0; q < 8; q++)
-            scratch[chunk(c * 8 + q)] = make_float4(__uint_as_float(w[4 * q]), __uint_as_float(w[4 * q + 1]),
+          for (int q = 0; q < 4; q++)
+            scratch[chunk(c * 4 + q)] = make_float4(__uint_as_float(w[4 * q]), __uint_as_float(w[4 * q + 1]),
                                                     __uint_as_float(w[4 * q + 2]), __uint_as_float(w[4 * q + 3]));
         }
         ml_other[slot * kTile + r] = make_float2(m_use, l_run);
@@ -608,16 +633,16 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
         other_f = z.y == 0.f ? 0.f : ex2(z.x - M);
         L = fmaf(L, mine_f, z.y * other_f);
       }
-#pragma unroll
-      for (int c = 0; c < D / 32; c++) {
-        uint32_t w[32];
-        float v[32];
-        tmem_ld32(obuf + c * 32, w);
+#pragma unroll 1
+      for (int c = 0; c < D / 16; c++) {
+        uint32_t w[16];
+        float v[16];
+        tmem_ld16(obuf + c * 16, w);
         tmem_wait_ld();
 #pragma unroll
-        for (int q = 0; q < 8; q++) {
+        for (int q = 0; q < 4; q++) {
           float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (joint) y = scratch[chunk(c * 8 + q)];
+          if (joint) y = scratch[chunk(c * 4 + q)];
           v[4 * q] = fmaf(__uint_as_float(w[4 * q]), mine_f, y.x * other_f);
           v[4 * q + 1] = fmaf(__uint_as_float(w[4 * q + 1]), mine_f, y.y * other_f);
           v[4 * q + 2] = fmaf(__uint_as_float(w[4 * q + 2]), mine_f, y.z * other_f);
@@ -625,16 +650,16 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
         }
         if (F > 1) {
 #pragma unroll
-          for (int q = 0; q < 8; q++)
-            scratch[chunk(c * 8 + q)] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+          for (int q = 0; q < 4; q++)
+            scratch[chunk(c * 4 + q)] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
         } else if (row < a.R) {
           if (whole) {
             const int t = (int)fdiv((uint32_t)row, a.div_g), h = g * a.G + (row - t * a.G);
-            put_columns(a, (((size_t)sw.b * a.Tq + t) * a.Hq + h) * D + c * 32, v, 1.f / L, live);
+            put_columns(a, (((size_t)sw.b * a.Tq + t) * a.Hq + h) * D + c * 16, v, 1.f / L, live);
           } else {
-            float4* to = reinterpret_cast<float4*>(a.part_o + (part + row - pr * 2 * kTile) * D) + c * 8;
+            float4* to = reinterpret_cast<float4*>(a.part_o + (part + row - pr * 2 * kTile) * D) + c * 4;
 #pragma unroll
-            for (int q = 0; q < 8; q++) to[q] = live ? make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]) : make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int q = 0; q < 4; q++) to[q] = live ? make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]) : make_float4(0.f, 0.f, 0.f, 0.f);
           }
         }
       }
@@ -648,14 +673,18 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
           const int ro = i / (D / 4), q = i % (D / 4), t = (int)fdiv((uint32_t)ro, a.div_g);
           RowSum x;
 #pragma unroll
-          for (int y = 0; y < F; y++) {
-            const float2 z = ml_own[grp * kTile + ro + y * NC];
+          for (int y = 0; y < F / 2; y++) {
+            const float2 z = ml_own[grp * kTile + ro + y * 64];
             if (z.y != 0.f) x.M = fmaxf(x.M, z.x);
           }
 #pragma unroll
-          for (int y = 0; y < F; y++) {
-            const int at = ro + y * NC;
+          for (int y = 0; y < F / 2; y++) {
+            const int at = ro + y * 64, below = at + NR;  // the high parts' lane, the low parts'
             x.add(x.M, ml_own[grp * kTile + at], all[at * (D / 4) + (q ^ (at & 7))]);
+            const float2 z = ml_own[grp * kTile + below];
+            const float4 v = all[below * (D / 4) + (q ^ (below & 7))];
+            const float k = z.y == 0.f ? 0.f : ex2(z.x - x.M);
+            x.v = make_float4(fmaf(k, v.x, x.v.x), fmaf(k, v.y, x.v.y), fmaf(k, v.z, x.v.z), fmaf(k, v.w, x.v.w));
           }
           if (t >= info[slot].nodes) x.S = 0.f, x.v = make_float4(0.f, 0.f, 0.f, 0.f);
           if (whole) {
@@ -673,7 +702,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
           a.lse[((size_t)sw.b * a.Hq + h) * a.Tq + t] = live ? (M + log2f(L)) * kPagedLn2 : -INFINITY;
         }
       }
-      if (grp == last) warp_arrive(q_empty + slot);
+      if (grp == last) {
+        if (RT == 1 || nu == 1) fence_proxy_async_smem();  // the slot's next queries come by copies
+        warp_arrive(q_empty + slot);
+      }
     }
     if (!ok) {
       *abort = 1;
@@ -735,16 +767,19 @@ cudaError_t launch_tree_t(const PagedTreeArgs& a, int grid, cudaStream_t s) {
   }
   const int bytes = tree_head(a.B) + TreeCfg<D>::kBytes + 1024;
   if (bytes > kSmemMax) return cudaErrorInvalidValue;
-  k_tree_sweep<D, RT, F><<<grid, kTreeThreads, (size_t)bytes, s>>>(a);
-  const cudaError_t e = cudaGetLastError();
+  constexpr int rows = kTile / F;
+  const long long chunks = (long long)a.Hkv * a.tiles * rows * (D / 8);
+  k_tree_prep<D><<<dim3((unsigned)((chunks + 127) / 128), (unsigned)a.B), 128, 0, s>>>(a, rows);
+  cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
+  if ((e = launch_pdl(k_tree_sweep<D, RT, F>, dim3((unsigned)grid), kTreeThreads, (size_t)bytes, s, a)) != cudaSuccess) return e;
   return launch_pdl(k_tree_join<D>, dim3((unsigned)grid, (unsigned)((a.rows + 512 / D - 1) / (512 / D))), 128, 0, s, a);
 }
 template <int D>
 cudaError_t launch_tree(const PagedTreeArgs& a, int grid, cudaStream_t s) {
   if (a.R > kTile) return launch_tree_t<D, 2, 1>(a, grid, s);
-  if (a.R > 64) return launch_tree_t<D, 1, 1>(a, grid, s);
-  return a.R > 32 ? launch_tree_t<D, 1, 2>(a, grid, s) : launch_tree_t<D, 1, 4>(a, grid, s);
+  const int copies = tree_copies(a.R);
+  return copies == 1 ? launch_tree_t<D, 1, 1>(a, grid, s) : (copies == 2 ? launch_tree_t<D, 1, 2>(a, grid, s) : launch_tree_t<D, 1, 4>(a, grid, s));
 }
 
 }  // namespace
