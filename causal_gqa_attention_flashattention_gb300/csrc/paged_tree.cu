@@ -55,18 +55,20 @@ struct TreeCfg {
   static constexpr uint32_t kSpan = D * 2;
   static constexpr uint32_t kSwz = D == 64 ? kSw128 : kSw64;
   static constexpr uint32_t kSBO = 8 * kSpan;
-  static constexpr int kStages = D == 64 ? 4 : 8;
+  // A key tile is free once its scores are done, a value tile two to three steps later: 3 and 6 stages (together 4: the
+  // loads' 1.25 us under load then bounded a step, 1750 clocks with 48 rows where 1450 are possible).
+  static constexpr int kKStages = D == 64 ? 3 : 4, kVStages = D == 64 ? 6 : 8;
   static constexpr int kOffK = 4 * kTileBytes;  // Q first: two slots of (high, low), or a pair's two row tiles
-  static constexpr int kOffV = kOffK + kStages * kTileBytes;
-  static constexpr int kBytes = kOffV + kStages * kTileBytes;
+  static constexpr int kOffV = kOffK + kKStages * kTileBytes;
+  static constexpr int kBytes = kOffV + kVStages * kTileBytes;
   static constexpr uint32_t kColO = 0, kColS = 128;  // group g: O at 64 g; step n: S, then P, at 128 + 128 (n % 3)
 };
-constexpr int kTreeVars = 384, kTreePlan = 392, kTreeSums = 448, kTreeInfo = 512, kTreeMl = 1664;
+constexpr int kTreeVars = 480, kTreePlan = 488, kTreeSums = 544, kTreeInfo = 608, kTreeMl = 1664;
 static_assert(sizeof(TreeInfo) % 16 == 0, "copied in one piece");
 constexpr int kTreeCum = kTreeMl + 4 * kTile * 8;
 static_assert(kTreeInfo + 2 * sizeof(TreeInfo) <= kTreeMl && kTreePlan + sizeof(SweepPlan) <= kTreeSums, "head");
-static_assert((4 + 2 * TreeCfg<32>::kStages + 4 + 4 + 3 + 4 + 2 + 2) * 8 <= kTreeVars, "barriers");
-__host__ __device__ constexpr int tree_head(int B) { return (kTreeCum + (2 * B + 1) * 4 + 1023) / 1024 * 1024; }
+static_assert((4 + 2 * TreeCfg<32>::kKStages + 2 * TreeCfg<32>::kVStages + 4 + 4 + 3 + 4 + 4 + 2 + 3) * 8 <= kTreeVars, "barriers");
+__host__ __device__ constexpr int tree_head(int B) { return (kTreeCum + (B + 1) * 4 + 1023) / 1024 * 1024; }
 
 // The tile's bits of a mask over positions that begins `r` positions before position 0 of the tree (r < 0: in the
 // context, all ones): 32 columns from there.
@@ -179,20 +181,23 @@ __device__ __forceinline__ void put_columns(const PagedTreeArgs& a, size_t to, c
 template <int D, int RT, int F>
 __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_constant__ PagedTreeArgs a) {
   using C = TreeCfg<D>;
-  constexpr int S = C::kStages, TB = C::kTileBytes;
+  constexpr int SK = C::kKStages, SV = C::kVStages, TB = C::kTileBytes;
   constexpr int NR = kTile / F, NC = F == 4 ? 64 : 128;  // rows of a copy, keys of a tile that it takes
   extern __shared__ uint8_t smem_raw[];
   uint8_t* head = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint64_t* q_full = reinterpret_cast<uint64_t*>(head);  // [2] the slot's queries are packed
   uint64_t* q_empty = q_full + 2;          // [2] the slot's segment has left it
-  uint64_t* kv_full = q_empty + 2;         // [S]
-  uint64_t* kv_empty = kv_full + S;        // [S] the last O += P V of the stage has completed
-  uint64_t* s_full = kv_empty + S;         // [group][2] the group's steps in turn
+  uint64_t* k_full = q_empty + 2;          // [SK]
+  uint64_t* k_empty = k_full + SK;         // [SK] the last S = Q K^T of the stage has completed
+  uint64_t* v_full = k_empty + SK;         // [SV]
+  uint64_t* v_empty = v_full + SV;         // [SV] the O += P V of the stage have completed
+  uint64_t* s_full = v_empty + SV;         // [group][2] the group's steps in turn
   uint64_t* p_ready = s_full + 4;          // [group][2]
-  uint64_t* pv_done = p_ready + 4;         // [3] per buffer of S and P
-  uint64_t* part_full = pv_done + 3;       // [group][2] the other group's part of a segment that this one finishes
+  uint64_t* pv_done = p_ready + 4;         // [3] per buffer of S and P, for the issuer of S
+  uint64_t* o_done = pv_done + 3;          // [group][2] the same per group's step, for the group
+  uint64_t* part_full = o_done + 4;        // [group][2] the other group's part of a segment that this one finishes
   uint64_t* gsync = part_full + 4;         // [group]
-  uint64_t* drain = gsync + 2;             // [2] per issuing thread
+  uint64_t* drain = gsync + 2;             // [3] per issuing thread
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(head + kTreeVars);
   volatile int* abort = reinterpret_cast<volatile int*>(head + kTreeVars) + 1;
   volatile SweepPlan* splan = reinterpret_cast<volatile SweepPlan*>(head + kTreePlan);
@@ -201,7 +206,6 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
   float2* ml_other = reinterpret_cast<float2*>(head + kTreeMl);    // [2][128] per slot
   float2* ml_own = ml_other + 2 * kTile;                           // [2][128] per group
   int* cum = reinterpret_cast<int*>(head + kTreeCum);
-  int* len = cum + a.B + 1;
   uint8_t* smem = head + tree_head(a.B);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, blk = (int)blockIdx.x;
   if (tid == 0) {
@@ -210,24 +214,30 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
       mbar_init(q_full + k, 1);
       mbar_init(q_empty + k, 4);
       mbar_init(gsync + k, 4);
-      mbar_init(drain + k, 1);
     }
-    for (int k = 0; k < S; k++) {
-      mbar_init(kv_full + k, 1);
-      mbar_init(kv_empty + k, 1);
+    for (int k = 0; k < SK; k++) {
+      mbar_init(k_full + k, 1);
+      mbar_init(k_empty + k, 1);
+    }
+    for (int k = 0; k < SV; k++) {
+      mbar_init(v_full + k, 1);
+      mbar_init(v_empty + k, RT);  // one for each row tile of the pair
     }
     for (int k = 0; k < 4; k++) {
       mbar_init(s_full + k, 2);
       mbar_init(p_ready + k, 4);
+      mbar_init(o_done + k, 1);
       mbar_init(part_full + k, 4);
     }
-    for (int k = 0; k < 3; k++) mbar_init(pv_done + k, 1);
+    for (int k = 0; k < 3; k++) {
+      mbar_init(pv_done + k, 1);
+      mbar_init(drain + k, 1);
+    }
     fence_mbar_init();
   }
   if (warp == 1) tmem_alloc(tmem_slot, 512);
   running_costs<kTreeThreads>(a.B, cum, wsum, tid, [&](int b) {
     const TreeShape x = tree_shape(a, b, blk == 0);
-    len[b] = x.len;
     return kTreeOver + max(1, (x.len + kTile - 1) / kTile);  // one even where nothing is read: its rows are written
   });
   Tiles tl;
@@ -263,11 +273,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
     const uint32_t pbytes = (uint32_t)prows * C::kSpan;
     // Page numbers 32 at a time, one to a lane, a window ahead: num_pages (outside the pool, read as zeros)
     // for a bad page and behind the last position.
-    const auto window = [&](const SegWalk<kTreeOver>& s, int w) {
+    const auto window = [&](int b, int len, int w) {
       const int i = w * 32 + lane;
       int id = a.num_pages;
-      if ((i << a.page_shift) < len[s.b]) {
-        id = a.table[(size_t)s.b * a.max_pages + i];
+      if ((i << a.page_shift) < len) {
+        id = a.table[(size_t)b * a.max_pages + i];
         if (id < 0 || id >= a.num_pages) {
           record_page(a.status);
           id = a.num_pages;
@@ -278,10 +288,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
     const auto page_of = [&](int n) { return (n * kTile) >> a.page_shift; };
     SegWalk<kTreeOver> ls = sw;  // the segment of the next window
     bool lon = ls.next();
-    int lw = 0, id = 0, nid = 0;
+    int lw = 0, llen = 0, id = 0, nid = 0;
     if (lon) {
       lw = page_of(ls.n0) >> 5;
-      nid = window(ls, lw);
+      llen = tree_shape(a, ls.b, false).len;
+      nid = window(ls.b, llen, lw);
     }
     const auto look = [&]() {
       id = nid;
@@ -290,14 +301,24 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
         lw++;
       } else {
         lon = ls.next();
-        if (lon) lw = page_of(ls.n0) >> 5;
+        if (lon) {
+          lw = page_of(ls.n0) >> 5;
+          llen = tree_shape(a, ls.b, false).len;
+        }
       }
-      if (lon) nid = window(ls, lw);
+      if (lon) nid = window(ls.b, llen, lw);
     };
+    SweepPlan plan;
+    plan.base = splan->base;
+    plan.rem = splan->rem;
+    plan.slack = splan->slack;
+    int4 cut = make_int4(-1, 0, 0, 0);
     bool ok = true;
-    int k = 0;  // stages handed out so far
+    int k = 0;  // tiles so far
     while (ok && sw.next()) {
       const int kvh = sw.g / a.pairs;
+      if (sw.n0 == 0 && sw.n1 < sw.nt)
+        cut = make_int4(sw.b, sw.g, tl.last(plan, cum[sw.b] * tl.Hkv + sw.g * (sw.nt + tl.over), sw.nt), 0);
       int win = -1;
 #pragma unroll 1
       for (int n = sw.n0; ok && n < sw.n1; n++, k++) {
@@ -307,48 +328,90 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
           look();
         }
         const int mine = __shfl_sync(0xffffffffu, id, (first & 31) + (lane < per ? lane : 0));
-        const int st = k % S, use = k / S;
-        if (use > 0) ok = __all_sync(0xffffffffu, mbar_wait(kv_empty + st, (use - 1) & 1, abort));
-        if (!ok) break;
-        if (lane == 0) mbar_arrive_expect_tx(kv_full + st, 2 * TB);
-        __syncwarp();
-        if (lane < per) {
-          const int off = (n * kTile) & ((1 << a.page_shift) - 1);
-          uint8_t *dk = smem + C::kOffK + st * TB + lane * pbytes, *dv = smem + C::kOffV + st * TB + lane * pbytes;
-          if (RT == 1 || a.pairs == 1) {
-            tma_load_4d(dk, &a.map_pk, kv_full + st, 0, off, kvh, mine, policy);
-            tma_load_4d(dv, &a.map_pv, kv_full + st, 0, off, kvh, mine, policy);
-          } else {  // the other pairs read it too
-            tma_load_4d(dk, &a.map_pk, kv_full + st, 0, off, kvh, mine);
-            tma_load_4d(dv, &a.map_pv, kv_full + st, 0, off, kvh, mine);
+        const int off = (n * kTile) & ((1 << a.page_shift) - 1);
+        const bool again = RT == 2 && a.pairs > 1;  // the other pairs read it too
+        const auto load = [&](const CUtensorMap* map, uint8_t* to, uint64_t* full, uint64_t* empty, int use) {
+          if (use > 0) ok = __all_sync(0xffffffffu, mbar_wait(empty, (use - 1) & 1, abort));
+          if (!ok) return;
+          if (lane == 0) mbar_arrive_expect_tx(full, TB);
+          __syncwarp();
+          if (lane < per) {
+            if (again)
+              tma_load_4d(to + lane * pbytes, map, full, 0, off, kvh, mine);
+            else
+              tma_load_4d(to + lane * pbytes, map, full, 0, off, kvh, mine, policy);
           }
+        };
+        load(&a.map_pk, smem + C::kOffK + k % SK * TB, k_full + k % SK, k_empty + k % SK, k / SK);
+        if (!ok) {
+          // V of this tile is not on its way: below, only what is
+          for (int x = k - SK < 0 ? 0 : k - SK; lane == 0 && x < k; x++) mbar_wait(k_full + x % SK, (x / SK) & 1, &never);
+          for (int x = k - SV < 0 ? 0 : k - SV; lane == 0 && x < k; x++) mbar_wait(v_full + x % SV, (x / SV) & 1, &never);
+          break;
+        }
+        load(&a.map_pv, smem + C::kOffV + k % SV * TB, v_full + k % SV, v_empty + k % SV, k / SV);
+        if (!ok) {
+          for (int x = k - SK + 1 < 0 ? 0 : k - SK + 1; lane == 0 && x <= k; x++) mbar_wait(k_full + x % SK, (x / SK) & 1, &never);
+          for (int x = k - SV < 0 ? 0 : k - SV; lane == 0 && x < k; x++) mbar_wait(v_full + x % SV, (x / SV) & 1, &never);
+          break;
         }
       }
     }
-    if (!ok && lane == 0) {
-      *abort = 1;
-      atomicExch(a.status, kStatusTimeout);
-    }
-    // let every copy issued above land before the block can exit
     if (lane == 0) {
-      for (int x = k - S < 0 ? 0 : k - S; x < k; x++) mbar_wait(kv_full + x % S, (x / S) & 1, &never);
+      a.cut[blk] = cut;
+      if (!ok) {
+        *abort = 1;
+        atomicExch(a.status, kStatusTimeout);
+      } else {
+        // let every copy issued above land before the block can exit
+        for (int x = k - SK < 0 ? 0 : k - SK; x < k; x++) mbar_wait(k_full + x % SK, (x / SK) & 1, &never);
+        for (int x = k - SV < 0 ? 0 : k - SV; x < k; x++) mbar_wait(v_full + x % SV, (x / SV) & 1, &never);
+      }
     }
   } else if (warp == 1) {
-    // ------------------------------------------------------------ S = Q K^T issuer
+    // ------------------------------------------------------------ queries and trees; S = Q K^T issuer
     if (lane == 0) {
       constexpr uint32_t idS = idesc_fp16(128, 128, false, false);
       constexpr uint32_t kStepK = 32 >> 4, tstep = (uint32_t)TB >> 4;
       const uint64_t dQ0 = smem_desc(smem_u32(smem), 16, C::kSBO, C::kSwz);
       const uint64_t dK0 = smem_desc(smem_u32(smem + C::kOffK), 16, C::kSBO, C::kSwz);
       bool ok = true;
-      int n = 0, k = 0, e = 0;  // steps, stages, segments
+      int n = 0, k = 0, e = 0, qe = 0;  // steps, tiles, segments; segments whose queries are on their way
+      SegWalk<kTreeOver> qs = sw;
+      bool qon = qs.next();
+      const auto load = [&]() {  // the next segment's queries: its slot is free
+        const int slot = slot_of(qe), nu = units(qs);
+        mbar_arrive_expect_tx(q_full + slot, (uint32_t)(nu * 2 * TB + sizeof(TreeInfo)));
+        bulk_load(info + slot, a.info + qs.b, sizeof(TreeInfo), q_full + slot);
+        constexpr uint32_t part = NR * C::kSpan;
+#pragma unroll 1
+        for (int u = 0; u < nu; u++) {
+          const unsigned char* from = a.packed + (((size_t)qs.b * a.Hkv + qs.g / a.pairs) * a.tiles + qs.g % a.pairs * 2 + u) * 2 * part;
+          uint8_t* to = smem + (RT == 1 ? 2 * slot : 2 * u) * TB;
+#pragma unroll
+          for (int f = 0; f < F; f++) {
+            bulk_load(to + f * part, from, part, q_full + slot);
+            bulk_load(to + TB + f * part, from + part, part, q_full + slot);
+          }
+        }
+        qe++;
+        qon = qs.next();
+      };
+      pdl_wait();  // k_tree_prep has written them
+      if (qon) load();
+      if (RT == 1 && qon) load();
       while (ok && sw.next()) {
         const int nu = units(sw), slot = slot_of(e);
+        if (qe == e) {
+          if (!(ok = mbar_wait(q_empty + slot, (use_of(e) - 1) & 1, abort))) break;
+          load();
+        }
         if (!(ok = mbar_wait(q_full + slot, use_of(e) & 1, abort))) break;
 #pragma unroll 1
         for (int i = sw.n0; ok && i < sw.n1; i++, k++) {
-          const int st = k % S;
-          if (!(ok = mbar_wait(kv_full + st, (k / S) & 1, abort))) break;
+          const int st = k % SK;
+          if (RT == 1 && qon && qe == e + 1 && use_of(qe) > 0 && mbar_test(q_empty + slot_of(qe), (use_of(qe) - 1) & 1)) load();
+          if (!(ok = mbar_wait(k_full + st, (k / SK) & 1, abort))) break;
 #pragma unroll 1
           for (int u = 0; u < nu; u++, n++) {
             const int buf = n % 3, use = n / 3;
@@ -362,6 +425,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
             mma_commit(full);
             mbar_arrive(full);  // what this thread has seen (the tree of the slot) comes with it
           }
+          if (ok) mma_commit(k_empty + st);
         }
         e++;
       }
@@ -371,93 +435,59 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
       }
       mma_commit(drain);
       mbar_wait(drain, 0, &never);
+      // let every copy issued above land before the block can exit: the last of each slot
+      if (RT == 1 && qe > 1) mbar_wait(q_full + slot_of(qe - 2), use_of(qe - 2) & 1, &never);
+      if (qe > 0) mbar_wait(q_full + slot_of(qe - 1), use_of(qe - 1) & 1, &never);
     }
-  } else if (warp == 2) {
-    // ------------------------------------------------------------ O += P V issuer
+  } else if (warp < 4) {
+    // ------------------------------------------------------------ O += P V issuer of a group
     if (lane == 0) {
+      const int grp = warp - 2;
       constexpr uint32_t idPV = idesc_bf16(128, D, false, true);
       constexpr uint32_t kStepMN = (16 * C::kSpan) >> 4, tstep = (uint32_t)TB >> 4;
       const uint64_t dV0 = smem_desc(smem_u32(smem + C::kOffV), 16, C::kSBO, C::kSwz);
+      const uint32_t o = tmem + C::kColO + 64u * grp;
       bool ok = true;
       int n = 0, k = 0;
       while (ok && sw.next()) {
-        const int nu = units(sw), first = n;
+        const int nu = units(sw), first = n, tiles = sw.n1 - sw.n0, end = first + tiles * nu;
 #pragma unroll 1
-        for (int i = sw.n0; ok && i < sw.n1; i++, k++) {
-          const int st = k % S;
-#pragma unroll 1
-          for (int u = 0; u < nu; u++, n++) {
-            const int buf = n % 3;
-            // the group has also read the O of its last segment before it arrives for this one
-            if (!(ok = mbar_wait(p_ready + 2 * (n & 1) + ((n >> 1) & 1), (n >> 2) & 1, abort))) break;
-            tc_fence_after();
-            const uint64_t dv = dV0 + (uint64_t)(st * tstep);
-            const uint32_t o = tmem + C::kColO + 64u * (n & 1), p = tmem + C::kColS + 128u * buf;
-            mma_ts_chain<4, false>(o, p, dv, kStepMN, idPV, n - first >= 2 ? 1u : 0u);
-            mma_ts_chain<4, false>(o, p + 32u, dv + (uint64_t)(4 * kStepMN), kStepMN, idPV, 1u);
-            if (F == 1) {
-              mma_ts_chain<4, false>(o, p + 64u, dv, kStepMN, idPV, 1u);
-              mma_ts_chain<4, false>(o, p + 96u, dv + (uint64_t)(4 * kStepMN), kStepMN, idPV, 1u);
-            }
-            mma_commit(pv_done + buf);
+        for (n = first + ((first ^ grp) & 1); n < end; n += 2) {
+          const int kt = k + (RT == 2 && nu == 2 ? (n - first) >> 1 : n - first), st = kt % SV, i = n >> 1;
+          // the group has also read the O of its last segment before it arrives for this one
+          if (!(ok = mbar_wait(p_ready + 2 * grp + (i & 1), (i >> 1) & 1, abort))) break;
+          if (!(ok = mbar_wait(v_full + st, (kt / SV) & 1, abort))) break;
+          tc_fence_after();
+          const uint64_t dv = dV0 + (uint64_t)(st * tstep);
+          const uint32_t p = tmem + C::kColS + 128u * (n % 3);
+          mma_ts_chain<4, false>(o, p, dv, kStepMN, idPV, n - first >= 2 ? 1u : 0u);
+          mma_ts_chain<4, false>(o, p + 32u, dv + (uint64_t)(4 * kStepMN), kStepMN, idPV, 1u);
+          if (F == 1) {
+            mma_ts_chain<4, false>(o, p + 64u, dv, kStepMN, idPV, 1u);
+            mma_ts_chain<4, false>(o, p + 96u, dv + (uint64_t)(4 * kStepMN), kStepMN, idPV, 1u);
           }
-          if (ok) mma_commit(kv_empty + st);  // V by these products, K by their scores, complete before
+          mma_commit(pv_done + n % 3);
+          mma_commit(o_done + 2 * grp + (i & 1));
+          mma_commit(v_empty + st);
+          if (RT == 2 && nu == 1) mbar_arrive(v_empty + st);
         }
+        n = end;
+        k += tiles;
       }
       if (!ok) {
         *abort = 1;
         atomicExch(a.status, kStatusTimeout);
       }
-      mma_commit(drain + 1);
-      mbar_wait(drain + 1, 0, &never);
-    }
-  } else if (warp == 3) {
-    // ------------------------------------------------------------ queries and trees, two segments ahead
-    if (lane == 0) {
-      bool ok = true;
-      int k = -1;  // the last segment whose queries are on their way
-      int4 cut = make_int4(-1, 0, 0, 0);
-      SweepPlan p;
-      p.base = splan->base;
-      p.rem = splan->rem;
-      p.slack = splan->slack;
-      pdl_wait();  // k_tree_prep has written them
-      for (int e = 0; ok && sw.next(); e++) {
-        const int slot = slot_of(e), use = use_of(e), pr = sw.g % a.pairs, g = sw.g / a.pairs;
-        if (sw.n0 == 0 && sw.n1 < sw.nt)
-          cut = make_int4(sw.b, sw.g, tl.last(p, cum[sw.b] * tl.Hkv + sw.g * (sw.nt + tl.over), sw.nt), 0);
-        if (use > 0 && !(ok = mbar_wait(q_empty + slot, (use - 1) & 1, abort))) break;
-        const int nu = units(sw);
-        mbar_arrive_expect_tx(q_full + slot, (uint32_t)(nu * 2 * TB + sizeof(TreeInfo)));
-        bulk_load(info + slot, a.info + sw.b, sizeof(TreeInfo), q_full + slot);
-        constexpr uint32_t part = NR * C::kSpan;
-        for (int u = 0; u < nu; u++) {
-          const unsigned char* from = a.packed + (((size_t)sw.b * a.Hkv + g) * a.tiles + pr * 2 + u) * 2 * part;
-          uint8_t* to = smem + (RT == 1 ? 2 * slot : 2 * u) * TB;
-#pragma unroll
-          for (int f = 0; f < F; f++) {
-            bulk_load(to + f * part, from, part, q_full + slot);
-            bulk_load(to + TB + f * part, from + part, part, q_full + slot);
-          }
-        }
-        k = e;
-      }
-      a.cut[blk] = cut;
-      if (!ok) {
-        *abort = 1;
-        atomicExch(a.status, kStatusTimeout);
-      }
-      // let every copy issued above land before the block can exit: the last of each slot
-      if (RT == 1 && k > 0) mbar_wait(q_full + slot_of(k - 1), use_of(k - 1) & 1, &never);
-      if (k >= 0) mbar_wait(q_full + slot_of(k), use_of(k) & 1, &never);
+      mma_commit(drain + 1 + grp);
+      mbar_wait(drain + 1 + grp, 0, &never);
     }
   } else {
     // ------------------------------------------------------------ softmax group
     regs_inc<200>();
     const int grp = (warp - 4) >> 2, q4 = warp & 3;
     const int r = q4 * 32 + lane, rr = r % NR;  // row of the tile: of the copy that takes
-    const bool low = F > 1 && (r / NR) & 1;     // the weights' low parts (F == 1: both),
-    const int half = F == 4 ? r / 64 : 0;       // this half of the keys
+    const bool low = F > 1 && (r / NR) & 1;  // the weights' low parts (F == 1: both)
+    const int half = F == 4 ? r / 64 : 0;  // this half of the keys
     const uint32_t trow = tmem + ((uint32_t)(q4 * 32) << 16);
     const uint32_t obuf = trow + C::kColO + 64u * grp;
     const float sl2 = a.scale_log2;
@@ -478,10 +508,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
       const int turn = last ? joined1 : joined0;
       if (joint) last ? joined1++ : joined0++;
       if (mine >= end) continue;
-      const int total = len[sw.b], pr = sw.g % a.pairs, u = nu == 2 ? (mine - first) & 1 : 0;
+      const int pr = sw.g % a.pairs, u = nu == 2 ? (mine - first) & 1 : 0;
       const int row = pr * 2 * kTile + u * kTile + rr;        // row of the (sequence, head)
       unsigned long long mask = 0;
-      int ctx = 0;
+      int ctx = 0, total = 0;
       bool live = false;
       float r_run = 0.f, l_run = 0.f, m_use = 0.f;
       int s = mine;
@@ -495,6 +525,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
           ctx = info[slot].ctx;
           const int t = row < a.R ? (int)fdiv((uint32_t)row, a.div_g) : kTreeMax;
           live = t < info[slot].nodes;
+          total = ctx + info[slot].nodes;
           if (live) mask = info[slot].mask[t];
         }
         uint32_t sc[NC];
@@ -515,11 +546,16 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
               if (!(see & (1u << x))) sc[32 * c + x] = 0xff800000u;
           }
           // what lies behind the last position may be anything: its weight is 0, but 0 times a NaN is not
-          if (u == 0 && r >= total - tile * kTile) {
-            uint4* v = reinterpret_cast<uint4*>(smem + C::kOffV + (k0 + tile - sw.n0) % S * TB + r * C::kSpan);
+          const int rem = total - tile * kTile, kt = k0 + tile - sw.n0;
+          if (rem < kTile) {
+            ok = __all_sync(0xffffffffu, mbar_wait(v_full + kt % SV, (kt / SV) & 1, abort));
+            if (!ok) break;
+            if (r >= rem) {
+              uint4* v = reinterpret_cast<uint4*>(smem + C::kOffV + kt % SV * TB + r * C::kSpan);
 #pragma unroll
-            for (int c = 0; c < D / 8; c++) v[c] = make_uint4(0u, 0u, 0u, 0u);
-            fence_proxy_async_smem();
+              for (int c = 0; c < D / 8; c++) v[c] = make_uint4(0u, 0u, 0u, 0u);
+              fence_proxy_async_smem();
+            }
           }
         }
         float mx8[8];
@@ -536,7 +572,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
           const float r_new = fmaxf(r_run, mxr), m_old = __fmul_rn(r_run, sl2), m_new = __fmul_rn(r_new, sl2);
           // O and the sum follow the maximum only when some row's grew by more than 2^8 (or came out of nothing)
           if (__any_sync(0xffffffffu, m_new > m_old + 8.0f)) {
-            ok = __all_sync(0xffffffffu, mbar_wait(pv_done + (s - 2) % 3, ((s - 2) / 3) & 1, abort));
+            ok = __all_sync(0xffffffffu, mbar_wait(o_done + 2 * grp + (((s - 2) >> 1) & 1), ((s - 2) >> 2) & 1, abort));
             if (!ok) break;
             tc_fence_after();
             r_use = r_new;
@@ -556,6 +592,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
         m_use = r_use == -INFINITY ? 0.f : __fmul_rn(r_use, sl2);
         uint64_t sum4[4] = {0ull, 0ull, 0ull, 0ull};
         const uint64_t sl2x2 = f2(sl2, sl2), negm = f2(-m_use, -m_use), minus = f2(-1.f, -1.f);
+        // one code for both kinds of lanes: two of them side by side starve the schedulers of instructions
 #pragma unroll
         for (int c = 0; c < NC / 16; c++) {
           uint32_t ph[8], pl[8];
@@ -567,20 +604,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
             const uint64_t pp = f2(ex2(x0), ex2(x1));
             f2_split(pp, x0, x1);
             ph[x] = pack_bf16(x0, x1);
-            if (F == 1 || low) {
-              f2_split(f2_fma(f2(bf_lo(ph[x]), bf_hi(ph[x])), minus, pp), l0, l1);
-              pl[x] = pack_bf16(l0, l1);
-            }
+            f2_split(f2_fma(f2(bf_lo(ph[x]), bf_hi(ph[x])), minus, pp), l0, l1);
+            pl[x] = pack_bf16(l0, l1);
+            if (F > 1) ph[x] = low ? pl[x] : ph[x];
             sum4[x & 3] = f2_add(sum4[x & 3], pp);
           }
-          if (F == 1) {
-            tmem_st8(sbuf + 8 * c, ph);
-            tmem_st8(sbuf + 64 + 8 * c, pl);
-          } else if (low) {
-            tmem_st8(sbuf + half * 32 + 8 * c, pl);
-          } else {
-            tmem_st8(sbuf + half * 32 + 8 * c, ph);
-          }
+          tmem_st8(sbuf + half * 32 + 8 * c, ph);
+          if (F == 1) tmem_st8(sbuf + 64 + 8 * c, pl);
         }
         tmem_wait_st();
         tc_fence_before();
@@ -595,7 +625,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
       }
       if (!ok) break;
       // the segment's unnormalised O, maximum (log2 units) and sum
-      ok = __all_sync(0xffffffffu, mbar_wait(pv_done + (s - 2) % 3, ((s - 2) / 3) & 1, abort));
+      ok = __all_sync(0xffffffffu, mbar_wait(o_done + 2 * grp + (((s - 2) >> 1) & 1), ((s - 2) >> 2) & 1, abort));
       if (!ok) break;
       tc_fence_after();
       int lr = r;
@@ -679,7 +709,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
           }
 #pragma unroll
           for (int y = 0; y < F / 2; y++) {
-            const int at = ro + y * 64, below = at + NR;  // the high parts' lane, the low parts'
+            const int at = ro + y * 64, below = at + NR;  // the high parts' lane and the low parts'; both have the row's sum
             x.add(x.M, ml_own[grp * kTile + at], all[at * (D / 4) + (q ^ (at & 7))]);
             const float2 z = ml_own[grp * kTile + below];
             const float4 v = all[below * (D / 4) + (q ^ (below & 7))];
