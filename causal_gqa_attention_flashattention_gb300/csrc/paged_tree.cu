@@ -61,13 +61,16 @@ struct TreeCfg {
   static constexpr int kOffK = 4 * kTileBytes;  // Q first: two slots of (high, low), or a pair's two row tiles
   static constexpr int kOffV = kOffK + kKStages * kTileBytes;
   static constexpr int kBytes = kOffV + kVStages * kTileBytes;
-  static constexpr uint32_t kColO = 0, kColS = 128;  // group g: O at 64 g; step n: S, then P, at 128 + 128 (n % 3)
+  // Tensor memory: group g's O at 64 g. With both parts of the weights in a lane (F == 1) step n has its S at 128 +
+  // 128 (n % 3), and P in its place; else a group has S at 128 + 128 g and P, 64 columns, at 384 + 64 g, so that
+  // its next scores are worked out while it is on its weights.
+  static constexpr uint32_t kColO = 0, kColS = 128, kColP = 384;
 };
 constexpr int kTreeVars = 480, kTreePlan = 488, kTreeSums = 544, kTreeInfo = 608, kTreeMl = 1664;
 static_assert(sizeof(TreeInfo) % 16 == 0, "copied in one piece");
 constexpr int kTreeCum = kTreeMl + 4 * kTile * 8;
 static_assert(kTreeInfo + 2 * sizeof(TreeInfo) <= kTreeMl && kTreePlan + sizeof(SweepPlan) <= kTreeSums, "head");
-static_assert((4 + 2 * TreeCfg<32>::kKStages + 2 * TreeCfg<32>::kVStages + 4 + 4 + 3 + 4 + 4 + 2 + 3) * 8 <= kTreeVars, "barriers");
+static_assert((4 + 2 * TreeCfg<32>::kKStages + 2 * TreeCfg<32>::kVStages + 4 + 8 + 3 + 4 + 4 + 2 + 3) * 8 <= kTreeVars, "barriers");
 __host__ __device__ constexpr int tree_head(int B) { return (kTreeCum + (B + 1) * 4 + 1023) / 1024 * 1024; }
 
 // The tile's bits of a mask over positions that begins `r` positions before position 0 of the tree (r < 0: in the
@@ -192,8 +195,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
   uint64_t* v_full = k_empty + SK;         // [SV]
   uint64_t* v_empty = v_full + SV;         // [SV] the O += P V of the stage have completed
   uint64_t* s_full = v_empty + SV;         // [group][2] the group's steps in turn
-  uint64_t* p_ready = s_full + 4;          // [group][2]
-  uint64_t* pv_done = p_ready + 4;         // [3] per buffer of S and P, for the issuer of S
+  uint64_t* p_ready = s_full + 4;          // [group][2][2] the weights (F == 1: of the tile's last 64 keys, and of the first)
+  uint64_t* pv_done = p_ready + 8;         // F == 1: [3] per buffer of S and P; else [group] the scores are in registers
   uint64_t* o_done = pv_done + 3;          // [group][2] the same per group's step, for the group
   uint64_t* part_full = o_done + 4;        // [group][2] the other group's part of a segment that this one finishes
   uint64_t* gsync = part_full + 4;         // [group]
@@ -225,12 +228,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
     }
     for (int k = 0; k < 4; k++) {
       mbar_init(s_full + k, 2);
-      mbar_init(p_ready + k, 4);
+      mbar_init(p_ready + 2 * k, 4);
+      mbar_init(p_ready + 2 * k + 1, 4);
       mbar_init(o_done + k, 1);
       mbar_init(part_full + k, 4);
     }
     for (int k = 0; k < 3; k++) {
-      mbar_init(pv_done + k, 1);
+      mbar_init(pv_done + k, F == 1 ? 1 : 4);
       mbar_init(drain + k, 1);
     }
     fence_mbar_init();
@@ -414,7 +418,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
           if (!(ok = mbar_wait(k_full + st, (k / SK) & 1, abort))) break;
 #pragma unroll 1
           for (int u = 0; u < nu; u++, n++) {
-            const int buf = n % 3, use = n / 3;
+            // F == 1: the buffer's weights have been read; else: the group's scores
+            const int buf = F == 1 ? n % 3 : n & 1, use = F == 1 ? n / 3 : n >> 1;
             if (use > 0 && !(ok = mbar_wait(pv_done + buf, (use - 1) & 1, abort))) break;
             tc_fence_after();
             const uint64_t dq = dQ0 + (uint64_t)((RT == 1 ? 2 * slot : 2 * u) * tstep), dk = dK0 + (uint64_t)(st * tstep);
@@ -455,18 +460,24 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
         for (n = first + ((first ^ grp) & 1); n < end; n += 2) {
           const int kt = k + (RT == 2 && nu == 2 ? (n - first) >> 1 : n - first), st = kt % SV, i = n >> 1;
           // the group has also read the O of its last segment before it arrives for this one
-          if (!(ok = mbar_wait(p_ready + 2 * grp + (i & 1), (i >> 1) & 1, abort))) break;
+          uint64_t* ready = p_ready + 4 * grp + 2 * (i & 1);
+          if (!(ok = mbar_wait(ready, (i >> 1) & 1, abort))) break;
           if (!(ok = mbar_wait(v_full + st, (kt / SV) & 1, abort))) break;
+          const uint64_t dv = dV0 + (uint64_t)(st * tstep), dv2 = dv + (uint64_t)(4 * kStepMN);
+          const uint32_t p = F == 1 ? tmem + C::kColS + 128u * (n % 3) : tmem + C::kColP + 64u * grp;
+          constexpr uint32_t kHalf = F == 1 ? 64u : 32u;  // columns of P for 64 keys
           tc_fence_after();
-          const uint64_t dv = dV0 + (uint64_t)(st * tstep);
-          const uint32_t p = tmem + C::kColS + 128u * (n % 3);
-          mma_ts_chain<4, false>(o, p, dv, kStepMN, idPV, n - first >= 2 ? 1u : 0u);
-          mma_ts_chain<4, false>(o, p + 32u, dv + (uint64_t)(4 * kStepMN), kStepMN, idPV, 1u);
+          mma_ts_chain<4, false>(o, p + kHalf, dv2, kStepMN, idPV, n - first >= 2 ? 1u : 0u);
           if (F == 1) {
-            mma_ts_chain<4, false>(o, p + 64u, dv, kStepMN, idPV, 1u);
-            mma_ts_chain<4, false>(o, p + 96u, dv + (uint64_t)(4 * kStepMN), kStepMN, idPV, 1u);
+            mma_ts_chain<4, false>(o, p + kHalf + 32u, dv2, kStepMN, idPV, 1u);
+            if (!(ok = mbar_wait(ready + 1, (i >> 1) & 1, abort))) break;
+            tc_fence_after();
           }
-          mma_commit(pv_done + n % 3);
+          mma_ts_chain<4, false>(o, p, dv, kStepMN, idPV, 1u);
+          if (F == 1) {
+            mma_ts_chain<4, false>(o, p + 32u, dv, kStepMN, idPV, 1u);
+            mma_commit(pv_done + n % 3);
+          }
           mma_commit(o_done + 2 * grp + (i & 1));
           mma_commit(v_empty + st);
           if (RT == 2 && nu == 1) mbar_arrive(v_empty + st);
@@ -486,11 +497,19 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
     regs_inc<200>();
     const int grp = (warp - 4) >> 2, q4 = warp & 3;
     const int r = q4 * 32 + lane, rr = r % NR;  // row of the tile: of the copy that takes
-    const bool low = F > 1 && (r / NR) & 1;  // the weights' low parts (F == 1: both)
+    // the weights' low parts (F == 1: both), the groups' the other way round: a scheduler then has a warp of each kind
+    const bool low = F > 1 && ((r / NR) ^ grp) & 1;
     const int half = F == 4 ? r / 64 : 0;  // this half of the keys
     const uint32_t trow = tmem + ((uint32_t)(q4 * 32) << 16);
     const uint32_t obuf = trow + C::kColO + 64u * grp;
     const float sl2 = a.scale_log2;
+    if (F == 4) {  // the weights of the half that the lane does not take stay zeros
+      const uint32_t z[16] = {0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+      const uint32_t zbuf = trow + C::kColP + 64u * grp + 32u * (1 - half);
+      tmem_st16(zbuf, z);
+      tmem_st16(zbuf + 16, z);
+      tmem_wait_st();
+    }
     bool ok = true;
     int n = 0, kt = 0, joined0 = 0, joined1 = 0, syncs = 0;  // steps, stages; segments that each group finished with the other; group barriers
     const auto group_sync = [&]() {
@@ -516,8 +535,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
       float r_run = 0.f, l_run = 0.f, m_use = 0.f;
       int s = mine;
       for (; s < end; s += 2) {
-        const int buf = s % 3, tile = sw.n0 + (nu == 2 ? (s - first) >> 1 : s - first);
-        const uint32_t sbuf = trow + C::kColS + 128u * buf;
+        const int buf = F == 1 ? s % 3 : grp, tile = sw.n0 + (nu == 2 ? (s - first) >> 1 : s - first);
+        const uint32_t sbuf = trow + C::kColS + 128u * buf, pbuf = F == 1 ? sbuf : trow + C::kColP + 64u * grp;
         ok = __all_sync(0xffffffffu, mbar_wait(s_full + 2 * grp + ((s >> 1) & 1), (s >> 2) & 1, abort));
         if (!ok) break;
         tc_fence_after();
@@ -528,44 +547,46 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
           total = ctx + info[slot].nodes;
           if (live) mask = info[slot].mask[t];
         }
-        uint32_t sc[NC];
-#pragma unroll
-        for (int c = 0; c < NC / 32; c++) tmem_ld32(sbuf + half * 64 + c * 32, *reinterpret_cast<uint32_t(*)[32]>(sc + 32 * c));
-        tmem_wait_ld();
-        if (F == 4) {  // the weights of the other half
-          const uint32_t z[16] = {0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
-          tmem_st16(sbuf + 32 * (1 - half), z);
-          tmem_st16(sbuf + 32 * (1 - half) + 16, z);
-        }
-        if ((tile + 1) * kTile > ctx) {  // the tile ends in the tree or behind it
-#pragma unroll
-          for (int c = 0; c < NC / 32; c++) {
-            const uint32_t see = tree_word(mask, tile * kTile + half * 64 + c * 32 - ctx);
-#pragma unroll
-            for (int x = 0; x < 32; x++)
-              if (!(see & (1u << x))) sc[32 * c + x] = 0xff800000u;
-          }
+        const bool edge = (tile + 1) * kTile > ctx;  // the tile ends in the tree or behind it
+        if (edge && total - tile * kTile < kTile) {
           // what lies behind the last position may be anything: its weight is 0, but 0 times a NaN is not
-          const int rem = total - tile * kTile, kt = k0 + tile - sw.n0;
-          if (rem < kTile) {
-            ok = __all_sync(0xffffffffu, mbar_wait(v_full + kt % SV, (kt / SV) & 1, abort));
-            if (!ok) break;
-            if (r >= rem) {
-              uint4* v = reinterpret_cast<uint4*>(smem + C::kOffV + kt % SV * TB + r * C::kSpan);
+          const int kt = k0 + tile - sw.n0;
+          ok = __all_sync(0xffffffffu, mbar_wait(v_full + kt % SV, (kt / SV) & 1, abort));
+          if (!ok) break;
+          if (r >= total - tile * kTile) {
+            uint4* v = reinterpret_cast<uint4*>(smem + C::kOffV + kt % SV * TB + r * C::kSpan);
 #pragma unroll
-              for (int c = 0; c < D / 8; c++) v[c] = make_uint4(0u, 0u, 0u, 0u);
-              fence_proxy_async_smem();
+            for (int c = 0; c < D / 8; c++) v[c] = make_uint4(0u, 0u, 0u, 0u);
+            fence_proxy_async_smem();
+          }
+        }
+        // 64 scores at a time, read once for the maximum and (but for the last 64) once more for the weights: with 128 in
+        // registers the loop does not fit the schedulers' instruction caches (warps then wait for instructions
+        // longer than they issue them)
+        uint32_t sc[64];
+        const auto load = [&](int h) {
+          tmem_ld32(sbuf + (half + h) * 64, *reinterpret_cast<uint32_t(*)[32]>(sc));
+          tmem_ld32(sbuf + (half + h) * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(sc + 32));
+          tmem_wait_ld();
+          if (edge) {
+#pragma unroll
+            for (int c = 0; c < 2; c++) {
+              const uint32_t see = tree_word(mask, tile * kTile + (half + h) * 64 + c * 32 - ctx);
+#pragma unroll
+              for (int x = 0; x < 32; x++)
+                if (!(see & (1u << x))) sc[32 * c + x] = 0xff800000u;
             }
           }
+        };
+        float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+        for (int h = 0; h < NC / 64; h++) {
+          load(h);
+#pragma unroll
+          for (int x = 0; x < 64; x += 2)
+            mx4[(x >> 1) & 3] = fmax3(mx4[(x >> 1) & 3], __uint_as_float(sc[x]), __uint_as_float(sc[x + 1]));
         }
-        float mx8[8];
-#pragma unroll
-        for (int x = 0; x < 8; x++) mx8[x] = -INFINITY;
-#pragma unroll
-        for (int x = 0; x < NC; x += 2)
-          mx8[(x >> 1) & 7] = fmax3(mx8[(x >> 1) & 7], __uint_as_float(sc[x]), __uint_as_float(sc[x + 1]));
-        const float mxr = fmaxf(fmaxf(fmaxf(mx8[0], mx8[1]), fmaxf(mx8[2], mx8[3])),
-                                fmaxf(fmaxf(mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])));
+        const float mxr = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
         float r_use = mxr, alpha = 1.f;
         if (s > mine) {
           r_use = r_run;
@@ -589,32 +610,53 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
           }
         }
         r_run = r_use;
+        if (F > 1 && s >= 2) {  // the weights of the step before have been read
+          ok = __all_sync(0xffffffffu, mbar_wait(o_done + 2 * grp + (((s - 2) >> 1) & 1), ((s - 2) >> 2) & 1, abort));
+          if (!ok) break;
+          tc_fence_after();
+        }
         m_use = r_use == -INFINITY ? 0.f : __fmul_rn(r_use, sl2);
         uint64_t sum4[4] = {0ull, 0ull, 0ull, 0ull};
         const uint64_t sl2x2 = f2(sl2, sl2), negm = f2(-m_use, -m_use), minus = f2(-1.f, -1.f);
-        // one code for both kinds of lanes: two of them side by side starve the schedulers of instructions
-#pragma unroll
-        for (int c = 0; c < NC / 16; c++) {
-          uint32_t ph[8], pl[8];
-#pragma unroll
-          for (int x = 0; x < 8; x++) {
-            const int k = 16 * c + 2 * x;
-            float x0, x1, l0, l1;
-            f2_split(f2_fma(f2(__uint_as_float(sc[k]), __uint_as_float(sc[k + 1])), sl2x2, negm), x0, x1);
-            const uint64_t pp = f2(ex2(x0), ex2(x1));
-            f2_split(pp, x0, x1);
-            ph[x] = pack_bf16(x0, x1);
-            f2_split(f2_fma(f2(bf_lo(ph[x]), bf_hi(ph[x])), minus, pp), l0, l1);
-            pl[x] = pack_bf16(l0, l1);
-            if (F > 1) ph[x] = low ? pl[x] : ph[x];
-            sum4[x & 3] = f2_add(sum4[x & 3], pp);
+#pragma unroll 1
+        for (int h = NC / 64 - 1; h >= 0; h--) {
+          if (h < NC / 64 - 1) load(h);
+          if (F > 1 && h == 0) {
+            tc_fence_before();
+            warp_arrive(pv_done + grp);
           }
-          tmem_st8(sbuf + half * 32 + 8 * c, ph);
-          if (F == 1) tmem_st8(sbuf + 64 + 8 * c, pl);
+          const uint32_t to = pbuf + (F == 1 ? 64 : 32) * (half + h);
+#pragma unroll
+          for (int c = 0; c < 4; c++) {
+            uint32_t ph[8], pl[8];
+            uint64_t pp[8];
+#pragma unroll
+            for (int x = 0; x < 8; x++) {
+              const int k = 16 * c + 2 * x;
+              float x0, x1;
+              f2_split(f2_fma(f2(__uint_as_float(sc[k]), __uint_as_float(sc[k + 1])), sl2x2, negm), x0, x1);
+              pp[x] = f2(ex2(x0), ex2(x1));
+              f2_split(pp[x], x0, x1);
+              ph[x] = pack_bf16(x0, x1);
+              sum4[x & 3] = f2_add(sum4[x & 3], pp[x]);
+            }
+            if (F == 1 || low) {
+#pragma unroll
+              for (int x = 0; x < 8; x++) {
+                float l0, l1;
+                f2_split(f2_fma(f2(bf_lo(ph[x]), bf_hi(ph[x])), minus, pp[x]), l0, l1);
+                (F == 1 ? pl : ph)[x] = pack_bf16(l0, l1);
+              }
+            }
+            tmem_st8(to + 8 * c, ph);
+            if (F == 1) tmem_st8(to + 32 + 8 * c, pl);
+          }
+          if (F == 1 || h == 0) {
+            tmem_wait_st();
+            tc_fence_before();
+            warp_arrive(p_ready + 4 * grp + 2 * ((s >> 1) & 1) + (F == 1 ? 1 - h : 0));
+          }
         }
-        tmem_wait_st();
-        tc_fence_before();
-        warp_arrive(p_ready + 2 * grp + ((s >> 1) & 1));
         float s0, s1, s2, s3, s4, s5, s6, s7;
         f2_split(sum4[0], s0, s1);
         f2_split(sum4[1], s2, s3);
