@@ -639,7 +639,7 @@ struct TreeWs {
 TreeWs tree_ws(int B, int R, int Hkv, int D) {
   const size_t rows = std::min(R, 2 * kTile);
   TreeWs w;
-  w.info = ws_up((size_t)B * Hkv * tree_tiles(R) * (kTile / tree_copies(R)) * D * 4);
+  w.info = ws_up((size_t)B * Hkv * tree_tiles(R) * tree_rows(R) * D * 4);
   w.part_o = w.info + ws_up(B * sizeof(TreeInfo));
   w.part_ml = w.part_o + ws_up(2 * kPagedMaxBlocks * rows * D * 4);
   w.cut = w.part_ml + ws_up(2 * kPagedMaxBlocks * rows * 8);

@@ -277,9 +277,8 @@ struct PagedTreeArgs {
 };
 inline int tree_tiles(int R) { return (R + kTile - 1) / kTile; }
 inline int tree_pairs(int R) { return (tree_tiles(R) + 1) / 2; }
-// Times that up to 64 rows are in their tile: each as the one that takes its weights' high parts and the one that
-// takes the low parts, up to 32 rows for each half of the keys.
-inline int tree_copies(int R) { return R > 64 ? 1 : (R > 32 ? 2 : 4); }
+// Rows of a tile: up to 64 have a lane for the high parts of their weights and one for the low parts.
+inline int tree_rows(int R) { return R > kTile / 2 ? kTile : kTile / 2; }
 
 // Attention of the newest tokens over a paged cache (see paged.cu).
 constexpr int kPagedMaxBlocks = 160;  // blocks of the sweep: bounds its partial results

@@ -14,10 +14,10 @@
 // of four softmax warps take the steps in turn, each with an O of its own.  With up to 128 rows the groups share the row
 // tile and take alternate key tiles (their two O are added at the end), with more each has one of the pair's.
 // A product of 128 rows and 64 columns takes the tensor cores as long as one of 128 columns (64 clocks for 16 keys), so
-// the two parts of the weights cost as much again as the two of the scores. Up to 64 rows are therefore twice in
-// their tile: the first copy's lanes hold the weights' high parts, the second's the low parts, and one product takes
-// both. Up to 32 rows are there four times, a pair of copies for each half of the tile's keys (its weights of the
-// other half are zeros), so that a thread has 64 scores and not 128.
+// the two parts of the weights cost as much again as the two of the scores. Up to 64 rows therefore have two lanes each:
+// of a warp's 32 lanes the first 16 hold the scores of its 16 rows and the high parts of their weights, the others the low
+// parts, and one product takes both. The warp reads the 16 lanes as a matrix fragment (two rows of four neighbouring
+// threads each), so that every thread works on half as many scores.
 // k_tree_prep packs the queries (normalised, rotated, two parts, laid out as the sweep has them in shared memory) and the trees.
 // A segment that is not the whole of its (sequence, head) leaves its parts to k_tree_join.
 #include "paged_sweep.cuh"
@@ -61,8 +61,8 @@ struct TreeCfg {
   static constexpr int kOffK = 4 * kTileBytes;  // Q first: two slots of (high, low), or a pair's two row tiles
   static constexpr int kOffV = kOffK + kKStages * kTileBytes;
   static constexpr int kBytes = kOffV + kVStages * kTileBytes;
-  // Tensor memory: group g's O at 64 g. With both parts of the weights in a lane (F == 1) step n has its S at 128 +
-  // 128 (n % 3), and P in its place; else a group has S at 128 + 128 g and P, 64 columns, at 384 + 64 g, so that
+  // Tensor memory: group g's O at 64 g. With both parts of the weights in one lane step n has its S at 128 +
+  // 128 (n % 3), and P in its place; with SPLIT a group has S at 128 + 128 g and P, 64 columns, at 384 + 64 g, so that
   // its next scores are worked out while it is on its weights.
   static constexpr uint32_t kColO = 0, kColS = 128, kColP = 384;
 };
@@ -180,12 +180,12 @@ __device__ __forceinline__ void put_columns(const PagedTreeArgs& a, size_t to, c
   }
 }
 
-// RT: row tiles of a pair (2: more than 128 rows), F: copies of the rows in the one tile (see above).
-template <int D, int RT, int F>
+// RT: row tiles of a pair (2: more than 128 rows). SPLIT: at most 64 rows, two lanes each (see above).
+template <int D, int RT, bool SPLIT>
 __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_constant__ PagedTreeArgs a) {
   using C = TreeCfg<D>;
   constexpr int SK = C::kKStages, SV = C::kVStages, TB = C::kTileBytes;
-  constexpr int NR = kTile / F, NC = F == 4 ? 64 : 128;  // rows of a copy, keys of a tile that it takes
+  constexpr int NR = SPLIT ? kTile / 2 : kTile;  // rows of a tile
   extern __shared__ uint8_t smem_raw[];
   uint8_t* head = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint64_t* q_full = reinterpret_cast<uint64_t*>(head);  // [2] the slot's queries are packed
@@ -195,8 +195,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
   uint64_t* v_full = k_empty + SK;         // [SV]
   uint64_t* v_empty = v_full + SV;         // [SV] the O += P V of the stage have completed
   uint64_t* s_full = v_empty + SV;         // [group][2] the group's steps in turn
-  uint64_t* p_ready = s_full + 4;          // [group][2][2] the weights (F == 1: of the tile's last 64 keys, and of the first)
-  uint64_t* pv_done = p_ready + 8;         // F == 1: [3] per buffer of S and P; else [group] the scores are in registers
+  uint64_t* p_ready = s_full + 4;          // [group][2][2] the weights of the tile's last 64 keys, and of the first (SPLIT: all)
+  uint64_t* pv_done = p_ready + 8;         // [3] per buffer of S and P; SPLIT: [group] the scores are in registers
   uint64_t* o_done = pv_done + 3;          // [group][2] the same per group's step, for the group
   uint64_t* part_full = o_done + 4;        // [group][2] the other group's part of a segment that this one finishes
   uint64_t* gsync = part_full + 4;         // [group]
@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
       mbar_init(part_full + k, 4);
     }
     for (int k = 0; k < 3; k++) {
-      mbar_init(pv_done + k, F == 1 ? 1 : 4);
+      mbar_init(pv_done + k, SPLIT ? 4 : 1);
       mbar_init(drain + k, 1);
     }
     fence_mbar_init();
@@ -385,17 +385,17 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
       bool qon = qs.next();
       const auto load = [&]() {  // the next segment's queries: its slot is free
         const int slot = slot_of(qe), nu = units(qs);
-        mbar_arrive_expect_tx(q_full + slot, (uint32_t)(nu * 2 * TB + sizeof(TreeInfo)));
+        constexpr uint32_t part = NR * C::kSpan, kBlocks = SPLIT ? 4 : 1, block = part / kBlocks;
+        mbar_arrive_expect_tx(q_full + slot, (uint32_t)(nu * 2 * part + sizeof(TreeInfo)));
         bulk_load(info + slot, a.info + qs.b, sizeof(TreeInfo), q_full + slot);
-        constexpr uint32_t part = NR * C::kSpan;
 #pragma unroll 1
         for (int u = 0; u < nu; u++) {
           const unsigned char* from = a.packed + (((size_t)qs.b * a.Hkv + qs.g / a.pairs) * a.tiles + qs.g % a.pairs * 2 + u) * 2 * part;
           uint8_t* to = smem + (RT == 1 ? 2 * slot : 2 * u) * TB;
 #pragma unroll
-          for (int f = 0; f < F; f++) {
-            bulk_load(to + f * part, from, part, q_full + slot);
-            bulk_load(to + TB + f * part, from + part, part, q_full + slot);
+          for (int f = 0; f < (int)kBlocks; f++) {  // the rows of a warp to the first half of its lanes
+            bulk_load(to + 2 * f * block, from + f * block, block, q_full + slot);
+            bulk_load(to + TB + 2 * f * block, from + part + f * block, block, q_full + slot);
           }
         }
         qe++;
@@ -418,8 +418,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
           if (!(ok = mbar_wait(k_full + st, (k / SK) & 1, abort))) break;
 #pragma unroll 1
           for (int u = 0; u < nu; u++, n++) {
-            // F == 1: the buffer's weights have been read; else: the group's scores
-            const int buf = F == 1 ? n % 3 : n & 1, use = F == 1 ? n / 3 : n >> 1;
+            // the buffer's weights have been read (SPLIT: the group's scores)
+            const int buf = SPLIT ? n & 1 : n % 3, use = SPLIT ? n >> 1 : n / 3;
             if (use > 0 && !(ok = mbar_wait(pv_done + buf, (use - 1) & 1, abort))) break;
             tc_fence_after();
             const uint64_t dq = dQ0 + (uint64_t)((RT == 1 ? 2 * slot : 2 * u) * tstep), dk = dK0 + (uint64_t)(st * tstep);
@@ -464,17 +464,17 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
           if (!(ok = mbar_wait(ready, (i >> 1) & 1, abort))) break;
           if (!(ok = mbar_wait(v_full + st, (kt / SV) & 1, abort))) break;
           const uint64_t dv = dV0 + (uint64_t)(st * tstep), dv2 = dv + (uint64_t)(4 * kStepMN);
-          const uint32_t p = F == 1 ? tmem + C::kColS + 128u * (n % 3) : tmem + C::kColP + 64u * grp;
-          constexpr uint32_t kHalf = F == 1 ? 64u : 32u;  // columns of P for 64 keys
+          const uint32_t p = SPLIT ? tmem + C::kColP + 64u * grp : tmem + C::kColS + 128u * (n % 3);
+          constexpr uint32_t kHalf = SPLIT ? 32u : 64u;  // columns of P for 64 keys
           tc_fence_after();
           mma_ts_chain<4, false>(o, p + kHalf, dv2, kStepMN, idPV, n - first >= 2 ? 1u : 0u);
-          if (F == 1) {
+          if (!SPLIT) {
             mma_ts_chain<4, false>(o, p + kHalf + 32u, dv2, kStepMN, idPV, 1u);
             if (!(ok = mbar_wait(ready + 1, (i >> 1) & 1, abort))) break;
             tc_fence_after();
           }
           mma_ts_chain<4, false>(o, p, dv, kStepMN, idPV, 1u);
-          if (F == 1) {
+          if (!SPLIT) {
             mma_ts_chain<4, false>(o, p + 32u, dv, kStepMN, idPV, 1u);
             mma_commit(pv_done + n % 3);
           }
@@ -496,20 +496,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
     // ------------------------------------------------------------ softmax group
     regs_inc<200>();
     const int grp = (warp - 4) >> 2, q4 = warp & 3;
-    const int r = q4 * 32 + lane, rr = r % NR;  // row of the tile: of the copy that takes
-    // the weights' low parts (F == 1: both), the groups' the other way round: a scheduler then has a warp of each kind
-    const bool low = F > 1 && ((r / NR) ^ grp) & 1;
-    const int half = F == 4 ? r / 64 : 0;  // this half of the keys
+    const int r = q4 * 32 + lane, rr = SPLIT ? q4 * 16 + (lane & 15) : r;  // lane of the tile and its row
     const uint32_t trow = tmem + ((uint32_t)(q4 * 32) << 16);
     const uint32_t obuf = trow + C::kColO + 64u * grp;
     const float sl2 = a.scale_log2;
-    if (F == 4) {  // the weights of the half that the lane does not take stay zeros
-      const uint32_t z[16] = {0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
-      const uint32_t zbuf = trow + C::kColP + 64u * grp + 32u * (1 - half);
-      tmem_st16(zbuf, z);
-      tmem_st16(zbuf + 16, z);
-      tmem_wait_st();
-    }
     bool ok = true;
     int n = 0, kt = 0, joined0 = 0, joined1 = 0, syncs = 0;  // steps, stages; segments that each group finished with the other; group barriers
     const auto group_sync = [&]() {
@@ -529,23 +519,29 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
       if (mine >= end) continue;
       const int pr = sw.g % a.pairs, u = nu == 2 ? (mine - first) & 1 : 0;
       const int row = pr * 2 * kTile + u * kTile + rr;        // row of the (sequence, head)
-      unsigned long long mask = 0;
       int ctx = 0, total = 0;
       bool live = false;
-      float r_run = 0.f, l_run = 0.f, m_use = 0.f;
+      // a thread's row, or (SPLIT) its two rows lane / 4 and lane / 4 + 8 of the warp's 16: mask, maximum, sum
+      constexpr int NQ = SPLIT ? 2 : 1;
+      unsigned long long mask[NQ];
+      float r_run[NQ], l_run[NQ], m_use[NQ];
       int s = mine;
       for (; s < end; s += 2) {
-        const int buf = F == 1 ? s % 3 : grp, tile = sw.n0 + (nu == 2 ? (s - first) >> 1 : s - first);
-        const uint32_t sbuf = trow + C::kColS + 128u * buf, pbuf = F == 1 ? sbuf : trow + C::kColP + 64u * grp;
+        const int buf = SPLIT ? grp : s % 3, tile = sw.n0 + (nu == 2 ? (s - first) >> 1 : s - first);
+        const uint32_t sbuf = trow + C::kColS + 128u * buf, pbuf = SPLIT ? trow + C::kColP + 64u * grp : sbuf;
         ok = __all_sync(0xffffffffu, mbar_wait(s_full + 2 * grp + ((s >> 1) & 1), (s >> 2) & 1, abort));
         if (!ok) break;
         tc_fence_after();
         if (s == mine) {
+          const auto token = [&](int x) { return x < a.R ? (int)fdiv((uint32_t)x, a.div_g) : kTreeMax; };
           ctx = info[slot].ctx;
-          const int t = row < a.R ? (int)fdiv((uint32_t)row, a.div_g) : kTreeMax;
-          live = t < info[slot].nodes;
           total = ctx + info[slot].nodes;
-          if (live) mask = info[slot].mask[t];
+          live = token(row) < info[slot].nodes;
+#pragma unroll
+          for (int i = 0; i < NQ; i++) {
+            const int t = token(SPLIT ? q4 * 16 + lane / 4 + 8 * i : row);
+            mask[i] = t < info[slot].nodes ? info[slot].mask[t] : 0ull;
+          }
         }
         const bool edge = (tile + 1) * kTile > ctx;  // the tile ends in the tree or behind it
         if (edge && total - tile * kTile < kTile) {
@@ -560,110 +556,173 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
             fence_proxy_async_smem();
           }
         }
-        // 64 scores at a time, read once for the maximum and (but for the last 64) once more for the weights: with 128 in
-        // registers the loop does not fit the schedulers' instruction caches (warps then wait for instructions
-        // longer than they issue them)
+        // 64 scores of a thread at a time. With one row and 128 they are read once for the maximum and (but for the last 64)
+        // once more for the weights: with all in registers the loop does not fit the schedulers' instruction caches
+        // (warps then wait for instructions longer than they issue them).
         uint32_t sc[64];
         const auto load = [&](int h) {
-          tmem_ld32(sbuf + (half + h) * 64, *reinterpret_cast<uint32_t(*)[32]>(sc));
-          tmem_ld32(sbuf + (half + h) * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(sc + 32));
+          uint32_t(&lo)[32] = *reinterpret_cast<uint32_t(*)[32]>(sc);
+          uint32_t(&hi)[32] = *reinterpret_cast<uint32_t(*)[32]>(sc + 32);
+          if (SPLIT) {
+            tmem_ld16x64(sbuf, lo);
+            tmem_ld16x64(sbuf + 64, hi);
+          } else {
+            tmem_ld32(sbuf + h * 64, lo);
+            tmem_ld32(sbuf + h * 64 + 32, hi);
+          }
           tmem_wait_ld();
-          if (edge) {
+          if (edge && SPLIT) {
+#pragma unroll
+            for (int c = 0; c < 4; c++) {
+              const int at = tile * kTile + c * 32 - ctx;
+              const uint32_t see[2] = {tree_word(mask[0], at) >> (2 * (lane & 3)), tree_word(mask[NQ - 1], at) >> (2 * (lane & 3))};
+#pragma unroll
+              for (int x = 0; x < 16; x++)  // columns 8 (x / 4) + 2 (lane % 4) + x % 2 of the 32, row x / 2 % 2
+                if (!(see[x / 2 % 2] & (1u << (8 * (x / 4) + x % 2)))) sc[16 * c + x] = 0xff800000u;
+            }
+          } else if (edge) {
 #pragma unroll
             for (int c = 0; c < 2; c++) {
-              const uint32_t see = tree_word(mask, tile * kTile + (half + h) * 64 + c * 32 - ctx);
+              const uint32_t see = tree_word(mask[0], tile * kTile + h * 64 + c * 32 - ctx);
 #pragma unroll
               for (int x = 0; x < 32; x++)
                 if (!(see & (1u << x))) sc[32 * c + x] = 0xff800000u;
             }
           }
         };
-        float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll 1
-        for (int h = 0; h < NC / 64; h++) {
-          load(h);
+        float mxr[NQ];
+        if (SPLIT) {
+          load(0);
+          tc_fence_before();
+          warp_arrive(pv_done + grp);
+          float m2[2][2] = {{-INFINITY, -INFINITY}, {-INFINITY, -INFINITY}};
 #pragma unroll
           for (int x = 0; x < 64; x += 2)
-            mx4[(x >> 1) & 3] = fmax3(mx4[(x >> 1) & 3], __uint_as_float(sc[x]), __uint_as_float(sc[x + 1]));
+            m2[(x >> 1) & 1][(x >> 2) & 1] = fmax3(m2[(x >> 1) & 1][(x >> 2) & 1], __uint_as_float(sc[x]), __uint_as_float(sc[x + 1]));
+#pragma unroll
+          for (int i = 0; i < NQ; i++) {
+            float m = fmaxf(m2[i][0], m2[i][1]);
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+            mxr[i] = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+          }
+        } else {
+          float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+          for (int h = 0; h < 2; h++) {
+            load(h);
+#pragma unroll
+            for (int x = 0; x < 64; x += 2)
+              mx4[(x >> 1) & 3] = fmax3(mx4[(x >> 1) & 3], __uint_as_float(sc[x]), __uint_as_float(sc[x + 1]));
+          }
+          mxr[0] = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
         }
-        const float mxr = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
-        float r_use = mxr, alpha = 1.f;
-        if (s > mine) {
-          r_use = r_run;
-          const float r_new = fmaxf(r_run, mxr), m_old = __fmul_rn(r_run, sl2), m_new = __fmul_rn(r_new, sl2);
+        float alpha[NQ];
+        if (s == mine) {
+#pragma unroll
+          for (int i = 0; i < NQ; i++) {
+            r_run[i] = mxr[i];
+            alpha[i] = 0.f;
+            l_run[i] = 0.f;
+          }
+        } else {
           // O and the sum follow the maximum only when some row's grew by more than 2^8 (or came out of nothing)
-          if (__any_sync(0xffffffffu, m_new > m_old + 8.0f)) {
+          bool grow = false;
+#pragma unroll
+          for (int i = 0; i < NQ; i++) {
+            alpha[i] = 1.f;
+            grow = grow || __fmul_rn(fmaxf(r_run[i], mxr[i]), sl2) > __fmul_rn(r_run[i], sl2) + 8.0f;
+          }
+          if (__any_sync(0xffffffffu, grow)) {
             ok = __all_sync(0xffffffffu, mbar_wait(o_done + 2 * grp + (((s - 2) >> 1) & 1), ((s - 2) >> 2) & 1, abort));
             if (!ok) break;
             tc_fence_after();
-            r_use = r_new;
-            alpha = r_run == -INFINITY ? 0.f : ex2(m_old - m_new);
+#pragma unroll
+            for (int i = 0; i < NQ; i++) {
+              const float r_new = fmaxf(r_run[i], mxr[i]);
+              alpha[i] = r_run[i] == -INFINITY ? 0.f : ex2(__fmul_rn(r_run[i], sl2) - __fmul_rn(r_new, sl2));
+              r_run[i] = r_new;
+            }
+            float lane_a = alpha[0];  // of the lane's row
+            if (SPLIT) {
+              const float x = __shfl_sync(0xffffffffu, alpha[0], 4 * (lane & 7)), y = __shfl_sync(0xffffffffu, alpha[NQ - 1], 4 * (lane & 7));
+              lane_a = lane & 8 ? y : x;
+            }
 #pragma unroll 1
             for (int c = 0; c < D / 16; c++) {
               uint32_t w[16];
               tmem_ld16(obuf + c * 16, w);
               tmem_wait_ld();
 #pragma unroll
-              for (int x = 0; x < 16; x++) w[x] = __float_as_uint(__uint_as_float(w[x]) * alpha);
+              for (int x = 0; x < 16; x++) w[x] = __float_as_uint(__uint_as_float(w[x]) * lane_a);
               tmem_st16(obuf + c * 16, w);
             }
           }
         }
-        r_run = r_use;
-        if (F > 1 && s >= 2) {  // the weights of the step before have been read
+        if (SPLIT && s >= 2) {  // the weights of the step before have been read
           ok = __all_sync(0xffffffffu, mbar_wait(o_done + 2 * grp + (((s - 2) >> 1) & 1), ((s - 2) >> 2) & 1, abort));
           if (!ok) break;
           tc_fence_after();
         }
-        m_use = r_use == -INFINITY ? 0.f : __fmul_rn(r_use, sl2);
-        uint64_t sum4[4] = {0ull, 0ull, 0ull, 0ull};
-        const uint64_t sl2x2 = f2(sl2, sl2), negm = f2(-m_use, -m_use), minus = f2(-1.f, -1.f);
-#pragma unroll 1
-        for (int h = NC / 64 - 1; h >= 0; h--) {
-          if (h < NC / 64 - 1) load(h);
-          if (F > 1 && h == 0) {
-            tc_fence_before();
-            warp_arrive(pv_done + grp);
-          }
-          const uint32_t to = pbuf + (F == 1 ? 64 : 32) * (half + h);
+        uint64_t sum[NQ][4 / NQ], negm[NQ];
 #pragma unroll
-          for (int c = 0; c < 4; c++) {
-            uint32_t ph[8], pl[8];
-            uint64_t pp[8];
+        for (int i = 0; i < NQ; i++) {
+          m_use[i] = r_run[i] == -INFINITY ? 0.f : __fmul_rn(r_run[i], sl2);
+          negm[i] = f2(-m_use[i], -m_use[i]);
 #pragma unroll
-            for (int x = 0; x < 8; x++) {
-              const int k = 16 * c + 2 * x;
-              float x0, x1;
-              f2_split(f2_fma(f2(__uint_as_float(sc[k]), __uint_as_float(sc[k + 1])), sl2x2, negm), x0, x1);
-              pp[x] = f2(ex2(x0), ex2(x1));
-              f2_split(pp[x], x0, x1);
-              ph[x] = pack_bf16(x0, x1);
-              sum4[x & 3] = f2_add(sum4[x & 3], pp[x]);
-            }
-            if (F == 1 || low) {
-#pragma unroll
-              for (int x = 0; x < 8; x++) {
-                float l0, l1;
-                f2_split(f2_fma(f2(bf_lo(ph[x]), bf_hi(ph[x])), minus, pp[x]), l0, l1);
-                (F == 1 ? pl : ph)[x] = pack_bf16(l0, l1);
-              }
-            }
-            tmem_st8(to + 8 * c, ph);
-            if (F == 1) tmem_st8(to + 32 + 8 * c, pl);
-          }
-          if (F == 1 || h == 0) {
-            tmem_wait_st();
-            tc_fence_before();
-            warp_arrive(p_ready + 4 * grp + 2 * ((s >> 1) & 1) + (F == 1 ? 1 - h : 0));
-          }
+          for (int j = 0; j < 4 / NQ; j++) sum[i][j] = 0ull;
         }
-        float s0, s1, s2, s3, s4, s5, s6, s7;
-        f2_split(sum4[0], s0, s1);
-        f2_split(sum4[1], s2, s3);
-        f2_split(sum4[2], s4, s5);
-        f2_split(sum4[3], s6, s7);
-        const float l = ((s0 + s1) + (s2 + s3)) + ((s4 + s5) + (s6 + s7));
-        l_run = s > mine ? fmaf(l_run, alpha, l) : l;
+        const uint64_t sl2x2 = f2(sl2, sl2), minus = f2(-1.f, -1.f);
+#pragma unroll 1
+        for (int h = 1; h >= (SPLIT ? 1 : 0); h--) {
+          if (h == 0) load(0);
+          uint32_t ph[32], pl[32];
+#pragma unroll
+          for (int x = 0; x < 32; x++) {
+            constexpr int kSums = 4 / NQ;
+            const int i = SPLIT ? x & 1 : 0, j = (SPLIT ? x >> 1 : x) % kSums;
+            float x0, x1, l0, l1;
+            f2_split(f2_fma(f2(__uint_as_float(sc[2 * x]), __uint_as_float(sc[2 * x + 1])), sl2x2, negm[i]), x0, x1);
+            const uint64_t pp = f2(ex2(x0), ex2(x1));
+            f2_split(pp, x0, x1);
+            ph[x] = pack_bf16(x0, x1);
+            f2_split(f2_fma(f2(bf_lo(ph[x]), bf_hi(ph[x])), minus, pp), l0, l1);
+            pl[x] = pack_bf16(l0, l1);
+            sum[i][j] = f2_add(sum[i][j], pp);
+            if (!SPLIT && x % 8 == 7) {
+              tmem_st8(pbuf + 64 * h + x - 7, *reinterpret_cast<uint32_t(*)[8]>(ph + x - 7));
+              tmem_st8(pbuf + 64 * h + 32 + x - 7, *reinterpret_cast<uint32_t(*)[8]>(pl + x - 7));
+            }
+            if (SPLIT && x % 16 == 15) {
+              tmem_st16x32(pbuf + 2 * (x - 15), *reinterpret_cast<uint32_t(*)[16]>(ph + x - 15));
+              tmem_st16x32(pbuf + (16u << 16) + 2 * (x - 15), *reinterpret_cast<uint32_t(*)[16]>(pl + x - 15));
+            }
+          }
+          tmem_wait_st();
+          tc_fence_before();
+          warp_arrive(p_ready + 4 * grp + 2 * ((s >> 1) & 1) + (h == 0 ? 1 : 0));
+        }
+#pragma unroll
+        for (int i = 0; i < NQ; i++) {
+          uint64_t t = f2_add(sum[i][0], sum[i][1]);
+          if (NQ == 1) t = f2_add(t, f2_add(sum[i][4 / NQ - 2], sum[i][4 / NQ - 1]));
+          float x, y;
+          f2_split(t, x, y);
+          l_run[i] = fmaf(l_run[i], alpha[i], x + y);
+        }
+      }
+      float lane_m = m_use[0], lane_l = l_run[0];  // of the lane's row
+      if (SPLIT) {
+        float m2[2], l2[2];
+#pragma unroll
+        for (int i = 0; i < NQ; i++) {
+          float l = l_run[i];
+          l += __shfl_xor_sync(0xffffffffu, l, 1);
+          l += __shfl_xor_sync(0xffffffffu, l, 2);
+          l2[i] = __shfl_sync(0xffffffffu, l, 4 * (lane & 7));
+          m2[i] = __shfl_sync(0xffffffffu, m_use[i], 4 * (lane & 7));
+        }
+        lane_m = lane & 8 ? m2[1] : m2[0];
+        lane_l = lane & 8 ? l2[1] : l2[0];
       }
       if (!ok) break;
       // the segment's unnormalised O, maximum (log2 units) and sum
@@ -687,7 +746,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
             scratch[chunk(c * 4 + q)] = make_float4(__uint_as_float(w[4 * q]), __uint_as_float(w[4 * q + 1]),
                                                     __uint_as_float(w[4 * q + 2]), __uint_as_float(w[4 * q + 3]));
         }
-        ml_other[slot * kTile + r] = make_float2(m_use, l_run);
+        ml_other[slot * kTile + r] = make_float2(lane_m, lane_l);
         tc_fence_before();
         warp_arrive(part_full + 2 * last + (turn & 1));
         continue;
@@ -695,13 +754,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
       const bool whole = sw.n0 == 0 && sw.n1 == sw.nt;
       const size_t part = (size_t)(2 * blk + (sw.n0 > 0 ? 0 : 1)) * a.rows;
       const int g = sw.g / a.pairs;
-      float M = m_use, L = l_run, mine_f = 1.f, other_f = 0.f;
+      float M = lane_m, L = lane_l, mine_f = 1.f, other_f = 0.f;
       if (joint) {
         ok = __all_sync(0xffffffffu, mbar_wait(part_full + 2 * grp + (turn & 1), (turn >> 1) & 1, abort));
         if (!ok) break;
         const float2 z = ml_other[slot * kTile + r];
         M = L == 0.f ? z.x : (z.y == 0.f ? M : fmaxf(M, z.x));
-        mine_f = L == 0.f ? 0.f : ex2(m_use - M);
+        mine_f = L == 0.f ? 0.f : ex2(lane_m - M);
         other_f = z.y == 0.f ? 0.f : ex2(z.x - M);
         L = fmaf(L, mine_f, z.y * other_f);
       }
@@ -720,7 +779,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
           v[4 * q + 2] = fmaf(__uint_as_float(w[4 * q + 2]), mine_f, y.z * other_f);
           v[4 * q + 3] = fmaf(__uint_as_float(w[4 * q + 3]), mine_f, y.w * other_f);
         }
-        if (F > 1) {
+        if (SPLIT) {
 #pragma unroll
           for (int q = 0; q < 4; q++)
             scratch[chunk(c * 4 + q)] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
@@ -736,28 +795,19 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
         }
       }
       tc_fence_before();
-      if (F > 1) {
-        // the copies of a row: a thread takes four of its columns
+      if (SPLIT) {
+        // a row's two lanes: a thread takes four of its columns
         ml_own[grp * kTile + r] = make_float2(M, L);
         if (!(ok = group_sync())) break;
         const float4* all = reinterpret_cast<const float4*>(smem + 2 * slot * TB);
         for (int i = r; i < a.R * (D / 4); i += kTile) {
-          const int ro = i / (D / 4), q = i % (D / 4), t = (int)fdiv((uint32_t)ro, a.div_g);
+          const int ro = i / (D / 4), q = i % (D / 4), t = (int)fdiv((uint32_t)ro, a.div_g), at = 32 * (ro / 16) + ro % 16;
+          const float2 z = ml_own[grp * kTile + at];
+          const float4 x0 = all[at * (D / 4) + (q ^ (at & 7))], x1 = all[(at + 16) * (D / 4) + (q ^ (at & 7))];
           RowSum x;
-#pragma unroll
-          for (int y = 0; y < F / 2; y++) {
-            const float2 z = ml_own[grp * kTile + ro + y * 64];
-            if (z.y != 0.f) x.M = fmaxf(x.M, z.x);
-          }
-#pragma unroll
-          for (int y = 0; y < F / 2; y++) {
-            const int at = ro + y * 64, below = at + NR;  // the high parts' lane and the low parts'; both have the row's sum
-            x.add(x.M, ml_own[grp * kTile + at], all[at * (D / 4) + (q ^ (at & 7))]);
-            const float2 z = ml_own[grp * kTile + below];
-            const float4 v = all[below * (D / 4) + (q ^ (below & 7))];
-            const float k = z.y == 0.f ? 0.f : ex2(z.x - x.M);
-            x.v = make_float4(fmaf(k, v.x, x.v.x), fmaf(k, v.y, x.v.y), fmaf(k, v.z, x.v.z), fmaf(k, v.w, x.v.w));
-          }
+          x.M = z.x;
+          x.S = z.y;
+          x.v = make_float4(x0.x + x1.x, x0.y + x1.y, x0.z + x1.z, x0.w + x1.w);
           if (t >= info[slot].nodes) x.S = 0.f, x.v = make_float4(0.f, 0.f, 0.f, 0.f);
           if (whole) {
             write_row<D>(a, sw.b, g, ro, q, x.v, x.M, x.S);
@@ -827,31 +877,30 @@ __global__ void __launch_bounds__(128) k_tree_join(const __grid_constant__ Paged
   write_row<D>(a, cut.x, g, r0 + row, q, x.v, x.M, x.S);
 }
 
-template <int D, int RT, int F>
+template <int D, int RT, bool SPLIT>
 cudaError_t launch_tree_t(const PagedTreeArgs& a, int grid, cudaStream_t s) {
   static bool attr_set[64] = {};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!attr_set[dev]) {
-    const cudaError_t e = cudaFuncSetAttribute(k_tree_sweep<D, RT, F>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
+    const cudaError_t e = cudaFuncSetAttribute(k_tree_sweep<D, RT, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
     if (e != cudaSuccess) return e;
     attr_set[dev] = true;
   }
   const int bytes = tree_head(a.B) + TreeCfg<D>::kBytes + 1024;
   if (bytes > kSmemMax) return cudaErrorInvalidValue;
-  constexpr int rows = kTile / F;
+  constexpr int rows = SPLIT ? kTile / 2 : kTile;
   const long long chunks = (long long)a.Hkv * a.tiles * rows * (D / 8);
   k_tree_prep<D><<<dim3((unsigned)((chunks + 127) / 128), (unsigned)a.B), 128, 0, s>>>(a, rows);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  if ((e = launch_pdl(k_tree_sweep<D, RT, F>, dim3((unsigned)grid), kTreeThreads, (size_t)bytes, s, a)) != cudaSuccess) return e;
+  if ((e = launch_pdl(k_tree_sweep<D, RT, SPLIT>, dim3((unsigned)grid), kTreeThreads, (size_t)bytes, s, a)) != cudaSuccess) return e;
   return launch_pdl(k_tree_join<D>, dim3((unsigned)grid, (unsigned)((a.rows + 512 / D - 1) / (512 / D))), 128, 0, s, a);
 }
 template <int D>
 cudaError_t launch_tree(const PagedTreeArgs& a, int grid, cudaStream_t s) {
-  if (a.R > kTile) return launch_tree_t<D, 2, 1>(a, grid, s);
-  const int copies = tree_copies(a.R);
-  return copies == 1 ? launch_tree_t<D, 1, 1>(a, grid, s) : (copies == 2 ? launch_tree_t<D, 1, 2>(a, grid, s) : launch_tree_t<D, 1, 4>(a, grid, s));
+  if (a.R > kTile) return launch_tree_t<D, 2, false>(a, grid, s);
+  return tree_rows(a.R) == kTile ? launch_tree_t<D, 1, false>(a, grid, s) : launch_tree_t<D, 1, true>(a, grid, s);
 }
 
 }  // namespace
