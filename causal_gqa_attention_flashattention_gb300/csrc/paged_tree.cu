@@ -71,7 +71,7 @@ static_assert(sizeof(TreeInfo) % 16 == 0, "copied in one piece");
 constexpr int kTreeCum = kTreeMl + 4 * kTile * 8;
 static_assert(kTreeInfo + 2 * sizeof(TreeInfo) <= kTreeMl && kTreePlan + sizeof(SweepPlan) <= kTreeSums, "head");
 static_assert((4 + 2 * TreeCfg<32>::kKStages + 2 * TreeCfg<32>::kVStages + 4 + 8 + 3 + 4 + 4 + 2 + 3) * 8 <= kTreeVars, "barriers");
-__host__ __device__ constexpr int tree_head(int B) { return (kTreeCum + (B + 1) * 4 + 1023) / 1024 * 1024; }
+__host__ __device__ constexpr int tree_head(int B) { return (kTreeCum + (B + 1) * 4 + B + 1023) / 1024 * 1024; }
 
 // The tile's bits of a mask over positions that begins `r` positions before position 0 of the tree (r < 0: in the
 // context, all ones): 32 columns from there.
@@ -86,15 +86,13 @@ __device__ __forceinline__ unsigned long long shfl64(unsigned long long x, int l
 }
 
 // Tokens lane and lane + 32 of a tree: masks of ancestors by doubling (after k rounds a token's mask holds itself and
-// 2^k - 1 ancestors, `up` the next one).
-__device__ __forceinline__ void tree_masks(const int* parents, int nodes, int lane, int* status,
-                                           unsigned long long (&mask)[2]) {
-  int up[2];
+// 2^k - 1 ancestors, `up`, their parents at first, the next one).
+__device__ __forceinline__ void tree_masks(int (&up)[2], int nodes, int lane, int* status, unsigned long long (&mask)[2]) {
 #pragma unroll
   for (int h = 0; h < 2; h++) {
     const int t = lane + 32 * h;
     mask[h] = t < nodes ? 1ull << t : 0ull;
-    up[h] = t < nodes ? parents[t] : -1;
+    if (t >= nodes) up[h] = -1;
     if (up[h] < -1 || up[h] >= t) {
       if (status) record_tree(status);
       up[h] = -1;
@@ -136,9 +134,12 @@ __global__ void __launch_bounds__(128) k_tree_prep(const __grid_constant__ Paged
   if (in) x.v = load_rope_chunk<D>(a.q + (size_t)(b * a.Tq + t) * a.q_stride + (g * a.G + (r - t * a.G)) * D, c, a.rope_half != 0);
   uint4 wv = make_uint4(0, 0, 0, 0);
   if (a.qw) wv = load_rope_chunk<D>(a.qw, c, a.rope_half != 0);
+  int up[2];
+#pragma unroll
+  for (int h = 0; h < 2; h++) up[h] = lane + 32 * h < a.Tq ? a.parents[b * a.parent_stride + lane + 32 * h] : -1;
   const TreeShape s = tree_shape(a, b, i == 0);
   unsigned long long mask[2];
-  tree_masks(a.parents + b * a.parent_stride, s.nodes, lane, i < 32 ? a.status : nullptr, mask);
+  tree_masks(up, s.nodes, lane, i < 32 ? a.status : nullptr, mask);
   const int depth[2] = {__popcll(mask[0]) - 1, __popcll(mask[1]) - 1};
   const int d0 = __shfl_sync(0xffffffffu, depth[0], t & 31), d1 = __shfl_sync(0xffffffffu, depth[1], t & 31);
   x.on = in && t < s.nodes;
@@ -209,6 +210,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
   float2* ml_other = reinterpret_cast<float2*>(head + kTreeMl);    // [2][128] per slot
   float2* ml_own = ml_other + 2 * kTile;                           // [2][128] per group
   int* cum = reinterpret_cast<int*>(head + kTreeCum);
+  uint8_t* pad = reinterpret_cast<uint8_t*>(cum + a.B + 1);  // positions that a sequence's last tile lacks
   uint8_t* smem = head + tree_head(a.B);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, blk = (int)blockIdx.x;
   if (tid == 0) {
@@ -242,7 +244,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
   if (warp == 1) tmem_alloc(tmem_slot, 512);
   running_costs<kTreeThreads>(a.B, cum, wsum, tid, [&](int b) {
     const TreeShape x = tree_shape(a, b, blk == 0);
-    return kTreeOver + max(1, (x.len + kTile - 1) / kTile);  // one even where nothing is read: its rows are written
+    const int nt = max(1, (x.len + kTile - 1) / kTile);  // one even where nothing is read: its rows are written
+    pad[b] = (uint8_t)(nt * kTile - x.len);
+    return kTreeOver + nt;
   });
   Tiles tl;
   tl.cum = cum;
@@ -277,11 +281,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
     const uint32_t pbytes = (uint32_t)prows * C::kSpan;
     // Page numbers 32 at a time, one to a lane, a window ahead: num_pages (outside the pool, read as zeros)
     // for a bad page and behind the last position.
-    const auto window = [&](int b, int len, int w) {
+    const auto window = [&](const SegWalk<kTreeOver>& x, int w) {
       const int i = w * 32 + lane;
       int id = a.num_pages;
-      if ((i << a.page_shift) < len) {
-        id = a.table[(size_t)b * a.max_pages + i];
+      if ((i << a.page_shift) < x.nt * kTile - pad[x.b]) {
+        id = a.table[(size_t)x.b * a.max_pages + i];
         if (id < 0 || id >= a.num_pages) {
           record_page(a.status);
           id = a.num_pages;
@@ -292,11 +296,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
     const auto page_of = [&](int n) { return (n * kTile) >> a.page_shift; };
     SegWalk<kTreeOver> ls = sw;  // the segment of the next window
     bool lon = ls.next();
-    int lw = 0, llen = 0, id = 0, nid = 0;
+    int lw = 0, id = 0, nid = 0;
     if (lon) {
       lw = page_of(ls.n0) >> 5;
-      llen = tree_shape(a, ls.b, false).len;
-      nid = window(ls.b, llen, lw);
+      nid = window(ls, lw);
     }
     const auto look = [&]() {
       id = nid;
@@ -305,12 +308,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
         lw++;
       } else {
         lon = ls.next();
-        if (lon) {
-          lw = page_of(ls.n0) >> 5;
-          llen = tree_shape(a, ls.b, false).len;
-        }
+        if (lon) lw = page_of(ls.n0) >> 5;
       }
-      if (lon) nid = window(ls.b, llen, lw);
+      if (lon) nid = window(ls, lw);
     };
     SweepPlan plan;
     plan.base = splan->base;
