@@ -267,8 +267,8 @@ struct PagedTreeArgs {
   float* lse;                   // or null
   float* part_o;                // [2 blocks, rows, D] unnormalised O of a block's first and last segment (workspace)
   float2* part_ml;              // [2 blocks, rows] their maximum (log2 units) and sum
-  int4* cut;                    // [blocks] the (sequence, head) that is cut and begins in the block: sequence (-1: none),
-                                // head, last block (workspace)
+  int4* cut;                    // [blocks] the cut (sequence, head) that begins in the block or goes through it: sequence
+                                // (-1: none), head, first and last block (workspace)
   long long q_stride, parent_stride;
   int B, Tq, Hq, Hkv, D, G, R, page_shift, num_pages, max_pages, rope_half, o_fp32;
   int tiles, pairs, rows;       // 128-row tiles of a head's queries, pairs of them, rows of the largest pair

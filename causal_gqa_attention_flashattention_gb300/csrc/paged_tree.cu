@@ -279,19 +279,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
     const uint64_t policy = evict_first();
     const int prows = min(1 << a.page_shift, kTile), per = kTile / prows;
     const uint32_t pbytes = (uint32_t)prows * C::kSpan;
-    // Page numbers 32 at a time, one to a lane, a window ahead: num_pages (outside the pool, read as zeros)
-    // for a bad page and behind the last position.
+    // Page numbers 32 at a time, one to a lane, a window ahead; behind the last position num_pages, outside the
+    // pool, which is read as zeros.
     const auto window = [&](const SegWalk<kTreeOver>& x, int w) {
       const int i = w * 32 + lane;
-      int id = a.num_pages;
-      if ((i << a.page_shift) < x.nt * kTile - pad[x.b]) {
-        id = a.table[(size_t)x.b * a.max_pages + i];
-        if (id < 0 || id >= a.num_pages) {
-          record_page(a.status);
-          id = a.num_pages;
-        }
-      }
-      return id;
+      return (i << a.page_shift) < x.nt * kTile - pad[x.b] ? a.table[(size_t)x.b * a.max_pages + i] : a.num_pages;
     };
     const auto page_of = [&](int n) { return (n * kTile) >> a.page_shift; };
     SegWalk<kTreeOver> ls = sw;  // the segment of the next window
@@ -302,7 +294,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
       nid = window(ls, lw);
     }
     const auto look = [&]() {
-      id = nid;
+      id = nid;  // looked at only now: the next window's are still on their way
+      if (id < 0 || id > a.num_pages || (id == a.num_pages && (lw * 32 + lane) << a.page_shift < ls.nt * kTile - pad[ls.b])) {
+        record_page(a.status);
+        id = a.num_pages;
+      }
       if (!lon) return;
       if (lw < page_of(ls.n1 - 1) >> 5) {
         lw++;
@@ -321,8 +317,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
     int k = 0;  // tiles so far
     while (ok && sw.next()) {
       const int kvh = sw.g / a.pairs;
-      if (sw.n0 == 0 && sw.n1 < sw.nt)
-        cut = make_int4(sw.b, sw.g, tl.last(plan, cum[sw.b] * tl.Hkv + sw.g * (sw.nt + tl.over), sw.nt), 0);
+      if (sw.n1 < sw.nt) {  // a cut one that begins here, or goes through the whole stretch
+        const int s0 = cum[sw.b] * tl.Hkv + sw.g * (sw.nt + tl.over);
+        cut = make_int4(sw.b, sw.g, sw.n0 == 0 ? blk : tl.first(plan, s0), tl.last(plan, s0, sw.nt));
+      }
       int win = -1;
 #pragma unroll 1
       for (int n = sw.n0; ok && n < sw.n1; n++, k++) {
@@ -843,38 +841,58 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
   }
 }
 
-// The cut (sequence, head)s: block c has the one that begins in the sweep's block c, a thread four columns of a
-// row, its parts in order.
+// The cut (sequence, head)s: one that lies in the sweep's blocks c .. c + n is joined by n columns of this grid, each
+// of which finds it with one load. A thread, or four neighbouring ones where there are many parts, takes four columns of a
+// row, its parts in order (each its own share, then thread by thread: the same sum whichever block does it).
+constexpr int kJoinThreads = 128, kJoinSlices = 8;
 template <int D>
-__global__ void __launch_bounds__(128) k_tree_join(const __grid_constant__ PagedTreeArgs a) {
+__global__ void __launch_bounds__(kJoinThreads) k_tree_join(const __grid_constant__ PagedTreeArgs a) {
+  const int tid = threadIdx.x;
   pdl_wait();
-  const int c0 = blockIdx.x, q = threadIdx.x % (D / 4), row = blockIdx.y * (512 / D) + threadIdx.x / (D / 4);
-  const int4 cut = a.cut[c0];
+  const int4 cut = __ldcg(a.cut + blockIdx.x);
   if (cut.x < 0) return;
-  const int g = cut.y / a.pairs, r0 = cut.y % a.pairs * 2 * kTile;
-  if (row >= a.rows || r0 + row >= a.R) return;
+  const int first = cut.z, last = cut.w, slice = ((int)blockIdx.x - first) * kJoinSlices + (int)blockIdx.y;
+  const int share = (last - first) * kJoinSlices, parts = last - first + 1;
+  const int g = cut.y / a.pairs, r0 = cut.y % a.pairs * 2 * kTile, rows = min(a.rows, a.R - r0);
   constexpr int kAhead = 8;
-  RowSum x;
-  for (int c = c0; c <= cut.z; c += kAhead) {
-    float2 z[kAhead];
-    float4 v[kAhead];
+  const int split = parts > kAhead ? 4 : 1, sub = tid & (split - 1), items = rows * (D / 4);
+  for (int i0 = (slice * kJoinThreads + tid) / split; i0 - tid / split < items; i0 += share * kJoinThreads / split) {
+    const int i = min(i0, items - 1), row = i / (D / 4), q = i % (D / 4);
+    RowSum x;
+    for (int c = first + sub; c <= last; c += kAhead * split) {
+      float2 z[kAhead];
+      float4 v[kAhead];
 #pragma unroll
-    for (int e = 0; e < kAhead; e++) {
-      const size_t at = (size_t)(2 * min(c + e, cut.z) + (c + e == c0 ? 1 : 0)) * a.rows + row;
-      z[e] = __ldcg(a.part_ml + at);
-      v[e] = __ldcg(reinterpret_cast<const float4*>(a.part_o + at * D) + q);
-      if (c + e > cut.z) z[e].y = 0.f;
+      for (int e = 0; e < kAhead; e++) {
+        z[e] = make_float2(-INFINITY, 0.f);
+        v[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+        const int at = c + e * split;
+        if (at <= last) {
+          const size_t p = (size_t)(2 * at + (at == first ? 1 : 0)) * a.rows + row;
+          z[e] = __ldcg(a.part_ml + p);
+          v[e] = __ldcg(reinterpret_cast<const float4*>(a.part_o + p * D) + q);
+        }
+      }
+      float top = x.M;
+#pragma unroll
+      for (int e = 0; e < kAhead; e++)
+        if (z[e].y != 0.f) top = fmaxf(top, z[e].x);
+      x.raise(top);
+#pragma unroll
+      for (int e = 0; e < kAhead; e++) x.add(top, z[e], v[e]);
     }
     float top = x.M;
-#pragma unroll
-    for (int e = 0; e < kAhead; e++)
-      if (z[e].y != 0.f) top = fmaxf(top, z[e].x);
+    for (int m = 1; m < split; m <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
     x.raise(top);
-#pragma unroll
-    for (int e = 0; e < kAhead; e++)
-      if (z[e].y != 0.f) x.add(top, z[e], v[e]);
+    for (int m = 1; m < split; m <<= 1) {
+      x.S += __shfl_xor_sync(0xffffffffu, x.S, m);
+      x.v.x += __shfl_xor_sync(0xffffffffu, x.v.x, m);
+      x.v.y += __shfl_xor_sync(0xffffffffu, x.v.y, m);
+      x.v.z += __shfl_xor_sync(0xffffffffu, x.v.z, m);
+      x.v.w += __shfl_xor_sync(0xffffffffu, x.v.w, m);
+    }
+    if (sub == 0 && i0 < items) write_row<D>(a, cut.x, g, r0 + row, q, x.v, x.M, x.S);
   }
-  write_row<D>(a, cut.x, g, r0 + row, q, x.v, x.M, x.S);
 }
 
 template <int D, int RT, bool SPLIT>
@@ -895,7 +913,7 @@ cudaError_t launch_tree_t(const PagedTreeArgs& a, int grid, cudaStream_t s) {
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   if ((e = launch_pdl(k_tree_sweep<D, RT, SPLIT>, dim3((unsigned)grid), kTreeThreads, (size_t)bytes, s, a)) != cudaSuccess) return e;
-  return launch_pdl(k_tree_join<D>, dim3((unsigned)grid, (unsigned)((a.rows + 512 / D - 1) / (512 / D))), 128, 0, s, a);
+  return launch_pdl(k_tree_join<D>, dim3((unsigned)grid, kJoinSlices), kJoinThreads, 0, s, a);
 }
 template <int D>
 cudaError_t launch_tree(const PagedTreeArgs& a, int grid, cudaStream_t s) {
