@@ -7,6 +7,7 @@ calls raise; there is no other implementation to fall back to.
 """
 import collections
 import ctypes
+import importlib.util
 import os
 
 import torch
@@ -660,31 +661,26 @@ def attn_decode_paged(q, k_pages, v_pages, page_table, kv_len, q_weight=None, ep
 PagedPlan = collections.namedtuple("PagedPlan", "kv_len held span cu_new slots positions")
 
 
-def _tree(parents, B, device):
-    """(tokens, row stride) of parents int32 [B, Tq], or [Tq]: one tree for the batch."""
-    n, s = parents.shape, parents.stride()
-    if (parents.dtype != torch.int32 or parents.device != device or len(n) not in (1, 2)
-            or (len(n) == 2 and n[0] != B) or (n[-1] > 1 and s[-1] != 1)):
-        raise ValueError("parents must be int32 [B, Tq] or [Tq], rows contiguous, on the call's device")
-    if len(n) == 1 or B == 1:
-        return n[-1], 0
-    if s[0] != 0 and s[0] < n[1]:
-        raise ValueError("parents: rows must not overlap")
-    return n[1], s[0]
+_bind = None
+BIND_PATH = os.path.join(_HERE, "_build", "_neattn_bind.so")
 
 
-def _out32(t, name, device, shape):
-    if t is None:
-        return torch.empty(shape, dtype=torch.int32, device=device)
-    _int32(t, name, device, shape)
-    return t
-
-
-def _apart(a, b, what):
-    # neither a byte of the one in the other
-    pa, pb = a.data_ptr(), b.data_ptr()
-    if pa < pb + 4 * b.numel() and pb < pa + 4 * a.numel():
-        raise ValueError("%s must not share memory" % what)
+def _compiled():
+    """The compiled part of the binding (csrc/bind.cpp), which has the library's entry points from here."""
+    global _bind
+    if _bind is None:
+        L = lib()
+        if not os.path.exists(BIND_PATH):
+            raise RuntimeError("_neattn_bind.so is not built (%s); run __graft_entry__.build()" % BIND_PATH)
+        spec = importlib.util.spec_from_file_location("_neattn_bind", BIND_PATH)
+        m = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(m)
+        names = ("ne_attn_paged_plan", "ne_attn_kv_append_slots", "ne_attn_decode_tree",
+                 "ne_attn_decode_tree_workspace_size", "ne_attn_kv_keep_paged")
+        m.init(dict({n: ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in names},
+                    OutOfMemoryError=torch.OutOfMemoryError))
+        _bind = m
+    return _bind
 
 
 def paged_plan(page_table, free_pages, held, free_span, kv_len, new_len, rows, page_size, parents=None, kv_len_out=None,
@@ -703,27 +699,11 @@ def paged_plan(page_table, free_pages, held, free_span, kv_len, new_len, rows, p
     if stream is not None:
         return _on(stream, paged_plan, page_table, free_pages, held, free_span, kv_len, new_len, rows, page_size, parents,
                    kv_len_out, held_out, span_out)
-    B, width = page_table.shape
-    dev = page_table.device
-    _need(page_table.is_cuda, "page_table must be a CUDA tensor")
-    _int32(page_table, "page_table", dev, (B, width))
-    _need(free_pages.dim() == 1, "free_pages must be [num_pages]")
-    _int32(free_pages, "free_pages", dev, free_pages.shape)
-    for t, n, shape in ((held, "held", (B,)), (free_span, "free_span", (2,)), (kv_len, "kv_len", (B,)), (new_len, "new_len", (B,))):
-        _int32(t, n, dev, shape)
-    Tq, pstride = (0, 0) if parents is None else _tree(parents, B, dev)
-    if kv_len_out is not None:
-        _int32(kv_len_out, "kv_len_out", dev, (B,))
-        _apart(kv_len_out, kv_len, "kv_len_out and kv_len")
-    total = _out32(kv_len_out, "kv_len_out", dev, (B,))
-    got, span = _out32(held_out, "held_out", dev, (B,)), _out32(span_out, "span_out", dev, (2,))
-    cu = torch.empty(B + 1, dtype=torch.int32, device=dev)
-    slots = torch.empty(rows, dtype=torch.int32, device=dev)
-    positions = torch.empty(rows, dtype=torch.int32, device=dev)
-    _run("ne_attn_paged_plan", dev, page_table.data_ptr(), free_pages.data_ptr(), held.data_ptr(), free_span.data_ptr(),
-         kv_len.data_ptr(), new_len.data_ptr(), _optr(parents), got.data_ptr(), span.data_ptr(), total.data_ptr(),
-         cu.data_ptr(), slots.data_ptr(), positions.data_ptr(), rows, B, Tq, page_size, free_pages.numel(), width, pstride)
-    return PagedPlan(total, got, span, cu, slots, positions)
+    r = (_bind or _compiled()).plan(page_table, free_pages, held, free_span, kv_len, new_len, rows, page_size, parents, kv_len_out,
+                                    held_out, span_out)
+    if type(r) is int:
+        raise NeAttnError("ne_attn_paged_plan", r)
+    return PagedPlan._make(r)
 
 
 def kv_append_slots(k_new, v_new, k_pages, v_pages, slots, positions, capacity, k_weight=None, eps=1e-6,
@@ -735,20 +715,9 @@ def kv_append_slots(k_new, v_new, k_pages, v_pages, slots, positions, capacity, 
     if stream is not None:
         return _on(stream, kv_append_slots, k_new, v_new, k_pages, v_pages, slots, positions, capacity, k_weight, eps,
                    rope_base, rope_half)
-    N, Hkv, D = k_new.shape
-    dev = k_new.device
-    _need(v_new.shape == k_new.shape, "k_new and v_new must have one shape")
-    ks, vs = _head_rows(k_new, "k_new"), _head_rows(v_new, "v_new", device=dev)
-    P, page, stride = _pools(k_pages, v_pages, Hkv, D, dev)
-    _int32(slots, "slots", dev, (N,))
-    _int32(positions, "positions", dev, (N,))
-    if k_weight is not None:
-        _vector(k_weight, D, "k_weight", dev)
-    if N == 0:
-        return
-    _run("ne_attn_kv_append_slots", dev, k_new.data_ptr(), v_new.data_ptr(), _optr(k_weight), k_pages.data_ptr(),
-         v_pages.data_ptr(), slots.data_ptr(), positions.data_ptr(), N, Hkv, D, page, P, capacity, stride, ks, vs, eps,
-         rope_base, ROPE_HALF if rope_half else 0)
+    st = (_bind or _compiled()).append(k_new, v_new, k_pages, v_pages, slots, positions, capacity, k_weight, eps, rope_base, rope_half)
+    if st != NE_OK:
+        raise NeAttnError("ne_attn_kv_append_slots", st)
 
 
 def decode_tree_workspace_size(B, Tq, Hq, Hkv, D):
@@ -768,25 +737,13 @@ def attn_decode_tree(q, k_pages, v_pages, page_table, kv_len, parents, tree_len=
     if stream is not None:
         return _on(stream, attn_decode_tree, q, k_pages, v_pages, page_table, kv_len, parents, tree_len, q_weight, eps,
                    rope_base, o, lse, o_dtype, workspace, rope_half)
-    B, Tq, Hq, D = q.shape
-    Hkv, dev = k_pages.shape[1], q.device
-    qs = _head_rows(q, "q")
-    P, page, stride = _pools(k_pages, v_pages, Hkv, D, dev)
-    width = page_table.shape[1]
-    _int32(page_table, "page_table", dev, (B, width))
-    _int32(kv_len, "kv_len", dev, (B,))
-    n, pstride = _tree(parents, B, dev)
-    _need(n == Tq, "parents must have a token for each of q's")
-    if tree_len is not None:
-        _int32(tree_len, "tree_len", dev, (B,))
-    if q_weight is not None:
-        _vector(q_weight, D, "q_weight", dev)
-    o, lse, fp32 = _outputs(o, lse, o_dtype, B, Tq, Hq, D, dev)
-    args = (q.data_ptr(), _optr(q_weight), k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(), kv_len.data_ptr(),
-            parents.data_ptr(), _optr(tree_len), o.data_ptr(), lse.data_ptr(), B, Tq, Hq, Hkv, D, page, P, width, stride, qs,
-            pstride, eps, rope_base, (O_FP32 if fp32 else 0) | (ROPE_HALF if rope_half else 0))
-    _run_ws("ne_attn_decode_tree", dev, args, workspace, lambda: decode_tree_workspace_size(B, Tq, Hq, Hkv, D))
-    return o, lse
+    if o_dtype is not torch.bfloat16 and o_dtype is not torch.float32 and o is None:
+        raise ValueError("o must be bfloat16 or float32")
+    r = (_bind or _compiled()).decode_tree(q, k_pages, v_pages, page_table, kv_len, parents, tree_len, q_weight, eps, rope_base, o, lse,
+                                           o_dtype is torch.float32, workspace, rope_half)
+    if type(r) is int:
+        raise NeAttnError("ne_attn_decode_tree", r)
+    return r
 
 
 def kv_keep_paged(k_pages, v_pages, page_table, kv_len, tree_len, path, path_len, kv_len_out=None, stream=None):
@@ -798,30 +755,10 @@ def kv_keep_paged(k_pages, v_pages, page_table, kv_len, tree_len, path, path_len
     table may be passed as one [num_pages, layers * Hkv, page_size, D]."""
     if stream is not None:
         return _on(stream, kv_keep_paged, k_pages, v_pages, page_table, kv_len, tree_len, path, path_len, kv_len_out)
-    dev = k_pages.device
-    _need(k_pages.is_cuda, "pools must be CUDA tensors")
-    Hkv, D = k_pages.shape[1], k_pages.shape[3]
-    P, page, stride = _pools(k_pages, v_pages, Hkv, D, dev)
-    B, width = page_table.shape
-    _int32(page_table, "page_table", dev, (B, width))
-    _int32(kv_len, "kv_len", dev, (B,))
-    _need(path.dim() == 2, "path must be [B, width]")
-    _int32(path, "path", dev, (B, path.shape[1]))
-    _int32(path_len, "path_len", dev, (B,))
-    tokens, lens = 0, None
-    if isinstance(tree_len, torch.Tensor):
-        _int32(tree_len, "tree_len", dev, (B,))
-        lens = tree_len
-    else:
-        tokens = int(tree_len)
-    if kv_len_out is not None:
-        _int32(kv_len_out, "kv_len_out", dev, (B,))
-        _apart(kv_len_out, kv_len, "kv_len_out and kv_len")
-    out = _out32(kv_len_out, "kv_len_out", dev, (B,))
-    _run("ne_attn_kv_keep_paged", dev, k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(), kv_len.data_ptr(),
-         _optr(lens), path.data_ptr(), path_len.data_ptr(), out.data_ptr(), B, tokens, path.shape[1], Hkv, D, page, P, width,
-         stride)
-    return out
+    r = (_bind or _compiled()).keep(k_pages, v_pages, page_table, kv_len, tree_len, path, path_len, kv_len_out)
+    if type(r) is int:
+        raise NeAttnError("ne_attn_kv_keep_paged", r)
+    return r
 
 
 class HostStepPipeline:
