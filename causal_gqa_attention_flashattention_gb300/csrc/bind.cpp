@@ -2,7 +2,9 @@
 // library's entry point in one step, since such calls take less time on the device than their checks do in
 // Python (one plan for 64 sequences 4.7 us on the device, 25 us of Python and ctypes, 10 us so). binding.py has the
 // public functions, gives the library's entry points to init() and turns a returned status into its error.
+#include <ATen/core/LegacyTypeDispatch.h>
 #include <ATen/core/Tensor.h>
+#include <ATen/ops/as_strided.h>
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -183,10 +185,20 @@ PyObject* plan(PyObject* const* a) {
   int Tq = 0;
   long long pstride = 0;
   const int* parents = given(a[8]) ? tree(a[8], B, c.dev, &Tq, &pstride) : nullptr;
-  const Tensor total = out32(a[9], "kv_len_out", c.dev, {B}), got = out32(a[10], "held_out", c.dev, {B});
-  const Tensor left = out32(a[11], "span_out", c.dev, {2});
-  if (given(a[9])) apart(total, THPVariable_Unpack(a[4]), "kv_len_out and kv_len must not share memory");
-  const Tensor cu = make({B + 1}, kInt, c.dev), slots = make({rows}, kInt, c.dev), pos = make({rows}, kInt, c.dev);
+  // what is not given lies in one allocation
+  at::AutoDispatchBelowADInplaceOrView plain;
+  const bool own_total = !given(a[9]), own_got = !given(a[10]), own_left = !given(a[11]);
+  const int64_t most = B + 1 + 2 * (int64_t)rows + (own_total ? B : 0) + (own_got ? B : 0) + (own_left ? 2 : 0);
+  const Tensor all = make({most}, kInt, c.dev);
+  int64_t at = 0;
+  const auto part = [&](int64_t n) {
+    at += n;
+    return at::as_strided(all, {n}, {1}, at - n);
+  };
+  const Tensor slots = part(rows), pos = part(rows), cu = part(B + 1);
+  const Tensor total = own_total ? part(B) : out32(a[9], "kv_len_out", c.dev, {B});
+  const Tensor got = own_got ? part(B) : out32(a[10], "held_out", c.dev, {B}), left = own_left ? part(2) : out32(a[11], "span_out", c.dev, {2});
+  if (!own_total) apart(total, THPVariable_Unpack(a[4]), "kv_len_out and kv_len must not share memory");
   const int st = f_plan(p_table, p_ring, held, span, len, add, parents, got.data_ptr<int>(), left.data_ptr<int>(),
                         total.data_ptr<int>(), cu.data_ptr<int>(), slots.data_ptr<int>(), pos.data_ptr<int>(), rows, (int)B, Tq, page,
                         (int)ring.size(0), (int)width, pstride, c.stream);

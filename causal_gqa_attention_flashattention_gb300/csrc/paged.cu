@@ -41,8 +41,8 @@ __global__ void __launch_bounds__(128) k_kv_append_paged(const PagedAppendArgs a
   int slot = -1, pos = 0, page = -1;
   if (SLOTS) {
     slot = in ? a.slots[n] : -1;
+    pos = in ? a.positions[n] : 0;  // at once: the rotation's coefficients are one trip nearer
     on = slot >= 0;
-    if (on) pos = a.positions[n];
   } else {
     on = in && (!a.cu || (int)n < a.cu[a.B]);
   }

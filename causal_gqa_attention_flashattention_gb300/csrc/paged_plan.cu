@@ -197,11 +197,12 @@ __global__ void __launch_bounds__(kPlanThreads) k_paged_plan(const PagedPlanArgs
   }
 }
 
-// The slots of many rows, four neighbouring ones a thread.
+// The slots of many rows: 128 neighbouring ones a warp, whose threads look a sequence up again only where it changes.
+constexpr int kSlotRows = 4;
 __global__ void __launch_bounds__(256) k_paged_slots(const PagedPlanArgs a) {
   pdl_wait();
   const int lane = threadIdx.x & 31;
-  const int n0 = (blockIdx.x * 256 + threadIdx.x) * 4, w0 = n0 - lane * 4;
+  const int w0 = (blockIdx.x * 8 + threadIdx.x / 32) * 32 * kSlotRows;
   if (w0 >= a.N) return;
   const int total = a.cu[a.B];
   int lo = 0, hi = a.B;  // the warp's first row: 32 probes at a time
@@ -211,39 +212,55 @@ __global__ void __launch_bounds__(256) k_paged_slots(const PagedPlanArgs a) {
     lo += (31 - __clz((int)le)) * step;
     hi = min(hi, lo + step);
   }
-  int b = lo;
-  for (int n = n0; n < min(n0 + 4, a.N); n++) {
+  int b = lo, first = a.cu[b], end = a.cu[b + 1], len = a.len[b];
+  bool granted = a.len_out[b] == len + (end - first);
+#pragma unroll
+  for (int i = 0; i < kSlotRows; i++) {
+    const int n = w0 + 32 * i + lane;
+    if (n >= a.N) return;
     if (n >= total) {
       a.slots[n] = -1;
       a.positions[n] = 0;
       continue;
     }
-    while (b + 1 < a.B && a.cu[b + 1] <= n) b++;
-    const int first = a.cu[b], add = a.cu[b + 1] - first, len = a.len[b];
-    plan_row(a, n, b, n - first, len, a.len_out[b] == len + add);
+    if (n >= end) {
+      do {
+        b++;
+        end = a.cu[b + 1];
+      } while (n >= end);
+      first = a.cu[b];
+      len = a.len[b];
+      granted = a.len_out[b] == len + (end - first);
+    }
+    plan_row(a, n, b, n - first, len, granted);
   }
 }
 
 // ====================================================================== the accepted path
 // Sequence b has len[b] positions, the last nodes[b] of them a tree; path[b, 0 .. count[b]) are the tokens
 // that stay, in rising order: token path[i] moves to position len - nodes + i.  path[i] >= i, so a row may be
-// both a source and a place: a block holds all rows of its (sequence, head) before it writes one.
-constexpr int kKeepThreads = 128;
+// both a source and a place, but a place only of a token before it: a warp takes a (sequence, head) and moves some rows
+// at a time, in order, all of them read before one is written.
+constexpr int kKeepThreads = 128, kKeepChunks = 8;
 template <int D>
 __global__ void __launch_bounds__(kKeepThreads) k_kv_keep(const PagedKeepArgs a) {
-  constexpr int kCPR = D / 8, kPer = 2 * kTreeMax * kCPR / kKeepThreads;
+  constexpr int kCPR = D / 8;
   __shared__ long long s_src[kTreeMax], s_dst[kTreeMax];
-  const int g = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
+  const int g0 = blockIdx.x * (kKeepThreads / 32), b = blockIdx.y, tid = threadIdx.x;
   const int cap = a.max_pages << a.page_shift, mask = (1 << a.page_shift) - 1;
   const int len = a.len[b], nodes = a.nodes ? a.nodes[b] : a.tokens, m = a.count[b];
+  int x = 0, before = -1;  // at once with the lengths
+  if (tid < a.width) {
+    x = a.path[(size_t)b * a.width + tid];
+    if (tid > 0) before = a.path[(size_t)b * a.width + tid - 1];
+  }
   if (len < nodes || len <= 0) {  // an idle slot of the batch
-    if (g == 0 && tid == 0) a.len_out[b] = max(len, 0);
+    if (g0 == 0 && tid == 0) a.len_out[b] = max(len, 0);
     return;
   }
   const int base = len - nodes;
   bool bad = nodes < 0 || m < 0 || m > min(nodes, a.width) || len > cap;
   if (!bad && tid < m) {
-    const int x = a.path[(size_t)b * a.width + tid], before = tid > 0 ? a.path[(size_t)b * a.width + tid - 1] : -1;
     bad = x <= before || x >= nodes;
     if (!bad) {
       const int from = base + x, to = base + tid;
@@ -251,35 +268,40 @@ __global__ void __launch_bounds__(kKeepThreads) k_kv_keep(const PagedKeepArgs a)
       const int pd = a.table[(size_t)b * a.max_pages + (to >> a.page_shift)];
       const bool there = ps >= 0 && ps < a.num_pages && pd >= 0 && pd < a.num_pages;
       if (!there) record_page(a.status);
-      s_src[tid] = (long long)ps * a.page_stride + (((long long)g << a.page_shift) + (from & mask)) * D;
-      s_dst[tid] = there && x != tid ? (long long)pd * a.page_stride + (((long long)g << a.page_shift) + (to & mask)) * D : -1;
+      s_src[tid] = (long long)ps * a.page_stride + (long long)(from & mask) * D;
+      s_dst[tid] = there && x != tid ? (long long)pd * a.page_stride + (long long)(to & mask) * D : -1;
     }
   }
   if (__syncthreads_or(bad)) {
-    if (g == 0 && tid == 0) {
+    if (g0 == 0 && tid == 0) {
       record_tree(a.status);
       a.len_out[b] = max(min(base, len), 0);
     }
     return;
   }
-  uint4 x[kPer];
-  // item i: chunk i % kCPR of row (i / kCPR) / 2, keys and values in turn
+  if (g0 == 0 && tid == 0) a.len_out[b] = base + m;
+  const int g = g0 + tid / 32, lane = tid & 31, c = lane % kCPR;
+  if (g >= a.Hkv) return;
+  // chunk c of keys or values in turn, of row after row: 32 / kCPR of them a step
+  constexpr int kRows = kKeepChunks * 32 / kCPR / 2;
+  const long long head = ((long long)g << a.page_shift) * D + c * 8;
+  for (int r0 = 0; r0 < m; r0 += kRows) {
+    uint4 v[kKeepChunks];
 #pragma unroll
-  for (int k = 0; k < kPer; k++) {
-    const int i = k * kKeepThreads + tid, r = i / (2 * kCPR);
-    if (r >= m || s_dst[r] < 0) continue;
-    const uint4* pool = (i / kCPR) & 1 ? reinterpret_cast<const uint4*>(a.vp + s_src[r]) : reinterpret_cast<const uint4*>(a.kp + s_src[r]);
-    x[k] = pool[i % kCPR];
-  }
-  __syncthreads();
+    for (int k = 0; k < kKeepChunks; k++) {
+      const int i = k * (32 / kCPR) + lane / kCPR, r = r0 + i / 2;
+      if (r >= m || s_dst[r] < 0) continue;
+      v[k] = *(i & 1 ? reinterpret_cast<const uint4*>(a.vp + s_src[r] + head) : reinterpret_cast<const uint4*>(a.kp + s_src[r] + head));
+    }
+    __syncwarp();
 #pragma unroll
-  for (int k = 0; k < kPer; k++) {
-    const int i = k * kKeepThreads + tid, r = i / (2 * kCPR);
-    if (r >= m || s_dst[r] < 0) continue;
-    uint4* pool = (i / kCPR) & 1 ? reinterpret_cast<uint4*>(a.vp + s_dst[r]) : reinterpret_cast<uint4*>(a.kp + s_dst[r]);
-    pool[i % kCPR] = x[k];
+    for (int k = 0; k < kKeepChunks; k++) {
+      const int i = k * (32 / kCPR) + lane / kCPR, r = r0 + i / 2;
+      if (r >= m || s_dst[r] < 0) continue;
+      *(i & 1 ? reinterpret_cast<uint4*>(a.vp + s_dst[r] + head) : reinterpret_cast<uint4*>(a.kp + s_dst[r] + head)) = v[k];
+    }
+    __syncwarp();
   }
-  if (g == 0 && tid == 0) a.len_out[b] = base + m;
 }
 
 }  // namespace
@@ -288,11 +310,11 @@ cudaError_t launch_paged_plan(const PagedPlanArgs& a, cudaStream_t s) {
   k_paged_plan<<<1, kPlanThreads, 0, s>>>(a);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || a.N <= kPlanRows) return e;
-  return launch_pdl(k_paged_slots, dim3((unsigned)((a.N + 1023) / 1024)), 256, 0, s, a);
+  return launch_pdl(k_paged_slots, dim3((unsigned)((a.N + 256 * kSlotRows - 1) / (256 * kSlotRows))), 256, 0, s, a);
 }
 
 cudaError_t launch_kv_keep(const PagedKeepArgs& a, int D, cudaStream_t s) {
-  const dim3 grid((unsigned)a.Hkv, (unsigned)a.B);
+  const dim3 grid((unsigned)((a.Hkv + kKeepThreads / 32 - 1) / (kKeepThreads / 32)), (unsigned)a.B);
   if (D == 64)
     k_kv_keep<64><<<grid, kKeepThreads, 0, s>>>(a);
   else
