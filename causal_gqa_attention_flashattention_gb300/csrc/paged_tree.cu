@@ -63,7 +63,8 @@ struct TreeCfg {
   static constexpr int kBytes = kOffV + kVStages * kTileBytes;
   // Tensor memory: group g's O at 64 g. With both parts of the weights in one lane step n has its S at 128 +
   // 128 (n % 3), and P in its place; with SPLIT a group has S at 128 + 128 g and P, 64 columns, at 384 + 64 g, so that
-  // its next scores are worked out while it is on its weights.
+  // its next scores are worked out while it is on its weights. With FULL a group has one buffer of S, at 128 + 128 g, and
+  // the third parts go to 384 + 64 g, with SPLIT in the place of S.
   static constexpr uint32_t kColO = 0, kColS = 128, kColP = 384;
 };
 constexpr int kTreeVars = 480, kTreePlan = 488, kTreeSums = 544, kTreeInfo = 608, kTreeMl = 1664;
@@ -181,8 +182,10 @@ __device__ __forceinline__ void put_columns(const PagedTreeArgs& a, size_t to, c
   }
 }
 
-// RT: row tiles of a pair (2: more than 128 rows). SPLIT: at most 64 rows, two lanes each (see above).
-template <int D, int RT, bool SPLIT>
+// RT: row tiles of a pair (2: more than 128 rows). SPLIT: at most 64 rows, two lanes each (see above). FULL: o is
+// float32, and the weights have a third part (2^-25; two are 2^-17 off, an eighth of a bf16 o's rounding but ten
+// times what fp32 sums are off).
+template <int D, int RT, bool SPLIT, bool FULL>
 __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_constant__ PagedTreeArgs a) {
   using C = TreeCfg<D>;
   constexpr int SK = C::kKStages, SV = C::kVStages, TB = C::kTileBytes;
@@ -197,7 +200,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
   uint64_t* v_empty = v_full + SV;         // [SV] the O += P V of the stage have completed
   uint64_t* s_full = v_empty + SV;         // [group][2] the group's steps in turn
   uint64_t* p_ready = s_full + 4;          // [group][2][2] the weights of the tile's last 64 keys, and of the first (SPLIT: all)
-  uint64_t* pv_done = p_ready + 8;         // [3] per buffer of S and P; SPLIT: [group] the scores are in registers
+  uint64_t* pv_done = p_ready + 8;         // [3] per buffer of S and P (FULL: [group]); SPLIT, not FULL: [group] the scores are in registers
   uint64_t* o_done = pv_done + 3;          // [group][2] the same per group's step, for the group
   uint64_t* part_full = o_done + 4;        // [group][2] the other group's part of a segment that this one finishes
   uint64_t* gsync = part_full + 4;         // [group]
@@ -236,7 +239,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
       mbar_init(part_full + k, 4);
     }
     for (int k = 0; k < 3; k++) {
-      mbar_init(pv_done + k, SPLIT ? 4 : 1);
+      mbar_init(pv_done + k, SPLIT && !FULL ? 4 : 1);
       mbar_init(drain + k, 1);
     }
     fence_mbar_init();
@@ -416,8 +419,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
           if (!(ok = mbar_wait(k_full + st, (k / SK) & 1, abort))) break;
 #pragma unroll 1
           for (int u = 0; u < nu; u++, n++) {
-            // the buffer's weights have been read (SPLIT: the group's scores)
-            const int buf = SPLIT ? n & 1 : n % 3, use = SPLIT ? n >> 1 : n / 3;
+            // the buffer's weights have been read (SPLIT, not FULL: the group's scores)
+            const int buf = SPLIT || FULL ? n & 1 : n % 3, use = SPLIT || FULL ? n >> 1 : n / 3;
             if (use > 0 && !(ok = mbar_wait(pv_done + buf, (use - 1) & 1, abort))) break;
             tc_fence_after();
             const uint64_t dq = dQ0 + (uint64_t)((RT == 1 ? 2 * slot : 2 * u) * tstep), dk = dK0 + (uint64_t)(st * tstep);
@@ -462,20 +465,23 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
           if (!(ok = mbar_wait(ready, (i >> 1) & 1, abort))) break;
           if (!(ok = mbar_wait(v_full + st, (kt / SV) & 1, abort))) break;
           const uint64_t dv = dV0 + (uint64_t)(st * tstep), dv2 = dv + (uint64_t)(4 * kStepMN);
-          const uint32_t p = SPLIT ? tmem + C::kColP + 64u * grp : tmem + C::kColS + 128u * (n % 3);
+          const uint32_t sb = tmem + C::kColS + 128u * (FULL ? grp : n % 3), pb = tmem + C::kColP + 64u * grp;
+          const uint32_t p = SPLIT ? pb : sb, third = SPLIT ? sb : pb;
           constexpr uint32_t kHalf = SPLIT ? 32u : 64u;  // columns of P for 64 keys
           tc_fence_after();
-          mma_ts_chain<4, false>(o, p + kHalf, dv2, kStepMN, idPV, n - first >= 2 ? 1u : 0u);
+          mma_ts_chain<4, false>(o, p + kHalf, dv2, kStepMN, idPV, !FULL && n - first >= 2 ? 1u : 0u);
           if (!SPLIT) {
             mma_ts_chain<4, false>(o, p + kHalf + 32u, dv2, kStepMN, idPV, 1u);
             if (!(ok = mbar_wait(ready + 1, (i >> 1) & 1, abort))) break;
             tc_fence_after();
           }
           mma_ts_chain<4, false>(o, p, dv, kStepMN, idPV, 1u);
-          if (!SPLIT) {
-            mma_ts_chain<4, false>(o, p + 32u, dv, kStepMN, idPV, 1u);
-            mma_commit(pv_done + n % 3);
+          if (!SPLIT) mma_ts_chain<4, false>(o, p + 32u, dv, kStepMN, idPV, 1u);
+          if (FULL) {
+            mma_ts_chain<4, false>(o, third + 32u, dv2, kStepMN, idPV, 1u);
+            mma_ts_chain<4, false>(o, third, dv, kStepMN, idPV, 1u);
           }
+          if (!SPLIT || FULL) mma_commit(pv_done + (FULL ? grp : n % 3));
           mma_commit(o_done + 2 * grp + (i & 1));
           mma_commit(v_empty + st);
           if (RT == 2 && nu == 1) mbar_arrive(v_empty + st);
@@ -523,10 +529,28 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
       constexpr int NQ = SPLIT ? 2 : 1;
       unsigned long long mask[NQ];
       float r_run[NQ], l_run[NQ], m_use[NQ];
+      float acc[FULL ? D : 1];  // FULL: O of the lane's row so far
+#pragma unroll
+      for (int x = 0; FULL && x < D; x++) acc[x] = 0.f;
+      // FULL: adds the O of step n to it, then scales both
+      const auto flush = [&](int n, float f) {
+        if (!__all_sync(0xffffffffu, mbar_wait(o_done + 2 * grp + ((n >> 1) & 1), (n >> 2) & 1, abort))) return false;
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < (FULL ? D / 16 : 0); c++) {
+          uint32_t w[16];
+          tmem_ld16(obuf + c * 16, w);
+          tmem_wait_ld();
+#pragma unroll
+          for (int x = 0; x < 16; x++) acc[(FULL ? 16 : 0) * c + (FULL ? x : 0)] = (acc[(FULL ? 16 : 0) * c + (FULL ? x : 0)] + __uint_as_float(w[x])) * f;
+        }
+        return true;
+      };
       int s = mine;
       for (; s < end; s += 2) {
-        const int buf = SPLIT ? grp : s % 3, tile = sw.n0 + (nu == 2 ? (s - first) >> 1 : s - first);
-        const uint32_t sbuf = trow + C::kColS + 128u * buf, pbuf = SPLIT ? trow + C::kColP + 64u * grp : sbuf;
+        const int buf = SPLIT || FULL ? grp : s % 3, tile = sw.n0 + (nu == 2 ? (s - first) >> 1 : s - first);
+        const uint32_t sbuf = trow + C::kColS + 128u * buf, pown = trow + C::kColP + 64u * grp;
+        const uint32_t pbuf = SPLIT ? pown : sbuf, third = SPLIT ? sbuf : pown;
         ok = __all_sync(0xffffffffu, mbar_wait(s_full + 2 * grp + ((s >> 1) & 1), (s >> 2) & 1, abort));
         if (!ok) break;
         tc_fence_after();
@@ -591,8 +615,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
         float mxr[NQ];
         if (SPLIT) {
           load(0);
-          tc_fence_before();
-          warp_arrive(pv_done + grp);
+          if (!FULL) {
+            tc_fence_before();
+            warp_arrive(pv_done + grp);
+          }
           float m2[2][2] = {{-INFINITY, -INFINITY}, {-INFINITY, -INFINITY}};
 #pragma unroll
           for (int x = 0; x < 64; x += 2)
@@ -630,33 +656,37 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
             alpha[i] = 1.f;
             grow = grow || __fmul_rn(fmaxf(r_run[i], mxr[i]), sl2) > __fmul_rn(r_run[i], sl2) + 8.0f;
           }
+          float lane_a = 1.f;  // of the lane's row
           if (__any_sync(0xffffffffu, grow)) {
-            ok = __all_sync(0xffffffffu, mbar_wait(o_done + 2 * grp + (((s - 2) >> 1) & 1), ((s - 2) >> 2) & 1, abort));
-            if (!ok) break;
-            tc_fence_after();
 #pragma unroll
             for (int i = 0; i < NQ; i++) {
               const float r_new = fmaxf(r_run[i], mxr[i]);
               alpha[i] = r_run[i] == -INFINITY ? 0.f : ex2(__fmul_rn(r_run[i], sl2) - __fmul_rn(r_new, sl2));
               r_run[i] = r_new;
             }
-            float lane_a = alpha[0];  // of the lane's row
+            lane_a = alpha[0];
             if (SPLIT) {
               const float x = __shfl_sync(0xffffffffu, alpha[0], 4 * (lane & 7)), y = __shfl_sync(0xffffffffu, alpha[NQ - 1], 4 * (lane & 7));
               lane_a = lane & 8 ? y : x;
             }
+            if (!FULL) {
+              ok = __all_sync(0xffffffffu, mbar_wait(o_done + 2 * grp + (((s - 2) >> 1) & 1), ((s - 2) >> 2) & 1, abort));
+              if (!ok) break;
+              tc_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < D / 16; c++) {
-              uint32_t w[16];
-              tmem_ld16(obuf + c * 16, w);
-              tmem_wait_ld();
+              for (int c = 0; c < D / 16; c++) {
+                uint32_t w[16];
+                tmem_ld16(obuf + c * 16, w);
+                tmem_wait_ld();
 #pragma unroll
-              for (int x = 0; x < 16; x++) w[x] = __float_as_uint(__uint_as_float(w[x]) * lane_a);
-              tmem_st16(obuf + c * 16, w);
+                for (int x = 0; x < 16; x++) w[x] = __float_as_uint(__uint_as_float(w[x]) * lane_a);
+                tmem_st16(obuf + c * 16, w);
+              }
             }
           }
+          if (FULL && !(ok = flush(s - 2, lane_a))) break;
         }
-        if (SPLIT && s >= 2) {  // the weights of the step before have been read
+        if (SPLIT ? s >= 2 : FULL && s >= 2 && s == mine) {  // the weights of the step before have been read
           ok = __all_sync(0xffffffffu, mbar_wait(o_done + 2 * grp + (((s - 2) >> 1) & 1), ((s - 2) >> 2) & 1, abort));
           if (!ok) break;
           tc_fence_after();
@@ -673,7 +703,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
 #pragma unroll 1
         for (int h = 1; h >= (SPLIT ? 1 : 0); h--) {
           if (h == 0) load(0);
-          uint32_t ph[32], pl[32];
+          uint32_t ph[32], pl[32], pt[32];
 #pragma unroll
           for (int x = 0; x < 32; x++) {
             constexpr int kSums = 4 / NQ;
@@ -683,16 +713,27 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
             const uint64_t pp = f2(ex2(x0), ex2(x1));
             f2_split(pp, x0, x1);
             ph[x] = pack_bf16(x0, x1);
-            f2_split(f2_fma(f2(bf_lo(ph[x]), bf_hi(ph[x])), minus, pp), l0, l1);
+            const uint64_t ll = f2_fma(f2(bf_lo(ph[x]), bf_hi(ph[x])), minus, pp);
+            f2_split(ll, l0, l1);
             pl[x] = pack_bf16(l0, l1);
+            if (FULL) {
+              f2_split(f2_fma(f2(bf_lo(pl[x]), bf_hi(pl[x])), minus, ll), l0, l1);
+              pt[x] = pack_bf16(l0, l1);
+            }
             sum[i][j] = f2_add(sum[i][j], pp);
             if (!SPLIT && x % 8 == 7) {
               tmem_st8(pbuf + 64 * h + x - 7, *reinterpret_cast<uint32_t(*)[8]>(ph + x - 7));
               tmem_st8(pbuf + 64 * h + 32 + x - 7, *reinterpret_cast<uint32_t(*)[8]>(pl + x - 7));
+              if (FULL) tmem_st8(third + 32 * h + x - 7, *reinterpret_cast<uint32_t(*)[8]>(pt + x - 7));
             }
             if (SPLIT && x % 16 == 15) {
               tmem_st16x32(pbuf + 2 * (x - 15), *reinterpret_cast<uint32_t(*)[16]>(ph + x - 15));
               tmem_st16x32(pbuf + (16u << 16) + 2 * (x - 15), *reinterpret_cast<uint32_t(*)[16]>(pl + x - 15));
+              if (FULL) {  // beside the low parts
+                const uint32_t none[16] = {0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+                tmem_st16x32(third + 2 * (x - 15), none);
+                tmem_st16x32(third + (16u << 16) + 2 * (x - 15), *reinterpret_cast<uint32_t(*)[16]>(pt + x - 15));
+              }
             }
           }
           tmem_wait_st();
@@ -724,6 +765,17 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
       }
       if (!ok) break;
       // the segment's unnormalised O, maximum (log2 units) and sum
+      if (FULL) {
+        if (!(ok = flush(s - 2, 1.f))) break;
+#pragma unroll
+        for (int c = 0; c < (FULL ? D / 16 : 0); c++) {
+          uint32_t w[16];
+#pragma unroll
+          for (int x = 0; x < 16; x++) w[x] = __float_as_uint(acc[(FULL ? 16 : 0) * c + (FULL ? x : 0)]);
+          tmem_st16(obuf + c * 16, w);
+        }
+        tmem_wait_st();
+      }
       ok = __all_sync(0xffffffffu, mbar_wait(o_done + 2 * grp + (((s - 2) >> 1) & 1), ((s - 2) >> 2) & 1, abort));
       if (!ok) break;
       tc_fence_after();
@@ -895,13 +947,13 @@ __global__ void __launch_bounds__(kJoinThreads) k_tree_join(const __grid_constan
   }
 }
 
-template <int D, int RT, bool SPLIT>
+template <int D, int RT, bool SPLIT, bool FULL>
 cudaError_t launch_tree_t(const PagedTreeArgs& a, int grid, cudaStream_t s) {
   static bool attr_set[64] = {};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!attr_set[dev]) {
-    const cudaError_t e = cudaFuncSetAttribute(k_tree_sweep<D, RT, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
+    const cudaError_t e = cudaFuncSetAttribute(k_tree_sweep<D, RT, SPLIT, FULL>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
     if (e != cudaSuccess) return e;
     attr_set[dev] = true;
   }
@@ -912,13 +964,13 @@ cudaError_t launch_tree_t(const PagedTreeArgs& a, int grid, cudaStream_t s) {
   k_tree_prep<D><<<dim3((unsigned)((chunks + 127) / 128), (unsigned)a.B), 128, 0, s>>>(a, rows);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  if ((e = launch_pdl(k_tree_sweep<D, RT, SPLIT>, dim3((unsigned)grid), kTreeThreads, (size_t)bytes, s, a)) != cudaSuccess) return e;
+  if ((e = launch_pdl(k_tree_sweep<D, RT, SPLIT, FULL>, dim3((unsigned)grid), kTreeThreads, (size_t)bytes, s, a)) != cudaSuccess) return e;
   return launch_pdl(k_tree_join<D>, dim3((unsigned)grid, kJoinSlices), kJoinThreads, 0, s, a);
 }
-template <int D>
+template <int D, bool FULL>
 cudaError_t launch_tree(const PagedTreeArgs& a, int grid, cudaStream_t s) {
-  if (a.R > kTile) return launch_tree_t<D, 2, false>(a, grid, s);
-  return tree_rows(a.R) == kTile ? launch_tree_t<D, 1, false>(a, grid, s) : launch_tree_t<D, 1, true>(a, grid, s);
+  if (a.R > kTile) return launch_tree_t<D, 2, false, FULL>(a, grid, s);
+  return tree_rows(a.R) == kTile ? launch_tree_t<D, 1, false, FULL>(a, grid, s) : launch_tree_t<D, 1, true, FULL>(a, grid, s);
 }
 
 }  // namespace
@@ -927,7 +979,8 @@ cudaError_t launch_decode_tree(const PagedTreeArgs& a, int nsm, cudaStream_t s) 
   PagedTreeArgs b = a;
   const int grid = nsm < kPagedMaxBlocks ? nsm : kPagedMaxBlocks;
   b.div_grid = make_fastdiv((uint32_t)grid);
-  return b.D == 64 ? launch_tree<64>(b, grid, s) : launch_tree<32>(b, grid, s);
+  if (b.D == 64) return b.o_fp32 ? launch_tree<64, true>(b, grid, s) : launch_tree<64, false>(b, grid, s);
+  return b.o_fp32 ? launch_tree<32, true>(b, grid, s) : launch_tree<32, false>(b, grid, s);
 }
 
 }  // namespace ne
