@@ -632,16 +632,15 @@ int check_tree(int B, int Tq, int Hq, int Hkv, int D) {
   if (Tq > kTreeMax || (long long)B * Tq * Hq * D >= (1LL << 31)) return NE_ERR_UNSUPPORTED;
   return NE_OK;
 }
-// Its workspace: the packed queries, the trees, the cut (sequence, head)s' parts, their (maximum, sum), where they are.
+// Its workspace: the cut (sequence, head)s' parts, their (maximum, sum), where they are.
 struct TreeWs {
-  size_t info, part_o, part_ml, cut, total;
+  size_t part_o, part_ml, cut, total;
 };
-TreeWs tree_ws(int B, int R, int Hkv, int D) {
+TreeWs tree_ws(int R, int D) {
   const size_t rows = std::min(R, 2 * kTile);
   TreeWs w;
-  w.info = ws_up((size_t)B * Hkv * tree_tiles(R) * tree_rows(R) * D * 4);
-  w.part_o = w.info + ws_up(B * sizeof(TreeInfo));
-  w.part_ml = w.part_o + ws_up(2 * kPagedMaxBlocks * rows * D * 4);
+  w.part_o = 0;
+  w.part_ml = ws_up(2 * kPagedMaxBlocks * rows * D * 4);
   w.cut = w.part_ml + ws_up(2 * kPagedMaxBlocks * rows * 8);
   w.total = w.cut + ws_up(kPagedMaxBlocks * sizeof(int4));
   return w;
@@ -1772,7 +1771,7 @@ int ne_attn_kv_append_slots(const void* k_new, const void* v_new, const void* k_
 
 size_t ne_attn_decode_tree_workspace_size(int B, int Tq, int Hq, int Hkv, int D) {
   if (check_paged(B, Hq, Hkv, D, 16, 1, 1, 16LL * Hkv * D) != NE_OK || check_tree(B, Tq, Hq, Hkv, D) != NE_OK) return 0;
-  return tree_ws(B, Hq / Hkv * Tq, Hkv, D).total;
+  return tree_ws(Hq / Hkv * Tq, D).total;
 }
 
 int ne_attn_decode_tree(const void* q, const void* q_w, const void* k_pages, const void* v_pages,
@@ -1824,7 +1823,6 @@ int ne_attn_decode_tree(const void* q, const void* q_w, const void* k_pages, con
   a.D = D;
   a.G = Hq / Hkv;
   a.R = a.G * Tq;
-  a.tiles = tree_tiles(a.R);
   a.pairs = pairs;
   a.rows = std::min(a.R, 2 * kTile);
   a.div_g = make_fastdiv((uint32_t)a.G);
@@ -1835,13 +1833,11 @@ int ne_attn_decode_tree(const void* q, const void* q_w, const void* k_pages, con
   a.o_fp32 = (flags & kFlagOFp32) ? 1 : 0;
   a.eps = eps;
   a.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)D));
-  const TreeWs w = tree_ws(B, a.R, Hkv, D);
+  const TreeWs w = tree_ws(a.R, D);
   void* wsp = workspace;
   unsigned* counters = nullptr;
   if (!wsp && (st = join_scratch(*d, s, w.total, &wsp, &counters)) != NE_OK) return st;
   unsigned char* ws = static_cast<unsigned char*>(wsp);
-  a.packed = ws;
-  a.info = reinterpret_cast<TreeInfo*>(ws + w.info);
   a.part_o = reinterpret_cast<float*>(ws + w.part_o);
   a.part_ml = reinterpret_cast<float2*>(ws + w.part_ml);
   a.cut = reinterpret_cast<int4*>(ws + w.cut);

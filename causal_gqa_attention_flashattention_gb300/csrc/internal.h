@@ -252,12 +252,10 @@ struct PagedKeepArgs {
 // Attention of a drafted tree over a paged cache (see paged_tree.cu).
 struct TreeInfo {               // a sequence's tree
   unsigned long long mask[kTreeMax];  // a token and its ancestors
-  int ctx, nodes, pad[2];
+  int ctx, nodes;
 };
 struct PagedTreeArgs {
   CUtensorMap map_pk, map_pv;   // pools {D, page, Hkv, num_pages}, box D x min(page, 128) rows
-  unsigned char* packed;        // [B, Hkv, tiles] queries as fp16 high and low parts, laid out as in shared memory (workspace)
-  TreeInfo* info;               // [B] (workspace)
   const __nv_bfloat16 *q, *qw;  // [B, Tq, Hq, D], positions q_stride values apart; qw [D] or null
   const int *table, *len;       // [B, max_pages], [B]
   const int *parents, *nodes;   // [B, Tq] rows parent_stride apart; [B] or null (all Tq)
@@ -271,14 +269,11 @@ struct PagedTreeArgs {
                                 // (-1: none), head, first and last block (workspace)
   long long q_stride, parent_stride;
   int B, Tq, Hq, Hkv, D, G, R, page_shift, num_pages, max_pages, rope_half, o_fp32;
-  int tiles, pairs, rows;       // 128-row tiles of a head's queries, pairs of them, rows of the largest pair
+  int pairs, rows;              // pairs of 128-row tiles of a head's queries, rows of the largest
   FastDiv div_g, div_grid;      // by G and the sweep's blocks
   float eps, scale_log2;
 };
-inline int tree_tiles(int R) { return (R + kTile - 1) / kTile; }
-inline int tree_pairs(int R) { return (tree_tiles(R) + 1) / 2; }
-// Rows of a tile: up to 64 have a lane for the high parts of their weights and one for the low parts.
-inline int tree_rows(int R) { return R > kTile / 2 ? kTile : kTile / 2; }
+inline int tree_pairs(int R) { return (R + 2 * kTile - 1) / (2 * kTile); }
 
 // Attention of the newest tokens over a paged cache (see paged.cu).
 constexpr int kPagedMaxBlocks = 160;  // blocks of the sweep: bounds its partial results

@@ -6,20 +6,35 @@
 // for j < ctx and for the positions ctx + u of t's ancestors u and of t itself; o and lse as ever.  A token's
 // ancestors and itself are a mask of 64 bits.
 //
-// The R = Tq * G queries of a key/value head fill tiles of 128 rows (row t * G + g).  The key tiles of every
-// (sequence, head, pair of row tiles) lie in one line that is cut into one equal stretch for each block, as
-// in the sweep of the paged decode, and each tile is worked off on the tensor cores: S = Q K^T and O += P V with
-// TMEM accumulators, q as two fp16 parts and the weights as two bf16 parts (the paged decode's precision: a
-// tree's rows are the decode's of the accepted path).  A step is one key tile for one row tile; two groups
-// of four softmax warps take the steps in turn, each with an O of its own.  With up to 128 rows the groups share the row
-// tile and take alternate key tiles (their two O are added at the end), with more each has one of the pair's.
+// The R = Tq * G queries of a key/value head fill tiles of 128 rows (row t * G + g). The key tiles of every
+// (sequence, head, pair of row tiles) lie in one line that is cut into one equal stretch for each block, as in the
+// sweep of the paged decode, and each tile is worked off on the tensor cores: S = Q K^T and O += P V with TMEM
+// accumulators, q as two fp16 parts and the weights as two bf16 parts (the paged decode's precision: a tree's rows are
+// the decode's of the accepted path). A step is one key tile for one row tile; two groups of four softmax warps take the
+// steps in turn, each with an O of its own. With up to 128 rows the groups share the row tile and take alternate key
+// tiles (their two O are added at the end), with more each has one of the pair's.
+//
 // A product of 128 rows and 64 columns takes the tensor cores as long as one of 128 columns (64 clocks for 16 keys), so
 // the two parts of the weights cost as much again as the two of the scores. Up to 64 rows therefore have two lanes each:
-// of a warp's 32 lanes the first 16 hold the scores of its 16 rows and the high parts of their weights, the others the low
-// parts, and one product takes both. The warp reads the 16 lanes as a matrix fragment (two rows of four neighbouring
-// threads each), so that every thread works on half as many scores.
-// k_tree_prep packs the queries (normalised, rotated, two parts, laid out as the sweep has them in shared memory) and the trees.
-// A segment that is not the whole of its (sequence, head) leaves its parts to k_tree_join.
+// of a warp's 32 lanes the first 16 hold the scores of its 16 rows and the high parts of their weights, the others the
+// low parts, and one product takes both. The warp reads the 16 lanes as a matrix fragment (two rows of four neighbouring
+// threads each), so that every thread works on half as many scores. (16 trees of 4 and of 16 tokens, 12 and 48 rows, on
+// contexts around 8192: 30.6 and 32.2 us; with a lane for each row 36.4 and 38.2.)
+//
+// The softmax warps pack the queries (normalised, rotated, two parts) and work the trees out themselves: those of a
+// block's first segments while its first keys are on their way, those of a later one when its slot is free. (16 trees of
+// 16: 32.2 us, with a kernel in front of the sweep 34.5, with four more warps for it 36 to 38, as the softmax then has
+// 192 registers. 64 trees of 32 with 128 rows pay for it, 58.0 -> 61.5.)
+//
+// A segment that is not the whole of its (sequence, head) leaves its parts to k_tree_join; a join inside the sweep, by
+// the block that is last to finish, kept the others waiting for memory fences (34.6 -> 39.8 us) and was taken out.
+//
+// What bounds it (device times; 4 key/value heads of 64): up to 64 rows and a long context the bytes of K and V, 0.74 us
+// for a tile of every block (a steady 6.8 TB/s); the call adds the start (lengths, tables, first tiles: 4 us), the last
+// tiles' steps (3 us) and the join (2 to 6 us). 16 trees of 16 on contexts around 8192, pages of 64: 32.2 us, 19.1 of them
+// the bytes; with pages of 16 39 us (eight copies a tile, each of 2 KB). With 128 rows a step takes the tensor cores
+// 2048 clocks for two parts of both factors and the softmax as long: 64 trees of 32 on 700 to 4096 positions, 61.5 us.
+// With 256 rows and an fp32 o (three parts), 64 tokens on 131001 positions, 113 us.
 #include "paged_sweep.cuh"
 
 namespace ne {
@@ -47,6 +62,8 @@ __device__ __forceinline__ TreeShape tree_shape(const PagedTreeArgs& a, int b, b
 constexpr int kTreeThreads = 384;
 // A segment's cost beside its tiles, in tiles; a (sequence, head) of at most so many tiles is never cut; a
 // boundary moves by so many to an end of a longer one.
+// Over 17 batches: a segment's cost of 1 takes up to 6 % more, one of 4 up to 4 % more (but 64 trees of 32 7 % less);
+// whole up to 8 and a boundary moved by 3 up to 3 % more; no moves 4 % more for 128 short sequences, and others 0 to 4 % less.
 constexpr int kTreeOver = 2, kTreeWhole = 4, kTreeSlack = 2;
 
 template <int D>
@@ -67,11 +84,11 @@ struct TreeCfg {
   // the third parts go to 384 + 64 g, with SPLIT in the place of S.
   static constexpr uint32_t kColO = 0, kColS = 128, kColP = 384;
 };
-constexpr int kTreeVars = 480, kTreePlan = 488, kTreeSums = 544, kTreeInfo = 608, kTreeMl = 1664;
-static_assert(sizeof(TreeInfo) % 16 == 0, "copied in one piece");
+constexpr int kTreeVars = 480, kTreePlan = 488, kTreeSums = 544, kTreeInfo = 608, kTreeMl = 2720;
 constexpr int kTreeCum = kTreeMl + 4 * kTile * 8;
-static_assert(kTreeInfo + 2 * sizeof(TreeInfo) <= kTreeMl && kTreePlan + sizeof(SweepPlan) <= kTreeSums, "head");
-static_assert((4 + 2 * TreeCfg<32>::kKStages + 2 * TreeCfg<32>::kVStages + 4 + 8 + 3 + 4 + 4 + 2 + 3) * 8 <= kTreeVars, "barriers");
+static_assert(kTreeInfo + 4 * sizeof(TreeInfo) <= kTreeMl && kTreePlan + sizeof(SweepPlan) <= kTreeSums, "head");
+static_assert((2 + 2 * TreeCfg<32>::kKStages + 2 * TreeCfg<32>::kVStages + 4 + 8 + 3 + 4 + 4 + 2 + 3) * 8 <= kTreeVars,
+              "barriers");
 __host__ __device__ constexpr int tree_head(int B) { return (kTreeCum + (B + 1) * 4 + B + 1023) / 1024 * 1024; }
 
 // The tile's bits of a mask over positions that begins `r` positions before position 0 of the tree (r < 0: in the
@@ -120,49 +137,6 @@ __device__ __forceinline__ void tree_masks(int (&up)[2], int nodes, int lane, in
   }
 }
 
-// Queries and trees: a thread takes a 16-byte chunk of a row of a (sequence, head); rows behind the last, and of tokens
-// that the tree does not have, are zeros. Every warp works the tree's masks out for itself while its
-// queries are on their way.
-template <int D>
-__global__ void __launch_bounds__(128) k_tree_prep(const __grid_constant__ PagedTreeArgs a, int rows) {
-  constexpr int kCPR = D / 8;
-  pdl_launch();
-  const int b = blockIdx.y, lane = threadIdx.x & 31, i = blockIdx.x * 128 + threadIdx.x;
-  const int c = i % kCPR, hr = i / kCPR, r = hr % (a.tiles * rows), g = hr / (a.tiles * rows);  // rows: of a tile, as packed
-  const bool in = g < a.Hkv && r < a.R;
-  const int t = in ? (int)fdiv((uint32_t)r, a.div_g) : 0;
-  QueryChunk x = {};
-  if (in) x.v = load_rope_chunk<D>(a.q + (size_t)(b * a.Tq + t) * a.q_stride + (g * a.G + (r - t * a.G)) * D, c, a.rope_half != 0);
-  uint4 wv = make_uint4(0, 0, 0, 0);
-  if (a.qw) wv = load_rope_chunk<D>(a.qw, c, a.rope_half != 0);
-  int up[2];
-#pragma unroll
-  for (int h = 0; h < 2; h++) up[h] = lane + 32 * h < a.Tq ? a.parents[b * a.parent_stride + lane + 32 * h] : -1;
-  const TreeShape s = tree_shape(a, b, i == 0);
-  unsigned long long mask[2];
-  tree_masks(up, s.nodes, lane, i < 32 ? a.status : nullptr, mask);
-  const int depth[2] = {__popcll(mask[0]) - 1, __popcll(mask[1]) - 1};
-  const int d0 = __shfl_sync(0xffffffffu, depth[0], t & 31), d1 = __shfl_sync(0xffffffffu, depth[1], t & 31);
-  x.on = in && t < s.nodes;
-  if (x.on) rope_coeffs<D>(a.rope, s.len - s.nodes + (t < 32 ? d0 : d1), c, x.c0, x.c1);
-  uint4 hi, lo;
-  query_finish<D>(a, x, a.qw != nullptr, wv, hi, lo);
-  if (g < a.Hkv) {
-    const size_t part = (size_t)rows * D * 2;
-    unsigned char* to = a.packed + (((size_t)b * a.Hkv + g) * a.tiles + r / rows) * 2 * part + swz(r % rows, c, D * 2);
-    *reinterpret_cast<uint4*>(to) = hi;
-    *reinterpret_cast<uint4*>(to + part) = lo;
-  }
-  if (i < 32) {
-    a.info[b].mask[lane] = mask[0];
-    a.info[b].mask[lane + 32] = mask[1];
-    if (lane == 0) {
-      a.info[b].ctx = s.len - s.nodes;
-      a.info[b].nodes = s.nodes;
-    }
-  }
-}
-
 // N values to place `to` of o (bf16 or fp32), scaled.
 template <int N>
 __device__ __forceinline__ void put_columns(const PagedTreeArgs& a, size_t to, const float (&v)[N], float inv, bool live) {
@@ -193,15 +167,15 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
   extern __shared__ uint8_t smem_raw[];
   uint8_t* head = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint64_t* q_full = reinterpret_cast<uint64_t*>(head);  // [2] the slot's queries are packed
-  uint64_t* q_empty = q_full + 2;          // [2] the slot's segment has left it
-  uint64_t* k_full = q_empty + 2;          // [SK]
+  uint64_t* k_full = q_full + 2;           // [SK]
   uint64_t* k_empty = k_full + SK;         // [SK] the last S = Q K^T of the stage has completed
   uint64_t* v_full = k_empty + SK;         // [SV]
   uint64_t* v_empty = v_full + SV;         // [SV] the O += P V of the stage have completed
   uint64_t* s_full = v_empty + SV;         // [group][2] the group's steps in turn
-  uint64_t* p_ready = s_full + 4;          // [group][2][2] the weights of the tile's last 64 keys, and of the first (SPLIT: all)
-  uint64_t* pv_done = p_ready + 8;         // [3] per buffer of S and P (FULL: [group]); SPLIT, not FULL: [group] the scores are in registers
-  uint64_t* o_done = pv_done + 3;          // [group][2] the same per group's step, for the group
+  uint64_t* p_ready = s_full + 4;          // [group][2][2] weights of the tile's last 64 keys, and of the first (SPLIT: all)
+  // [3] per buffer of S and P its weights are read (FULL: [group]); SPLIT, not FULL: [group] the scores are in registers
+  uint64_t* pv_done = p_ready + 8;
+  uint64_t* o_done = pv_done + 3;          // [group][2] the group's steps in turn: O has the step
   uint64_t* part_full = o_done + 4;        // [group][2] the other group's part of a segment that this one finishes
   uint64_t* gsync = part_full + 4;         // [group]
   uint64_t* drain = gsync + 2;             // [3] per issuing thread
@@ -209,7 +183,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
   volatile int* abort = reinterpret_cast<volatile int*>(head + kTreeVars) + 1;
   volatile SweepPlan* splan = reinterpret_cast<volatile SweepPlan*>(head + kTreePlan);
   int* wsum = reinterpret_cast<int*>(head + kTreeSums);
-  TreeInfo* info = reinterpret_cast<TreeInfo*>(head + kTreeInfo);  // [2] per slot
+  // [4] segments in turn: with RT == 2 a group can be at its first step of one while the other packs the next but one
+  TreeInfo* info = reinterpret_cast<TreeInfo*>(head + kTreeInfo);
   float2* ml_other = reinterpret_cast<float2*>(head + kTreeMl);    // [2][128] per slot
   float2* ml_own = ml_other + 2 * kTile;                           // [2][128] per group
   int* cum = reinterpret_cast<int*>(head + kTreeCum);
@@ -219,8 +194,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
   if (tid == 0) {
     *abort = 0;
     for (int k = 0; k < 2; k++) {
-      mbar_init(q_full + k, 1);
-      mbar_init(q_empty + k, 4);
+      mbar_init(q_full + k, RT * 4);  // the warps that pack a row tile
       mbar_init(gsync + k, 4);
     }
     for (int k = 0; k < SK; k++) {
@@ -356,7 +330,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
         }
         load(&a.map_pv, smem + C::kOffV + k % SV * TB, v_full + k % SV, v_empty + k % SV, k / SV);
         if (!ok) {
-          for (int x = k - SK + 1 < 0 ? 0 : k - SK + 1; lane == 0 && x <= k; x++) mbar_wait(k_full + x % SK, (x / SK) & 1, &never);
+          const int k0 = k - SK + 1 < 0 ? 0 : k - SK + 1;
+          for (int x = k0; lane == 0 && x <= k; x++) mbar_wait(k_full + x % SK, (x / SK) & 1, &never);
           for (int x = k - SV < 0 ? 0 : k - SV; lane == 0 && x < k; x++) mbar_wait(v_full + x % SV, (x / SV) & 1, &never);
           break;
         }
@@ -374,48 +349,20 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
       }
     }
   } else if (warp == 1) {
-    // ------------------------------------------------------------ queries and trees; S = Q K^T issuer
+    // ------------------------------------------------------------ S = Q K^T issuer
     if (lane == 0) {
       constexpr uint32_t idS = idesc_fp16(128, 128, false, false);
       constexpr uint32_t kStepK = 32 >> 4, tstep = (uint32_t)TB >> 4;
       const uint64_t dQ0 = smem_desc(smem_u32(smem), 16, C::kSBO, C::kSwz);
       const uint64_t dK0 = smem_desc(smem_u32(smem + C::kOffK), 16, C::kSBO, C::kSwz);
       bool ok = true;
-      int n = 0, k = 0, e = 0, qe = 0;  // steps, tiles, segments; segments whose queries are on their way
-      SegWalk<kTreeOver> qs = sw;
-      bool qon = qs.next();
-      const auto load = [&]() {  // the next segment's queries: its slot is free
-        const int slot = slot_of(qe), nu = units(qs);
-        constexpr uint32_t part = NR * C::kSpan, kBlocks = SPLIT ? 4 : 1, block = part / kBlocks;
-        mbar_arrive_expect_tx(q_full + slot, (uint32_t)(nu * 2 * part + sizeof(TreeInfo)));
-        bulk_load(info + slot, a.info + qs.b, sizeof(TreeInfo), q_full + slot);
-#pragma unroll 1
-        for (int u = 0; u < nu; u++) {
-          const unsigned char* from = a.packed + (((size_t)qs.b * a.Hkv + qs.g / a.pairs) * a.tiles + qs.g % a.pairs * 2 + u) * 2 * part;
-          uint8_t* to = smem + (RT == 1 ? 2 * slot : 2 * u) * TB;
-#pragma unroll
-          for (int f = 0; f < (int)kBlocks; f++) {  // the rows of a warp to the first half of its lanes
-            bulk_load(to + 2 * f * block, from + f * block, block, q_full + slot);
-            bulk_load(to + TB + 2 * f * block, from + part + f * block, block, q_full + slot);
-          }
-        }
-        qe++;
-        qon = qs.next();
-      };
-      pdl_wait();  // k_tree_prep has written them
-      if (qon) load();
-      if (RT == 1 && qon) load();
+      int n = 0, k = 0, e = 0;  // steps, tiles, segments
       while (ok && sw.next()) {
         const int nu = units(sw), slot = slot_of(e);
-        if (qe == e) {
-          if (!(ok = mbar_wait(q_empty + slot, (use_of(e) - 1) & 1, abort))) break;
-          load();
-        }
         if (!(ok = mbar_wait(q_full + slot, use_of(e) & 1, abort))) break;
 #pragma unroll 1
         for (int i = sw.n0; ok && i < sw.n1; i++, k++) {
           const int st = k % SK;
-          if (RT == 1 && qon && qe == e + 1 && use_of(qe) > 0 && mbar_test(q_empty + slot_of(qe), (use_of(qe) - 1) & 1)) load();
           if (!(ok = mbar_wait(k_full + st, (k / SK) & 1, abort))) break;
 #pragma unroll 1
           for (int u = 0; u < nu; u++, n++) {
@@ -429,7 +376,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
             mma_ss_chain<D / 16>(to, dq + (uint64_t)tstep, kStepK, dk, kStepK, idS, 1u);
             uint64_t* full = s_full + 2 * (n & 1) + ((n >> 1) & 1);
             mma_commit(full);
-            mbar_arrive(full);  // what this thread has seen (the tree of the slot) comes with it
+            mbar_arrive(full);  // what this thread has seen (the tree of the segment) comes with it
           }
           if (ok) mma_commit(k_empty + st);
         }
@@ -441,9 +388,6 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
       }
       mma_commit(drain);
       mbar_wait(drain, 0, &never);
-      // let every copy issued above land before the block can exit: the last of each slot
-      if (RT == 1 && qe > 1) mbar_wait(q_full + slot_of(qe - 2), use_of(qe - 2) & 1, &never);
-      if (qe > 0) mbar_wait(q_full + slot_of(qe - 1), use_of(qe - 1) & 1, &never);
     }
   } else if (warp < 4) {
     // ------------------------------------------------------------ O += P V issuer of a group
@@ -504,380 +448,461 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
     const uint32_t trow = tmem + ((uint32_t)(q4 * 32) << 16);
     const uint32_t obuf = trow + C::kColO + 64u * grp;
     const float sl2 = a.scale_log2;
+    uint4 wv = make_uint4(0, 0, 0, 0);
+    // This group packs row tile u of a segment, number e of the block, and signals it `times` times.
+    const auto pack = [&](const SegWalk<kTreeOver>& x, int e, int u, int times) {
+      constexpr int kCPR = D / 8, kItems = NR * kCPR / 128, kBatch = kItems < 4 ? kItems : 4;  // 16-byte chunks of a thread
+      const int pr = x.g % a.pairs, g = x.g / a.pairs, c = lane % kCPR, r0 = pr * 2 * kTile + u * kTile;
+      uint8_t* to = smem + (RT == 1 ? 2 * slot_of(e) : 2 * u) * TB;
+      const int total = x.nt * kTile - pad[x.b];
+      int up[2];
+#pragma unroll
+      for (int h = 0; h < 2; h++) up[h] = lane + 32 * h < a.Tq ? a.parents[x.b * a.parent_stride + lane + 32 * h] : -1;
+      const int nodes = total > 0 ? (a.nodes ? a.nodes[x.b] : a.Tq) : 0;
+      TreeInfo& tree = info[e & 3];
+      if (a.qw) wv = load_rope_chunk<D>(a.qw, c, a.rope_half != 0);
+      unsigned long long mask[2];
+      tree_masks(up, nodes, lane, q4 == 0 ? a.status : nullptr, mask);
+      const int depth[2] = {__popcll(mask[0]) - 1, __popcll(mask[1]) - 1};
+      if (q4 == 0) {
+        tree.mask[lane] = mask[0];
+        tree.mask[lane + 32] = mask[1];
+        if (lane == 0) {
+          tree.ctx = total - nodes;
+          tree.nodes = nodes;
+        }
+      }
+#pragma unroll 1
+      for (int i0 = 0; i0 < kItems; i0 += kBatch) {
+        QueryChunk q[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; i++) {
+          const int rt = ((i0 + i) * 128 + r) / kCPR, row = r0 + rt, t = row < a.R ? (int)fdiv((uint32_t)row, a.div_g) : 0;
+          const int d0 = __shfl_sync(0xffffffffu, depth[0], t & 31), d1 = __shfl_sync(0xffffffffu, depth[1], t & 31);
+          q[i] = query_load_at<D>(a, row < a.R && t < nodes, x.b, g, row, t, c, total - nodes + (t < 32 ? d0 : d1));
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; i++) {
+          const int rt = ((i0 + i) * 128 + r) / kCPR;
+          uint4 hi, lo;
+          query_finish<D>(a, q[i], a.qw != nullptr, wv, hi, lo);
+          const uint32_t at = swz(SPLIT ? 32 * (rt / 16) + rt % 16 : rt, c, C::kSpan);
+          *reinterpret_cast<uint4*>(to + at) = hi;
+          *reinterpret_cast<uint4*>(to + TB + at) = lo;
+        }
+      }
+      fence_proxy_async_smem();
+      for (int i = 0; i < times; i++) warp_arrive(q_full + slot_of(e));
+    };
+    // Segments are packed two ahead where two have slots of their own (RT == 1), else one.
+    constexpr int kAhead = RT == 1 ? 2 : 1;
+    SegWalk<kTreeOver> qs = sw;
+    bool qon = true;
     bool ok = true;
-    int n = 0, kt = 0, joined0 = 0, joined1 = 0, syncs = 0;  // steps, stages; segments that each group finished with the other; group barriers
+    int n = 0, kt = 0, syncs = 0;      // steps, stages, group barriers
+    int joined0 = 0, joined1 = 0;      // segments that each group finished with the other
     const auto group_sync = [&]() {
       warp_arrive(gsync + grp);
       return __all_sync(0xffffffffu, mbar_wait(gsync + grp, syncs++ & 1, abort));
     };
-    for (int e = 0; ok && sw.next(); e++) {
-      const int nu = units(sw), slot = slot_of(e), first = n, end = first + (sw.n1 - sw.n0) * nu;
-      const int mine = first + ((first ^ grp) & 1);           // this group's first step
-      const bool joint = nu == 1 && end - first >= 2;         // both groups have a part of the same rows
-      const int last = (end - 1) & 1;                         // the group of the last step
-      const int k0 = kt;
-      n = end;
-      kt += sw.n1 - sw.n0;
-      const int turn = last ? joined1 : joined0;
-      if (joint) last ? joined1++ : joined0++;
-      if (mine >= end) continue;
-      const int pr = sw.g % a.pairs, u = nu == 2 ? (mine - first) & 1 : 0;
-      const int row = pr * 2 * kTile + u * kTile + rr;        // row of the (sequence, head)
-      int ctx = 0, total = 0;
-      bool live = false;
-      // a thread's row, or (SPLIT) its two rows lane / 4 and lane / 4 + 8 of the warp's 16: mask, maximum, sum
-      constexpr int NQ = SPLIT ? 2 : 1;
-      unsigned long long mask[NQ];
-      float r_run[NQ], l_run[NQ], m_use[NQ];
-      float acc[FULL ? D : 1];  // FULL: O of the lane's row so far
-#pragma unroll
-      for (int x = 0; FULL && x < D; x++) acc[x] = 0.f;
-      // FULL: adds the O of step n to it, then scales both
-      const auto flush = [&](int n, float f) {
-        if (!__all_sync(0xffffffffu, mbar_wait(o_done + 2 * grp + ((n >> 1) & 1), (n >> 2) & 1, abort))) return false;
-        tc_fence_after();
-#pragma unroll
-        for (int c = 0; c < (FULL ? D / 16 : 0); c++) {
-          uint32_t w[16];
-          tmem_ld16(obuf + c * 16, w);
-          tmem_wait_ld();
-#pragma unroll
-          for (int x = 0; x < 16; x++) acc[(FULL ? 16 : 0) * c + (FULL ? x : 0)] = (acc[(FULL ? 16 : 0) * c + (FULL ? x : 0)] + __uint_as_float(w[x])) * f;
+    for (int e = -kAhead; ok; e++) {
+      qon = qon && qs.next();  // segment e + kAhead, of which this group packs row tiles pack0 .. pack1 - 1
+      int pack0 = 0, pack1 = 0, times = 1;
+      if (e < 0) {
+        if (!qon) continue;
+        if (RT == 1) {
+          pack1 = grp == e + kAhead ? 1 : 0;
+        } else {
+          pack0 = grp;
+          pack1 = min(grp + 1, units(qs));
+          times = units(qs) == 2 ? 1 : 2;
         }
-        return true;
-      };
-      int s = mine;
-      for (; s < end; s += 2) {
-        const int buf = SPLIT || FULL ? grp : s % 3, tile = sw.n0 + (nu == 2 ? (s - first) >> 1 : s - first);
-        const uint32_t sbuf = trow + C::kColS + 128u * buf, pown = trow + C::kColP + 64u * grp;
-        const uint32_t pbuf = SPLIT ? pown : sbuf, third = SPLIT ? sbuf : pown;
-        ok = __all_sync(0xffffffffu, mbar_wait(s_full + 2 * grp + ((s >> 1) & 1), (s >> 2) & 1, abort));
-        if (!ok) break;
-        tc_fence_after();
-        if (s == mine) {
-          const auto token = [&](int x) { return x < a.R ? (int)fdiv((uint32_t)x, a.div_g) : kTreeMax; };
-          ctx = info[slot].ctx;
-          total = ctx + info[slot].nodes;
-          live = token(row) < info[slot].nodes;
+      } else {
+        if (!sw.next()) break;
+        const int nu = units(sw), slot = slot_of(e), first = n, end = first + (sw.n1 - sw.n0) * nu;
+        const int mine = first + ((first ^ grp) & 1);           // this group's first step
+        const bool joint = nu == 1 && end - first >= 2;         // both groups have a part of the same rows
+        const int last = (end - 1) & 1;                         // the group of the last step
+        const int k0 = kt;
+        n = end;
+        kt += sw.n1 - sw.n0;
+        const int turn = last ? joined1 : joined0;
+        if (joint) last ? joined1++ : joined0++;
+        if (mine >= end) continue;
+        const int pr = sw.g % a.pairs, u = nu == 2 ? (mine - first) & 1 : 0;
+        const int row = pr * 2 * kTile + u * kTile + rr;        // row of the (sequence, head)
+        int ctx = 0, total = 0;
+        bool live = false;
+        // a thread's row, or (SPLIT) its two rows lane / 4 and lane / 4 + 8 of the warp's 16: mask, maximum, sum
+        constexpr int NQ = SPLIT ? 2 : 1;
+        unsigned long long mask[NQ];
+        float r_run[NQ], l_run[NQ], m_use[NQ];
+        float acc[FULL ? D : 1];  // FULL: O of the lane's row so far
 #pragma unroll
-          for (int i = 0; i < NQ; i++) {
-            const int t = token(SPLIT ? q4 * 16 + lane / 4 + 8 * i : row);
-            mask[i] = t < info[slot].nodes ? info[slot].mask[t] : 0ull;
-          }
-        }
-        const bool edge = (tile + 1) * kTile > ctx;  // the tile ends in the tree or behind it
-        if (edge && total - tile * kTile < kTile) {
-          // what lies behind the last position may be anything: its weight is 0, but 0 times a NaN is not
-          const int kt = k0 + tile - sw.n0;
-          ok = __all_sync(0xffffffffu, mbar_wait(v_full + kt % SV, (kt / SV) & 1, abort));
-          if (!ok) break;
-          if (r >= total - tile * kTile) {
-            uint4* v = reinterpret_cast<uint4*>(smem + C::kOffV + kt % SV * TB + r * C::kSpan);
+        for (int x = 0; FULL && x < D; x++) acc[x] = 0.f;
+        // FULL: adds the O of step n to it, then scales both
+        const auto flush = [&](int n, float f) {
+          if (!__all_sync(0xffffffffu, mbar_wait(o_done + 2 * grp + ((n >> 1) & 1), (n >> 2) & 1, abort))) return false;
+          tc_fence_after();
 #pragma unroll
-            for (int c = 0; c < D / 8; c++) v[c] = make_uint4(0u, 0u, 0u, 0u);
-            fence_proxy_async_smem();
-          }
-        }
-        // 64 scores of a thread at a time. With one row and 128 they are read once for the maximum and (but for the last 64)
-        // once more for the weights: with all in registers the loop does not fit the schedulers' instruction caches
-        // (warps then wait for instructions longer than they issue them).
-        uint32_t sc[64];
-        const auto load = [&](int h) {
-          uint32_t(&lo)[32] = *reinterpret_cast<uint32_t(*)[32]>(sc);
-          uint32_t(&hi)[32] = *reinterpret_cast<uint32_t(*)[32]>(sc + 32);
-          if (SPLIT) {
-            tmem_ld16x64(sbuf, lo);
-            tmem_ld16x64(sbuf + 64, hi);
-          } else {
-            tmem_ld32(sbuf + h * 64, lo);
-            tmem_ld32(sbuf + h * 64 + 32, hi);
-          }
-          tmem_wait_ld();
-          if (edge && SPLIT) {
+          for (int c = 0; c < (FULL ? D / 16 : 0); c++) {
+            uint32_t w[16];
+            tmem_ld16(obuf + c * 16, w);
+            tmem_wait_ld();
 #pragma unroll
-            for (int c = 0; c < 4; c++) {
-              const int at = tile * kTile + c * 32 - ctx;
-              const uint32_t see[2] = {tree_word(mask[0], at) >> (2 * (lane & 3)), tree_word(mask[NQ - 1], at) >> (2 * (lane & 3))};
-#pragma unroll
-              for (int x = 0; x < 16; x++)  // columns 8 (x / 4) + 2 (lane % 4) + x % 2 of the 32, row x / 2 % 2
-                if (!(see[x / 2 % 2] & (1u << (8 * (x / 4) + x % 2)))) sc[16 * c + x] = 0xff800000u;
-            }
-          } else if (edge) {
-#pragma unroll
-            for (int c = 0; c < 2; c++) {
-              const uint32_t see = tree_word(mask[0], tile * kTile + h * 64 + c * 32 - ctx);
-#pragma unroll
-              for (int x = 0; x < 32; x++)
-                if (!(see & (1u << x))) sc[32 * c + x] = 0xff800000u;
+            for (int x = 0; x < 16; x++) {
+              float& y = acc[FULL ? 16 * c + x : 0];
+              y = (y + __uint_as_float(w[x])) * f;
             }
           }
+          return true;
         };
-        float mxr[NQ];
-        if (SPLIT) {
-          load(0);
-          if (!FULL) {
-            tc_fence_before();
-            warp_arrive(pv_done + grp);
-          }
-          float m2[2][2] = {{-INFINITY, -INFINITY}, {-INFINITY, -INFINITY}};
-#pragma unroll
-          for (int x = 0; x < 64; x += 2)
-            m2[(x >> 1) & 1][(x >> 2) & 1] = fmax3(m2[(x >> 1) & 1][(x >> 2) & 1], __uint_as_float(sc[x]), __uint_as_float(sc[x + 1]));
-#pragma unroll
-          for (int i = 0; i < NQ; i++) {
-            float m = fmaxf(m2[i][0], m2[i][1]);
-            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-            mxr[i] = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-          }
-        } else {
-          float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll 1
-          for (int h = 0; h < 2; h++) {
-            load(h);
-#pragma unroll
-            for (int x = 0; x < 64; x += 2)
-              mx4[(x >> 1) & 3] = fmax3(mx4[(x >> 1) & 3], __uint_as_float(sc[x]), __uint_as_float(sc[x + 1]));
-          }
-          mxr[0] = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
-        }
-        float alpha[NQ];
-        if (s == mine) {
-#pragma unroll
-          for (int i = 0; i < NQ; i++) {
-            r_run[i] = mxr[i];
-            alpha[i] = 0.f;
-            l_run[i] = 0.f;
-          }
-        } else {
-          // O and the sum follow the maximum only when some row's grew by more than 2^8 (or came out of nothing)
-          bool grow = false;
-#pragma unroll
-          for (int i = 0; i < NQ; i++) {
-            alpha[i] = 1.f;
-            grow = grow || __fmul_rn(fmaxf(r_run[i], mxr[i]), sl2) > __fmul_rn(r_run[i], sl2) + 8.0f;
-          }
-          float lane_a = 1.f;  // of the lane's row
-          if (__any_sync(0xffffffffu, grow)) {
-#pragma unroll
-            for (int i = 0; i < NQ; i++) {
-              const float r_new = fmaxf(r_run[i], mxr[i]);
-              alpha[i] = r_run[i] == -INFINITY ? 0.f : ex2(__fmul_rn(r_run[i], sl2) - __fmul_rn(r_new, sl2));
-              r_run[i] = r_new;
-            }
-            lane_a = alpha[0];
-            if (SPLIT) {
-              const float x = __shfl_sync(0xffffffffu, alpha[0], 4 * (lane & 7)), y = __shfl_sync(0xffffffffu, alpha[NQ - 1], 4 * (lane & 7));
-              lane_a = lane & 8 ? y : x;
-            }
-            if (!FULL) {
-              ok = __all_sync(0xffffffffu, mbar_wait(o_done + 2 * grp + (((s - 2) >> 1) & 1), ((s - 2) >> 2) & 1, abort));
-              if (!ok) break;
-              tc_fence_after();
-#pragma unroll 1
-              for (int c = 0; c < D / 16; c++) {
-                uint32_t w[16];
-                tmem_ld16(obuf + c * 16, w);
-                tmem_wait_ld();
-#pragma unroll
-                for (int x = 0; x < 16; x++) w[x] = __float_as_uint(__uint_as_float(w[x]) * lane_a);
-                tmem_st16(obuf + c * 16, w);
-              }
-            }
-          }
-          if (FULL && !(ok = flush(s - 2, lane_a))) break;
-        }
-        if (SPLIT ? s >= 2 : FULL && s >= 2 && s == mine) {  // the weights of the step before have been read
-          ok = __all_sync(0xffffffffu, mbar_wait(o_done + 2 * grp + (((s - 2) >> 1) & 1), ((s - 2) >> 2) & 1, abort));
+        int s = mine;
+        for (; s < end; s += 2) {
+          const int buf = SPLIT || FULL ? grp : s % 3, tile = sw.n0 + (nu == 2 ? (s - first) >> 1 : s - first);
+          const uint32_t sbuf = trow + C::kColS + 128u * buf, pown = trow + C::kColP + 64u * grp;
+          const uint32_t pbuf = SPLIT ? pown : sbuf, third = SPLIT ? sbuf : pown;
+          ok = __all_sync(0xffffffffu, mbar_wait(s_full + 2 * grp + ((s >> 1) & 1), (s >> 2) & 1, abort));
           if (!ok) break;
           tc_fence_after();
-        }
-        uint64_t sum[NQ][4 / NQ], negm[NQ];
+          if (s == mine) {
+            const auto token = [&](int x) { return x < a.R ? (int)fdiv((uint32_t)x, a.div_g) : kTreeMax; };
+            ctx = info[e & 3].ctx;
+            total = ctx + info[e & 3].nodes;
+            live = token(row) < info[e & 3].nodes;
 #pragma unroll
-        for (int i = 0; i < NQ; i++) {
-          m_use[i] = r_run[i] == -INFINITY ? 0.f : __fmul_rn(r_run[i], sl2);
-          negm[i] = f2(-m_use[i], -m_use[i]);
-#pragma unroll
-          for (int j = 0; j < 4 / NQ; j++) sum[i][j] = 0ull;
-        }
-        const uint64_t sl2x2 = f2(sl2, sl2), minus = f2(-1.f, -1.f);
-#pragma unroll 1
-        for (int h = 1; h >= (SPLIT ? 1 : 0); h--) {
-          if (h == 0) load(0);
-          uint32_t ph[32], pl[32], pt[32];
-#pragma unroll
-          for (int x = 0; x < 32; x++) {
-            constexpr int kSums = 4 / NQ;
-            const int i = SPLIT ? x & 1 : 0, j = (SPLIT ? x >> 1 : x) % kSums;
-            float x0, x1, l0, l1;
-            f2_split(f2_fma(f2(__uint_as_float(sc[2 * x]), __uint_as_float(sc[2 * x + 1])), sl2x2, negm[i]), x0, x1);
-            const uint64_t pp = f2(ex2(x0), ex2(x1));
-            f2_split(pp, x0, x1);
-            ph[x] = pack_bf16(x0, x1);
-            const uint64_t ll = f2_fma(f2(bf_lo(ph[x]), bf_hi(ph[x])), minus, pp);
-            f2_split(ll, l0, l1);
-            pl[x] = pack_bf16(l0, l1);
-            if (FULL) {
-              f2_split(f2_fma(f2(bf_lo(pl[x]), bf_hi(pl[x])), minus, ll), l0, l1);
-              pt[x] = pack_bf16(l0, l1);
-            }
-            sum[i][j] = f2_add(sum[i][j], pp);
-            if (!SPLIT && x % 8 == 7) {
-              tmem_st8(pbuf + 64 * h + x - 7, *reinterpret_cast<uint32_t(*)[8]>(ph + x - 7));
-              tmem_st8(pbuf + 64 * h + 32 + x - 7, *reinterpret_cast<uint32_t(*)[8]>(pl + x - 7));
-              if (FULL) tmem_st8(third + 32 * h + x - 7, *reinterpret_cast<uint32_t(*)[8]>(pt + x - 7));
-            }
-            if (SPLIT && x % 16 == 15) {
-              tmem_st16x32(pbuf + 2 * (x - 15), *reinterpret_cast<uint32_t(*)[16]>(ph + x - 15));
-              tmem_st16x32(pbuf + (16u << 16) + 2 * (x - 15), *reinterpret_cast<uint32_t(*)[16]>(pl + x - 15));
-              if (FULL) {  // beside the low parts
-                const uint32_t none[16] = {0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
-                tmem_st16x32(third + 2 * (x - 15), none);
-                tmem_st16x32(third + (16u << 16) + 2 * (x - 15), *reinterpret_cast<uint32_t(*)[16]>(pt + x - 15));
-              }
+            for (int i = 0; i < NQ; i++) {
+              const int t = token(SPLIT ? q4 * 16 + lane / 4 + 8 * i : row);
+              mask[i] = t < info[e & 3].nodes ? info[e & 3].mask[t] : 0ull;
             }
           }
-          tmem_wait_st();
-          tc_fence_before();
-          warp_arrive(p_ready + 4 * grp + 2 * ((s >> 1) & 1) + (h == 0 ? 1 : 0));
-        }
+          const bool edge = (tile + 1) * kTile > ctx;  // the tile ends in the tree or behind it
+          if (edge && total - tile * kTile < kTile) {
+            // what lies behind the last position may be anything: its weight is 0, but 0 times a NaN is not
+            const int kt = k0 + tile - sw.n0;
+            ok = __all_sync(0xffffffffu, mbar_wait(v_full + kt % SV, (kt / SV) & 1, abort));
+            if (!ok) break;
+            if (r >= total - tile * kTile) {
+              uint4* v = reinterpret_cast<uint4*>(smem + C::kOffV + kt % SV * TB + r * C::kSpan);
 #pragma unroll
-        for (int i = 0; i < NQ; i++) {
-          uint64_t t = f2_add(sum[i][0], sum[i][1]);
-          if (NQ == 1) t = f2_add(t, f2_add(sum[i][4 / NQ - 2], sum[i][4 / NQ - 1]));
-          float x, y;
-          f2_split(t, x, y);
-          l_run[i] = fmaf(l_run[i], alpha[i], x + y);
-        }
-      }
-      float lane_m = m_use[0], lane_l = l_run[0];  // of the lane's row
-      if (SPLIT) {
-        float m2[2], l2[2];
+              for (int c = 0; c < D / 8; c++) v[c] = make_uint4(0u, 0u, 0u, 0u);
+              fence_proxy_async_smem();
+            }
+          }
+          // 64 scores of a thread at a time. With one row and 128 they are read once for the maximum and (but for the last 64)
+          // once more for the weights: with all in registers the loop does not fit the schedulers' instruction caches
+          // (warps then wait for instructions longer than they issue them).
+          uint32_t sc[64];
+          const auto load = [&](int h) {
+            uint32_t(&lo)[32] = *reinterpret_cast<uint32_t(*)[32]>(sc);
+            uint32_t(&hi)[32] = *reinterpret_cast<uint32_t(*)[32]>(sc + 32);
+            if (SPLIT) {
+              tmem_ld16x64(sbuf, lo);
+              tmem_ld16x64(sbuf + 64, hi);
+            } else {
+              tmem_ld32(sbuf + h * 64, lo);
+              tmem_ld32(sbuf + h * 64 + 32, hi);
+            }
+            tmem_wait_ld();
+            if (edge && SPLIT) {
 #pragma unroll
-        for (int i = 0; i < NQ; i++) {
-          float l = l_run[i];
-          l += __shfl_xor_sync(0xffffffffu, l, 1);
-          l += __shfl_xor_sync(0xffffffffu, l, 2);
-          l2[i] = __shfl_sync(0xffffffffu, l, 4 * (lane & 7));
-          m2[i] = __shfl_sync(0xffffffffu, m_use[i], 4 * (lane & 7));
-        }
-        lane_m = lane & 8 ? m2[1] : m2[0];
-        lane_l = lane & 8 ? l2[1] : l2[0];
-      }
-      if (!ok) break;
-      // the segment's unnormalised O, maximum (log2 units) and sum
-      if (FULL) {
-        if (!(ok = flush(s - 2, 1.f))) break;
+              for (int c = 0; c < 4; c++) {
+                const int at = tile * kTile + c * 32 - ctx;
+                const int by = 2 * (lane & 3);
+                const uint32_t see[2] = {tree_word(mask[0], at) >> by, tree_word(mask[NQ - 1], at) >> by};
 #pragma unroll
-        for (int c = 0; c < (FULL ? D / 16 : 0); c++) {
-          uint32_t w[16];
+                for (int x = 0; x < 16; x++)  // columns 8 (x / 4) + 2 (lane % 4) + x % 2 of the 32, row x / 2 % 2
+                  if (!(see[x / 2 % 2] & (1u << (8 * (x / 4) + x % 2)))) sc[16 * c + x] = 0xff800000u;
+              }
+            } else if (edge) {
 #pragma unroll
-          for (int x = 0; x < 16; x++) w[x] = __float_as_uint(acc[(FULL ? 16 : 0) * c + (FULL ? x : 0)]);
-          tmem_st16(obuf + c * 16, w);
+              for (int c = 0; c < 2; c++) {
+                const uint32_t see = tree_word(mask[0], tile * kTile + h * 64 + c * 32 - ctx);
+#pragma unroll
+                for (int x = 0; x < 32; x++)
+                  if (!(see & (1u << x))) sc[32 * c + x] = 0xff800000u;
+              }
+            }
+          };
+          float mxr[NQ];
+          if (SPLIT) {
+            load(0);
+            if (!FULL) {
+              tc_fence_before();
+              warp_arrive(pv_done + grp);
+            }
+            float m2[2][2] = {{-INFINITY, -INFINITY}, {-INFINITY, -INFINITY}};
+#pragma unroll
+            for (int x = 0; x < 64; x += 2) {
+              float& y = m2[(x >> 1) & 1][(x >> 2) & 1];
+              y = fmax3(y, __uint_as_float(sc[x]), __uint_as_float(sc[x + 1]));
+            }
+#pragma unroll
+            for (int i = 0; i < NQ; i++) {
+              float m = fmaxf(m2[i][0], m2[i][1]);
+              m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+              mxr[i] = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+            }
+          } else {
+            float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+            for (int h = 0; h < 2; h++) {
+              load(h);
+#pragma unroll
+              for (int x = 0; x < 64; x += 2)
+                mx4[(x >> 1) & 3] = fmax3(mx4[(x >> 1) & 3], __uint_as_float(sc[x]), __uint_as_float(sc[x + 1]));
+            }
+            mxr[0] = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
+          }
+          float alpha[NQ];
+          if (s == mine) {
+#pragma unroll
+            for (int i = 0; i < NQ; i++) {
+              r_run[i] = mxr[i];
+              alpha[i] = 0.f;
+              l_run[i] = 0.f;
+            }
+          } else {
+            // O and the sum follow the maximum only when some row's grew by more than 2^8 (or came out of nothing)
+            bool grow = false;
+#pragma unroll
+            for (int i = 0; i < NQ; i++) {
+              alpha[i] = 1.f;
+              grow = grow || __fmul_rn(fmaxf(r_run[i], mxr[i]), sl2) > __fmul_rn(r_run[i], sl2) + 8.0f;
+            }
+            float lane_a = 1.f;  // of the lane's row
+            if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+              for (int i = 0; i < NQ; i++) {
+                const float r_new = fmaxf(r_run[i], mxr[i]);
+                alpha[i] = r_run[i] == -INFINITY ? 0.f : ex2(__fmul_rn(r_run[i], sl2) - __fmul_rn(r_new, sl2));
+                r_run[i] = r_new;
+              }
+              lane_a = alpha[0];
+              if (SPLIT) {
+                const float x = __shfl_sync(0xffffffffu, alpha[0], 4 * (lane & 7));
+                const float y = __shfl_sync(0xffffffffu, alpha[NQ - 1], 4 * (lane & 7));
+                lane_a = lane & 8 ? y : x;
+              }
+              if (!FULL) {
+                ok = __all_sync(0xffffffffu, mbar_wait(o_done + 2 * grp + (((s - 2) >> 1) & 1), ((s - 2) >> 2) & 1, abort));
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll 1
+                for (int c = 0; c < D / 16; c++) {
+                  uint32_t w[16];
+                  tmem_ld16(obuf + c * 16, w);
+                  tmem_wait_ld();
+#pragma unroll
+                  for (int x = 0; x < 16; x++) w[x] = __float_as_uint(__uint_as_float(w[x]) * lane_a);
+                  tmem_st16(obuf + c * 16, w);
+                }
+              }
+            }
+            if (FULL && !(ok = flush(s - 2, lane_a))) break;
+          }
+          if (SPLIT ? s >= 2 : FULL && s >= 2 && s == mine) {  // the weights of the step before have been read
+            ok = __all_sync(0xffffffffu, mbar_wait(o_done + 2 * grp + (((s - 2) >> 1) & 1), ((s - 2) >> 2) & 1, abort));
+            if (!ok) break;
+            tc_fence_after();
+          }
+          uint64_t sum[NQ][4 / NQ], negm[NQ];
+#pragma unroll
+          for (int i = 0; i < NQ; i++) {
+            m_use[i] = r_run[i] == -INFINITY ? 0.f : __fmul_rn(r_run[i], sl2);
+            negm[i] = f2(-m_use[i], -m_use[i]);
+#pragma unroll
+            for (int j = 0; j < 4 / NQ; j++) sum[i][j] = 0ull;
+          }
+          const uint64_t sl2x2 = f2(sl2, sl2), minus = f2(-1.f, -1.f);
+#pragma unroll 1
+          for (int h = 1; h >= (SPLIT ? 1 : 0); h--) {
+            if (h == 0) load(0);
+            uint32_t ph[32], pl[32], pt[32];
+#pragma unroll
+            for (int x = 0; x < 32; x++) {
+              constexpr int kSums = 4 / NQ;
+              const int i = SPLIT ? x & 1 : 0, j = (SPLIT ? x >> 1 : x) % kSums;
+              float x0, x1, l0, l1;
+              f2_split(f2_fma(f2(__uint_as_float(sc[2 * x]), __uint_as_float(sc[2 * x + 1])), sl2x2, negm[i]), x0, x1);
+              const uint64_t pp = f2(ex2(x0), ex2(x1));
+              f2_split(pp, x0, x1);
+              ph[x] = pack_bf16(x0, x1);
+              const uint64_t ll = f2_fma(f2(bf_lo(ph[x]), bf_hi(ph[x])), minus, pp);
+              f2_split(ll, l0, l1);
+              pl[x] = pack_bf16(l0, l1);
+              if (FULL) {
+                f2_split(f2_fma(f2(bf_lo(pl[x]), bf_hi(pl[x])), minus, ll), l0, l1);
+                pt[x] = pack_bf16(l0, l1);
+              }
+              sum[i][j] = f2_add(sum[i][j], pp);
+              if (!SPLIT && x % 8 == 7) {
+                tmem_st8(pbuf + 64 * h + x - 7, *reinterpret_cast<uint32_t(*)[8]>(ph + x - 7));
+                tmem_st8(pbuf + 64 * h + 32 + x - 7, *reinterpret_cast<uint32_t(*)[8]>(pl + x - 7));
+                if (FULL) tmem_st8(third + 32 * h + x - 7, *reinterpret_cast<uint32_t(*)[8]>(pt + x - 7));
+              }
+              if (SPLIT && x % 16 == 15) {
+                tmem_st16x32(pbuf + 2 * (x - 15), *reinterpret_cast<uint32_t(*)[16]>(ph + x - 15));
+                tmem_st16x32(pbuf + (16u << 16) + 2 * (x - 15), *reinterpret_cast<uint32_t(*)[16]>(pl + x - 15));
+                if (FULL) {  // beside the low parts
+                  const uint32_t none[16] = {0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+                  tmem_st16x32(third + 2 * (x - 15), none);
+                  tmem_st16x32(third + (16u << 16) + 2 * (x - 15), *reinterpret_cast<uint32_t(*)[16]>(pt + x - 15));
+                }
+              }
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            warp_arrive(p_ready + 4 * grp + 2 * ((s >> 1) & 1) + (h == 0 ? 1 : 0));
+          }
+#pragma unroll
+          for (int i = 0; i < NQ; i++) {
+            uint64_t t = f2_add(sum[i][0], sum[i][1]);
+            if (NQ == 1) t = f2_add(t, f2_add(sum[i][4 / NQ - 2], sum[i][4 / NQ - 1]));
+            float x, y;
+            f2_split(t, x, y);
+            l_run[i] = fmaf(l_run[i], alpha[i], x + y);
+          }
         }
-        tmem_wait_st();
-      }
-      ok = __all_sync(0xffffffffu, mbar_wait(o_done + 2 * grp + (((s - 2) >> 1) & 1), ((s - 2) >> 2) & 1, abort));
-      if (!ok) break;
-      tc_fence_after();
-      int lr = r;
-      asm volatile("" : "+r"(lr));  // addresses of this part are not kept in registers over the steps
-      float4* scratch = reinterpret_cast<float4*>(smem + 2 * slot * TB) + lr * (D / 4);  // the slot's queries are no longer needed
-      const auto chunk = [&](int q) { return q ^ (lr & 7); };
-      if (joint && grp != last) {
-        ok = __all_sync(0xffffffffu, mbar_wait(s_full + 2 * last + (((end - 1) >> 1) & 1), ((end - 1) >> 2) & 1, abort));
+        float lane_m = m_use[0], lane_l = l_run[0];  // of the lane's row
+        if (SPLIT) {
+          float m2[2], l2[2];
+#pragma unroll
+          for (int i = 0; i < NQ; i++) {
+            float l = l_run[i];
+            l += __shfl_xor_sync(0xffffffffu, l, 1);
+            l += __shfl_xor_sync(0xffffffffu, l, 2);
+            l2[i] = __shfl_sync(0xffffffffu, l, 4 * (lane & 7));
+            m2[i] = __shfl_sync(0xffffffffu, m_use[i], 4 * (lane & 7));
+          }
+          lane_m = lane & 8 ? m2[1] : m2[0];
+          lane_l = lane & 8 ? l2[1] : l2[0];
+        }
         if (!ok) break;
+        // the segment's unnormalised O, maximum (log2 units) and sum
+        if (FULL) {
+          if (!(ok = flush(s - 2, 1.f))) break;
+#pragma unroll
+          for (int c = 0; c < (FULL ? D / 16 : 0); c++) {
+            uint32_t w[16];
+#pragma unroll
+            for (int x = 0; x < 16; x++) w[x] = __float_as_uint(acc[FULL ? 16 * c + x : 0]);
+            tmem_st16(obuf + c * 16, w);
+          }
+          tmem_wait_st();
+        }
+        ok = __all_sync(0xffffffffu, mbar_wait(o_done + 2 * grp + (((s - 2) >> 1) & 1), ((s - 2) >> 2) & 1, abort));
+        if (!ok) break;
+        tc_fence_after();
+        int lr = r;
+        asm volatile("" : "+r"(lr));  // addresses of this part are not kept in registers over the steps
+        // the slot's queries are no longer needed
+        float4* scratch = reinterpret_cast<float4*>(smem + 2 * slot * TB) + lr * (D / 4);
+        const auto chunk = [&](int q) { return q ^ (lr & 7); };
+        if (joint && grp != last) {
+          ok = __all_sync(0xffffffffu, mbar_wait(s_full + 2 * last + (((end - 1) >> 1) & 1), ((end - 1) >> 2) & 1, abort));
+          if (!ok) break;
+#pragma unroll 1
+          for (int c = 0; c < D / 16; c++) {
+            uint32_t w[16];
+            tmem_ld16(obuf + c * 16, w);
+            tmem_wait_ld();
+#pragma unroll
+            for (int q = 0; q < 4; q++)
+              scratch[chunk(c * 4 + q)] = make_float4(__uint_as_float(w[4 * q]), __uint_as_float(w[4 * q + 1]),
+                                                      __uint_as_float(w[4 * q + 2]), __uint_as_float(w[4 * q + 3]));
+          }
+          ml_other[slot * kTile + r] = make_float2(lane_m, lane_l);
+          tc_fence_before();
+          warp_arrive(part_full + 2 * last + (turn & 1));
+          continue;
+        }
+        const bool whole = sw.n0 == 0 && sw.n1 == sw.nt;
+        const size_t part = (size_t)(2 * blk + (sw.n0 > 0 ? 0 : 1)) * a.rows;
+        const int g = sw.g / a.pairs;
+        float M = lane_m, L = lane_l, mine_f = 1.f, other_f = 0.f;
+        if (joint) {
+          ok = __all_sync(0xffffffffu, mbar_wait(part_full + 2 * grp + (turn & 1), (turn >> 1) & 1, abort));
+          if (!ok) break;
+          const float2 z = ml_other[slot * kTile + r];
+          M = L == 0.f ? z.x : (z.y == 0.f ? M : fmaxf(M, z.x));
+          mine_f = L == 0.f ? 0.f : ex2(lane_m - M);
+          other_f = z.y == 0.f ? 0.f : ex2(z.x - M);
+          L = fmaf(L, mine_f, z.y * other_f);
+        }
 #pragma unroll 1
         for (int c = 0; c < D / 16; c++) {
           uint32_t w[16];
+          float v[16];
           tmem_ld16(obuf + c * 16, w);
           tmem_wait_ld();
 #pragma unroll
-          for (int q = 0; q < 4; q++)
-            scratch[chunk(c * 4 + q)] = make_float4(__uint_as_float(w[4 * q]), __uint_as_float(w[4 * q + 1]),
-                                                    __uint_as_float(w[4 * q + 2]), __uint_as_float(w[4 * q + 3]));
+          for (int q = 0; q < 4; q++) {
+            float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (joint) y = scratch[chunk(c * 4 + q)];
+            v[4 * q] = fmaf(__uint_as_float(w[4 * q]), mine_f, y.x * other_f);
+            v[4 * q + 1] = fmaf(__uint_as_float(w[4 * q + 1]), mine_f, y.y * other_f);
+            v[4 * q + 2] = fmaf(__uint_as_float(w[4 * q + 2]), mine_f, y.z * other_f);
+            v[4 * q + 3] = fmaf(__uint_as_float(w[4 * q + 3]), mine_f, y.w * other_f);
+          }
+          if (SPLIT) {
+#pragma unroll
+            for (int q = 0; q < 4; q++)
+              scratch[chunk(c * 4 + q)] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+          } else if (row < a.R) {
+            if (whole) {
+              const int t = (int)fdiv((uint32_t)row, a.div_g), h = g * a.G + (row - t * a.G);
+              put_columns(a, (((size_t)sw.b * a.Tq + t) * a.Hq + h) * D + c * 16, v, 1.f / L, live);
+            } else {
+              float4* to = reinterpret_cast<float4*>(a.part_o + (part + row - pr * 2 * kTile) * D) + c * 4;
+#pragma unroll
+              for (int q = 0; q < 4; q++)
+                to[q] = live ? make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]) : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+          }
         }
-        ml_other[slot * kTile + r] = make_float2(lane_m, lane_l);
         tc_fence_before();
-        warp_arrive(part_full + 2 * last + (turn & 1));
-        continue;
-      }
-      const bool whole = sw.n0 == 0 && sw.n1 == sw.nt;
-      const size_t part = (size_t)(2 * blk + (sw.n0 > 0 ? 0 : 1)) * a.rows;
-      const int g = sw.g / a.pairs;
-      float M = lane_m, L = lane_l, mine_f = 1.f, other_f = 0.f;
-      if (joint) {
-        ok = __all_sync(0xffffffffu, mbar_wait(part_full + 2 * grp + (turn & 1), (turn >> 1) & 1, abort));
-        if (!ok) break;
-        const float2 z = ml_other[slot * kTile + r];
-        M = L == 0.f ? z.x : (z.y == 0.f ? M : fmaxf(M, z.x));
-        mine_f = L == 0.f ? 0.f : ex2(lane_m - M);
-        other_f = z.y == 0.f ? 0.f : ex2(z.x - M);
-        L = fmaf(L, mine_f, z.y * other_f);
-      }
-#pragma unroll 1
-      for (int c = 0; c < D / 16; c++) {
-        uint32_t w[16];
-        float v[16];
-        tmem_ld16(obuf + c * 16, w);
-        tmem_wait_ld();
-#pragma unroll
-        for (int q = 0; q < 4; q++) {
-          float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (joint) y = scratch[chunk(c * 4 + q)];
-          v[4 * q] = fmaf(__uint_as_float(w[4 * q]), mine_f, y.x * other_f);
-          v[4 * q + 1] = fmaf(__uint_as_float(w[4 * q + 1]), mine_f, y.y * other_f);
-          v[4 * q + 2] = fmaf(__uint_as_float(w[4 * q + 2]), mine_f, y.z * other_f);
-          v[4 * q + 3] = fmaf(__uint_as_float(w[4 * q + 3]), mine_f, y.w * other_f);
-        }
         if (SPLIT) {
-#pragma unroll
-          for (int q = 0; q < 4; q++)
-            scratch[chunk(c * 4 + q)] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+          // a row's two lanes: a thread takes four of its columns
+          ml_own[grp * kTile + r] = make_float2(M, L);
+          if (!(ok = group_sync())) break;
+          const float4* all = reinterpret_cast<const float4*>(smem + 2 * slot * TB);
+          for (int i = r; i < a.R * (D / 4); i += kTile) {
+            const int ro = i / (D / 4), q = i % (D / 4), t = (int)fdiv((uint32_t)ro, a.div_g), at = 32 * (ro / 16) + ro % 16;
+            const float2 z = ml_own[grp * kTile + at];
+            const float4 x0 = all[at * (D / 4) + (q ^ (at & 7))], x1 = all[(at + 16) * (D / 4) + (q ^ (at & 7))];
+            RowSum x;
+            x.M = z.x;
+            x.S = z.y;
+            x.v = make_float4(x0.x + x1.x, x0.y + x1.y, x0.z + x1.z, x0.w + x1.w);
+            if (t >= info[e & 3].nodes) x.S = 0.f, x.v = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (whole) {
+              write_row<D>(a, sw.b, g, ro, q, x.v, x.M, x.S);
+            } else {
+              reinterpret_cast<float4*>(a.part_o + (part + ro) * D)[q] = x.v;
+              if (q == 0) a.part_ml[part + ro] = make_float2(x.M, x.S);
+            }
+          }
         } else if (row < a.R) {
-          if (whole) {
+          if (!whole)
+            a.part_ml[part + row - pr * 2 * kTile] = make_float2(M, live ? L : 0.f);
+          else if (a.lse) {
             const int t = (int)fdiv((uint32_t)row, a.div_g), h = g * a.G + (row - t * a.G);
-            put_columns(a, (((size_t)sw.b * a.Tq + t) * a.Hq + h) * D + c * 16, v, 1.f / L, live);
-          } else {
-            float4* to = reinterpret_cast<float4*>(a.part_o + (part + row - pr * 2 * kTile) * D) + c * 4;
-#pragma unroll
-            for (int q = 0; q < 4; q++) to[q] = live ? make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]) : make_float4(0.f, 0.f, 0.f, 0.f);
+            a.lse[((size_t)sw.b * a.Hq + h) * a.Tq + t] = live ? (M + log2f(L)) * kPagedLn2 : -INFINITY;
           }
         }
-      }
-      tc_fence_before();
-      if (SPLIT) {
-        // a row's two lanes: a thread takes four of its columns
-        ml_own[grp * kTile + r] = make_float2(M, L);
-        if (!(ok = group_sync())) break;
-        const float4* all = reinterpret_cast<const float4*>(smem + 2 * slot * TB);
-        for (int i = r; i < a.R * (D / 4); i += kTile) {
-          const int ro = i / (D / 4), q = i % (D / 4), t = (int)fdiv((uint32_t)ro, a.div_g), at = 32 * (ro / 16) + ro % 16;
-          const float2 z = ml_own[grp * kTile + at];
-          const float4 x0 = all[at * (D / 4) + (q ^ (at & 7))], x1 = all[(at + 16) * (D / 4) + (q ^ (at & 7))];
-          RowSum x;
-          x.M = z.x;
-          x.S = z.y;
-          x.v = make_float4(x0.x + x1.x, x0.y + x1.y, x0.z + x1.z, x0.w + x1.w);
-          if (t >= info[slot].nodes) x.S = 0.f, x.v = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (whole) {
-            write_row<D>(a, sw.b, g, ro, q, x.v, x.M, x.S);
-          } else {
-            reinterpret_cast<float4*>(a.part_o + (part + ro) * D)[q] = x.v;
-            if (q == 0) a.part_ml[part + ro] = make_float2(x.M, x.S);
-          }
+        if (qon && RT == 1) {
+          pack1 = grp == last ? 1 : 0;
+        } else if (qon) {
+          // a row tile is free once its own steps are done; with one in the pair the group of the last step has both
+          const int next = units(qs);
+          times = next == 2 ? 1 : 2;
+          pack0 = nu == 2 ? u : 0;
+          pack1 = nu == 2 ? min(u + 1, next) : (grp == last ? next : 0);
         }
-      } else if (row < a.R) {
-        if (!whole)
-          a.part_ml[part + row - pr * 2 * kTile] = make_float2(M, live ? L : 0.f);
-        else if (a.lse) {
-          const int t = (int)fdiv((uint32_t)row, a.div_g), h = g * a.G + (row - t * a.G);
-          a.lse[((size_t)sw.b * a.Hq + h) * a.Tq + t] = live ? (M + log2f(L)) * kPagedLn2 : -INFINITY;
-        }
+        if ((SPLIT || joint) && pack0 < pack1 && !(ok = group_sync())) break;  // every warp is done with the slot
       }
-      if (grp == last) {
-        if (RT == 1 || nu == 1) fence_proxy_async_smem();  // the slot's next queries come by copies
-        warp_arrive(q_empty + slot);
-      }
+      for (int u = pack0; u < pack1; u++) pack(qs, e + kAhead, u, times);
     }
     if (!ok) {
       *abort = 1;
@@ -959,18 +984,15 @@ cudaError_t launch_tree_t(const PagedTreeArgs& a, int grid, cudaStream_t s) {
   }
   const int bytes = tree_head(a.B) + TreeCfg<D>::kBytes + 1024;
   if (bytes > kSmemMax) return cudaErrorInvalidValue;
-  constexpr int rows = SPLIT ? kTile / 2 : kTile;
-  const long long chunks = (long long)a.Hkv * a.tiles * rows * (D / 8);
-  k_tree_prep<D><<<dim3((unsigned)((chunks + 127) / 128), (unsigned)a.B), 128, 0, s>>>(a, rows);
-  cudaError_t e = cudaGetLastError();
+  k_tree_sweep<D, RT, SPLIT, FULL><<<grid, kTreeThreads, (size_t)bytes, s>>>(a);
+  const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  if ((e = launch_pdl(k_tree_sweep<D, RT, SPLIT, FULL>, dim3((unsigned)grid), kTreeThreads, (size_t)bytes, s, a)) != cudaSuccess) return e;
   return launch_pdl(k_tree_join<D>, dim3((unsigned)grid, kJoinSlices), kJoinThreads, 0, s, a);
 }
 template <int D, bool FULL>
 cudaError_t launch_tree(const PagedTreeArgs& a, int grid, cudaStream_t s) {
   if (a.R > kTile) return launch_tree_t<D, 2, false, FULL>(a, grid, s);
-  return tree_rows(a.R) == kTile ? launch_tree_t<D, 1, false, FULL>(a, grid, s) : launch_tree_t<D, 1, true, FULL>(a, grid, s);
+  return a.R > kTile / 2 ? launch_tree_t<D, 1, false, FULL>(a, grid, s) : launch_tree_t<D, 1, true, FULL>(a, grid, s);
 }
 
 }  // namespace
