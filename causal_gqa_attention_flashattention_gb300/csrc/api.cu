@@ -1673,9 +1673,9 @@ int ne_attn_paged_plan(int* page_table, int* free_pages, const int* held, const 
                        int* cu_new, int* slots, int* positions, int N, int B, int Tq, int page_size, int num_pages,
                        int max_pages, long long parent_stride, void* stream) {
   if (!page_table || !free_pages || !held || !free_span || !kv_len || !new_len || !held_out || !free_span_out ||
-      !kv_len_out || !cu_new || !slots || !positions)
+      !kv_len_out || !cu_new || (N > 0 && (!slots || !positions)))
     return NE_ERR_ARG;
-  if (B < 1 || N < 1 || max_pages < 1 || kv_len_out == kv_len) return NE_ERR_ARG;
+  if (B < 1 || N < 0 || max_pages < 1 || kv_len_out == kv_len) return NE_ERR_ARG;
   int st = check_slots(page_size, num_pages);
   if (st != NE_OK) return st;
   if (B > kPagedMaxBatch || (long long)max_pages * page_size > kPagedMaxPositions || N > (1 << 30))

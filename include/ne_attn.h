@@ -446,7 +446,8 @@ int ne_attn_decode_paged(const void* q, const void* q_w, const void* k_pages, co
  * sequence) kv_len[b] + depth(t) (0 at or past cu_new[B]).
  * A sequence with a negative or too large length or count (more than max_pages * page_size positions, more than
  * N rows up to its last, more than Tq tokens of a tree) is refused and recorded as NE_ERR_PAGE, and so are all if
- * free_span is not a part of the ring.  B <= 2048, num_pages * page_size < 2^31.  One block, for more than 4096 rows a second launch.
+ * free_span is not a part of the ring.  With N = 0 (slots and positions may then be NULL) a step only takes pages
+ * back.  B <= 2048, num_pages * page_size < 2^31.  One block, for more than 4096 rows a second launch.
  */
 int ne_attn_paged_plan(int* page_table, int* free_pages, const int* held, const int* free_span, const int* kv_len,
                        const int* new_len, const int* parents, int* held_out, int* free_span_out, int* kv_len_out,

@@ -40,7 +40,8 @@ def test_plan(libne, mem):
     for name in "table ring held span len new parents held_o span_o len_o cu slots pos".split():
         assert f(**{name: p + 2}) == -2
     assert f(len_o=p) == -1                       # the old lengths are read until the end
-    assert f(N=0) == -1 and f(B=0) == -1 and f(P=0) == -1 and f(width=0) == -1
+    assert f(N=-1) == -1 and f(B=0) == -1 and f(P=0) == -1 and f(width=0) == -1
+    assert f(N=0, slots=None, pos=None, page=8) == -3
     assert f(page=8) == -3 and f(page=48) == -3 and f(page=512) == -3
     assert f(B=2049) == -3 and f(width=(1 << 16) + 1) == -3 and f(P=1 << 27) == -3 and f(N=(1 << 30) + 1) == -3
     assert f(Tq=0) == -1 and f(Tq=65, pstride=65) == -3 and f(pstride=3) == -1 and f(pstride=-4) == -1
