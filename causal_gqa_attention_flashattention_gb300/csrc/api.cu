@@ -1797,6 +1797,11 @@ int ne_attn_decode_tree(const void* q, const void* q_w, const void* k_pages, con
   if (workspace && (workspace_bytes < ne_attn_decode_tree_workspace_size(B, Tq, Hq, Hkv, D) ||
                     (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0))
     return NE_ERR_WORKSPACE;
+  // a block may pack its last queries when others have written their rows of o
+  const uintptr_t q0 = reinterpret_cast<uintptr_t>(q), o0 = reinterpret_cast<uintptr_t>(o);
+  const uintptr_t rows = (uintptr_t)B * Tq, row = (uintptr_t)Hq * D;
+  if (q0 < o0 + rows * row * ((flags & kFlagOFp32) ? 4 : 2) && o0 < q0 + ((rows - 1) * (uintptr_t)q_stride + row) * 2)
+    return NE_ERR_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   std::lock_guard<std::mutex> lock(g_mu);
   int dev, nsm = 0;

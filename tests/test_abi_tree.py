@@ -88,6 +88,18 @@ def test_decode_tree(libne, mem):
     assert f(bytes=n - 1) == -5 and f(ws=p + 64) == -5
 
 
+@pytest.mark.parametrize("fp32", [0, 1])
+def test_tree_outputs_on_the_queries(libne, mem, fp32):
+    """q has 10 rows of 128 values 160 apart, 3136 bytes; o 10 of 128, 2560 bytes or 5120: any common byte is refused."""
+    p = mem[1]
+    good = dict(q=p + 8192, qw=p, kp=p, vp=p, table=p, len=p, parents=p, nodes=p, o=p, lse=p, B=2, Tq=5, Hq=4, Hkv=2, D=32, page=16,
+                P=4, width=3, stride=1024, qs=160, pstride=5, eps=1e-6, base=1e4, flags=fp32, ws=p, bytes=1 << 40, stream=None)
+    f = lambda **c: call(libne.ne_attn_decode_tree, TREE, good, **c)
+    q, n = p + 8192, 5120 if fp32 else 2560
+    for o in (q, q + 16, q + 3136 - 16, q - 16, q - n + 16):
+        assert f(o=o) == -1
+
+
 def test_keep(libne, mem):
     p = mem[1]
     good = dict(kp=p, vp=p, table=p, len=p, nodes=p, path=p, count=p, out=p + 64, B=2, tokens=0, width=4, Hkv=2, D=32,

@@ -84,6 +84,22 @@ def test_no_page_of_its_own(nb):
     assert torch.equal(o[0], o[1]) and torch.equal(lse[0], lse[1])
 
 
+def test_outputs_on_the_queries(nb):
+    """Queries are read while rows of others are written: o may not lie on them."""
+    s = setup([40, 3], [4, 4], 4, 4, 2, 64, 16, seed=32)
+    args = (s["kp"], s["vp"], s["table"], s["lens"], s["parents"])
+    want = nb.attn_decode_tree(s["q"], *args, rope_base=BASE)[0]
+    with pytest.raises(nb.NeAttnError) as e:
+        nb.attn_decode_tree(s["q"], *args, rope_base=BASE, o=s["q"])
+    assert e.value.status == -1
+    room = torch.empty(2 * s["q"].numel(), dtype=torch.bfloat16, device="cuda")
+    q, o = room[:s["q"].numel()].view_as(s["q"]), room[s["q"].numel():].view_as(s["q"])
+    q.copy_(s["q"])
+    assert torch.equal(nb.attn_decode_tree(q, *args, rope_base=BASE, o=o)[0], want)  # side by side is fine
+    with pytest.raises(nb.NeAttnError):
+        nb.attn_decode_tree(q, *args, rope_base=BASE, o=room[8:8 + q.numel()].view_as(q))
+
+
 def test_graphs_share_a_workspace(nb):
     """Two captured calls of different shapes on one workspace, replayed in turn with new lengths, trees and queries."""
     a = setup([3000, 10], [16, 9], 16, 12, 4, 64, 64, seed=41)
