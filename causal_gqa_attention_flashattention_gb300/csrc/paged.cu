@@ -23,7 +23,8 @@ namespace {
 // A thread takes one 16-byte chunk of a key row and of the value row; the D / 8
 // threads of a row are neighbouring lanes (the norm adds up squares by shuffles).  Bound by the
 // bytes: 23 prompts with 17,000 rows of four heads (34.9 MB) take 9.3 us, a step of 64 tokens 3.1 us.
-// With SLOTS every row is given its place in the pool and its rotary position (negative slot: no place).
+// With SLOTS every row is given its place in the pool and its rotary position (negative slot: no place): 256 rows of
+// four heads 2.1 us, 16381 (33.3 MB) 8.6 us.
 template <int D, bool SLOTS>
 __global__ void __launch_bounds__(128) k_kv_append_paged(const PagedAppendArgs a) {
   constexpr int kCPR = D / 8;
