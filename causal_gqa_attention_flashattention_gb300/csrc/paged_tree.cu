@@ -22,19 +22,24 @@
 // contexts around 8192: 30.6 and 32.2 us; with a lane for each row 36.4 and 38.2.)
 //
 // The softmax warps pack the queries (normalised, rotated, two parts) and work the trees out themselves: those of a
-// block's first segments while its first keys are on their way, those of a later one when its slot is free. (16 trees of
-// 16: 32.2 us, with a kernel in front of the sweep 34.5, with four more warps for it 36 to 38, as the softmax then has
-// 192 registers. 64 trees of 32 with 128 rows pay for it, 58.0 -> 61.5.)
+// block's first segments while its first keys are on their way, those of a later one when its slot is free, by the group
+// that does not write the rows of the segment before out; that one reads the other's O where it is, in TMEM. (16 trees of
+// 16: 32.5 us, with a kernel in front of the sweep 34.5, with four more warps for it 36 to 38. 64 trees of 32 with 128
+// rows: 54; with one group doing both 61.5, with the kernel 58.0.)
+//
+// The warps wait for instructions as often as for scores, so code that is not part of a step is kept small (its loops
+// rolled, its waits short), and registers are kept for the steps: four spilled words or a part of a segment's end unrolled
+// took 2 to 4 us of a call.
 //
 // A segment that is not the whole of its (sequence, head) leaves its parts to k_tree_join; a join inside the sweep, by
 // the block that is last to finish, kept the others waiting for memory fences (34.6 -> 39.8 us) and was taken out.
 //
 // What bounds it (device times; 4 key/value heads of 64): up to 64 rows and a long context the bytes of K and V, 0.74 us
 // for a tile of every block (a steady 6.8 TB/s); the call adds the start (lengths, tables, first tiles: 4 us), the last
-// tiles' steps (3 us) and the join (2 to 6 us). 16 trees of 16 on contexts around 8192, pages of 64: 32.2 us, 19.1 of them
+// tiles' steps (3 us) and the join (2 to 6 us). 16 trees of 16 on contexts around 8192, pages of 64: 32.5 us, 19.1 of them
 // the bytes; with pages of 16 39 us (eight copies a tile, each of 2 KB). With 128 rows a step takes the tensor cores
-// 2048 clocks for two parts of both factors and the softmax as long: 64 trees of 32 on 700 to 4096 positions, 61.5 us.
-// With 256 rows and an fp32 o (three parts), 64 tokens on 131001 positions, 113 us.
+// 1536 clocks for two parts of both factors and the softmax as long: 64 trees of 32 on 700 to 4096 positions, 54 us.
+// With 256 rows and an fp32 o (three parts), 64 tokens on 131001 positions, 112 us.
 #include "paged_sweep.cuh"
 
 namespace ne {
@@ -59,10 +64,22 @@ __device__ __forceinline__ TreeShape tree_shape(const PagedTreeArgs& a, int b, b
   return x;
 }
 
+// mbar_wait in fewer instructions: the sweep's warps wait for instructions as it is (16 trees of 16 on contexts around
+// 8192 33.6 -> 32.6 us). At most 2^17 tries of at most 20 us.
+__device__ __forceinline__ bool tree_wait(uint64_t* bar, uint32_t parity, const volatile int* abort) {
+  if (mbar_try_wait(bar, parity)) return true;
+#pragma unroll 1
+  for (int i = 0; i < 1 << 17; i++) {
+    if (mbar_try_wait_sleep(bar, parity, 20000u)) return true;
+    if (*abort) return false;
+  }
+  return false;
+}
+
 constexpr int kTreeThreads = 384;
 // A segment's cost beside its tiles, in tiles; a (sequence, head) of at most so many tiles is never cut; a
 // boundary moves by so many to an end of a longer one.
-// Over 17 batches: a segment's cost of 1 takes up to 6 % more, one of 4 up to 4 % more (but 64 trees of 32 7 % less);
+// Over 17 batches: a segment's cost of 1 takes up to 6 % more, one of 3 up to 4 % more or less, one of 4 up to 4 % more;
 // whole up to 8 and a boundary moved by 3 up to 3 % more; no moves 4 % more for 128 short sequences, and others 0 to 4 % less.
 constexpr int kTreeOver = 2, kTreeWhole = 4, kTreeSlack = 2;
 
@@ -84,10 +101,10 @@ struct TreeCfg {
   // the third parts go to 384 + 64 g, with SPLIT in the place of S.
   static constexpr uint32_t kColO = 0, kColS = 128, kColP = 384;
 };
-constexpr int kTreeVars = 480, kTreePlan = 488, kTreeSums = 544, kTreeInfo = 608, kTreeMl = 2720;
-constexpr int kTreeCum = kTreeMl + 4 * kTile * 8;
-static_assert(kTreeInfo + 4 * sizeof(TreeInfo) <= kTreeMl && kTreePlan + sizeof(SweepPlan) <= kTreeSums, "head");
-static_assert((2 + 2 * TreeCfg<32>::kKStages + 2 * TreeCfg<32>::kVStages + 4 + 8 + 3 + 4 + 4 + 2 + 3) * 8 <= kTreeVars,
+constexpr int kTreeVars = 480, kTreePlan = 488, kTreeSums = 544, kTreeInfo = 608, kTrees = 5, kTreeMl = 3248;
+constexpr int kTreeWalk = kTreeMl + 4 * kTile * 8, kTreeCum = kTreeWalk + 8 * 2 * 6 * 4;
+static_assert(kTreeInfo + kTrees * sizeof(TreeInfo) <= kTreeMl && kTreePlan + sizeof(SweepPlan) <= kTreeSums, "head");
+static_assert((2 + 2 * TreeCfg<32>::kKStages + 2 * TreeCfg<32>::kVStages + 4 + 8 + 3 + 4 + 8 + 2 + 3) * 8 <= kTreeVars,
               "barriers");
 __host__ __device__ constexpr int tree_head(int B) { return (kTreeCum + (B + 1) * 4 + B + 1023) / 1024 * 1024; }
 
@@ -176,17 +193,17 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
   // [3] per buffer of S and P its weights are read (FULL: [group]); SPLIT, not FULL: [group] the scores are in registers
   uint64_t* pv_done = p_ready + 8;
   uint64_t* o_done = pv_done + 3;          // [group][2] the group's steps in turn: O has the step
-  uint64_t* part_full = o_done + 4;        // [group][2] the other group's part of a segment that this one finishes
-  uint64_t* gsync = part_full + 4;         // [group]
-  uint64_t* drain = gsync + 2;             // [3] per issuing thread
+  uint64_t* part_full = o_done + 4;        // [group][4] the other group is done with a segment that this one finishes
+  uint64_t* o_read = part_full + 8;        // [group] the group's O of such a segment has been read by the other
+  uint64_t* drain = o_read + 2;             // [3] per issuing thread
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(head + kTreeVars);
   volatile int* abort = reinterpret_cast<volatile int*>(head + kTreeVars) + 1;
   volatile SweepPlan* splan = reinterpret_cast<volatile SweepPlan*>(head + kTreePlan);
   int* wsum = reinterpret_cast<int*>(head + kTreeSums);
-  // [4] segments in turn: with RT == 2 a group can be at its first step of one while the other packs the next but one
+  // [kTrees] segments in turn. Scores wait for the weights three steps before, so while a group packs segment e + 2 (the
+  // last scores of e are there) the other may still read the tree of e - 2, e - 1 or e.
   TreeInfo* info = reinterpret_cast<TreeInfo*>(head + kTreeInfo);
-  float2* ml_other = reinterpret_cast<float2*>(head + kTreeMl);    // [2][128] per slot
-  float2* ml_own = ml_other + 2 * kTile;                           // [2][128] per group
+  float2* ml_other = reinterpret_cast<float2*>(head + kTreeMl);    // [4][128] segments in turn
   int* cum = reinterpret_cast<int*>(head + kTreeCum);
   uint8_t* pad = reinterpret_cast<uint8_t*>(cum + a.B + 1);  // positions that a sequence's last tile lacks
   uint8_t* smem = head + tree_head(a.B);
@@ -195,7 +212,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
     *abort = 0;
     for (int k = 0; k < 2; k++) {
       mbar_init(q_full + k, RT * 4);  // the warps that pack a row tile
-      mbar_init(gsync + k, 4);
+      mbar_init(o_read + k, 4);
     }
     for (int k = 0; k < SK; k++) {
       mbar_init(k_full + k, 1);
@@ -211,6 +228,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
       mbar_init(p_ready + 2 * k + 1, 4);
       mbar_init(o_done + k, 1);
       mbar_init(part_full + k, 4);
+      mbar_init(part_full + 4 + k, 4);
     }
     for (int k = 0; k < 3; k++) {
       mbar_init(pv_done + k, SPLIT && !FULL ? 4 : 1);
@@ -240,13 +258,15 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
   const volatile int never = 0;
   SegWalk<kTreeOver> sw;
   sw.init(tl, splan);
+  const auto head_of = [&](int g) { return RT == 1 ? g : g / a.pairs; };  // (up to 128 rows are one pair)
+  const auto pair_of = [&](int g) { return RT == 1 ? 0 : g % a.pairs; };
   const auto units = [&](const SegWalk<kTreeOver>& x) {  // row tiles of the segment's pair
-    return RT == 1 ? 1 : (2 * (x.g % a.pairs) * kTile + kTile < a.R ? 2 : 1);
+    return RT == 1 ? 1 : (2 * (pair_of(x.g)) * kTile + kTile < a.R ? 2 : 1);
   };
   const auto slot_of = [](int e) { return RT == 1 ? e & 1 : 0; };
   const auto use_of = [](int e) { return RT == 1 ? e >> 1 : e; };
-  // registers: 384 x 168 at launch; 128 x 104 + 256 x 200
-  if (warp < 4) regs_dec<104>();
+  // registers: 384 x 168 at launch; 128 x 120 + 256 x 192, with O in registers 128 x 72 + 256 x 216
+  if (warp < 4) regs_dec<FULL ? 72 : 120>();
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
@@ -293,7 +313,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
     bool ok = true;
     int k = 0;  // tiles so far
     while (ok && sw.next()) {
-      const int kvh = sw.g / a.pairs;
+      const int kvh = head_of(sw.g);
       if (sw.n1 < sw.nt) {  // a cut one that begins here, or goes through the whole stretch
         const int s0 = cum[sw.b] * tl.Hkv + sw.g * (sw.nt + tl.over);
         cut = make_int4(sw.b, sw.g, sw.n0 == 0 ? blk : tl.first(plan, s0), tl.last(plan, s0, sw.nt));
@@ -310,7 +330,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
         const int off = (n * kTile) & ((1 << a.page_shift) - 1);
         const bool again = RT == 2 && a.pairs > 1;  // the other pairs read it too
         const auto load = [&](const CUtensorMap* map, uint8_t* to, uint64_t* full, uint64_t* empty, int use) {
-          if (use > 0) ok = __all_sync(0xffffffffu, mbar_wait(empty, (use - 1) & 1, abort));
+          if (use > 0) ok = __all_sync(0xffffffffu, tree_wait(empty, (use - 1) & 1, abort));
           if (!ok) return;
           if (lane == 0) mbar_arrive_expect_tx(full, TB);
           __syncwarp();
@@ -324,15 +344,15 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
         load(&a.map_pk, smem + C::kOffK + k % SK * TB, k_full + k % SK, k_empty + k % SK, k / SK);
         if (!ok) {
           // V of this tile is not on its way: below, only what is
-          for (int x = k - SK < 0 ? 0 : k - SK; lane == 0 && x < k; x++) mbar_wait(k_full + x % SK, (x / SK) & 1, &never);
-          for (int x = k - SV < 0 ? 0 : k - SV; lane == 0 && x < k; x++) mbar_wait(v_full + x % SV, (x / SV) & 1, &never);
+          for (int x = k - SK < 0 ? 0 : k - SK; lane == 0 && x < k; x++) tree_wait(k_full + x % SK, (x / SK) & 1, &never);
+          for (int x = k - SV < 0 ? 0 : k - SV; lane == 0 && x < k; x++) tree_wait(v_full + x % SV, (x / SV) & 1, &never);
           break;
         }
         load(&a.map_pv, smem + C::kOffV + k % SV * TB, v_full + k % SV, v_empty + k % SV, k / SV);
         if (!ok) {
           const int k0 = k - SK + 1 < 0 ? 0 : k - SK + 1;
-          for (int x = k0; lane == 0 && x <= k; x++) mbar_wait(k_full + x % SK, (x / SK) & 1, &never);
-          for (int x = k - SV < 0 ? 0 : k - SV; lane == 0 && x < k; x++) mbar_wait(v_full + x % SV, (x / SV) & 1, &never);
+          for (int x = k0; lane == 0 && x <= k; x++) tree_wait(k_full + x % SK, (x / SK) & 1, &never);
+          for (int x = k - SV < 0 ? 0 : k - SV; lane == 0 && x < k; x++) tree_wait(v_full + x % SV, (x / SV) & 1, &never);
           break;
         }
       }
@@ -344,8 +364,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
         atomicExch(a.status, kStatusTimeout);
       } else {
         // let every copy issued above land before the block can exit
-        for (int x = k - SK < 0 ? 0 : k - SK; x < k; x++) mbar_wait(k_full + x % SK, (x / SK) & 1, &never);
-        for (int x = k - SV < 0 ? 0 : k - SV; x < k; x++) mbar_wait(v_full + x % SV, (x / SV) & 1, &never);
+        for (int x = k - SK < 0 ? 0 : k - SK; x < k; x++) tree_wait(k_full + x % SK, (x / SK) & 1, &never);
+        for (int x = k - SV < 0 ? 0 : k - SV; x < k; x++) tree_wait(v_full + x % SV, (x / SV) & 1, &never);
       }
     }
   } else if (warp == 1) {
@@ -359,16 +379,16 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
       int n = 0, k = 0, e = 0;  // steps, tiles, segments
       while (ok && sw.next()) {
         const int nu = units(sw), slot = slot_of(e);
-        if (!(ok = mbar_wait(q_full + slot, use_of(e) & 1, abort))) break;
+        if (!(ok = tree_wait(q_full + slot, use_of(e) & 1, abort))) break;
 #pragma unroll 1
         for (int i = sw.n0; ok && i < sw.n1; i++, k++) {
           const int st = k % SK;
-          if (!(ok = mbar_wait(k_full + st, (k / SK) & 1, abort))) break;
+          if (!(ok = tree_wait(k_full + st, (k / SK) & 1, abort))) break;
 #pragma unroll 1
           for (int u = 0; u < nu; u++, n++) {
             // the buffer's weights have been read (SPLIT, not FULL: the group's scores)
             const int buf = SPLIT || FULL ? n & 1 : n % 3, use = SPLIT || FULL ? n >> 1 : n / 3;
-            if (use > 0 && !(ok = mbar_wait(pv_done + buf, (use - 1) & 1, abort))) break;
+            if (use > 0 && !(ok = tree_wait(pv_done + buf, (use - 1) & 1, abort))) break;
             tc_fence_after();
             const uint64_t dq = dQ0 + (uint64_t)((RT == 1 ? 2 * slot : 2 * u) * tstep), dk = dK0 + (uint64_t)(st * tstep);
             const uint32_t to = tmem + C::kColS + 128u * buf;
@@ -387,7 +407,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
         atomicExch(a.status, kStatusTimeout);
       }
       mma_commit(drain);
-      mbar_wait(drain, 0, &never);
+      tree_wait(drain, 0, &never);
     }
   } else if (warp < 4) {
     // ------------------------------------------------------------ O += P V issuer of a group
@@ -397,8 +417,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
       constexpr uint32_t kStepMN = (16 * C::kSpan) >> 4, tstep = (uint32_t)TB >> 4;
       const uint64_t dV0 = smem_desc(smem_u32(smem + C::kOffV), 16, C::kSBO, C::kSwz);
       const uint32_t o = tmem + C::kColO + 64u * grp;
-      bool ok = true;
-      int n = 0, k = 0;
+      bool ok = true, lent = false;  // the other group reads O of the last segment
+      int n = 0, k = 0, reads = 0;
       while (ok && sw.next()) {
         const int nu = units(sw), first = n, tiles = sw.n1 - sw.n0, end = first + tiles * nu;
 #pragma unroll 1
@@ -406,8 +426,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
           const int kt = k + (RT == 2 && nu == 2 ? (n - first) >> 1 : n - first), st = kt % SV, i = n >> 1;
           // the group has also read the O of its last segment before it arrives for this one
           uint64_t* ready = p_ready + 4 * grp + 2 * (i & 1);
-          if (!(ok = mbar_wait(ready, (i >> 1) & 1, abort))) break;
-          if (!(ok = mbar_wait(v_full + st, (kt / SV) & 1, abort))) break;
+          if (!(ok = tree_wait(ready, (i >> 1) & 1, abort))) break;
+          if (!(ok = tree_wait(v_full + st, (kt / SV) & 1, abort))) break;
+          if (lent) {
+            if (!(ok = tree_wait(o_read + grp, reads++ & 1, abort))) break;
+            lent = false;
+          }
           const uint64_t dv = dV0 + (uint64_t)(st * tstep), dv2 = dv + (uint64_t)(4 * kStepMN);
           const uint32_t sb = tmem + C::kColS + 128u * (FULL ? grp : n % 3), pb = tmem + C::kColP + 64u * grp;
           const uint32_t p = SPLIT ? pb : sb, third = SPLIT ? sb : pb;
@@ -416,7 +440,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
           mma_ts_chain<4, false>(o, p + kHalf, dv2, kStepMN, idPV, !FULL && n - first >= 2 ? 1u : 0u);
           if (!SPLIT) {
             mma_ts_chain<4, false>(o, p + kHalf + 32u, dv2, kStepMN, idPV, 1u);
-            if (!(ok = mbar_wait(ready + 1, (i >> 1) & 1, abort))) break;
+            if (!(ok = tree_wait(ready + 1, (i >> 1) & 1, abort))) break;
             tc_fence_after();
           }
           mma_ts_chain<4, false>(o, p, dv, kStepMN, idPV, 1u);
@@ -430,6 +454,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
           mma_commit(v_empty + st);
           if (RT == 2 && nu == 1) mbar_arrive(v_empty + st);
         }
+        lent = lent || (nu == 1 && tiles >= 2 && ((end - 1) & 1) != grp);
         n = end;
         k += tiles;
       }
@@ -438,11 +463,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
         atomicExch(a.status, kStatusTimeout);
       }
       mma_commit(drain + 1 + grp);
-      mbar_wait(drain + 1 + grp, 0, &never);
+      tree_wait(drain + 1 + grp, 0, &never);
     }
   } else {
     // ------------------------------------------------------------ softmax group
-    regs_inc<200>();
+    regs_inc<FULL ? 216 : 192>();
     const int grp = (warp - 4) >> 2, q4 = warp & 3;
     const int r = q4 * 32 + lane, rr = SPLIT ? q4 * 16 + (lane & 15) : r;  // lane of the tile and its row
     const uint32_t trow = tmem + ((uint32_t)(q4 * 32) << 16);
@@ -452,14 +477,14 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
     // This group packs row tile u of a segment, number e of the block, and signals it `times` times.
     const auto pack = [&](const SegWalk<kTreeOver>& x, int e, int u, int times) {
       constexpr int kCPR = D / 8, kItems = NR * kCPR / 128, kBatch = kItems < 4 ? kItems : 4;  // 16-byte chunks of a thread
-      const int pr = x.g % a.pairs, g = x.g / a.pairs, c = lane % kCPR, r0 = pr * 2 * kTile + u * kTile;
+      const int pr = pair_of(x.g), g = head_of(x.g), c = lane % kCPR, r0 = pr * 2 * kTile + u * kTile;
       uint8_t* to = smem + (RT == 1 ? 2 * slot_of(e) : 2 * u) * TB;
       const int total = x.nt * kTile - pad[x.b];
       int up[2];
 #pragma unroll
       for (int h = 0; h < 2; h++) up[h] = lane + 32 * h < a.Tq ? a.parents[x.b * a.parent_stride + lane + 32 * h] : -1;
       const int nodes = total > 0 ? (a.nodes ? a.nodes[x.b] : a.Tq) : 0;
-      TreeInfo& tree = info[e & 3];
+      TreeInfo& tree = info[(unsigned)e % kTrees];
       if (a.qw) wv = load_rope_chunk<D>(a.qw, c, a.rope_half != 0);
       unsigned long long mask[2];
       tree_masks(up, nodes, lane, q4 == 0 ? a.status : nullptr, mask);
@@ -496,30 +521,62 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
     };
     // Segments are packed two ahead where two have slots of their own (RT == 1), else one.
     constexpr int kAhead = RT == 1 ? 2 : 1;
-    SegWalk<kTreeOver> qs = sw;
+    // The walks to the segment that is worked off and to the one that is packed lie in shared memory (the warp's own): the
+    // steps between need the registers.
+    volatile int* walk = reinterpret_cast<volatile int*>(head + kTreeWalk) + (warp - 4) * 12;
+    const auto put = [&](const SegWalk<kTreeOver>& x, int i) {
+      __syncwarp();
+      if (lane == 0) {
+        walk[6 * i] = x.w;
+        walk[6 * i + 1] = x.b;
+        walk[6 * i + 2] = x.g;
+        walk[6 * i + 3] = x.n0;
+        walk[6 * i + 4] = x.n1;
+        walk[6 * i + 5] = x.nt;
+      }
+      __syncwarp();
+    };
+    const auto get = [&](int i) {
+      SegWalk<kTreeOver> x;
+      x.cum = cum;
+      x.Hkv = tl.Hkv;
+      x.end = splan->end;
+      x.w = walk[6 * i];
+      x.b = walk[6 * i + 1];
+      x.g = walk[6 * i + 2];
+      x.n0 = walk[6 * i + 3];
+      x.n1 = walk[6 * i + 4];
+      x.nt = walk[6 * i + 5];
+      return x;
+    };
+    put(sw, 0);
+    put(sw, 1);
     bool qon = true;
     bool ok = true;
-    int n = 0, kt = 0, syncs = 0;      // steps, stages, group barriers
+    int n = 0, kt = 0;                 // steps, stages
     int joined0 = 0, joined1 = 0;      // segments that each group finished with the other
-    const auto group_sync = [&]() {
-      warp_arrive(gsync + grp);
-      return __all_sync(0xffffffffu, mbar_wait(gsync + grp, syncs++ & 1, abort));
-    };
     for (int e = -kAhead; ok; e++) {
-      qon = qon && qs.next();  // segment e + kAhead, of which this group packs row tiles pack0 .. pack1 - 1
-      int pack0 = 0, pack1 = 0, times = 1;
+      int pack0 = 0, pack1 = 0, times = 1;  // this group packs row tiles pack0 .. pack1 - 1 of segment e + kAhead
+      if (qon) {
+        SegWalk<kTreeOver> qs = get(1);
+        qon = qs.next();
+        put(qs, 1);
+      }
       if (e < 0) {
         if (!qon) continue;
         if (RT == 1) {
           pack1 = grp == e + kAhead ? 1 : 0;
         } else {
+          const int next = units(get(1));
           pack0 = grp;
-          pack1 = min(grp + 1, units(qs));
-          times = units(qs) == 2 ? 1 : 2;
+          pack1 = min(grp + 1, next);
+          times = next == 2 ? 1 : 2;
         }
       } else {
+        SegWalk<kTreeOver> sw = get(0);
         if (!sw.next()) break;
-        const int nu = units(sw), slot = slot_of(e), first = n, end = first + (sw.n1 - sw.n0) * nu;
+        put(sw, 0);
+        const int n0 = sw.n0, nu = units(sw), first = n, end = first + (sw.n1 - sw.n0) * nu;
         const int mine = first + ((first ^ grp) & 1);           // this group's first step
         const bool joint = nu == 1 && end - first >= 2;         // both groups have a part of the same rows
         const int last = (end - 1) & 1;                         // the group of the last step
@@ -528,381 +585,350 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
         kt += sw.n1 - sw.n0;
         const int turn = last ? joined1 : joined0;
         if (joint) last ? joined1++ : joined0++;
-        if (mine >= end) continue;
-        const int pr = sw.g % a.pairs, u = nu == 2 ? (mine - first) & 1 : 0;
-        const int row = pr * 2 * kTile + u * kTile + rr;        // row of the (sequence, head)
-        int ctx = 0, total = 0;
-        bool live = false;
-        // a thread's row, or (SPLIT) its two rows lane / 4 and lane / 4 + 8 of the warp's 16: mask, maximum, sum
-        constexpr int NQ = SPLIT ? 2 : 1;
-        unsigned long long mask[NQ];
-        float r_run[NQ], l_run[NQ], m_use[NQ];
-        float acc[FULL ? D : 1];  // FULL: O of the lane's row so far
+        const int u = nu == 2 ? (mine - first) & 1 : 0;
+        if (mine < end) {
+          const auto token = [&](int x) { return x < a.R ? (int)fdiv((uint32_t)x, a.div_g) : kTreeMax; };
+          const TreeInfo& tree = info[(unsigned)e % kTrees];
+          const auto row_of = [&](int x) { return pair_of(get(0).g) * 2 * kTile + u * kTile + x; };  // row of the (sequence, head)
+          int ctx = 0;
+          bool live = false;
+          // a thread's row, or (SPLIT) its two rows lane / 4 and lane / 4 + 8 of the warp's 16: maximum, sum
+          constexpr int NQ = SPLIT ? 2 : 1;
+          float r_run[NQ], l_run[NQ];
+          float acc[FULL ? D : 1];  // FULL: O of the lane's row so far
 #pragma unroll
-        for (int x = 0; FULL && x < D; x++) acc[x] = 0.f;
-        // FULL: adds the O of step n to it, then scales both
-        const auto flush = [&](int n, float f) {
-          if (!__all_sync(0xffffffffu, mbar_wait(o_done + 2 * grp + ((n >> 1) & 1), (n >> 2) & 1, abort))) return false;
-          tc_fence_after();
+          for (int x = 0; FULL && x < D; x++) acc[x] = 0.f;
+          // FULL: adds the O of step n to it, then scales both
+          const auto flush = [&](int n, float f) {
+            if (!__all_sync(0xffffffffu, tree_wait(o_done + 2 * grp + ((n >> 1) & 1), (n >> 2) & 1, abort))) return false;
+            tc_fence_after();
 #pragma unroll
-          for (int c = 0; c < (FULL ? D / 16 : 0); c++) {
-            uint32_t w[16];
-            tmem_ld16(obuf + c * 16, w);
-            tmem_wait_ld();
+            for (int c = 0; c < (FULL ? D / 16 : 0); c++) {
+              uint32_t w[16];
+              tmem_ld16(obuf + c * 16, w);
+              tmem_wait_ld();
 #pragma unroll
-            for (int x = 0; x < 16; x++) {
-              float& y = acc[FULL ? 16 * c + x : 0];
-              y = (y + __uint_as_float(w[x])) * f;
-            }
-          }
-          return true;
-        };
-        int s = mine;
-        for (; s < end; s += 2) {
-          const int buf = SPLIT || FULL ? grp : s % 3, tile = sw.n0 + (nu == 2 ? (s - first) >> 1 : s - first);
-          const uint32_t sbuf = trow + C::kColS + 128u * buf, pown = trow + C::kColP + 64u * grp;
-          const uint32_t pbuf = SPLIT ? pown : sbuf, third = SPLIT ? sbuf : pown;
-          ok = __all_sync(0xffffffffu, mbar_wait(s_full + 2 * grp + ((s >> 1) & 1), (s >> 2) & 1, abort));
-          if (!ok) break;
-          tc_fence_after();
-          if (s == mine) {
-            const auto token = [&](int x) { return x < a.R ? (int)fdiv((uint32_t)x, a.div_g) : kTreeMax; };
-            ctx = info[e & 3].ctx;
-            total = ctx + info[e & 3].nodes;
-            live = token(row) < info[e & 3].nodes;
-#pragma unroll
-            for (int i = 0; i < NQ; i++) {
-              const int t = token(SPLIT ? q4 * 16 + lane / 4 + 8 * i : row);
-              mask[i] = t < info[e & 3].nodes ? info[e & 3].mask[t] : 0ull;
-            }
-          }
-          const bool edge = (tile + 1) * kTile > ctx;  // the tile ends in the tree or behind it
-          if (edge && total - tile * kTile < kTile) {
-            // what lies behind the last position may be anything: its weight is 0, but 0 times a NaN is not
-            const int kt = k0 + tile - sw.n0;
-            ok = __all_sync(0xffffffffu, mbar_wait(v_full + kt % SV, (kt / SV) & 1, abort));
-            if (!ok) break;
-            if (r >= total - tile * kTile) {
-              uint4* v = reinterpret_cast<uint4*>(smem + C::kOffV + kt % SV * TB + r * C::kSpan);
-#pragma unroll
-              for (int c = 0; c < D / 8; c++) v[c] = make_uint4(0u, 0u, 0u, 0u);
-              fence_proxy_async_smem();
-            }
-          }
-          // 64 scores of a thread at a time. With one row and 128 they are read once for the maximum and (but for the last 64)
-          // once more for the weights: with all in registers the loop does not fit the schedulers' instruction caches
-          // (warps then wait for instructions longer than they issue them).
-          uint32_t sc[64];
-          const auto load = [&](int h) {
-            uint32_t(&lo)[32] = *reinterpret_cast<uint32_t(*)[32]>(sc);
-            uint32_t(&hi)[32] = *reinterpret_cast<uint32_t(*)[32]>(sc + 32);
-            if (SPLIT) {
-              tmem_ld16x64(sbuf, lo);
-              tmem_ld16x64(sbuf + 64, hi);
-            } else {
-              tmem_ld32(sbuf + h * 64, lo);
-              tmem_ld32(sbuf + h * 64 + 32, hi);
-            }
-            tmem_wait_ld();
-            if (edge && SPLIT) {
-#pragma unroll
-              for (int c = 0; c < 4; c++) {
-                const int at = tile * kTile + c * 32 - ctx;
-                const int by = 2 * (lane & 3);
-                const uint32_t see[2] = {tree_word(mask[0], at) >> by, tree_word(mask[NQ - 1], at) >> by};
-#pragma unroll
-                for (int x = 0; x < 16; x++)  // columns 8 (x / 4) + 2 (lane % 4) + x % 2 of the 32, row x / 2 % 2
-                  if (!(see[x / 2 % 2] & (1u << (8 * (x / 4) + x % 2)))) sc[16 * c + x] = 0xff800000u;
-              }
-            } else if (edge) {
-#pragma unroll
-              for (int c = 0; c < 2; c++) {
-                const uint32_t see = tree_word(mask[0], tile * kTile + h * 64 + c * 32 - ctx);
-#pragma unroll
-                for (int x = 0; x < 32; x++)
-                  if (!(see & (1u << x))) sc[32 * c + x] = 0xff800000u;
+              for (int x = 0; x < 16; x++) {
+                float& y = acc[FULL ? 16 * c + x : 0];
+                y = (y + __uint_as_float(w[x])) * f;
               }
             }
+            return true;
           };
-          float mxr[NQ];
-          if (SPLIT) {
-            load(0);
-            if (!FULL) {
-              tc_fence_before();
-              warp_arrive(pv_done + grp);
-            }
-            float m2[2][2] = {{-INFINITY, -INFINITY}, {-INFINITY, -INFINITY}};
-#pragma unroll
-            for (int x = 0; x < 64; x += 2) {
-              float& y = m2[(x >> 1) & 1][(x >> 2) & 1];
-              y = fmax3(y, __uint_as_float(sc[x]), __uint_as_float(sc[x + 1]));
-            }
-#pragma unroll
-            for (int i = 0; i < NQ; i++) {
-              float m = fmaxf(m2[i][0], m2[i][1]);
-              m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-              mxr[i] = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-            }
-          } else {
-            float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll 1
-            for (int h = 0; h < 2; h++) {
-              load(h);
-#pragma unroll
-              for (int x = 0; x < 64; x += 2)
-                mx4[(x >> 1) & 3] = fmax3(mx4[(x >> 1) & 3], __uint_as_float(sc[x]), __uint_as_float(sc[x + 1]));
-            }
-            mxr[0] = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
-          }
-          float alpha[NQ];
-          if (s == mine) {
-#pragma unroll
-            for (int i = 0; i < NQ; i++) {
-              r_run[i] = mxr[i];
-              alpha[i] = 0.f;
-              l_run[i] = 0.f;
-            }
-          } else {
-            // O and the sum follow the maximum only when some row's grew by more than 2^8 (or came out of nothing)
-            bool grow = false;
-#pragma unroll
-            for (int i = 0; i < NQ; i++) {
-              alpha[i] = 1.f;
-              grow = grow || __fmul_rn(fmaxf(r_run[i], mxr[i]), sl2) > __fmul_rn(r_run[i], sl2) + 8.0f;
-            }
-            float lane_a = 1.f;  // of the lane's row
-            if (__any_sync(0xffffffffu, grow)) {
-#pragma unroll
-              for (int i = 0; i < NQ; i++) {
-                const float r_new = fmaxf(r_run[i], mxr[i]);
-                alpha[i] = r_run[i] == -INFINITY ? 0.f : ex2(__fmul_rn(r_run[i], sl2) - __fmul_rn(r_new, sl2));
-                r_run[i] = r_new;
-              }
-              lane_a = alpha[0];
-              if (SPLIT) {
-                const float x = __shfl_sync(0xffffffffu, alpha[0], 4 * (lane & 7));
-                const float y = __shfl_sync(0xffffffffu, alpha[NQ - 1], 4 * (lane & 7));
-                lane_a = lane & 8 ? y : x;
-              }
-              if (!FULL) {
-                ok = __all_sync(0xffffffffu, mbar_wait(o_done + 2 * grp + (((s - 2) >> 1) & 1), ((s - 2) >> 2) & 1, abort));
-                if (!ok) break;
-                tc_fence_after();
-#pragma unroll 1
-                for (int c = 0; c < D / 16; c++) {
-                  uint32_t w[16];
-                  tmem_ld16(obuf + c * 16, w);
-                  tmem_wait_ld();
-#pragma unroll
-                  for (int x = 0; x < 16; x++) w[x] = __float_as_uint(__uint_as_float(w[x]) * lane_a);
-                  tmem_st16(obuf + c * 16, w);
-                }
-              }
-            }
-            if (FULL && !(ok = flush(s - 2, lane_a))) break;
-          }
-          if (SPLIT ? s >= 2 : FULL && s >= 2 && s == mine) {  // the weights of the step before have been read
-            ok = __all_sync(0xffffffffu, mbar_wait(o_done + 2 * grp + (((s - 2) >> 1) & 1), ((s - 2) >> 2) & 1, abort));
+          int s = mine;
+          for (; s < end; s += 2) {
+            const int buf = SPLIT || FULL ? grp : s % 3, tile = n0 + (nu == 2 ? (s - first) >> 1 : s - first);
+            const uint32_t sbuf = trow + C::kColS + 128u * buf, pown = trow + C::kColP + 64u * grp;
+            const uint32_t pbuf = SPLIT ? pown : sbuf, third = SPLIT ? sbuf : pown;
+            ok = __all_sync(0xffffffffu, tree_wait(s_full + 2 * grp + ((s >> 1) & 1), (s >> 2) & 1, abort));
             if (!ok) break;
             tc_fence_after();
-          }
-          uint64_t sum[NQ][4 / NQ], negm[NQ];
+            if (s == mine) {
+              ctx = tree.ctx;
+              live = token(row_of(rr)) < tree.nodes;
+            }
+            const bool edge = (tile + 1) * kTile > ctx;  // the tile ends in the tree or behind it
+            unsigned long long mask[NQ];
+            if (edge) {
+              const int nodes = tree.nodes, row0 = row_of(0), past = ctx + nodes - tile * kTile;
 #pragma unroll
-          for (int i = 0; i < NQ; i++) {
-            m_use[i] = r_run[i] == -INFINITY ? 0.f : __fmul_rn(r_run[i], sl2);
-            negm[i] = f2(-m_use[i], -m_use[i]);
-#pragma unroll
-            for (int j = 0; j < 4 / NQ; j++) sum[i][j] = 0ull;
-          }
-          const uint64_t sl2x2 = f2(sl2, sl2), minus = f2(-1.f, -1.f);
-#pragma unroll 1
-          for (int h = 1; h >= (SPLIT ? 1 : 0); h--) {
-            if (h == 0) load(0);
-            uint32_t ph[32], pl[32], pt[32];
-#pragma unroll
-            for (int x = 0; x < 32; x++) {
-              constexpr int kSums = 4 / NQ;
-              const int i = SPLIT ? x & 1 : 0, j = (SPLIT ? x >> 1 : x) % kSums;
-              float x0, x1, l0, l1;
-              f2_split(f2_fma(f2(__uint_as_float(sc[2 * x]), __uint_as_float(sc[2 * x + 1])), sl2x2, negm[i]), x0, x1);
-              const uint64_t pp = f2(ex2(x0), ex2(x1));
-              f2_split(pp, x0, x1);
-              ph[x] = pack_bf16(x0, x1);
-              const uint64_t ll = f2_fma(f2(bf_lo(ph[x]), bf_hi(ph[x])), minus, pp);
-              f2_split(ll, l0, l1);
-              pl[x] = pack_bf16(l0, l1);
-              if (FULL) {
-                f2_split(f2_fma(f2(bf_lo(pl[x]), bf_hi(pl[x])), minus, ll), l0, l1);
-                pt[x] = pack_bf16(l0, l1);
+              for (int i = 0; i < NQ; i++) {
+                const int t = token(row0 + (SPLIT ? q4 * 16 + lane / 4 + 8 * i : r));
+                mask[i] = t < nodes ? tree.mask[t] : 0ull;
               }
-              sum[i][j] = f2_add(sum[i][j], pp);
-              if (!SPLIT && x % 8 == 7) {
-                tmem_st8(pbuf + 64 * h + x - 7, *reinterpret_cast<uint32_t(*)[8]>(ph + x - 7));
-                tmem_st8(pbuf + 64 * h + 32 + x - 7, *reinterpret_cast<uint32_t(*)[8]>(pl + x - 7));
-                if (FULL) tmem_st8(third + 32 * h + x - 7, *reinterpret_cast<uint32_t(*)[8]>(pt + x - 7));
-              }
-              if (SPLIT && x % 16 == 15) {
-                tmem_st16x32(pbuf + 2 * (x - 15), *reinterpret_cast<uint32_t(*)[16]>(ph + x - 15));
-                tmem_st16x32(pbuf + (16u << 16) + 2 * (x - 15), *reinterpret_cast<uint32_t(*)[16]>(pl + x - 15));
-                if (FULL) {  // beside the low parts
-                  const uint32_t none[16] = {0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
-                  tmem_st16x32(third + 2 * (x - 15), none);
-                  tmem_st16x32(third + (16u << 16) + 2 * (x - 15), *reinterpret_cast<uint32_t(*)[16]>(pt + x - 15));
+              if (past < kTile) {
+                // what lies behind the last position may be anything: its weight is 0, but 0 times a NaN is not
+                const int kt = k0 + tile - n0;
+                ok = __all_sync(0xffffffffu, tree_wait(v_full + kt % SV, (kt / SV) & 1, abort));
+                if (!ok) break;
+                if (r >= past) {
+                  uint4* v = reinterpret_cast<uint4*>(smem + C::kOffV + kt % SV * TB + r * C::kSpan);
+#pragma unroll
+                  for (int c = 0; c < D / 8; c++) v[c] = make_uint4(0u, 0u, 0u, 0u);
+                  fence_proxy_async_smem();
                 }
               }
             }
-            tmem_wait_st();
-            tc_fence_before();
-            warp_arrive(p_ready + 4 * grp + 2 * ((s >> 1) & 1) + (h == 0 ? 1 : 0));
-          }
+            // 64 scores of a thread at a time. With one row and 128 they are read once for the maximum and (but for the last 64)
+            // once more for the weights: with all in registers the loop does not fit the schedulers' instruction caches
+            // (warps then wait for instructions longer than they issue them).
+            uint32_t sc[64];
+            const auto load = [&](int h) {
+              uint32_t(&lo)[32] = *reinterpret_cast<uint32_t(*)[32]>(sc);
+              uint32_t(&hi)[32] = *reinterpret_cast<uint32_t(*)[32]>(sc + 32);
+              if (SPLIT) {
+                tmem_ld16x64(sbuf, lo);
+                tmem_ld16x64(sbuf + 64, hi);
+              } else {
+                tmem_ld32(sbuf + h * 64, lo);
+                tmem_ld32(sbuf + h * 64 + 32, hi);
+              }
+              tmem_wait_ld();
+              if (edge && SPLIT) {
 #pragma unroll
-          for (int i = 0; i < NQ; i++) {
-            uint64_t t = f2_add(sum[i][0], sum[i][1]);
-            if (NQ == 1) t = f2_add(t, f2_add(sum[i][4 / NQ - 2], sum[i][4 / NQ - 1]));
-            float x, y;
-            f2_split(t, x, y);
-            l_run[i] = fmaf(l_run[i], alpha[i], x + y);
-          }
-        }
-        float lane_m = m_use[0], lane_l = l_run[0];  // of the lane's row
-        if (SPLIT) {
-          float m2[2], l2[2];
+                for (int c = 0; c < 4; c++) {
+                  const int at = tile * kTile + c * 32 - ctx;
+                  const int by = 2 * (lane & 3);
+                  const uint32_t see[2] = {tree_word(mask[0], at) >> by, tree_word(mask[NQ - 1], at) >> by};
 #pragma unroll
-          for (int i = 0; i < NQ; i++) {
-            float l = l_run[i];
-            l += __shfl_xor_sync(0xffffffffu, l, 1);
-            l += __shfl_xor_sync(0xffffffffu, l, 2);
-            l2[i] = __shfl_sync(0xffffffffu, l, 4 * (lane & 7));
-            m2[i] = __shfl_sync(0xffffffffu, m_use[i], 4 * (lane & 7));
-          }
-          lane_m = lane & 8 ? m2[1] : m2[0];
-          lane_l = lane & 8 ? l2[1] : l2[0];
-        }
-        if (!ok) break;
-        // the segment's unnormalised O, maximum (log2 units) and sum
-        if (FULL) {
-          if (!(ok = flush(s - 2, 1.f))) break;
+                  for (int x = 0; x < 16; x++)  // columns 8 (x / 4) + 2 (lane % 4) + x % 2 of the 32, row x / 2 % 2
+                    if (!(see[x / 2 % 2] & (1u << (8 * (x / 4) + x % 2)))) sc[16 * c + x] = 0xff800000u;
+                }
+              } else if (edge) {
 #pragma unroll
-          for (int c = 0; c < (FULL ? D / 16 : 0); c++) {
-            uint32_t w[16];
+                for (int c = 0; c < 2; c++) {
+                  const uint32_t see = tree_word(mask[0], tile * kTile + h * 64 + c * 32 - ctx);
 #pragma unroll
-            for (int x = 0; x < 16; x++) w[x] = __float_as_uint(acc[FULL ? 16 * c + x : 0]);
-            tmem_st16(obuf + c * 16, w);
-          }
-          tmem_wait_st();
-        }
-        ok = __all_sync(0xffffffffu, mbar_wait(o_done + 2 * grp + (((s - 2) >> 1) & 1), ((s - 2) >> 2) & 1, abort));
-        if (!ok) break;
-        tc_fence_after();
-        int lr = r;
-        asm volatile("" : "+r"(lr));  // addresses of this part are not kept in registers over the steps
-        // the slot's queries are no longer needed
-        float4* scratch = reinterpret_cast<float4*>(smem + 2 * slot * TB) + lr * (D / 4);
-        const auto chunk = [&](int q) { return q ^ (lr & 7); };
-        if (joint && grp != last) {
-          ok = __all_sync(0xffffffffu, mbar_wait(s_full + 2 * last + (((end - 1) >> 1) & 1), ((end - 1) >> 2) & 1, abort));
-          if (!ok) break;
+                  for (int x = 0; x < 32; x++)
+                    if (!(see & (1u << x))) sc[32 * c + x] = 0xff800000u;
+                }
+              }
+            };
+            float mxr[NQ];
+            if (SPLIT) {
+              load(0);
+              if (!FULL) {
+                tc_fence_before();
+                warp_arrive(pv_done + grp);
+              }
+              float m2[2][2] = {{-INFINITY, -INFINITY}, {-INFINITY, -INFINITY}};
+#pragma unroll
+              for (int x = 0; x < 64; x += 2) {
+                float& y = m2[(x >> 1) & 1][(x >> 2) & 1];
+                y = fmax3(y, __uint_as_float(sc[x]), __uint_as_float(sc[x + 1]));
+              }
+#pragma unroll
+              for (int i = 0; i < NQ; i++) {
+                float m = fmaxf(m2[i][0], m2[i][1]);
+                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+                mxr[i] = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+              }
+            } else {
+              float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
-          for (int c = 0; c < D / 16; c++) {
-            uint32_t w[16];
-            tmem_ld16(obuf + c * 16, w);
-            tmem_wait_ld();
+              for (int h = 0; h < 2; h++) {
+                load(h);
 #pragma unroll
-            for (int q = 0; q < 4; q++)
-              scratch[chunk(c * 4 + q)] = make_float4(__uint_as_float(w[4 * q]), __uint_as_float(w[4 * q + 1]),
-                                                      __uint_as_float(w[4 * q + 2]), __uint_as_float(w[4 * q + 3]));
-          }
-          ml_other[slot * kTile + r] = make_float2(lane_m, lane_l);
-          tc_fence_before();
-          warp_arrive(part_full + 2 * last + (turn & 1));
-          continue;
-        }
-        const bool whole = sw.n0 == 0 && sw.n1 == sw.nt;
-        const size_t part = (size_t)(2 * blk + (sw.n0 > 0 ? 0 : 1)) * a.rows;
-        const int g = sw.g / a.pairs;
-        float M = lane_m, L = lane_l, mine_f = 1.f, other_f = 0.f;
-        if (joint) {
-          ok = __all_sync(0xffffffffu, mbar_wait(part_full + 2 * grp + (turn & 1), (turn >> 1) & 1, abort));
-          if (!ok) break;
-          const float2 z = ml_other[slot * kTile + r];
-          M = L == 0.f ? z.x : (z.y == 0.f ? M : fmaxf(M, z.x));
-          mine_f = L == 0.f ? 0.f : ex2(lane_m - M);
-          other_f = z.y == 0.f ? 0.f : ex2(z.x - M);
-          L = fmaf(L, mine_f, z.y * other_f);
-        }
+                for (int x = 0; x < 64; x += 2)
+                  mx4[(x >> 1) & 3] = fmax3(mx4[(x >> 1) & 3], __uint_as_float(sc[x]), __uint_as_float(sc[x + 1]));
+              }
+              mxr[0] = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
+            }
+            float alpha[NQ];
+            if (s == mine) {
+#pragma unroll
+              for (int i = 0; i < NQ; i++) {
+                r_run[i] = mxr[i];
+                alpha[i] = 0.f;
+                l_run[i] = 0.f;
+              }
+            } else {
+              // O and the sum follow the maximum only when some row's grew by more than 2^8 (or came out of nothing)
+              bool grow = false;
+#pragma unroll
+              for (int i = 0; i < NQ; i++) {
+                alpha[i] = 1.f;
+                grow = grow || __fmul_rn(fmaxf(r_run[i], mxr[i]), sl2) > __fmul_rn(r_run[i], sl2) + 8.0f;
+              }
+              float lane_a = 1.f;  // of the lane's row
+              if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+                for (int i = 0; i < NQ; i++) {
+                  const float r_new = fmaxf(r_run[i], mxr[i]);
+                  alpha[i] = r_run[i] == -INFINITY ? 0.f : ex2(__fmul_rn(r_run[i], sl2) - __fmul_rn(r_new, sl2));
+                  r_run[i] = r_new;
+                }
+                lane_a = alpha[0];
+                if (SPLIT) {
+                  const float x = __shfl_sync(0xffffffffu, alpha[0], 4 * (lane & 7));
+                  const float y = __shfl_sync(0xffffffffu, alpha[NQ - 1], 4 * (lane & 7));
+                  lane_a = lane & 8 ? y : x;
+                }
+                if (!FULL) {
+                  ok = __all_sync(0xffffffffu, tree_wait(o_done + 2 * grp + (((s - 2) >> 1) & 1), ((s - 2) >> 2) & 1, abort));
+                  if (!ok) break;
+                  tc_fence_after();
 #pragma unroll 1
-        for (int c = 0; c < D / 16; c++) {
-          uint32_t w[16];
-          float v[16];
-          tmem_ld16(obuf + c * 16, w);
-          tmem_wait_ld();
+                  for (int c = 0; c < D / 16; c++) {
+                    uint32_t w[16];
+                    tmem_ld16(obuf + c * 16, w);
+                    tmem_wait_ld();
 #pragma unroll
-          for (int q = 0; q < 4; q++) {
-            float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (joint) y = scratch[chunk(c * 4 + q)];
-            v[4 * q] = fmaf(__uint_as_float(w[4 * q]), mine_f, y.x * other_f);
-            v[4 * q + 1] = fmaf(__uint_as_float(w[4 * q + 1]), mine_f, y.y * other_f);
-            v[4 * q + 2] = fmaf(__uint_as_float(w[4 * q + 2]), mine_f, y.z * other_f);
-            v[4 * q + 3] = fmaf(__uint_as_float(w[4 * q + 3]), mine_f, y.w * other_f);
+                    for (int x = 0; x < 16; x++) w[x] = __float_as_uint(__uint_as_float(w[x]) * lane_a);
+                    tmem_st16(obuf + c * 16, w);
+                  }
+                }
+              }
+              if (FULL && !(ok = flush(s - 2, lane_a))) break;
+            }
+            if (SPLIT ? s >= 2 : FULL && s >= 2 && s == mine) {  // the weights of the step before have been read
+              ok = __all_sync(0xffffffffu, tree_wait(o_done + 2 * grp + (((s - 2) >> 1) & 1), ((s - 2) >> 2) & 1, abort));
+              if (!ok) break;
+              tc_fence_after();
+            }
+            uint64_t sum[NQ][4 / NQ], negm[NQ];
+#pragma unroll
+            for (int i = 0; i < NQ; i++) {
+              const float m = r_run[i] == -INFINITY ? 0.f : __fmul_rn(r_run[i], sl2);
+              negm[i] = f2(-m, -m);
+#pragma unroll
+              for (int j = 0; j < 4 / NQ; j++) sum[i][j] = 0ull;
+            }
+            const uint64_t sl2x2 = f2(sl2, sl2), minus = f2(-1.f, -1.f);
+#pragma unroll 1
+            for (int h = 1; h >= (SPLIT ? 1 : 0); h--) {
+              if (h == 0) load(0);
+              uint32_t ph[32], pl[32], pt[32];
+#pragma unroll
+              for (int x = 0; x < 32; x++) {
+                constexpr int kSums = 4 / NQ;
+                const int i = SPLIT ? x & 1 : 0, j = (SPLIT ? x >> 1 : x) % kSums;
+                float x0, x1, l0, l1;
+                f2_split(f2_fma(f2(__uint_as_float(sc[2 * x]), __uint_as_float(sc[2 * x + 1])), sl2x2, negm[i]), x0, x1);
+                const uint64_t pp = f2(ex2(x0), ex2(x1));
+                f2_split(pp, x0, x1);
+                ph[x] = pack_bf16(x0, x1);
+                const uint64_t ll = f2_fma(f2(bf_lo(ph[x]), bf_hi(ph[x])), minus, pp);
+                f2_split(ll, l0, l1);
+                pl[x] = pack_bf16(l0, l1);
+                if (FULL) {
+                  f2_split(f2_fma(f2(bf_lo(pl[x]), bf_hi(pl[x])), minus, ll), l0, l1);
+                  pt[x] = pack_bf16(l0, l1);
+                }
+                sum[i][j] = f2_add(sum[i][j], pp);
+                if (!SPLIT && x % 8 == 7) {
+                  tmem_st8(pbuf + 64 * h + x - 7, *reinterpret_cast<uint32_t(*)[8]>(ph + x - 7));
+                  tmem_st8(pbuf + 64 * h + 32 + x - 7, *reinterpret_cast<uint32_t(*)[8]>(pl + x - 7));
+                  if (FULL) tmem_st8(third + 32 * h + x - 7, *reinterpret_cast<uint32_t(*)[8]>(pt + x - 7));
+                }
+                if (SPLIT && x % 16 == 15) {
+                  tmem_st16x32(pbuf + 2 * (x - 15), *reinterpret_cast<uint32_t(*)[16]>(ph + x - 15));
+                  tmem_st16x32(pbuf + (16u << 16) + 2 * (x - 15), *reinterpret_cast<uint32_t(*)[16]>(pl + x - 15));
+                  if (FULL) {  // beside the low parts
+                    const uint32_t none[16] = {0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+                    tmem_st16x32(third + 2 * (x - 15), none);
+                    tmem_st16x32(third + (16u << 16) + 2 * (x - 15), *reinterpret_cast<uint32_t(*)[16]>(pt + x - 15));
+                  }
+                }
+              }
+              tmem_wait_st();
+              tc_fence_before();
+              warp_arrive(p_ready + 4 * grp + 2 * ((s >> 1) & 1) + (h == 0 ? 1 : 0));
+            }
+#pragma unroll
+            for (int i = 0; i < NQ; i++) {
+              uint64_t t = f2_add(sum[i][0], sum[i][1]);
+              if (NQ == 1) t = f2_add(t, f2_add(sum[i][4 / NQ - 2], sum[i][4 / NQ - 1]));
+              float x, y;
+              f2_split(t, x, y);
+              l_run[i] = fmaf(l_run[i], alpha[i], x + y);
+            }
           }
+          if (!ok) break;
+          float lane_m = r_run[0], lane_l = l_run[0];  // of the lane's row
           if (SPLIT) {
+            float m2[2], l2[2];
 #pragma unroll
-            for (int q = 0; q < 4; q++)
-              scratch[chunk(c * 4 + q)] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
-          } else if (row < a.R) {
-            if (whole) {
-              const int t = (int)fdiv((uint32_t)row, a.div_g), h = g * a.G + (row - t * a.G);
-              put_columns(a, (((size_t)sw.b * a.Tq + t) * a.Hq + h) * D + c * 16, v, 1.f / L, live);
-            } else {
-              float4* to = reinterpret_cast<float4*>(a.part_o + (part + row - pr * 2 * kTile) * D) + c * 4;
+            for (int i = 0; i < NQ; i++) {
+              float l = l_run[i];
+              l += __shfl_xor_sync(0xffffffffu, l, 1);
+              l += __shfl_xor_sync(0xffffffffu, l, 2);
+              l2[i] = __shfl_sync(0xffffffffu, l, 4 * (lane & 7));
+              m2[i] = __shfl_sync(0xffffffffu, r_run[i], 4 * (lane & 7));
+            }
+            lane_m = lane & 8 ? m2[1] : m2[0];
+            lane_l = lane & 8 ? l2[1] : l2[0];
+          }
+          lane_m = lane_m == -INFINITY ? 0.f : __fmul_rn(lane_m, sl2);
+          sw = get(0);
+          const int row = row_of(rr);
+          // the segment's unnormalised O, maximum (log2 units) and sum
+          if (FULL) {
+            if (!(ok = flush(s - 2, 1.f))) break;
 #pragma unroll
-              for (int q = 0; q < 4; q++)
-                to[q] = live ? make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]) : make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int c = 0; c < (FULL ? D / 16 : 0); c++) {
+              uint32_t w[16];
+#pragma unroll
+              for (int x = 0; x < 16; x++) w[x] = __float_as_uint(acc[FULL ? 16 * c + x : 0]);
+              tmem_st16(obuf + c * 16, w);
+            }
+            tmem_wait_st();
+          }
+          if (joint && grp != last) {
+            // the other group reads this one's O where it is
+            ml_other[(e & 3) * kTile + r] = make_float2(lane_m, lane_l);
+            tc_fence_before();
+            warp_arrive(part_full + 4 * last + (turn & 3));
+          } else {
+            const auto done = [&](int g, int n) {
+              return __all_sync(0xffffffffu, tree_wait(o_done + 2 * g + ((n >> 1) & 1), (n >> 2) & 1, abort));
+            };
+            if (!(ok = done(grp, s - 2))) break;
+            const bool whole = sw.n0 == 0 && sw.n1 == sw.nt;
+            const size_t part = (size_t)(2 * blk + (sw.n0 > 0 ? 0 : 1)) * a.rows + u * kTile + rr;
+            const int g = head_of(sw.g), t = row < a.R ? (int)fdiv((uint32_t)row, a.div_g) : 0, h = g * a.G + (row - t * a.G);
+            float M = lane_m, L = lane_l, mine_f = 1.f, other_f = 0.f;
+            if (joint) {
+              ok = __all_sync(0xffffffffu, tree_wait(part_full + 4 * grp + (turn & 3), (turn >> 2) & 1, abort));
+              if (!ok || !(ok = done(grp ^ 1, end - 2))) break;
+              const float2 z = ml_other[(e & 3) * kTile + r];
+              M = L == 0.f ? z.x : (z.y == 0.f ? M : fmaxf(M, z.x));
+              mine_f = L == 0.f ? 0.f : ex2(lane_m - M);
+              other_f = z.y == 0.f ? 0.f : ex2(z.x - M);
+              L = fmaf(L, mine_f, z.y * other_f);
+            }
+            tc_fence_after();
+            const float inv = L == 0.f ? 0.f : 1.f / L;
+#pragma unroll 1
+            for (int c = 0; c < D / 16; c++) {
+              uint32_t w[16], x[16];
+              float v[16];
+              tmem_ld16(obuf + c * 16, w);
+              if (joint) tmem_ld16(trow + C::kColO + 64u * (grp ^ 1) + c * 16, x);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 16; i++) {
+                v[i] = __uint_as_float(w[i]) * mine_f;
+                if (joint) v[i] = fmaf(__uint_as_float(x[i]), other_f, v[i]);
+                if (SPLIT) v[i] += __shfl_xor_sync(0xffffffffu, v[i], 16);  // a row's two lanes, each of which writes half
+              }
+              if (row < a.R && !(SPLIT && (c < D / 32) != (lane < 16))) {
+                if (whole) {
+                  put_columns(a, (((size_t)sw.b * a.Tq + t) * a.Hq + h) * D + c * 16, v, inv, live);
+                } else {
+                  float4* to = reinterpret_cast<float4*>(a.part_o + part * D) + c * 4;
+#pragma unroll
+                  for (int q = 0; q < 4; q++)
+                    to[q] = live ? make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]) : make_float4(0.f, 0.f, 0.f, 0.f);
+                }
+              }
+              __syncwarp();
+            }
+            tc_fence_before();
+            if (joint) warp_arrive(o_read + (grp ^ 1));
+            if (row < a.R && !(SPLIT && lane >= 16)) {
+              if (!whole)
+                a.part_ml[part] = make_float2(M, live ? L : 0.f);
+              else if (a.lse)
+                a.lse[((size_t)sw.b * a.Hq + h) * a.Tq + t] = live ? (M + log2f(L)) * kPagedLn2 : -INFINITY;
             }
           }
         }
-        tc_fence_before();
-        if (SPLIT) {
-          // a row's two lanes: a thread takes four of its columns
-          ml_own[grp * kTile + r] = make_float2(M, L);
-          if (!(ok = group_sync())) break;
-          const float4* all = reinterpret_cast<const float4*>(smem + 2 * slot * TB);
-          for (int i = r; i < a.R * (D / 4); i += kTile) {
-            const int ro = i / (D / 4), q = i % (D / 4), t = (int)fdiv((uint32_t)ro, a.div_g), at = 32 * (ro / 16) + ro % 16;
-            const float2 z = ml_own[grp * kTile + at];
-            const float4 x0 = all[at * (D / 4) + (q ^ (at & 7))], x1 = all[(at + 16) * (D / 4) + (q ^ (at & 7))];
-            RowSum x;
-            x.M = z.x;
-            x.S = z.y;
-            x.v = make_float4(x0.x + x1.x, x0.y + x1.y, x0.z + x1.z, x0.w + x1.w);
-            if (t >= info[e & 3].nodes) x.S = 0.f, x.v = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (whole) {
-              write_row<D>(a, sw.b, g, ro, q, x.v, x.M, x.S);
-            } else {
-              reinterpret_cast<float4*>(a.part_o + (part + ro) * D)[q] = x.v;
-              if (q == 0) a.part_ml[part + ro] = make_float2(x.M, x.S);
-            }
-          }
-        } else if (row < a.R) {
-          if (!whole)
-            a.part_ml[part + row - pr * 2 * kTile] = make_float2(M, live ? L : 0.f);
-          else if (a.lse) {
-            const int t = (int)fdiv((uint32_t)row, a.div_g), h = g * a.G + (row - t * a.G);
-            a.lse[((size_t)sw.b * a.Hq + h) * a.Tq + t] = live ? (M + log2f(L)) * kPagedLn2 : -INFINITY;
-          }
-        }
-        if (qon && RT == 1) {
-          pack1 = grp == last ? 1 : 0;
-        } else if (qon) {
-          // a row tile is free once its own steps are done; with one in the pair the group of the last step has both
-          const int next = units(qs);
+        // The slot of a segment is free once its last scores are there. With one row tile the group without the last step
+        // packs, while the other finishes the segment; with two each its own.
+        if (qon && nu == 2) {
+          const int next = units(get(1));
           times = next == 2 ? 1 : 2;
-          pack0 = nu == 2 ? u : 0;
-          pack1 = nu == 2 ? min(u + 1, next) : (grp == last ? next : 0);
+          pack0 = u;
+          pack1 = min(u + 1, next);
+        } else if (qon && grp != last) {
+          pack1 = RT == 1 ? 1 : units(get(1));
+          times = RT == 1 || pack1 == 2 ? 1 : 2;
+          ok = __all_sync(0xffffffffu, tree_wait(s_full + 2 * last + (((end - 1) >> 1) & 1), ((end - 1) >> 2) & 1, abort));
+          if (!ok) break;
         }
-        if ((SPLIT || joint) && pack0 < pack1 && !(ok = group_sync())) break;  // every warp is done with the slot
       }
-      for (int u = pack0; u < pack1; u++) pack(qs, e + kAhead, u, times);
+      for (int u = pack0; u < pack1; u++) pack(get(1), e + kAhead, u, times);
     }
     if (!ok) {
       *abort = 1;
@@ -982,6 +1008,7 @@ cudaError_t launch_tree_t(const PagedTreeArgs& a, int grid, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     attr_set[dev] = true;
   }
+  static_assert(tree_head(2048) + TreeCfg<D>::kBytes + 1024 <= kSmemMax, "the largest batch");
   const int bytes = tree_head(a.B) + TreeCfg<D>::kBytes + 1024;
   if (bytes > kSmemMax) return cudaErrorInvalidValue;
   k_tree_sweep<D, RT, SPLIT, FULL><<<grid, kTreeThreads, (size_t)bytes, s>>>(a);
