@@ -25,7 +25,7 @@
 // block's first segments while its first keys are on their way, those of a later one when its slot is free, by the group
 // that does not write the rows of the segment before out; that one reads the other's O where it is, in TMEM. (16 trees of
 // 16: 32.5 us, with a kernel in front of the sweep 34.5, with four more warps for it 36 to 38. 64 trees of 32 with 128
-// rows: 54; with one group doing both 61.5, with the kernel 58.0.)
+// rows: 54.4; with one group doing both 61.5, with the kernel 58.0.)
 //
 // The warps wait for instructions as often as for scores, so code that is not part of a step is kept small (its loops
 // rolled, its waits short), and registers are kept for the steps: four spilled words or a part of a segment's end unrolled
@@ -38,8 +38,8 @@
 // for a tile of every block (a steady 6.8 TB/s); the call adds the start (lengths, tables, first tiles: 4 us), the last
 // tiles' steps (3 us) and the join (2 to 6 us). 16 trees of 16 on contexts around 8192, pages of 64: 32.5 us, 19.1 of them
 // the bytes; with pages of 16 39 us (eight copies a tile, each of 2 KB). With 128 rows a step takes the tensor cores
-// 1536 clocks for two parts of both factors and the softmax as long: 64 trees of 32 on 700 to 4096 positions, 54 us.
-// With 256 rows and an fp32 o (three parts), 64 tokens on 131001 positions, 112 us.
+// 1536 clocks for two parts of both factors and the softmax as long: 64 trees of 32 on 700 to 4096 positions, 53.3 us.
+// With 256 rows and an fp32 o (three parts), 64 tokens on 131001 positions, 110 us.
 #include "paged_sweep.cuh"
 
 namespace ne {
@@ -628,6 +628,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
               live = token(row_of(rr)) < tree.nodes;
             }
             const bool edge = (tile + 1) * kTile > ctx;  // the tile ends in the tree or behind it
+            // What a row does not see becomes -infinity: a lane's scores where they lie, SPLIT a thread's once it has them (less
+            // code in a step against a trip to TMEM in the last ones: 64 trees of 32 54.4 -> 53.4 us; 16 of 16 32.6 -> 33.1).
             unsigned long long mask[NQ];
             if (edge) {
               const int nodes = tree.nodes, row0 = row_of(0), past = ctx + nodes - tile * kTile;
@@ -636,6 +638,18 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
                 const int t = token(row0 + (SPLIT ? q4 * 16 + lane / 4 + 8 * i : r));
                 mask[i] = t < nodes ? tree.mask[t] : 0ull;
               }
+#pragma unroll 1
+              for (int c = SPLIT ? kTile / 16 : max(0, ctx - tile * kTile) / 16; c < kTile / 16; c++) {
+                const uint32_t see = tree_word(mask[0], tile * kTile + c * 16 - ctx);
+                uint32_t w[16];
+                tmem_ld16(sbuf + c * 16, w);
+                tmem_wait_ld();
+#pragma unroll
+                for (int x = 0; x < 16; x++)
+                  if (!(see & (1u << x))) w[x] = 0xff800000u;
+                tmem_st16(sbuf + c * 16, w);
+              }
+              if (!SPLIT) tmem_wait_st();
               if (past < kTile) {
                 // what lies behind the last position may be anything: its weight is 0, but 0 times a NaN is not
                 const int kt = k0 + tile - n0;
@@ -664,7 +678,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
                 tmem_ld32(sbuf + h * 64 + 32, hi);
               }
               tmem_wait_ld();
-              if (edge && SPLIT) {
+              if (SPLIT && edge) {
 #pragma unroll
                 for (int c = 0; c < 4; c++) {
                   const int at = tile * kTile + c * 32 - ctx;
@@ -673,14 +687,6 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
 #pragma unroll
                   for (int x = 0; x < 16; x++)  // columns 8 (x / 4) + 2 (lane % 4) + x % 2 of the 32, row x / 2 % 2
                     if (!(see[x / 2 % 2] & (1u << (8 * (x / 4) + x % 2)))) sc[16 * c + x] = 0xff800000u;
-                }
-              } else if (edge) {
-#pragma unroll
-                for (int c = 0; c < 2; c++) {
-                  const uint32_t see = tree_word(mask[0], tile * kTile + h * 64 + c * 32 - ctx);
-#pragma unroll
-                  for (int x = 0; x < 32; x++)
-                    if (!(see & (1u << x))) sc[32 * c + x] = 0xff800000u;
                 }
               }
             };
