@@ -27,6 +27,7 @@ namespace {
 // four heads 2.1 us, 16381 (33.3 MB) 8.6 us.
 template <int D, bool SLOTS>
 __global__ void __launch_bounds__(128) k_kv_append_paged(const PagedAppendArgs a) {
+  if (SLOTS) pdl_wait();
   constexpr int kCPR = D / 8;
   const int lane = threadIdx.x & 31;
   const long long total = (long long)a.N * a.Hkv * kCPR;
@@ -136,6 +137,10 @@ template <bool SLOTS>
 static cudaError_t launch_append(const PagedAppendArgs& a, int D, cudaStream_t s) {
   const long long n = (long long)a.N * a.Hkv * (D / 8);
   const unsigned grid = (unsigned)((n + 127) / 128);
+  if (SLOTS) {
+    return D == 64 ? launch_pdl(k_kv_append_paged<64, SLOTS>, dim3(grid), 128, 0, s, a)
+                   : launch_pdl(k_kv_append_paged<32, SLOTS>, dim3(grid), 128, 0, s, a);
+  }
   if (D == 64)
     k_kv_append_paged<64, SLOTS><<<grid, 128, 0, s>>>(a);
   else

@@ -88,6 +88,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_paged_plan(const PagedPlanArgs
   __shared__ bool s_ok[kPlanMaxB];
   __shared__ unsigned long long wsum[32];
   __shared__ int s_first_short;
+  pdl_wait();
   pdl_launch();
   const int tid = threadIdx.x, P = a.num_pages, cap = a.max_pages << a.page_shift;
   int first = a.span[0], count = a.span[1];
@@ -252,6 +253,7 @@ template <int D>
 __global__ void __launch_bounds__(kKeepThreads) k_kv_keep(const PagedKeepArgs a) {
   constexpr int kCPR = D / 8;
   __shared__ long long s_src[kTreeMax], s_dst[kTreeMax];
+  pdl_wait();
   const int g0 = blockIdx.x * (kKeepThreads / 32), b = blockIdx.y, tid = threadIdx.x;
   const int cap = a.max_pages << a.page_shift, mask = (1 << a.page_shift) - 1;
   const int len = a.len[b], nodes = a.nodes ? a.nodes[b] : a.tokens, m = a.count[b];
@@ -313,19 +315,14 @@ __global__ void __launch_bounds__(kKeepThreads) k_kv_keep(const PagedKeepArgs a)
 }  // namespace
 
 cudaError_t launch_paged_plan(const PagedPlanArgs& a, cudaStream_t s) {
-  k_paged_plan<<<1, kPlanThreads, 0, s>>>(a);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_pdl(k_paged_plan, dim3(1), kPlanThreads, 0, s, a);
   if (e != cudaSuccess || a.N <= kPlanRows) return e;
   return launch_pdl(k_paged_slots, dim3((unsigned)((a.N + 256 * kSlotRows - 1) / (256 * kSlotRows))), 256, 0, s, a);
 }
 
 cudaError_t launch_kv_keep(const PagedKeepArgs& a, int D, cudaStream_t s) {
   const dim3 grid((unsigned)((a.Hkv + kKeepThreads / 32 - 1) / (kKeepThreads / 32)), (unsigned)a.B);
-  if (D == 64)
-    k_kv_keep<64><<<grid, kKeepThreads, 0, s>>>(a);
-  else
-    k_kv_keep<32><<<grid, kKeepThreads, 0, s>>>(a);
-  return cudaGetLastError();
+  return D == 64 ? launch_pdl(k_kv_keep<64>, grid, kKeepThreads, 0, s, a) : launch_pdl(k_kv_keep<32>, grid, kKeepThreads, 0, s, a);
 }
 
 }  // namespace ne

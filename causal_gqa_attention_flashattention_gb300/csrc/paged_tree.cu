@@ -236,6 +236,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_sweep(const __grid_con
     }
     fence_mbar_init();
   }
+  pdl_wait();  // before the tensor memory is taken: the kernel in front may still need some
   if (warp == 1) tmem_alloc(tmem_slot, 512);
   running_costs<kTreeThreads>(a.B, cum, wsum, tid, [&](int b) {
     const TreeShape x = tree_shape(a, b, blk == 0);
@@ -1017,8 +1018,7 @@ cudaError_t launch_tree_t(const PagedTreeArgs& a, int grid, cudaStream_t s) {
   static_assert(tree_head(2048) + TreeCfg<D>::kBytes + 1024 <= kSmemMax, "the largest batch");
   const int bytes = tree_head(a.B) + TreeCfg<D>::kBytes + 1024;
   if (bytes > kSmemMax) return cudaErrorInvalidValue;
-  k_tree_sweep<D, RT, SPLIT, FULL><<<grid, kTreeThreads, (size_t)bytes, s>>>(a);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_pdl(k_tree_sweep<D, RT, SPLIT, FULL>, dim3((unsigned)grid), kTreeThreads, (size_t)bytes, s, a);
   if (e != cudaSuccess) return e;
   return launch_pdl(k_tree_join<D>, dim3((unsigned)grid, kJoinSlices), kJoinThreads, 0, s, a);
 }
