@@ -15,7 +15,7 @@ namespace {
 // A returned page serves the next call, so what is read of the ring and what is written are different
 // places.  One block does the sums and moves the pages: the state is a few KB, and what bounds the
 // kernel is its chain of round trips, not the bytes: launch and lengths, ring, table, parents.  64 sequences
-// of one new token 4.7 us on the device, 48 trees of 5 to 24 tokens 6.5 us.
+// of one new token 4.4 us on the device (4.7 if the launch waits for the kernel in front), 48 trees of 5 to 24 tokens 6.1 us.
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanMaxB = 2048;
 // Rows up to which that block writes the slots too (64 sequences with 2048 rows in all 6.1 us, with a second launch
@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_paged_plan(const PagedPlanArgs
 }
 
 // The slots of many rows: 128 neighbouring ones a warp, whose threads look a sequence up again only where it changes.  With
-// the plan in front 11.7 us for 200 prompts of 33 to 4096 tokens: the plan's block, a launch, and the
+// the plan in front 11.3 us for 200 prompts of 33 to 4096 tokens: the plan's block, a launch, and the
 // trips cu -> table -> slot (the rows' 3.3 MB take 0.5 us).
 constexpr int kSlotRows = 4;
 __global__ void __launch_bounds__(256) k_paged_slots(const PagedPlanArgs a) {
@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(256) k_paged_slots(const PagedPlanArgs a) {
 // that stay, in rising order: token path[i] moves to position len - nodes + i.  path[i] >= i, so a row may be
 // both a source and a place, but a place only of a token before it: a warp takes a (sequence, head) and moves some rows
 // at a time, in order, all of them read before one is written.  Bound by the trips lengths -> path -> table ->
-// row: one tree of 8 tokens 2.4 us, 64 trees with 64 heads (16 layers of 4), 13.8 MB, 4.3 us; 6.5 us with a block for
+// row: one tree of 8 tokens 2.0 us, 64 trees with 64 heads (16 layers of 4), 13.8 MB, 3.8 us; 6.5 us with a block for
 // each, whose threads wait for one another.
 constexpr int kKeepThreads = 128, kKeepChunks = 8;
 template <int D>

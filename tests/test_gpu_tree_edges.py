@@ -175,3 +175,47 @@ def test_longest_table(nb):
         # the bound of check with M = 0 and A, the mean of |v|, below 1
         assert float((o[0, t, 0].double() - want).abs().max()) <= 2.0 ** -14
         assert abs(float(lse[0, 0, t]) - np.log(n + len(see))) <= 2.0 ** -14 + 2.0 ** -22 * 14
+
+
+@pytest.mark.parametrize("front", ["nothing", "memset", "copy", "host", "kernel", "join"])
+def test_captured_behind_other_work(nb, front):
+    """The calls' kernels are dependent launches: a step captured behind every kind of node, which writes what it reads."""
+    s = setup([300, 20], [8, 6], 8, 12, 4, 64, 16, seed=45)
+    q, lens, path = s["q"].clone(), s["lens"].clone(), i32([[0, 1], [0, 2]])
+    host = s["q"].cpu().pin_memory()
+    side = torch.cuda.Stream()
+
+    def step():
+        if front == "memset":
+            s["q"].zero_()
+        elif front == "copy":
+            s["q"].copy_(q)
+        elif front == "host":
+            s["q"].copy_(host, non_blocking=True)
+        elif front == "kernel":
+            torch.mul(q, 2, out=s["q"])
+        elif front == "join":
+            side.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(side):
+                torch.mul(q, 2, out=s["q"])
+            torch.add(lens, 0, out=s["lens"])
+            torch.cuda.current_stream().wait_stream(side)
+        got = nb.attn_decode_tree(s["q"], s["kp"], s["vp"], s["table"], s["lens"], s["parents"], tree_len=s["nodes"], rope_base=BASE)
+        kp, vp = s["kp"].clone(), s["vp"].clone()
+        n = nb.kv_keep_paged(kp, vp, s["table"], s["lens"], s["nodes"], path, i32two)
+        return (*got, n, kp.view(torch.int16), vp.view(torch.int16))
+    i32two = i32([2, 1])
+    want = [x.clone() for x in step()]
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = step()
+    for _ in range(3):
+        if front not in ("nothing",):
+            s["q"].fill_(7)
+        for x in got:
+            x.zero_()
+        g.replay()
+        nb.check_status()
+        for x, y in zip(got, want):
+            assert torch.equal(x, y)
