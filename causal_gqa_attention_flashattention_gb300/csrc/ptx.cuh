@@ -91,7 +91,6 @@ __device__ __forceinline__ bool mbar_try_wait_sleep(uint64_t* bar, uint32_t pari
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, const volatile int* abort,
                                           unsigned long long limit_ns = kWaitLimitNs) {
   if (mbar_try_wait(bar, parity)) return true;
-  if (mbar_try_wait_sleep(bar, parity, 20000u)) return true;
   const unsigned long long t0 = globaltimer();
   for (;;) {
     if (mbar_try_wait_sleep(bar, parity, 20000u)) return true;
