@@ -93,6 +93,8 @@ def lib():
         L.ne_attn_decode_paged.restype = i
         L.ne_attn_paged_plan.argtypes = [vp] * 13 + [i] * 6 + [ll, vp]
         L.ne_attn_paged_plan.restype = i
+        L.ne_attn_paged_plan_ex.argtypes = [vp] * 14 + [i] * 6 + [ll, vp]
+        L.ne_attn_paged_plan_ex.restype = i
         L.ne_attn_kv_append_slots.argtypes = [vp] * 7 + [i] * 6 + [ll] * 3 + [f, f, i, vp]
         L.ne_attn_kv_append_slots.restype = i
         L.ne_attn_decode_tree_workspace_size.argtypes = [i, i, i, i, i]
@@ -658,7 +660,9 @@ def attn_decode_paged(q, k_pages, v_pages, page_table, kv_len, q_weight=None, ep
 
 
 # ------------------------------------------------------------------ drafted trees over the paged cache
-PagedPlan = collections.namedtuple("PagedPlan", "kv_len held span cu_new slots positions")
+class PagedPlan(collections.namedtuple("PagedPlan", "kv_len held span cu_new slots positions")):
+    """What paged_plan returns.  new_len [B], the positions that each sequence was granted, is an attribute beside the tuple."""
+    new_len = None
 
 
 _bind = None
@@ -675,7 +679,7 @@ def _compiled():
         spec = importlib.util.spec_from_file_location("_neattn_bind", BIND_PATH)
         m = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(m)
-        names = ("ne_attn_paged_plan", "ne_attn_kv_append_slots", "ne_attn_decode_tree",
+        names = ("ne_attn_paged_plan_ex", "ne_attn_kv_append_slots", "ne_attn_decode_tree",
                  "ne_attn_decode_tree_workspace_size", "ne_attn_kv_keep_paged")
         m.init(dict({n: ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in names},
                     OutOfMemoryError=torch.OutOfMemoryError))
@@ -684,7 +688,7 @@ def _compiled():
 
 
 def paged_plan(page_table, free_pages, held, free_span, kv_len, new_len, rows, page_size, parents=None, kv_len_out=None,
-               held_out=None, span_out=None, stream=None):
+               held_out=None, span_out=None, stream=None, new_len_out=None):
     """Block tables and slot maps from lengths, on the device (ne_attn_paged_plan).
 
     Sequence b has kv_len[b] positions, holds the first held[b] pages of its row of page_table [B, max_pages] and
@@ -694,16 +698,19 @@ def paged_plan(page_table, free_pages, held, free_span, kv_len, new_len, rows, p
 
     Returns PagedPlan(kv_len [B], held [B], span [2], cu_new [B + 1], slots [rows], positions [rows]): the new
     lengths and pages held (a sequence whose pages the ring no longer has keeps its old ones), where each
-    sequence's rows begin, and the place (-1: none) and rotary position of every row for kv_append_slots.
-    held_out and span_out may be held and free_span themselves, kv_len_out may not be kv_len."""
+    sequence's rows begin, and the place (-1: none) and rotary position of every row for kv_append_slots.  Its new_len
+    [B] is what each sequence was granted, 0 where refused: the tree_len of attn_decode_tree and kv_keep_paged.
+    held_out, span_out and new_len_out may be held, free_span and new_len themselves, kv_len_out may not be kv_len."""
     if stream is not None:
         return _on(stream, paged_plan, page_table, free_pages, held, free_span, kv_len, new_len, rows, page_size, parents,
-                   kv_len_out, held_out, span_out)
+                   kv_len_out, held_out, span_out, None, new_len_out)
     r = (_bind or _compiled()).plan(page_table, free_pages, held, free_span, kv_len, new_len, rows, page_size, parents, kv_len_out,
-                                    held_out, span_out)
+                                    held_out, span_out, new_len_out)
     if type(r) is int:
         raise NeAttnError("ne_attn_paged_plan", r)
-    return PagedPlan._make(r)
+    p = PagedPlan._make(r[:6])
+    p.new_len = r[6]
+    return p
 
 
 def kv_append_slots(k_new, v_new, k_pages, v_pages, slots, positions, capacity, k_weight=None, eps=1e-6,
@@ -750,7 +757,8 @@ def kv_keep_paged(k_pages, v_pages, page_table, kv_len, tree_len, path, path_len
     """Keeps the accepted path of every sequence's tree (ne_attn_kv_keep_paged): the keys and values of its tokens
     path[b, :path_len[b]] (int32 [B, width] and [B], rising) move to the positions right behind the context, in place.
 
-    kv_len int32 [B] counts the cached positions, the tree's tree_len (int32 [B], or one number for all) included;
+    kv_len int32 [B] counts the cached positions, the tree's tree_len (int32 [B], or one number for all) included; one of 0
+    keeps nothing and its length, whatever its path holds;
     returns the new lengths (kv_len_out if given, which may not be kv_len).  The pools of several layers with one
     table may be passed as one [num_pages, layers * Hkv, page_size, D]."""
     if stream is not None:

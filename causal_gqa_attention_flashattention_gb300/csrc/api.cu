@@ -1672,6 +1672,15 @@ int ne_attn_paged_plan(int* page_table, int* free_pages, const int* held, const 
                        const int* new_len, const int* parents, int* held_out, int* free_span_out, int* kv_len_out,
                        int* cu_new, int* slots, int* positions, int N, int B, int Tq, int page_size, int num_pages,
                        int max_pages, long long parent_stride, void* stream) {
+  return ne_attn_paged_plan_ex(page_table, free_pages, held, free_span, kv_len, new_len, parents, held_out, free_span_out,
+                               kv_len_out, nullptr, cu_new, slots, positions, N, B, Tq, page_size, num_pages, max_pages,
+                               parent_stride, stream);
+}
+
+int ne_attn_paged_plan_ex(int* page_table, int* free_pages, const int* held, const int* free_span, const int* kv_len,
+                          const int* new_len, const int* parents, int* held_out, int* free_span_out, int* kv_len_out,
+                          int* new_len_out, int* cu_new, int* slots, int* positions, int N, int B, int Tq, int page_size,
+                          int num_pages, int max_pages, long long parent_stride, void* stream) {
   if (!page_table || !free_pages || !held || !free_span || !kv_len || !new_len || !held_out || !free_span_out ||
       !kv_len_out || !cu_new || (N > 0 && (!slots || !positions)))
     return NE_ERR_ARG;
@@ -1685,7 +1694,7 @@ int ne_attn_paged_plan(int* page_table, int* free_pages, const int* held, const 
     if (Tq > kTreeMax) return NE_ERR_UNSUPPORTED;
   }
   const void* all[] = {page_table, free_pages, held, free_span, kv_len, new_len, parents, held_out, free_span_out,
-                       kv_len_out, cu_new, slots, positions};
+                       kv_len_out, new_len_out, cu_new, slots, positions};
   for (const void* p : all)
     if (!aligned4(p)) return NE_ERR_ALIGN;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -1705,6 +1714,7 @@ int ne_attn_paged_plan(int* page_table, int* free_pages, const int* held, const 
   a.held_out = held_out;
   a.span_out = free_span_out;
   a.len_out = kv_len_out;
+  a.new_out = new_len_out;
   a.cu = cu_new;
   a.slots = slots;
   a.positions = positions;

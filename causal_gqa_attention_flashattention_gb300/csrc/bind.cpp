@@ -20,7 +20,7 @@
 
 namespace {
 
-decltype(&ne_attn_paged_plan) f_plan = nullptr;
+decltype(&ne_attn_paged_plan_ex) f_plan = nullptr;
 decltype(&ne_attn_kv_append_slots) f_append = nullptr;
 decltype(&ne_attn_decode_tree) f_tree = nullptr;
 decltype(&ne_attn_decode_tree_workspace_size) f_tree_size = nullptr;
@@ -169,7 +169,7 @@ PyObject* wrap(std::initializer_list<Tensor> out) {
   return t;
 }
 
-// page_table, free_pages, held, free_span, kv_len, new_len, rows, page_size, parents, kv_len_out, held_out, span_out
+// page_table, free_pages, held, free_span, kv_len, new_len, rows, page_size, parents, kv_len_out, held_out, span_out, new_len_out
 PyObject* plan(PyObject* const* a) {
   const Tensor& table = tensor(a[0], "page_table");
   Call c(table, "page_table");
@@ -188,8 +188,8 @@ PyObject* plan(PyObject* const* a) {
   const int* parents = given(a[8]) ? tree(a[8], B, c.dev, &Tq, &pstride) : nullptr;
   // what is not given lies in one allocation
   at::AutoDispatchBelowADInplaceOrView plain;
-  const bool own_total = !given(a[9]), own_got = !given(a[10]), own_left = !given(a[11]);
-  const int64_t most = B + 1 + 2 * (int64_t)rows + (own_total ? B : 0) + (own_got ? B : 0) + (own_left ? 2 : 0);
+  const bool own_total = !given(a[9]), own_got = !given(a[10]), own_left = !given(a[11]), own_new = !given(a[12]);
+  const int64_t most = B + 1 + 2 * (int64_t)rows + (own_total ? B : 0) + (own_got ? B : 0) + (own_left ? 2 : 0) + (own_new ? B : 0);
   const Tensor all = make({most}, kInt, c.dev);
   int64_t at = 0;
   const auto part = [&](int64_t n) {
@@ -199,11 +199,12 @@ PyObject* plan(PyObject* const* a) {
   const Tensor slots = part(rows), pos = part(rows), cu = part(B + 1);
   const Tensor total = own_total ? part(B) : out32(a[9], "kv_len_out", c.dev, {B});
   const Tensor got = own_got ? part(B) : out32(a[10], "held_out", c.dev, {B}), left = own_left ? part(2) : out32(a[11], "span_out", c.dev, {2});
+  const Tensor granted = own_new ? part(B) : out32(a[12], "new_len_out", c.dev, {B});
   if (!own_total) apart(total, THPVariable_Unpack(a[4]), "kv_len_out and kv_len must not share memory");
   const int st = f_plan(p_table, p_ring, held, span, len, add, parents, got.data_ptr<int>(), left.data_ptr<int>(),
-                        total.data_ptr<int>(), cu.data_ptr<int>(), slots.data_ptr<int>(), pos.data_ptr<int>(), rows, (int)B, Tq, page,
-                        (int)ring.size(0), (int)width, pstride, c.stream);
-  return st == NE_OK ? wrap({total, got, left, cu, slots, pos}) : status(st);
+                        total.data_ptr<int>(), granted.data_ptr<int>(), cu.data_ptr<int>(), slots.data_ptr<int>(), pos.data_ptr<int>(), rows, (int)B,
+                        Tq, page, (int)ring.size(0), (int)width, pstride, c.stream);
+  return st == NE_OK ? wrap({total, got, left, cu, slots, pos, granted}) : status(st);
 }
 
 // k_new, v_new, k_pages, v_pages, slots, positions, capacity, k_weight, eps, rope_base, rope_half
@@ -340,7 +341,7 @@ PyObject* init(PyObject*, PyObject* d) {
     PyErr_SetString(PyExc_TypeError, "init takes a dict of addresses");
     return nullptr;
   }
-  if (!take(d, "ne_attn_paged_plan", &f_plan) || !take(d, "ne_attn_kv_append_slots", &f_append) ||
+  if (!take(d, "ne_attn_paged_plan_ex", &f_plan) || !take(d, "ne_attn_kv_append_slots", &f_append) ||
       !take(d, "ne_attn_decode_tree", &f_tree) || !take(d, "ne_attn_decode_tree_workspace_size", &f_tree_size) ||
       !take(d, "ne_attn_kv_keep_paged", &f_keep))
     return nullptr;
@@ -356,7 +357,7 @@ PyObject* init(PyObject*, PyObject* d) {
 
 #define FAST(f, n) reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&entry<f, n>)), METH_FASTCALL, nullptr
 PyMethodDef methods[] = {{"init", init, METH_O, nullptr},
-                         {"plan", FAST(plan, 12)},
+                         {"plan", FAST(plan, 13)},
                          {"append", FAST(append, 11)},
                          {"decode_tree", FAST(decode_tree, 15)},
                          {"keep", FAST(keep, 8)},

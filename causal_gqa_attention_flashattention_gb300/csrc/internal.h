@@ -231,6 +231,7 @@ struct PagedPlanArgs {
   const int *held, *span, *len, *add;          // [B], [2] (first, count), [B], [B]
   const int* parents;                          // [B, Tq] parent_stride apart, or null
   int *held_out, *span_out, *len_out;          // the first two may be held and span
+  int* new_out;                                // [B] or null; may be add
   int *cu, *slots, *positions;                 // [B + 1], [N], [N] (N may be 0)
   int* status;
   long long parent_stride;

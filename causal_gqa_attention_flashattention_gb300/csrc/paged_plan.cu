@@ -156,6 +156,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_paged_plan(const PagedPlanArgs
     // a refused sequence keeps what it has
     a.held_out[b] = want[i];
     a.len_out[b] = len[i] + (ok[i] ? add[i] : 0);
+    if (a.new_out) a.new_out[b] = ok[i] ? add[i] : 0;
     s_len[b] = len[i];
     s_ok[b] = ok[i];
   }
@@ -256,7 +257,8 @@ __global__ void __launch_bounds__(kKeepThreads) k_kv_keep(const PagedKeepArgs a)
   pdl_wait();
   const int g0 = blockIdx.x * (kKeepThreads / 32), b = blockIdx.y, tid = threadIdx.x;
   const int cap = a.max_pages << a.page_shift, mask = (1 << a.page_shift) - 1;
-  const int len = a.len[b], nodes = a.nodes ? a.nodes[b] : a.tokens, m = a.count[b];
+  const int len = a.len[b], nodes = a.nodes ? a.nodes[b] : a.tokens;
+  const int m = nodes == 0 ? 0 : a.count[b];  // no tree (the plan gave it no place): whatever its path holds
   int x = 0, before = -1;  // at once with the lengths
   if (tid < a.width) {
     x = a.path[(size_t)b * a.width + tid];

@@ -423,8 +423,10 @@ int ne_attn_decode_paged(const void* q, const void* q_w, const void* k_pages, co
  * every sequence the pages for its drafted tokens and every token its slot and rotary position;
  * ne_attn_kv_append_slots writes their keys and values; ne_attn_decode_tree is their attention; once it is known which
  * of them stay, ne_attn_kv_keep_paged moves those behind the cached positions, and the next plan takes back
- * the pages that are left over.  Lengths, trees, tables and paths are int32 arrays in device memory, read when
- * the kernels run, so a captured CUDA graph of the whole step replays with new ones.
+ * the pages that are left over.  A sequence that the plan refuses sits the step out: the tree_len of the attention
+ * and of keep is what the plan granted (new_len_out of ne_attn_paged_plan_ex, 0 where refused), not what was asked for,
+ * which would take the last positions of its context for a tree.  Lengths, trees, tables and paths are int32 arrays in
+ * device memory, read when the kernels run, so a captured CUDA graph of the whole step replays with new ones.
  *
  * A tree has at most 64 tokens.  Token t of sequence b hangs on token parents[b, t] < t, or on the context
  * (-1; several may); rows of parents lie parent_stride values apart (0: one tree for the whole batch, else at least Tq).  Its
@@ -453,6 +455,12 @@ int ne_attn_paged_plan(int* page_table, int* free_pages, const int* held, const 
                        const int* new_len, const int* parents, int* held_out, int* free_span_out, int* kv_len_out,
                        int* cu_new, int* slots, int* positions, int N, int B, int Tq, int page_size, int num_pages,
                        int max_pages, long long parent_stride, void* stream);
+/* The same, and new_len_out [B] (may be new_len itself, or NULL): the positions that each sequence was granted, new_len
+ * or, where it was refused, 0. */
+int ne_attn_paged_plan_ex(int* page_table, int* free_pages, const int* held, const int* free_span, const int* kv_len,
+                          const int* new_len, const int* parents, int* held_out, int* free_span_out, int* kv_len_out,
+                          int* new_len_out, int* cu_new, int* slots, int* positions, int N, int B, int Tq, int page_size,
+                          int num_pages, int max_pages, long long parent_stride, void* stream);
 
 /*
  * ne_attn_kv_append_slots: as ne_attn_kv_append_paged, with the place and the rotary position of every row given: row n
@@ -487,10 +495,10 @@ int ne_attn_decode_tree(const void* q, const void* q_w, const void* k_pages, con
  * path[b, 0], path[b, 1], .. stay (path [B, width], width <= 64; rising, as a child comes after its parent): the keys
  * and values of token path[b, i] move to position kv_len[b] - tree_len[b] + i, in place, whatever the
  * overlap.  Writes kv_len_out[b] = kv_len[b] - tree_len[b] + path_len[b] (a buffer of its own; idle slots, with
- * kv_len[b] below tree_len[b] or 0, keep max(kv_len, 0)).  A path that does not rise or leaves the tree
- * is recorded as NE_ERR_TREE and none of it stays.  The moved keys keep the rotation of their depth, which
- * is right for a path from the context on.  The pools of layers that share one table may be given as one, with all their heads:
- * [num_pages, layers * Hkv, page_size, D].
+ * kv_len[b] below tree_len[b] or 0, keep max(kv_len, 0); a tree_len[b] of 0 keeps kv_len[b], whatever its path
+ * holds).  A path that does not rise or leaves the tree is recorded as NE_ERR_TREE and none of it stays.  The moved
+ * keys keep the rotation of their depth, which is right for a path from the context on.  The pools of layers that share
+ * one table may be given as one, with all their heads: [num_pages, layers * Hkv, page_size, D].
  */
 int ne_attn_kv_keep_paged(void* k_pages, void* v_pages, const int* page_table, const int* kv_len, const int* tree_len,
                           const int* path, const int* path_len, int* kv_len_out, int B, int tokens, int width, int Hkv,

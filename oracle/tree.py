@@ -18,7 +18,7 @@ def ancestors(parents, t):
 
 
 def plan(table, ring, held, span, kv_len, new_len, rows, page, parents=None):
-    """(table, ring, held, span, kv_len, cu, slots, positions) after the call; lists and nested lists."""
+    """(table, ring, held, span, kv_len, cu, slots, positions, granted) after the call; lists and nested lists."""
     table, ring, held = [list(r) for r in table], list(ring), list(held)
     P, (first, count) = len(ring), span
     want = [-(-(k + n) // page) for k, n in zip(kv_len, new_len)]
@@ -40,6 +40,7 @@ def plan(table, ring, held, span, kv_len, new_len, rows, page, parents=None):
             total.append(k + n)
     for j, pg in enumerate(back):
         ring[(first + count + j) % P] = pg
+    granted = [t - k for t, k in zip(total, kv_len)]
     cu, slots, positions = [0], [-1] * rows, [0] * rows
     for b, (k, n) in enumerate(zip(kv_len, new_len)):
         for t in range(n):
@@ -48,7 +49,7 @@ def plan(table, ring, held, span, kv_len, new_len, rows, page, parents=None):
                 slots[r] = table[b][at // page] * page + at % page
             positions[r] = at if parents is None else k + len(ancestors(parents[b], t)) - 1
         cu.append(cu[-1] + n)
-    return table, ring, held, [(first + taken) % P, count - taken + len(back)], total, cu, slots, positions
+    return table, ring, held, [(first + taken) % P, count - taken + len(back)], total, cu, slots, positions, granted
 
 
 def decode_tree(q, q_w, kp, vp, table, lens, parents, nodes, base, eps=1e-6, half=False):
@@ -79,8 +80,9 @@ def decode_tree(q, q_w, kp, vp, table, lens, parents, nodes, base, eps=1e-6, hal
 
 
 def keep(kp, vp, table, lens, nodes, path, count, page):
-    """(kp, vp, lengths) after the accepted paths have moved; pools [P, H, page, D]."""
+    """(kp, vp, lengths) after the accepted paths have moved; pools [P, H, page, D].  No tree: no path, whatever it holds."""
     kp, vp, out = kp.copy(), vp.copy(), []
+    count = [c if n else 0 for c, n in zip(count, nodes)]
     for b in range(len(lens)):
         if lens[b] <= 0 or lens[b] < nodes[b]:
             out.append(max(lens[b], 0))
