@@ -45,7 +45,8 @@
 namespace ne {
 namespace {
 
-// Sequence b: its positions and tokens, both 0 for an idle slot of the batch (or one that cannot be).
+// Sequence b: its positions and tokens, both 0 for an idle slot of the batch (or one that cannot be, or one without a
+// tree in this call: nothing of its context is read).
 struct TreeShape {
   int len, nodes;
 };
@@ -60,7 +61,7 @@ __device__ __forceinline__ TreeShape tree_shape(const PagedTreeArgs& a, int b, b
     if (record) record_page(a.status);
     return {0, 0};
   }
-  if (x.len < x.nodes) return {0, 0};
+  if (x.len < x.nodes || x.nodes == 0) return {0, 0};
   return x;
 }
 
