@@ -258,12 +258,13 @@ __global__ void __launch_bounds__(kKeepThreads) k_kv_keep(const PagedKeepArgs a)
   const int g0 = blockIdx.x * (kKeepThreads / 32), b = blockIdx.y, tid = threadIdx.x;
   const int cap = a.max_pages << a.page_shift, mask = (1 << a.page_shift) - 1;
   const int len = a.len[b], nodes = a.nodes ? a.nodes[b] : a.tokens;
-  const int m = nodes == 0 ? 0 : a.count[b];  // no tree (the plan gave it no place): whatever its path holds
+  int m = a.count[b];
   int x = 0, before = -1;  // at once with the lengths
   if (tid < a.width) {
     x = a.path[(size_t)b * a.width + tid];
     if (tid > 0) before = a.path[(size_t)b * a.width + tid - 1];
   }
+  if (nodes == 0) m = 0;  // no tree (the plan gave it no place): whatever its path holds
   if (len < nodes || len <= 0) {  // an idle slot of the batch
     if (g0 == 0 && tid == 0) a.len_out[b] = max(len, 0);
     return;
