@@ -11,6 +11,8 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cxxabi.h>
+
 #include <algorithm>
 #include <exception>
 #include <stdexcept>
@@ -35,6 +37,16 @@ constexpr auto kInt = at::kInt, kFloat = at::kFloat, kBf16 = at::kBFloat16, kHal
 void need(bool ok, const char* what) {
   if (!ok) bad(what);
 }
+
+// Other Python threads run while this lives: an allocation may wait for the device, the library's entry points for its
+// mutex, for a workspace that grows or for room in a launch queue.  (A thread that is ended while it waits for its turn, as
+// the interpreter shuts down, is unwound through the destructor.)
+struct NoGil {
+  PyThreadState* state = PyEval_SaveThread();
+  NoGil() = default;
+  NoGil(const NoGil&) = delete;
+  ~NoGil() noexcept(false) { PyEval_RestoreThread(state); }
+};
 
 const Tensor& tensor(PyObject* o, const char* name) {
   if (!THPVariable_Check(o)) bad(std::string(name) + " must be a tensor");
@@ -128,7 +140,16 @@ const int* tree(PyObject* o, int64_t B, c10::Device dev, int* Tq, long long* str
   return t.data_ptr<int>();
 }
 
-Tensor make(Sizes shape, at::ScalarType type, c10::Device dev) { return at::empty(shape, at::TensorOptions().dtype(type).device(dev)); }
+Tensor make(Sizes shape, at::ScalarType type, c10::Device dev) {
+  NoGil others;
+  return at::empty(shape, at::TensorOptions().dtype(type).device(dev));
+}
+// The status of a library call.
+template <class F>
+int library(F call) {
+  NoGil others;
+  return call();
+}
 // `o` of the given shape, or a new one.
 Tensor out32(PyObject* o, const char* name, c10::Device dev, Sizes shape) {
   if (!given(o)) return make(shape, kInt, dev);
@@ -201,9 +222,12 @@ PyObject* plan(PyObject* const* a) {
   const Tensor got = own_got ? part(B) : out32(a[10], "held_out", c.dev, {B}), left = own_left ? part(2) : out32(a[11], "span_out", c.dev, {2});
   const Tensor granted = own_new ? part(B) : out32(a[12], "new_len_out", c.dev, {B});
   if (!own_total) apart(total, THPVariable_Unpack(a[4]), "kv_len_out and kv_len must not share memory");
-  const int st = f_plan(p_table, p_ring, held, span, len, add, parents, got.data_ptr<int>(), left.data_ptr<int>(),
-                        total.data_ptr<int>(), granted.data_ptr<int>(), cu.data_ptr<int>(), slots.data_ptr<int>(), pos.data_ptr<int>(), rows, (int)B,
-                        Tq, page, (int)ring.size(0), (int)width, pstride, c.stream);
+  const int P = (int)ring.size(0);
+  const int st = library([&] {
+    return f_plan(p_table, p_ring, held, span, len, add, parents, got.data_ptr<int>(), left.data_ptr<int>(), total.data_ptr<int>(),
+                  granted.data_ptr<int>(), cu.data_ptr<int>(), slots.data_ptr<int>(), pos.data_ptr<int>(), rows, (int)B, Tq, page, P,
+                  (int)width, pstride, c.stream);
+  });
   return st == NE_OK ? wrap({total, got, left, cu, slots, pos, granted}) : status(st);
 }
 
@@ -220,8 +244,13 @@ PyObject* append(PyObject* const* a) {
   const int *slots = ints(a[4], "slots", c.dev, {N}), *pos = ints(a[5], "positions", c.dev, {N});
   const void* w = weight(a[7], "k_weight", c.dev, p.D);
   if (N == 0) return status(NE_OK);
-  return status(f_append(k.data_ptr(), v.data_ptr(), w, p.k, p.v, slots, pos, (int)N, p.heads, p.D, p.page, p.pages, number(a[6]), p.stride,
-                         ks, vs, real(a[8]), real(a[9]), truth(a[10]) ? NE_ATTN_ROPE_HALF : 0, c.stream));
+  const void *pk = k.data_ptr(), *pv = v.data_ptr();
+  const int capacity = number(a[6]), flags = truth(a[10]) ? NE_ATTN_ROPE_HALF : 0;
+  const float eps = real(a[8]), base = real(a[9]);
+  return status(library([&] {
+    return f_append(pk, pv, w, p.k, p.v, slots, pos, (int)N, p.heads, p.D, p.page, p.pages, capacity, p.stride, ks, vs, eps, base, flags,
+                    c.stream);
+  }));
 }
 
 // q, k_pages, v_pages, page_table, kv_len, parents, tree_len, q_weight, eps, rope_base, o, lse, fp32 of a new o, workspace,
@@ -262,9 +291,13 @@ PyObject* decode_tree(PyObject* const* a) {
   }
   const int flags = (o.scalar_type() == kFloat ? NE_ATTN_O_FP32 : 0) | (truth(a[14]) ? NE_ATTN_ROPE_HALF : 0);
   const float eps = real(a[8]), base = real(a[9]);
+  const void* pq = q.data_ptr();
+  const int width = (int)table.size(1);
   const auto call = [&](void* ws, size_t bytes) {
-    return f_tree(q.data_ptr(), w, p.k, p.v, p_table, len, parents, nodes, o.data_ptr(), lse.data_ptr<float>(), (int)B, (int)Tq, (int)Hq,
-                  p.heads, p.D, p.page, p.pages, (int)table.size(1), p.stride, qs, pstride, eps, base, flags, ws, bytes, c.stream);
+    return library([&] {
+      return f_tree(pq, w, p.k, p.v, p_table, len, parents, nodes, o.data_ptr(), lse.data_ptr<float>(), (int)B, (int)Tq, (int)Hq, p.heads,
+                    p.D, p.page, p.pages, width, p.stride, qs, pstride, eps, base, flags, ws, bytes, c.stream);
+    });
   };
   int st;
   if (given(a[13])) {
@@ -298,8 +331,11 @@ PyObject* keep(PyObject* const* a) {
   const int* nodes = each ? ints(a[4], "tree_len", c.dev, {B}) : nullptr;
   const Tensor out = out32(a[7], "kv_len_out", c.dev, {B});
   if (given(a[7])) apart(out, THPVariable_Unpack(a[3]), "kv_len_out and kv_len must not share memory");
-  const int st = f_keep(p.k, p.v, p_table, len, nodes, p_path, count, out.data_ptr<int>(), (int)B, each ? 0 : number(a[4]),
-                        (int)path.size(1), p.heads, p.D, p.page, p.pages, (int)table.size(1), p.stride, c.stream);
+  const int tokens = each ? 0 : number(a[4]), width = (int)path.size(1), max_pages = (int)table.size(1);
+  const int st = library([&] {
+    return f_keep(p.k, p.v, p_table, len, nodes, p_path, count, out.data_ptr<int>(), (int)B, tokens, width, p.heads, p.D, p.page, p.pages,
+                  max_pages, p.stride, c.stream);
+  });
   return st == NE_OK ? THPVariable_Wrap(out) : status(st);
 }
 
@@ -319,6 +355,8 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
     PyErr_SetString(out_of_memory, e.what_without_backtrace());
   } catch (const std::exception& e) {
     PyErr_SetString(PyExc_RuntimeError, e.what());
+  } catch (abi::__forced_unwind&) {  // the thread ends
+    throw;
   } catch (...) {
     PyErr_SetString(PyExc_RuntimeError, "unknown error");
   }

@@ -478,9 +478,9 @@ int ne_attn_kv_append_slots(const void* k_new, const void* v_new, const void* k_
  * its tree's.  The query of token t < tree_len[b], q[b, t] (otherwise as in ne_attn_decode_paged), attends to the
  * positions before the tree, to its ancestors and to itself.  o and lse as there; tokens at or past
  * tree_len[b], and all of an idle slot (kv_len[b] <= 0 or below tree_len[b]), see no key: o = 0, lse =
- * -infinity.  Nothing is read of the context of a sequence with a tree_len of 0.  A kv_len past the table (NE_ERR_PAGE) or a tree_len outside 0 .. Tq (NE_ERR_TREE) makes the slot an idle
- * one.  Bad pages, values that must be numbers, and workspaces as for ne_attn_decode_paged; B * Tq * Hq * D < 2^31;
- * o may not overlap q (NE_ERR_ARG).
+ * -infinity.  Nothing is read of the context of a sequence with a tree_len of 0.  A kv_len past the table (NE_ERR_PAGE)
+ * or a tree_len outside 0 .. Tq (NE_ERR_TREE) makes the slot an idle one.  Bad pages, values that must be numbers, and
+ * workspaces as for ne_attn_decode_paged; B * Tq * Hq * D < 2^31; o may not overlap q (NE_ERR_ARG).
  * The result is bitwise reproducible.
  */
 size_t ne_attn_decode_tree_workspace_size(int B, int Tq, int Hq, int Hkv, int D);
