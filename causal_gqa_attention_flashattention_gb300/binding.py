@@ -12,6 +12,8 @@ import os
 
 import torch
 
+from .build import bind_path
+
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_build", "libneattn.so")
 
@@ -666,7 +668,7 @@ class PagedPlan(collections.namedtuple("PagedPlan", "kv_len held span cu_new slo
 
 
 _bind = None
-BIND_PATH = os.path.join(_HERE, "_build", "_neattn_bind.so")
+BIND_PATH = bind_path()  # for this interpreter and this torch
 
 
 def _compiled():
@@ -675,7 +677,7 @@ def _compiled():
     if _bind is None:
         L = lib()
         if not os.path.exists(BIND_PATH):
-            raise RuntimeError("_neattn_bind.so is not built (%s); run __graft_entry__.build()" % BIND_PATH)
+            raise RuntimeError("the compiled part of the binding is not built (%s); run __graft_entry__.build()" % BIND_PATH)
         spec = importlib.util.spec_from_file_location("_neattn_bind", BIND_PATH)
         m = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(m)

@@ -3,18 +3,20 @@
 nvcc compiles each translation unit for sm_103a in parallel, then links a
 shared library with the CUDA runtime linked statically (the driver API is
 reached through cudaGetDriverEntryPointByVersion, so libcuda is not linked).
+g++ compiles the part of binding.py that is C++ against the installed torch.
 """
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libneattn.so")
-BIND_SOURCE = os.path.join(CSRC, "bind.cpp")
-BIND = os.path.join(BUILD, "_neattn_bind.so")  # the compiled part of binding.py, for this interpreter and torch
+HEADER = os.path.join(HERE, "..", "include", "ne_attn.h")
+BIND_SOURCE = "bind.cpp"  # the compiled part of binding.py
 SOURCES = ["api.cu", "attn_fwd.cu", "attn_bwd.cu", "attn_decode.cu", "qkv_proj.cu", "qk_norm.cu", "paged.cu",
            "paged_prefix.cu", "paged_plan.cu", "paged_tree.cu"]
 HEADERS = ["ptx.cuh", "rope.cuh", "internal.h", "paged.cuh", "paged_sweep.cuh", "paged_prefix.cuh"]
@@ -23,36 +25,44 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr"]
 
 
-def _newest_input():
-    paths = [os.path.join(CSRC, f) for f in SOURCES + HEADERS]
-    paths.append(os.path.join(HERE, "..", "include", "ne_attn.h"))
-    paths += [os.path.abspath(__file__), BIND_SOURCE]
-    return max(os.path.getmtime(p) for p in paths)
+def _stale(path, sources):
+    """Whether `path` is missing or older than one of its inputs."""
+    inputs = [os.path.join(CSRC, f) for f in sources] + [HEADER, os.path.abspath(__file__)]
+    return not os.path.exists(path) or os.path.getmtime(path) < max(os.path.getmtime(p) for p in inputs)
 
 
-def _compile_bind():
-    import sysconfig
+def bind_path():
+    """The compiled part of binding.py.  It uses the interpreter's and torch's C++ interfaces, so its name says which."""
+    import torch
+    return os.path.join(BUILD, "_neattn_bind.torch-%s%s" % (torch.__version__, sysconfig.get_config_var("EXT_SUFFIX")))
 
+
+def _build_bind(force):
+    try:
+        path = bind_path()
+    except ModuleNotFoundError as e:
+        if e.name != "torch":
+            raise
+        sys.stderr.write("torch is not installed: the compiled part of its binding is left out\n")
+        return
+    if not force and not _stale(path, [BIND_SOURCE]):
+        return
     import torch
     root = os.path.dirname(torch.__file__)
     inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
            sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include")]
     lib = os.path.join(root, "lib")
-    tmp = BIND + ".%d.tmp" % os.getpid()
+    tmp = path + ".%d.tmp" % os.getpid()
     cmd = (["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-w",
             "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI)] + ["-I" + p for p in inc]
-           + [BIND_SOURCE, "-o", tmp, "-L" + lib, "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10_cuda", "-lc10"])
+           + [os.path.join(CSRC, BIND_SOURCE), "-o", tmp, "-L" + lib, "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10_cuda", "-lc10"])
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError("g++ failed for bind.cpp:\n%s\n%s" % (r.stdout, r.stderr))
-    os.replace(tmp, BIND)
+        raise RuntimeError("g++ failed for %s:\n%s\n%s" % (BIND_SOURCE, r.stdout, r.stderr))
+    os.replace(tmp, path)
 
 
-def build(force=False, verbose=False):
-    os.makedirs(BUILD, exist_ok=True)
-    newest = _newest_input()
-    if not force and all(os.path.exists(p) and os.path.getmtime(p) >= newest for p in (LIB, BIND)):
-        return LIB
+def _build_lib(ex, verbose):
     extra = ["-Xptxas", "-v"] if verbose else []
 
     def compile_one(src):
@@ -65,16 +75,25 @@ def build(force=False, verbose=False):
             sys.stderr.write(r.stderr)
         return obj
 
-    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        bind = ex.submit(_compile_bind)
-        objs = list(ex.map(compile_one, SOURCES))
-        bind.result()
+    objs = list(ex.map(compile_one, SOURCES))
     tmp = LIB + ".%d.tmp" % os.getpid()
     cmd = [NVCC] + ARCH + ["-shared", "-cudart", "static", "-o", tmp] + objs
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError("link failed:\n%s\n%s" % (r.stdout, r.stderr))
     os.replace(tmp, LIB)
+
+
+def build(force=False, verbose=False):
+    """Builds what is out of date and returns the library's path.  The library needs no torch; the compiled part of the
+    binding does: it is left out where torch is not installed, and where it does not compile this raises once the library
+    is there."""
+    os.makedirs(BUILD, exist_ok=True)
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        bind = ex.submit(_build_bind, force)
+        if force or _stale(LIB, SOURCES + HEADERS):
+            _build_lib(ex, verbose)
+        bind.result()
     return LIB
 
 
