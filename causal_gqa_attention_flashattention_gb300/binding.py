@@ -702,7 +702,8 @@ def paged_plan(page_table, free_pages, held, free_span, kv_len, new_len, rows, p
     lengths and pages held (a sequence whose pages the ring no longer has keeps its old ones), where each
     sequence's rows begin, and the place (-1: none) and rotary position of every row for kv_append_slots.  Its new_len
     [B] is what each sequence was granted, 0 where refused: the tree_len of attn_decode_tree and kv_keep_paged.
-    held_out, span_out and new_len_out may be held, free_span and new_len themselves, kv_len_out may not be kv_len."""
+    held_out, span_out and new_len_out may be held, free_span and new_len themselves; kv_len_out may not lie on kv_len,
+    the table, the ring or parents."""
     if stream is not None:
         return _on(stream, paged_plan, page_table, free_pages, held, free_span, kv_len, new_len, rows, page_size, parents,
                    kv_len_out, held_out, span_out, None, new_len_out)
@@ -761,7 +762,7 @@ def kv_keep_paged(k_pages, v_pages, page_table, kv_len, tree_len, path, path_len
 
     kv_len int32 [B] counts the cached positions, the tree's tree_len (int32 [B], or one number for all) included; one of 0
     keeps nothing and its length, whatever its path holds;
-    returns the new lengths (kv_len_out if given, which may not be kv_len).  The pools of several layers with one
+    returns the new lengths (kv_len_out if given, which may lie on none of the tensors read).  The pools of several layers with one
     table may be passed as one [num_pages, layers * Hkv, page_size, D]."""
     if stream is not None:
         return _on(stream, kv_keep_paged, k_pages, v_pages, page_table, kv_len, tree_len, path, path_len, kv_len_out)

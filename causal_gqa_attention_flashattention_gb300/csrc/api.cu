@@ -8,6 +8,7 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 #include <queue>
 #include <utility>
@@ -589,6 +590,19 @@ bool row_stride_ok(long long stride, int H, int D) {
   return stride >= (long long)H * D && stride % 8 == 0 && stride < (1LL << 40);
 }
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+// Whether the int32 array `out` of n has no entry in common with any of the arrays in `in` (NULL: none there).
+struct Ints {
+  const int* p;
+  long long n;
+};
+bool apart(const int* out, long long n, std::initializer_list<Ints> in) {
+  const uintptr_t o = reinterpret_cast<uintptr_t>(out);
+  for (const Ints& x : in) {
+    const uintptr_t i = reinterpret_cast<uintptr_t>(x.p);
+    if (x.p && o < i + 4 * (uintptr_t)x.n && i < o + 4 * (uintptr_t)n) return false;
+  }
+  return true;
+}
 int log2_of(int v) {
   int s = 0;
   while ((1 << s) < v) s++;
@@ -1697,6 +1711,11 @@ int ne_attn_paged_plan_ex(int* page_table, int* free_pages, const int* held, con
                        kv_len_out, new_len_out, cu_new, slots, positions};
   for (const void* p : all)
     if (!aligned4(p)) return NE_ERR_ALIGN;
+  // read when they have been written, in part by a second launch (held, free_span and new_len are read before)
+  const std::initializer_list<Ints> read = {
+      {kv_len, B}, {page_table, (long long)B * max_pages}, {free_pages, num_pages}, {parents, (B - 1) * parent_stride + Tq}};
+  if (!apart(kv_len_out, B, read)) return NE_ERR_ARG;
+  if (new_len_out && (!apart(new_len_out, B, read) || !apart(new_len_out, B, {{kv_len_out, B}}))) return NE_ERR_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   std::lock_guard<std::mutex> lock(g_mu);
   int dev, nsm = 0;
@@ -1879,6 +1898,9 @@ int ne_attn_kv_keep_paged(void* k_pages, void* v_pages, const int* page_table, c
   if (!aligned16(k_pages) || !aligned16(v_pages) || !aligned4(page_table) || !aligned4(kv_len) || !aligned4(tree_len) ||
       !aligned4(path) || !aligned4(path_len) || !aligned4(kv_len_out))
     return NE_ERR_ALIGN;
+  // the blocks of a sequence's heads read them all, one of them writes its length
+  if (!apart(kv_len_out, B, {{kv_len, B}, {tree_len, B}, {path_len, B}, {path, (long long)B * width}, {page_table, (long long)B * max_pages}}))
+    return NE_ERR_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   std::lock_guard<std::mutex> lock(g_mu);
   int dev, nsm = 0;

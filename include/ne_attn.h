@@ -442,7 +442,8 @@ int ne_attn_decode_paged(const void* q, const void* q_w, const void* k_pages, co
  * the next call.  Pages are handed out as long as they last: from the first sequence whose need goes past
  * them, every one that needs pages gets none of them, keeps what it holds, and its rows get no slots.
  * Writes held_out [B], free_span_out [2] (these may be held and free_span), kv_len_out [B] (kv_len + new_len, or
- * kv_len where refused; a buffer of its own), cu_new [B + 1] (the running sum of new_len, at most N), and for each of the N rows
+ * kv_len where refused; kv_len, page_table, free_pages and parents are still read then: NE_ERR_ARG if it lies on them),
+ * cu_new [B + 1] (the running sum of new_len, at most N), and for each of the N rows
  * n = cu_new[b] + t: slots[n] = the place of position kv_len[b] + t in the pools, page * page_size + row of the page (-1
  * where refused and at or past cu_new[B]), positions[n] = kv_len[b] + t, with parents (at most Tq new tokens a
  * sequence) kv_len[b] + depth(t) (0 at or past cu_new[B]).
@@ -455,8 +456,8 @@ int ne_attn_paged_plan(int* page_table, int* free_pages, const int* held, const 
                        const int* new_len, const int* parents, int* held_out, int* free_span_out, int* kv_len_out,
                        int* cu_new, int* slots, int* positions, int N, int B, int Tq, int page_size, int num_pages,
                        int max_pages, long long parent_stride, void* stream);
-/* The same, and new_len_out [B] (may be new_len itself, or NULL): the positions that each sequence was granted, new_len
- * or, where it was refused, 0. */
+/* The same, and new_len_out [B] (may be new_len itself, or NULL; where it may not lie as kv_len_out): the positions that
+ * each sequence was granted, new_len or, where it was refused, 0. */
 int ne_attn_paged_plan_ex(int* page_table, int* free_pages, const int* held, const int* free_span, const int* kv_len,
                           const int* new_len, const int* parents, int* held_out, int* free_span_out, int* kv_len_out,
                           int* new_len_out, int* cu_new, int* slots, int* positions, int N, int B, int Tq, int page_size,
@@ -494,8 +495,9 @@ int ne_attn_decode_tree(const void* q, const void* q_w, const void* k_pages, con
  * ne_attn_kv_keep_paged: of the tree at the end of sequence b (tree_len[b] tokens, NULL: `tokens`) the path_len[b] tokens
  * path[b, 0], path[b, 1], .. stay (path [B, width], width <= 64; rising, as a child comes after its parent): the keys
  * and values of token path[b, i] move to position kv_len[b] - tree_len[b] + i, in place, whatever the
- * overlap.  Writes kv_len_out[b] = kv_len[b] - tree_len[b] + path_len[b] (a buffer of its own; idle slots, with
- * kv_len[b] below tree_len[b] or 0, keep max(kv_len, 0); a tree_len[b] of 0 keeps kv_len[b], whatever its path
+ * overlap.  Writes kv_len_out[b] = kv_len[b] - tree_len[b] + path_len[b] (NE_ERR_ARG if it lies on one of the arrays that
+ * are read; idle slots, with kv_len[b] below tree_len[b] or 0, keep max(kv_len, 0); a tree_len[b] of 0 keeps kv_len[b],
+ * whatever its path
  * holds).  A path that does not rise or leaves the tree is recorded as NE_ERR_TREE and none of it stays.  The moved
  * keys keep the rotation of their depth, which is right for a path from the context on.  The pools of layers that share
  * one table may be given as one, with all their heads: [num_pages, layers * Hkv, page_size, D].
