@@ -134,6 +134,7 @@ const int* tree(PyObject* o, int64_t B, c10::Device dev, int* Tq, long long* str
   need(t.scalar_type() == kInt && t.device() == dev && (d == 1 || (d == 2 && t.size(0) == B)) &&
            (t.size(d - 1) <= 1 || t.stride(d - 1) == 1) && t.size(d - 1) < (1LL << 31),
        "parents must be int32 [B, Tq] or [Tq], rows contiguous, on the call's device");
+  need(t.size(d - 1) > 0, "parents must have a token");  // an empty tensor's pointer would read as none given
   *Tq = (int)t.size(d - 1);
   *stride = d == 1 || B == 1 ? 0 : t.stride(0);
   need(*stride == 0 || *stride >= *Tq, "parents: rows must not overlap");
