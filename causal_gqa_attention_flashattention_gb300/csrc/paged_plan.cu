@@ -83,7 +83,7 @@ __device__ __forceinline__ void plan_row(const PagedPlanArgs& a, int n, int b, i
   a.positions[n] = a.parents && t < a.Tq ? (int)((unsigned)len + tree_depth(a.parents + b * a.parent_stride, t, a.status)) : at;
 }
 
-__global__ void __launch_bounds__(kPlanThreads) k_paged_plan(const PagedPlanArgs a) {
+__global__ void __launch_bounds__(kPlanThreads, 1) k_paged_plan(const PagedPlanArgs a) {
   __shared__ int s_got[kPlanMaxB], s_give[kPlanMaxB], s_cu[kPlanMaxB], s_from[kPlanMaxB], s_len[kPlanMaxB];
   __shared__ bool s_ok[kPlanMaxB];
   __shared__ unsigned long long wsum[32];
