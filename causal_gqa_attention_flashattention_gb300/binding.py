@@ -740,7 +740,8 @@ def attn_decode_tree(q, k_pages, v_pages, page_table, kv_len, parents, tree_len=
     """o, lse for a tree of drafted tokens q [B,Tq,Hq,D] (bf16) of every sequence over a paged cache
     (ne_attn_decode_tree).
 
-    kv_len int32 [B] counts the cached positions, the tree's tree_len[b] own included (int32 [B]; None: Tq).  parents
+    kv_len int32 [B] counts the cached positions, the tree's tree_len[b] own included (int32 [B]; None: Tq; after a plan
+    what it granted, new_len, as a refused sequence has no tree at its end).  parents
     int32 [B, Tq] or [Tq] (one tree for all): the token each hangs on, -1 for the context.  A token sees the
     positions before the tree, its ancestors and itself; tokens past tree_len, and idle slots (kv_len 0), get o = 0
     and lse = -inf.  q_weight [D]: the queries are normalised first."""

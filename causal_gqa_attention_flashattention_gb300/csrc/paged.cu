@@ -24,7 +24,7 @@ namespace {
 // threads of a row are neighbouring lanes (the norm adds up squares by shuffles).  Bound by the
 // bytes: 23 prompts with 17,000 rows of four heads (34.9 MB) take 9.3 us, a step of 64 tokens 3.1 us.
 // With SLOTS every row is given its place in the pool and its rotary position (negative slot: no place): 256 rows of
-// four heads 1.7 us, 16381 (33.3 MB) 8.0 us.
+// four heads 1.7 us, 16381 (33.3 MB) 8.0 us: two and a quarter waves of blocks (12 an SM).
 template <int D, bool SLOTS>
 __global__ void __launch_bounds__(128) k_kv_append_paged(const PagedAppendArgs a) {
   if (SLOTS) pdl_wait();
